@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "gla_common.cuh"
+#include "gla_delta.cuh"
 
 namespace gla {
 
@@ -58,6 +59,25 @@ int decode_step_gated_bf16(const void *, const void *, const void *, const void 
                            const int32_t *, int, void *, int, int, int, int, cudaStream_t);
 int decode_step_layers_bf16(const void *, const void *, const void *, const void *, int, const float *, float *,
                             const int32_t *, int, int, int, int, void *, int, int, int, int, cudaStream_t);
+namespace delta {
+template <typename T>
+int simt_fwd(const Shape &, const T *, const T *, const T *, const void *, const void *, const float *, T *, float *,
+             cudaStream_t);
+size_t simt_bwd_workspace(const Shape &);
+template <typename T>
+int simt_bwd(const Shape &, const T *, const T *, const T *, const void *, const void *, const T *, const float *,
+             const float *, T *, T *, T *, void *, void *, float *, void *, cudaStream_t);
+int decode_step(const void *, const void *, const void *, const void *, const void *, float *, const int32_t *, int,
+                void *, int, int, int, int, int, int, int, cudaStream_t);
+}  // namespace delta
+namespace norm {
+size_t workspace(int64_t, int, int);
+int group_norm(const void *, const float *, const float *, const void *, int, float, void *, int64_t, int, int, int,
+               cudaStream_t);
+int group_norm_bwd(const void *, const void *, const float *, const float *, const void *, int, float, void *, float *,
+                   float *, void *, void *, int64_t, int, int, int, cudaStream_t);
+}  // namespace norm
+int take_status_delta(cudaStream_t);
 int take_status_conv(cudaStream_t);
 int take_status_simt(cudaStream_t);
 int take_status_bwd(cudaStream_t);
@@ -148,6 +168,65 @@ int check_decode(const void *q, const void *k, const void *v, const float *ld, c
     if (dk > 256 || dv < 4 || dv > 1024 || dv % 4) return GLA_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(state) ||
         !aligned16(ld))
+        return GLA_ERR_ALIGN;
+    if (!device_info().ok) return GLA_ERR_UNSUPPORTED;
+    return GLA_OK;
+}
+
+// Sizes and types of the gated delta rule's chunked entry points.
+int check_delta_sizes(int B, int T, int H, int Hk, int dk, int dv, int dtype, int packed) {
+    if (dtype != GLA_BF16 && dtype != GLA_F32) return GLA_ERR_ARG;
+    if (B <= 0 || T < 0 || H <= 0 || Hk <= 0 || dk <= 0 || dv <= 0 || H % Hk) return GLA_ERR_ARG;
+    if (dk < 16 || dk > 256 || dv < 16 || dv > 512 || dk % 8 || dv % 8) return GLA_ERR_UNSUPPORTED;
+    const long long rows = packed ? (long long)T : (long long)B * T;
+    // block indexes (chains, and chunks of 32 tokens of all heads) and row offsets of packed batches are 32-bit
+    if (rows > 0x7fffffffLL || (long long)B * H > 0x7fffffffLL || (rows / 32 + B + 1) * H > 0x7fffffffLL)
+        return GLA_ERR_UNSUPPORTED;
+    return GLA_OK;
+}
+
+int check_delta(const void *q, const void *k, const void *v, const void *g, const void *beta, const float *h0,
+                const void *out, const float *hT, int B, int T, int H, int Hk, int dk, int dv, int dtype,
+                int gate_dtype, const int32_t *cu, const void *ws) {
+    int rc = check_delta_sizes(B, T, H, Hk, dk, dv, dtype, cu != nullptr);
+    if (rc) return rc;
+    if (gate_dtype != GLA_F32 && gate_dtype != dtype) return GLA_ERR_ARG;
+    if (T > 0 && (!q || !k || !v || !g || !beta || !out)) return GLA_ERR_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g) || !aligned16(beta) || !aligned16(h0) ||
+        !aligned16(out) || !aligned16(hT) || !aligned16(cu) || !aligned16(ws))
+        return GLA_ERR_ALIGN;
+    if (!device_info().ok) return GLA_ERR_UNSUPPORTED;
+    return GLA_OK;
+}
+
+delta::Shape delta_shape(int B, int T, int H, int Hk, int dk, int dv, int dtype, int gate_dtype, const int32_t *cu) {
+    delta::Shape p{};
+    p.nseq = B;
+    p.T = T;
+    p.H = H;
+    p.Hk = Hk;
+    p.dk = dk;
+    p.dv = dv;
+    p.gate_f32 = gate_dtype == GLA_F32;
+    p.cu = cu;
+    return p;
+}
+
+long long delta_workspace(int op, const delta::Shape &p, int dtype) {
+    (void)dtype;
+    if (op == GLA_OP_FORWARD) return 0;
+    return (long long)delta::simt_bwd_workspace(p);
+}
+
+int check_norm(const void *x, const float *weight, const float *bias, const void *gate, int act, float eps,
+               const void *out, long long rows, int groups, int width, int dtype) {
+    if (dtype != GLA_BF16 && dtype != GLA_F32) return GLA_ERR_ARG;
+    if (act != GLA_ACT_NONE && act != GLA_ACT_SILU && act != GLA_ACT_SIGMOID) return GLA_ERR_ARG;
+    if (rows < 0 || groups <= 0 || width <= 0 || !(eps > 0.f)) return GLA_ERR_ARG;
+    if (rows > 0 && (!x || !out)) return GLA_ERR_ARG;
+    if (width % 8 || width > 2048 || (long long)groups * width > (1 << 20) || rows > (1LL << 40))
+        return GLA_ERR_UNSUPPORTED;
+    if (!aligned16(x) || !aligned16(weight) || !aligned16(bias) || !aligned16(gate) || !aligned16(out))
         return GLA_ERR_ALIGN;
     if (!device_info().ok) return GLA_ERR_UNSUPPORTED;
     return GLA_OK;
@@ -363,11 +442,101 @@ int gla_conv1d_silu_step(const void *x, const float *weight, const float *bias, 
     return conv1d_silu_step_bf16(x, weight, bias, state_inout, y, N, D, (cudaStream_t)stream);
 }
 
+long long gla_delta_workspace_bytes(int op, int B, int T, int H, int Hk, int dk, int dv, int dtype, int packed) {
+    if (op != GLA_OP_FORWARD && op != GLA_OP_BACKWARD) return GLA_ERR_ARG;
+    int rc = check_delta_sizes(B, T, H, Hk, dk, dv, dtype, packed);
+    if (rc) return rc;
+    // only whether offsets are given matters here, never their address
+    static const int32_t some = 0;
+    return delta_workspace(op, delta_shape(B, T, H, Hk, dk, dv, dtype, dtype, packed ? &some : nullptr), dtype);
+}
+
+int gla_delta_chunk_fwd(const void *q, const void *k, const void *v, const void *g, const void *beta, const float *h0,
+                        void *out, float *hT, int B, int T, int H, int Hk, int dk, int dv, int dtype, int gate_dtype,
+                        const int32_t *cu_seqlens, void *ws, long long ws_bytes, void *stream) {
+    int rc = check_delta(q, k, v, g, beta, h0, out, hT, B, T, H, Hk, dk, dv, dtype, gate_dtype, cu_seqlens, ws);
+    if (rc) return rc;
+    const delta::Shape p = delta_shape(B, T, H, Hk, dk, dv, dtype, gate_dtype, cu_seqlens);
+    const long long need = delta_workspace(GLA_OP_FORWARD, p, dtype);
+    if (need > 0 && (!ws || ws_bytes < need)) return GLA_ERR_ARG;
+    cudaStream_t st = (cudaStream_t)stream;
+    using H16 = __nv_bfloat16;
+    if (dtype == GLA_F32)
+        return delta::simt_fwd<float>(p, (const float *)q, (const float *)k, (const float *)v, g, beta, h0,
+                                      (float *)out, hT, st);
+    return delta::simt_fwd<H16>(p, (const H16 *)q, (const H16 *)k, (const H16 *)v, g, beta, h0, (H16 *)out, hT, st);
+}
+
+int gla_delta_chunk_bwd(const void *q, const void *k, const void *v, const void *g, const void *beta, const void *dout,
+                        const float *h0, const float *dhT, void *dq, void *dk_out, void *dv_out, void *dg,
+                        void *dbeta, float *dh0, int B, int T, int H, int Hk, int dk, int dv, int dtype,
+                        int gate_dtype, const int32_t *cu_seqlens, void *ws, long long ws_bytes, void *stream) {
+    int rc = check_delta(q, k, v, g, beta, h0, dout, dhT, B, T, H, Hk, dk, dv, dtype, gate_dtype, cu_seqlens, ws);
+    if (rc) return rc;
+    if (T > 0 && (!dq || !dk_out || !dv_out || !dg || !dbeta)) return GLA_ERR_ARG;
+    if (!aligned16(dq) || !aligned16(dk_out) || !aligned16(dv_out) || !aligned16(dg) || !aligned16(dbeta) ||
+        !aligned16(dh0))
+        return GLA_ERR_ALIGN;
+    const delta::Shape p = delta_shape(B, T, H, Hk, dk, dv, dtype, gate_dtype, cu_seqlens);
+    if (!ws || ws_bytes < delta_workspace(GLA_OP_BACKWARD, p, dtype)) return GLA_ERR_ARG;
+    cudaStream_t st = (cudaStream_t)stream;
+    using H16 = __nv_bfloat16;
+    if (dtype == GLA_F32)
+        return delta::simt_bwd<float>(p, (const float *)q, (const float *)k, (const float *)v, g, beta,
+                                      (const float *)dout, h0, dhT, (float *)dq, (float *)dk_out, (float *)dv_out, dg,
+                                      dbeta, dh0, ws, st);
+    return delta::simt_bwd<H16>(p, (const H16 *)q, (const H16 *)k, (const H16 *)v, g, beta, (const H16 *)dout, h0, dhT,
+                                (H16 *)dq, (H16 *)dk_out, (H16 *)dv_out, dg, dbeta, dh0, ws, st);
+}
+
+int gla_delta_decode_step(const void *q, const void *k, const void *v, const void *g, const void *beta, float *state,
+                          const int32_t *slots, int nslots, void *out, int N, int H, int Hk, int dk, int dv, int dtype,
+                          int gate_dtype, void *stream) {
+    if (dtype != GLA_BF16 && dtype != GLA_F32) return GLA_ERR_ARG;
+    if (gate_dtype != GLA_F32 && gate_dtype != dtype) return GLA_ERR_ARG;
+    if (N < 0 || H <= 0 || Hk <= 0 || dk <= 0 || dv <= 0 || H % Hk || (slots && nslots <= 0)) return GLA_ERR_ARG;
+    if (dk > 256 || dv < 4 || dv > 1024 || dv % 4) return GLA_ERR_UNSUPPORTED;
+    if (N == 0) return GLA_OK;
+    if (!q || !k || !v || !g || !beta || !state || !out) return GLA_ERR_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g) || !aligned16(beta) || !aligned16(state) ||
+        !aligned16(slots) || !aligned16(out))
+        return GLA_ERR_ALIGN;
+    if (!device_info().ok) return GLA_ERR_UNSUPPORTED;
+    return delta::decode_step(q, k, v, g, beta, state, slots, nslots, out, N, H, Hk, dk, dv, dtype, gate_dtype,
+                              (cudaStream_t)stream);
+}
+
+int gla_group_norm(const void *x, const float *weight, const float *bias, const void *gate, int act, float eps,
+                   void *out, long long rows, int groups, int width, int dtype, void *stream) {
+    int rc = check_norm(x, weight, bias, gate, act, eps, out, rows, groups, width, dtype);
+    if (rc) return rc;
+    return norm::group_norm(x, weight, bias, gate, act, eps, out, rows, groups, width, dtype, (cudaStream_t)stream);
+}
+
+long long gla_group_norm_workspace_bytes(long long rows, int groups, int width) {
+    if (rows < 0 || groups <= 0 || width <= 0) return GLA_ERR_ARG;
+    if (width % 8 || width > 2048 || (long long)groups * width > (1 << 20)) return GLA_ERR_UNSUPPORTED;
+    return (long long)norm::workspace(rows, groups, width);
+}
+
+int gla_group_norm_bwd(const void *dout, const void *x, const float *weight, const float *bias, const void *gate,
+                       int act, float eps, void *dx, float *dweight, float *dbias, void *dgate, long long rows,
+                       int groups, int width, int dtype, void *ws, long long ws_bytes, void *stream) {
+    int rc = check_norm(x, weight, bias, gate, act, eps, dx, rows, groups, width, dtype);
+    if (rc) return rc;
+    if (rows > 0 && (!dout || (gate && !dgate))) return GLA_ERR_ARG;
+    if (!ws || ws_bytes < (long long)norm::workspace(rows, groups, width)) return GLA_ERR_ARG;
+    if (!aligned16(dout) || !aligned16(dweight) || !aligned16(dbias) || !aligned16(dgate) || !aligned16(ws))
+        return GLA_ERR_ALIGN;
+    return norm::group_norm_bwd(dout, x, weight, bias, gate, act, eps, dx, dweight, dbias, dgate, ws, rows, groups,
+                                width, dtype, (cudaStream_t)stream);
+}
+
 int gla_last_device_status(void *stream) {
     cudaStream_t st = (cudaStream_t)stream;
     int result = GLA_OK;
-    const int parts[5] = {take_status_simt(st), take_status_decode(st), take_status_tc(st), take_status_bwd(st),
-                          take_status_conv(st)};
+    const int parts[6] = {take_status_simt(st), take_status_decode(st), take_status_tc(st), take_status_bwd(st),
+                          take_status_conv(st), take_status_delta(st)};
     for (int p : parts) {
         if (p == GLA_ERR_LAUNCH) return GLA_ERR_LAUNCH;
         if (result == GLA_OK && p != 0) result = p;
@@ -405,6 +574,6 @@ int gla_chunk_kernel(int op, int dtype, int dk, int dv, int chunk) {
 
 uint64_t gla_kernel_launches(void) { return g_launches.load(std::memory_order_relaxed); }
 
-int gla_version(void) { return 200; }
+int gla_version(void) { return 300; }
 
 }  // extern "C"

@@ -1,0 +1,659 @@
+// gla_delta.cu — the gated delta rule: decode step, and the token-by-token kernels that take every type and
+// size of its forward and its gradient in f32 arithmetic.
+//
+// Per chain (sequence, value head), see gla_delta.cuh:
+//     u = beta (v - a k S),   S <- a S + k^T u,   o = q S.
+// Every column of S (one of the dv) obeys this map by itself: only k, q, a and beta are shared.  So the
+// columns of a chain are split over threads, warps and blocks without any exchange between them.
+#include "gla_delta.cuh"
+
+GLA_DEFINE_STATUS(delta)
+
+namespace gla {
+namespace delta {
+namespace {
+
+// ---- decode step ---------------------------------------------------------------------------------------------
+//
+// Bound by HBM: 8 bytes per state element (read once, written once) against 7 FLOP.  u needs the sum over dk of
+// k S before any element can be written, so a block holds its whole slice of the state in registers between the
+// two: 16 row groups x up to 16 groups of four columns, kRows rows of 16 bytes a thread.  Both sums (k S and
+// q S) are formed from that one read; o = a q S + (q k) u needs no second pass over the new state.
+constexpr int kStepGroups = 16;   // row groups per block
+
+template <typename T> __device__ __forceinline__ void load4(const T *p, float (&x)[4]);
+template <> __device__ __forceinline__ void load4<float>(const float *p, float (&x)[4]) {
+    const float4 t = __ldg(reinterpret_cast<const float4 *>(p));
+    x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
+}
+template <> __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16 *p, float (&x)[4]) {
+    const uint2 t = __ldg(reinterpret_cast<const uint2 *>(p));
+    x[0] = __uint_as_float(t.x << 16); x[1] = __uint_as_float(t.x & 0xffff0000u);
+    x[2] = __uint_as_float(t.y << 16); x[3] = __uint_as_float(t.y & 0xffff0000u);
+}
+template <typename T> __device__ __forceinline__ void store4(T *p, const float (&x)[4]);
+template <> __device__ __forceinline__ void store4<float>(float *p, const float (&x)[4]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *p, const float (&x)[4]) {
+    __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    uint2 t;
+    t.x = *reinterpret_cast<uint32_t *>(&a);
+    t.y = *reinterpret_cast<uint32_t *>(&b);
+    *reinterpret_cast<uint2 *>(p) = t;
+}
+
+template <typename T, int kRows>
+__global__ void __launch_bounds__(256)
+delta_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, const void *__restrict__ g,
+                  const void *__restrict__ beta, int gate_f32, float *__restrict__ state,
+                  const int32_t *__restrict__ slots, int nslots, T *__restrict__ out, int H, int Hk, int dk, int dv,
+                  int ncg, int nslices) {
+    extern __shared__ __align__(16) float sm[];
+    float *red = sm;                                 // [2][kStepGroups][4 ncg], read and written by float4: first
+    float *redqk = red + 2 * kStepGroups * 4 * ncg;  // [kStepGroups]
+    float *ks = redqk + kStepGroups, *qs = ks + dk;  // [dk] each
+    const int64_t chain = blockIdx.x / nslices;  // n * H + h
+    const int slice = blockIdx.x % nslices;
+    const int64_t n = chain / H;
+    const int h = (int)(chain % H);
+    const int64_t kchain = n * Hk + h / (H / Hk);
+    const int tid = threadIdx.x, cg = tid % ncg, rg = tid / ncg;
+    const int col = (slice * ncg + cg) * 4;
+    const bool live = col < dv;
+    int64_t page = chain;
+    if (slots != nullptr) {
+        const int slot = __ldg(slots + n);
+        if (slot < 0 || slot >= nslots) {  // padding row (or a bad slot, reported): zero output, no page
+            if (slot >= nslots && tid == 0) record_status(GLA_ERR_DEVICE_ARG);
+            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+            if (rg == 0 && live) store4(out + chain * dv + col, zero);
+            return;
+        }
+        page = (int64_t)slot * H + h;
+    }
+    float4 *S = reinterpret_cast<float4 *>(state + page * dk * dv + col);
+    const int rowf4 = dv >> 2;
+    float4 s[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int r = rg + i * kStepGroups;
+        s[i] = r < dk && live ? __ldcs(S + (int64_t)r * rowf4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int i = tid; i < dk; i += blockDim.x) {
+        ks[i] = to_f32(k[kchain * dk + i]);
+        qs[i] = to_f32(q[kchain * dk + i]);
+    }
+    const float a = expf(load_gate<T>(g, chain, gate_f32)), be = load_gate<T>(beta, chain, gate_f32);
+    float vv[4] = {0.f, 0.f, 0.f, 0.f};
+    if (live) load4<T>(v + chain * dv + col, vv);
+    __syncthreads();
+    float pk[4] = {0.f, 0.f, 0.f, 0.f}, pq[4] = {0.f, 0.f, 0.f, 0.f}, pqk = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int r = rg + i * kStepGroups;
+        if (r < dk) {
+            const float kr = ks[r], qr = qs[r];
+            pk[0] = fmaf(kr, s[i].x, pk[0]); pk[1] = fmaf(kr, s[i].y, pk[1]);
+            pk[2] = fmaf(kr, s[i].z, pk[2]); pk[3] = fmaf(kr, s[i].w, pk[3]);
+            pq[0] = fmaf(qr, s[i].x, pq[0]); pq[1] = fmaf(qr, s[i].y, pq[1]);
+            pq[2] = fmaf(qr, s[i].z, pq[2]); pq[3] = fmaf(qr, s[i].w, pq[3]);
+            pqk = fmaf(kr, qr, pqk);
+        }
+    }
+    const int wide = 4 * ncg;
+    *reinterpret_cast<float4 *>(red + rg * wide + cg * 4) = make_float4(pk[0], pk[1], pk[2], pk[3]);
+    *reinterpret_cast<float4 *>(red + (kStepGroups + rg) * wide + cg * 4) = make_float4(pq[0], pq[1], pq[2], pq[3]);
+    if (cg == 0) redqk[rg] = pqk;
+    __syncthreads();
+    float u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < kStepGroups; ++j) {
+        const float4 t = *reinterpret_cast<const float4 *>(red + j * wide + cg * 4);
+        u[0] += t.x; u[1] += t.y; u[2] += t.z; u[3] += t.w;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) u[c] = be * (vv[c] - a * u[c]);
+    if (!live) return;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int r = rg + i * kStepGroups;
+        if (r < dk) {
+            const float kr = ks[r];
+            __stcs(S + (int64_t)r * rowf4, make_float4(fmaf(a, s[i].x, kr * u[0]), fmaf(a, s[i].y, kr * u[1]),
+                                                       fmaf(a, s[i].z, kr * u[2]), fmaf(a, s[i].w, kr * u[3])));
+        }
+    }
+    if (rg == 0) {
+        float o[4] = {0.f, 0.f, 0.f, 0.f}, qk = 0.f;
+#pragma unroll
+        for (int j = 0; j < kStepGroups; ++j) {
+            const float4 t = *reinterpret_cast<const float4 *>(red + (kStepGroups + j) * wide + cg * 4);
+            o[0] += t.x; o[1] += t.y; o[2] += t.z; o[3] += t.w;
+            qk += redqk[j];
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] = fmaf(a, o[c], qk * u[c]);
+        store4(out + chain * dv + col, o);
+    }
+}
+
+template <typename T>
+int launch_step(const T *q, const T *k, const T *v, const void *g, const void *beta, int gate_f32, float *state,
+                const int32_t *slots, int nslots, T *out, int N, int H, int Hk, int dk, int dv, cudaStream_t st) {
+    // slices of at most 64 columns, as even as they come
+    const int nslices = (dv / 4 + 15) / 16, ncg = (dv / 4 + nslices - 1) / nslices;
+    const long long blocks = (long long)N * H * nslices;
+    if (blocks > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
+    const size_t bytes = (size_t)(2 * dk + 2 * kStepGroups * 4 * ncg + kStepGroups) * sizeof(float);
+    const int rows = (dk + kStepGroups - 1) / kStepGroups;
+#define GLA_STEP(R)                                                                                                 \
+    delta_step_kernel<T, R><<<(unsigned)blocks, ncg * kStepGroups, bytes, st>>>(q, k, v, g, beta, gate_f32, state,   \
+                                                                                slots, nslots, out, H, Hk, dk, dv,  \
+                                                                                ncg, nslices)
+    if (rows <= 4) GLA_STEP(4);
+    else if (rows <= 6) GLA_STEP(6);
+    else if (rows <= 8) GLA_STEP(8);
+    else GLA_STEP(16);
+#undef GLA_STEP
+    count_launches(1);
+    return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
+}
+
+// ---- token-by-token recurrences -------------------------------------------------------------------------------
+//
+// A warp owns eight columns, four lanes to a column, and each lane kRpl of its dk rows in registers (rows past dk
+// are zero and stay so).  A token costs 3 dk multiply-adds a column and two sums over four lanes.  Blocks of kTok
+// tokens of q, k, v and the gates are staged in shared memory in f32.
+constexpr int kTok = 16;      // tokens staged at once
+constexpr int kCols = 32;     // columns per block of four warps
+
+template <int kRpl> constexpr int row_words() { return 4 * (kRpl + 4); }  // [4][kRpl + 4]: the lanes' reads meet no bank twice
+
+// Rows of [.., dk] into shared memory as [tok][4][kRpl + 4] f32, zero past dk and past the last token.
+template <typename T, int kRpl>
+__device__ __forceinline__ void stage_rows(float *dst, const T *src, int64_t row, int64_t stride, int n, int dk) {
+    for (int i = threadIdx.x; i < kTok * 4 * kRpl; i += blockDim.x) {
+        const int t = i / (4 * kRpl), r = i % (4 * kRpl);
+        dst[t * row_words<kRpl>() + (r / kRpl) * (kRpl + 4) + r % kRpl] =
+            t < n && r < dk ? to_f32(src[(row + t) * stride + r]) : 0.f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void stage_cols(float *dst, const T *src, int64_t row, int64_t stride, int n, int col, int dv) {
+    for (int i = threadIdx.x; i < kTok * kCols; i += blockDim.x) {
+        const int t = i / kCols, c = i % kCols;
+        dst[i] = t < n && col + c < dv ? to_f32(src[(row + t) * stride + c]) : 0.f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void write_cols(T *dst, const float *src, int64_t row, int64_t stride, int n, int col, int dv) {
+    for (int i = threadIdx.x; i < kTok * kCols; i += blockDim.x) {
+        const int t = i / kCols, c = i % kCols;
+        if (t < n && col + c < dv) dst[(row + t) * stride + c] = from_f32<T>(src[i]);
+    }
+}
+__device__ __forceinline__ float sum4(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+
+// Forward: out (or, for the gradient, the residuals r = v - a k S in f32 and the state before every 64th token).
+template <typename T, int kRpl>
+__global__ void __launch_bounds__(128)
+delta_rec_fwd_kernel(Shape p, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+                     const void *__restrict__ g, const void *__restrict__ beta, const float *__restrict__ h0,
+                     T *__restrict__ out, float *__restrict__ hT, float *__restrict__ resid, float *__restrict__ states) {
+    __shared__ __align__(16) float ks[kTok * row_words<kRpl>()], qs[kTok * row_words<kRpl>()];
+    __shared__ float vs[kTok * kCols], al[kTok], be[kTok];
+    const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / p.group();
+    const int col0 = blockIdx.y * kCols;
+    const int lane = threadIdx.x & 31, sub = lane & 3, c = (threadIdx.x >> 5) * 8 + (lane >> 2);
+    const bool live = col0 + c < p.dv;
+    SeqRange r;
+    if (!seq_range(s, p.T, p.cu, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
+    const int64_t chain = ((int64_t)s * p.H + h) * p.dk * p.dv + col0 + c;
+    float S[kRpl];
+#pragma unroll
+    for (int i = 0; i < kRpl; ++i) {
+        const int row = sub * kRpl + i;
+        S[i] = h0 != nullptr && live && row < p.dk ? h0[chain + (int64_t)row * p.dv] : 0.f;
+    }
+    const int64_t slot0 = r.start / 64 + s;
+    for (int64_t t0 = 0; t0 < r.len; t0 += kTok) {
+        const int n = (int)(r.len - t0 < kTok ? r.len - t0 : kTok);
+        const int64_t row = r.start + t0;
+        if (states != nullptr && (t0 & 63) == 0) {
+            float *to = states + ((slot0 + t0 / 64) * p.H + h) * p.dk * p.dv + col0 + c;
+#pragma unroll
+            for (int i = 0; i < kRpl; ++i)
+                if (live && sub * kRpl + i < p.dk) to[(int64_t)(sub * kRpl + i) * p.dv] = S[i];
+        }
+        __syncthreads();  // the last block's outputs have been written from vs
+        stage_rows<T, kRpl>(ks, k + (int64_t)hk * p.dk, row, (int64_t)p.Hk * p.dk, n, p.dk);
+        if (out != nullptr) stage_rows<T, kRpl>(qs, q + (int64_t)hk * p.dk, row, (int64_t)p.Hk * p.dk, n, p.dk);
+        stage_cols(vs, v + (int64_t)h * p.dv + col0, row, (int64_t)p.H * p.dv, n, col0, p.dv);
+        if (threadIdx.x < n) {
+            al[threadIdx.x] = expf(load_gate<T>(g, (row + threadIdx.x) * p.H + h, p.gate_f32));
+            be[threadIdx.x] = load_gate<T>(beta, (row + threadIdx.x) * p.H + h, p.gate_f32);
+        }
+        __syncthreads();
+        for (int t = 0; t < n; ++t) {
+            const float4 *kt = reinterpret_cast<const float4 *>(ks + t * row_words<kRpl>() + sub * (kRpl + 4));
+            const float4 *qt = reinterpret_cast<const float4 *>(qs + t * row_words<kRpl>() + sub * (kRpl + 4));
+            const float a = al[t];
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int i = 0; i < kRpl / 4; ++i) {
+                const float4 kk = kt[i];
+                x = fmaf(kk.x, S[4 * i], x); y = fmaf(kk.y, S[4 * i + 1], y);
+                x = fmaf(kk.z, S[4 * i + 2], x); y = fmaf(kk.w, S[4 * i + 3], y);
+            }
+            const float res = vs[t * kCols + c] - a * sum4(x + y);
+            const float u = be[t] * res;
+            x = y = 0.f;
+            if (out != nullptr) {
+#pragma unroll
+                for (int i = 0; i < kRpl / 4; ++i) {
+                    const float4 kk = kt[i], qq = qt[i];
+                    S[4 * i] = fmaf(a, S[4 * i], kk.x * u); x = fmaf(qq.x, S[4 * i], x);
+                    S[4 * i + 1] = fmaf(a, S[4 * i + 1], kk.y * u); y = fmaf(qq.y, S[4 * i + 1], y);
+                    S[4 * i + 2] = fmaf(a, S[4 * i + 2], kk.z * u); x = fmaf(qq.z, S[4 * i + 2], x);
+                    S[4 * i + 3] = fmaf(a, S[4 * i + 3], kk.w * u); y = fmaf(qq.w, S[4 * i + 3], y);
+                }
+                x = sum4(x + y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kRpl / 4; ++i) {
+                    const float4 kk = kt[i];
+                    S[4 * i] = fmaf(a, S[4 * i], kk.x * u);
+                    S[4 * i + 1] = fmaf(a, S[4 * i + 1], kk.y * u);
+                    S[4 * i + 2] = fmaf(a, S[4 * i + 2], kk.z * u);
+                    S[4 * i + 3] = fmaf(a, S[4 * i + 3], kk.w * u);
+                }
+                x = res;
+            }
+            __syncwarp();
+            if (sub == 0) vs[t * kCols + c] = x;  // a column's v is read by its own four lanes only
+        }
+        __syncthreads();
+        if (out != nullptr) write_cols(out + (int64_t)h * p.dv + col0, vs, row, (int64_t)p.H * p.dv, n, col0, p.dv);
+        else write_cols(resid + (int64_t)h * p.dv + col0, vs, row, (int64_t)p.H * p.dv, n, col0, p.dv);
+    }
+    if (hT != nullptr && live) {
+#pragma unroll
+        for (int i = 0; i < kRpl; ++i)
+            if (sub * kRpl + i < p.dk) hT[chain + (int64_t)(sub * kRpl + i) * p.dv] = S[i];
+    }
+}
+
+// Backward in time.  dS is the gradient with respect to the state after token t:
+//     dS += q^T do,  y = k dS,  dv = beta y,  dS <- a (dS - k^T dv).
+// Writes dv, y (f32) and dS at the end of every 64 tokens of a sequence, before the token's own q^T do.
+template <typename T, int kRpl>
+__global__ void __launch_bounds__(128)
+delta_rec_bwd_kernel(Shape p, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ dout,
+                     const void *__restrict__ g, const void *__restrict__ beta, const float *__restrict__ dhT,
+                     T *__restrict__ dv, float *__restrict__ ys, float *__restrict__ states, float *__restrict__ dh0) {
+    __shared__ __align__(16) float ks[kTok * row_words<kRpl>()], qs[kTok * row_words<kRpl>()];
+    __shared__ float vs[kTok * kCols], al[kTok], be[kTok];
+    const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / p.group();
+    const int col0 = blockIdx.y * kCols;
+    const int lane = threadIdx.x & 31, sub = lane & 3, c = (threadIdx.x >> 5) * 8 + (lane >> 2);
+    const bool live = col0 + c < p.dv;
+    SeqRange r;
+    if (!seq_range(s, p.T, p.cu, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
+    const int64_t chain = ((int64_t)s * p.H + h) * p.dk * p.dv + col0 + c;
+    float S[kRpl];
+#pragma unroll
+    for (int i = 0; i < kRpl; ++i) {
+        const int row = sub * kRpl + i;
+        S[i] = dhT != nullptr && live && row < p.dk ? dhT[chain + (int64_t)row * p.dv] : 0.f;
+    }
+    const int64_t slot0 = r.start / 64 + s;
+    for (int64_t t0 = r.len > 0 ? (r.len - 1) / kTok * kTok : -1; t0 >= 0; t0 -= kTok) {
+        const int n = (int)(r.len - t0 < kTok ? r.len - t0 : kTok);
+        const int64_t row = r.start + t0;
+        if (((t0 + kTok) & 63) == 0 || t0 + kTok >= r.len) {
+            float *to = states + ((slot0 + t0 / 64) * p.H + h) * p.dk * p.dv + col0 + c;
+#pragma unroll
+            for (int i = 0; i < kRpl; ++i)
+                if (live && sub * kRpl + i < p.dk) to[(int64_t)(sub * kRpl + i) * p.dv] = S[i];
+        }
+        __syncthreads();
+        stage_rows<T, kRpl>(ks, k + (int64_t)hk * p.dk, row, (int64_t)p.Hk * p.dk, n, p.dk);
+        stage_rows<T, kRpl>(qs, q + (int64_t)hk * p.dk, row, (int64_t)p.Hk * p.dk, n, p.dk);
+        stage_cols(vs, dout + (int64_t)h * p.dv + col0, row, (int64_t)p.H * p.dv, n, col0, p.dv);
+        if (threadIdx.x < n) {
+            al[threadIdx.x] = expf(load_gate<T>(g, (row + threadIdx.x) * p.H + h, p.gate_f32));
+            be[threadIdx.x] = load_gate<T>(beta, (row + threadIdx.x) * p.H + h, p.gate_f32);
+        }
+        __syncthreads();
+        for (int t = n - 1; t >= 0; --t) {
+            const float4 *kt = reinterpret_cast<const float4 *>(ks + t * row_words<kRpl>() + sub * (kRpl + 4));
+            const float4 *qt = reinterpret_cast<const float4 *>(qs + t * row_words<kRpl>() + sub * (kRpl + 4));
+            const float a = al[t], d = vs[t * kCols + c];
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int i = 0; i < kRpl / 4; ++i) {
+                const float4 kk = kt[i], qq = qt[i];
+                S[4 * i] = fmaf(qq.x, d, S[4 * i]); x = fmaf(kk.x, S[4 * i], x);
+                S[4 * i + 1] = fmaf(qq.y, d, S[4 * i + 1]); y = fmaf(kk.y, S[4 * i + 1], y);
+                S[4 * i + 2] = fmaf(qq.z, d, S[4 * i + 2]); x = fmaf(kk.z, S[4 * i + 2], x);
+                S[4 * i + 3] = fmaf(qq.w, d, S[4 * i + 3]); y = fmaf(kk.w, S[4 * i + 3], y);
+            }
+            x = sum4(x + y);
+            const float w = be[t] * x;
+#pragma unroll
+            for (int i = 0; i < kRpl / 4; ++i) {
+                const float4 kk = kt[i];
+                S[4 * i] = a * fmaf(-kk.x, w, S[4 * i]);
+                S[4 * i + 1] = a * fmaf(-kk.y, w, S[4 * i + 1]);
+                S[4 * i + 2] = a * fmaf(-kk.z, w, S[4 * i + 2]);
+                S[4 * i + 3] = a * fmaf(-kk.w, w, S[4 * i + 3]);
+            }
+            __syncwarp();
+            if (sub == 0) vs[t * kCols + c] = x;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < n * kCols; i += blockDim.x) {
+            const int t = i / kCols, cc = i % kCols;
+            if (col0 + cc < p.dv) {
+                const int64_t at = ((row + t) * p.H + h) * p.dv + col0 + cc;
+                ys[at] = vs[i];
+                dv[at] = from_f32<T>(be[t] * vs[i]);
+            }
+        }
+    }
+    if (dh0 != nullptr && live) {
+#pragma unroll
+        for (int i = 0; i < kRpl; ++i)
+            if (sub * kRpl + i < p.dk) dh0[chain + (int64_t)(sub * kRpl + i) * p.dv] = S[i];
+    }
+}
+
+// ---- gradient of the shared inputs ------------------------------------------------------------------------------
+//
+// Given the residuals r, the y of the backward recurrence and, for a chunk of 64 tokens, the state S0 before it
+// and the gradient dS1 after it, everything else is local to the chunk.  With D_ij the decay from token j to i,
+// c_i from the chunk's start to i, d_j from j to its end and kappa = K K^T:
+//     R_ij = beta_j D_ij (do_i . r_j), j <= i        N_ij = -beta_i beta_j D_ij (y_i . r_j), j < i
+//     dq_i = c_i do_i S0^T + sum_j R_ij k_j
+//     dk_i = d_i beta_i r_i dS1^T - c_i beta_i y_i S0^T + sum_j (R_ji q_j + (N_ij + N_ji) k_j)
+//     dbeta_i = y_i . r_i
+//     dg_l = sum_{j < l <= i} (R_ij q_i.k_j + N_ij kappa_ij) + sum_{i >= l} w_i + sum_{j < l} x_j + c_63 <S0, dS1>
+// where w_i = q_i . (c_i do_i S0^T) - k_i . (c_i beta_i y_i S0^T) and x_j = k_j . (d_j beta_j r_j dS1^T): each term of
+// the loss crosses the decay of token l if it starts before l and is read at or after it.
+constexpr int kG = 64;        // chunk of the gradient
+constexpr int kGP = kG + 1;
+
+struct Tiles {
+    float (*a)[kG + 4];
+    float (*b)[kG + 4];
+};
+
+// f(i, n, sum_k fa(i, k) fb(k, n)) for i < 64 and n < N, 4 x 4 a thread; 256 threads, all of them call f for
+// whole micro-tiles (n >= N included, with a zero sum).
+template <class FA, class FB, class F>
+__device__ __forceinline__ void tile_product(Tiles sm, int N, int K, FA fa, FB fb, F f) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    for (int n0 = 0; n0 < N; n0 += kG) {
+        float acc[4][4] = {};
+        for (int k0 = 0; k0 < K; k0 += 16) {
+            __syncthreads();
+            for (int e = threadIdx.x; e < 16 * kG; e += 256) {
+                const int i = e >> 4, kk = e & 15;
+                sm.a[kk][i] = k0 + kk < K ? fa(i, k0 + kk) : 0.f;
+            }
+            for (int e = threadIdx.x; e < 16 * kG; e += 256) {
+                const int kk = e >> 6, n = e & 63;
+                sm.b[kk][n] = k0 + kk < K && n0 + n < N ? fb(k0 + kk, n0 + n) : 0.f;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int kk = 0; kk < 16; ++kk) {
+                const float4 x = *reinterpret_cast<const float4 *>(&sm.a[kk][ty * 4]);
+                const float4 y = *reinterpret_cast<const float4 *>(&sm.b[kk][tx * 4]);
+                const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[i], ys[j], acc[i][j]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f(ty * 4 + i, n0 + tx * 4 + j, i, acc[i][j]);
+    }
+    __syncthreads();
+}
+
+// to[i] = the sum over the 16 threads of a row of part[i]: one writer a row, a fixed order.
+__device__ __forceinline__ void row_sums(float *to, float (&part)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float x = part[i];
+        for (int m = 8; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+        if ((threadIdx.x & 15) == 0) to[(threadIdx.x >> 4) * 4 + i] += x;
+        part[i] = 0.f;
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+delta_grad_simt_kernel(Shape p, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ dout,
+                       const void *__restrict__ g, const void *__restrict__ beta, const float *__restrict__ resid,
+                       const float *__restrict__ ys, const float *__restrict__ s0, const float *__restrict__ ds1,
+                       T *__restrict__ dq, T *__restrict__ dk, void *__restrict__ dg, void *__restrict__ dbeta) {
+    extern __shared__ __align__(16) float sm[];
+    const int64_t slot = blockIdx.x / p.Hk;
+    const int hk = blockIdx.x % p.Hk;
+    ChunkAt at;
+    if (!chunk_of_slot<kG>(slot, p, at)) return;
+    const int L = at.len, dkk = p.dk, dvv = p.dv, tid = threadIdx.x;
+    float *kap = sm, *qk = kap + kG * kGP, *R = qk + kG * kGP, *Nm = R + kG * kGP;  // [64][65] each
+    float *aq = Nm + kG * kGP, *ak = aq + kG * dkk;                                 // [64][dk] each
+    float *al = ak + kG * dkk, *be = al + kG, *c = be + kG, *d = c + kG, *w = d + kG, *x = w + kG, *rs = x + kG,
+          *cs = rs + kG, *part = cs + kG;                                            // [64] each, part [8]
+    Tiles tl{reinterpret_cast<float(*)[kG + 4]>(part + 8), reinterpret_cast<float(*)[kG + 4]>(part + 8 + 16 * (kG + 4))};
+    const T *kr = k + (at.row * p.Hk + hk) * dkk, *qr = q + (at.row * p.Hk + hk) * dkk;
+    const int64_t kst = (int64_t)p.Hk * dkk, vst = (int64_t)p.H * dvv;
+    auto K = [&](int i, int n) { return i < L ? to_f32(kr[i * kst + n]) : 0.f; };
+    auto Q = [&](int i, int n) { return i < L ? to_f32(qr[i * kst + n]) : 0.f; };
+    for (int i = tid; i < 2 * kG * dkk; i += 256) aq[i] = 0.f;  // aq and ak
+    tile_product(tl, kG, dkk, K, [&](int kk, int n) { return K(n, kk); },
+                 [&](int i, int n, int, float s) { kap[i * kGP + n] = s; });
+    tile_product(tl, kG, dkk, Q, [&](int kk, int n) { return K(n, kk); },
+                 [&](int i, int n, int, float s) { qk[i * kGP + n] = s; });
+    for (int h = hk * p.group(); h < (hk + 1) * p.group(); ++h) {
+        const int64_t vat = (at.row * p.H + h) * dvv, sat = (slot * p.H + h) * dkk * dvv;
+        const T *dor = dout + vat;
+        const float *rr = resid + vat, *yr = ys + vat, *S0 = s0 + sat, *S1 = ds1 + sat;
+        auto DO = [&](int i, int n) { return i < L ? to_f32(dor[i * vst + n]) : 0.f; };
+        auto RR = [&](int i, int n) { return i < L ? rr[i * vst + n] : 0.f; };
+        auto Y = [&](int i, int n) { return i < L ? yr[i * vst + n] : 0.f; };
+        __syncthreads();
+        if (tid < kG) {
+            al[tid] = tid < L ? expf(load_gate<T>(g, (at.row + tid) * p.H + h, p.gate_f32)) : 1.f;
+            be[tid] = tid < L ? load_gate<T>(beta, (at.row + tid) * p.H + h, p.gate_f32) : 0.f;
+            w[tid] = x[tid] = 0.f;
+        }
+        __syncthreads();
+        if (tid < kG) {  // column tid of D as running products of the decays: no difference of logarithms
+            float f = 0.f;
+            for (int i = 0; i < kG; ++i) {
+                f = i == tid ? 1.f : f * al[i];
+                R[i * kGP + tid] = Nm[i * kGP + tid] = f;
+            }
+            d[tid] = f;
+        } else if (tid == kG) {
+            float f = 1.f;
+            for (int i = 0; i < kG; ++i) c[i] = f *= al[i];
+        }
+        float rp[4] = {};
+        tile_product(tl, kG, dvv, DO, [&](int kk, int n) { return RR(n, kk); }, [&](int i, int n, int, float s) {
+            R[i * kGP + n] = n <= i ? R[i * kGP + n] * be[n] * s : 0.f;
+        });
+        tile_product(tl, kG, dvv, Y, [&](int kk, int n) { return RR(n, kk); }, [&](int i, int n, int, float s) {
+            Nm[i * kGP + n] = n < i ? -(Nm[i * kGP + n] * be[n] * be[i]) * s : 0.f;
+            if (n == i && i < L) store_gate<T>(dbeta, (at.row + i) * p.H + h, p.gate_f32, s);
+        });
+        auto S0T = [&](int kk, int n) { return S0[(int64_t)n * dvv + kk]; };
+        tile_product(tl, dkk, dvv, DO, S0T, [&](int i, int n, int m, float s) {
+            if (n < dkk) {
+                s *= c[i];
+                aq[i * dkk + n] += s;
+                rp[m] = fmaf(Q(i, n), s, rp[m]);
+            }
+        });
+        tile_product(tl, dkk, dvv, Y, S0T, [&](int i, int n, int m, float s) {
+            if (n < dkk) {
+                s *= -c[i] * be[i];
+                ak[i * dkk + n] += s;
+                rp[m] = fmaf(K(i, n), s, rp[m]);
+            }
+        });
+        row_sums(w, rp);
+        tile_product(tl, dkk, dvv, RR, [&](int kk, int n) { return S1[(int64_t)n * dvv + kk]; },
+                     [&](int i, int n, int m, float s) {
+                         if (n < dkk) {
+                             s *= d[i] * be[i];
+                             ak[i * dkk + n] += s;
+                             rp[m] = fmaf(K(i, n), s, rp[m]);
+                         }
+                     });
+        row_sums(x, rp);
+        tile_product(tl, dkk, kG, [&](int i, int kk) { return R[i * kGP + kk]; }, K,
+                     [&](int i, int n, int, float s) { if (n < dkk) aq[i * dkk + n] += s; });
+        tile_product(tl, dkk, kG, [&](int i, int kk) { return R[kk * kGP + i]; }, Q,
+                     [&](int i, int n, int, float s) { if (n < dkk) ak[i * dkk + n] += s; });
+        tile_product(tl, dkk, kG, [&](int i, int kk) { return Nm[i * kGP + kk] + Nm[kk * kGP + i]; }, K,
+                     [&](int i, int n, int, float s) { if (n < dkk) ak[i * dkk + n] += s; });
+        float inner = 0.f;
+        for (int i = tid; i < dkk * dvv; i += 256) inner = fmaf(S0[i], S1[i], inner);
+        for (int m = 16; m > 0; m >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, m);
+        if ((tid & 31) == 0) part[tid >> 5] = inner;
+        if (tid < kG) {  // row and column sums of z_ij = R_ij q_i.k_j + N_ij kappa_ij over j < i
+            float a = 0.f, b = 0.f;
+            for (int j = 0; j < kG; ++j) {
+                if (j < tid) a += R[tid * kGP + j] * qk[tid * kGP + j] + Nm[tid * kGP + j] * kap[tid * kGP + j];
+                if (j > tid) b += R[j * kGP + tid] * qk[j * kGP + tid] + Nm[j * kGP + tid] * kap[j * kGP + tid];
+            }
+            rs[tid] = a;
+            cs[tid] = b;
+        }
+        __syncthreads();
+        if (tid < L) {
+            float f = 0.f;
+            for (int m = 0; m < 8; ++m) f += part[m];
+            f *= c[kG - 1];
+            for (int m = 0; m < tid; ++m) f += (cs[m] - rs[m]) + x[m];
+            for (int m = tid; m < kG; ++m) f += w[m];
+            store_gate<T>(dg, (at.row + tid) * p.H + h, p.gate_f32, f);
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < L * dkk; i += 256) {
+        const int t = i / dkk, n = i % dkk;
+        dq[(at.row + t) * kst + (int64_t)hk * dkk + n] = from_f32<T>(aq[i]);
+        dk[(at.row + t) * kst + (int64_t)hk * dkk + n] = from_f32<T>(ak[i]);
+    }
+}
+
+size_t grad_simt_smem(int dk) {
+    return (size_t)(4 * kG * kGP + 2 * kG * dk + 8 * kG + 8 + 2 * 16 * (kG + 4)) * sizeof(float);
+}
+
+int check_launch(int n) {
+    count_launches(n);
+    return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
+}
+
+// rows of the state a lane holds: a quarter of dk, rounded up to what the kernels are built for
+#define GLA_BY_ROWS(dk, CALL)      \
+    do {                           \
+        if (dk <= 32) { CALL(8); } \
+        else if (dk <= 64) { CALL(16); } \
+        else if (dk <= 96) { CALL(24); } \
+        else if (dk <= 128) { CALL(32); } \
+        else { CALL(64); }         \
+    } while (0)
+
+template <typename T>
+int rec_fwd(const Shape &p, const T *q, const T *k, const T *v, const void *g, const void *beta, const float *h0,
+            T *out, float *hT, float *resid, float *states, cudaStream_t st) {
+    const dim3 grid((unsigned)((long long)p.nseq * p.H), (unsigned)((p.dv + kCols - 1) / kCols));
+#define GLA_CALL(R) \
+    delta_rec_fwd_kernel<T, R><<<grid, 128, 0, st>>>(p, q, k, v, g, beta, h0, out, hT, resid, states)
+    GLA_BY_ROWS(p.dk, GLA_CALL);
+#undef GLA_CALL
+    return check_launch(1);
+}
+
+}  // namespace
+
+size_t simt_bwd_workspace(const Shape &p) {
+    const size_t rows = (size_t)total_rows(p) * p.H * p.dv;
+    const size_t state = (size_t)chunk_slots(total_rows(p), p.nseq, kG) * p.H * p.dk * p.dv;
+    return 2 * (rows + state) * sizeof(float);
+}
+
+template <typename T>
+int simt_fwd(const Shape &p, const T *q, const T *k, const T *v, const void *g, const void *beta, const float *h0,
+             T *out, float *hT, cudaStream_t st) {
+    return rec_fwd<T>(p, q, k, v, g, beta, h0, out, hT, nullptr, nullptr, st);
+}
+
+template <typename T>
+int simt_bwd(const Shape &p, const T *q, const T *k, const T *v, const void *g, const void *beta, const T *dout,
+             const float *h0, const float *dhT, T *dq, T *dk, T *dv, void *dg, void *dbeta, float *dh0, void *ws,
+             cudaStream_t st) {
+    const long long rows = total_rows(p), slots = chunk_slots(rows, p.nseq, kG);
+    if (slots * p.Hk > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
+    const size_t state = (size_t)slots * p.H * p.dk * p.dv;
+    float *s0 = (float *)ws, *ds1 = s0 + state, *resid = ds1 + state, *ys = resid + (size_t)rows * p.H * p.dv;
+    int rc = rec_fwd<T>(p, q, k, v, g, beta, h0, nullptr, nullptr, resid, s0, st);
+    if (rc != GLA_OK) return rc;
+    const dim3 grid((unsigned)((long long)p.nseq * p.H), (unsigned)((p.dv + kCols - 1) / kCols));
+#define GLA_CALL(R) \
+    delta_rec_bwd_kernel<T, R><<<grid, 128, 0, st>>>(p, q, k, dout, g, beta, dhT, dv, ys, ds1, dh0)
+    GLA_BY_ROWS(p.dk, GLA_CALL);
+#undef GLA_CALL
+    rc = check_launch(1);
+    if (rc != GLA_OK || rows == 0) return rc;
+    const size_t bytes = grad_simt_smem(p.dk);
+    if (cudaFuncSetAttribute(delta_grad_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
+        cudaSuccess)
+        return GLA_ERR_LAUNCH;
+    delta_grad_simt_kernel<T><<<(unsigned)(slots * p.Hk), 256, bytes, st>>>(p, q, k, dout, g, beta, resid, ys, s0, ds1,
+                                                                            dq, dk, dg, dbeta);
+    return check_launch(1);
+}
+
+template int simt_fwd<float>(const Shape &, const float *, const float *, const float *, const void *, const void *,
+                             const float *, float *, float *, cudaStream_t);
+template int simt_fwd<__nv_bfloat16>(const Shape &, const __nv_bfloat16 *, const __nv_bfloat16 *, const __nv_bfloat16 *,
+                                     const void *, const void *, const float *, __nv_bfloat16 *, float *, cudaStream_t);
+template int simt_bwd<float>(const Shape &, const float *, const float *, const float *, const void *, const void *,
+                             const float *, const float *, const float *, float *, float *, float *, void *, void *,
+                             float *, void *, cudaStream_t);
+template int simt_bwd<__nv_bfloat16>(const Shape &, const __nv_bfloat16 *, const __nv_bfloat16 *,
+                                     const __nv_bfloat16 *, const void *, const void *, const __nv_bfloat16 *,
+                                     const float *, const float *, __nv_bfloat16 *, __nv_bfloat16 *, __nv_bfloat16 *,
+                                     void *, void *, float *, void *, cudaStream_t);
+
+int decode_step(const void *q, const void *k, const void *v, const void *g, const void *beta, float *state,
+                const int32_t *slots, int nslots, void *out, int N, int H, int Hk, int dk, int dv, int dtype,
+                int gate_dtype, cudaStream_t st) {
+    using B = __nv_bfloat16;
+    const int gf = gate_dtype == GLA_F32;
+    if (dtype == GLA_F32)
+        return launch_step<float>((const float *)q, (const float *)k, (const float *)v, g, beta, gf, state, slots,
+                                  nslots, (float *)out, N, H, Hk, dk, dv, st);
+    return launch_step<B>((const B *)q, (const B *)k, (const B *)v, g, beta, gf, state, slots, nslots, (B *)out, N, H,
+                          Hk, dk, dv, st);
+}
+
+}  // namespace delta
+}  // namespace gla

@@ -10,6 +10,7 @@ library is missing this module raises instead of computing anything itself.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -24,7 +25,7 @@ STATUS = {0: "GLA_OK", -1: "GLA_ERR_ARG", -2: "GLA_ERR_UNSUPPORTED", -3: "GLA_ER
           -5: "GLA_ERR_TIMEOUT", -6: "GLA_ERR_NOMEM", -7: "GLA_ERR_DEVICE_ARG", -8: "GLA_ERR_SCRATCH_LIMIT"}
 
 # C signatures (argtypes, restype) of every exported entry point, as declared in include/gla.h
-_P, _I = ctypes.c_void_p, ctypes.c_int
+_P, _I, _L, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
 SIGNATURES = {
     "gla_chunk_fwd": ([_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P], _I),
     "gla_chunk_fwd_gated": ([_P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P], _I),
@@ -45,6 +46,13 @@ SIGNATURES = {
     "gla_conv1d_silu": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P], _I),
     "gla_conv1d_silu_f32": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P], _I),
     "gla_conv1d_silu_step": ([_P, _P, _P, _P, _P, _I, _I, _P], _I),
+    "gla_delta_workspace_bytes": ([_I] * 9, _L),
+    "gla_delta_chunk_fwd": ([_P] * 8 + [_I] * 8 + [_P, _P, _L, _P], _I),
+    "gla_delta_chunk_bwd": ([_P] * 14 + [_I] * 8 + [_P, _P, _L, _P], _I),
+    "gla_delta_decode_step": ([_P] * 7 + [_I, _P] + [_I] * 7 + [_P], _I),
+    "gla_group_norm": ([_P, _P, _P, _P, _I, _F, _P, _L, _I, _I, _I, _P], _I),
+    "gla_group_norm_workspace_bytes": ([_L, _I, _I], _L),
+    "gla_group_norm_bwd": ([_P, _P, _P, _P, _P, _I, _F, _P, _P, _P, _P, _L, _I, _I, _I, _P, _L, _P], _I),
     "gla_last_device_status": ([_P], _I),
     "gla_status_str": ([_I], ctypes.c_char_p),
     "gla_chunk_kernel": ([_I, _I, _I, _I, _I], _I),
@@ -433,6 +441,179 @@ def gla_conv1d_silu_step(x, weight, bias, state_inout, y, stream=None) -> None:
     _raise(rc, "gla_conv1d_silu_step")
 
 
+# ---- gated delta rule and group normalisation ---------------------------------------------------
+
+ACT_NONE, ACT_SILU, ACT_SIGMOID = 0, 1, 2  # gla_act
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float32:
+        return F32
+    raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+
+
+def _delta_args(q, k, v, g, beta, h0, out, hT, cu_seqlens):
+    """Checks shared by the chunked delta entry points; returns the sizes and types of the C call."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be [B, T, Hk, dk] and v [B, T, H, dv] (packed: B = 1)")
+    B, T, Hk, dk = q.shape
+    H, dv = v.shape[2:]
+    dtype, gates = _dtype(q, "q"), _dtype(g, "g")
+    if Hk == 0 or H % Hk:
+        raise ValueError(f"the {H} value heads must be a multiple of the {Hk} key heads")
+    if gates != F32 and gates != dtype:
+        raise ValueError("g and beta must be torch.float32 or of the type of q")
+    _check(q, "q", q.dtype)
+    _check(k, "k", q.dtype, (B, T, Hk, dk))
+    _check(v, "v", q.dtype, (B, T, H, dv))
+    _check(g, "g", g.dtype, (B, T, H))
+    _check(beta, "beta", g.dtype, (B, T, H))
+    _check(out, "out", q.dtype, (B, T, H, dv))
+    nseq = B
+    if cu_seqlens is not None:
+        if B != 1:
+            raise ValueError("a packed batch has leading dimension 1")
+        _check(cu_seqlens, "cu_seqlens", torch.int32)
+        nseq = cu_seqlens.numel() - 1
+    _check(h0, "h0", torch.float32, (nseq, H, dk, dv), allow_none=True)
+    _check(hT, "hT", torch.float32, (nseq, H, dk, dv), allow_none=True)
+    return nseq, T, H, Hk, dk, dv, dtype, gates
+
+
+def gla_delta_workspace_bytes(op: int, B: int, T: int, H: int, Hk: int, dk: int, dv: int, dtype: int,
+                              packed: bool) -> int:
+    """Workspace bytes of gla_delta_chunk_fwd (OP_FORWARD) or gla_delta_chunk_bwd (OP_BACKWARD)."""
+    n = int(load().gla_delta_workspace_bytes(int(op), int(B), int(T), int(H), int(Hk), int(dk), int(dv), int(dtype),
+                                             int(bool(packed))))
+    if n < 0:
+        raise GLAError(n, "gla_delta_workspace_bytes")
+    return n
+
+
+def _allocating_on(stream, device):
+    """Memory that a call on ``stream`` writes comes from that stream's pool, so that it can neither still be in
+    use by earlier work of another stream nor be handed out again before the call's work is done."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _workspace(given, need: int, device, stream):
+    """The caller's workspace, or one from torch's allocator that stays valid for work on ``stream``."""
+    if given is not None:
+        if not given.is_cuda or not given.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        return given, given.numel() * given.element_size()
+    if need == 0:
+        return None, 0
+    with _allocating_on(stream, device):
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+
+
+def gla_delta_chunk_fwd(q, k, v, g, beta, h0, out, hT, cu_seqlens=None, workspace=None, stream=None) -> None:
+    """Gated delta rule over whole sequences: writes ``out`` and (if given) ``hT``.  ``workspace``: at least
+    gla_delta_workspace_bytes(OP_FORWARD, ...) bytes, or None to take it from torch.  See include/gla.h."""
+    nseq, T, H, Hk, dk, dv, dtype, gates = _delta_args(q, k, v, g, beta, h0, out, hT, cu_seqlens)
+    need = gla_delta_workspace_bytes(OP_FORWARD, nseq, T, H, Hk, dk, dv, dtype, cu_seqlens is not None)
+    ws, n = _workspace(workspace, need, q.device, stream)
+    rc = load().gla_delta_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(out), _ptr(hT), nseq,
+                                    T, H, Hk, dk, dv, dtype, gates, _ptr(cu_seqlens), _ptr(ws), n, _stream(stream))
+    _raise(rc, "gla_delta_chunk_fwd")
+
+
+def gla_delta_chunk_bwd(q, k, v, g, beta, dout, h0, dhT, dq, dk, dv, dg, dbeta, dh0, cu_seqlens=None, workspace=None,
+                        stream=None) -> None:
+    """Gradients of gla_delta_chunk_fwd: writes dq, dk, dv, dg, dbeta and (if given) dh0.  See include/gla.h."""
+    nseq, T, H, Hk, dk_, dv_, dtype, gates = _delta_args(q, k, v, g, beta, h0, dout, dhT, cu_seqlens)
+    _check(dq, "dq", q.dtype, tuple(q.shape))
+    _check(dk, "dk", q.dtype, tuple(q.shape))
+    _check(dv, "dv", q.dtype, tuple(v.shape))
+    _check(dg, "dg", g.dtype, tuple(g.shape))
+    _check(dbeta, "dbeta", g.dtype, tuple(g.shape))
+    _check(dh0, "dh0", torch.float32, (nseq, H, dk_, dv_), allow_none=True)
+    need = gla_delta_workspace_bytes(OP_BACKWARD, nseq, T, H, Hk, dk_, dv_, dtype, cu_seqlens is not None)
+    ws, n = _workspace(workspace, need, q.device, stream)
+    rc = load().gla_delta_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(dout), _ptr(h0), _ptr(dhT),
+                                    _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dh0), nseq, T, H, Hk, dk_,
+                                    dv_, dtype, gates, _ptr(cu_seqlens), _ptr(ws), n, _stream(stream))
+    _raise(rc, "gla_delta_chunk_bwd")
+
+
+def gla_delta_decode_step(q, k, v, g, beta, state, out, slots=None, stream=None) -> None:
+    """One token of the gated delta rule for N sequences, in place on ``state`` [N, H, dk, dv], or with ``slots``
+    on pages of a pool [nslots, H, dk, dv] (negative slot: padding row, zero out).  See include/gla.h."""
+    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
+        raise ValueError("q must be [N, Hk, dk], v [N, H, dv] and state [.., H, dk, dv]")
+    N, Hk, dk = q.shape
+    H, dv = v.shape[1:]
+    dtype, gates = _dtype(q, "q"), _dtype(g, "g")
+    if Hk == 0 or H % Hk:
+        raise ValueError(f"the {H} value heads must be a multiple of the {Hk} key heads")
+    if gates != F32 and gates != dtype:
+        raise ValueError("g and beta must be torch.float32 or of the type of q")
+    _check(q, "q", q.dtype)
+    _check(k, "k", q.dtype, (N, Hk, dk))
+    _check(v, "v", q.dtype, (N, H, dv))
+    _check(g, "g", g.dtype, (N, H))
+    _check(beta, "beta", g.dtype, (N, H))
+    _check(out, "out", q.dtype, (N, H, dv))
+    _check(state, "state", torch.float32, (state.shape[0] if slots is not None else N, H, dk, dv))
+    _check(slots, "slots", torch.int32, (N,), allow_none=True)
+    rc = load().gla_delta_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(slots),
+                                      int(state.shape[0]), _ptr(out), N, H, Hk, dk, dv, dtype, gates, _stream(stream))
+    _raise(rc, "gla_delta_decode_step")
+
+
+def _norm_args(x, weight, bias, groups, gate, out):
+    if x.dim() < 1 or groups <= 0 or x.shape[-1] % groups:
+        raise ValueError("the last dimension of x must be a multiple of groups")
+    C = x.shape[-1]
+    dtype = _dtype(x, "x")
+    _check(x, "x", x.dtype)
+    _check(out, "out", x.dtype, tuple(x.shape))
+    _check(gate, "gate", x.dtype, tuple(x.shape), allow_none=True)
+    _check(weight, "weight", torch.float32, (C,), allow_none=True)
+    _check(bias, "bias", torch.float32, (C,), allow_none=True)
+    return x.numel() // C if C else 0, C // groups, dtype
+
+
+def gla_group_norm(x, weight, bias, groups: int, out, gate=None, act: int = ACT_SILU, eps: float = 1e-5,
+                   stream=None) -> None:
+    """Group normalisation of each token's channels with an activation (of ``gate`` if given): x, gate, out
+    [..., groups * width], weight and bias [groups * width] f32 or None.  See include/gla.h."""
+    rows, width, dtype = _norm_args(x, weight, bias, int(groups), gate, out)
+    rc = load().gla_group_norm(_ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), int(act), float(eps), _ptr(out), rows,
+                               int(groups), width, dtype, _stream(stream))
+    _raise(rc, "gla_group_norm")
+
+
+def gla_group_norm_workspace_bytes(rows: int, groups: int, width: int) -> int:
+    """Workspace bytes of gla_group_norm_bwd."""
+    n = int(load().gla_group_norm_workspace_bytes(int(rows), int(groups), int(width)))
+    if n < 0:
+        raise GLAError(n, "gla_group_norm_workspace_bytes")
+    return n
+
+
+def gla_group_norm_bwd(dout, x, weight, bias, groups: int, dx, dweight, dbias, dgate=None, gate=None,
+                       act: int = ACT_SILU, eps: float = 1e-5, workspace=None, stream=None) -> None:
+    """Gradients of gla_group_norm: writes dx, dweight, dbias and (with a gate) dgate.  See include/gla.h."""
+    rows, width, dtype = _norm_args(x, weight, bias, int(groups), gate, dx)
+    _check(dout, "dout", x.dtype, tuple(x.shape))
+    _check(dgate, "dgate", x.dtype, tuple(x.shape), allow_none=gate is None)
+    _check(dweight, "dweight", torch.float32, (x.shape[-1],), allow_none=True)
+    _check(dbias, "dbias", torch.float32, (x.shape[-1],), allow_none=True)
+    ws, n = _workspace(workspace, gla_group_norm_workspace_bytes(rows, int(groups), width), x.device, stream)
+    rc = load().gla_group_norm_bwd(_ptr(dout), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), int(act), float(eps),
+                                   _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(dgate), rows, int(groups), width, dtype,
+                                   _ptr(ws), n, _stream(stream))
+    _raise(rc, "gla_group_norm_bwd")
+
+
 def gla_last_device_status(stream=None) -> int:
     """Synchronise the stream; return and clear the library's device status word."""
     return int(load().gla_last_device_status(_stream(stream)))
@@ -497,3 +678,48 @@ def decode_step(q, k, v, log_decay, state, stream=None):
     else:
         gla_decode_step(q, k, v, log_decay, state, out, stream)
     return out
+
+
+def delta_chunk_fwd(q, k, v, g, beta, h0=None, cu_seqlens=None, final_state: bool = True, stream=None):
+    """Allocate ``out`` (and ``hT``) and run the gated delta rule; returns (out, hT or None)."""
+    nseq = q.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+    with _allocating_on(stream, q.device):
+        out = torch.empty_like(v)
+        hT = torch.empty((nseq, v.shape[2], q.shape[3], v.shape[3]), dtype=torch.float32, device=q.device) \
+            if final_state else None
+    gla_delta_chunk_fwd(q, k, v, g, beta, h0, out, hT, cu_seqlens, None, stream)
+    return out, hT
+
+
+def delta_chunk_bwd(q, k, v, g, beta, dout, h0=None, dhT=None, cu_seqlens=None, stream=None):
+    """Allocate and return (dq, dk, dv, dg, dbeta, dh0) of the gated delta rule; dh0 is None without h0."""
+    with _allocating_on(stream, q.device):
+        grads = [torch.empty_like(t) for t in (q, k, v, g, beta)]
+        dh0 = None if h0 is None else torch.empty_like(h0)
+    gla_delta_chunk_bwd(q, k, v, g, beta, dout, h0, dhT, *grads, dh0, cu_seqlens, None, stream)
+    return (*grads, dh0)
+
+
+def delta_decode_step(q, k, v, g, beta, state, slots=None, stream=None):
+    """Run one gated delta step in place on ``state`` (or on pages ``slots`` of it); returns the new ``out``."""
+    with _allocating_on(stream, q.device):
+        out = torch.empty_like(v)
+    gla_delta_decode_step(q, k, v, g, beta, state, out, slots, stream)
+    return out
+
+
+def group_norm(x, weight, bias, groups: int, gate=None, act: int = ACT_SILU, eps: float = 1e-5, stream=None):
+    """Allocate and return the group normalisation of ``x`` with its activation."""
+    with _allocating_on(stream, x.device):
+        out = torch.empty_like(x)
+    gla_group_norm(x, weight, bias, groups, out, gate, act, eps, stream)
+    return out
+
+
+def group_norm_bwd(dout, x, weight, bias, groups: int, gate=None, act: int = ACT_SILU, eps: float = 1e-5, stream=None):
+    """Allocate and return (dx, dweight, dbias, dgate) of the group normalisation; dgate is None without a gate."""
+    with _allocating_on(stream, x.device):
+        dx, dgate = torch.empty_like(x), None if gate is None else torch.empty_like(gate)
+        dweight, dbias = (torch.empty(x.shape[-1], dtype=torch.float32, device=x.device) for _ in range(2))
+    gla_group_norm_bwd(dout, x, weight, bias, groups, dx, dweight, dbias, dgate, gate, act, eps, None, stream)
+    return dx, dweight, dbias, dgate

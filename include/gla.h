@@ -70,6 +70,10 @@ typedef enum {
     GLA_GATE_SIGMOID = 1  /* out = o / (1 + exp(-g)) */
 } gla_gate_kind;
 
+/* Operations and element types that entry points and queries name. */
+typedef enum { GLA_OP_FORWARD = 0, GLA_OP_FORWARD_GATED = 1, GLA_OP_BACKWARD = 2 } gla_op;
+typedef enum { GLA_BF16 = 0, GLA_F32 = 1 } gla_dtype;
+
 /*
  * gla_chunk_fwd — chunkwise-parallel prefill / training forward, bf16 q, k, v, out.
  *
@@ -435,6 +439,108 @@ GLA_API int gla_conv1d_silu_step(const void *x, const float *weight, const float
                                  void *y, int N, int D, void *stream);
 
 /*
+ * The gated delta rule.  Every (sequence, value head) chain keeps a dk x dv matrix state S like the mixer
+ * above, with a decay and a write strength per token, and writes the difference between v_t and what the
+ * state already answers to k_t:
+ *     u_t = beta_t (v_t - a_t k_t S_{t-1}),  S_t = a_t S_{t-1} + k_t^T u_t,  o_t = q_t S_t,  a_t = exp(g_t)
+ * There is no extra scale or normalisation of q and k: both belong to the caller (the recurrence is stable
+ * where beta_t |k_t|^2 <= 2 and g_t <= 0).  g_t = -inf (a_t = 0) is a full reset of the state.
+ *
+ * Heads: q and k have Hk heads, v, g, beta, out and the states H; Hk divides H, and value head h reads query
+ * and key head h / (H / Hk).  The gradients of q and k are sums over the value heads that read them.
+ *   dtype       GLA_BF16 or GLA_F32: q, k, v, out and their gradients
+ *   gate_dtype  GLA_F32, or dtype: g, beta and their gradients.  (With bf16 inputs the gradients carry the
+ *               rounding of bf16 products, about 2e-3 of their size, in either type.)
+ * All states and sums are f32.  Sizes: 16 <= dk <= 256, 16 <= dv <= 512, both multiples of 8.
+ */
+
+/*
+ * gla_delta_workspace_bytes — bytes of the workspace that gla_delta_chunk_fwd (op GLA_OP_FORWARD) or
+ * gla_delta_chunk_bwd (op GLA_OP_BACKWARD) needs for these sizes (packed: nonzero with cu_seqlens), 0 if
+ * none; negative: a gla_status for sizes that the call rejects.  The caller owns the workspace (device,
+ * 16-byte aligned) and may use it for anything else once the call's work on its stream is done.
+ */
+GLA_API long long gla_delta_workspace_bytes(int op, int B, int T, int H, int Hk, int dk, int dv, int dtype, int packed);
+
+/*
+ * gla_delta_chunk_fwd — the gated delta rule over whole sequences (prefill, training forward).
+ *   q, k        [B, T, Hk, dk];  v, out [B, T, H, dv] (out written);  g, beta [B, T, H]
+ *   h0, hT      [B, H, dk, dv] f32: initial state or NULL (zeros); final state, written, or NULL to skip
+ *   cu_seqlens  NULL, or a DEVICE int32 [B+1] of offsets into packed [1, T, ...] tensors, as gla_chunk_fwd
+ *               (an empty sequence gets hT = h0; a sequence with bad offsets is skipped and
+ *               GLA_ERR_DEVICE_ARG recorded); T = 0 (packed) leaves only empty sequences
+ *   ws, ws_bytes  workspace of at least gla_delta_workspace_bytes(GLA_OP_FORWARD, ...) bytes (else
+ *               GLA_ERR_ARG); NULL where that is 0
+ * bf16 out is rounded once; hT comes from f32 sums over unrounded products (f32 accuracy) in both types.
+ * Returns a gla_status.
+ */
+GLA_API int gla_delta_chunk_fwd(const void *q, const void *k, const void *v, const void *g, const void *beta,
+                                const float *h0, void *out, float *hT, int B, int T, int H, int Hk, int dk, int dv,
+                                int dtype, int gate_dtype, const int32_t *cu_seqlens, void *ws, long long ws_bytes,
+                                void *stream);
+
+/*
+ * gla_delta_chunk_bwd — its gradients, with L = sum(dout .* out) + sum(dhT .* hT).  With dS_t the gradient
+ * with respect to S_t, backwards in time from dS_T = dhT + q_T^T dout_T:
+ *     y_t = k_t dS_t,  dv_t = beta_t y_t,  dbeta_t = y_t . u_t / beta_t,  dq_t = dout_t S_t^T,
+ *     dk_t = u_t dS_t^T - dv_t (a_t S_{t-1})^T,  dg_t = <dS_t - k_t^T dv_t, a_t S_{t-1}>,
+ *     dS_{t-1} = a_t (dS_t - k_t^T dv_t) + q_{t-1}^T dout_{t-1},  dh0 = a_1 (dS_1 - k_1^T dv_1)
+ * The states are recomputed; nothing is kept from the forward.
+ *   dout        as out;  dhT [B, H, dk, dv] f32 or NULL (zeros)
+ *   dq, dk_out  as q, k;  dv_out as v;  dg, dbeta as g, beta: written
+ *   dh0         [B, H, dk, dv] f32, written; NULL to skip
+ *   ws, ws_bytes  workspace of at least gla_delta_workspace_bytes(GLA_OP_BACKWARD, ...) bytes
+ * No array may alias another.  Returns a gla_status.
+ */
+GLA_API int gla_delta_chunk_bwd(const void *q, const void *k, const void *v, const void *g, const void *beta,
+                                const void *dout, const float *h0, const float *dhT, void *dq, void *dk_out,
+                                void *dv_out, void *dg, void *dbeta, float *dh0, int B, int T, int H, int Hk, int dk,
+                                int dv, int dtype, int gate_dtype, const int32_t *cu_seqlens, void *ws,
+                                long long ws_bytes, void *stream);
+
+/*
+ * gla_delta_decode_step — one token of N sequences, in place on their states.
+ *   q, k        [N, Hk, dk];  v, out [N, H, dv] (out written);  g, beta [N, H]
+ *   state       [N, H, dk, dv] f32; with slots: a pool [nslots, H, dk, dv] of pages
+ *   slots       NULL (row n uses state n), or [N] int32 on the device: row n uses page slots[n]; negative: a
+ *               padding row (zero out, no page touched); >= nslots: the same, and GLA_ERR_DEVICE_ARG is
+ *               recorded.  Two rows must not name the same page.
+ *   1 <= dk <= 256; 4 <= dv <= 1024, a multiple of 4; N = 0 does nothing
+ * Makes no allocation or synchronisation: it can be captured in a CUDA graph.  Returns a gla_status.
+ */
+GLA_API int gla_delta_decode_step(const void *q, const void *k, const void *v, const void *g, const void *beta,
+                                  float *state, const int32_t *slots, int nslots, void *out, int N, int H, int Hk,
+                                  int dk, int dv, int dtype, int gate_dtype, void *stream);
+
+/*
+ * gla_group_norm — group normalisation of each token's channels (channels last, `groups` groups of `width`
+ * neighbouring channels: one to a head behind a mixer), with an activation:
+ *     h = (x - mean) / sqrt(variance + eps) over the token's group,  z = weight * h + bias,
+ *     out = z * act(gate) with a gate, act(z) without;  act: identity, SiLU or sigmoid
+ * A causal mixer may not mix statistics over time, so they are a token's own.
+ *   x, gate, out  [rows, groups * width] of dtype (GLA_BF16 or GLA_F32); gate may be NULL
+ *   weight, bias  [groups * width] f32, NULL for ones / zeros
+ *   act           a gla_act;  eps > 0
+ *   width         a multiple of 8, 8 <= width <= 2048; groups * width <= 1048576; rows >= 0
+ * Statistics and arithmetic are f32; out is rounded once.  Returns a gla_status.
+ */
+typedef enum { GLA_ACT_NONE = 0, GLA_ACT_SILU = 1, GLA_ACT_SIGMOID = 2 } gla_act;
+GLA_API int gla_group_norm(const void *x, const float *weight, const float *bias, const void *gate, int act, float eps,
+                           void *out, long long rows, int groups, int width, int dtype, void *stream);
+
+/*
+ * gla_group_norm_bwd — its gradients: dx and (with a gate) dgate like x, dweight and dbias [groups * width]
+ * f32 (either may be NULL).  The statistics are recomputed from x.  ws: device workspace of at least
+ * gla_group_norm_workspace_bytes(rows, groups, width) bytes for the blocks' sums of dweight and dbias, which are
+ * added up in a fixed order.  Returns a gla_status.
+ */
+GLA_API long long gla_group_norm_workspace_bytes(long long rows, int groups, int width);
+GLA_API int gla_group_norm_bwd(const void *dout, const void *x, const float *weight, const float *bias,
+                               const void *gate, int act, float eps, void *dx, float *dweight, float *dbias,
+                               void *dgate, long long rows, int groups, int width, int dtype, void *ws,
+                               long long ws_bytes, void *stream);
+
+/*
  * gla_last_device_status — synchronise `stream`, then return and clear the
  * device status word: GLA_OK, GLA_ERR_TIMEOUT or GLA_ERR_DEVICE_ARG for the
  * first failure recorded by any kernel of this library on the current device
@@ -467,8 +573,6 @@ GLA_API int gla_last_device_status(void *stream);
  * other case runs the f32-FMA SIMT kernel, which is correct for all of them
  * but about ten times slower on the shapes both kernels take.
  */
-typedef enum { GLA_OP_FORWARD = 0, GLA_OP_FORWARD_GATED = 1, GLA_OP_BACKWARD = 2 } gla_op;
-typedef enum { GLA_BF16 = 0, GLA_F32 = 1 } gla_dtype;
 typedef enum { GLA_KERNEL_TENSOR_CORE = 1, GLA_KERNEL_SIMT = 2 } gla_kernel_kind;
 GLA_API int gla_chunk_kernel(int op, int dtype, int dk, int dv, int chunk);
 
