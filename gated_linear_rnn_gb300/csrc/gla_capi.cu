@@ -67,6 +67,10 @@ size_t simt_bwd_workspace(const Shape &);
 template <typename T>
 int simt_bwd(const Shape &, const T *, const T *, const T *, const void *, const void *, const T *, const float *,
              const float *, T *, T *, T *, void *, void *, float *, void *, cudaStream_t);
+bool mma_supported(int dk);
+size_t mma_fwd_workspace(const Shape &);
+int mma_fwd(const Shape &, const void *, const void *, const void *, const void *, const void *, const float *, void *,
+            float *, void *, cudaStream_t);
 int decode_step(const void *, const void *, const void *, const void *, const void *, float *, const int32_t *, int,
                 void *, int, int, int, int, int, int, int, cudaStream_t);
 }  // namespace delta
@@ -78,6 +82,7 @@ int group_norm_bwd(const void *, const void *, const float *, const float *, con
                    float *, void *, void *, int64_t, int, int, int, cudaStream_t);
 }  // namespace norm
 int take_status_delta(cudaStream_t);
+int take_status_delta_mma(cudaStream_t);
 int take_status_conv(cudaStream_t);
 int take_status_simt(cudaStream_t);
 int take_status_bwd(cudaStream_t);
@@ -213,8 +218,8 @@ delta::Shape delta_shape(int B, int T, int H, int Hk, int dk, int dv, int dtype,
 }
 
 long long delta_workspace(int op, const delta::Shape &p, int dtype) {
-    (void)dtype;
-    if (op == GLA_OP_FORWARD) return 0;
+    if (op == GLA_OP_FORWARD)
+        return dtype == GLA_BF16 && delta::mma_supported(p.dk) ? (long long)delta::mma_fwd_workspace(p) : 0;
     return (long long)delta::simt_bwd_workspace(p);
 }
 
@@ -464,6 +469,7 @@ int gla_delta_chunk_fwd(const void *q, const void *k, const void *v, const void 
     if (dtype == GLA_F32)
         return delta::simt_fwd<float>(p, (const float *)q, (const float *)k, (const float *)v, g, beta, h0,
                                       (float *)out, hT, st);
+    if (delta::mma_supported(dk)) return delta::mma_fwd(p, q, k, v, g, beta, h0, out, hT, ws, st);
     return delta::simt_fwd<H16>(p, (const H16 *)q, (const H16 *)k, (const H16 *)v, g, beta, h0, (H16 *)out, hT, st);
 }
 
@@ -535,8 +541,8 @@ int gla_group_norm_bwd(const void *dout, const void *x, const float *weight, con
 int gla_last_device_status(void *stream) {
     cudaStream_t st = (cudaStream_t)stream;
     int result = GLA_OK;
-    const int parts[6] = {take_status_simt(st), take_status_decode(st), take_status_tc(st), take_status_bwd(st),
-                          take_status_conv(st), take_status_delta(st)};
+    const int parts[7] = {take_status_simt(st), take_status_decode(st), take_status_tc(st), take_status_bwd(st),
+                          take_status_conv(st), take_status_delta(st), take_status_delta_mma(st)};
     for (int p : parts) {
         if (p == GLA_ERR_LAUNCH) return GLA_ERR_LAUNCH;
         if (result == GLA_OK && p != 0) result = p;

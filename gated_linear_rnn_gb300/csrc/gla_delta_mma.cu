@@ -1,0 +1,518 @@
+// gla_delta_mma.cu — the gated delta rule over whole sequences on the tensor cores (bf16 inputs).
+//
+// A chunk of C = 32 tokens with D_ij the decay from token j to token i (1 for i = j), c_i the decay from the
+// chunk's start to token i, d_j from token j to its end, kappa_ij = k_i . k_j and L_ij = D_ij kappa_ij (j < i):
+//     X = V - diag(c) K S0                       what the chunk's tokens would write into S0 alone
+//     R = (I + L diag(beta))^-1 X                the residuals v_t - a_t k_t S_{t-1}
+//     O = diag(c) Q S0 + (D o Q K^T) diag(beta) R
+//     S1 = c_31 S0 + K^T diag(d beta) R
+//
+// Two kernels.  delta_prep_kernel forms, for every chunk and head at once, what does not depend on the state:
+// M = (I + L diag(beta))^-1 by substitution in f32, P = D o Q K^T diag(beta), c and d beta.  delta_fwd_kernel
+// then walks each chain.  All of its products leave the columns of S (the dv dimension) apart, so a warp owns 16
+// columns for the whole walk and meets no other warp: it keeps S^T in registers as the f32 accumulators of
+// mma.sync m16n8k16, whose layout is also that of the A operand, and every product has the form
+// (16 columns x n) = (16 columns x k)(k x n) with the B operand from shared memory:
+//     Y = S^T K^T,  X^T = V^T - Y diag(c),  R^T = X^T M^T,  O^T = S^T Q^T diag(c) + R^T P^T,
+//     S^T = c_31 S^T + (R^T diag(d beta)) K.
+// A step of a chain is three products long, without a barrier or a trip through memory between them; that, and
+// not the rate of the tensor cores, is what a walk over a long sequence is made of.  tcgen05 runs four times the
+// rate of mma.sync (1,020 multiply-adds a clock and SM, measured) but its accumulators would have to go through
+// the registers and back to shared memory, split in two, between any two of the products.
+//
+// Precision: q, k and v are bf16 and so exact as operands.  S, X, M and R are f32 values; where a product with
+// them reaches the state, each is taken as two bf16 parts, hi + lo, whose sum holds 16 bits of it (2^-17 relative);
+// M X takes three products, the others two.  So hT has f32 accuracy.  O, itself rounded to bf16, takes the hi
+// parts alone.
+//
+// A warp of its own fetches the rows of K, Q, V and the chunk's M, P, c and d beta by bulk copies into a ring
+// of stages; a row's stride is an odd number of 16-byte units, so that ldmatrix meets no bank twice.
+#include "gla_delta.cuh"
+#include "sm100_ptx.cuh"
+
+GLA_DEFINE_STATUS(delta_mma)
+
+namespace gla {
+namespace delta {
+namespace {
+
+using bf16 = __nv_bfloat16;
+constexpr int kC = 32;                  // tokens per chunk of a walk
+constexpr int kMaxWarps = 12;           // column tiles of 16 per block
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+// Per chunk and value head, in the order of the B operands: [4 tiles of 8 columns][32 lanes] x 16 bytes
+// (k 0..15 then 16..31).
+struct FwdRecord {
+    uint4 mhi[4][32], mlo[4][32], p[4][32];
+    float c[kC], db[kC];  // c_i and d_j beta_j
+};
+static_assert(sizeof(FwdRecord) % 16 == 0, "bulk copies take multiples of 16 bytes");
+
+// ---- fragments -----------------------------------------------------------------------------------------------
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void stsm4t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
+                 ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 t;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(t.x), "=r"(t.y), "=r"(t.z), "=r"(t.w) : "r"(addr) : "memory");
+    return t;
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t addr) {
+    float2 t;
+    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(t.x), "=f"(t.y) : "r"(addr) : "memory");
+    return t;
+}
+// two f32 to two bf16 (x in the low half), round to nearest
+__device__ __forceinline__ uint32_t pack(float x, float y) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lo_f(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float hi_f(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+// x, y as hi + lo parts of 8 bits each
+__device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = pack(x, y);
+    lo = pack(x - lo_f(hi), y - hi_f(hi));
+}
+
+// ---- what does not depend on the state -----------------------------------------------------------------------
+//
+// One warp per chunk and value head.  K K^T and Q K^T by mma.sync (their inputs are exact, their sums f32); then
+// lane j owns column j: D as a running product of the decays (no difference of logarithms, so a decay of zero is
+// as exact as any), and column j of the inverse by substitution, t_i = [i = j] - sum_{l < i} L_il beta_l t_l, with
+// L's rows broadcast from shared memory.
+constexpr int kPrepWarps = 4;
+constexpr int kLd = 36;  // f32 row stride of the 32 x 32 tiles: rows 16-byte aligned, columns on different banks
+
+template <int KT> constexpr int row_bytes() { return KT * 32 + 16; }  // KT * 16 bf16 and an odd number of 16-byte units
+template <int KT> constexpr int prep_warp_bytes() {
+    const int tiles = 2 * kC * row_bytes<KT>(), mats = 2 * kC * kLd * 4;
+    return tiles > mats ? tiles : mats;
+}
+
+// rows of 32 tokens of a head into shared memory, zero past len and past dk
+template <int KT>
+__device__ __forceinline__ void load_rows(char *dst, const bf16 *src, int64_t stride, int len, int dk, int lane) {
+    for (int i = lane; i < kC * KT * 2; i += 32) {
+        const int t = i / (KT * 2), u = i % (KT * 2);
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (t < len && u * 8 < dk) x = __ldg(reinterpret_cast<const uint4 *>(src + t * stride) + u);
+        *reinterpret_cast<uint4 *>(dst + t * row_bytes<KT>() + u * 16) = x;
+    }
+}
+
+template <int KT>
+__global__ void __launch_bounds__(kPrepWarps * 32)
+delta_prep_kernel(Shape p, int64_t units, const bf16 *__restrict__ q, const bf16 *__restrict__ k,
+                  const void *__restrict__ g, const void *__restrict__ beta, FwdRecord *__restrict__ records) {
+    extern __shared__ __align__(128) char sm_raw[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t unit = (int64_t)blockIdx.x * kPrepWarps + warp;  // slot * H + h
+    if (unit >= units) return;
+    const int h = (int)(unit % p.H), hk = h / p.group();
+    ChunkAt at;
+    if (!chunk_of_slot<kC>(unit / p.H, p, at)) return;
+    char *ks = sm_raw + warp * prep_warp_bytes<KT>(), *qs = ks + kC * row_bytes<KT>();
+    float *kap = reinterpret_cast<float *>(ks), *qk = kap + kC * kLd;
+    load_rows<KT>(ks, k + (at.row * p.Hk + hk) * p.dk, (int64_t)p.Hk * p.dk, at.len, p.dk, lane);
+    load_rows<KT>(qs, q + (at.row * p.Hk + hk) * p.dk, (int64_t)p.Hk * p.dk, at.len, p.dk, lane);
+    float a = 1.f, be = 0.f;
+    if (lane < at.len) {
+        a = expf(load_gate<bf16>(g, (at.row + lane) * p.H + h, p.gate_f32));
+        be = load_gate<bf16>(beta, (at.row + lane) * p.H + h, p.gate_f32);
+    }
+    __syncwarp();
+    const uint32_t ka = ptx::smem_u32(ks), qa = ptx::smem_u32(qs);
+    const int m8 = lane >> 3, r8 = lane & 7;
+    float kk[2][4][4] = {}, qq[2][4][4] = {};
+#pragma unroll
+    for (int s = 0; s < KT; ++s) {
+        uint32_t b[2][4], ak[2][4], aq[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {  // tokens 16 t ..: as columns (B) and as rows (A)
+            ldsm4(b[t], ka + (t * 16 + (m8 >> 1) * 8 + r8) * row_bytes<KT>() + s * 32 + (m8 & 1) * 16);
+            const uint32_t off = (t * 16 + (m8 & 1) * 8 + r8) * row_bytes<KT>() + s * 32 + (m8 >> 1) * 16;
+            ldsm4(ak[t], ka + off);
+            ldsm4(aq[t], qa + off);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int t = 0; t <= i; ++t) {  // tiles on and below the diagonal
+                mma(kk[i][2 * t], ak[i], b[t][0], b[t][1]);
+                mma(kk[i][2 * t + 1], ak[i], b[t][2], b[t][3]);
+                mma(qq[i][2 * t], aq[i], b[t][0], b[t][1]);
+                mma(qq[i][2 * t + 1], aq[i], b[t][2], b[t][3]);
+            }
+    }
+    __syncwarp();  // the tiles are read: their place takes kappa and Q K^T
+    const int gr = lane >> 2, tg = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int at0 = (i * 16 + gr) * kLd + t * 8 + 2 * tg;
+            *reinterpret_cast<float2 *>(kap + at0) = make_float2(kk[i][t][0], kk[i][t][1]);
+            *reinterpret_cast<float2 *>(kap + at0 + 8 * kLd) = make_float2(kk[i][t][2], kk[i][t][3]);
+            *reinterpret_cast<float2 *>(qk + at0) = make_float2(qq[i][t][0], qq[i][t][1]);
+            *reinterpret_cast<float2 *>(qk + at0 + 8 * kLd) = make_float2(qq[i][t][2], qq[i][t][3]);
+        }
+    __syncwarp();
+    float f = 0.f, run = 1.f, c = 1.f;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+        const float ai = __shfl_sync(0xffffffffu, a, i);
+        run *= ai;
+        if (i == lane) c = run;
+        f = i == lane ? 1.f : f * ai;
+        const int e = i * kLd + lane;
+        kap[e] = i > lane ? f * kap[e] : 0.f;
+        qk[e] = i >= lane ? f * qk[e] * be : 0.f;
+    }
+    __syncwarp();
+    float t[kC], s[kC];  // t: column `lane` of the inverse, s: beta t
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+        float x0 = i == lane ? 1.f : 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
+#pragma unroll
+        for (int l = 0; l < i; l += 4) {
+            const float4 row = *reinterpret_cast<const float4 *>(kap + i * kLd + l);
+            x0 = fmaf(-row.x, s[l], x0);
+            if (l + 1 < i) x1 = fmaf(-row.y, s[l + 1], x1);
+            if (l + 2 < i) x2 = fmaf(-row.z, s[l + 2], x2);
+            if (l + 3 < i) x3 = fmaf(-row.w, s[l + 3], x3);
+        }
+        t[i] = (x0 + x1) + (x2 + x3);
+        s[i] = t[i] * __shfl_sync(0xffffffffu, be, i);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kC; ++i) kap[i * kLd + lane] = t[i];
+    __syncwarp();
+    FwdRecord *rec = records + unit;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        uint32_t hi[4], lo[4], pp[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int at0 = (n * 8 + gr) * kLd + e * 8 + 2 * tg;
+            const float2 m = *reinterpret_cast<const float2 *>(kap + at0);
+            const float2 x = *reinterpret_cast<const float2 *>(qk + at0);
+            split(m.x, m.y, hi[e], lo[e]);
+            pp[e] = pack(x.x, x.y);
+        }
+        rec->mhi[n][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        rec->mlo[n][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        rec->p[n][lane] = make_uint4(pp[0], pp[1], pp[2], pp[3]);
+    }
+    rec->c[lane] = c;
+    rec->db[lane] = f * be;
+}
+
+// ---- the walk ---------------------------------------------------------------------------------------------------
+
+struct Walk {           // one block's share of a chain
+    int warps, splits;  // column tiles per block, blocks per chain
+    int vrow;           // bytes of a staged row of V, an odd number of 16-byte units
+    int stages, stage_bytes;
+};
+
+constexpr int kOutRow = 48;  // bytes of a staged row of 16 output columns: an odd number of 16-byte units
+
+template <int KT>
+__global__ void __launch_bounds__((kMaxWarps + 1) * 32)
+delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16 *__restrict__ v,
+                 const FwdRecord *__restrict__ records, const float *__restrict__ h0, bf16 *__restrict__ out,
+                 float *__restrict__ hT) {
+    extern __shared__ __align__(128) char sm_raw[];
+    constexpr int kRow = row_bytes<KT>(), kTile = kC * kRow;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t chain = blockIdx.x / w.splits;
+    const int part = blockIdx.x % w.splits;
+    const int s = (int)(chain / p.H), h = (int)(chain % p.H), hk = h / p.group();
+    const int col0 = part * w.warps * 16;                       // first column of the block
+    const int width = min(w.warps * 16, p.dv - col0);           // its columns, a multiple of 8
+    SeqRange r;
+    if (!seq_range(s, p.T, p.cu, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
+    const int nch = (int)((r.len + kC - 1) / kC);
+    // shared memory: barriers, the warps' output tiles, the stages (K | Q | V | record)
+    const uint32_t base = ptx::smem_u32(sm_raw);
+    const uint32_t full = base, empty = base + 8 * w.stages;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm_raw + 16 * w.stages);
+    const uint32_t outs = base + 128, ring = outs + w.warps * kC * kOutRow;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < w.stages; ++i) {
+            ptx::mbar_init(full + 8 * i, 1);
+            ptx::mbar_init(empty + 8 * i, w.warps);
+        }
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    // columns that no copy writes (past dk, past the block's columns) are zero in every stage
+    for (int i = threadIdx.x; i < w.stages * kC; i += blockDim.x) {
+        char *st = sm_raw + (ring - base) + (i / kC) * w.stage_bytes;
+        for (int u = p.dk / 8; u < KT * 2; ++u) {
+            *reinterpret_cast<uint4 *>(st + (i % kC) * kRow + u * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(st + kTile + (i % kC) * kRow + u * 16) = make_uint4(0, 0, 0, 0);
+        }
+        for (int u = width / 8; u < w.warps * 2; ++u)
+            *reinterpret_cast<uint4 *>(st + 2 * kTile + (i % kC) * w.vrow + u * 16) = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    const int64_t slot0 = r.start / kC + s;
+
+    if (warp == w.warps) {  // the fetching warp: lane = token of the chunk
+        int issued = 0;
+        for (int c = 0; c < nch; ++c) {
+            const int sg = c % w.stages;
+            if (c >= w.stages && !ptx::mbar_wait(empty + 8 * sg, (c / w.stages + 1) & 1, abort_flag, kWaitNs)) {
+                *abort_flag = 1;
+                break;
+            }
+            const int len = (int)min((int64_t)kC, r.len - (int64_t)c * kC);
+            const uint32_t at = ring + sg * w.stage_bytes;
+            if (lane >= len) {  // the last chunk's missing rows
+                char *st = sm_raw + (at - base);
+                for (int u = 0; u < KT * 2; ++u) {
+                    *reinterpret_cast<uint4 *>(st + lane * kRow + u * 16) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(st + kTile + lane * kRow + u * 16) = make_uint4(0, 0, 0, 0);
+                }
+                for (int u = 0; u < w.warps * 2; ++u)
+                    *reinterpret_cast<uint4 *>(st + 2 * kTile + lane * w.vrow + u * 16) = make_uint4(0, 0, 0, 0);
+            }
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_expect_tx(full + 8 * sg, len * (2 * p.dk + width) * 2 + (int)sizeof(FwdRecord));
+            __syncwarp();
+            const int64_t row = r.start + (int64_t)c * kC + lane;
+            if (lane < len) {
+                ptx::bulk_load_g2s(at + lane * kRow, k + (row * p.Hk + hk) * p.dk, p.dk * 2, full + 8 * sg);
+                ptx::bulk_load_g2s(at + kTile + lane * kRow, q + (row * p.Hk + hk) * p.dk, p.dk * 2, full + 8 * sg);
+                ptx::bulk_load_g2s(at + 2 * kTile + lane * w.vrow, v + (row * p.H + h) * p.dv + col0, width * 2,
+                                   full + 8 * sg);
+            }
+            if (lane == 0)
+                ptx::bulk_load_g2s(at + 2 * kTile + kC * w.vrow, records + (slot0 + c) * p.H + h, sizeof(FwdRecord),
+                                   full + 8 * sg);
+            issued = c + 1;
+        }
+        __syncwarp();
+        if (*abort_flag)  // nothing may be in flight into a block that ends early
+            for (int c = max(0, issued - w.stages); c < issued; ++c)
+                ptx::mbar_wait(full + 8 * (c % w.stages), (c / w.stages) & 1, nullptr, kWaitNs);
+        return;
+    }
+
+    const int gr = lane >> 2, tg = lane & 3, m8 = lane >> 3, r8 = lane & 7;
+    const int col = col0 + warp * 16;
+    const bool lo_ok = col < p.dv, hi_ok = col + 8 < p.dv;
+    const int64_t sat = chain * p.dk * p.dv + col + gr;
+    float S[2 * KT][4];
+#pragma unroll
+    for (int n = 0; n < 2 * KT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int row = n * 8 + 2 * tg + (e & 1);
+            S[n][e] = h0 != nullptr && row < p.dk && (e < 2 ? lo_ok : hi_ok) ? h0[sat + (int64_t)row * p.dv + (e >> 1) * 8]
+                                                                            : 0.f;
+        }
+    const uint32_t o_tile = outs + warp * kC * kOutRow;
+    for (int c = 0; c < nch; ++c) {
+        const int sg = c % w.stages;
+        if (!ptx::mbar_wait(full + 8 * sg, (c / w.stages) & 1, abort_flag, kWaitNs)) {
+            if (lane == 0) {
+                *abort_flag = 1;
+                record_status(GLA_ERR_TIMEOUT);
+            }
+            return;
+        }
+        const uint32_t ks = ring + sg * w.stage_bytes, qs = ks + kTile, vs = qs + kTile + warp * 32,
+                       rec = qs + kTile + kC * w.vrow;
+        const uint32_t vec = rec + (uint32_t)offsetof(FwdRecord, c) + 8 * tg;
+        // Y = S^T K^T and O = S^T Q^T
+        float Y[4][4] = {}, O[4][4] = {};
+        const uint32_t row_off = ((m8 >> 1) * 8 + r8) * kRow + (m8 & 1) * 16;
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+            uint32_t ah[4], al[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                split(S[2 * i + (e >> 1)][(e & 1) * 2], S[2 * i + (e >> 1)][(e & 1) * 2 + 1], ah[e], al[e]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                uint32_t b[4];
+                ldsm4(b, ks + row_off + t * 16 * kRow + i * 32);
+                mma(Y[2 * t], ah, b[0], b[1]);
+                mma(Y[2 * t + 1], ah, b[2], b[3]);
+                mma(Y[2 * t], al, b[0], b[1]);
+                mma(Y[2 * t + 1], al, b[2], b[3]);
+                ldsm4(b, qs + row_off + t * 16 * kRow + i * 32);
+                mma(O[2 * t], ah, b[0], b[1]);
+                mma(O[2 * t + 1], ah, b[2], b[3]);
+            }
+        }
+        // X^T = V^T - Y diag(c), as hi and lo parts; O diag(c)
+        uint32_t xh[2][4], xl[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            uint32_t b[4];
+            ldsm4t(b, vs + (t * 16 + (m8 >> 1) * 8 + r8) * w.vrow + (m8 & 1) * 16);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int n = 2 * t + u;
+                const float2 cc = lds_f2(vec + n * 32);
+                split(fmaf(-cc.x, Y[n][0], lo_f(b[2 * u])), fmaf(-cc.y, Y[n][1], hi_f(b[2 * u])), xh[t][2 * u], xl[t][2 * u]);
+                split(fmaf(-cc.x, Y[n][2], lo_f(b[2 * u + 1])), fmaf(-cc.y, Y[n][3], hi_f(b[2 * u + 1])),
+                      xh[t][2 * u + 1], xl[t][2 * u + 1]);
+                O[n][0] *= cc.x; O[n][1] *= cc.y; O[n][2] *= cc.x; O[n][3] *= cc.y;
+            }
+        }
+        // R^T = X^T M^T: M is lower triangular, so the first 16 rows meet the first 16 columns only
+        float R[4][4] = {};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const uint4 mh = lds128(rec + n * 512 + lane * 16), ml = lds128(rec + 2048 + n * 512 + lane * 16);
+            mma(R[n], xh[0], mh.x, mh.y);
+            mma(R[n], xl[0], mh.x, mh.y);
+            mma(R[n], xh[0], ml.x, ml.y);
+            if (n >= 2) {
+                mma(R[n], xh[1], mh.z, mh.w);
+                mma(R[n], xl[1], mh.z, mh.w);
+                mma(R[n], xh[1], ml.z, ml.w);
+            }
+        }
+        // O += R^T P^T with R rounded to bf16; U = R diag(d beta) as hi and lo parts
+        uint32_t rh[2][4], uh[2][4], ul[2][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int t = n >> 1, u = (n & 1) * 2;
+            const float2 db = lds_f2(vec + 4 * kC + n * 32);
+            rh[t][u] = pack(R[n][0], R[n][1]);
+            rh[t][u + 1] = pack(R[n][2], R[n][3]);
+            split(R[n][0] * db.x, R[n][1] * db.y, uh[t][u], ul[t][u]);
+            split(R[n][2] * db.x, R[n][3] * db.y, uh[t][u + 1], ul[t][u + 1]);
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const uint4 pp = lds128(rec + 4096 + n * 512 + lane * 16);
+            mma(O[n], rh[0], pp.x, pp.y);
+            if (n >= 2) mma(O[n], rh[1], pp.z, pp.w);
+        }
+        // S^T = c_31 S^T + U K
+        const float last = lds_f2(rec + (uint32_t)offsetof(FwdRecord, c) + 8 * 15).y;
+#pragma unroll
+        for (int n = 0; n < 2 * KT; ++n) {
+            uint32_t b[4];
+            ldsm4t(b, ks + lane * kRow + n * 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[n][e] *= last;
+            mma(S[n], uh[0], b[0], b[1]);
+            mma(S[n], uh[1], b[2], b[3]);
+            mma(S[n], ul[0], b[0], b[1]);
+            mma(S[n], ul[1], b[2], b[3]);
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(empty + 8 * sg);
+        // O^T through the warp's tile to rows of 32 bytes
+        const uint32_t to = o_tile + ((m8 >> 1) * 8 + r8) * kOutRow + (m8 & 1) * 16;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            stsm4t(to + t * 16 * kOutRow, pack(O[2 * t][0], O[2 * t][1]), pack(O[2 * t][2], O[2 * t][3]),
+                   pack(O[2 * t + 1][0], O[2 * t + 1][1]), pack(O[2 * t + 1][2], O[2 * t + 1][3]));
+        __syncwarp();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int i = t * 16 + (lane >> 1), cc = col + (lane & 1) * 8;
+            const int64_t tok = (int64_t)c * kC + i;
+            const uint4 x = lds128(o_tile + i * kOutRow + (lane & 1) * 16);
+            if (tok < r.len && cc < p.dv) *reinterpret_cast<uint4 *>(out + ((r.start + tok) * p.H + h) * p.dv + cc) = x;
+        }
+        __syncwarp();
+    }
+    if (hT != nullptr) {
+#pragma unroll
+        for (int n = 0; n < 2 * KT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = n * 8 + 2 * tg + (e & 1);
+                if (row < p.dk && (e < 2 ? lo_ok : hi_ok)) hT[sat + (int64_t)row * p.dv + (e >> 1) * 8] = S[n][e];
+            }
+    }
+}
+
+// Blocks per chain: one where the chains fill the GPU (the fewest reads of K and Q), else as many as fill it.
+// B8 T2048 H16 dk96 dv192 (128 chains, 152 SMs) runs one block of 12 column tiles to a chain; B1 (16 chains) six
+// blocks of two.
+template <int KT>
+Walk make_walk(const Shape &p) {
+    Walk w{};
+    const int tiles = (p.dv + 15) / 16, sms = device_info().sm_count;
+    const long long chains = (long long)p.nseq * p.H;
+    int splits = (tiles + kMaxWarps - 1) / kMaxWarps;
+    if (chains * splits < sms) splits = (int)min((long long)tiles, sms / chains);
+    w.warps = (tiles + splits - 1) / splits;
+    w.splits = (tiles + w.warps - 1) / w.warps;
+    w.vrow = (w.warps * 2 | 1) * 16;
+    w.stage_bytes = 2 * kC * row_bytes<KT>() + kC * w.vrow + (int)sizeof(FwdRecord);
+    w.stages = 4;
+    return w;
+}
+
+template <int KT>
+int fwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const void *g, const void *beta,
+           const float *h0, bf16 *out, float *hT, FwdRecord *records, cudaStream_t st) {
+    const int64_t units = chunk_slots(total_rows(p), p.nseq, kC) * p.H;
+    const int prep_bytes = kPrepWarps * prep_warp_bytes<KT>();
+    const Walk w = make_walk<KT>(p);
+    const int bytes = 128 + w.warps * kC * kOutRow + w.stages * w.stage_bytes;
+    if (cudaFuncSetAttribute(delta_prep_kernel<KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, prep_bytes) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(delta_fwd_kernel<KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return GLA_ERR_LAUNCH;
+    const long long blocks = (long long)p.nseq * p.H * w.splits;
+    if (blocks > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
+    delta_prep_kernel<KT><<<(unsigned)((units + kPrepWarps - 1) / kPrepWarps), kPrepWarps * 32, prep_bytes, st>>>(
+        p, units, q, k, g, beta, records);
+    delta_fwd_kernel<KT><<<(unsigned)blocks, (w.warps + 1) * 32, bytes, st>>>(p, w, q, k, v, records, h0, out, hT);
+    count_launches(2);
+    return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
+}
+
+}  // namespace
+
+// bf16 with dk <= 128: a warp's share of the state fits its registers.
+bool mma_supported(int dk) { return dk <= 128; }
+
+size_t mma_fwd_workspace(const Shape &p) {
+    return (size_t)chunk_slots(total_rows(p), p.nseq, kC) * p.H * sizeof(FwdRecord);
+}
+
+int mma_fwd(const Shape &p, const void *q, const void *k, const void *v, const void *g, const void *beta,
+            const float *h0, void *out, float *hT, void *ws, cudaStream_t st) {
+#define GLA_CALL(KT) \
+    return fwd_kt<KT>(p, (const bf16 *)q, (const bf16 *)k, (const bf16 *)v, g, beta, h0, (bf16 *)out, hT, (FwdRecord *)ws, st)
+    if (p.dk <= 32) { GLA_CALL(2); }
+    if (p.dk <= 64) { GLA_CALL(4); }
+    if (p.dk <= 96) { GLA_CALL(6); }
+    GLA_CALL(8);
+#undef GLA_CALL
+}
+
+}  // namespace delta
+}  // namespace gla
