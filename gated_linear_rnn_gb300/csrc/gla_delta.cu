@@ -53,10 +53,10 @@ delta_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
     float *red = sm;                                 // [2][kStepGroups][4 ncg], read and written by float4: first
     float *redqk = red + 2 * kStepGroups * 4 * ncg;  // [kStepGroups]
     float *ks = redqk + kStepGroups, *qs = ks + dk;  // [dk] each
-    const int64_t chain = blockIdx.x / nslices;  // n * H + h
-    const int slice = blockIdx.x % nslices;
-    const int64_t n = chain / H;
-    const int h = (int)(chain % H);
+    const unsigned chain32 = blockIdx.x / (unsigned)nslices;  // n * H + h
+    const int slice = (int)(blockIdx.x % (unsigned)nslices);
+    const int64_t chain = chain32, n = chain32 / (unsigned)H;
+    const int h = (int)(chain32 % (unsigned)H);
     const int64_t kchain = n * Hk + h / (H / Hk);
     const int tid = threadIdx.x, cg = tid % ncg, rg = tid / ncg;
     const int col = (slice * ncg + cg) * 4;
@@ -447,8 +447,7 @@ delta_grad_simt_kernel(Shape p, const T *__restrict__ q, const T *__restrict__ k
                        const float *__restrict__ ys, const float *__restrict__ s0, const float *__restrict__ ds1,
                        T *__restrict__ dq, T *__restrict__ dk, void *__restrict__ dg, void *__restrict__ dbeta) {
     extern __shared__ __align__(16) float sm[];
-    const int64_t slot = blockIdx.x / p.Hk;
-    const int hk = blockIdx.x % p.Hk;
+    const int slot = (int)(blockIdx.x / (unsigned)p.Hk), hk = (int)(blockIdx.x % (unsigned)p.Hk);
     ChunkAt at;
     if (!chunk_of_slot<kG>(slot, p, at)) return;
     const int L = at.len, dkk = p.dk, dvv = p.dv, tid = threadIdx.x;
@@ -467,7 +466,7 @@ delta_grad_simt_kernel(Shape p, const T *__restrict__ q, const T *__restrict__ k
     tile_product(tl, kG, dkk, Q, [&](int kk, int n) { return K(n, kk); },
                  [&](int i, int n, int, float s) { qk[i * kGP + n] = s; });
     for (int h = hk * p.group(); h < (hk + 1) * p.group(); ++h) {
-        const int64_t vat = (at.row * p.H + h) * dvv, sat = (slot * p.H + h) * dkk * dvv;
+        const int64_t vat = (at.row * p.H + h) * dvv, sat = ((int64_t)slot * p.H + h) * dkk * dvv;
         const T *dor = dout + vat;
         const float *rr = resid + vat, *yr = ys + vat, *S0 = s0 + sat, *S1 = ds1 + sat;
         auto DO = [&](int i, int n) { return i < L ? to_f32(dor[i * vst + n]) : 0.f; };

@@ -32,33 +32,26 @@ struct ChunkAt {
     bool first, last;  // first / last chunk of its sequence
 };
 
-// The chunk that owns a slot; false for slots that no chunk has (and for sequences with bad offsets).
+// The chunk that owns a slot; false for slots that no chunk has (and for sequences with bad offsets).  Slots and
+// rows are below 2^31 (the entry points see to it).
 template <int C>
-__device__ __forceinline__ bool chunk_of_slot(int64_t slot, const Shape &p, ChunkAt &at) {
-    int lo = 0;
-    if (p.cu == nullptr) {
-        lo = 0;
-        int hi = p.nseq - 1;  // largest s with s * T / C + s <= slot
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if ((int64_t)mid * p.T / C + mid <= slot) lo = mid; else hi = mid - 1;
-        }
-    } else {
-        int hi = p.nseq - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if ((int64_t)(__ldg(p.cu + mid) / C) + mid <= slot) lo = mid; else hi = mid - 1;
-        }
+__device__ __forceinline__ bool chunk_of_slot(int slot, const Shape &p, ChunkAt &at) {
+    int lo = 0, hi = p.nseq - 1;  // the largest s with start_s / C + s <= slot
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        const int start = p.cu == nullptr ? mid * p.T : __ldg(p.cu + mid);
+        if (start / C + mid <= slot) lo = mid; else hi = mid - 1;
     }
     SeqRange r;
     if (!seq_range(lo, p.T, p.cu, r)) return false;
-    const int64_t c = slot - (r.start / C + lo);
-    if (c < 0 || c * C >= r.len) return false;
-    at.row = r.start + c * C;
-    at.len = (int)(r.len - c * C < C ? r.len - c * C : C);
+    const int start = (int)r.start, len = (int)r.len;
+    const int c = slot - (start / C + lo);
+    if (c < 0 || c >= (len + C - 1) / C) return false;
+    at.row = start + c * C;
+    at.len = min(len - c * C, C);
     at.seq = lo;
     at.first = c == 0;
-    at.last = (c + 1) * C >= r.len;
+    at.last = c == (len + C - 1) / C - 1;
     return true;
 }
 

@@ -25,8 +25,9 @@
 // M X takes three products, the others two.  So hT has f32 accuracy.  O, itself rounded to bf16, takes the hi
 // parts alone.
 //
-// A warp of its own fetches the rows of K, Q, V and the chunk's M, P, c and d beta by bulk copies into a ring
-// of stages; a row's stride is an odd number of 16-byte units, so that ldmatrix meets no bank twice.
+// A warp of its own fetches the rows of K, Q and V by 16-byte asynchronous copies (zero past a sequence's end, so
+// a short chunk is computed like a whole one) and the chunk's M, P, c and d beta by one bulk copy into a ring of
+// stages; a row's stride is an odd number of 16-byte units, so that ldmatrix meets no bank twice.
 #include "gla_delta.cuh"
 #include "sm100_ptx.cuh"
 
@@ -51,7 +52,7 @@ static_assert(sizeof(FwdRecord) % 16 == 0, "bulk copies take multiples of 16 byt
 
 // ---- fragments -----------------------------------------------------------------------------------------------
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -77,6 +78,15 @@ __device__ __forceinline__ float2 lds_f2(uint32_t addr) {
     asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(t.x), "=f"(t.y) : "r"(addr) : "memory");
     return t;
 }
+// 16 bytes from global to shared memory, or 16 zero bytes
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool has) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(has ? 16 : 0) : "memory");
+}
+// this thread's arrival on `bar` once all of its copies so far have landed
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // two f32 to two bf16 (x in the low half), round to nearest
 __device__ __forceinline__ uint32_t pack(float x, float y) {
     uint32_t r;
@@ -106,39 +116,40 @@ template <int KT> constexpr int prep_warp_bytes() {
     return tiles > mats ? tiles : mats;
 }
 
-// rows of 32 tokens of a head into shared memory, zero past len and past dk
+// rows of 32 tokens of a head into shared memory, zero past len and past dk; asynchronous
 template <int KT>
-__device__ __forceinline__ void load_rows(char *dst, const bf16 *src, int64_t stride, int len, int dk, int lane) {
-    for (int i = lane; i < kC * KT * 2; i += 32) {
-        const int t = i / (KT * 2), u = i % (KT * 2);
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (t < len && u * 8 < dk) x = __ldg(reinterpret_cast<const uint4 *>(src + t * stride) + u);
-        *reinterpret_cast<uint4 *>(dst + t * row_bytes<KT>() + u * 16) = x;
+__device__ __forceinline__ void fetch_rows(uint32_t dst, const bf16 *src, int64_t stride, int len, int dk, int lane) {
+#pragma unroll
+    for (int i = 0; i < KT * 2; ++i) {
+        const int e = i * 32 + lane, t = e / (KT * 2), u = e % (KT * 2);
+        const bool has = t < len && u * 8 < dk;
+        cp_async16(dst + t * row_bytes<KT>() + u * 16, src + (has ? t * stride + u * 8 : 0), has);
     }
 }
 
 template <int KT>
 __global__ void __launch_bounds__(kPrepWarps * 32)
-delta_prep_kernel(Shape p, int64_t units, const bf16 *__restrict__ q, const bf16 *__restrict__ k,
+delta_prep_kernel(Shape p, unsigned units, const bf16 *__restrict__ q, const bf16 *__restrict__ k,
                   const void *__restrict__ g, const void *__restrict__ beta, FwdRecord *__restrict__ records) {
     extern __shared__ __align__(128) char sm_raw[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t unit = (int64_t)blockIdx.x * kPrepWarps + warp;  // slot * H + h
+    const unsigned unit = blockIdx.x * kPrepWarps + warp;  // slot * H + h
     if (unit >= units) return;
-    const int h = (int)(unit % p.H), hk = h / p.group();
+    const int h = (int)(unit % (unsigned)p.H), hk = h / p.group();
     ChunkAt at;
-    if (!chunk_of_slot<kC>(unit / p.H, p, at)) return;
+    if (!chunk_of_slot<kC>((int)(unit / (unsigned)p.H), p, at)) return;
     char *ks = sm_raw + warp * prep_warp_bytes<KT>(), *qs = ks + kC * row_bytes<KT>();
     float *kap = reinterpret_cast<float *>(ks), *qk = kap + kC * kLd;
-    load_rows<KT>(ks, k + (at.row * p.Hk + hk) * p.dk, (int64_t)p.Hk * p.dk, at.len, p.dk, lane);
-    load_rows<KT>(qs, q + (at.row * p.Hk + hk) * p.dk, (int64_t)p.Hk * p.dk, at.len, p.dk, lane);
+    const uint32_t ka = ptx::smem_u32(ks), qa = ptx::smem_u32(qs);
+    fetch_rows<KT>(ka, k + (at.row * p.Hk + hk) * p.dk, (int64_t)p.Hk * p.dk, at.len, p.dk, lane);
+    fetch_rows<KT>(qa, q + (at.row * p.Hk + hk) * p.dk, (int64_t)p.Hk * p.dk, at.len, p.dk, lane);
     float a = 1.f, be = 0.f;
     if (lane < at.len) {
         a = expf(load_gate<bf16>(g, (at.row + lane) * p.H + h, p.gate_f32));
         be = load_gate<bf16>(beta, (at.row + lane) * p.H + h, p.gate_f32);
     }
+    cp_async_wait_all();
     __syncwarp();
-    const uint32_t ka = ptx::smem_u32(ks), qa = ptx::smem_u32(qs);
     const int m8 = lane >> 3, r8 = lane & 7;
     float kk[2][4][4] = {}, qq[2][4][4] = {};
 #pragma unroll
@@ -243,9 +254,8 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
     extern __shared__ __align__(128) char sm_raw[];
     constexpr int kRow = row_bytes<KT>(), kTile = kC * kRow;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t chain = blockIdx.x / w.splits;
-    const int part = blockIdx.x % w.splits;
-    const int s = (int)(chain / p.H), h = (int)(chain % p.H), hk = h / p.group();
+    const int chain = (int)(blockIdx.x / (unsigned)w.splits), part = (int)(blockIdx.x % (unsigned)w.splits);
+    const int s = chain / p.H, h = chain % p.H, hk = h / p.group();
     const int col0 = part * w.warps * 16;                       // first column of the block
     const int width = min(w.warps * 16, p.dv - col0);           // its columns, a multiple of 8
     SeqRange r;
@@ -258,71 +268,65 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
     const uint32_t outs = base + 128, ring = outs + w.warps * kC * kOutRow;
     if (threadIdx.x == 0) {
         for (int i = 0; i < w.stages; ++i) {
-            ptx::mbar_init(full + 8 * i, 1);
+            ptx::mbar_init(full + 8 * i, 33);  // the fetching warp's lanes, and its first lane's record
             ptx::mbar_init(empty + 8 * i, w.warps);
         }
         *abort_flag = 0;
         ptx::fence_mbar_init();
     }
-    // columns that no copy writes (past dk, past the block's columns) are zero in every stage
-    for (int i = threadIdx.x; i < w.stages * kC; i += blockDim.x) {
-        char *st = sm_raw + (ring - base) + (i / kC) * w.stage_bytes;
-        for (int u = p.dk / 8; u < KT * 2; ++u) {
-            *reinterpret_cast<uint4 *>(st + (i % kC) * kRow + u * 16) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(st + kTile + (i % kC) * kRow + u * 16) = make_uint4(0, 0, 0, 0);
-        }
-        for (int u = width / 8; u < w.warps * 2; ++u)
-            *reinterpret_cast<uint4 *>(st + 2 * kTile + (i % kC) * w.vrow + u * 16) = make_uint4(0, 0, 0, 0);
-    }
     __syncthreads();
     const int64_t slot0 = r.start / kC + s;
 
-    if (warp == w.warps) {  // the fetching warp: lane = token of the chunk
-        int issued = 0;
+    if (warp == w.warps) {  // the fetching warp
+        const int vunits = w.warps * 2, vlive = width / 8, kunits = p.dk / 8;
+        const int64_t kstride = (int64_t)p.Hk * p.dk, vstride = (int64_t)p.H * p.dv;
+        const bf16 *kr = k + r.start * kstride + hk * p.dk, *qr = q + r.start * kstride + hk * p.dk,
+                   *vr = v + r.start * vstride + (int64_t)h * p.dv + col0;
+        bool ok = true;
         for (int c = 0; c < nch; ++c) {
             const int sg = c % w.stages;
-            if (c >= w.stages && !ptx::mbar_wait(empty + 8 * sg, (c / w.stages + 1) & 1, abort_flag, kWaitNs)) {
-                *abort_flag = 1;
-                break;
-            }
+            ok = c < w.stages || ptx::mbar_wait(empty + 8 * sg, (c / w.stages + 1) & 1, abort_flag, kWaitNs);
+            if (!__all_sync(0xffffffffu, ok)) break;
             const int len = (int)min((int64_t)kC, r.len - (int64_t)c * kC);
             const uint32_t at = ring + sg * w.stage_bytes;
-            if (lane >= len) {  // the last chunk's missing rows
-                char *st = sm_raw + (at - base);
-                for (int u = 0; u < KT * 2; ++u) {
-                    *reinterpret_cast<uint4 *>(st + lane * kRow + u * 16) = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4 *>(st + kTile + lane * kRow + u * 16) = make_uint4(0, 0, 0, 0);
-                }
-                for (int u = 0; u < w.warps * 2; ++u)
-                    *reinterpret_cast<uint4 *>(st + 2 * kTile + lane * w.vrow + u * 16) = make_uint4(0, 0, 0, 0);
-            }
-            __syncwarp();
-            if (lane == 0)
-                ptx::mbar_expect_tx(full + 8 * sg, len * (2 * p.dk + width) * 2 + (int)sizeof(FwdRecord));
-            __syncwarp();
-            const int64_t row = r.start + (int64_t)c * kC + lane;
-            if (lane < len) {
-                ptx::bulk_load_g2s(at + lane * kRow, k + (row * p.Hk + hk) * p.dk, p.dk * 2, full + 8 * sg);
-                ptx::bulk_load_g2s(at + kTile + lane * kRow, q + (row * p.Hk + hk) * p.dk, p.dk * 2, full + 8 * sg);
-                ptx::bulk_load_g2s(at + 2 * kTile + lane * w.vrow, v + (row * p.H + h) * p.dv + col0, width * 2,
-                                   full + 8 * sg);
-            }
-            if (lane == 0)
+            if (lane == 0) {
+                ptx::mbar_expect_tx(full + 8 * sg, (uint32_t)sizeof(FwdRecord));
                 ptx::bulk_load_g2s(at + 2 * kTile + kC * w.vrow, records + (slot0 + c) * p.H + h, sizeof(FwdRecord),
                                    full + 8 * sg);
-            issued = c + 1;
+            }
+#pragma unroll 2
+            for (int i = 0; i < KT * 2; ++i) {  // 32 tokens x KT * 2 units of 16 bytes, zero past len and past dk
+                const int e = i * 32 + lane, t = e / (KT * 2), u = e % (KT * 2);
+                const bool has = t < len && u < kunits;
+                const int64_t off = has ? t * kstride + u * 8 : 0;
+                cp_async16(at + t * kRow + u * 16, kr + off, has);
+                cp_async16(at + kTile + t * kRow + u * 16, qr + off, has);
+            }
+#pragma unroll 2
+            for (int e = lane; e < kC * vunits; e += 32) {
+                const int t = e / vunits, u = e - t * vunits;
+                const bool has = t < len && u < vlive;
+                cp_async16(at + 2 * kTile + t * w.vrow + u * 16, vr + (has ? t * vstride + u * 8 : 0), has);
+            }
+            cp_async_arrive(full + 8 * sg);
+            kr += kC * kstride;
+            qr += kC * kstride;
+            vr += kC * vstride;
         }
-        __syncwarp();
-        if (*abort_flag)  // nothing may be in flight into a block that ends early
-            for (int c = max(0, issued - w.stages); c < issued; ++c)
-                ptx::mbar_wait(full + 8 * (c % w.stages), (c / w.stages) & 1, nullptr, kWaitNs);
+        // nothing may be in flight into a block that ends early; a whole walk has waited for every stage
+        cp_async_wait_all();
+        if (!__all_sync(0xffffffffu, ok)) {
+            *abort_flag = 1;
+            for (int i = 0; i < w.stages; ++i)  // the records' bulk copies, bounded like every wait
+                for (int par = 0; par < 2; ++par) ptx::mbar_wait(full + 8 * i, par, nullptr, kWaitNs / 1000);
+        }
         return;
     }
 
     const int gr = lane >> 2, tg = lane & 3, m8 = lane >> 3, r8 = lane & 7;
     const int col = col0 + warp * 16;
     const bool lo_ok = col < p.dv, hi_ok = col + 8 < p.dv;
-    const int64_t sat = chain * p.dk * p.dv + col + gr;
+    const int64_t sat = (int64_t)chain * p.dk * p.dv + col + gr;
     float S[2 * KT][4];
 #pragma unroll
     for (int n = 0; n < 2 * KT; ++n)
@@ -345,8 +349,8 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
         const uint32_t ks = ring + sg * w.stage_bytes, qs = ks + kTile, vs = qs + kTile + warp * 32,
                        rec = qs + kTile + kC * w.vrow;
         const uint32_t vec = rec + (uint32_t)offsetof(FwdRecord, c) + 8 * tg;
-        // Y = S^T K^T and O = S^T Q^T
-        float Y[4][4] = {}, O[4][4] = {};
+        // Y = S^T K^T
+        float Y[4][4] = {};
         const uint32_t row_off = ((m8 >> 1) * 8 + r8) * kRow + (m8 & 1) * 16;
 #pragma unroll
         for (int i = 0; i < KT; ++i) {
@@ -354,20 +358,20 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 split(S[2 * i + (e >> 1)][(e & 1) * 2], S[2 * i + (e >> 1)][(e & 1) * 2 + 1], ah[e], al[e]);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                uint32_t b[4];
-                ldsm4(b, ks + row_off + t * 16 * kRow + i * 32);
-                mma(Y[2 * t], ah, b[0], b[1]);
-                mma(Y[2 * t + 1], ah, b[2], b[3]);
-                mma(Y[2 * t], al, b[0], b[1]);
-                mma(Y[2 * t + 1], al, b[2], b[3]);
-                ldsm4(b, qs + row_off + t * 16 * kRow + i * 32);
-                mma(O[2 * t], ah, b[0], b[1]);
-                mma(O[2 * t + 1], ah, b[2], b[3]);
-            }
+            // four independent sums in turn: an accumulator is ready again 21 clocks after its product began
+            uint32_t b0[4], b1[4];
+            ldsm4(b0, ks + row_off + i * 32);
+            ldsm4(b1, ks + row_off + 16 * kRow + i * 32);
+            mma(Y[0], ah, b0[0], b0[1]);
+            mma(Y[1], ah, b0[2], b0[3]);
+            mma(Y[2], ah, b1[0], b1[1]);
+            mma(Y[3], ah, b1[2], b1[3]);
+            mma(Y[0], al, b0[0], b0[1]);
+            mma(Y[1], al, b0[2], b0[3]);
+            mma(Y[2], al, b1[0], b1[1]);
+            mma(Y[3], al, b1[2], b1[3]);
         }
-        // X^T = V^T - Y diag(c), as hi and lo parts; O diag(c)
+        // X^T = V^T - Y diag(c), as hi and lo parts
         uint32_t xh[2][4], xl[2][4];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -380,24 +384,30 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
                 split(fmaf(-cc.x, Y[n][0], lo_f(b[2 * u])), fmaf(-cc.y, Y[n][1], hi_f(b[2 * u])), xh[t][2 * u], xl[t][2 * u]);
                 split(fmaf(-cc.x, Y[n][2], lo_f(b[2 * u + 1])), fmaf(-cc.y, Y[n][3], hi_f(b[2 * u + 1])),
                       xh[t][2 * u + 1], xl[t][2 * u + 1]);
-                O[n][0] *= cc.x; O[n][1] *= cc.y; O[n][2] *= cc.x; O[n][3] *= cc.y;
             }
         }
         // R^T = X^T M^T: M is lower triangular, so the first 16 rows meet the first 16 columns only
         float R[4][4] = {};
+        {
+            uint4 m[4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const uint4 mh = lds128(rec + n * 512 + lane * 16), ml = lds128(rec + 2048 + n * 512 + lane * 16);
-            mma(R[n], xh[0], mh.x, mh.y);
-            mma(R[n], xl[0], mh.x, mh.y);
-            mma(R[n], xh[0], ml.x, ml.y);
-            if (n >= 2) {
-                mma(R[n], xh[1], mh.z, mh.w);
-                mma(R[n], xl[1], mh.z, mh.w);
-                mma(R[n], xh[1], ml.z, ml.w);
-            }
+            for (int n = 0; n < 4; ++n) m[n] = lds128(rec + n * 512 + lane * 16);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) mma(R[n], xh[0], m[n].x, m[n].y);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) mma(R[n], xl[0], m[n].x, m[n].y);
+            mma(R[2], xh[1], m[2].z, m[2].w);
+            mma(R[3], xh[1], m[3].z, m[3].w);
+            mma(R[2], xl[1], m[2].z, m[2].w);
+            mma(R[3], xl[1], m[3].z, m[3].w);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) m[n] = lds128(rec + 2048 + n * 512 + lane * 16);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) mma(R[n], xh[0], m[n].x, m[n].y);
+            mma(R[2], xh[1], m[2].z, m[2].w);
+            mma(R[3], xh[1], m[3].z, m[3].w);
         }
-        // O += R^T P^T with R rounded to bf16; U = R diag(d beta) as hi and lo parts
+        // O = S^T Q^T diag(c) + R^T P^T with S and R rounded to bf16; U = R diag(d beta) as hi and lo parts
         uint32_t rh[2][4], uh[2][4], ul[2][4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -408,8 +418,24 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
             split(R[n][0] * db.x, R[n][1] * db.y, uh[t][u], ul[t][u]);
             split(R[n][2] * db.x, R[n][3] * db.y, uh[t][u + 1], ul[t][u + 1]);
         }
+        float O[4][4] = {};
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+            uint32_t a[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[e] = pack(S[2 * i + (e >> 1)][(e & 1) * 2], S[2 * i + (e >> 1)][(e & 1) * 2 + 1]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                uint32_t b[4];
+                ldsm4(b, qs + row_off + t * 16 * kRow + i * 32);
+                mma(O[2 * t], a, b[0], b[1]);
+                mma(O[2 * t + 1], a, b[2], b[3]);
+            }
+        }
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
+            const float2 cc = lds_f2(vec + n * 32);
+            O[n][0] *= cc.x; O[n][1] *= cc.y; O[n][2] *= cc.x; O[n][3] *= cc.y;
             const uint4 pp = lds128(rec + 4096 + n * 512 + lane * 16);
             mma(O[n], rh[0], pp.x, pp.y);
             if (n >= 2) mma(O[n], rh[1], pp.z, pp.w);
@@ -417,15 +443,22 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
         // S^T = c_31 S^T + U K
         const float last = lds_f2(rec + (uint32_t)offsetof(FwdRecord, c) + 8 * 15).y;
 #pragma unroll
-        for (int n = 0; n < 2 * KT; ++n) {
-            uint32_t b[4];
-            ldsm4t(b, ks + lane * kRow + n * 16);
+        for (int n = 0; n < 2 * KT; n += 4) {
+            uint32_t b[4][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[n][e] *= last;
-            mma(S[n], uh[0], b[0], b[1]);
-            mma(S[n], uh[1], b[2], b[3]);
-            mma(S[n], ul[0], b[0], b[1]);
-            mma(S[n], ul[1], b[2], b[3]);
+            for (int m = 0; m < 4; ++m) {
+                ldsm4t(b[m], ks + lane * kRow + (n + m) * 16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[n + m][e] *= last;
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) mma(S[n + m], uh[0], b[m][0], b[m][1]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) mma(S[n + m], uh[1], b[m][2], b[m][3]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) mma(S[n + m], ul[0], b[m][0], b[m][1]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) mma(S[n + m], ul[1], b[m][2], b[m][3]);
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(empty + 8 * sg);
@@ -477,7 +510,7 @@ Walk make_walk(const Shape &p) {
 template <int KT>
 int fwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const void *g, const void *beta,
            const float *h0, bf16 *out, float *hT, FwdRecord *records, cudaStream_t st) {
-    const int64_t units = chunk_slots(total_rows(p), p.nseq, kC) * p.H;
+    const unsigned units = (unsigned)(chunk_slots(total_rows(p), p.nseq, kC) * p.H);
     const int prep_bytes = kPrepWarps * prep_warp_bytes<KT>();
     const Walk w = make_walk<KT>(p);
     const int bytes = 128 + w.warps * kC * kOutRow + w.stages * w.stage_bytes;
@@ -487,7 +520,7 @@ int fwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
         return GLA_ERR_LAUNCH;
     const long long blocks = (long long)p.nseq * p.H * w.splits;
     if (blocks > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
-    delta_prep_kernel<KT><<<(unsigned)((units + kPrepWarps - 1) / kPrepWarps), kPrepWarps * 32, prep_bytes, st>>>(
+    delta_prep_kernel<KT><<<(units + kPrepWarps - 1) / kPrepWarps, kPrepWarps * 32, prep_bytes, st>>>(
         p, units, q, k, g, beta, records);
     delta_fwd_kernel<KT><<<(unsigned)blocks, (w.warps + 1) * 32, bytes, st>>>(p, w, q, k, v, records, h0, out, hT);
     count_launches(2);
