@@ -240,14 +240,22 @@ delta_prep_kernel(Shape p, unsigned units, const bf16 *__restrict__ q, const bf1
 
 struct Walk {           // one block's share of a chain
     int warps, splits;  // column tiles per block, blocks per chain
+    int groups;         // warpgroups that hold those tiles; one more fetches
     int vrow;           // bytes of a staged row of V, an odd number of 16-byte units
     int stages, stage_bytes;
 };
 
+// A block is launched with 128 registers a thread; the fetching warpgroup gives back 72 of them and each of the
+// others takes 24 more: g 152 + 56 <= (g + 1) 128 for up to three.
+constexpr int kMaxThreads = (kMaxWarps / 4 + 1) * 128;
+static_assert(kMaxWarps == 12, "three warpgroups of column tiles: 3 * 152 + 56 = 4 * 128");
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 152;"); }
+
 constexpr int kOutRow = 48;  // bytes of a staged row of 16 output columns: an odd number of 16-byte units
 
 template <int KT>
-__global__ void __launch_bounds__((kMaxWarps + 1) * 32)
+__global__ void __launch_bounds__(kMaxThreads)
 delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16 *__restrict__ v,
                  const FwdRecord *__restrict__ records, const float *__restrict__ h0, bf16 *__restrict__ out,
                  float *__restrict__ hT) {
@@ -268,7 +276,7 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
     const uint32_t outs = base + 128, ring = outs + w.warps * kC * kOutRow;
     if (threadIdx.x == 0) {
         for (int i = 0; i < w.stages; ++i) {
-            ptx::mbar_init(full + 8 * i, 33);  // the fetching warp's lanes, and its first lane's record
+            ptx::mbar_init(full + 8 * i, 129);  // the fetching threads, and the record
             ptx::mbar_init(empty + 8 * i, w.warps);
         }
         *abort_flag = 0;
@@ -277,36 +285,37 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
     __syncthreads();
     const int64_t slot0 = r.start / kC + s;
 
-    if (warp == w.warps) {  // the fetching warp
+    if (warp >= w.groups * 4) {  // the fetching warpgroup: four threads to a token's row
+        give_registers();
+        const int id = threadIdx.x - w.groups * 128, t = id >> 2, u0 = id & 3;
         const int vunits = w.warps * 2, vlive = width / 8, kunits = p.dk / 8;
         const int64_t kstride = (int64_t)p.Hk * p.dk, vstride = (int64_t)p.H * p.dv;
-        const bf16 *kr = k + r.start * kstride + hk * p.dk, *qr = q + r.start * kstride + hk * p.dk,
-                   *vr = v + r.start * vstride + (int64_t)h * p.dv + col0;
+        const bf16 *kr = k + (r.start + t) * kstride + hk * p.dk + u0 * 8,
+                   *qr = q + (r.start + t) * kstride + hk * p.dk + u0 * 8,
+                   *vr = v + (r.start + t) * vstride + (int64_t)h * p.dv + col0 + u0 * 8;
+        const uint32_t kdst = ring + t * kRow + u0 * 16, vdst = ring + 2 * kTile + t * w.vrow + u0 * 16;
         bool ok = true;
         for (int c = 0; c < nch; ++c) {
             const int sg = c % w.stages;
             ok = c < w.stages || ptx::mbar_wait(empty + 8 * sg, (c / w.stages + 1) & 1, abort_flag, kWaitNs);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            const int len = (int)min((int64_t)kC, r.len - (int64_t)c * kC);
-            const uint32_t at = ring + sg * w.stage_bytes;
-            if (lane == 0) {
+            if (!ok) break;
+            const bool row = c * kC + t < r.len;  // a short chunk's missing rows are zero, and not read
+            const uint32_t at = sg * w.stage_bytes;
+            if (id == 0) {
                 ptx::mbar_expect_tx(full + 8 * sg, (uint32_t)sizeof(FwdRecord));
-                ptx::bulk_load_g2s(at + 2 * kTile + kC * w.vrow, records + (slot0 + c) * p.H + h, sizeof(FwdRecord),
-                                   full + 8 * sg);
+                ptx::bulk_load_g2s(ring + at + 2 * kTile + kC * w.vrow, records + (slot0 + c) * p.H + h,
+                                   sizeof(FwdRecord), full + 8 * sg);
+            }
+#pragma unroll
+            for (int u = 0; u < KT * 2; u += 4) {
+                const bool has = row && u0 + u < kunits;
+                cp_async16(kdst + at + u * 16, has ? kr + u * 8 : k, has);
+                cp_async16(kdst + at + kTile + u * 16, has ? qr + u * 8 : q, has);
             }
 #pragma unroll 2
-            for (int i = 0; i < KT * 2; ++i) {  // 32 tokens x KT * 2 units of 16 bytes, zero past len and past dk
-                const int e = i * 32 + lane, t = e / (KT * 2), u = e % (KT * 2);
-                const bool has = t < len && u < kunits;
-                const int64_t off = has ? t * kstride + u * 8 : 0;
-                cp_async16(at + t * kRow + u * 16, kr + off, has);
-                cp_async16(at + kTile + t * kRow + u * 16, qr + off, has);
-            }
-#pragma unroll 2
-            for (int e = lane; e < kC * vunits; e += 32) {
-                const int t = e / vunits, u = e - t * vunits;
-                const bool has = t < len && u < vlive;
-                cp_async16(at + 2 * kTile + t * w.vrow + u * 16, vr + (has ? t * vstride + u * 8 : 0), has);
+            for (int u = 0; u < vunits - u0; u += 4) {
+                const bool has = row && u0 + u < vlive;
+                cp_async16(vdst + at + u * 16, has ? vr + u * 8 : v, has);
             }
             cp_async_arrive(full + 8 * sg);
             kr += kC * kstride;
@@ -315,7 +324,7 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
         }
         // nothing may be in flight into a block that ends early; a whole walk has waited for every stage
         cp_async_wait_all();
-        if (!__all_sync(0xffffffffu, ok)) {
+        if (!ok) {
             *abort_flag = 1;
             for (int i = 0; i < w.stages; ++i)  // the records' bulk copies, bounded like every wait
                 for (int par = 0; par < 2; ++par) ptx::mbar_wait(full + 8 * i, par, nullptr, kWaitNs / 1000);
@@ -323,6 +332,8 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
         return;
     }
 
+    take_registers();
+    if (warp >= w.warps) return;
     const int gr = lane >> 2, tg = lane & 3, m8 = lane >> 3, r8 = lane & 7;
     const int col = col0 + warp * 16;
     const bool lo_ok = col < p.dv, hi_ok = col + 8 < p.dv;
@@ -501,6 +512,7 @@ Walk make_walk(const Shape &p) {
     if (chains * splits < sms) splits = (int)min((long long)tiles, sms / chains);
     w.warps = (tiles + splits - 1) / splits;
     w.splits = (tiles + w.warps - 1) / w.warps;
+    w.groups = (w.warps + 3) / 4;
     w.vrow = (w.warps * 2 | 1) * 16;
     w.stage_bytes = 2 * kC * row_bytes<KT>() + kC * w.vrow + (int)sizeof(FwdRecord);
     w.stages = 4;
@@ -522,7 +534,7 @@ int fwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
     if (blocks > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
     delta_prep_kernel<KT><<<(units + kPrepWarps - 1) / kPrepWarps, kPrepWarps * 32, prep_bytes, st>>>(
         p, units, q, k, g, beta, records);
-    delta_fwd_kernel<KT><<<(unsigned)blocks, (w.warps + 1) * 32, bytes, st>>>(p, w, q, k, v, records, h0, out, hT);
+    delta_fwd_kernel<KT><<<(unsigned)blocks, (w.groups + 1) * 128, bytes, st>>>(p, w, q, k, v, records, h0, out, hT);
     count_launches(2);
     return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
 }
