@@ -68,6 +68,10 @@ template <typename T>
 int simt_bwd(const Shape &, const T *, const T *, const T *, const void *, const void *, const T *, const float *,
              const float *, T *, T *, T *, void *, void *, float *, void *, cudaStream_t);
 bool mma_supported(int dk);
+bool mma_bwd_supported(int dk, int dv);
+size_t mma_bwd_workspace(const Shape &);
+int mma_bwd(const Shape &, const void *, const void *, const void *, const void *, const void *, const void *,
+            const float *, const float *, void *, void *, void *, void *, void *, float *, void *, cudaStream_t);
 size_t mma_fwd_workspace(const Shape &);
 int mma_fwd(const Shape &, const void *, const void *, const void *, const void *, const void *, const float *, void *,
             float *, void *, cudaStream_t);
@@ -83,6 +87,7 @@ int group_norm_bwd(const void *, const void *, const float *, const float *, con
 }  // namespace norm
 int take_status_delta(cudaStream_t);
 int take_status_delta_mma(cudaStream_t);
+int take_status_delta_bwd(cudaStream_t);
 int take_status_conv(cudaStream_t);
 int take_status_simt(cudaStream_t);
 int take_status_bwd(cudaStream_t);
@@ -220,7 +225,8 @@ delta::Shape delta_shape(int B, int T, int H, int Hk, int dk, int dv, int dtype,
 long long delta_workspace(int op, const delta::Shape &p, int dtype) {
     if (op == GLA_OP_FORWARD)
         return dtype == GLA_BF16 && delta::mma_supported(p.dk) ? (long long)delta::mma_fwd_workspace(p) : 0;
-    return (long long)delta::simt_bwd_workspace(p);
+    return (long long)(dtype == GLA_BF16 && delta::mma_bwd_supported(p.dk, p.dv) ? delta::mma_bwd_workspace(p)
+                                                                                : delta::simt_bwd_workspace(p));
 }
 
 int check_norm(const void *x, const float *weight, const float *bias, const void *gate, int act, float eps,
@@ -491,6 +497,8 @@ int gla_delta_chunk_bwd(const void *q, const void *k, const void *v, const void 
         return delta::simt_bwd<float>(p, (const float *)q, (const float *)k, (const float *)v, g, beta,
                                       (const float *)dout, h0, dhT, (float *)dq, (float *)dk_out, (float *)dv_out, dg,
                                       dbeta, dh0, ws, st);
+    if (delta::mma_bwd_supported(dk, dv))
+        return delta::mma_bwd(p, q, k, v, g, beta, dout, h0, dhT, dq, dk_out, dv_out, dg, dbeta, dh0, ws, st);
     return delta::simt_bwd<H16>(p, (const H16 *)q, (const H16 *)k, (const H16 *)v, g, beta, (const H16 *)dout, h0, dhT,
                                 (H16 *)dq, (H16 *)dk_out, (H16 *)dv_out, dg, dbeta, dh0, ws, st);
 }
@@ -541,8 +549,9 @@ int gla_group_norm_bwd(const void *dout, const void *x, const float *weight, con
 int gla_last_device_status(void *stream) {
     cudaStream_t st = (cudaStream_t)stream;
     int result = GLA_OK;
-    const int parts[7] = {take_status_simt(st), take_status_decode(st), take_status_tc(st), take_status_bwd(st),
-                          take_status_conv(st), take_status_delta(st), take_status_delta_mma(st)};
+    const int parts[8] = {take_status_simt(st), take_status_decode(st), take_status_tc(st), take_status_bwd(st),
+                          take_status_conv(st), take_status_delta(st), take_status_delta_mma(st),
+                          take_status_delta_bwd(st)};
     for (int p : parts) {
         if (p == GLA_ERR_LAUNCH) return GLA_ERR_LAUNCH;
         if (result == GLA_OK && p != 0) result = p;

@@ -28,78 +28,13 @@
 // A warp of its own fetches the rows of K, Q and V by 16-byte asynchronous copies (zero past a sequence's end, so
 // a short chunk is computed like a whole one) and the chunk's M, P, c and d beta by one bulk copy into a ring of
 // stages; a row's stride is an odd number of 16-byte units, so that ldmatrix meets no bank twice.
-#include "gla_delta.cuh"
-#include "sm100_ptx.cuh"
+#include "gla_delta_mma.cuh"
 
 GLA_DEFINE_STATUS(delta_mma)
 
 namespace gla {
 namespace delta {
 namespace {
-
-using bf16 = __nv_bfloat16;
-constexpr int kC = 32;                  // tokens per chunk of a walk
-constexpr int kMaxWarps = 12;           // column tiles of 16 per block
-constexpr uint64_t kWaitNs = 2000000000ull;
-
-// Per chunk and value head, in the order of the B operands: [4 tiles of 8 columns][32 lanes] x 16 bytes
-// (k 0..15 then 16..31).
-struct FwdRecord {
-    uint4 mhi[4][32], mlo[4][32], p[4][32];
-    float c[kC], db[kC];  // c_i and d_j beta_j
-};
-static_assert(sizeof(FwdRecord) % 16 == 0, "bulk copies take multiples of 16 bytes");
-
-// ---- fragments -----------------------------------------------------------------------------------------------
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void stsm4t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
-                 ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 t;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(t.x), "=r"(t.y), "=r"(t.z), "=r"(t.w) : "r"(addr) : "memory");
-    return t;
-}
-__device__ __forceinline__ float2 lds_f2(uint32_t addr) {
-    float2 t;
-    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(t.x), "=f"(t.y) : "r"(addr) : "memory");
-    return t;
-}
-// 16 bytes from global to shared memory, or 16 zero bytes
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool has) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(has ? 16 : 0) : "memory");
-}
-// this thread's arrival on `bar` once all of its copies so far have landed
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// two f32 to two bf16 (x in the low half), round to nearest
-__device__ __forceinline__ uint32_t pack(float x, float y) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
-    return r;
-}
-__device__ __forceinline__ float lo_f(uint32_t p) { return __uint_as_float(p << 16); }
-__device__ __forceinline__ float hi_f(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
-// x, y as hi + lo parts of 8 bits each
-__device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &lo) {
-    hi = pack(x, y);
-    lo = pack(x - lo_f(hi), y - hi_f(hi));
-}
 
 // ---- what does not depend on the state -----------------------------------------------------------------------
 //
@@ -110,7 +45,6 @@ __device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &
 constexpr int kPrepWarps = 4;
 constexpr int kLd = 36;  // f32 row stride of the 32 x 32 tiles: rows 16-byte aligned, columns on different banks
 
-template <int KT> constexpr int row_bytes() { return KT * 32 + 16; }  // KT * 16 bf16 and an odd number of 16-byte units
 template <int KT> constexpr int prep_warp_bytes() {
     const int tiles = 2 * kC * row_bytes<KT>(), mats = 2 * kC * kLd * 4;
     return tiles > mats ? tiles : mats;
@@ -127,10 +61,46 @@ __device__ __forceinline__ void fetch_rows(uint32_t dst, const bf16 *src, int64_
     }
 }
 
-template <int KT>
+// column `lane` of (I + L diag(beta))^-1 in t
+__device__ __forceinline__ void invert(const float *L, float be, int lane, float (&t)[kC]) {
+    float s[kC];  // beta t
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+        float x0 = i == lane ? 1.f : 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
+#pragma unroll
+        for (int l = 0; l < i; l += 4) {
+            const float4 row = *reinterpret_cast<const float4 *>(L + i * kLd + l);
+            x0 = fmaf(-row.x, s[l], x0);
+            if (l + 1 < i) x1 = fmaf(-row.y, s[l + 1], x1);
+            if (l + 2 < i) x2 = fmaf(-row.z, s[l + 2], x2);
+            if (l + 3 < i) x3 = fmaf(-row.w, s[l + 3], x3);
+        }
+        t[i] = (x0 + x1) + (x2 + x3);
+        s[i] = t[i] * __shfl_sync(0xffffffffu, be, i);
+    }
+}
+// column `lane` of (I + diag(beta) L)^-1 in t
+__device__ __forceinline__ void invert_left(const float *L, float be, int lane, float (&t)[kC]) {
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+        float x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
+#pragma unroll
+        for (int l = 0; l < i; l += 4) {
+            const float4 row = *reinterpret_cast<const float4 *>(L + i * kLd + l);
+            x0 = fmaf(row.x, t[l], x0);
+            if (l + 1 < i) x1 = fmaf(row.y, t[l + 1], x1);
+            if (l + 2 < i) x2 = fmaf(row.z, t[l + 2], x2);
+            if (l + 3 < i) x3 = fmaf(row.w, t[l + 3], x3);
+        }
+        t[i] = (i == lane ? 1.f : 0.f) - __shfl_sync(0xffffffffu, be, i) * ((x0 + x1) + (x2 + x3));
+    }
+}
+
+template <int KT, bool kGrad>
 __global__ void __launch_bounds__(kPrepWarps * 32)
 delta_prep_kernel(Shape p, unsigned units, const bf16 *__restrict__ q, const bf16 *__restrict__ k,
-                  const void *__restrict__ g, const void *__restrict__ beta, FwdRecord *__restrict__ records) {
+                  const void *__restrict__ g, const void *__restrict__ beta, FwdRecord *__restrict__ records,
+                  AgainRecord *__restrict__ again, BwdRecord *__restrict__ back) {
     extern __shared__ __align__(128) char sm_raw[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned unit = blockIdx.x * kPrepWarps + warp;  // slot * H + h
@@ -194,29 +164,42 @@ delta_prep_kernel(Shape p, unsigned units, const bf16 *__restrict__ q, const bf1
         f = i == lane ? 1.f : f * ai;
         const int e = i * kLd + lane;
         kap[e] = i > lane ? f * kap[e] : 0.f;
-        qk[e] = i >= lane ? f * qk[e] * be : 0.f;
+        qk[e] = i >= lane ? f * qk[e] * (kGrad ? 1.f : be) : 0.f;
     }
     __syncwarp();
-    float t[kC], s[kC];  // t: column `lane` of the inverse, s: beta t
+    float t[kC];
+    if (kGrad) {
+        // (I + diag(beta) L)^-1 goes out first; L stays for the other inverse
+        float left[kC];
+        invert_left(kap, be, lane, left);
+        invert(kap, be, lane, t);
+        __syncwarp();
 #pragma unroll
-    for (int i = 0; i < kC; ++i) {
-        float x0 = i == lane ? 1.f : 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
+        for (int i = 0; i < kC; ++i) kap[i * kLd + lane] = left[i];
+        __syncwarp();
+        BwdRecord *rec = back + unit;
 #pragma unroll
-        for (int l = 0; l < i; l += 4) {
-            const float4 row = *reinterpret_cast<const float4 *>(kap + i * kLd + l);
-            x0 = fmaf(-row.x, s[l], x0);
-            if (l + 1 < i) x1 = fmaf(-row.y, s[l + 1], x1);
-            if (l + 2 < i) x2 = fmaf(-row.z, s[l + 2], x2);
-            if (l + 3 < i) x3 = fmaf(-row.w, s[l + 3], x3);
+        for (int n = 0; n < 4; ++n) {
+            uint32_t mm[4], pp[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int at0 = (e * 8 + 2 * tg) * kLd + n * 8 + gr;
+                mm[e] = pack(kap[at0], kap[at0 + kLd]);
+                pp[e] = pack(qk[at0], qk[at0 + kLd]);
+            }
+            rec->m[n][lane] = make_uint4(mm[0], mm[1], mm[2], mm[3]);
+            rec->p[n][lane] = make_uint4(pp[0], pp[1], pp[2], pp[3]);
         }
-        t[i] = (x0 + x1) + (x2 + x3);
-        s[i] = t[i] * __shfl_sync(0xffffffffu, be, i);
+        rec->c[lane] = c;
+        rec->d[lane] = f;
+        rec->b[lane] = be;
+    } else {
+        invert(kap, be, lane, t);
     }
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < kC; ++i) kap[i * kLd + lane] = t[i];
     __syncwarp();
-    FwdRecord *rec = records + unit;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
         uint32_t hi[4], lo[4], pp[4];
@@ -228,31 +211,19 @@ delta_prep_kernel(Shape p, unsigned units, const bf16 *__restrict__ q, const bf1
             split(m.x, m.y, hi[e], lo[e]);
             pp[e] = pack(x.x, x.y);
         }
-        rec->mhi[n][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        rec->mlo[n][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        rec->p[n][lane] = make_uint4(pp[0], pp[1], pp[2], pp[3]);
+        if (kGrad) {
+            again[unit].mhi[n][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        } else {
+            records[unit].mhi[n][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            records[unit].mlo[n][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            records[unit].p[n][lane] = make_uint4(pp[0], pp[1], pp[2], pp[3]);
+        }
     }
-    rec->c[lane] = c;
-    rec->db[lane] = f * be;
+    (kGrad ? again[unit].c : records[unit].c)[lane] = c;
+    (kGrad ? again[unit].db : records[unit].db)[lane] = f * be;
 }
 
 // ---- the walk ---------------------------------------------------------------------------------------------------
-
-struct Walk {           // one block's share of a chain
-    int warps, splits;  // column tiles per block, blocks per chain
-    int groups;         // warpgroups that hold those tiles; one more fetches
-    int vrow;           // bytes of a staged row of V, an odd number of 16-byte units
-    int stages, stage_bytes;
-};
-
-// A block is launched with 128 registers a thread; the fetching warpgroup gives back 72 of them and each of the
-// others takes 24 more: g 152 + 56 <= (g + 1) 128 for up to three.
-constexpr int kMaxThreads = (kMaxWarps / 4 + 1) * 128;
-static_assert(kMaxWarps == 12, "three warpgroups of column tiles: 3 * 152 + 56 = 4 * 128");
-__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
-__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 152;"); }
-
-constexpr int kOutRow = 48;  // bytes of a staged row of 16 output columns: an odd number of 16-byte units
 
 template <int KT>
 __global__ void __launch_bounds__(kMaxThreads)
@@ -261,103 +232,30 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
                  float *__restrict__ hT) {
     extern __shared__ __align__(128) char sm_raw[];
     constexpr int kRow = row_bytes<KT>(), kTile = kC * kRow;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int chain = (int)(blockIdx.x / (unsigned)w.splits), part = (int)(blockIdx.x % (unsigned)w.splits);
-    const int s = chain / p.H, h = chain % p.H, hk = h / p.group();
-    const int col0 = part * w.warps * 16;                       // first column of the block
-    const int width = min(w.warps * 16, p.dv - col0);           // its columns, a multiple of 8
-    SeqRange r;
-    if (!seq_range(s, p.T, p.cu, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
-    const int nch = (int)((r.len + kC - 1) / kC);
-    // shared memory: barriers, the warps' output tiles, the stages (K | Q | V | record)
-    const uint32_t base = ptx::smem_u32(sm_raw);
-    const uint32_t full = base, empty = base + 8 * w.stages;
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm_raw + 16 * w.stages);
-    const uint32_t outs = base + 128, ring = outs + w.warps * kC * kOutRow;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < w.stages; ++i) {
-            ptx::mbar_init(full + 8 * i, 129);  // the fetching threads, and the record
-            ptx::mbar_init(empty + 8 * i, w.warps);
-        }
-        *abort_flag = 0;
-        ptx::fence_mbar_init();
-    }
-    __syncthreads();
-    const int64_t slot0 = r.start / kC + s;
-
-    if (warp >= w.groups * 4) {  // the fetching warpgroup: four threads to a token's row
+    const Frame f(p, w, sm_raw);
+    if (f.bad && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
+    if (f.warp >= w.groups * 4) {
         give_registers();
-        const int id = threadIdx.x - w.groups * 128, t = id >> 2, u0 = id & 3;
-        const int vunits = w.warps * 2, vlive = width / 8, kunits = p.dk / 8;
-        const int64_t kstride = (int64_t)p.Hk * p.dk, vstride = (int64_t)p.H * p.dv;
-        const bf16 *kr = k + (r.start + t) * kstride + hk * p.dk + u0 * 8,
-                   *qr = q + (r.start + t) * kstride + hk * p.dk + u0 * 8,
-                   *vr = v + (r.start + t) * vstride + (int64_t)h * p.dv + col0 + u0 * 8;
-        const uint32_t kdst = ring + t * kRow + u0 * 16, vdst = ring + 2 * kTile + t * w.vrow + u0 * 16;
-        bool ok = true;
-        for (int c = 0; c < nch; ++c) {
-            const int sg = c % w.stages;
-            ok = c < w.stages || ptx::mbar_wait(empty + 8 * sg, (c / w.stages + 1) & 1, abort_flag, kWaitNs);
-            if (!ok) break;
-            const bool row = c * kC + t < r.len;  // a short chunk's missing rows are zero, and not read
-            const uint32_t at = sg * w.stage_bytes;
-            if (id == 0) {
-                ptx::mbar_expect_tx(full + 8 * sg, (uint32_t)sizeof(FwdRecord));
-                ptx::bulk_load_g2s(ring + at + 2 * kTile + kC * w.vrow, records + (slot0 + c) * p.H + h,
-                                   sizeof(FwdRecord), full + 8 * sg);
-            }
-#pragma unroll
-            for (int u = 0; u < KT * 2; u += 4) {
-                const bool has = row && u0 + u < kunits;
-                cp_async16(kdst + at + u * 16, has ? kr + u * 8 : k, has);
-                cp_async16(kdst + at + kTile + u * 16, has ? qr + u * 8 : q, has);
-            }
-#pragma unroll 2
-            for (int u = 0; u < vunits - u0; u += 4) {
-                const bool has = row && u0 + u < vlive;
-                cp_async16(vdst + at + u * 16, has ? vr + u * 8 : v, has);
-            }
-            cp_async_arrive(full + 8 * sg);
-            kr += kC * kstride;
-            qr += kC * kstride;
-            vr += kC * vstride;
-        }
-        // nothing may be in flight into a block that ends early; a whole walk has waited for every stage
-        cp_async_wait_all();
-        if (!ok) {
-            *abort_flag = 1;
-            for (int i = 0; i < w.stages; ++i)  // the records' bulk copies, bounded like every wait
-                for (int par = 0; par < 2; ++par) ptx::mbar_wait(full + 8 * i, par, nullptr, kWaitNs / 1000);
-        }
+        fetch<KT, true, false>(p, w, f, q, k, v, records);
         return;
     }
-
     take_registers();
-    if (warp >= w.warps) return;
-    const int gr = lane >> 2, tg = lane & 3, m8 = lane >> 3, r8 = lane & 7;
-    const int col = col0 + warp * 16;
-    const bool lo_ok = col < p.dv, hi_ok = col + 8 < p.dv;
-    const int64_t sat = (int64_t)chain * p.dk * p.dv + col + gr;
+    if (f.warp >= w.warps) return;
+    const int lane = f.lane, tg = lane & 3, m8 = lane >> 3, r8 = lane & 7;
+    const int col = f.col0 + f.warp * 16;
+    const uint32_t o_tile = f.outs + f.warp * kC * kOutRow;
     float S[2 * KT][4];
-#pragma unroll
-    for (int n = 0; n < 2 * KT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int row = n * 8 + 2 * tg + (e & 1);
-            S[n][e] = h0 != nullptr && row < p.dk && (e < 2 ? lo_ok : hi_ok) ? h0[sat + (int64_t)row * p.dv + (e >> 1) * 8]
-                                                                            : 0.f;
-        }
-    const uint32_t o_tile = outs + warp * kC * kOutRow;
-    for (int c = 0; c < nch; ++c) {
+    load_state<KT>(S, h0, p, f.chain, col, lane);
+    for (int c = 0; c < f.nch; ++c) {
         const int sg = c % w.stages;
-        if (!ptx::mbar_wait(full + 8 * sg, (c / w.stages) & 1, abort_flag, kWaitNs)) {
+        if (!ptx::mbar_wait(f.full + 8 * sg, (c / w.stages) & 1, f.abort_flag, kWaitNs)) {
             if (lane == 0) {
-                *abort_flag = 1;
+                *f.abort_flag = 1;
                 record_status(GLA_ERR_TIMEOUT);
             }
             return;
         }
-        const uint32_t ks = ring + sg * w.stage_bytes, qs = ks + kTile, vs = qs + kTile + warp * 32,
+        const uint32_t ks = f.ring + sg * w.stage_bytes, qs = ks + kTile, vs = qs + kTile + f.warp * 32,
                        rec = qs + kTile + kC * w.vrow;
         const uint32_t vec = rec + (uint32_t)offsetof(FwdRecord, c) + 8 * tg;
         // Y = S^T K^T
@@ -472,70 +370,40 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
             for (int m = 0; m < 4; ++m) mma(S[n + m], ul[1], b[m][2], b[m][3]);
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(empty + 8 * sg);
-        // O^T through the warp's tile to rows of 32 bytes
-        const uint32_t to = o_tile + ((m8 >> 1) * 8 + r8) * kOutRow + (m8 & 1) * 16;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-            stsm4t(to + t * 16 * kOutRow, pack(O[2 * t][0], O[2 * t][1]), pack(O[2 * t][2], O[2 * t][3]),
-                   pack(O[2 * t + 1][0], O[2 * t + 1][1]), pack(O[2 * t + 1][2], O[2 * t + 1][3]));
-        __syncwarp();
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int i = t * 16 + (lane >> 1), cc = col + (lane & 1) * 8;
-            const int64_t tok = (int64_t)c * kC + i;
-            const uint4 x = lds128(o_tile + i * kOutRow + (lane & 1) * 16);
-            if (tok < r.len && cc < p.dv) *reinterpret_cast<uint4 *>(out + ((r.start + tok) * p.H + h) * p.dv + cc) = x;
-        }
-        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(f.empty + 8 * sg);
+        write_tile(out, O, p, f, c, col, o_tile);
     }
-    if (hT != nullptr) {
-#pragma unroll
-        for (int n = 0; n < 2 * KT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = n * 8 + 2 * tg + (e & 1);
-                if (row < p.dk && (e < 2 ? lo_ok : hi_ok)) hT[sat + (int64_t)row * p.dv + (e >> 1) * 8] = S[n][e];
-            }
-    }
+    if (hT != nullptr) store_state<KT>(hT, S, p, f.chain, col, lane);
 }
 
-// Blocks per chain: one where the chains fill the GPU (the fewest reads of K and Q), else as many as fill it.
-// B8 T2048 H16 dk96 dv192 (128 chains, 152 SMs) runs one block of 12 column tiles to a chain; B1 (16 chains) six
-// blocks of two.
-template <int KT>
-Walk make_walk(const Shape &p) {
-    Walk w{};
-    const int tiles = (p.dv + 15) / 16, sms = device_info().sm_count;
-    const long long chains = (long long)p.nseq * p.H;
-    int splits = (tiles + kMaxWarps - 1) / kMaxWarps;
-    if (chains * splits < sms) splits = (int)min((long long)tiles, sms / chains);
-    w.warps = (tiles + splits - 1) / splits;
-    w.splits = (tiles + w.warps - 1) / w.warps;
-    w.groups = (w.warps + 3) / 4;
-    w.vrow = (w.warps * 2 | 1) * 16;
-    w.stage_bytes = 2 * kC * row_bytes<KT>() + kC * w.vrow + (int)sizeof(FwdRecord);
-    w.stages = 4;
-    return w;
+template <int KT, bool kGrad>
+int launch_prep(const Shape &p, const bf16 *q, const bf16 *k, const void *g, const void *beta, FwdRecord *records,
+                AgainRecord *again, BwdRecord *back, cudaStream_t st) {
+    const unsigned units = (unsigned)(chunk_slots(total_rows(p), p.nseq, kC) * p.H);
+    const int bytes = kPrepWarps * prep_warp_bytes<KT>();
+    if (cudaFuncSetAttribute(delta_prep_kernel<KT, kGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+        cudaSuccess)
+        return GLA_ERR_LAUNCH;
+    delta_prep_kernel<KT, kGrad><<<(units + kPrepWarps - 1) / kPrepWarps, kPrepWarps * 32, bytes, st>>>(
+        p, units, q, k, g, beta, records, again, back);
+    count_launches(1);
+    return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
 }
 
 template <int KT>
 int fwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const void *g, const void *beta,
            const float *h0, bf16 *out, float *hT, FwdRecord *records, cudaStream_t st) {
-    const unsigned units = (unsigned)(chunk_slots(total_rows(p), p.nseq, kC) * p.H);
-    const int prep_bytes = kPrepWarps * prep_warp_bytes<KT>();
-    const Walk w = make_walk<KT>(p);
-    const int bytes = 128 + w.warps * kC * kOutRow + w.stages * w.stage_bytes;
-    if (cudaFuncSetAttribute(delta_prep_kernel<KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, prep_bytes) !=
-            cudaSuccess ||
-        cudaFuncSetAttribute(delta_fwd_kernel<KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-        return GLA_ERR_LAUNCH;
+    const Walk w = make_walk<KT, FwdRecord>(p, true);
     const long long blocks = (long long)p.nseq * p.H * w.splits;
     if (blocks > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
-    delta_prep_kernel<KT><<<(units + kPrepWarps - 1) / kPrepWarps, kPrepWarps * 32, prep_bytes, st>>>(
-        p, units, q, k, g, beta, records);
-    delta_fwd_kernel<KT><<<(unsigned)blocks, (w.groups + 1) * 128, bytes, st>>>(p, w, q, k, v, records, h0, out, hT);
-    count_launches(2);
+    if (cudaFuncSetAttribute(delta_fwd_kernel<KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, walk_bytes(w)) !=
+        cudaSuccess)
+        return GLA_ERR_LAUNCH;
+    int rc = launch_prep<KT, false>(p, q, k, g, beta, records, nullptr, nullptr, st);
+    if (rc != GLA_OK) return rc;
+    delta_fwd_kernel<KT><<<(unsigned)blocks, (w.groups + 1) * 128, walk_bytes(w), st>>>(p, w, q, k, v, records, h0, out,
+                                                                                      hT);
+    count_launches(1);
     return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
 }
 
@@ -552,10 +420,17 @@ int mma_fwd(const Shape &p, const void *q, const void *k, const void *v, const v
             const float *h0, void *out, float *hT, void *ws, cudaStream_t st) {
 #define GLA_CALL(KT) \
     return fwd_kt<KT>(p, (const bf16 *)q, (const bf16 *)k, (const bf16 *)v, g, beta, h0, (bf16 *)out, hT, (FwdRecord *)ws, st)
-    if (p.dk <= 32) { GLA_CALL(2); }
-    if (p.dk <= 64) { GLA_CALL(4); }
-    if (p.dk <= 96) { GLA_CALL(6); }
-    GLA_CALL(8);
+    GLA_BY_KT(p.dk, GLA_CALL);
+#undef GLA_CALL
+}
+
+// The gradient's records (gla_delta_bwd.cu).
+int mma_prep_grad(const Shape &p, const void *q, const void *k, const void *g, const void *beta, void *again, void *back,
+                  cudaStream_t st) {
+#define GLA_CALL(KT)                                                                                               \
+    return launch_prep<KT, true>(p, (const bf16 *)q, (const bf16 *)k, g, beta, nullptr, (AgainRecord *)again,      \
+                                 (BwdRecord *)back, st)
+    GLA_BY_KT(p.dk, GLA_CALL);
 #undef GLA_CALL
 }
 

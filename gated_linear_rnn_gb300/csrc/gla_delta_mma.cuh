@@ -1,0 +1,280 @@
+// gla_delta_mma.cuh — what the tensor-core kernels of the gated delta rule share: chunk records, mma.sync
+// fragments, and the frame of a walk over a chain (fetching warpgroup, stages, state and output tiles).
+#pragma once
+
+#include "gla_delta.cuh"
+#include "sm100_ptx.cuh"
+
+namespace gla {
+namespace delta {
+namespace {
+
+using bf16 = __nv_bfloat16;
+constexpr int kC = 32;                  // tokens per chunk of a walk
+constexpr int kMaxWarps = 12;           // column tiles of 16 per block
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+// Per chunk and value head, in the order of the B operands: [4 tiles of 8 columns][32 lanes] x 16 bytes
+// (k 0..15 then 16..31).
+struct FwdRecord {
+    uint4 mhi[4][32], mlo[4][32], p[4][32];
+    float c[kC], db[kC];  // c_i and d_j beta_j
+};
+// For the gradient: the walk that recomputes the residuals takes M alone; the walk backwards takes P without beta
+// and (I + diag(beta) L)^-1, both as B operands of products over the token that reads (k = i, n = j).
+struct AgainRecord {
+    uint4 mhi[4][32];
+    float c[kC], db[kC];
+};
+struct BwdRecord {
+    uint4 p[4][32], m[4][32];
+    float c[kC], d[kC], b[kC];
+};
+static_assert(sizeof(FwdRecord) % 16 == 0 && sizeof(AgainRecord) % 16 == 0 && sizeof(BwdRecord) % 16 == 0,
+              "bulk copies take multiples of 16 bytes");
+
+// ---- fragments -----------------------------------------------------------------------------------------------
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void stsm4t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
+                 ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 t;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(t.x), "=r"(t.y), "=r"(t.z), "=r"(t.w) : "r"(addr) : "memory");
+    return t;
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t addr) {
+    float2 t;
+    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(t.x), "=f"(t.y) : "r"(addr) : "memory");
+    return t;
+}
+// 16 bytes from global to shared memory, or 16 zero bytes
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool has) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(has ? 16 : 0) : "memory");
+}
+// this thread's arrival on `bar` once all of its copies so far have landed
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// two f32 to two bf16 (x in the low half), round to nearest
+__device__ __forceinline__ uint32_t pack(float x, float y) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lo_f(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float hi_f(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+// x, y as hi + lo parts of 8 bits each
+__device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = pack(x, y);
+    lo = pack(x - lo_f(hi), y - hi_f(hi));
+}
+
+// 8 x 8 b16 values, a row's pair in each lane, transposed within the warp
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int KT> constexpr int row_bytes() { return KT * 32 + 16; }  // KT * 16 bf16 and an odd number of 16-byte units
+
+// ---- the frame of a walk -----------------------------------------------------------------------------------------
+
+struct Walk {           // one block's share of a chain
+    int warps, splits;  // column tiles per block, blocks per chain
+    int groups;         // warpgroups that hold those tiles; one more fetches
+    int vrow;           // bytes of a staged row of V, an odd number of 16-byte units
+    int stages, stage_bytes;
+};
+
+// A block is launched with 128 registers a thread; the fetching warpgroup gives back 72 of them and each of the
+// others takes 24 more: g 152 + 56 <= (g + 1) 128 for up to three.
+constexpr int kMaxThreads = (kMaxWarps / 4 + 1) * 128;
+static_assert(kMaxWarps == 12, "three warpgroups of column tiles: 3 * 152 + 56 = 4 * 128");
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 152;"); }
+
+constexpr int kOutRow = 48;  // bytes of a staged row of 16 output columns: an odd number of 16-byte units
+
+// Blocks per chain: one where the chains fill the GPU (the fewest reads of K and Q), else as many as fill it.
+// B8 T2048 H16 dk96 dv192 (128 chains, 152 SMs) runs one block of 12 column tiles to a chain; B1 (16 chains) six
+// blocks of two.
+template <int KT, class Rec>
+Walk make_walk(const Shape &p, bool with_q) {
+    Walk w{};
+    const int tiles = (p.dv + 15) / 16, sms = device_info().sm_count;
+    const long long chains = (long long)p.nseq * p.H;
+    int splits = (tiles + kMaxWarps - 1) / kMaxWarps;
+    if (chains * splits < sms) splits = (int)min((long long)tiles, sms / chains);
+    w.warps = (tiles + splits - 1) / splits;
+    w.splits = (tiles + w.warps - 1) / w.warps;
+    w.groups = (w.warps + 3) / 4;
+    w.vrow = (w.warps * 2 | 1) * 16;
+    w.stage_bytes = (with_q ? 2 : 1) * kC * row_bytes<KT>() + kC * w.vrow + (int)sizeof(Rec);
+    w.stages = 4;
+    return w;
+}
+inline int walk_bytes(const Walk &w) { return 128 + w.warps * kC * kOutRow + w.stages * w.stage_bytes; }
+
+// Who a block and a thread are, and the shared memory: barriers, the warps' output tiles, the stages (K | Q | V |
+// record).
+struct Frame {
+    int lane, warp, chain, s, h, hk, col0, width, nch;
+    SeqRange r;
+    bool bad;  // the sequence's offsets are invalid
+    int64_t slot0;
+    uint32_t full, empty, outs, ring;
+    volatile int *abort_flag;
+
+    __device__ __forceinline__ Frame(const Shape &p, const Walk &w, char *sm) {
+        lane = threadIdx.x & 31;
+        warp = threadIdx.x >> 5;
+        chain = (int)(blockIdx.x / (unsigned)w.splits);
+        s = chain / p.H;
+        h = chain % p.H;
+        hk = h / p.group();
+        col0 = (int)(blockIdx.x % (unsigned)w.splits) * w.warps * 16;  // first column of the block
+        width = min(w.warps * 16, p.dv - col0);                        // its columns, a multiple of 8
+        bad = !seq_range(s, p.T, p.cu, r);
+        nch = (int)((r.len + kC - 1) / kC);
+        slot0 = r.start / kC + s;
+        full = ptx::smem_u32(sm);
+        empty = full + 8 * w.stages;
+        abort_flag = reinterpret_cast<volatile int *>(sm + 16 * w.stages);
+        outs = full + 128;
+        ring = outs + w.warps * kC * kOutRow;
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < w.stages; ++i) {
+                ptx::mbar_init(full + 8 * i, 129);  // the fetching threads, and the record
+                ptx::mbar_init(empty + 8 * i, w.warps);
+            }
+            *abort_flag = 0;
+            ptx::fence_mbar_init();
+        }
+        __syncthreads();
+    }
+};
+
+// The fetching warpgroup: four threads to a token's row.  kBack walks the chunks from the last to the first.
+template <int KT, bool kQ, bool kBack, class Rec>
+__device__ __forceinline__ void fetch(const Shape &p, const Walk &w, const Frame &f, const bf16 *q, const bf16 *k,
+                                      const bf16 *v, const Rec *records) {
+    constexpr int kRow = row_bytes<KT>(), kTile = kC * kRow, kV = (kQ ? 2 : 1) * kTile;
+    const int id = threadIdx.x - w.groups * 128, t = id >> 2, u0 = id & 3;
+    const int vunits = w.warps * 2, vlive = f.width / 8, kunits = p.dk / 8;
+    const int64_t kstride = (int64_t)p.Hk * p.dk, vstride = (int64_t)p.H * p.dv;
+    const int64_t row0 = f.r.start + t + (kBack ? (int64_t)(f.nch - 1) * kC : 0);
+    const bf16 *kr = k + row0 * kstride + f.hk * p.dk + u0 * 8, *qr = q + row0 * kstride + f.hk * p.dk + u0 * 8,
+               *vr = v + row0 * vstride + (int64_t)f.h * p.dv + f.col0 + u0 * 8;
+    const uint32_t kdst = f.ring + t * kRow + u0 * 16, vdst = f.ring + kV + t * w.vrow + u0 * 16;
+    bool ok = true;
+    for (int i = 0; i < f.nch; ++i) {
+        const int c = kBack ? f.nch - 1 - i : i, sg = i % w.stages;
+        ok = i < w.stages || ptx::mbar_wait(f.empty + 8 * sg, (i / w.stages + 1) & 1, f.abort_flag, kWaitNs);
+        if (!ok) break;
+        const bool row = c * kC + t < f.r.len;  // a short chunk's missing rows are zero, and not read
+        const uint32_t at = sg * w.stage_bytes;
+        if (id == 0) {
+            ptx::mbar_expect_tx(f.full + 8 * sg, (uint32_t)sizeof(Rec));
+            ptx::bulk_load_g2s(f.ring + at + kV + kC * w.vrow, records + (f.slot0 + c) * p.H + f.h, sizeof(Rec),
+                               f.full + 8 * sg);
+        }
+#pragma unroll
+        for (int u = 0; u < KT * 2; u += 4) {
+            const bool has = row && u0 + u < kunits;
+            cp_async16(kdst + at + u * 16, has ? kr + u * 8 : k, has);
+            if (kQ) cp_async16(kdst + at + kTile + u * 16, has ? qr + u * 8 : q, has);
+        }
+#pragma unroll 2
+        for (int u = 0; u < vunits - u0; u += 4) {
+            const bool has = row && u0 + u < vlive;
+            cp_async16(vdst + at + u * 16, has ? vr + u * 8 : v, has);
+        }
+        cp_async_arrive(f.full + 8 * sg);
+        kr += (kBack ? -kC : kC) * kstride;
+        qr += (kBack ? -kC : kC) * kstride;
+        vr += (kBack ? -kC : kC) * vstride;
+    }
+    // nothing may be in flight into a block that ends early; a whole walk has waited for every stage
+    cp_async_wait_all();
+    if (!ok) {
+        *f.abort_flag = 1;
+        for (int i = 0; i < w.stages; ++i)  // the records' bulk copies, bounded like every wait
+            for (int par = 0; par < 2; ++par) ptx::mbar_wait(f.full + 8 * i, par, nullptr, kWaitNs / 1000);
+    }
+}
+
+// A warp's 16 columns of a state [dk][dv] in f32 as the accumulators of S^T (16 x dk).
+template <int KT>
+__device__ __forceinline__ void load_state(float (&S)[2 * KT][4], const float *from, const Shape &p, int chain, int col,
+                                           int lane) {
+    const int64_t at = (int64_t)chain * p.dk * p.dv + col + (lane >> 2);
+#pragma unroll
+    for (int n = 0; n < 2 * KT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int row = n * 8 + 2 * (lane & 3) + (e & 1);
+            const bool has = from != nullptr && row < p.dk && col + (e >> 1) * 8 < p.dv;
+            S[n][e] = has ? from[at + (int64_t)row * p.dv + (e >> 1) * 8] : 0.f;
+        }
+}
+template <int KT>
+__device__ __forceinline__ void store_state(float *to, const float (&S)[2 * KT][4], const Shape &p, int chain, int col,
+                                            int lane) {
+    const int64_t at = (int64_t)chain * p.dk * p.dv + col + (lane >> 2);
+#pragma unroll
+    for (int n = 0; n < 2 * KT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int row = n * 8 + 2 * (lane & 3) + (e & 1);
+            if (row < p.dk && col + (e >> 1) * 8 < p.dv) to[at + (int64_t)row * p.dv + (e >> 1) * 8] = S[n][e];
+        }
+}
+
+// O^T (16 columns x 32 tokens) through the warp's tile to rows of 32 bytes of `out` [rows, H, dv].
+__device__ __forceinline__ void write_tile(bf16 *out, const float (&O)[4][4], const Shape &p, const Frame &f, int c, int col,
+                                           uint32_t tile) {
+    const int lane = f.lane, m8 = lane >> 3, r8 = lane & 7;
+    const uint32_t to = tile + ((m8 >> 1) * 8 + r8) * kOutRow + (m8 & 1) * 16;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+        stsm4t(to + t * 16 * kOutRow, pack(O[2 * t][0], O[2 * t][1]), pack(O[2 * t][2], O[2 * t][3]),
+               pack(O[2 * t + 1][0], O[2 * t + 1][1]), pack(O[2 * t + 1][2], O[2 * t + 1][3]));
+    __syncwarp();
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int i = t * 16 + (lane >> 1), cc = col + (lane & 1) * 8;
+        const int64_t tok = (int64_t)c * kC + i;
+        const uint4 x = lds128(tile + i * kOutRow + (lane & 1) * 16);
+        if (tok < f.r.len && cc < p.dv) *reinterpret_cast<uint4 *>(out + ((f.r.start + tok) * p.H + f.h) * p.dv + cc) = x;
+    }
+    __syncwarp();
+}
+
+}  // namespace
+}  // namespace delta
+}  // namespace gla
+
+// the kernels' width of a state's rows, in units of 16
+#define GLA_BY_KT(dk, CALL)        \
+    do {                           \
+        if (dk <= 32) { CALL(2); } \
+        else if (dk <= 64) { CALL(4); } \
+        else if (dk <= 96) { CALL(6); } \
+        else { CALL(8); }          \
+    } while (0)
