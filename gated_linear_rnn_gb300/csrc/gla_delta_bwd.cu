@@ -12,8 +12,10 @@
 //   delta_grad_kernel  the rest is local to 64 tokens given S0, dS1, R, Y and dO (the residuals and Y belong to
 //                      their tokens, not to a chunk's length): dq, dk, dg and dbeta.
 // Both walks keep S^T (dS^T) in registers, 16 columns to a warp, as the forward does.  The gradients are rounded
-// to bf16 at the end, so their products take bf16 operands without the lo parts that the forward's state needs;
-// states and all sums are f32.
+// to bf16 at the end, so most of their products take operands rounded to bf16, without the lo parts that the
+// forward's state needs; states and all sums are f32.  One rounding to bf16 is 1.7e-3 of a vector's norm, and
+// they add in squares: X and dU, which every residual and every Y are made of, keep their lo parts (six products of
+// 16 x 8 x 16 a chunk each), which takes dbeta, a product of both, from 4.7e-3 to 4e-3.
 #include "gla_delta_mma.cuh"
 
 GLA_DEFINE_STATUS(delta_bwd)
@@ -113,7 +115,7 @@ delta_again_kernel(Shape p, Walk w, const bf16 *__restrict__ k, const bf16 *__re
         const uint32_t vec = rec + (uint32_t)offsetof(AgainRecord, c) + 8 * tg;
         float Y[4][4] = {};
         state_times_rows<KT>(Y, S, ks, lane);
-        uint32_t x[2][4];
+        uint32_t x[2][4], xl[2][4];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             uint32_t b[4];
@@ -122,8 +124,9 @@ delta_again_kernel(Shape p, Walk w, const bf16 *__restrict__ k, const bf16 *__re
             for (int u = 0; u < 2; ++u) {
                 const int n = 2 * t + u;
                 const float2 cc = lds_f2(vec + n * 32);
-                x[t][2 * u] = pack(fmaf(-cc.x, Y[n][0], lo_f(b[2 * u])), fmaf(-cc.y, Y[n][1], hi_f(b[2 * u])));
-                x[t][2 * u + 1] = pack(fmaf(-cc.x, Y[n][2], lo_f(b[2 * u + 1])), fmaf(-cc.y, Y[n][3], hi_f(b[2 * u + 1])));
+                split(fmaf(-cc.x, Y[n][0], lo_f(b[2 * u])), fmaf(-cc.y, Y[n][1], hi_f(b[2 * u])), x[t][2 * u], xl[t][2 * u]);
+                split(fmaf(-cc.x, Y[n][2], lo_f(b[2 * u + 1])), fmaf(-cc.y, Y[n][3], hi_f(b[2 * u + 1])),
+                      x[t][2 * u + 1], xl[t][2 * u + 1]);
             }
         }
         float R[4][4] = {};
@@ -132,8 +135,12 @@ delta_again_kernel(Shape p, Walk w, const bf16 *__restrict__ k, const bf16 *__re
         for (int n = 0; n < 4; ++n) m[n] = lds128(rec + n * 512 + lane * 16);
 #pragma unroll
         for (int n = 0; n < 4; ++n) mma(R[n], x[0], m[n].x, m[n].y);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) mma(R[n], xl[0], m[n].x, m[n].y);
         mma(R[2], x[1], m[2].z, m[2].w);
         mma(R[3], x[1], m[3].z, m[3].w);
+        mma(R[2], xl[1], m[2].z, m[2].w);
+        mma(R[3], xl[1], m[3].z, m[3].w);
         uint32_t u[2][4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -208,18 +215,22 @@ delta_back_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__res
         for (int n = 0; n < 4; ++n) mma(U[n], a[1], m[n].z, m[n].w);
         mma(U[0], a[0], m[0].x, m[0].y);
         mma(U[1], a[0], m[1].x, m[1].y);
-        uint32_t u[2][4];
+        uint32_t u[2][4], ul[2][4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            u[n >> 1][(n & 1) * 2] = pack(U[n][0], U[n][1]);
-            u[n >> 1][(n & 1) * 2 + 1] = pack(U[n][2], U[n][3]);
+            split(U[n][0], U[n][1], u[n >> 1][(n & 1) * 2], ul[n >> 1][(n & 1) * 2]);
+            split(U[n][2], U[n][3], u[n >> 1][(n & 1) * 2 + 1], ul[n >> 1][(n & 1) * 2 + 1]);
             m[n] = lds128(rec + 2048 + n * 512 + lane * 16);
         }
         float Y[4][4] = {};
 #pragma unroll
         for (int n = 0; n < 4; ++n) mma(Y[n], u[1], m[n].z, m[n].w);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) mma(Y[n], ul[1], m[n].z, m[n].w);
         mma(Y[0], u[0], m[0].x, m[0].y);
         mma(Y[1], u[0], m[1].x, m[1].y);
+        mma(Y[0], ul[0], m[0].x, m[0].y);
+        mma(Y[1], ul[0], m[1].x, m[1].y);
         // dS^T = c_31 dS^T + dO^T diag(c) Q - dV^T diag(c) K
         float D[4][4];
         uint32_t e[2][4];
