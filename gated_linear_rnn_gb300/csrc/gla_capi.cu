@@ -68,7 +68,7 @@ template <typename T>
 int simt_bwd(const Shape &, const T *, const T *, const T *, const void *, const void *, const T *, const float *,
              const float *, T *, T *, T *, void *, void *, float *, void *, cudaStream_t);
 bool mma_supported(int dk);
-bool mma_bwd_supported(int dk, int dv);
+bool mma_bwd_supported(int dk);
 size_t mma_bwd_workspace(const Shape &);
 int mma_bwd(const Shape &, const void *, const void *, const void *, const void *, const void *, const void *,
             const float *, const float *, void *, void *, void *, void *, void *, float *, void *, cudaStream_t);
@@ -225,7 +225,7 @@ delta::Shape delta_shape(int B, int T, int H, int Hk, int dk, int dv, int dtype,
 long long delta_workspace(int op, const delta::Shape &p, int dtype) {
     if (op == GLA_OP_FORWARD)
         return dtype == GLA_BF16 && delta::mma_supported(p.dk) ? (long long)delta::mma_fwd_workspace(p) : 0;
-    return (long long)(dtype == GLA_BF16 && delta::mma_bwd_supported(p.dk, p.dv) ? delta::mma_bwd_workspace(p)
+    return (long long)(dtype == GLA_BF16 && delta::mma_bwd_supported(p.dk) ? delta::mma_bwd_workspace(p)
                                                                                 : delta::simt_bwd_workspace(p));
 }
 
@@ -497,7 +497,7 @@ int gla_delta_chunk_bwd(const void *q, const void *k, const void *v, const void 
         return delta::simt_bwd<float>(p, (const float *)q, (const float *)k, (const float *)v, g, beta,
                                       (const float *)dout, h0, dhT, (float *)dq, (float *)dk_out, (float *)dv_out, dg,
                                       dbeta, dh0, ws, st);
-    if (delta::mma_bwd_supported(dk, dv))
+    if (delta::mma_bwd_supported(dk))
         return delta::mma_bwd(p, q, k, v, g, beta, dout, h0, dhT, dq, dk_out, dv_out, dg, dbeta, dh0, ws, st);
     return delta::simt_bwd<H16>(p, (const H16 *)q, (const H16 *)k, (const H16 *)v, g, beta, (const H16 *)dout, h0, dhT,
                                 (H16 *)dq, (H16 *)dk_out, (H16 *)dv_out, dg, dbeta, dh0, ws, st);

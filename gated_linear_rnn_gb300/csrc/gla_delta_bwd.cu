@@ -103,7 +103,7 @@ delta_again_kernel(Shape p, Walk w, const bf16 *__restrict__ k, const bf16 *__re
     load_state<KT>(S, h0, p, f.chain, col, lane);
     for (int c = 0; c < f.nch; ++c) {
         const int sg = c % w.stages;
-        if (!ptx::mbar_wait(f.full + 8 * sg, (c / w.stages) & 1, f.abort_flag, kWaitNs)) {
+        if (!warp_wait(f.full + 8 * sg, (c / w.stages) & 1, f.abort_flag)) {
             if (lane == 0) {
                 *f.abort_flag = 1;
                 record_status(GLA_ERR_TIMEOUT);
@@ -185,7 +185,7 @@ delta_back_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__res
     load_state<KT>(S, dhT, p, f.chain, col, lane);
     for (int i = 0; i < f.nch; ++i) {
         const int c = f.nch - 1 - i, sg = i % w.stages;
-        if (!ptx::mbar_wait(f.full + 8 * sg, (i / w.stages) & 1, f.abort_flag, kWaitNs)) {
+        if (!warp_wait(f.full + 8 * sg, (i / w.stages) & 1, f.abort_flag)) {
             if (lane == 0) {
                 *f.abort_flag = 1;
                 record_status(GLA_ERR_TIMEOUT);
@@ -261,8 +261,7 @@ delta_back_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__res
 
 // ---- dq, dk, dg, dbeta -----------------------------------------------------------------------------------------
 //
-// One block per 64 tokens and key head, eight warps: warps 0-3 own 16 tokens each of the query's side, warps 4-7
-// of the key's.  With D_ij, c_i and d_j over the 64 tokens,
+// A unit is 64 tokens of a value head.  With D_ij, c_i and d_j over the 64 tokens,
 //     R'_ij = beta_j D_ij (do_i . r_j), j <= i             N_ij = -beta_i beta_j D_ij (y_i . r_j), j < i
 //     dq = diag(c) dO S0^T + R' K
 //     dk = diag(d beta) R dS1^T - diag(c beta) Y S0^T + R'^T Q + N^T K + N K
@@ -275,58 +274,50 @@ delta_back_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__res
 // ends of a product carry the same rounding and cancel to f32.
 // D_ij comes from products of decays alone (a decay of zero is as good as any): within 16 tokens as a table, across
 // them as (from the tile's start to i)(whole tiles between)(from j to its tile's end).
-constexpr int kGradThreads = 256;
+//
+// One block per SM walks over units.  Twelve warps compute, in three roles of four (16 tokens each): dO's side (T = dO
+// R^T, dO S0^T, R' K -> dq), Y's (Y R^T, Y S0^T, N K) and R's (R dS1^T, R'^T Q + N^T K); the last two meet in
+// shared memory -> dk.  A fourth warpgroup fetches ahead: K, Q and the decay products of the next unit, and
+// slabs of 32 columns of dO, Y, R and of both states through a ring.  With one block per unit that loaded its whole
+// share first and read the states from L2 between products, the kernel took 489 us on the layer's gradient.
+constexpr int kGradWarps = 12;
+constexpr int kGradThreads = (kGradWarps + 4) * 32;
 constexpr int kMRow = kG * 2 + 16;  // bytes of a row of R' and N
+constexpr int kSlabRow = 80;        // bytes of a row of 32 columns: an odd number of 16-byte units
 
-struct GradPlan {
-    int vrow;                                 // bytes of a row of dO, Y, R
-    int off_q, off_do, off_y, off_r, off_m, off_n, off_f, total;
+struct Decays {                     // of one unit
+    float diag[4][256];             // D within a tile of 16 tokens
+    float pre[kG], suf[kG], c[kG], d[kG], beta[kG], whole[4], pad[4];
 };
-template <int KT>
-__host__ __device__ inline GradPlan grad_plan(int dv) {
-    GradPlan g{};
-    g.vrow = ((dv + 15) / 16 * 2 | 1) * 16;
-    g.off_q = kG * row_bytes<KT>();
-    g.off_do = 2 * g.off_q;
-    g.off_y = g.off_do + kG * g.vrow;
-    g.off_r = g.off_y + kG * g.vrow;
-    g.off_m = g.off_r + kG * g.vrow;
-    g.off_n = g.off_m + kG * kMRow;
-    g.off_f = g.off_n + kG * kMRow;
-    g.total = g.off_f + (4 * 256 + 11 * kG + 16) * 4;
-    return g;
+struct Sums {                       // per token
+    float wq[kG], wk[kG], x[kG], mq[kG], my[kG], mr[kG], inner[kGradWarps], pad[4];
+};
+template <int KT> struct GradPlan {
+    static constexpr int kTile = kG * row_bytes<KT>();
+    static constexpr int kHead = 2 * kTile + (int)sizeof(Decays);                  // K | Q | decays, two of them
+    static constexpr int kImage = 2 * KT * 512;                                    // two column tiles of a state
+    static constexpr int kSlab = 3 * kG * kSlabRow + 2 * kImage;                   // dO | Y | R | S0 | dS1
+    static constexpr int kStages = KT <= 6 ? 3 : 2;
+    static constexpr int kXRow = KT * 16 + 4;                                      // f32 row of the exchange tile
+    static constexpr int kOffHead = 128, kOffSlab = kOffHead + 2 * kHead, kOffM = kOffSlab + kStages * kSlab,
+                         kOffX = kOffM + 2 * kG * kMRow, kOffSums = kOffX + kG * kXRow * 4,
+                         kTotal = kOffSums + 2 * (int)sizeof(Sums);
+    static_assert(kTotal <= 227 * 1024, "shared memory of a block");
+    static_assert(kTile % 16 == 0 && kHead % 16 == 0 && kSlab % 16 == 0 && kOffX % 16 == 0, "16-byte copies");
+};
+
+__device__ __forceinline__ void compute_sync() { ptx::named_bar_sync(1, kGradWarps * 32); }
+// the same, and whether any of the threads brings a failure: all of them leave together or none
+__device__ __forceinline__ bool compute_sync_any(bool failed) {
+    uint32_t any;
+    asm volatile("{\n\t.reg .pred p, r;\n\t"
+                 "setp.ne.u32 p, %1, 0;\n\t"
+                 "barrier.cta.red.or.pred r, 1, %2, p;\n\t"
+                 "selp.u32 %0, 1, 0, r;\n\t}"
+                 : "=r"(any) : "r"((uint32_t)failed), "n"(kGradWarps * 32) : "memory");
+    return any != 0;
 }
 
-// rows of 64 tokens into shared memory, zero past len and past n; asynchronous
-__device__ __forceinline__ void fetch_tile(uint32_t dst, int row_bytes_, int units, const bf16 *src, int64_t stride, int len,
-                                           int n) {
-    for (int e = threadIdx.x; e < kG * 4; e += kGradThreads) {
-        const int t = e >> 2;
-        for (int u = e & 3; u < units; u += 4) {
-            const bool has = t < len && u * 8 < n;
-            cp_async16(dst + t * row_bytes_ + u * 16, has ? src + t * stride + u * 8 : src, has);
-        }
-    }
-}
-
-// acc (16 rows x KT * 16) += rows (16 x dv, from shared memory) times an image (dv x dk, from global memory)
-template <int KT>
-__device__ __forceinline__ void rows_times_image(float (&acc)[2 * KT][4], uint32_t rows, int vrow, const uint4 *image,
-                                                 int tiles, int lane) {
-    const uint32_t at = rows + (((lane >> 3) & 1) * 8 + (lane & 7)) * vrow + ((lane >> 3) >> 1) * 16;
-    for (int s = 0; s < tiles; ++s) {
-        uint32_t a[4];
-        uint4 b[KT];
-#pragma unroll
-        for (int i = 0; i < KT; ++i) b[i] = __ldg(image + (s * KT + i) * 32 + lane);
-        ldsm4(a, at + s * 32);
-#pragma unroll
-        for (int i = 0; i < KT; ++i) {
-            mma(acc[2 * i], a, b[i].x, b[i].y);
-            mma(acc[2 * i + 1], a, b[i].z, b[i].w);
-        }
-    }
-}
 // acc (16 rows x KT * 16) += A (16 x 16) times 16 rows of a tile
 template <int KT>
 __device__ __forceinline__ void add_rows(float (&acc)[2 * KT][4], const uint32_t (&a)[4], uint32_t rows, int lane) {
@@ -339,6 +330,11 @@ __device__ __forceinline__ void add_rows(float (&acc)[2 * KT][4], const uint32_t
         mma(acc[2 * i + 1], a, b[2], b[3]);
     }
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t x;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+    return x;
+}
 // sums over dk of acc's two rows of this lane with the rows of a tile: lo for row gr, hi for row gr + 8
 template <int KT>
 __device__ __forceinline__ void row_dots(const float (&acc)[2 * KT][4], uint32_t rows, int lane, float &lo, float &hi) {
@@ -346,9 +342,7 @@ __device__ __forceinline__ void row_dots(const float (&acc)[2 * KT][4], uint32_t
     lo = hi = 0.f;
 #pragma unroll
     for (int n = 0; n < 2 * KT; ++n) {
-        uint32_t x, y;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(at + n * 16) : "memory");
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(y) : "r"(at + 8 * row_bytes<KT>() + n * 16) : "memory");
+        const uint32_t x = lds32(at + n * 16), y = lds32(at + 8 * row_bytes<KT>() + n * 16);
         lo = fmaf(acc[n][0], lo_f(x), fmaf(acc[n][1], hi_f(x), lo));
         hi = fmaf(acc[n][2], lo_f(y), fmaf(acc[n][3], hi_f(y), hi));
     }
@@ -358,223 +352,379 @@ __device__ __forceinline__ void row_dots(const float (&acc)[2 * KT][4], uint32_t
     hi += __shfl_xor_sync(0xffffffffu, hi, 2);
 }
 
+struct GradArgs {
+    const bf16 *q, *k, *dout;
+    const void *g, *beta;
+    const bf16 *resid, *ys;
+    const uint4 *s_images, *ds_images;
+    bf16 *dq, *dk;          // written when each key head has one value head
+    float *dq_part, *dk_part;  // else [rows, H, dk] each, summed by delta_heads_kernel
+    void *dg, *dbeta;
+    unsigned units;         // slots * H
+};
+
+template <int KT>
+__device__ __forceinline__ void grad_fetch(const Shape &p, const GradArgs &a, char *sm) {
+    using P = GradPlan<KT>;
+    const uint32_t base = ptx::smem_u32(sm);
+    const uint32_t hfull = base, hempty = base + 16, full = base + 32, empty = full + 8 * P::kStages;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + 120);
+    const int id = threadIdx.x - kGradWarps * 32;
+    const int tiles = (p.dv + 15) / 16, slabs = (tiles + 1) / 2;
+    int n = 0, ns = 0;  // units and slabs so far
+    bool ok = true;
+    for (unsigned unit = blockIdx.x; ok && unit < a.units; unit += gridDim.x) {
+        const int slot = (int)(unit / (unsigned)p.H), h = (int)(unit % (unsigned)p.H), hk = h / p.group();
+        ChunkAt at;
+        if (!chunk_of_slot<kG>(slot, p, at)) continue;
+        const int hb = n & 1;
+        if (n >= 2 && !(ok = warp_wait(hempty + 8 * hb, (n / 2 + 1) & 1, abort_flag))) break;
+        ++n;
+        char *head = sm + P::kOffHead + hb * P::kHead;
+        const uint32_t ka = base + P::kOffHead + hb * P::kHead;
+        {
+            const int t = id >> 1;  // two threads to a row
+            const bf16 *kr = a.k + ((at.row + t) * p.Hk + hk) * p.dk, *qr = a.q + ((at.row + t) * p.Hk + hk) * p.dk;
+            for (int u = id & 1; u < KT * 2; u += 2) {
+                const bool has = t < at.len && u * 8 < p.dk;
+                cp_async16(ka + t * row_bytes<KT>() + u * 16, has ? kr + u * 8 : a.k, has);
+                cp_async16(ka + P::kTile + t * row_bytes<KT>() + u * 16, has ? qr + u * 8 : a.q, has);
+            }
+            cp_async_arrive(hfull + 8 * hb);
+        }
+        // the decays: thread j < 64 is column j of its tile of 16; both warps take all 64 tokens' decays
+        Decays &dc = *reinterpret_cast<Decays *>(head + 2 * P::kTile);
+        if (id < kG) {
+            const int lane = id & 31, b = id >> 4, j = id & 15;
+            float al[2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int tok = m * 32 + lane;
+                al[m] = tok < at.len ? expf(load_gate<bf16>(a.g, (at.row + tok) * p.H + h, p.gate_f32)) : 1.f;
+            }
+            dc.beta[id] = id < at.len ? load_gate<bf16>(a.beta, (at.row + id) * p.H + h, p.gate_f32) : 0.f;
+            const float mine = id < 32 ? al[0] : al[1];
+            float f = 0.f, run = 1.f, pre = 1.f, whole0 = 1.f, whole1 = 1.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float y = __shfl_sync(0xffffffffu, mine, i, 16);
+                run *= y;
+                if (i == j) pre = run;
+                f = i == j ? 1.f : f * y;
+                dc.diag[b][i * 16 + j] = f;
+                whole0 *= __shfl_sync(0xffffffffu, al[0], i, 16);
+                whole1 *= __shfl_sync(0xffffffffu, al[1], i, 16);
+            }
+            float before = 1.f, after = 1.f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const float x = __shfl_sync(0xffffffffu, t < 2 ? whole0 : whole1, (t & 1) * 16);
+                if (t < b) before *= x;
+                if (t > b) after *= x;
+                if (id == 0) dc.whole[t] = x;
+            }
+            dc.pre[id] = pre;
+            dc.suf[id] = f;
+            dc.c[id] = before * pre;
+            dc.d[id] = f * after;
+        }
+        ptx::mbar_arrive(hfull + 8 * hb);
+        const int64_t vst = (int64_t)p.H * p.dv;
+        const int t = id >> 1, u0 = (id & 1) * 2;  // two threads to a slab's row, two units each
+        const int64_t vat = (at.row + t) * vst + (int64_t)h * p.dv + u0 * 8;
+        const uint4 *s0 = a.s_images + image_at<KT>(p, slot, h, 0), *s1 = a.ds_images + image_at<KT>(p, slot, h, 0);
+        for (int s = 0; s < slabs; ++s, ++ns) {
+            const int sg = ns % P::kStages;
+            if (ns >= P::kStages && !(ok = warp_wait(empty + 8 * sg, (ns / P::kStages + 1) & 1, abort_flag))) break;
+            const uint32_t to = base + P::kOffSlab + sg * P::kSlab;
+            const int here = min(2, tiles - 2 * s) * KT * 512;
+            if (id == 0) {
+                ptx::mbar_expect_tx(full + 8 * sg, 2 * here);
+                ptx::bulk_load_g2s(to + 3 * kG * kSlabRow, s0 + s * 2 * KT * 32, here, full + 8 * sg);
+                ptx::bulk_load_g2s(to + 3 * kG * kSlabRow + P::kImage, s1 + s * 2 * KT * 32, here, full + 8 * sg);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const bool has = t < at.len && s * 32 + (u0 + u) * 8 < p.dv;
+                const int64_t off = has ? vat + s * 32 + u * 8 : 0;
+                const uint32_t dst = to + t * kSlabRow + (u0 + u) * 16;
+                cp_async16(dst, a.dout + off, has);
+                cp_async16(dst + kG * kSlabRow, a.ys + off, has);
+                cp_async16(dst + 2 * kG * kSlabRow, a.resid + off, has);
+            }
+            cp_async_arrive(full + 8 * sg);
+        }
+    }
+    // nothing may be in flight into a block that ends early; a whole walk over units has waited for every stage
+    cp_async_wait_all();
+    if (!ok) {
+        *abort_flag = 1;
+        for (int i = 0; i < P::kStages; ++i)
+            for (int par = 0; par < 2; ++par) ptx::mbar_wait(full + 8 * i, par, nullptr, kWaitNs / 1000);
+    }
+}
+
 template <int KT>
 __global__ void __launch_bounds__(kGradThreads)
-delta_grad_kernel(Shape p, const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16 *__restrict__ dout,
-                  const void *__restrict__ g, const void *__restrict__ beta, const bf16 *__restrict__ resid,
-                  const bf16 *__restrict__ ys, const uint4 *__restrict__ s_images, const uint4 *__restrict__ ds_images,
-                  bf16 *__restrict__ dq, bf16 *__restrict__ dk, void *__restrict__ dg, void *__restrict__ dbeta) {
+delta_grad_kernel(Shape p, GradArgs a) {
+    using P = GradPlan<KT>;
     extern __shared__ __align__(128) char sm_raw[];
-    const GradPlan pl = grad_plan<KT>(p.dv);
-    const int slot = (int)(blockIdx.x / (unsigned)p.Hk), hk = (int)(blockIdx.x % (unsigned)p.Hk);
-    ChunkAt at;
-    if (!chunk_of_slot<kG>(slot, p, at)) return;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rt = warp & 3, gr = lane >> 2, tg = lane & 3;
-    const bool key = warp >= 4;
-    const int m8 = lane >> 3, r8 = lane & 7;
-    const uint32_t base = ptx::smem_u32(sm_raw), ks = base, qs = base + pl.off_q, dos = base + pl.off_do,
-                   yss = base + pl.off_y, rss = base + pl.off_r;
-    char *Mt = sm_raw + pl.off_m, *Nt = sm_raw + pl.off_n;
-    float *diag = reinterpret_cast<float *>(sm_raw + pl.off_f);  // [4][16][16]: D within a tile of 16 tokens
-    float *pre = diag + 4 * 256, *suf = pre + kG, *cc = suf + kG, *dd = cc + kG, *be = dd + kG, *al = be + kG,
-          *wq = al + kG, *wk = wq + kG, *xs = wk + kG, *mq = xs + kG, *mk = mq + kG, *part = mk + kG, *whole = part + 8;
+    const uint32_t base = ptx::smem_u32(sm_raw);
+    const uint32_t hfull = base, hempty = base + 16, full = base + 32, empty = full + 8 * P::kStages;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm_raw + 120);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(hfull + 8 * i, 256);  // the fetching threads' copies, and their decays
+            ptx::mbar_init(hempty + 8 * i, kGradWarps);
+        }
+        for (int i = 0; i < P::kStages; ++i) {
+            ptx::mbar_init(full + 8 * i, 129);
+            ptx::mbar_init(empty + 8 * i, kGradWarps);
+        }
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    if (warp >= kGradWarps) {
+        give_registers();
+        grad_fetch<KT>(p, a, sm_raw);
+        return;
+    }
+    take_registers();
+    const int role = warp >> 2, rt = warp & 3, gr = lane >> 2, tg = lane & 3, m8 = lane >> 3, r8 = lane & 7;
     const int row0 = rt * 16 + gr;  // this lane's rows: row0 and row0 + 8
-    const int tiles = (p.dv + 15) / 16;
-    fetch_tile(ks, row_bytes<KT>(), KT * 2, k + (at.row * p.Hk + hk) * p.dk, (int64_t)p.Hk * p.dk, at.len, p.dk);
-    fetch_tile(qs, row_bytes<KT>(), KT * 2, q + (at.row * p.Hk + hk) * p.dk, (int64_t)p.Hk * p.dk, at.len, p.dk);
-    float total[2 * KT][4] = {};  // dq's or dk's rows, over the value heads of this key head
-    for (int h = hk * p.group(); h < (hk + 1) * p.group(); ++h) {
-        const int64_t vat = (at.row * p.H + h) * p.dv, vst = (int64_t)p.H * p.dv;
-        fetch_tile(dos, pl.vrow, tiles * 2, dout + vat, vst, at.len, p.dv);
-        fetch_tile(yss, pl.vrow, tiles * 2, ys + vat, vst, at.len, p.dv);
-        fetch_tile(rss, pl.vrow, tiles * 2, resid + vat, vst, at.len, p.dv);
-        const uint4 *s0 = s_images + image_at<KT>(p, slot, h, 0), *ds1 = ds_images + image_at<KT>(p, slot, h, 0);
-        if (tid < kG) {
-            al[tid] = tid < at.len ? expf(load_gate<bf16>(g, (at.row + tid) * p.H + h, p.gate_f32)) : 1.f;
-            be[tid] = tid < at.len ? load_gate<bf16>(beta, (at.row + tid) * p.H + h, p.gate_f32) : 0.f;
-        }
-        __syncthreads();
-        if (tid < kG) {  // column tid of its tile's D, and the products from the tile's start and to its end
-            const int b = tid >> 4, j = tid & 15;
-            float f = 0.f, run = 1.f;
-            for (int i = 0; i < 16; ++i) {
-                const float a = al[b * 16 + i];
-                run *= a;
-                if (i == j) pre[tid] = run;
-                f = i == j ? 1.f : f * a;
-                diag[b * 256 + i * 16 + j] = f;
-            }
-            suf[tid] = f;
-            if (j == 0) whole[b] = run;
-        }
-        float inner = 0.f;  // <S0, dS1>
-        for (int i = tid; i < tiles * KT * 32; i += kGradThreads) {
-            const uint4 x = __ldg(s0 + i), y = __ldg(ds1 + i);
-            const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+    const int tiles = (p.dv + 15) / 16, slabs = (tiles + 1) / 2;
+    const uint32_t mt = base + P::kOffM, nt = mt + kG * kMRow;
+    float *exchange = reinterpret_cast<float *>(sm_raw + P::kOffX);
+    int n = 0, ns = 0;
+    for (unsigned unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
+        const int slot = (int)(unit / (unsigned)p.H), h = (int)(unit % (unsigned)p.H);
+        ChunkAt at;
+        if (!chunk_of_slot<kG>(slot, p, at)) continue;
+        const int hb = n & 1;
+        // a warp whose wait runs out goes on to the next barrier, where all learn of it and leave together
+        bool ok = warp_wait(hfull + 8 * hb, (n / 2) & 1, abort_flag);
+        Sums &sums = *reinterpret_cast<Sums *>(sm_raw + P::kOffSums + hb * sizeof(Sums));
+        ++n;
+        const uint32_t ks = base + P::kOffHead + hb * P::kHead, qs = ks + P::kTile;
+        const Decays &dc = *reinterpret_cast<const Decays *>(sm_raw + P::kOffHead + hb * P::kHead + 2 * P::kTile);
+        // T = do_i . r_j (or y_i . r_j) on and below the diagonal; A: this role's product with a state
+        float T[8][4] = {}, A[2 * KT][4] = {}, inner = 0.f;
+        for (int s = 0; s < slabs; ++s, ++ns) {
+            const int sg = ns % P::kStages;
+            ok = ok && warp_wait(full + 8 * sg, (ns / P::kStages) & 1, abort_flag);
+            if (!ok) break;
+            const uint32_t slab = base + P::kOffSlab + sg * P::kSlab;
+            const uint32_t a_at = slab + (role * kG + rt * 16 + (m8 & 1) * 8 + r8) * kSlabRow + (m8 >> 1) * 16;
+            const uint32_t b_at = slab + (2 * kG + (m8 >> 1) * 8 + r8) * kSlabRow + (m8 & 1) * 16;
+            const uint32_t image = slab + 3 * kG * kSlabRow + (role == 2 ? P::kImage : 0) + lane * 16;
+            const int here = min(2, tiles - 2 * s);
+            for (int x = 0; x < here; ++x) {
+                uint32_t f[4];
+                ldsm4(f, a_at + x * 32);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) inner = fmaf(lo_f(xw[e]), lo_f(yw[e]), fmaf(hi_f(xw[e]), hi_f(yw[e]), inner));
+                for (int i = 0; i < KT; ++i) {
+                    const uint4 b = lds128(image + (x * KT + i) * 512);
+                    mma(A[2 * i], f, b.x, b.y);
+                    mma(A[2 * i + 1], f, b.z, b.w);
+                }
+                if (role < 2) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        if (t <= rt) {
+                            uint32_t b[4];
+                            ldsm4(b, b_at + t * 16 * kSlabRow + x * 32);
+                            mma(T[2 * t], f, b[0], b[1]);
+                            mma(T[2 * t + 1], f, b[2], b[3]);
+                        }
+                }
+            }
+            for (int i = tid; i < here * KT * 32; i += kGradWarps * 32) {  // <S0, dS1>
+                const uint4 x = lds128(slab + 3 * kG * kSlabRow + i * 16),
+                            y = lds128(slab + 3 * kG * kSlabRow + P::kImage + i * 16);
+                const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) inner = fmaf(lo_f(xw[e]), lo_f(yw[e]), fmaf(hi_f(xw[e]), hi_f(yw[e]), inner));
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(empty + 8 * sg);
+        }
+        if (!ok && lane == 0) {
+            *abort_flag = 1;
+            record_status(GLA_ERR_TIMEOUT);
         }
         for (int m = 16; m > 0; m >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, m);
-        if (lane == 0) part[warp] = inner;
-        cp_async_wait_all();
-        __syncthreads();
-        if (tid < kG) {
-            const int b = tid >> 4;
-            float before = 1.f, after = 1.f;
+        if (lane == 0) sums.inner[warp] = inner;
+        float lo, hi;
+        // the state's part of dq and dk, and its share of dg
+        {
+            const float *v = role == 2 ? dc.d : dc.c;
+            float f0 = v[row0], f1 = v[row0 + 8];
+            if (role > 0) {
+                f0 *= role == 1 ? -dc.beta[row0] : dc.beta[row0];
+                f1 *= role == 1 ? -dc.beta[row0 + 8] : dc.beta[row0 + 8];
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * KT; ++i) {
+                A[i][0] *= f0; A[i][1] *= f0; A[i][2] *= f1; A[i][3] *= f1;
+            }
+            row_dots<KT>(A, (role ? ks : qs) + rt * 16 * row_bytes<KT>(), lane, lo, hi);
+            float *to = role == 0 ? sums.wq : role == 1 ? sums.wk : sums.x;
+            if (tg == 0) {
+                to[row0] = lo;
+                to[row0 + 8] = hi;
+            }
+        }
+        if (role < 2) {  // R' or N
+            float between[4];  // whole tiles strictly between tile t and this warp's
+#pragma unroll
             for (int t = 0; t < 4; ++t) {
-                if (t < b) before *= whole[t];
-                if (t > b) after *= whole[t];
+                float f = 1.f;
+                for (int m = t + 1; m < rt; ++m) f *= dc.whole[m];
+                between[t] = f;
             }
-            cc[tid] = before * pre[tid];
-            dd[tid] = suf[tid] * after;
-        }
-        // do_i . r_j (or y_i . r_j) on and below the diagonal
-        float T[8][4] = {};
-        {
-            const uint32_t a_at = (key ? yss : dos) + (rt * 16 + (m8 & 1) * 8 + r8) * pl.vrow + (m8 >> 1) * 16;
-            const uint32_t b_at = rss + ((m8 >> 1) * 8 + r8) * pl.vrow + (m8 & 1) * 16;
-            for (int s = 0; s < tiles; ++s) {
-                uint32_t a[4];
-                ldsm4(a, a_at + s * 32);
+            const float p0 = dc.pre[row0], p1 = dc.pre[row0 + 8];
+            const float g0 = role ? -dc.beta[row0] : 1.f, g1 = role ? -dc.beta[row0 + 8] : 1.f;
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    if (t <= rt) {
-                        uint32_t b[4];
-                        ldsm4(b, b_at + t * 16 * pl.vrow + s * 32);
-                        mma(T[2 * t], a, b[0], b[1]);
-                        mma(T[2 * t + 1], a, b[2], b[3]);
-                    }
-            }
-        }
-        __syncthreads();  // cc and dd; part, diag and whole have been read by those who write them next
-        float between[4];  // whole tiles strictly between tile t and this warp's
+            for (int t = 0; t < 8; ++t)
+                if (t <= 2 * rt + 1) {
+                    const int j = t * 8 + 2 * tg;
+                    const float b0 = dc.beta[j], b1 = dc.beta[j + 1];
+                    float x[4];
+                    if ((t >> 1) == rt) {
+                        const float *D = dc.diag[rt] + gr * 16 + (j & 15);
+                        const float2 u = *reinterpret_cast<const float2 *>(D), v = *reinterpret_cast<const float2 *>(D + 128);
+                        const int i0 = row0, i1 = row0 + 8, off = role;  // N leaves the diagonal out
+                        if (role) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            float f = 1.f;
-            for (int m = t + 1; m < rt; ++m) f *= whole[m];
-            between[t] = f;
-        }
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-            if (t <= 2 * rt + 1) {
-                float x[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = row0 + (e >> 1) * 8, j = t * 8 + 2 * tg + (e & 1);
-                    const float D = (t >> 1) == rt ? diag[rt * 256 + (i & 15) * 16 + (j & 15)]
-                                                   : pre[i] * between[t >> 1] * suf[j];
-                    if (key) {
-                        if (i == j && i < at.len) store_gate<bf16>(dbeta, (at.row + i) * p.H + h, p.gate_f32, T[t][e]);
-                        x[e] = j < i ? -(be[i] * be[j]) * D * T[t][e] : 0.f;
+                            for (int e = 0; e < 4; ++e) {
+                                const int i = e < 2 ? i0 : i1;
+                                if (i == j + (e & 1) && i < at.len)
+                                    store_gate<bf16>(a.dbeta, (at.row + i) * p.H + h, p.gate_f32, T[t][e]);
+                            }
+                        }
+                        x[0] = j + off <= i0 ? g0 * b0 * u.x * T[t][0] : 0.f;
+                        x[1] = j + 1 + off <= i0 ? g0 * b1 * u.y * T[t][1] : 0.f;
+                        x[2] = j + off <= i1 ? g1 * b0 * v.x * T[t][2] : 0.f;
+                        x[3] = j + 1 + off <= i1 ? g1 * b1 * v.y * T[t][3] : 0.f;
                     } else {
-                        x[e] = j <= i ? be[j] * D * T[t][e] : 0.f;
+                        const float m = between[t >> 1], s0 = m * dc.suf[j] * b0, s1 = m * dc.suf[j + 1] * b1;
+                        x[0] = g0 * p0 * s0 * T[t][0];
+                        x[1] = g0 * p0 * s1 * T[t][1];
+                        x[2] = g1 * p1 * s0 * T[t][2];
+                        x[3] = g1 * p1 * s1 * T[t][3];
+                    }
+                    char *to = sm_raw + P::kOffM + (role * kG + row0) * kMRow + j * 2;
+                    *reinterpret_cast<uint32_t *>(to) = pack(x[0], x[1]);
+                    *reinterpret_cast<uint32_t *>(to + 8 * kMRow) = pack(x[2], x[3]);
+                }
+        }
+        if (compute_sync_any(!ok)) return;  // R' and N are whole
+        {
+            float acc[2 * KT][4] = {};
+            if (role < 2) {  // R' K or N K
+                const uint32_t own = (role ? nt : mt) + (rt * 16 + (m8 & 1) * 8 + r8) * kMRow + (m8 >> 1) * 16;
+                for (int t = 0; t <= rt; ++t) {
+                    uint32_t f[4];
+                    ldsm4(f, own + t * 32);
+                    add_rows<KT>(acc, f, ks + t * 16 * row_bytes<KT>(), lane);
+                }
+            } else {  // R'^T Q + N^T K
+                const uint32_t flip = ((m8 >> 1) * 8 + r8) * kMRow + rt * 32 + (m8 & 1) * 16;
+                for (int t = rt; t < 4; ++t) {
+                    uint32_t f[4];
+                    ldsm4t(f, mt + flip + t * 16 * kMRow);
+                    add_rows<KT>(acc, f, qs + t * 16 * row_bytes<KT>(), lane);
+                    ldsm4t(f, nt + flip + t * 16 * kMRow);
+                    add_rows<KT>(acc, f, ks + t * 16 * row_bytes<KT>(), lane);
+                }
+            }
+            row_dots<KT>(acc, (role ? ks : qs) + rt * 16 * row_bytes<KT>(), lane, lo, hi);
+            float *to = role == 0 ? sums.mq : role == 1 ? sums.my : sums.mr;
+            if (tg == 0) {
+                to[row0] = role == 2 ? lo : -lo;
+                to[row0 + 8] = role == 2 ? hi : -hi;
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * KT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) A[i][e] += acc[i][e];
+        }
+        if (role == 2) {
+#pragma unroll
+            for (int i = 0; i < 2 * KT; ++i) {
+                *reinterpret_cast<float2 *>(exchange + row0 * P::kXRow + i * 8 + 2 * tg) = make_float2(A[i][0], A[i][1]);
+                *reinterpret_cast<float2 *>(exchange + (row0 + 8) * P::kXRow + i * 8 + 2 * tg) = make_float2(A[i][2], A[i][3]);
+            }
+        }
+        compute_sync();  // R's part of dk and all sums are there; K, Q and the decays are read
+        if (role == 1) {
+#pragma unroll
+            for (int i = 0; i < 2 * KT; ++i) {
+                const float2 u = *reinterpret_cast<const float2 *>(exchange + row0 * P::kXRow + i * 8 + 2 * tg);
+                const float2 v = *reinterpret_cast<const float2 *>(exchange + (row0 + 8) * P::kXRow + i * 8 + 2 * tg);
+                A[i][0] += u.x; A[i][1] += u.y; A[i][2] += v.x; A[i][3] += v.y;
+            }
+        }
+        if (role < 2) {
+            const bool single = a.dq_part == nullptr;
+            const int64_t at0 = ((at.row + row0) * p.H + h) * p.dk + 2 * tg, far = (int64_t)8 * p.H * p.dk;
+#pragma unroll
+            for (int i = 0; i < 2 * KT; ++i)
+                if (i * 8 < p.dk) {
+                    if (single) {
+                        bf16 *to = (role ? a.dk : a.dq) + at0 + i * 8;
+                        if (row0 < at.len) *reinterpret_cast<uint32_t *>(to) = pack(A[i][0], A[i][1]);
+                        if (row0 + 8 < at.len) *reinterpret_cast<uint32_t *>(to + far) = pack(A[i][2], A[i][3]);
+                    } else {
+                        float *to = (role ? a.dk_part : a.dq_part) + at0 + i * 8;
+                        if (row0 < at.len) *reinterpret_cast<float2 *>(to) = make_float2(A[i][0], A[i][1]);
+                        if (row0 + 8 < at.len) *reinterpret_cast<float2 *>(to + far) = make_float2(A[i][2], A[i][3]);
                     }
                 }
-                char *to = (key ? Nt : Mt) + row0 * kMRow + (t * 8 + 2 * tg) * 2;
-                *reinterpret_cast<uint32_t *>(to) = pack(x[0], x[1]);
-                *reinterpret_cast<uint32_t *>(to + 8 * kMRow) = pack(x[2], x[3]);
-            }
-        // products with the states
-        {
-            float acc[2 * KT][4] = {};
-            rows_times_image<KT>(acc, (key ? yss : dos) + rt * 16 * pl.vrow, pl.vrow, s0, tiles, lane);
-            const float f0 = key ? -cc[row0] * be[row0] : cc[row0], f1 = key ? -cc[row0 + 8] * be[row0 + 8] : cc[row0 + 8];
-#pragma unroll
-            for (int n = 0; n < 2 * KT; ++n) {
-                acc[n][0] *= f0; acc[n][1] *= f0; acc[n][2] *= f1; acc[n][3] *= f1;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) total[n][e] += acc[n][e];
-            }
-            float lo, hi;
-            row_dots<KT>(acc, (key ? ks : qs) + rt * 16 * row_bytes<KT>(), lane, lo, hi);
-            if (tg == 0) {
-                (key ? wk : wq)[row0] = lo;
-                (key ? wk : wq)[row0 + 8] = hi;
-            }
         }
-        if (key) {
-            float acc[2 * KT][4] = {};
-            rows_times_image<KT>(acc, rss + rt * 16 * pl.vrow, pl.vrow, ds1, tiles, lane);
-            const float f0 = dd[row0] * be[row0], f1 = dd[row0 + 8] * be[row0 + 8];
-#pragma unroll
-            for (int n = 0; n < 2 * KT; ++n) {
-                acc[n][0] *= f0; acc[n][1] *= f0; acc[n][2] *= f1; acc[n][3] *= f1;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) total[n][e] += acc[n][e];
-            }
-            float lo, hi;
-            row_dots<KT>(acc, ks + rt * 16 * row_bytes<KT>(), lane, lo, hi);
-            if (tg == 0) {
-                xs[row0] = lo;
-                xs[row0 + 8] = hi;
-            }
-        }
-        __syncthreads();  // R' and N are whole
-        // products inside the chunk
-        {
-            const uint32_t mt = base + pl.off_m, nt = base + pl.off_n;
-            const uint32_t own = (rt * 16 + (m8 & 1) * 8 + r8) * kMRow + (m8 >> 1) * 16;   // A = rows of this warp
-            const uint32_t flip = ((m8 >> 1) * 8 + r8) * kMRow + rt * 32 + (m8 & 1) * 16;  // A = columns of this warp
-            float acc[2 * KT][4] = {};
-            float lo, hi;
-            for (int t = 0; t <= rt; ++t) {  // R' K (query) or N K (key)
-                uint32_t a[4];
-                ldsm4(a, (key ? nt : mt) + own + t * 32);
-                add_rows<KT>(acc, a, ks + t * 16 * row_bytes<KT>(), lane);
-            }
-            row_dots<KT>(acc, (key ? ks : qs) + rt * 16 * row_bytes<KT>(), lane, lo, hi);
-#pragma unroll
-            for (int n = 0; n < 2 * KT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) total[n][e] += acc[n][e];
-            float sum0 = -lo, sum1 = -hi;
-            if (key) {
-#pragma unroll
-                for (int n = 0; n < 2 * KT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-                for (int t = rt; t < 4; ++t) {  // R'^T Q + N^T K
-                    uint32_t a[4];
-                    ldsm4t(a, mt + flip + t * 16 * kMRow);
-                    add_rows<KT>(acc, a, qs + t * 16 * row_bytes<KT>(), lane);
-                    ldsm4t(a, nt + flip + t * 16 * kMRow);
-                    add_rows<KT>(acc, a, ks + t * 16 * row_bytes<KT>(), lane);
-                }
-                row_dots<KT>(acc, ks + rt * 16 * row_bytes<KT>(), lane, lo, hi);
-                sum0 += lo;
-                sum1 += hi;
-#pragma unroll
-                for (int n = 0; n < 2 * KT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) total[n][e] += acc[n][e];
-            }
-            if (tg == 0) {
-                (key ? mk : mq)[row0] = sum0;
-                (key ? mk : mq)[row0 + 8] = sum1;
-            }
-        }
-        __syncthreads();
-        if (tid < at.len) {
+        if (warp == 8) {  // dg: lane owns tokens 2 lane and 2 lane + 1
             float f = 0.f;
-            for (int m = 0; m < 8; ++m) f += part[m];
-            f *= cc[kG - 1];
-            for (int m = 0; m < kG; ++m) f += m < tid ? xs[m] + (mq[m] + mk[m]) : wq[m] + wk[m];
-            store_gate<bf16>(dg, (at.row + tid) * p.H + h, p.gate_f32, f);
-        }
-        __syncthreads();  // the next head's tiles and sums may come
-    }
-    bf16 *to = (key ? dk : dq) + ((at.row + row0) * p.Hk + hk) * p.dk + 2 * tg;
 #pragma unroll
-    for (int n = 0; n < 2 * KT; ++n)
-        if (n * 8 < p.dk) {
-            if (row0 < at.len) *reinterpret_cast<uint32_t *>(to + n * 8) = pack(total[n][0], total[n][1]);
-            if (row0 + 8 < at.len)
-                *reinterpret_cast<uint32_t *>(to + (int64_t)8 * p.Hk * p.dk + n * 8) = pack(total[n][2], total[n][3]);
+            for (int m = 0; m < kGradWarps; ++m) f += sums.inner[m];
+            f *= dc.c[kG - 1];
+            const int i = 2 * lane;
+            const float w0 = sums.wq[i] + sums.wk[i], w1 = sums.wq[i + 1] + sums.wk[i + 1];
+            const float x0 = sums.x[i] + (sums.mq[i] + sums.my[i] + sums.mr[i]),
+                        x1 = sums.x[i + 1] + (sums.mq[i + 1] + sums.my[i + 1] + sums.mr[i + 1]);
+            float pre = x0 + x1, suf = w0 + w1;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const float u = __shfl_up_sync(0xffffffffu, pre, m), v = __shfl_down_sync(0xffffffffu, suf, m);
+                if (lane >= m) pre += u;
+                if (lane + m < 32) suf += v;
+            }
+            const float left = pre - (x0 + x1);  // tokens before 2 lane
+            if (i < at.len) store_gate<bf16>(a.dg, (at.row + i) * p.H + h, p.gate_f32, f + left + suf);
+            if (i + 1 < at.len) store_gate<bf16>(a.dg, (at.row + i + 1) * p.H + h, p.gate_f32, f + left + x0 + (suf - w0));
         }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(hempty + 8 * hb);
+    }
+}
+
+// dq and dk of a key head: the sum over its value heads' parts, four elements a thread, in a fixed order.
+__global__ void __launch_bounds__(256)
+delta_heads_kernel(const float *__restrict__ part, bf16 *__restrict__ out, int64_t n, int dk, int group) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;  // element of [rows, Hk, dk]
+    if (i >= n) return;
+    const float *from = part + (i / dk) * group * dk + i % dk;
+    float4 s = *reinterpret_cast<const float4 *>(from);
+    for (int m = 1; m < group; ++m) {
+        const float4 x = *reinterpret_cast<const float4 *>(from + (int64_t)m * dk);
+        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    }
+    *reinterpret_cast<uint2 *>(out + i) = make_uint2(pack(s.x, s.y), pack(s.z, s.w));
 }
 
 struct Workspace {
-    size_t again, back, s_images, ds_images, resid, ys, total;
+    size_t again, back, s_images, ds_images, resid, ys, dq_part, dk_part, total;
 };
 template <int KT> Workspace workspace_kt(const Shape &p) {
     const long long rows = total_rows(p);
@@ -590,6 +740,9 @@ template <int KT> Workspace workspace_kt(const Shape &p) {
     w.ds_images = take(image);
     w.resid = take(vecs);
     w.ys = take(vecs);
+    const size_t parts = p.H == p.Hk ? 0 : (size_t)rows * p.H * p.dk * sizeof(float);
+    w.dq_part = take(parts);
+    w.dk_part = take(parts);
     w.total = at;
     return w;
 }
@@ -601,9 +754,9 @@ int bwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
     const Workspace at = workspace_kt<KT>(p);
     const long long rows = total_rows(p), slots = chunk_slots(rows, p.nseq, kG);
     const Walk wa = make_walk<KT, AgainRecord>(p, false), wb = make_walk<KT, BwdRecord>(p, true);
-    const int grad_bytes = grad_plan<KT>(p.dv).total;
+    const int grad_bytes = GradPlan<KT>::kTotal;
     const long long blocks = (long long)p.nseq * p.H * wa.splits;
-    if (blocks > 0x7fffffffLL || slots * p.Hk > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
+    if (blocks > 0x7fffffffLL || slots * p.H > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
     if (cudaFuncSetAttribute(delta_again_kernel<KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, walk_bytes(wa)) !=
             cudaSuccess ||
         cudaFuncSetAttribute(delta_back_kernel<KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, walk_bytes(wb)) !=
@@ -621,18 +774,27 @@ int bwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
         p, wb, q, k, dout, (const BwdRecord *)(ws + at.back), dhT, ys, dv, ds_img, dh0);
     count_launches(2);
     if (rows > 0) {
-        delta_grad_kernel<KT><<<(unsigned)(slots * p.Hk), kGradThreads, grad_bytes, st>>>(
-            p, q, k, dout, g, beta, resid, ys, s_img, ds_img, dq, dk, dg, dbeta);
+        const bool single = p.H == p.Hk;
+        GradArgs a{q, k, dout, g, beta, resid, ys, s_img, ds_img, dq, dk, single ? nullptr : (float *)(ws + at.dq_part),
+                   single ? nullptr : (float *)(ws + at.dk_part), dg, dbeta, (unsigned)(slots * p.H)};
+        const unsigned sms = (unsigned)device_info().sm_count;
+        delta_grad_kernel<KT><<<a.units < sms ? a.units : sms, kGradThreads, grad_bytes, st>>>(p, a);
         count_launches(1);
+        if (!single) {
+            const int64_t n = (int64_t)rows * p.Hk * p.dk;
+            const unsigned nb = (unsigned)((n / 4 + 255) / 256);
+            delta_heads_kernel<<<nb, 256, 0, st>>>(a.dq_part, dq, n, p.dk, p.group());
+            delta_heads_kernel<<<nb, 256, 0, st>>>(a.dk_part, dk, n, p.dk, p.group());
+            count_launches(2);
+        }
     }
     return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
 }
 
 }  // namespace
 
-// bf16 with dk <= 128 (a warp's share of the state fits its registers) and dv <= 256 (the gradient kernel's three
-// tiles of 64 x dv fit in shared memory).
-bool mma_bwd_supported(int dk, int dv) { return dk <= 128 && dv <= 256; }
+// bf16 with dk <= 128: a warp's share of the state fits its registers.
+bool mma_bwd_supported(int dk) { return dk <= 128; }
 
 size_t mma_bwd_workspace(const Shape &p) {
 #define GLA_CALL(KT) return workspace_kt<KT>(p).total

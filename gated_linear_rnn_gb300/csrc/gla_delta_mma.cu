@@ -248,7 +248,7 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
     load_state<KT>(S, h0, p, f.chain, col, lane);
     for (int c = 0; c < f.nch; ++c) {
         const int sg = c % w.stages;
-        if (!ptx::mbar_wait(f.full + 8 * sg, (c / w.stages) & 1, f.abort_flag, kWaitNs)) {
+        if (!warp_wait(f.full + 8 * sg, (c / w.stages) & 1, f.abort_flag)) {
             if (lane == 0) {
                 *f.abort_flag = 1;
                 record_status(GLA_ERR_TIMEOUT);

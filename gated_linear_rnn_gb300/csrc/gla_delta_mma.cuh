@@ -131,6 +131,11 @@ Walk make_walk(const Shape &p, bool with_q) {
 }
 inline int walk_bytes(const Walk &w) { return 128 + w.warps * kC * kOutRow + w.stages * w.stage_bytes; }
 
+// A bounded wait of a whole warp: all lanes learn the same.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
+    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort_flag, kWaitNs));
+}
+
 // Who a block and a thread are, and the shared memory: barriers, the warps' output tiles, the stages (K | Q | V |
 // record).
 struct Frame {
@@ -185,7 +190,7 @@ __device__ __forceinline__ void fetch(const Shape &p, const Walk &w, const Frame
     bool ok = true;
     for (int i = 0; i < f.nch; ++i) {
         const int c = kBack ? f.nch - 1 - i : i, sg = i % w.stages;
-        ok = i < w.stages || ptx::mbar_wait(f.empty + 8 * sg, (i / w.stages + 1) & 1, f.abort_flag, kWaitNs);
+        ok = i < w.stages || warp_wait(f.empty + 8 * sg, (i / w.stages + 1) & 1, f.abort_flag);
         if (!ok) break;
         const bool row = c * kC + t < f.r.len;  // a short chunk's missing rows are zero, and not read
         const uint32_t at = sg * w.stage_bytes;
