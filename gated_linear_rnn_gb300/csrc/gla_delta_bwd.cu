@@ -492,7 +492,10 @@ delta_grad_kernel(Shape p, GradArgs a) {
         return;
     }
     take_registers();
-    const int role = warp >> 2, rt = warp & 3, gr = lane >> 2, tg = lane & 3, m8 = lane >> 3, r8 = lane & 7;
+    // A tile of 16 tokens costs the more the further down it lies (T, R', N are triangular); the four SM quarters
+    // take warps in turn, so Y's tiles run against dO's.
+    const int role = warp >> 2, rt = role == 1 ? 3 - (warp & 3) : warp & 3;
+    const int gr = lane >> 2, tg = lane & 3, m8 = lane >> 3, r8 = lane & 7;
     const int row0 = rt * 16 + gr;  // this lane's rows: row0 and row0 + 8
     const int tiles = (p.dv + 15) / 16, slabs = (tiles + 1) / 2;
     const uint32_t mt = base + P::kOffM, nt = mt + kG * kMRow;
@@ -520,7 +523,9 @@ delta_grad_kernel(Shape p, GradArgs a) {
             const uint32_t b_at = slab + (2 * kG + (m8 >> 1) * 8 + r8) * kSlabRow + (m8 & 1) * 16;
             const uint32_t image = slab + 3 * kG * kSlabRow + (role == 2 ? P::kImage : 0) + lane * 16;
             const int here = min(2, tiles - 2 * s);
-            for (int x = 0; x < here; ++x) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (x >= here) break;
                 uint32_t f[4];
                 ldsm4(f, a_at + x * 32);
 #pragma unroll
@@ -584,6 +589,7 @@ delta_grad_kernel(Shape p, GradArgs a) {
                 for (int m = t + 1; m < rt; ++m) f *= dc.whole[m];
                 between[t] = f;
             }
+            float own0 = 0.f, own1 = 0.f;  // the diagonal's two elements, where tg == gr / 2
             const float p0 = dc.pre[row0], p1 = dc.pre[row0 + 8];
             const float g0 = role ? -dc.beta[row0] : 1.f, g1 = role ? -dc.beta[row0 + 8] : 1.f;
 #pragma unroll
@@ -596,14 +602,8 @@ delta_grad_kernel(Shape p, GradArgs a) {
                         const float *D = dc.diag[rt] + gr * 16 + (j & 15);
                         const float2 u = *reinterpret_cast<const float2 *>(D), v = *reinterpret_cast<const float2 *>(D + 128);
                         const int i0 = row0, i1 = row0 + 8, off = role;  // N leaves the diagonal out
-                        if (role) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int i = e < 2 ? i0 : i1;
-                                if (i == j + (e & 1) && i < at.len)
-                                    store_gate<bf16>(a.dbeta, (at.row + i) * p.H + h, p.gate_f32, T[t][e]);
-                            }
-                        }
+                        if (t == 2 * rt) own0 = gr & 1 ? T[t][1] : T[t][0];
+                        else own1 = gr & 1 ? T[t][3] : T[t][2];
                         x[0] = j + off <= i0 ? g0 * b0 * u.x * T[t][0] : 0.f;
                         x[1] = j + 1 + off <= i0 ? g0 * b1 * u.y * T[t][1] : 0.f;
                         x[2] = j + off <= i1 ? g1 * b0 * v.x * T[t][2] : 0.f;
@@ -619,6 +619,10 @@ delta_grad_kernel(Shape p, GradArgs a) {
                     *reinterpret_cast<uint32_t *>(to) = pack(x[0], x[1]);
                     *reinterpret_cast<uint32_t *>(to + 8 * kMRow) = pack(x[2], x[3]);
                 }
+            if (role && tg == gr >> 1) {
+                if (row0 < at.len) store_gate<bf16>(a.dbeta, (at.row + row0) * p.H + h, p.gate_f32, own0);
+                if (row0 + 8 < at.len) store_gate<bf16>(a.dbeta, (at.row + row0 + 8) * p.H + h, p.gate_f32, own1);
+            }
         }
         if (compute_sync_any(!ok)) return;  // R' and N are whole
         {
@@ -667,21 +671,35 @@ delta_grad_kernel(Shape p, GradArgs a) {
                 A[i][0] += u.x; A[i][1] += u.y; A[i][2] += v.x; A[i][3] += v.y;
             }
         }
-        if (role < 2) {
-            const bool single = a.dq_part == nullptr;
-            const int64_t at0 = ((at.row + row0) * p.H + h) * p.dk + 2 * tg, far = (int64_t)8 * p.H * p.dk;
+        if (role < 2 && a.dq_part == nullptr) {
+            // 64 columns at a time through this warp's own 16 rows of R' or N, which the barrier has left free
+            const uint32_t tile = (role ? nt : mt) + rt * 16 * kMRow;
+            bf16 *to = (role ? a.dk : a.dq) + ((at.row + rt * 16) * p.H + h) * p.dk;
+#pragma unroll
+            for (int i0 = 0; i0 < 2 * KT; i0 += 8) {
+                __syncwarp();
+#pragma unroll
+                for (int i = i0; i < (i0 + 8 < 2 * KT ? i0 + 8 : 2 * KT); i += 2)
+                    stsm4(tile + ((m8 & 1) * 8 + r8) * kMRow + (i - i0 + (m8 >> 1)) * 16, pack(A[i][0], A[i][1]),
+                          pack(A[i][2], A[i][3]), pack(A[i + 1][0], A[i + 1][1]), pack(A[i + 1][2], A[i + 1][3]));
+                __syncwarp();
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int row = x * 4 + (lane >> 3), u = i0 + (lane & 7);
+                    if (rt * 16 + row < at.len && u * 8 < p.dk)
+                        *reinterpret_cast<uint4 *>(to + (int64_t)row * p.H * p.dk + u * 8) =
+                            lds128(tile + row * kMRow + (lane & 7) * 16);
+                }
+            }
+            __syncwarp();
+        } else if (role < 2) {
+            float *to = (role ? a.dk_part : a.dq_part) + ((at.row + row0) * p.H + h) * p.dk + 2 * tg;
+            const int64_t far = (int64_t)8 * p.H * p.dk;
 #pragma unroll
             for (int i = 0; i < 2 * KT; ++i)
                 if (i * 8 < p.dk) {
-                    if (single) {
-                        bf16 *to = (role ? a.dk : a.dq) + at0 + i * 8;
-                        if (row0 < at.len) *reinterpret_cast<uint32_t *>(to) = pack(A[i][0], A[i][1]);
-                        if (row0 + 8 < at.len) *reinterpret_cast<uint32_t *>(to + far) = pack(A[i][2], A[i][3]);
-                    } else {
-                        float *to = (role ? a.dk_part : a.dq_part) + at0 + i * 8;
-                        if (row0 < at.len) *reinterpret_cast<float2 *>(to) = make_float2(A[i][0], A[i][1]);
-                        if (row0 + 8 < at.len) *reinterpret_cast<float2 *>(to + far) = make_float2(A[i][2], A[i][3]);
-                    }
+                    if (row0 < at.len) *reinterpret_cast<float2 *>(to + i * 8) = make_float2(A[i][0], A[i][1]);
+                    if (row0 + 8 < at.len) *reinterpret_cast<float2 *>(to + far + i * 8) = make_float2(A[i][2], A[i][3]);
                 }
         }
         if (warp == 8) {  // dg: lane owns tokens 2 lane and 2 lane + 1
