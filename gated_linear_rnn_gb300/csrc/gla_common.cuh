@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "gla.h"
 
 namespace gla {
@@ -67,6 +69,21 @@ const DeviceInfo &device_info();
 
 // Host-side count of kernel launches made by the library (gla_kernel_launches).
 void count_launches(int n);
+
+// Lets a kernel (with no static shared memory) use all of a block's shared memory on the current device; asked of the
+// runtime once per kernel and device, since the call costs about as much host time as half a launch.
+template <auto kKernel> bool allow_smem() {
+    constexpr int kDevices = 64;
+    static std::atomic<bool> allowed[kDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < kDevices && allowed[dev].load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, device_info().max_smem_optin) !=
+        cudaSuccess)
+        return false;
+    if (dev < kDevices) allowed[dev].store(true, std::memory_order_release);
+    return true;
+}
 
 }  // namespace gla
 

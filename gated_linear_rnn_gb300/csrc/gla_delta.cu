@@ -622,9 +622,7 @@ int simt_bwd(const Shape &p, const T *q, const T *k, const T *v, const void *g, 
     rc = check_launch(1);
     if (rc != GLA_OK || rows == 0) return rc;
     const size_t bytes = grad_simt_smem(p.dk);
-    if (cudaFuncSetAttribute(delta_grad_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
-        cudaSuccess)
-        return GLA_ERR_LAUNCH;
+    if (!allow_smem<delta_grad_simt_kernel<T>>()) return GLA_ERR_LAUNCH;
     delta_grad_simt_kernel<T><<<(unsigned)(slots * p.Hk), 256, bytes, st>>>(p, q, k, dout, g, beta, resid, ys, s0, ds1,
                                                                             dq, dk, dg, dbeta);
     return check_launch(1);

@@ -1,11 +1,10 @@
 // gla_delta_bwd.cu — the gradient of the gated delta rule on the tensor cores (bf16 inputs).
 //
-// Four kernels, with the notation of gla_delta_mma.cu (dS1: the gradient after a chunk, dS0: before it):
+// Three kernels, with the notation of gla_delta_mma.cu (dS1: the gradient after a chunk, dS0: before it):
 //   delta_prep_kernel  for every chunk of 32 tokens and head: what does not depend on the states.
-//   delta_again_kernel walks each chain forwards as the forward does, without its output: the residuals R, and the
-//                      state before every 64th token.
-//   delta_back_kernel  walks each chain backwards. With dU = P^T dO + diag(d) K dS1 the gradient that reaches a
-//                      token's write from outside the chunk and from its reads inside,
+//   delta_walks_kernel walks each chain forwards as the forward does, without its output: the residuals R, and the
+//                      state before every 64th token; and backwards: with dU = P^T dO + diag(d) K dS1 the gradient
+//                      that reaches a token's write from outside the chunk and from its reads inside,
 //                          Y = (I + diag(beta) L)^-T dU,  dV = diag(beta) Y,
 //                          dS0 = c_31 dS1 + Q^T diag(c) dO - K^T diag(c) dV,
 //                      and writes Y, dV and the gradient after every 64 tokens.
@@ -78,14 +77,14 @@ __device__ __forceinline__ void add_outer(float (&S)[2 * KT][4], const uint32_t 
     }
 }
 
+// Forwards, without an output.
 template <int KT>
-__global__ void __launch_bounds__(kMaxThreads)
-delta_again_kernel(Shape p, Walk w, const bf16 *__restrict__ k, const bf16 *__restrict__ v,
-                   const AgainRecord *__restrict__ records, const float *__restrict__ h0, bf16 *__restrict__ resid,
-                   uint4 *__restrict__ images) {
-    extern __shared__ __align__(128) char sm_raw[];
+__device__ __forceinline__ void walk_again(const Shape &p, const Walk &w, unsigned block, char *sm_raw,
+                                           const bf16 *__restrict__ k, const bf16 *__restrict__ v,
+                                           const AgainRecord *__restrict__ records, const float *__restrict__ h0,
+                                           bf16 *__restrict__ resid, uint4 *__restrict__ images) {
     constexpr int kTile = kC * row_bytes<KT>();
-    const Frame f(p, w, sm_raw);
+    const Frame f(p, w, block, sm_raw);
     if (f.bad && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
     if (f.warp >= w.groups * 4) {
         give_registers();
@@ -160,14 +159,15 @@ delta_again_kernel(Shape p, Walk w, const bf16 *__restrict__ k, const bf16 *__re
     }
 }
 
+// Backwards.
 template <int KT>
-__global__ void __launch_bounds__(kMaxThreads)
-delta_back_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16 *__restrict__ dout,
-                  const BwdRecord *__restrict__ records, const float *__restrict__ dhT, bf16 *__restrict__ ys,
-                  bf16 *__restrict__ dv, uint4 *__restrict__ images, float *__restrict__ dh0) {
-    extern __shared__ __align__(128) char sm_raw[];
+__device__ __forceinline__ void walk_back(const Shape &p, const Walk &w, unsigned block, char *sm_raw,
+                                          const bf16 *__restrict__ q, const bf16 *__restrict__ k,
+                                          const bf16 *__restrict__ dout, const BwdRecord *__restrict__ records,
+                                          const float *__restrict__ dhT, bf16 *__restrict__ ys, bf16 *__restrict__ dv,
+                                          uint4 *__restrict__ images, float *__restrict__ dh0) {
     constexpr int kTile = kC * row_bytes<KT>();
-    const Frame f(p, w, sm_raw);
+    const Frame f(p, w, block, sm_raw);
     if (f.bad && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
     if (f.warp >= w.groups * 4) {
         give_registers();
@@ -257,6 +257,27 @@ delta_back_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__res
         write_tile(dv, D, p, f, c, col, tile);
     }
     if (dh0 != nullptr) store_state<KT>(dh0, S, p, f.chain, col, lane);
+}
+
+struct WalkArgs {
+    const bf16 *q, *k, *v, *dout;
+    const AgainRecord *again;
+    const BwdRecord *back;
+    const float *h0, *dhT;
+    bf16 *resid, *ys, *dv;
+    uint4 *s_images, *ds_images;
+    float *dh0;
+};
+
+// Both walks in one launch, since neither needs the other: the blocks of the longer one, backwards, come first.
+template <int KT>
+__global__ void __launch_bounds__(kMaxThreads)
+delta_walks_kernel(Shape p, Walk again, Walk back, unsigned blocks, WalkArgs a) {
+    extern __shared__ __align__(128) char sm_raw[];
+    if (blockIdx.x < blocks)
+        walk_back<KT>(p, back, blockIdx.x, sm_raw, a.q, a.k, a.dout, a.back, a.dhT, a.ys, a.dv, a.ds_images, a.dh0);
+    else
+        walk_again<KT>(p, again, blockIdx.x - blocks, sm_raw, a.k, a.v, a.again, a.h0, a.resid, a.s_images);
 }
 
 // ---- dq, dk, dg, dbeta -----------------------------------------------------------------------------------------
@@ -729,7 +750,10 @@ delta_grad_kernel(Shape p, GradArgs a) {
 
 // dq and dk of a key head: the sum over its value heads' parts, four elements a thread, in a fixed order.
 __global__ void __launch_bounds__(256)
-delta_heads_kernel(const float *__restrict__ part, bf16 *__restrict__ out, int64_t n, int dk, int group) {
+delta_heads_kernel(const float *__restrict__ dq_part, const float *__restrict__ dk_part, bf16 *__restrict__ dq,
+                   bf16 *__restrict__ dk_out, int64_t n, int dk, int group) {
+    const float *part = blockIdx.y ? dk_part : dq_part;
+    bf16 *out = blockIdx.y ? dk_out : dq;
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;  // element of [rows, Hk, dk]
     if (i >= n) return;
     const float *from = part + (i / dk) * group * dk + i % dk;
@@ -774,23 +798,19 @@ int bwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
     const Walk wa = make_walk<KT, AgainRecord>(p, false), wb = make_walk<KT, BwdRecord>(p, true);
     const int grad_bytes = GradPlan<KT>::kTotal;
     const long long blocks = (long long)p.nseq * p.H * wa.splits;
-    if (blocks > 0x7fffffffLL || slots * p.H > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
-    if (cudaFuncSetAttribute(delta_again_kernel<KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, walk_bytes(wa)) !=
-            cudaSuccess ||
-        cudaFuncSetAttribute(delta_back_kernel<KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, walk_bytes(wb)) !=
-            cudaSuccess ||
-        cudaFuncSetAttribute(delta_grad_kernel<KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, grad_bytes) !=
-            cudaSuccess)
+    if (2 * blocks > 0x7fffffffLL || slots * p.H > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
+    const int walks_bytes = max(walk_bytes(wa), walk_bytes(wb));
+    if (!allow_smem<delta_walks_kernel<KT>>() || !allow_smem<delta_grad_kernel<KT>>())
         return GLA_ERR_LAUNCH;
     int rc = mma_prep_grad(p, q, k, g, beta, ws + at.again, ws + at.back, st);
     if (rc != GLA_OK) return rc;
     bf16 *resid = (bf16 *)(ws + at.resid), *ys = (bf16 *)(ws + at.ys);
     uint4 *s_img = (uint4 *)(ws + at.s_images), *ds_img = (uint4 *)(ws + at.ds_images);
-    delta_again_kernel<KT><<<(unsigned)blocks, (wa.groups + 1) * 128, walk_bytes(wa), st>>>(
-        p, wa, k, v, (const AgainRecord *)(ws + at.again), h0, resid, s_img);
-    delta_back_kernel<KT><<<(unsigned)blocks, (wb.groups + 1) * 128, walk_bytes(wb), st>>>(
-        p, wb, q, k, dout, (const BwdRecord *)(ws + at.back), dhT, ys, dv, ds_img, dh0);
-    count_launches(2);
+    const WalkArgs wargs{q, k, v, dout, (const AgainRecord *)(ws + at.again), (const BwdRecord *)(ws + at.back), h0, dhT,
+                         resid, ys, dv, s_img, ds_img, dh0};
+    delta_walks_kernel<KT><<<(unsigned)(2 * blocks), (wb.groups + 1) * 128, walks_bytes, st>>>(p, wa, wb, (unsigned)blocks,
+                                                                                          wargs);
+    count_launches(1);
     if (rows > 0) {
         const bool single = p.H == p.Hk;
         GradArgs a{q, k, dout, g, beta, resid, ys, s_img, ds_img, dq, dk, single ? nullptr : (float *)(ws + at.dq_part),
@@ -800,10 +820,9 @@ int bwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
         count_launches(1);
         if (!single) {
             const int64_t n = (int64_t)rows * p.Hk * p.dk;
-            const unsigned nb = (unsigned)((n / 4 + 255) / 256);
-            delta_heads_kernel<<<nb, 256, 0, st>>>(a.dq_part, dq, n, p.dk, p.group());
-            delta_heads_kernel<<<nb, 256, 0, st>>>(a.dk_part, dk, n, p.dk, p.group());
-            count_launches(2);
+            const dim3 grid((unsigned)((n / 4 + 255) / 256), 2);
+            delta_heads_kernel<<<grid, 256, 0, st>>>(a.dq_part, a.dk_part, dq, dk, n, p.dk, p.group());
+            count_launches(1);
         }
     }
     return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;

@@ -232,7 +232,7 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
                  float *__restrict__ hT) {
     extern __shared__ __align__(128) char sm_raw[];
     constexpr int kRow = row_bytes<KT>(), kTile = kC * kRow;
-    const Frame f(p, w, sm_raw);
+    const Frame f(p, w, blockIdx.x, sm_raw);
     if (f.bad && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
     if (f.warp >= w.groups * 4) {
         give_registers();
@@ -381,9 +381,7 @@ int launch_prep(const Shape &p, const bf16 *q, const bf16 *k, const void *g, con
                 AgainRecord *again, BwdRecord *back, cudaStream_t st) {
     const unsigned units = (unsigned)(chunk_slots(total_rows(p), p.nseq, kC) * p.H);
     const int bytes = kPrepWarps * prep_warp_bytes<KT>();
-    if (cudaFuncSetAttribute(delta_prep_kernel<KT, kGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-        cudaSuccess)
-        return GLA_ERR_LAUNCH;
+    if (!allow_smem<delta_prep_kernel<KT, kGrad>>()) return GLA_ERR_LAUNCH;
     delta_prep_kernel<KT, kGrad><<<(units + kPrepWarps - 1) / kPrepWarps, kPrepWarps * 32, bytes, st>>>(
         p, units, q, k, g, beta, records, again, back);
     count_launches(1);
@@ -396,9 +394,7 @@ int fwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
     const Walk w = make_walk<KT, FwdRecord>(p, true);
     const long long blocks = (long long)p.nseq * p.H * w.splits;
     if (blocks > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
-    if (cudaFuncSetAttribute(delta_fwd_kernel<KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, walk_bytes(w)) !=
-        cudaSuccess)
-        return GLA_ERR_LAUNCH;
+    if (!allow_smem<delta_fwd_kernel<KT>>()) return GLA_ERR_LAUNCH;
     int rc = launch_prep<KT, false>(p, q, k, g, beta, records, nullptr, nullptr, st);
     if (rc != GLA_OK) return rc;
     delta_fwd_kernel<KT><<<(unsigned)blocks, (w.groups + 1) * 128, walk_bytes(w), st>>>(p, w, q, k, v, records, h0, out,

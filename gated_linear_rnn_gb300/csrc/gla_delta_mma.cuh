@@ -150,14 +150,14 @@ struct Frame {
     uint32_t full, empty, outs, ring;
     volatile int *abort_flag;
 
-    __device__ __forceinline__ Frame(const Shape &p, const Walk &w, char *sm) {
+    __device__ __forceinline__ Frame(const Shape &p, const Walk &w, unsigned block, char *sm) {
         lane = threadIdx.x & 31;
         warp = threadIdx.x >> 5;
-        chain = (int)(blockIdx.x / (unsigned)w.splits);
+        chain = (int)(block / (unsigned)w.splits);
         s = chain / p.H;
         h = chain % p.H;
         hk = h / p.group();
-        col0 = (int)(blockIdx.x % (unsigned)w.splits) * w.warps * 16;  // first column of the block
+        col0 = (int)(block % (unsigned)w.splits) * w.warps * 16;  // first column of the block
         width = min(w.warps * 16, p.dv - col0);                        // its columns, a multiple of 8
         bad = !seq_range(s, p.T, p.cu, r);
         nch = (int)((r.len + kC - 1) / kC);

@@ -10,36 +10,105 @@
 //     dweight = sum over tokens of dz h,      dbias = sum over tokens of dz.
 //
 // Both are bound by HBM: every array is read or written once.  A thread keeps the same channels for all of its
-// tokens (kVec vectors of eight), so weight and bias stay in registers, as do the sums of dweight and dbias; the
+// tokens (kVec vectors of four), so weight and bias stay in registers, as do the sums of dweight and dbias; the
 // statistics are taken from the registers in two steps (mean, then centred squares) by shuffles between the
-// lanes of a group.  The blocks' sums of dweight and dbias go to a workspace that a second kernel adds up in a
-// fixed order.
+// lanes of a group.  The next token's vectors are on their way while one is computed.  The gradient does some
+// thirty operations an element, so arithmetic runs on pairs of f32 (fma.rn.f32x2 and the like).  The blocks' sums of dweight
+// and dbias go to a workspace that a second kernel adds up in a fixed order.
 #include "gla_common.cuh"
 
 namespace gla {
 namespace norm {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 
 enum Act { kNone = GLA_ACT_NONE, kSilu = GLA_ACT_SILU, kSigmoid = GLA_ACT_SIGMOID };
 
-// 1 / (1 + e^-x); for x below about -87 the exponential overflows and the quotient is the limit 0.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// ---- pairs of f32 ----------------------------------------------------------------------------------------------
+struct Pair { unsigned long long v; };
+__device__ __forceinline__ Pair pair(float a, float b) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b));
+    return p;
+}
+__device__ __forceinline__ Pair both(float a) { return pair(a, a); }
+__device__ __forceinline__ float2 parts(Pair p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p.v));
+    return f;
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+    Pair p;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+    return p;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+    Pair p;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+    return p;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+    Pair p;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return p;
+}
+__device__ __forceinline__ float total(Pair p) {
+    const float2 f = parts(p);
+    return f.x + f.y;
+}
 
-// Lanes per group (a power of two) and vectors of eight channels per lane.
+// q = 1 / (1 + e^-x) and rest = 1 - q, each to a few units in its last place: rest is e^-x q (1 - q would leave 2^-24
+// of one where q is near 1, which SiLU's slope multiplies by x).  Below x = -80 q stays at e^-80: the product
+// of an infinite e^-x with 0 would not be a number.
+__device__ __forceinline__ void sigmoid(Pair x, Pair &q, Pair &rest) {
+    const float2 f = parts(x);
+    const float2 t = parts(pair(fmaxf(f.x, -80.f), fmaxf(f.y, -80.f)) * both(-1.4426950408889634f));
+    float e0, e1, q0, q1;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t.y));
+    const Pair e = pair(e0, e1);
+    const float2 d = parts(e + both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q0) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q1) : "f"(d.y));
+    q = pair(q0, q1);
+    rest = e * q;
+}
+
+// Lanes per group (a power of two, whole warps above 32) and vectors of four channels per lane.
 struct Plan {
     int lanes, vecs, slots, per_block, blocks_y, rows_per_block;
 };
 
+// The vectors per lane that the kernels are built for: more would not fit their registers.
+#define GLA_BY_VEC(v, CALL)       \
+    switch (v) {                  \
+        case 1: CALL(1); break;   \
+        case 2: CALL(2); break;   \
+        case 3: CALL(3); break;   \
+        default: CALL(4); break;  \
+    }
+
+#define GLA_BY_ACT(V, RUN)                              \
+    if (gate) {                                         \
+        if (act == kNone) RUN(V, true, kNone);          \
+        else if (act == kSilu) RUN(V, true, kSilu);     \
+        else RUN(V, true, kSigmoid);                    \
+    } else {                                            \
+        if (act == kNone) RUN(V, false, kNone);         \
+        else if (act == kSilu) RUN(V, false, kSilu);    \
+        else RUN(V, false, kSigmoid);                   \
+    }
+
 Plan make_plan(int groups, int width) {
-    const int nv = width / 8;
+    const int nv = width / 4;
     Plan best{};
     int cost = 1 << 30;
-    for (int L = 1; L <= 32; L *= 2) {  // fewest idle vectors, then the most lanes (longer contiguous reads)
+    for (int L = 1; L <= 128; L *= 2) {
         const int v = (nv + L - 1) / L;
-        if (v > 8) continue;
-        const int c = (L * v - nv) * 64 - L + (v > 4 ? 16 : 0);
+        if (v > 4) continue;
+        // fewest idle vectors, then the fewest shuffles but at least eight lanes (64 neighbouring bytes of bf16)
+        const int c = (L * v - nv) * 64 + (L < 8 ? 8 / L : 0) + L / 4;
         if (c < cost) {
             cost = c;
             best.lanes = L;
@@ -53,223 +122,231 @@ Plan make_plan(int groups, int width) {
     return best;
 }
 
-template <typename T> struct Vec;  // eight elements as they lie in memory
+template <typename T> struct Vec;  // four elements as they lie in memory
 template <> struct Vec<__nv_bfloat16> {
-    uint4 a;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldcs(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+    uint2 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldcs(reinterpret_cast<const uint2 *>(p)); }
+    __device__ __forceinline__ void clear() { a = make_uint2(0, 0); }
+    __device__ __forceinline__ Pair get(int e) const {
+        const uint32_t w = e ? a.y : a.x;
+        return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
-    static __device__ __forceinline__ void put(__nv_bfloat16 *p, const float (&x)[8]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&t);
-        }
-        __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
+    static __device__ __forceinline__ void put(__nv_bfloat16 *p, const Pair (&x)[2]) {
+        const float2 f = parts(x[0]), g = parts(x[1]);
+        const __nv_bfloat162 u = __floats2bfloat162_rn(f.x, f.y), v = __floats2bfloat162_rn(g.x, g.y);
+        __stcs(reinterpret_cast<uint2 *>(p),
+               make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v)));
     }
 };
 template <> struct Vec<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float *p) {
-        a = __ldcs(reinterpret_cast<const float4 *>(p));
-        b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    }
-    static __device__ __forceinline__ void put(float *p, const float (&x)[8]) {
-        __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
-        __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
+    float4 a;
+    __device__ __forceinline__ void load(const float *p) { a = __ldcs(reinterpret_cast<const float4 *>(p)); }
+    __device__ __forceinline__ void clear() { a = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ Pair get(int e) const { return e ? pair(a.z, a.w) : pair(a.x, a.y); }
+    static __device__ __forceinline__ void put(float *p, const Pair (&x)[2]) {
+        const float2 f = parts(x[0]), g = parts(x[1]);
+        __stcs(reinterpret_cast<float4 *>(p), make_float4(f.x, f.y, g.x, g.y));
     }
 };
+// four parameters of this thread's vector, or a constant where the array or the vector is absent
+__device__ __forceinline__ void load_param(Pair (&to)[2], const float *from, int at, bool has, float otherwise) {
+    float4 f = make_float4(otherwise, otherwise, otherwise, otherwise);
+    if (has && from != nullptr) f = __ldg(reinterpret_cast<const float4 *>(from + at));
+    to[0] = pair(f.x, f.y);
+    to[1] = pair(f.z, f.w);
+}
 
-__device__ __forceinline__ float group_sum(float x, int lanes) {
-    for (int m = lanes >> 1; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+// The sum over a group's lanes.  Groups of more than a warp meet in `wide`; every thread of the block calls this.
+__device__ __forceinline__ float group_sum(float x, int lanes, float *wide) {
+    for (int m = min(lanes, 32) >> 1; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    if (lanes > 32) {
+        const int warp = threadIdx.x >> 5, warps = lanes >> 5, first = warp / warps * warps;
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) wide[warp] = x;
+        __syncthreads();
+        x = 0.f;
+        for (int m = 0; m < warps; ++m) x += wide[first + m];
+    }
     return x;
 }
 
-// Where a thread stands: its first channel, and whether each of its vectors exists.
-template <int kVec> struct Place {
-    int row_in_block, channel, nv, sub, lanes;
-    bool live;
-    __device__ __forceinline__ Place(int groups, int width, int lanes_, int per_block) : lanes(lanes_) {
+// Where a thread stands: its row in the block, its first channel, and how many of its vectors exist.
+struct Place {
+    int row_in_block, channel, count, stride;
+    __device__ __forceinline__ Place(int groups, int width, int lanes, int per_block) {
         const int slot = blockIdx.y * per_block + threadIdx.x % per_block;
         row_in_block = threadIdx.x / per_block;
-        nv = width >> 3;
-        sub = slot % lanes;
-        channel = (slot / lanes) * width + sub * 8;
-        live = slot < groups * lanes && row_in_block < kThreads / per_block;
+        const int sub = slot % lanes, nv = width >> 2;
+        channel = (slot / lanes) * width + sub * 4;
+        stride = lanes * 4;
+        count = slot < groups * lanes && row_in_block < kThreads / per_block && sub < nv ? (nv - sub + lanes - 1) / lanes : 0;
     }
-    __device__ __forceinline__ bool has(int j) const { return live && sub + j * lanes < nv; }
-    __device__ __forceinline__ int at(int j) const { return channel + j * lanes * 8; }
 };
 
-// Mean and 1 / sqrt(variance + eps) of the group whose part x a lane holds (zeros where it has no vector).
-template <int kVec>
-__device__ __forceinline__ void statistics(const float (&x)[kVec][8], const Place<kVec> &pl, float inv_width, float eps,
-                                           float &mean, float &r) {
-    float s = 0.f;
+// The centred values d of a lane's part of its group (an absent vector is zero and stays out of both sums) and 1 /
+// sqrt(variance + eps).
+template <typename T, int kVec>
+__device__ __forceinline__ void centre(const Vec<T> (&x)[kVec], Pair (&d)[kVec][2], int count, int lanes, float inv_width,
+                                       float eps, float *wide, float &r) {
+    Pair s = both(0.f);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += x[j][e];
-    mean = group_sum(s, pl.lanes) * inv_width;
-    s = 0.f;
+    for (int j = 0; j < kVec; ++j) s = s + (x[j].get(0) + x[j].get(1));
+    const float mean = group_sum(total(s), lanes, wide) * inv_width;
+    s = both(0.f);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-        if (pl.has(j)) {
+        const Pair m = both(j < count ? -mean : 0.f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float d = x[j][e] - mean;
-                s = fmaf(d, d, s);
-            }
+        for (int e = 0; e < 2; ++e) {
+            d[j][e] = x[j].get(e) + m;
+            s = fma(d[j][e], d[j][e], s);
         }
     }
-    r = rsqrtf(fmaf(group_sum(s, pl.lanes), inv_width, eps));
+    r = rsqrtf(fmaf(group_sum(total(s), lanes, wide), inv_width, eps));
 }
 
-template <typename T, int kVec, bool kGate>
+template <typename T, int kVec>
+__device__ __forceinline__ void fetch(Vec<T> (&v)[kVec], const T *from, int64_t at, int count, int stride) {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+        if (j < count) v[j].load(from + at + j * stride);
+        else v[j].clear();
+    }
+}
+
+template <typename T, int kVec, bool kGate, int kAct>
 __global__ void __launch_bounds__(kThreads)
 norm_fwd_kernel(const T *__restrict__ x, const float *__restrict__ weight, const float *__restrict__ bias,
-                const T *__restrict__ gate, int act, float eps, T *__restrict__ out, int64_t rows, int groups, int width,
+                const T *__restrict__ gate, float eps, T *__restrict__ out, int64_t rows, int groups, int width,
                 int lanes, int per_block) {
-    const Place<kVec> pl(groups, width, lanes, per_block);
+    __shared__ float wide[kThreads / 32];
+    const Place pl(groups, width, lanes, per_block);
     const int64_t C = (int64_t)groups * width;
-    float w[kVec][8], b[kVec][8];
-#pragma unroll
-    for (int j = 0; j < kVec; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w[j][e] = pl.has(j) && weight != nullptr ? __ldg(weight + pl.at(j) + e) : 1.f;
-            b[j][e] = pl.has(j) && bias != nullptr ? __ldg(bias + pl.at(j) + e) : 0.f;
-        }
     const int step = kThreads / per_block;
+    const int64_t hop = (int64_t)gridDim.x * step;
+    int64_t row = (int64_t)blockIdx.x * step + pl.row_in_block;
+    Vec<T> nx[kVec], ng[kVec];
+    fetch<T, kVec>(nx, x, row * C + pl.channel, row < rows ? pl.count : 0, pl.stride);
+    if (kGate) fetch<T, kVec>(ng, gate, row * C + pl.channel, row < rows ? pl.count : 0, pl.stride);
+    Pair w[kVec][2], b[kVec][2];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+        load_param(w[j], weight, pl.channel + j * pl.stride, j < pl.count, 1.f);
+        load_param(b[j], bias, pl.channel + j * pl.stride, j < pl.count, 0.f);
+    }
     const float inv_width = 1.f / (float)width;
-    for (int64_t r0 = (int64_t)blockIdx.x * step; r0 < rows; r0 += (int64_t)gridDim.x * step) {
-        const int64_t row = r0 + pl.row_in_block;
-        const bool live = row < rows;
+    for (int64_t r0 = (int64_t)blockIdx.x * step; r0 < rows; r0 += hop, row += hop) {
         Vec<T> vx[kVec], vg[kVec];
 #pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            if (live && pl.has(j)) {
-                vx[j].load(x + row * C + pl.at(j));
-                if (kGate) vg[j].load(gate + row * C + pl.at(j));
-            }
-        float f[kVec][8], mean, r;
-#pragma unroll
         for (int j = 0; j < kVec; ++j) {
-            if (live && pl.has(j)) vx[j].get(f[j]);
-            else
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[j][e] = 0.f;
+            vx[j] = nx[j];
+            if (kGate) vg[j] = ng[j];
         }
-        statistics<kVec>(f, pl, inv_width, eps, mean, r);
+        const int count = row < rows ? pl.count : 0, next = row + hop < rows ? pl.count : 0;
+        fetch<T, kVec>(nx, x, (row + hop) * C + pl.channel, next, pl.stride);
+        if (kGate) fetch<T, kVec>(ng, gate, (row + hop) * C + pl.channel, next, pl.stride);
+        float r;
+        Pair d[kVec][2];
+        centre<T, kVec>(vx, d, pl.count, lanes, inv_width, eps, wide, r);
+        const Pair rr = both(r);
 #pragma unroll
         for (int j = 0; j < kVec; ++j)
-            if (live && pl.has(j)) {
-                float g[8], y[8];
-                if (kGate) vg[j].get(g);
+            if (j < count) {
+                Pair y[2];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float z = fmaf((f[j][e] - mean) * r, w[j][e], b[j][e]);
-                    const float t = kGate ? g[e] : z;
-                    if (act == kNone) y[e] = kGate ? z * t : z;
-                    else if (act == kSilu) y[e] = (kGate ? z * t : z) * sigmoid(t);
-                    else y[e] = kGate ? z * sigmoid(t) : sigmoid(t);
+                for (int e = 0; e < 2; ++e) {
+                    const Pair z = fma(d[j][e] * rr, w[j][e], b[j][e]);
+                    const Pair t = kGate ? vg[j].get(e) : z;
+                    Pair q, rest;
+                    if (kAct != kNone) sigmoid(t, q, rest);
+                    if (kAct == kNone) y[e] = kGate ? z * t : z;
+                    else if (kAct == kSilu) y[e] = (kGate ? z * t : z) * q;
+                    else y[e] = kGate ? z * q : q;
                 }
-                Vec<T>::put(out + row * C + pl.at(j), y);
+                Vec<T>::put(out + row * C + pl.channel + j * pl.stride, y);
             }
     }
 }
 
-template <typename T, int kVec, bool kGate>
+template <typename T, int kVec, bool kGate, int kAct>
 __global__ void __launch_bounds__(kThreads)
 norm_bwd_kernel(const T *__restrict__ dout, const T *__restrict__ x, const float *__restrict__ weight,
-                const float *__restrict__ bias, const T *__restrict__ gate, int act, float eps, T *__restrict__ dx,
+                const float *__restrict__ bias, const T *__restrict__ gate, float eps, T *__restrict__ dx,
                 T *__restrict__ dgate, float *__restrict__ part, int64_t rows, int groups, int width, int lanes,
                 int per_block) {
-    __shared__ float sums[kThreads][9];
-    const Place<kVec> pl(groups, width, lanes, per_block);
+    __shared__ float sums[kThreads][5], wide[kThreads / 32];
+    const Place pl(groups, width, lanes, per_block);
     const int64_t C = (int64_t)groups * width;
-    float w[kVec][8], b[kVec][8], dw[kVec][8], db[kVec][8];
-#pragma unroll
-    for (int j = 0; j < kVec; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w[j][e] = pl.has(j) && weight != nullptr ? __ldg(weight + pl.at(j) + e) : 1.f;
-            b[j][e] = pl.has(j) && bias != nullptr ? __ldg(bias + pl.at(j) + e) : 0.f;
-            dw[j][e] = db[j][e] = 0.f;
-        }
     const int step = kThreads / per_block;
+    const int64_t hop = (int64_t)gridDim.x * step;
+    int64_t row = (int64_t)blockIdx.x * step + pl.row_in_block;
+    Vec<T> nx[kVec], nd[kVec], ng[kVec];
+    {
+        const int count = row < rows ? pl.count : 0;
+        fetch<T, kVec>(nx, x, row * C + pl.channel, count, pl.stride);
+        fetch<T, kVec>(nd, dout, row * C + pl.channel, count, pl.stride);
+        if (kGate) fetch<T, kVec>(ng, gate, row * C + pl.channel, count, pl.stride);
+    }
+    Pair w[kVec][2], b[kVec][2], dw[kVec][2], db[kVec][2];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+        load_param(w[j], weight, pl.channel + j * pl.stride, j < pl.count, 1.f);
+        load_param(b[j], bias, pl.channel + j * pl.stride, j < pl.count, 0.f);
+        dw[j][0] = dw[j][1] = db[j][0] = db[j][1] = both(0.f);
+    }
     const float inv_width = 1.f / (float)width;
-    for (int64_t r0 = (int64_t)blockIdx.x * step; r0 < rows; r0 += (int64_t)gridDim.x * step) {
-        const int64_t row = r0 + pl.row_in_block;
-        const bool live = row < rows;
-        Vec<T> vx[kVec], vg[kVec], vd[kVec];
-#pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            if (live && pl.has(j)) {
-                vx[j].load(x + row * C + pl.at(j));
-                vd[j].load(dout + row * C + pl.at(j));
-                if (kGate) vg[j].load(gate + row * C + pl.at(j));
-            }
-        float f[kVec][8], d[kVec][8], mean, r;
+    for (int64_t r0 = (int64_t)blockIdx.x * step; r0 < rows; r0 += hop, row += hop) {
+        Vec<T> vx[kVec], vd[kVec], vg[kVec];
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
-            if (live && pl.has(j)) vx[j].get(f[j]);
-            else
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[j][e] = 0.f;
+            vx[j] = nx[j];
+            vd[j] = nd[j];
+            if (kGate) vg[j] = ng[j];
         }
-        statistics<kVec>(f, pl, inv_width, eps, mean, r);
-        float s = 0.f, sh = 0.f;
+        const int count = row < rows ? pl.count : 0, next = row + hop < rows ? pl.count : 0;
+        fetch<T, kVec>(nx, x, (row + hop) * C + pl.channel, next, pl.stride);
+        fetch<T, kVec>(nd, dout, (row + hop) * C + pl.channel, next, pl.stride);
+        if (kGate) fetch<T, kVec>(ng, gate, (row + hop) * C + pl.channel, next, pl.stride);
+        float r;
+        Pair h[kVec][2], dh[kVec][2], s2 = both(0.f), sh2 = both(0.f);
+        centre<T, kVec>(vx, h, pl.count, lanes, inv_width, eps, wide, r);
+        const Pair rr = both(r);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
-            if (live && pl.has(j)) {
-                float g[8], dg[8];
-                vd[j].get(d[j]);
-                if (kGate) vg[j].get(g);
+            if (j < count) {
+                Pair dg[2];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float h = (f[j][e] - mean) * r, z = fmaf(h, w[j][e], b[j][e]);
-                    const float t = kGate ? g[e] : z, q = sigmoid(t);
-                    const float slope = act == kNone ? 1.f : act == kSilu ? q * fmaf(t, 1.f - q, 1.f) : q * (1.f - q);
-                    float dz;
+                for (int e = 0; e < 2; ++e) {
+                    h[j][e] = h[j][e] * rr;
+                    const Pair z = fma(h[j][e], w[j][e], b[j][e]), up = vd[j].get(e);
+                    const Pair t = kGate ? vg[j].get(e) : z;
+                    Pair q, rest, slope;
+                    if (kAct != kNone) sigmoid(t, q, rest);
+                    if (kAct == kSilu) slope = q * fma(t, rest, both(1.f));
+                    if (kAct == kSigmoid) slope = q * rest;
+                    Pair dz = kAct == kNone ? up : up * slope;  // through the activation's slope
                     if (kGate) {
-                        const float up = d[j][e];
-                        dz = up * (act == kNone ? t : act == kSilu ? t * q : q);
-                        dg[e] = up * z * slope;
-                    } else {
-                        dz = d[j][e] * slope;
+                        dg[e] = dz * z;
+                        dz = up * (kAct == kNone ? t : kAct == kSilu ? t * q : q);
                     }
-                    dw[j][e] = fmaf(dz, h, dw[j][e]);
-                    db[j][e] += dz;
-                    const float dh = dz * w[j][e];
-                    s += dh;
-                    sh = fmaf(dh, h, sh);
-                    f[j][e] = h;
-                    d[j][e] = dh;
+                    dw[j][e] = fma(dz, h[j][e], dw[j][e]);
+                    db[j][e] = db[j][e] + dz;
+                    dh[j][e] = dz * w[j][e];
+                    s2 = s2 + dh[j][e];
+                    sh2 = fma(dh[j][e], h[j][e], sh2);
                 }
-                if (kGate) Vec<T>::put(dgate + row * C + pl.at(j), dg);
+                if (kGate) Vec<T>::put(dgate + row * C + pl.channel + j * pl.stride, dg);
             }
         }
-        s = group_sum(s, pl.lanes) * inv_width;
-        sh = group_sum(sh, pl.lanes) * inv_width;
+        const Pair s = both(-group_sum(total(s2), lanes, wide) * inv_width),
+                   sh = both(-group_sum(total(sh2), lanes, wide) * inv_width);
 #pragma unroll
         for (int j = 0; j < kVec; ++j)
-            if (live && pl.has(j)) {
-                float y[8];
+            if (j < count) {
+                Pair y[2];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = r * (d[j][e] - s - f[j][e] * sh);
-                Vec<T>::put(dx + row * C + pl.at(j), y);
+                for (int e = 0; e < 2; ++e) y[e] = rr * fma(h[j][e], sh, dh[j][e] + s);
+                Vec<T>::put(dx + row * C + pl.channel + j * pl.stride, y);
             }
     }
     // the block's rows of one channel set meet in shared memory; one writer per channel
@@ -278,17 +355,19 @@ norm_bwd_kernel(const T *__restrict__ dout, const T *__restrict__ x, const float
     for (int j = 0; j < kVec; ++j)
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
-            __syncthreads();
+            const float2 lo = parts(which ? db[j][0] : dw[j][0]), hi = parts(which ? db[j][1] : dw[j][1]);
+            float v[4] = {lo.x, lo.y, hi.x, hi.y};
+            if (step > 1) {
+                __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sums[threadIdx.x][e] = which ? db[j][e] : dw[j][e];
-            __syncthreads();
-            if (pl.row_in_block == 0 && pl.has(j)) {
+                for (int e = 0; e < 4; ++e) sums[threadIdx.x][e] = v[e];
+                __syncthreads();
+            }
+            if (pl.row_in_block == 0 && j < pl.count) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float v = 0.f;
-                    for (int m = 0; m < step; ++m) v += sums[threadIdx.x + m * per_block][e];
-                    to[which * C + pl.at(j) + e] = v;
-                }
+                for (int e = 0; e < 4; ++e)
+                    for (int m = 1; m < step; ++m) v[e] += sums[threadIdx.x + m * per_block][e];
+                *reinterpret_cast<float4 *>(to + which * C + pl.channel + j * pl.stride) = make_float4(v[0], v[1], v[2], v[3]);
             }
         }
 }
@@ -302,6 +381,7 @@ norm_param_kernel(const float *__restrict__ part, int nblocks, int64_t C, float 
     const int run = threadIdx.x >> 5;
     float s = 0.f;
     if (c < 2 * C)
+#pragma unroll 8
         for (int i = run; i < nblocks; i += 8) s += part[(int64_t)i * 2 * C + c];
     sm[run][threadIdx.x & 31] = s;
     __syncthreads();
@@ -315,38 +395,27 @@ norm_param_kernel(const float *__restrict__ part, int nblocks, int64_t C, float 
 }
 
 int blocks_x(const Plan &pl, int64_t rows, int per_sm) {
+    // blocks of one column set that run at once; more rows than that are walked over
     const int64_t need = (rows + pl.rows_per_block - 1) / pl.rows_per_block;
     int64_t most = (int64_t)device_info().sm_count * per_sm / pl.blocks_y;
     if (most < 1) most = 1;
     return (int)(need < most ? need : most);
 }
 
-constexpr int kBwdPerSm = 4;
-
-#define GLA_BY_VEC(v, CALL)      \
-    switch (v) {                 \
-        case 1: CALL(1); break;  \
-        case 2: CALL(2); break;  \
-        case 3: CALL(3); break;  \
-        case 4: CALL(4); break;  \
-        case 5: CALL(5); break;  \
-        case 6: CALL(6); break;  \
-        case 7: CALL(7); break;  \
-        default: CALL(8); break; \
-    }
+constexpr int kBwdPerSm = 2;  // blocks of the gradient that an SM holds at its 128 registers
 
 template <typename T>
 int fwd(const T *x, const float *weight, const float *bias, const T *gate, int act, float eps, T *out, int64_t rows,
         int groups, int width, cudaStream_t st) {
     if (rows == 0) return GLA_OK;
     const Plan pl = make_plan(groups, width);
-    const dim3 grid((unsigned)blocks_x(pl, rows, 16), (unsigned)pl.blocks_y);
-#define GLA_CALL(V)                                                                                               \
-    if (gate) norm_fwd_kernel<T, V, true><<<grid, kThreads, 0, st>>>(x, weight, bias, gate, act, eps, out, rows,   \
-                                                                     groups, width, pl.lanes, pl.per_block);       \
-    else norm_fwd_kernel<T, V, false><<<grid, kThreads, 0, st>>>(x, weight, bias, gate, act, eps, out, rows,       \
-                                                                 groups, width, pl.lanes, pl.per_block)
+    const dim3 grid((unsigned)blocks_x(pl, rows, 4), (unsigned)pl.blocks_y);
+#define GLA_RUN(V, G, A)                                                                                           \
+    norm_fwd_kernel<T, V, G, A><<<grid, kThreads, 0, st>>>(x, weight, bias, gate, eps, out, rows, groups, width,    \
+                                                           pl.lanes, pl.per_block)
+#define GLA_CALL(V) GLA_BY_ACT(V, GLA_RUN)
     GLA_BY_VEC(pl.vecs, GLA_CALL)
+#undef GLA_RUN
 #undef GLA_CALL
     count_launches(1);
     return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
@@ -361,13 +430,12 @@ int bwd(const T *dout, const T *x, const float *weight, const float *bias, const
     if (rows > 0) {
         nb = blocks_x(pl, rows, kBwdPerSm);
         const dim3 grid((unsigned)nb, (unsigned)pl.blocks_y);
-#define GLA_CALL(V)                                                                                                  \
-    if (gate) norm_bwd_kernel<T, V, true><<<grid, kThreads, 0, st>>>(dout, x, weight, bias, gate, act, eps, dx,       \
-                                                                     dgate, ws, rows, groups, width, pl.lanes,        \
-                                                                     pl.per_block);                                   \
-    else norm_bwd_kernel<T, V, false><<<grid, kThreads, 0, st>>>(dout, x, weight, bias, gate, act, eps, dx, dgate,    \
-                                                                 ws, rows, groups, width, pl.lanes, pl.per_block)
+#define GLA_RUN(V, G, A)                                                                                             \
+    norm_bwd_kernel<T, V, G, A><<<grid, kThreads, 0, st>>>(dout, x, weight, bias, gate, eps, dx, dgate, ws, rows,     \
+                                                           groups, width, pl.lanes, pl.per_block)
+#define GLA_CALL(V) GLA_BY_ACT(V, GLA_RUN)
         GLA_BY_VEC(pl.vecs, GLA_CALL)
+#undef GLA_RUN
 #undef GLA_CALL
         count_launches(1);
     }

@@ -74,6 +74,8 @@ _lib = None
 def load(path: Optional[str] = None):
     """Load libgla.so once (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or LIB_PATH
@@ -442,51 +444,76 @@ def gla_conv1d_silu_step(x, weight, bias, state_inout, y, stream=None) -> None:
 
 
 # ---- gated delta rule and group normalisation ---------------------------------------------------
+#
+# A step of these takes a few microseconds on the GPU, so their checks are one pass of comparisons that hands out
+# the pointer; _check is asked what is wrong only where something is.
 
 ACT_NONE, ACT_SILU, ACT_SIGMOID = 0, 1, 2  # gla_act
 
 
+def _arg(t: Optional[torch.Tensor], name: str, dtype, shape, allow_none: bool = False):
+    """The device pointer of a contiguous CUDA tensor of this type and shape (None for an absent one)."""
+    if t is None:
+        if not allow_none:
+            raise ValueError(f"{name} is required")
+        return None
+    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+        _check(t, name, dtype, shape)
+    return t.data_ptr()
+
+
+def _raw_stream(stream, device: torch.device) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}  # gla_dtype
+
+
 def _dtype(t: torch.Tensor, name: str) -> int:
-    if t.dtype == torch.bfloat16:
-        return BF16
-    if t.dtype == torch.float32:
-        return F32
-    raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return code
 
 
-def _delta_args(q, k, v, g, beta, h0, out, hT, cu_seqlens):
-    """Checks shared by the chunked delta entry points; returns the sizes and types of the C call."""
-    if q.dim() != 4 or v.dim() != 4:
-        raise ValueError("q must be [B, T, Hk, dk] and v [B, T, H, dv] (packed: B = 1)")
-    B, T, Hk, dk = q.shape
-    H, dv = v.shape[2:]
+def _delta_types(q, g, H, Hk):
     dtype, gates = _dtype(q, "q"), _dtype(g, "g")
     if Hk == 0 or H % Hk:
         raise ValueError(f"the {H} value heads must be a multiple of the {Hk} key heads")
     if gates != F32 and gates != dtype:
         raise ValueError("g and beta must be torch.float32 or of the type of q")
-    _check(q, "q", q.dtype)
-    _check(k, "k", q.dtype, (B, T, Hk, dk))
-    _check(v, "v", q.dtype, (B, T, H, dv))
-    _check(g, "g", g.dtype, (B, T, H))
-    _check(beta, "beta", g.dtype, (B, T, H))
-    _check(out, "out", q.dtype, (B, T, H, dv))
+    return dtype, gates
+
+
+def _delta_args(q, k, v, g, beta, h0, out, hT, cu_seqlens):
+    """Checks shared by the chunked delta entry points; returns the pointers and the sizes and types of the C call."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be [B, T, Hk, dk] and v [B, T, H, dv] (packed: B = 1)")
+    B, T, Hk, dk = q.shape
+    _, _, H, dv = v.shape
+    dtype, gates = _delta_types(q, g, H, Hk)
     nseq = B
+    cu = None
     if cu_seqlens is not None:
         if B != 1:
             raise ValueError("a packed batch has leading dimension 1")
         _check(cu_seqlens, "cu_seqlens", torch.int32)
-        nseq = cu_seqlens.numel() - 1
-    _check(h0, "h0", torch.float32, (nseq, H, dk, dv), allow_none=True)
-    _check(hT, "hT", torch.float32, (nseq, H, dk, dv), allow_none=True)
-    return nseq, T, H, Hk, dk, dv, dtype, gates
+        nseq, cu = cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
+    qs, vs, gs, hs = q.shape, (B, T, H, dv), (B, T, H), (nseq, H, dk, dv)
+    t, gt = q.dtype, g.dtype
+    ptrs = (_arg(q, "q", t, qs), _arg(k, "k", t, qs), _arg(v, "v", t, vs), _arg(g, "g", gt, gs),
+            _arg(beta, "beta", gt, gs), _arg(h0, "h0", torch.float32, hs, True), _arg(out, "out", t, vs),
+            _arg(hT, "hT", torch.float32, hs, True))
+    return ptrs, (nseq, T, H, Hk, dk, dv, dtype, gates), cu
 
 
 def gla_delta_workspace_bytes(op: int, B: int, T: int, H: int, Hk: int, dk: int, dv: int, dtype: int,
                               packed: bool) -> int:
     """Workspace bytes of gla_delta_chunk_fwd (OP_FORWARD) or gla_delta_chunk_bwd (OP_BACKWARD)."""
-    n = int(load().gla_delta_workspace_bytes(int(op), int(B), int(T), int(H), int(Hk), int(dk), int(dv), int(dtype),
-                                             int(bool(packed))))
+    n = load().gla_delta_workspace_bytes(int(op), int(B), int(T), int(H), int(Hk), int(dk), int(dv), int(dtype),
+                                         int(bool(packed)))
     if n < 0:
         raise GLAError(n, "gla_delta_workspace_bytes")
     return n
@@ -503,43 +530,41 @@ def _allocating_on(stream, device):
 
 
 def _workspace(given, need: int, device, stream):
-    """The caller's workspace, or one from torch's allocator that stays valid for work on ``stream``."""
+    """(tensor, pointer, bytes) of the caller's workspace, or of one from torch's allocator on ``stream``."""
     if given is not None:
         if not given.is_cuda or not given.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor")
-        return given, given.numel() * given.element_size()
+        return given, given.data_ptr(), given.numel() * given.element_size()
     if need == 0:
-        return None, 0
+        return None, None, 0
     with _allocating_on(stream, device):
-        return torch.empty(need, dtype=torch.uint8, device=device), need
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), need
 
 
 def gla_delta_chunk_fwd(q, k, v, g, beta, h0, out, hT, cu_seqlens=None, workspace=None, stream=None) -> None:
     """Gated delta rule over whole sequences: writes ``out`` and (if given) ``hT``.  ``workspace``: at least
     gla_delta_workspace_bytes(OP_FORWARD, ...) bytes, or None to take it from torch.  See include/gla.h."""
-    nseq, T, H, Hk, dk, dv, dtype, gates = _delta_args(q, k, v, g, beta, h0, out, hT, cu_seqlens)
-    need = gla_delta_workspace_bytes(OP_FORWARD, nseq, T, H, Hk, dk, dv, dtype, cu_seqlens is not None)
-    ws, n = _workspace(workspace, need, q.device, stream)
-    rc = load().gla_delta_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(out), _ptr(hT), nseq,
-                                    T, H, Hk, dk, dv, dtype, gates, _ptr(cu_seqlens), _ptr(ws), n, _stream(stream))
+    ptrs, sizes, cu = _delta_args(q, k, v, g, beta, h0, out, hT, cu_seqlens)
+    need = gla_delta_workspace_bytes(OP_FORWARD, *sizes[:7], cu is not None)
+    ws, at, n = _workspace(workspace, need, q.device, stream)
+    rc = load().gla_delta_chunk_fwd(*ptrs, *sizes, cu, at, n, _raw_stream(stream, q.device))
     _raise(rc, "gla_delta_chunk_fwd")
 
 
 def gla_delta_chunk_bwd(q, k, v, g, beta, dout, h0, dhT, dq, dk, dv, dg, dbeta, dh0, cu_seqlens=None, workspace=None,
                         stream=None) -> None:
     """Gradients of gla_delta_chunk_fwd: writes dq, dk, dv, dg, dbeta and (if given) dh0.  See include/gla.h."""
-    nseq, T, H, Hk, dk_, dv_, dtype, gates = _delta_args(q, k, v, g, beta, h0, dout, dhT, cu_seqlens)
-    _check(dq, "dq", q.dtype, tuple(q.shape))
-    _check(dk, "dk", q.dtype, tuple(q.shape))
-    _check(dv, "dv", q.dtype, tuple(v.shape))
-    _check(dg, "dg", g.dtype, tuple(g.shape))
-    _check(dbeta, "dbeta", g.dtype, tuple(g.shape))
-    _check(dh0, "dh0", torch.float32, (nseq, H, dk_, dv_), allow_none=True)
-    need = gla_delta_workspace_bytes(OP_BACKWARD, nseq, T, H, Hk, dk_, dv_, dtype, cu_seqlens is not None)
-    ws, n = _workspace(workspace, need, q.device, stream)
-    rc = load().gla_delta_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(dout), _ptr(h0), _ptr(dhT),
-                                    _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dh0), nseq, T, H, Hk, dk_,
-                                    dv_, dtype, gates, _ptr(cu_seqlens), _ptr(ws), n, _stream(stream))
+    ptrs, sizes, cu = _delta_args(q, k, v, g, beta, h0, dout, dhT, cu_seqlens)
+    nseq, _, H, _, dk_, dv_ = sizes[:6]
+    grads = (_arg(dq, "dq", q.dtype, q.shape), _arg(dk, "dk", q.dtype, q.shape), _arg(dv, "dv", q.dtype, v.shape),
+             _arg(dg, "dg", g.dtype, g.shape), _arg(dbeta, "dbeta", g.dtype, g.shape),
+             _arg(dh0, "dh0", torch.float32, (nseq, H, dk_, dv_), True))
+    need = gla_delta_workspace_bytes(OP_BACKWARD, *sizes[:7], cu is not None)
+    ws, at, n = _workspace(workspace, need, q.device, stream)
+    p = ptrs
+    rc = load().gla_delta_chunk_bwd(p[0], p[1], p[2], p[3], p[4], p[6], p[5], p[7], *grads, *sizes, cu, at, n,
+                                    _raw_stream(stream, q.device))
     _raise(rc, "gla_delta_chunk_bwd")
 
 
@@ -549,51 +574,42 @@ def gla_delta_decode_step(q, k, v, g, beta, state, out, slots=None, stream=None)
     if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
         raise ValueError("q must be [N, Hk, dk], v [N, H, dv] and state [.., H, dk, dv]")
     N, Hk, dk = q.shape
-    H, dv = v.shape[1:]
-    dtype, gates = _dtype(q, "q"), _dtype(g, "g")
-    if Hk == 0 or H % Hk:
-        raise ValueError(f"the {H} value heads must be a multiple of the {Hk} key heads")
-    if gates != F32 and gates != dtype:
-        raise ValueError("g and beta must be torch.float32 or of the type of q")
-    _check(q, "q", q.dtype)
-    _check(k, "k", q.dtype, (N, Hk, dk))
-    _check(v, "v", q.dtype, (N, H, dv))
-    _check(g, "g", g.dtype, (N, H))
-    _check(beta, "beta", g.dtype, (N, H))
-    _check(out, "out", q.dtype, (N, H, dv))
-    _check(state, "state", torch.float32, (state.shape[0] if slots is not None else N, H, dk, dv))
-    _check(slots, "slots", torch.int32, (N,), allow_none=True)
-    rc = load().gla_delta_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(slots),
-                                      int(state.shape[0]), _ptr(out), N, H, Hk, dk, dv, dtype, gates, _stream(stream))
-    _raise(rc, "gla_delta_decode_step")
+    _, H, dv = v.shape
+    dtype, gates = _delta_types(q, g, H, Hk)
+    pages = state.shape[0] if slots is not None else N
+    qs, vs, gs, t, gt = q.shape, (N, H, dv), (N, H), q.dtype, g.dtype
+    rc = load().gla_delta_decode_step(
+        _arg(q, "q", t, qs), _arg(k, "k", t, qs), _arg(v, "v", t, vs), _arg(g, "g", gt, gs), _arg(beta, "beta", gt, gs),
+        _arg(state, "state", torch.float32, (pages, H, dk, dv)), _arg(slots, "slots", torch.int32, (N,), True), pages,
+        _arg(out, "out", t, vs), N, H, Hk, dk, dv, dtype, gates, _raw_stream(stream, q.device))
+    if rc:
+        raise GLAError(rc, "gla_delta_decode_step")
 
 
 def _norm_args(x, weight, bias, groups, gate, out):
-    if x.dim() < 1 or groups <= 0 or x.shape[-1] % groups:
+    C = x.shape[-1] if x.dim() else 0
+    if groups <= 0 or C % groups or C == 0:
         raise ValueError("the last dimension of x must be a multiple of groups")
-    C = x.shape[-1]
     dtype = _dtype(x, "x")
-    _check(x, "x", x.dtype)
-    _check(out, "out", x.dtype, tuple(x.shape))
-    _check(gate, "gate", x.dtype, tuple(x.shape), allow_none=True)
-    _check(weight, "weight", torch.float32, (C,), allow_none=True)
-    _check(bias, "bias", torch.float32, (C,), allow_none=True)
-    return x.numel() // C if C else 0, C // groups, dtype
+    t, s = x.dtype, x.shape
+    ptrs = (_arg(x, "x", t, s), _arg(weight, "weight", torch.float32, (C,), True),
+            _arg(bias, "bias", torch.float32, (C,), True), _arg(gate, "gate", t, s, True))
+    return ptrs, _arg(out, "out", t, s), x.numel() // C, C // groups, dtype
 
 
 def gla_group_norm(x, weight, bias, groups: int, out, gate=None, act: int = ACT_SILU, eps: float = 1e-5,
                    stream=None) -> None:
     """Group normalisation of each token's channels with an activation (of ``gate`` if given): x, gate, out
     [..., groups * width], weight and bias [groups * width] f32 or None.  See include/gla.h."""
-    rows, width, dtype = _norm_args(x, weight, bias, int(groups), gate, out)
-    rc = load().gla_group_norm(_ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), int(act), float(eps), _ptr(out), rows,
-                               int(groups), width, dtype, _stream(stream))
-    _raise(rc, "gla_group_norm")
+    ptrs, to, rows, width, dtype = _norm_args(x, weight, bias, groups, gate, out)
+    rc = load().gla_group_norm(*ptrs, act, eps, to, rows, groups, width, dtype, _raw_stream(stream, x.device))
+    if rc:
+        raise GLAError(rc, "gla_group_norm")
 
 
 def gla_group_norm_workspace_bytes(rows: int, groups: int, width: int) -> int:
     """Workspace bytes of gla_group_norm_bwd."""
-    n = int(load().gla_group_norm_workspace_bytes(int(rows), int(groups), int(width)))
+    n = load().gla_group_norm_workspace_bytes(int(rows), int(groups), int(width))
     if n < 0:
         raise GLAError(n, "gla_group_norm_workspace_bytes")
     return n
@@ -602,15 +618,13 @@ def gla_group_norm_workspace_bytes(rows: int, groups: int, width: int) -> int:
 def gla_group_norm_bwd(dout, x, weight, bias, groups: int, dx, dweight, dbias, dgate=None, gate=None,
                        act: int = ACT_SILU, eps: float = 1e-5, workspace=None, stream=None) -> None:
     """Gradients of gla_group_norm: writes dx, dweight, dbias and (with a gate) dgate.  See include/gla.h."""
-    rows, width, dtype = _norm_args(x, weight, bias, int(groups), gate, dx)
-    _check(dout, "dout", x.dtype, tuple(x.shape))
-    _check(dgate, "dgate", x.dtype, tuple(x.shape), allow_none=gate is None)
-    _check(dweight, "dweight", torch.float32, (x.shape[-1],), allow_none=True)
-    _check(dbias, "dbias", torch.float32, (x.shape[-1],), allow_none=True)
-    ws, n = _workspace(workspace, gla_group_norm_workspace_bytes(rows, int(groups), width), x.device, stream)
-    rc = load().gla_group_norm_bwd(_ptr(dout), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), int(act), float(eps),
-                                   _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(dgate), rows, int(groups), width, dtype,
-                                   _ptr(ws), n, _stream(stream))
+    ptrs, to, rows, width, dtype = _norm_args(x, weight, bias, groups, gate, dx)
+    C = (x.shape[-1],)
+    grads = (_arg(dweight, "dweight", torch.float32, C, True), _arg(dbias, "dbias", torch.float32, C, True),
+             _arg(dgate, "dgate", x.dtype, x.shape, gate is None))
+    ws, at, n = _workspace(workspace, gla_group_norm_workspace_bytes(rows, groups, width), x.device, stream)
+    rc = load().gla_group_norm_bwd(_arg(dout, "dout", x.dtype, x.shape), *ptrs, act, eps, to, *grads, rows, groups, width,
+                                   dtype, at, n, _raw_stream(stream, x.device))
     _raise(rc, "gla_group_norm_bwd")
 
 
