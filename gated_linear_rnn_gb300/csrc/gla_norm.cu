@@ -214,8 +214,12 @@ __device__ __forceinline__ void fetch(Vec<T> (&v)[kVec], const T *from, int64_t 
     }
 }
 
+// Blocks that an SM holds at once, by the registers that a thread's vectors take.
+template <typename T> constexpr int fwd_per_sm(int vecs) { return vecs * (int)sizeof(T) <= 6 ? 3 : 2; }
+template <typename T> constexpr int bwd_per_sm(int vecs) { return vecs * (int)sizeof(T) <= 6 ? 2 : 1; }
+
 template <typename T, int kVec, bool kGate, int kAct>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, fwd_per_sm<T>(kVec))
 norm_fwd_kernel(const T *__restrict__ x, const float *__restrict__ weight, const float *__restrict__ bias,
                 const T *__restrict__ gate, float eps, T *__restrict__ out, int64_t rows, int groups, int width,
                 int lanes, int per_block) {
@@ -269,7 +273,7 @@ norm_fwd_kernel(const T *__restrict__ x, const float *__restrict__ weight, const
 }
 
 template <typename T, int kVec, bool kGate, int kAct>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, bwd_per_sm<T>(kVec))
 norm_bwd_kernel(const T *__restrict__ dout, const T *__restrict__ x, const float *__restrict__ weight,
                 const float *__restrict__ bias, const T *__restrict__ gate, float eps, T *__restrict__ dx,
                 T *__restrict__ dgate, float *__restrict__ part, int64_t rows, int groups, int width, int lanes,
@@ -402,14 +406,12 @@ int blocks_x(const Plan &pl, int64_t rows, int per_sm) {
     return (int)(need < most ? need : most);
 }
 
-constexpr int kBwdPerSm = 2;  // blocks of the gradient that an SM holds at its 128 registers
-
 template <typename T>
 int fwd(const T *x, const float *weight, const float *bias, const T *gate, int act, float eps, T *out, int64_t rows,
         int groups, int width, cudaStream_t st) {
     if (rows == 0) return GLA_OK;
     const Plan pl = make_plan(groups, width);
-    const dim3 grid((unsigned)blocks_x(pl, rows, 4), (unsigned)pl.blocks_y);
+    const dim3 grid((unsigned)blocks_x(pl, rows, fwd_per_sm<T>(pl.vecs)), (unsigned)pl.blocks_y);
 #define GLA_RUN(V, G, A)                                                                                           \
     norm_fwd_kernel<T, V, G, A><<<grid, kThreads, 0, st>>>(x, weight, bias, gate, eps, out, rows, groups, width,    \
                                                            pl.lanes, pl.per_block)
@@ -428,7 +430,7 @@ int bwd(const T *dout, const T *x, const float *weight, const float *bias, const
     const int64_t C = (int64_t)groups * width;
     int nb = 0;
     if (rows > 0) {
-        nb = blocks_x(pl, rows, kBwdPerSm);
+        nb = blocks_x(pl, rows, bwd_per_sm<T>(pl.vecs));
         const dim3 grid((unsigned)nb, (unsigned)pl.blocks_y);
 #define GLA_RUN(V, G, A)                                                                                             \
     norm_bwd_kernel<T, V, G, A><<<grid, kThreads, 0, st>>>(dout, x, weight, bias, gate, eps, dx, dgate, ws, rows,     \
@@ -448,10 +450,10 @@ int bwd(const T *dout, const T *x, const float *weight, const float *bias, const
 
 }  // namespace
 
-// Bytes of the blocks' sums of dweight and dbias.
+// Bytes of the blocks' sums of dweight and dbias (bf16's blocks are never fewer than f32's).
 size_t workspace(int64_t rows, int groups, int width) {
     const Plan pl = make_plan(groups, width);
-    return (size_t)blocks_x(pl, rows < 1 ? 1 : rows, kBwdPerSm) * 2 * groups * width * sizeof(float);
+    return (size_t)blocks_x(pl, rows < 1 ? 1 : rows, bwd_per_sm<__nv_bfloat16>(pl.vecs)) * 2 * groups * width * sizeof(float);
 }
 
 int group_norm(const void *x, const float *weight, const float *bias, const void *gate, int act, float eps, void *out,
