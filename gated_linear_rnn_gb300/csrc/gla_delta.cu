@@ -43,8 +43,12 @@ template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 
     *reinterpret_cast<uint2 *>(p) = t;
 }
 
+// Blocks per SM: the more of them, the more bytes in flight (four hold 98 KB of a 96 x 192 state); above that the
+// registers of kRows rows set the number.
+constexpr int step_per_sm(int rows) { return rows <= 6 ? 4 : rows <= 8 ? 3 : 1; }
+
 template <typename T, int kRows>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, step_per_sm(kRows))
 delta_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, const void *__restrict__ g,
                   const void *__restrict__ beta, int gate_f32, float *__restrict__ state,
                   const int32_t *__restrict__ slots, int nslots, T *__restrict__ out, int H, int Hk, int dk, int dv,
@@ -102,13 +106,27 @@ delta_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
         }
     }
     const int wide = 4 * ncg;
-    *reinterpret_cast<float4 *>(red + rg * wide + cg * 4) = make_float4(pk[0], pk[1], pk[2], pk[3]);
-    *reinterpret_cast<float4 *>(red + (kStepGroups + rg) * wide + cg * 4) = make_float4(pq[0], pq[1], pq[2], pq[3]);
-    if (cg == 0) redqk[rg] = pqk;
+    // with 16 column groups a warp holds two row groups: they meet by shuffle, and half as many sums in shared memory
+    int np = kStepGroups, at = rg;
+    if (ncg == 16) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            pk[c] += __shfl_xor_sync(0xffffffffu, pk[c], 16);
+            pq[c] += __shfl_xor_sync(0xffffffffu, pq[c], 16);
+        }
+        pqk += __shfl_xor_sync(0xffffffffu, pqk, 16);
+        np = kStepGroups / 2;
+        at = rg >> 1;
+    }
+    if (ncg != 16 || (rg & 1) == 0) {
+        *reinterpret_cast<float4 *>(red + at * wide + cg * 4) = make_float4(pk[0], pk[1], pk[2], pk[3]);
+        *reinterpret_cast<float4 *>(red + (kStepGroups + at) * wide + cg * 4) = make_float4(pq[0], pq[1], pq[2], pq[3]);
+        if (cg == 0) redqk[at] = pqk;
+    }
     __syncthreads();
     float u[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < kStepGroups; ++j) {
+#pragma unroll 8
+    for (int j = 0; j < np; ++j) {
         const float4 t = *reinterpret_cast<const float4 *>(red + j * wide + cg * 4);
         u[0] += t.x; u[1] += t.y; u[2] += t.z; u[3] += t.w;
     }
@@ -126,8 +144,8 @@ delta_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
     }
     if (rg == 0) {
         float o[4] = {0.f, 0.f, 0.f, 0.f}, qk = 0.f;
-#pragma unroll
-        for (int j = 0; j < kStepGroups; ++j) {
+#pragma unroll 8
+        for (int j = 0; j < np; ++j) {
             const float4 t = *reinterpret_cast<const float4 *>(red + (kStepGroups + j) * wide + cg * 4);
             o[0] += t.x; o[1] += t.y; o[2] += t.z; o[3] += t.w;
             qk += redqk[j];
