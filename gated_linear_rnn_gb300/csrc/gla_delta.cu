@@ -17,9 +17,9 @@ namespace {
 //
 // Bound by HBM: 8 bytes per state element (read once, written once) against 7 FLOP.  u needs the sum over dk of
 // k S before any element can be written, so a block holds its whole slice of the state in registers between the
-// two: 16 row groups x up to 16 groups of four columns, kRows rows of 16 bytes a thread.  Both sums (k S and
+// two: 8 row groups x up to 16 groups of four columns, kRows rows of 16 bytes a thread.  Both sums (k S and
 // q S) are formed from that one read; o = a q S + (q k) u needs no second pass over the new state.
-constexpr int kStepGroups = 16;   // row groups per block
+constexpr int kStepGroups = 8;    // row groups per block
 
 template <typename T> __device__ __forceinline__ void load4(const T *p, float (&x)[4]);
 template <> __device__ __forceinline__ void load4<float>(const float *p, float (&x)[4]) {
@@ -43,12 +43,12 @@ template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 
     *reinterpret_cast<uint2 *>(p) = t;
 }
 
-// Blocks per SM: the more of them, the more bytes in flight (four hold 98 KB of a 96 x 192 state); above that the
-// registers of kRows rows set the number.
-constexpr int step_per_sm(int rows) { return rows <= 6 ? 4 : rows <= 8 ? 3 : 1; }
+// Blocks per SM: the more of them, the more bytes in flight (five hold 123 KB of a 96 x 192 state); the registers of
+// kRows rows set the number.
+constexpr int step_per_sm(int rows) { return rows <= 8 ? 7 : rows <= 12 ? 5 : rows <= 16 ? 4 : 2; }
 
 template <typename T, int kRows>
-__global__ void __launch_bounds__(256, step_per_sm(kRows))
+__global__ void __launch_bounds__(kStepGroups * 16, step_per_sm(kRows))
 delta_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, const void *__restrict__ g,
                   const void *__restrict__ beta, int gate_f32, float *__restrict__ state,
                   const int32_t *__restrict__ slots, int nslots, T *__restrict__ out, int H, int Hk, int dk, int dv,
@@ -125,7 +125,7 @@ delta_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
     }
     __syncthreads();
     float u[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
+#pragma unroll 4
     for (int j = 0; j < np; ++j) {
         const float4 t = *reinterpret_cast<const float4 *>(red + j * wide + cg * 4);
         u[0] += t.x; u[1] += t.y; u[2] += t.z; u[3] += t.w;
@@ -144,7 +144,7 @@ delta_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
     }
     if (rg == 0) {
         float o[4] = {0.f, 0.f, 0.f, 0.f}, qk = 0.f;
-#pragma unroll 8
+#pragma unroll 4
         for (int j = 0; j < np; ++j) {
             const float4 t = *reinterpret_cast<const float4 *>(red + (kStepGroups + j) * wide + cg * 4);
             o[0] += t.x; o[1] += t.y; o[2] += t.z; o[3] += t.w;
@@ -169,10 +169,10 @@ int launch_step(const T *q, const T *k, const T *v, const void *g, const void *b
     delta_step_kernel<T, R><<<(unsigned)blocks, ncg * kStepGroups, bytes, st>>>(q, k, v, g, beta, gate_f32, state,   \
                                                                                 slots, nslots, out, H, Hk, dk, dv,  \
                                                                                 ncg, nslices)
-    if (rows <= 4) GLA_STEP(4);
-    else if (rows <= 6) GLA_STEP(6);
-    else if (rows <= 8) GLA_STEP(8);
-    else GLA_STEP(16);
+    if (rows <= 8) GLA_STEP(8);
+    else if (rows <= 12) GLA_STEP(12);
+    else if (rows <= 16) GLA_STEP(16);
+    else GLA_STEP(32);
 #undef GLA_STEP
     count_launches(1);
     return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
