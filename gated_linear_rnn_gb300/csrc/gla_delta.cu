@@ -181,128 +181,196 @@ int launch_step(const T *q, const T *k, const T *v, const void *g, const void *b
 // ---- token-by-token recurrences -------------------------------------------------------------------------------
 //
 // A warp owns eight columns, four lanes to a column, and each lane kRpl of its dk rows in registers (rows past dk
-// are zero and stay so).  A token costs 3 dk multiply-adds a column and two sums over four lanes.  Blocks of kTok
-// tokens of q, k, v and the gates are staged in shared memory in f32.
-constexpr int kTok = 16;      // tokens staged at once
+// are zero and stay so).  A token costs 3 dk multiply-adds a column and two sums over four lanes, of which the
+// chain from token to token is a quarter of dk multiply-adds and one sum: some 100 clocks, which bounds few chains;
+// many are bound by the multiply-adds.  Blocks of tokens of q, k, v and the gates are staged in shared memory in
+// f32, the next block while one is computed.  Tokens past a sequence's end are staged as k = q = v = 0, beta = 0,
+// decay 1, which leaves the state as it is, so every block runs whole.
 constexpr int kCols = 32;     // columns per block of four warps
 
-template <int kRpl> constexpr int row_words() { return 4 * (kRpl + 4); }  // [4][kRpl + 4]: the lanes' reads meet no bank twice
+template <int kRpl> struct Staged {  // one block of tokens
+    static constexpr int kTok = kRpl > 32 ? 8 : 16;
+    static constexpr int kRow = 4 * (kRpl + 4);  // [4][kRpl + 4]: the lanes' reads meet no bank twice
+    float k[kTok][kRow], q[kTok][kRow], v[kTok][kCols], a[kTok], beta[kTok];
+};
 
-// Rows of [.., dk] into shared memory as [tok][4][kRpl + 4] f32, zero past dk and past the last token.
+__device__ __forceinline__ void copy4(float *dst, const float *src, bool has) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(has ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(float *dst, const __nv_bfloat16 *src, bool has) {
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (has) load4<__nv_bfloat16>(src, x);
+    *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+}
+// rows of [.., dk] of n tokens, zero past dk and past n
 template <typename T, int kRpl>
-__device__ __forceinline__ void stage_rows(float *dst, const T *src, int64_t row, int64_t stride, int n, int dk) {
-    for (int i = threadIdx.x; i < kTok * 4 * kRpl; i += blockDim.x) {
-        const int t = i / (4 * kRpl), r = i % (4 * kRpl);
-        dst[t * row_words<kRpl>() + (r / kRpl) * (kRpl + 4) + r % kRpl] =
-            t < n && r < dk ? to_f32(src[(row + t) * stride + r]) : 0.f;
+__device__ __forceinline__ void stage_rows(float (*dst)[Staged<kRpl>::kRow], const T *src, int64_t row, int64_t stride, int n,
+                                           int dk) {
+#pragma unroll
+    for (int i = threadIdx.x; i < Staged<kRpl>::kTok * kRpl; i += 128) {
+        const int t = i / kRpl, r = i % kRpl * 4;
+        const bool has = t < n && r < dk;
+        copy4(&dst[t][r / kRpl * (kRpl + 4) + r % kRpl], has ? src + (row + t) * stride + r : src, has);
     }
 }
-template <typename T>
-__device__ __forceinline__ void stage_cols(float *dst, const T *src, int64_t row, int64_t stride, int n, int col, int dv) {
-    for (int i = threadIdx.x; i < kTok * kCols; i += blockDim.x) {
-        const int t = i / kCols, c = i % kCols;
-        dst[i] = t < n && col + c < dv ? to_f32(src[(row + t) * stride + c]) : 0.f;
+template <typename T, int kRpl>
+__device__ __forceinline__ void stage(Staged<kRpl> &to, const Shape &p, const T *q, const T *k, const T *v, int64_t row, int n,
+                                      int h, int hk, int col0) {
+    stage_rows<T, kRpl>(to.k, k + (int64_t)hk * p.dk, row, (int64_t)p.Hk * p.dk, n, p.dk);
+    if (q != nullptr) stage_rows<T, kRpl>(to.q, q + (int64_t)hk * p.dk, row, (int64_t)p.Hk * p.dk, n, p.dk);
+    const T *vr = v + (int64_t)h * p.dv + col0;
+#pragma unroll
+    for (int i = threadIdx.x; i < Staged<kRpl>::kTok * kCols / 4; i += 128) {
+        const int t = i / (kCols / 4), c = i % (kCols / 4) * 4;
+        const bool has = t < n && col0 + c < p.dv;
+        copy4(&to.v[t][c], has ? vr + (row + t) * p.H * p.dv + c : v, has);
     }
 }
-template <typename T>
-__device__ __forceinline__ void write_cols(T *dst, const float *src, int64_t row, int64_t stride, int n, int col, int dv) {
-    for (int i = threadIdx.x; i < kTok * kCols; i += blockDim.x) {
-        const int t = i / kCols, c = i % kCols;
-        if (t < n && col + c < dv) dst[(row + t) * stride + c] = from_f32<T>(src[i]);
+// the gates of a block's tokens: their loads before a block is computed, their place in shared memory after
+struct Gates {
+    float a, beta;
+    template <typename T>
+    __device__ __forceinline__ void load(const Shape &p, const void *g, const void *b, int64_t row, int n, int h) {
+        a = 1.f;
+        beta = 0.f;
+        if ((int)threadIdx.x < n) {
+            a = load_gate<T>(g, (row + threadIdx.x) * p.H + h, p.gate_f32);
+            beta = load_gate<T>(b, (row + threadIdx.x) * p.H + h, p.gate_f32);
+        }
     }
-}
+    template <int kRpl> __device__ __forceinline__ void put(Staged<kRpl> &to, int n) const {
+        if (threadIdx.x < Staged<kRpl>::kTok) {
+            to.a[threadIdx.x] = (int)threadIdx.x < n ? expf(a) : 1.f;
+            to.beta[threadIdx.x] = beta;
+        }
+    }
+};
 __device__ __forceinline__ float sum4(float x) {
     x += __shfl_xor_sync(0xffffffffu, x, 1);
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
+// Four lanes with four parts each (one to a token): lane sub gets the sum of part sub.
+__device__ __forceinline__ float sum4_of(const float (&x)[4], int sub) {
+    const bool odd = sub & 1, high = sub & 2;
+    const float a = (odd ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[1], 1);
+    const float b = (odd ? x[3] : x[2]) + __shfl_xor_sync(0xffffffffu, odd ? x[2] : x[3], 1);
+    return (high ? b : a) + __shfl_xor_sync(0xffffffffu, high ? a : b, 2);
+}
+// this lane's part of a row times its part of the state
+template <int kRpl> __device__ __forceinline__ float dot(const float4 *row, const float (&S)[kRpl]) {
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kRpl / 4; ++i) {
+        const float4 r = row[i];
+        x[0] = fmaf(r.x, S[4 * i], x[0]);
+        x[1] = fmaf(r.y, S[4 * i + 1], x[1]);
+        x[2] = fmaf(r.z, S[4 * i + 2], x[2]);
+        x[3] = fmaf(r.w, S[4 * i + 3], x[3]);
+    }
+    return (x[0] + x[1]) + (x[2] + x[3]);
+}
+// S = a S + u row
+template <int kRpl> __device__ __forceinline__ void update(float (&S)[kRpl], float a, float u, const float4 *row) {
+#pragma unroll
+    for (int i = 0; i < kRpl / 4; ++i) {
+        const float4 r = row[i];
+        S[4 * i] = fmaf(a, S[4 * i], r.x * u);
+        S[4 * i + 1] = fmaf(a, S[4 * i + 1], r.y * u);
+        S[4 * i + 2] = fmaf(a, S[4 * i + 2], r.z * u);
+        S[4 * i + 3] = fmaf(a, S[4 * i + 3], r.w * u);
+    }
+}
+
+// Who a thread is, and its part of a state [dk][dv].
+template <int kRpl> struct Lane {
+    int s, h, hk, col0, sub, c;
+    bool live;
+    int64_t chain;
+    __device__ __forceinline__ Lane(const Shape &p) {
+        s = blockIdx.x / p.H;
+        h = blockIdx.x % p.H;
+        hk = h / p.group();
+        col0 = blockIdx.y * kCols;
+        const int lane = threadIdx.x & 31;
+        sub = lane & 3;
+        c = (threadIdx.x >> 5) * 8 + (lane >> 2);
+        live = col0 + c < p.dv;
+        chain = ((int64_t)s * p.H + h) * p.dk * p.dv + col0 + c;
+    }
+    __device__ __forceinline__ void load(float (&S)[kRpl], const float *from, const Shape &p) const {
+#pragma unroll
+        for (int i = 0; i < kRpl; ++i) {
+            const int row = sub * kRpl + i;
+            S[i] = from != nullptr && live && row < p.dk ? from[chain + (int64_t)row * p.dv] : 0.f;
+        }
+    }
+    __device__ __forceinline__ void store(float *to, const float (&S)[kRpl], const Shape &p) const {
+#pragma unroll
+        for (int i = 0; i < kRpl; ++i)
+            if (live && sub * kRpl + i < p.dk) to[(int64_t)(sub * kRpl + i) * p.dv] = S[i];
+    }
+};
 
 // Forward: out (or, for the gradient, the residuals r = v - a k S in f32 and the state before every 64th token).
-template <typename T, int kRpl>
+template <typename T, int kRpl, bool kResid>
 __global__ void __launch_bounds__(128)
 delta_rec_fwd_kernel(Shape p, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
                      const void *__restrict__ g, const void *__restrict__ beta, const float *__restrict__ h0,
                      T *__restrict__ out, float *__restrict__ hT, float *__restrict__ resid, float *__restrict__ states) {
-    __shared__ __align__(16) float ks[kTok * row_words<kRpl>()], qs[kTok * row_words<kRpl>()];
-    __shared__ float vs[kTok * kCols], al[kTok], be[kTok];
-    const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / p.group();
-    const int col0 = blockIdx.y * kCols;
-    const int lane = threadIdx.x & 31, sub = lane & 3, c = (threadIdx.x >> 5) * 8 + (lane >> 2);
-    const bool live = col0 + c < p.dv;
+    using St = Staged<kRpl>;
+    constexpr int kTok = St::kTok;
+    __shared__ __align__(16) St sm[2];
+    const Lane<kRpl> ln(p);
     SeqRange r;
-    if (!seq_range(s, p.T, p.cu, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
-    const int64_t chain = ((int64_t)s * p.H + h) * p.dk * p.dv + col0 + c;
+    if (!seq_range(ln.s, p.T, p.cu, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
     float S[kRpl];
-#pragma unroll
-    for (int i = 0; i < kRpl; ++i) {
-        const int row = sub * kRpl + i;
-        S[i] = h0 != nullptr && live && row < p.dk ? h0[chain + (int64_t)row * p.dv] : 0.f;
+    ln.load(S, h0, p);
+    const int64_t slot0 = r.start / 64 + ln.s;
+    const auto count = [&](int64_t t0) { return (int)(r.len - t0 < kTok ? max(r.len - t0, (int64_t)0) : kTok); };
+    Gates gates;
+    const T *qq = kResid ? nullptr : q;
+    if (r.len > 0) {
+        gates.load<T>(p, g, beta, r.start, count(0), ln.h);
+        stage<T, kRpl>(sm[0], p, qq, k, v, r.start, count(0), ln.h, ln.hk, ln.col0);
+        gates.put(sm[0], count(0));
     }
-    const int64_t slot0 = r.start / 64 + s;
     for (int64_t t0 = 0; t0 < r.len; t0 += kTok) {
-        const int n = (int)(r.len - t0 < kTok ? r.len - t0 : kTok);
+        const St &cur = sm[(t0 / kTok) & 1];
+        St &next = sm[(t0 / kTok + 1) & 1];
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        const int ahead = count(t0 + kTok);
         const int64_t row = r.start + t0;
-        if (states != nullptr && (t0 & 63) == 0) {
-            float *to = states + ((slot0 + t0 / 64) * p.H + h) * p.dk * p.dv + col0 + c;
-#pragma unroll
-            for (int i = 0; i < kRpl; ++i)
-                if (live && sub * kRpl + i < p.dk) to[(int64_t)(sub * kRpl + i) * p.dv] = S[i];
+        if (ahead > 0) {
+            gates.load<T>(p, g, beta, row + kTok, ahead, ln.h);
+            stage<T, kRpl>(next, p, qq, k, v, row + kTok, ahead, ln.h, ln.hk, ln.col0);
         }
-        __syncthreads();  // the last block's outputs have been written from vs
-        stage_rows<T, kRpl>(ks, k + (int64_t)hk * p.dk, row, (int64_t)p.Hk * p.dk, n, p.dk);
-        if (out != nullptr) stage_rows<T, kRpl>(qs, q + (int64_t)hk * p.dk, row, (int64_t)p.Hk * p.dk, n, p.dk);
-        stage_cols(vs, v + (int64_t)h * p.dv + col0, row, (int64_t)p.H * p.dv, n, col0, p.dv);
-        if (threadIdx.x < n) {
-            al[threadIdx.x] = expf(load_gate<T>(g, (row + threadIdx.x) * p.H + h, p.gate_f32));
-            be[threadIdx.x] = load_gate<T>(beta, (row + threadIdx.x) * p.H + h, p.gate_f32);
-        }
-        __syncthreads();
-        for (int t = 0; t < n; ++t) {
-            const float4 *kt = reinterpret_cast<const float4 *>(ks + t * row_words<kRpl>() + sub * (kRpl + 4));
-            const float4 *qt = reinterpret_cast<const float4 *>(qs + t * row_words<kRpl>() + sub * (kRpl + 4));
-            const float a = al[t];
-            float x = 0.f, y = 0.f;
+        if (kResid && (t0 & 63) == 0)
+            ln.store(states + ((slot0 + t0 / 64) * p.H + ln.h) * p.dk * p.dv + ln.col0 + ln.c, S, p);
+#pragma unroll 1
+        for (int t = 0; t < kTok; t += 4) {
+            float x[4];  // q S, summed over the lanes once for the four tokens: off the chain from token to token
 #pragma unroll
-            for (int i = 0; i < kRpl / 4; ++i) {
-                const float4 kk = kt[i];
-                x = fmaf(kk.x, S[4 * i], x); y = fmaf(kk.y, S[4 * i + 1], y);
-                x = fmaf(kk.z, S[4 * i + 2], x); y = fmaf(kk.w, S[4 * i + 3], y);
+            for (int u = 0; u < 4; ++u) {
+                const float4 *kt = reinterpret_cast<const float4 *>(cur.k[t + u] + ln.sub * (kRpl + 4));
+                const float a = cur.a[t + u];
+                const float res = cur.v[t + u][ln.c] - a * sum4(dot<kRpl>(kt, S));
+                update<kRpl>(S, a, cur.beta[t + u] * res, kt);
+                x[u] = kResid ? res : dot<kRpl>(reinterpret_cast<const float4 *>(cur.q[t + u] + ln.sub * (kRpl + 4)), S);
             }
-            const float res = vs[t * kCols + c] - a * sum4(x + y);
-            const float u = be[t] * res;
-            x = y = 0.f;
-            if (out != nullptr) {
-#pragma unroll
-                for (int i = 0; i < kRpl / 4; ++i) {
-                    const float4 kk = kt[i], qq = qt[i];
-                    S[4 * i] = fmaf(a, S[4 * i], kk.x * u); x = fmaf(qq.x, S[4 * i], x);
-                    S[4 * i + 1] = fmaf(a, S[4 * i + 1], kk.y * u); y = fmaf(qq.y, S[4 * i + 1], y);
-                    S[4 * i + 2] = fmaf(a, S[4 * i + 2], kk.z * u); x = fmaf(qq.z, S[4 * i + 2], x);
-                    S[4 * i + 3] = fmaf(a, S[4 * i + 3], kk.w * u); y = fmaf(qq.w, S[4 * i + 3], y);
-                }
-                x = sum4(x + y);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kRpl / 4; ++i) {
-                    const float4 kk = kt[i];
-                    S[4 * i] = fmaf(a, S[4 * i], kk.x * u);
-                    S[4 * i + 1] = fmaf(a, S[4 * i + 1], kk.y * u);
-                    S[4 * i + 2] = fmaf(a, S[4 * i + 2], kk.z * u);
-                    S[4 * i + 3] = fmaf(a, S[4 * i + 3], kk.w * u);
-                }
-                x = res;
+            // this lane writes token t + sub of its column
+            const float keep = kResid ? (ln.sub & 2 ? (ln.sub & 1 ? x[3] : x[2]) : (ln.sub & 1 ? x[1] : x[0])) : sum4_of(x, ln.sub);
+            const int64_t tok = t0 + t + ln.sub;
+            if (tok < r.len && ln.live) {
+                const int64_t at = ((r.start + tok) * p.H + ln.h) * p.dv + ln.col0 + ln.c;
+                if (kResid) resid[at] = keep;
+                else out[at] = from_f32<T>(keep);
             }
-            __syncwarp();
-            if (sub == 0) vs[t * kCols + c] = x;  // a column's v is read by its own four lanes only
         }
-        __syncthreads();
-        if (out != nullptr) write_cols(out + (int64_t)h * p.dv + col0, vs, row, (int64_t)p.H * p.dv, n, col0, p.dv);
-        else write_cols(resid + (int64_t)h * p.dv + col0, vs, row, (int64_t)p.H * p.dv, n, col0, p.dv);
+        if (ahead > 0) gates.put(next, ahead);
     }
-    if (hT != nullptr && live) {
-#pragma unroll
-        for (int i = 0; i < kRpl; ++i)
-            if (sub * kRpl + i < p.dk) hT[chain + (int64_t)(sub * kRpl + i) * p.dv] = S[i];
-    }
+    if (hT != nullptr) ln.store(hT + ln.chain, S, p);
 }
 
 // Backward in time.  dS is the gradient with respect to the state after token t:
@@ -313,81 +381,59 @@ __global__ void __launch_bounds__(128)
 delta_rec_bwd_kernel(Shape p, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ dout,
                      const void *__restrict__ g, const void *__restrict__ beta, const float *__restrict__ dhT,
                      T *__restrict__ dv, float *__restrict__ ys, float *__restrict__ states, float *__restrict__ dh0) {
-    __shared__ __align__(16) float ks[kTok * row_words<kRpl>()], qs[kTok * row_words<kRpl>()];
-    __shared__ float vs[kTok * kCols], al[kTok], be[kTok];
-    const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / p.group();
-    const int col0 = blockIdx.y * kCols;
-    const int lane = threadIdx.x & 31, sub = lane & 3, c = (threadIdx.x >> 5) * 8 + (lane >> 2);
-    const bool live = col0 + c < p.dv;
+    using St = Staged<kRpl>;
+    constexpr int kTok = St::kTok;
+    __shared__ __align__(16) St sm[2];
+    const Lane<kRpl> ln(p);
     SeqRange r;
-    if (!seq_range(s, p.T, p.cu, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
-    const int64_t chain = ((int64_t)s * p.H + h) * p.dk * p.dv + col0 + c;
+    if (!seq_range(ln.s, p.T, p.cu, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
     float S[kRpl];
-#pragma unroll
-    for (int i = 0; i < kRpl; ++i) {
-        const int row = sub * kRpl + i;
-        S[i] = dhT != nullptr && live && row < p.dk ? dhT[chain + (int64_t)row * p.dv] : 0.f;
+    ln.load(S, dhT, p);
+    const int64_t slot0 = r.start / 64 + ln.s, last = r.len > 0 ? (r.len - 1) / kTok * kTok : -1;
+    Gates gates;
+    if (last >= 0) {
+        const int n = (int)(r.len - last);
+        gates.load<T>(p, g, beta, r.start + last, n, ln.h);
+        stage<T, kRpl>(sm[(last / kTok) & 1], p, q, k, dout, r.start + last, n, ln.h, ln.hk, ln.col0);
+        gates.put(sm[(last / kTok) & 1], n);
     }
-    const int64_t slot0 = r.start / 64 + s;
-    for (int64_t t0 = r.len > 0 ? (r.len - 1) / kTok * kTok : -1; t0 >= 0; t0 -= kTok) {
-        const int n = (int)(r.len - t0 < kTok ? r.len - t0 : kTok);
+    for (int64_t t0 = last; t0 >= 0; t0 -= kTok) {
+        const St &cur = sm[(t0 / kTok) & 1];
+        St &next = sm[(t0 / kTok + 1) & 1];
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
         const int64_t row = r.start + t0;
-        if (((t0 + kTok) & 63) == 0 || t0 + kTok >= r.len) {
-            float *to = states + ((slot0 + t0 / 64) * p.H + h) * p.dk * p.dv + col0 + c;
-#pragma unroll
-            for (int i = 0; i < kRpl; ++i)
-                if (live && sub * kRpl + i < p.dk) to[(int64_t)(sub * kRpl + i) * p.dv] = S[i];
+        if (t0 > 0) {  // every block before the last is whole
+            gates.load<T>(p, g, beta, row - kTok, kTok, ln.h);
+            stage<T, kRpl>(next, p, q, k, dout, row - kTok, kTok, ln.h, ln.hk, ln.col0);
         }
-        __syncthreads();
-        stage_rows<T, kRpl>(ks, k + (int64_t)hk * p.dk, row, (int64_t)p.Hk * p.dk, n, p.dk);
-        stage_rows<T, kRpl>(qs, q + (int64_t)hk * p.dk, row, (int64_t)p.Hk * p.dk, n, p.dk);
-        stage_cols(vs, dout + (int64_t)h * p.dv + col0, row, (int64_t)p.H * p.dv, n, col0, p.dv);
-        if (threadIdx.x < n) {
-            al[threadIdx.x] = expf(load_gate<T>(g, (row + threadIdx.x) * p.H + h, p.gate_f32));
-            be[threadIdx.x] = load_gate<T>(beta, (row + threadIdx.x) * p.H + h, p.gate_f32);
-        }
-        __syncthreads();
-        for (int t = n - 1; t >= 0; --t) {
-            const float4 *kt = reinterpret_cast<const float4 *>(ks + t * row_words<kRpl>() + sub * (kRpl + 4));
-            const float4 *qt = reinterpret_cast<const float4 *>(qs + t * row_words<kRpl>() + sub * (kRpl + 4));
-            const float a = al[t], d = vs[t * kCols + c];
-            float x = 0.f, y = 0.f;
+        if (((t0 + kTok) & 63) == 0 || t0 == last)
+            ln.store(states + ((slot0 + t0 / 64) * p.H + ln.h) * p.dk * p.dv + ln.col0 + ln.c, S, p);
+#pragma unroll 1
+        for (int t = kTok - 4; t >= 0; t -= 4) {
+            float keep = 0.f, b = 0.f;
 #pragma unroll
-            for (int i = 0; i < kRpl / 4; ++i) {
-                const float4 kk = kt[i], qq = qt[i];
-                S[4 * i] = fmaf(qq.x, d, S[4 * i]); x = fmaf(kk.x, S[4 * i], x);
-                S[4 * i + 1] = fmaf(qq.y, d, S[4 * i + 1]); y = fmaf(kk.y, S[4 * i + 1], y);
-                S[4 * i + 2] = fmaf(qq.z, d, S[4 * i + 2]); x = fmaf(kk.z, S[4 * i + 2], x);
-                S[4 * i + 3] = fmaf(qq.w, d, S[4 * i + 3]); y = fmaf(kk.w, S[4 * i + 3], y);
+            for (int u = 3; u >= 0; --u) {
+                const float4 *kt = reinterpret_cast<const float4 *>(cur.k[t + u] + ln.sub * (kRpl + 4));
+                const float a = cur.a[t + u], be = cur.beta[t + u];
+                update<kRpl>(S, 1.f, cur.v[t + u][ln.c], reinterpret_cast<const float4 *>(cur.q[t + u] + ln.sub * (kRpl + 4)));
+                const float y = sum4(dot<kRpl>(kt, S));
+                update<kRpl>(S, a, -a * (be * y), kt);
+                if (ln.sub == u) {
+                    keep = y;
+                    b = be;
+                }
             }
-            x = sum4(x + y);
-            const float w = be[t] * x;
-#pragma unroll
-            for (int i = 0; i < kRpl / 4; ++i) {
-                const float4 kk = kt[i];
-                S[4 * i] = a * fmaf(-kk.x, w, S[4 * i]);
-                S[4 * i + 1] = a * fmaf(-kk.y, w, S[4 * i + 1]);
-                S[4 * i + 2] = a * fmaf(-kk.z, w, S[4 * i + 2]);
-                S[4 * i + 3] = a * fmaf(-kk.w, w, S[4 * i + 3]);
-            }
-            __syncwarp();
-            if (sub == 0) vs[t * kCols + c] = x;
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < n * kCols; i += blockDim.x) {
-            const int t = i / kCols, cc = i % kCols;
-            if (col0 + cc < p.dv) {
-                const int64_t at = ((row + t) * p.H + h) * p.dv + col0 + cc;
-                ys[at] = vs[i];
-                dv[at] = from_f32<T>(be[t] * vs[i]);
+            const int64_t tok = t0 + t + ln.sub;
+            if (tok < r.len && ln.live) {
+                const int64_t at = ((r.start + tok) * p.H + ln.h) * p.dv + ln.col0 + ln.c;
+                ys[at] = keep;
+                dv[at] = from_f32<T>(b * keep);
             }
         }
+        if (t0 > 0) gates.put(next, kTok);
     }
-    if (dh0 != nullptr && live) {
-#pragma unroll
-        for (int i = 0; i < kRpl; ++i)
-            if (sub * kRpl + i < p.dk) dh0[chain + (int64_t)(sub * kRpl + i) * p.dv] = S[i];
-    }
+    if (dh0 != nullptr) ln.store(dh0 + ln.chain, S, p);
 }
 
 // ---- gradient of the shared inputs ------------------------------------------------------------------------------
@@ -597,12 +643,16 @@ int check_launch(int n) {
         else { CALL(64); }         \
     } while (0)
 
+// out null: the residuals and states instead
 template <typename T>
 int rec_fwd(const Shape &p, const T *q, const T *k, const T *v, const void *g, const void *beta, const float *h0,
             T *out, float *hT, float *resid, float *states, cudaStream_t st) {
     const dim3 grid((unsigned)((long long)p.nseq * p.H), (unsigned)((p.dv + kCols - 1) / kCols));
-#define GLA_CALL(R) \
-    delta_rec_fwd_kernel<T, R><<<grid, 128, 0, st>>>(p, q, k, v, g, beta, h0, out, hT, resid, states)
+#define GLA_CALL(R)                                                                                                \
+    if (states == nullptr)                                                                                         \
+        delta_rec_fwd_kernel<T, R, false><<<grid, 128, 0, st>>>(p, q, k, v, g, beta, h0, out, hT, resid, states);   \
+    else                                                                                                           \
+        delta_rec_fwd_kernel<T, R, true><<<grid, 128, 0, st>>>(p, q, k, v, g, beta, h0, out, hT, resid, states)
     GLA_BY_ROWS(p.dk, GLA_CALL);
 #undef GLA_CALL
     return check_launch(1);
