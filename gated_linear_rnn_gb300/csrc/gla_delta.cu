@@ -6,6 +6,7 @@
 // Every column of S (one of the dv) obeys this map by itself: only k, q, a and beta are shared.  So the
 // columns of a chain are split over threads, warps and blocks without any exchange between them.
 #include "gla_delta.cuh"
+#include "gla_pairs.cuh"
 
 GLA_DEFINE_STATUS(delta)
 
@@ -257,28 +258,39 @@ __device__ __forceinline__ float sum4_of(const float (&x)[4], int sub) {
     const float b = (odd ? x[3] : x[2]) + __shfl_xor_sync(0xffffffffu, odd ? x[2] : x[3], 1);
     return (high ? b : a) + __shfl_xor_sync(0xffffffffu, high ? a : b, 2);
 }
+// two pairs of a staged row
+struct Pairs2 { Pair a, b; };
+__device__ __forceinline__ Pairs2 pairs_at(const float4 *row, int i) {
+    const ulonglong2 t = reinterpret_cast<const ulonglong2 *>(row)[i];
+    return {{t.x}, {t.y}};
+}
 // this lane's part of a row times its part of the state
-template <int kRpl> __device__ __forceinline__ float dot(const float4 *row, const float (&S)[kRpl]) {
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
+template <int kRpl> __device__ __forceinline__ float dot(const float4 *row, const Pair (&S)[kRpl / 2]) {
+    Pair x = both(0.f), y = both(0.f);
 #pragma unroll
     for (int i = 0; i < kRpl / 4; ++i) {
-        const float4 r = row[i];
-        x[0] = fmaf(r.x, S[4 * i], x[0]);
-        x[1] = fmaf(r.y, S[4 * i + 1], x[1]);
-        x[2] = fmaf(r.z, S[4 * i + 2], x[2]);
-        x[3] = fmaf(r.w, S[4 * i + 3], x[3]);
+        const Pairs2 r = pairs_at(row, i);
+        x = fma(r.a, S[2 * i], x);
+        y = fma(r.b, S[2 * i + 1], y);
     }
-    return (x[0] + x[1]) + (x[2] + x[3]);
+    return total(x + y);
 }
 // S = a S + u row
-template <int kRpl> __device__ __forceinline__ void update(float (&S)[kRpl], float a, float u, const float4 *row) {
+template <int kRpl> __device__ __forceinline__ void update(Pair (&S)[kRpl / 2], Pair a, Pair u, const float4 *row) {
 #pragma unroll
     for (int i = 0; i < kRpl / 4; ++i) {
-        const float4 r = row[i];
-        S[4 * i] = fmaf(a, S[4 * i], r.x * u);
-        S[4 * i + 1] = fmaf(a, S[4 * i + 1], r.y * u);
-        S[4 * i + 2] = fmaf(a, S[4 * i + 2], r.z * u);
-        S[4 * i + 3] = fmaf(a, S[4 * i + 3], r.w * u);
+        const Pairs2 r = pairs_at(row, i);
+        S[2 * i] = fma(a, S[2 * i], r.a * u);
+        S[2 * i + 1] = fma(a, S[2 * i + 1], r.b * u);
+    }
+}
+// S = S + u row
+template <int kRpl> __device__ __forceinline__ void add(Pair (&S)[kRpl / 2], Pair u, const float4 *row) {
+#pragma unroll
+    for (int i = 0; i < kRpl / 4; ++i) {
+        const Pairs2 r = pairs_at(row, i);
+        S[2 * i] = fma(r.a, u, S[2 * i]);
+        S[2 * i + 1] = fma(r.b, u, S[2 * i + 1]);
     }
 }
 
@@ -298,17 +310,24 @@ template <int kRpl> struct Lane {
         live = col0 + c < p.dv;
         chain = ((int64_t)s * p.H + h) * p.dk * p.dv + col0 + c;
     }
-    __device__ __forceinline__ void load(float (&S)[kRpl], const float *from, const Shape &p) const {
+    __device__ __forceinline__ void load(Pair (&S)[kRpl / 2], const float *from, const Shape &p) const {
 #pragma unroll
-        for (int i = 0; i < kRpl; ++i) {
-            const int row = sub * kRpl + i;
-            S[i] = from != nullptr && live && row < p.dk ? from[chain + (int64_t)row * p.dv] : 0.f;
+        for (int i = 0; i < kRpl / 2; ++i) {
+            const int row = sub * kRpl + 2 * i;  // dk is even: a pair is whole or absent
+            const bool has = from != nullptr && live && row < p.dk;
+            S[i] = has ? pair(from[chain + (int64_t)row * p.dv], from[chain + (int64_t)(row + 1) * p.dv]) : both(0.f);
         }
     }
-    __device__ __forceinline__ void store(float *to, const float (&S)[kRpl], const Shape &p) const {
+    __device__ __forceinline__ void store(float *to, const Pair (&S)[kRpl / 2], const Shape &p) const {
 #pragma unroll
-        for (int i = 0; i < kRpl; ++i)
-            if (live && sub * kRpl + i < p.dk) to[(int64_t)(sub * kRpl + i) * p.dv] = S[i];
+        for (int i = 0; i < kRpl / 2; ++i) {
+            const int row = sub * kRpl + 2 * i;
+            if (live && row < p.dk) {
+                const float2 f = parts(S[i]);
+                to[(int64_t)row * p.dv] = f.x;
+                to[(int64_t)(row + 1) * p.dv] = f.y;
+            }
+        }
     }
 };
 
@@ -324,7 +343,7 @@ delta_rec_fwd_kernel(Shape p, const T *__restrict__ q, const T *__restrict__ k, 
     const Lane<kRpl> ln(p);
     SeqRange r;
     if (!seq_range(ln.s, p.T, p.cu, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
-    float S[kRpl];
+    Pair S[kRpl / 2];
     ln.load(S, h0, p);
     const int64_t slot0 = r.start / 64 + ln.s;
     const auto count = [&](int64_t t0) { return (int)(r.len - t0 < kTok ? max(r.len - t0, (int64_t)0) : kTok); };
@@ -356,7 +375,7 @@ delta_rec_fwd_kernel(Shape p, const T *__restrict__ q, const T *__restrict__ k, 
                 const float4 *kt = reinterpret_cast<const float4 *>(cur.k[t + u] + ln.sub * (kRpl + 4));
                 const float a = cur.a[t + u];
                 const float res = cur.v[t + u][ln.c] - a * sum4(dot<kRpl>(kt, S));
-                update<kRpl>(S, a, cur.beta[t + u] * res, kt);
+                update<kRpl>(S, both(a), both(cur.beta[t + u] * res), kt);
                 x[u] = kResid ? res : dot<kRpl>(reinterpret_cast<const float4 *>(cur.q[t + u] + ln.sub * (kRpl + 4)), S);
             }
             // this lane writes token t + sub of its column
@@ -387,7 +406,7 @@ delta_rec_bwd_kernel(Shape p, const T *__restrict__ q, const T *__restrict__ k, 
     const Lane<kRpl> ln(p);
     SeqRange r;
     if (!seq_range(ln.s, p.T, p.cu, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
-    float S[kRpl];
+    Pair S[kRpl / 2];
     ln.load(S, dhT, p);
     const int64_t slot0 = r.start / 64 + ln.s, last = r.len > 0 ? (r.len - 1) / kTok * kTok : -1;
     Gates gates;
@@ -416,9 +435,9 @@ delta_rec_bwd_kernel(Shape p, const T *__restrict__ q, const T *__restrict__ k, 
             for (int u = 3; u >= 0; --u) {
                 const float4 *kt = reinterpret_cast<const float4 *>(cur.k[t + u] + ln.sub * (kRpl + 4));
                 const float a = cur.a[t + u], be = cur.beta[t + u];
-                update<kRpl>(S, 1.f, cur.v[t + u][ln.c], reinterpret_cast<const float4 *>(cur.q[t + u] + ln.sub * (kRpl + 4)));
+                add<kRpl>(S, both(cur.v[t + u][ln.c]), reinterpret_cast<const float4 *>(cur.q[t + u] + ln.sub * (kRpl + 4)));
                 const float y = sum4(dot<kRpl>(kt, S));
-                update<kRpl>(S, a, -a * (be * y), kt);
+                update<kRpl>(S, both(a), both(-a * (be * y)), kt);
                 if (ln.sub == u) {
                     keep = y;
                     b = be;

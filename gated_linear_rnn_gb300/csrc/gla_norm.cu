@@ -15,7 +15,7 @@
 // lanes of a group.  The next token's vectors are on their way while one is computed.  The gradient does some
 // thirty operations an element, so arithmetic runs on pairs of f32 (fma.rn.f32x2 and the like).  The blocks' sums of dweight
 // and dbias go to a workspace that a second kernel adds up in a fixed order.
-#include "gla_common.cuh"
+#include "gla_pairs.cuh"
 
 namespace gla {
 namespace norm {
@@ -24,39 +24,6 @@ namespace {
 constexpr int kThreads = 256;
 
 enum Act { kNone = GLA_ACT_NONE, kSilu = GLA_ACT_SILU, kSigmoid = GLA_ACT_SIGMOID };
-
-// ---- pairs of f32 ----------------------------------------------------------------------------------------------
-struct Pair { unsigned long long v; };
-__device__ __forceinline__ Pair pair(float a, float b) {
-    Pair p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b));
-    return p;
-}
-__device__ __forceinline__ Pair both(float a) { return pair(a, a); }
-__device__ __forceinline__ float2 parts(Pair p) {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p.v));
-    return f;
-}
-__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
-    Pair p;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
-    return p;
-}
-__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
-    Pair p;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
-    return p;
-}
-__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
-    Pair p;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return p;
-}
-__device__ __forceinline__ float total(Pair p) {
-    const float2 f = parts(p);
-    return f.x + f.y;
-}
 
 // q = 1 / (1 + e^-x) and rest = 1 - q, each to a few units in its last place: rest is e^-x q (1 - q would leave 2^-24
 // of one where q is near 1, which SiLU's slope multiplies by x).  Below x = -80 q stays at e^-80: the product
