@@ -99,7 +99,7 @@ __device__ __forceinline__ void walk_again(const Shape &p, const Walk &w, unsign
     const int64_t slot64 = f.r.start / kG + f.s;
     const bool live = col < p.dv;
     float S[2 * KT][4];
-    load_state<KT>(S, h0, p, f.chain, col, lane);
+    load_state<KT>(S, h0, f.walk, p.dk, p.dv, col, lane);
     for (int c = 0; c < f.nch; ++c) {
         const int sg = c % w.stages;
         if (!warp_wait(f.full + 8 * sg, (c / w.stages) & 1, f.abort_flag)) {
@@ -182,7 +182,7 @@ __device__ __forceinline__ void walk_back(const Shape &p, const Walk &w, unsigne
     const int64_t slot64 = f.r.start / kG + f.s;
     const bool live = col < p.dv;
     float S[2 * KT][4];
-    load_state<KT>(S, dhT, p, f.chain, col, lane);
+    load_state<KT>(S, dhT, f.walk, p.dk, p.dv, col, lane);
     for (int i = 0; i < f.nch; ++i) {
         const int c = f.nch - 1 - i, sg = i % w.stages;
         if (!warp_wait(f.full + 8 * sg, (i / w.stages) & 1, f.abort_flag)) {
@@ -256,7 +256,7 @@ __device__ __forceinline__ void walk_back(const Shape &p, const Walk &w, unsigne
         write_tile(ys, Y, p, f, c, col, tile);
         write_tile(dv, D, p, f, c, col, tile);
     }
-    if (dh0 != nullptr) store_state<KT>(dh0, S, p, f.chain, col, lane);
+    if (dh0 != nullptr) store_state<KT>(dh0, S, f.walk, p.dk, p.dv, col, lane);
 }
 
 struct WalkArgs {
@@ -795,9 +795,11 @@ int bwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
            float *dh0, char *ws, cudaStream_t st) {
     const Workspace at = workspace_kt<KT>(p);
     const long long rows = total_rows(p), slots = chunk_slots(rows, p.nseq, kG);
-    const Walk wa = make_walk<KT, AgainRecord>(p, false), wb = make_walk<KT, BwdRecord>(p, true);
+    const long long chains = (long long)p.nseq * p.H;
+    const int tiles = (p.dv + 15) / 16;
+    const Walk wa = make_walk<KT, AgainRecord>(chains, tiles, false), wb = make_walk<KT, BwdRecord>(chains, tiles, true);
     const int grad_bytes = GradPlan<KT>::kTotal;
-    const long long blocks = (long long)p.nseq * p.H * wa.splits;
+    const long long blocks = chains * wa.splits;
     if (2 * blocks > 0x7fffffffLL || slots * p.H > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
     const int walks_bytes = max(walk_bytes(wa), walk_bytes(wb));
     if (!allow_smem<delta_walks_kernel<KT>>() || !allow_smem<delta_grad_kernel<KT>>())

@@ -225,27 +225,49 @@ delta_prep_kernel(Shape p, unsigned units, const bf16 *__restrict__ q, const bf1
 
 // ---- the walk ---------------------------------------------------------------------------------------------------
 
-template <int KT>
+// kSegment: a segment's part of the map S -> M S + N alone, from zero: its first tiles carry N (the state that v leaves,
+// from a zero state), the others M (from the identity, with v = 0: a column past dv is staged as zero).
+struct FwdArgs {
+    const bf16 *q, *k, *v;
+    const FwdRecord *records;
+    const float *h0;       // [nseq, H, dk, dv] or null
+    const float *starts;   // with segments: the state before each, [slots, H, dk, dv]
+    bf16 *out;
+    float *hT;
+    float *N, *M;          // [slots, H, dk, dv], [slots, H, dk, dk]
+};
+
+template <int KT, bool kSegment>
 __global__ void __launch_bounds__(kMaxThreads)
-delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16 *__restrict__ v,
-                 const FwdRecord *__restrict__ records, const float *__restrict__ h0, bf16 *__restrict__ out,
-                 float *__restrict__ hT) {
+delta_fwd_kernel(Shape p, Walk w, FwdArgs a) {
     extern __shared__ __align__(128) char sm_raw[];
-    constexpr int kRow = row_bytes<KT>(), kTile = kC * kRow;
+    constexpr int kRow = row_bytes<KT>(), kTile = kC * kRow, kV = (kSegment ? 1 : 2) * kTile;
     const Frame f(p, w, blockIdx.x, sm_raw);
     if (f.bad && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
+    if (!f.exists || (kSegment && f.last)) return;  // nothing starts where a sequence ends
     if (f.warp >= w.groups * 4) {
         give_registers();
-        fetch<KT, true, false>(p, w, f, q, k, v, records);
+        fetch<KT, !kSegment, false>(p, w, f, a.q, a.k, a.v, a.records);
         return;
     }
     take_registers();
     if (f.warp >= w.warps) return;
     const int lane = f.lane, tg = lane & 3, m8 = lane >> 3, r8 = lane & 7;
     const int col = f.col0 + f.warp * 16;
+    const int mcol = col - (p.dv + 15) / 16 * 16;  // kSegment: column of M, or negative
     const uint32_t o_tile = f.outs + f.warp * kC * kOutRow;
     float S[2 * KT][4];
-    load_state<KT>(S, h0, p, f.chain, col, lane);
+    if (kSegment) {
+#pragma unroll
+        for (int n = 0; n < 2 * KT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                S[n][e] = mcol >= 0 && n * 8 + 2 * tg + (e & 1) == mcol + (lane >> 2) + (e >> 1) * 8 ? 1.f : 0.f;
+    } else if (w.segment) {
+        load_state<KT>(S, a.starts, f.walk, p.dk, p.dv, col, lane);
+    } else {
+        load_state<KT>(S, a.h0, f.walk, p.dk, p.dv, col, lane);
+    }
     for (int c = 0; c < f.nch; ++c) {
         const int sg = c % w.stages;
         if (!warp_wait(f.full + 8 * sg, (c / w.stages) & 1, f.abort_flag)) {
@@ -255,8 +277,8 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
             }
             return;
         }
-        const uint32_t ks = f.ring + sg * w.stage_bytes, qs = ks + kTile, vs = qs + kTile + f.warp * 32,
-                       rec = qs + kTile + kC * w.vrow;
+        const uint32_t ks = f.ring + sg * w.stage_bytes, qs = ks + kTile, vs = ks + kV + f.warp * 32,
+                       rec = ks + kV + kC * w.vrow;
         const uint32_t vec = rec + (uint32_t)offsetof(FwdRecord, c) + 8 * tg;
         // Y = S^T K^T
         float Y[4][4] = {};
@@ -328,6 +350,7 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
             split(R[n][2] * db.x, R[n][3] * db.y, uh[t][u + 1], ul[t][u + 1]);
         }
         float O[4][4] = {};
+        if (!kSegment) {
 #pragma unroll
         for (int i = 0; i < KT; ++i) {
             uint32_t a[4];
@@ -348,6 +371,7 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
             const uint4 pp = lds128(rec + 4096 + n * 512 + lane * 16);
             mma(O[n], rh[0], pp.x, pp.y);
             if (n >= 2) mma(O[n], rh[1], pp.z, pp.w);
+        }
         }
         // S^T = c_31 S^T + U K
         const float last = lds_f2(rec + (uint32_t)offsetof(FwdRecord, c) + 8 * 15).y;
@@ -371,9 +395,108 @@ delta_fwd_kernel(Shape p, Walk w, const bf16 *__restrict__ q, const bf16 *__rest
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(f.empty + 8 * sg);
-        write_tile(out, O, p, f, c, col, o_tile);
+        if (!kSegment) write_tile(a.out, O, p, f, c, col, o_tile);
     }
-    if (hT != nullptr) store_state<KT>(hT, S, p, f.chain, col, lane);
+    if (kSegment) {
+        if (mcol < 0) store_state<KT>(a.N, S, f.walk, p.dk, p.dv, col, lane);
+        else store_state<KT>(a.M, S, f.walk, p.dk, p.dk, mcol, lane);
+    } else if (a.hT != nullptr && f.last) {
+        store_state<KT>(a.hT, S, (int64_t)f.s * p.H + f.h, p.dk, p.dv, col, lane);
+    }
+}
+
+// The state before every segment of a chain, S_{i+1} = M_i S_i + N_i from h0, for 32 columns of a head: 256 threads, a
+// column and an eighth of the rows each; M's rows come through shared memory, the state stays there.  A sequence
+// without tokens (or with bad offsets) has no segments: its final state is written here.
+constexpr int kJoinCols = 32;
+__global__ void __launch_bounds__(256)
+delta_join_kernel(Shape p, int segment, const float *__restrict__ M, const float *__restrict__ N,
+                  const float *__restrict__ h0, float *__restrict__ starts, float *__restrict__ hT) {
+    __shared__ float S[128][kJoinCols];
+    __shared__ __align__(16) float m[8][128];
+    const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, col = blockIdx.y * kJoinCols + (threadIdx.x & 31);
+    const int part = threadIdx.x >> 5;
+    const bool live = col < p.dv;
+    SeqRange r;
+    if (!seq_range(s, p.T, p.cu, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
+    const int64_t slot0 = r.start / segment + s;
+    const int n = (int)((r.len + segment - 1) / segment);
+    const int64_t h_at = ((int64_t)s * p.H + h) * p.dk * p.dv + col;
+    if (n == 0) {
+        if (hT != nullptr && live)
+            for (int i = part; i < p.dk; i += 8) hT[h_at + (int64_t)i * p.dv] = h0 != nullptr ? h0[h_at + (int64_t)i * p.dv] : 0.f;
+        return;
+    }
+    for (int i = part; i < p.dk; i += 8) S[i][threadIdx.x & 31] = live && h0 != nullptr ? h0[h_at + (int64_t)i * p.dv] : 0.f;
+    for (int g = 0; g < n; ++g) {
+        const int64_t at = (slot0 + g) * p.H + h;
+        float next[16] = {};  // rows part, part + 8, ...
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+            const int i = x * 8 + part;
+            if (i < p.dk && live) {
+                starts[at * p.dk * p.dv + (int64_t)i * p.dv + col] = S[i][threadIdx.x & 31];
+                if (g + 1 < n) next[x] = N[at * p.dk * p.dv + (int64_t)i * p.dv + col];
+            }
+        }
+        if (g + 1 == n) break;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+            if (x * 8 >= p.dk) break;
+            __syncwarp();  // a warp's row of M: row x * 8 + part
+            for (int j = threadIdx.x & 31; j < p.dk; j += 32)
+                m[part][j] = x * 8 + part < p.dk ? M[at * p.dk * p.dk + (int64_t)(x * 8 + part) * p.dk + j] : 0.f;
+            __syncwarp();
+            float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+            for (int j = 0; j < p.dk; j += 4) {
+                const float4 t = *reinterpret_cast<const float4 *>(&m[part][j]);
+                a0 = fmaf(t.x, S[j][threadIdx.x & 31], a0);
+                a1 = fmaf(t.y, S[j + 1][threadIdx.x & 31], a1);
+                a2 = fmaf(t.z, S[j + 2][threadIdx.x & 31], a2);
+                a3 = fmaf(t.w, S[j + 3][threadIdx.x & 31], a3);
+            }
+            next[x] += (a0 + a1) + (a2 + a3);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+            const int i = x * 8 + part;
+            if (i < p.dk) S[i][threadIdx.x & 31] = next[x];
+        }
+    }
+}
+
+// Tokens per segment, or 0 for whole chains.  A walk is one product after another, so few chains leave most of the
+// GPU idle: B1 T32768 H16 dk96 dv192 took 1,416 us as 16 chains.  Segments cost their map first (dk more columns than
+// dv, without the output: some 1.2 walks), which pays off from about six of them on; so chains are cut where a
+// sixth of the GPU's column tiles (12 to an SM) would do for all of them, into as many segments as fill it, none
+// shorter than 256 tokens, where that makes four of a sequence (of a packed batch, whose lengths only the device
+// knows, four in all: a sequence of one segment costs nothing more).
+int segment_tokens(const Shape &p) {
+    const long long rows = total_rows(p), tiles = (p.dv + 15) / 16, chains = (long long)p.nseq * p.H;
+    const long long room = (long long)device_info().sm_count * kMaxWarps;
+    if (rows == 0 || chains * tiles * 6 > room) return 0;
+    const long long segments = max(1LL, room / (p.H * tiles));
+    const long long tokens = max(256LL, (rows + segments - 1) / segments);
+    if (rows < 4 * tokens * (p.cu ? 1 : p.nseq)) return 0;
+    return (int)((tokens + kC - 1) / kC * kC);
+}
+struct Segments {
+    int tokens;
+    size_t slots, M, N, starts, total;  // offsets in bytes
+};
+Segments plan_segments(const Shape &p) {
+    Segments g{};
+    g.tokens = segment_tokens(p);
+    if (g.tokens == 0) return g;
+    g.slots = (size_t)chunk_slots(total_rows(p), p.nseq, g.tokens);
+    const size_t n = g.slots * p.H * p.dk * sizeof(float);
+    g.M = 0;
+    g.N = (n * p.dk + 255) / 256 * 256;
+    g.starts = g.N + (n * p.dv + 255) / 256 * 256;
+    g.total = g.starts + n * p.dv;
+    return g;
 }
 
 template <int KT, bool kGrad>
@@ -388,17 +511,32 @@ int launch_prep(const Shape &p, const bf16 *q, const bf16 *k, const void *g, con
     return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
 }
 
+size_t record_bytes(const Shape &p) {
+    return ((size_t)chunk_slots(total_rows(p), p.nseq, kC) * p.H * sizeof(FwdRecord) + 255) / 256 * 256;
+}
+
 template <int KT>
 int fwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const void *g, const void *beta,
-           const float *h0, bf16 *out, float *hT, FwdRecord *records, cudaStream_t st) {
-    const Walk w = make_walk<KT, FwdRecord>(p, true);
-    const long long blocks = (long long)p.nseq * p.H * w.splits;
-    if (blocks > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
-    if (!allow_smem<delta_fwd_kernel<KT>>()) return GLA_ERR_LAUNCH;
+           const float *h0, bf16 *out, float *hT, char *ws, cudaStream_t st) {
+    const Segments sg = plan_segments(p);
+    const int tiles = (p.dv + 15) / 16;
+    const long long walks = sg.tokens ? (long long)sg.slots * p.H : (long long)p.nseq * p.H;
+    Walk w = make_walk<KT, FwdRecord>(walks, tiles, true), ws_ = make_walk<KT, FwdRecord>(walks, tiles + KT, false);
+    w.segment = ws_.segment = sg.tokens;
+    if (walks * max(w.splits, ws_.splits) > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
+    if (!allow_smem<delta_fwd_kernel<KT, false>>() || !allow_smem<delta_fwd_kernel<KT, true>>()) return GLA_ERR_LAUNCH;
+    FwdRecord *records = (FwdRecord *)ws;
     int rc = launch_prep<KT, false>(p, q, k, g, beta, records, nullptr, nullptr, st);
     if (rc != GLA_OK) return rc;
-    delta_fwd_kernel<KT><<<(unsigned)blocks, (w.groups + 1) * 128, walk_bytes(w), st>>>(p, w, q, k, v, records, h0, out,
-                                                                                      hT);
+    char *seg = ws + record_bytes(p);
+    const FwdArgs a{q, k, v, records, h0, (float *)(seg + sg.starts), out, hT, (float *)(seg + sg.N), (float *)(seg + sg.M)};
+    if (sg.tokens) {
+        delta_fwd_kernel<KT, true><<<(unsigned)(walks * ws_.splits), (ws_.groups + 1) * 128, walk_bytes(ws_), st>>>(p, ws_, a);
+        const dim3 grid((unsigned)(p.nseq * p.H), (unsigned)((p.dv + kJoinCols - 1) / kJoinCols));
+        delta_join_kernel<<<grid, 256, 0, st>>>(p, sg.tokens, a.M, a.N, h0, (float *)(seg + sg.starts), hT);
+        count_launches(2);
+    }
+    delta_fwd_kernel<KT, false><<<(unsigned)(walks * w.splits), (w.groups + 1) * 128, walk_bytes(w), st>>>(p, w, a);
     count_launches(1);
     return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
 }
@@ -408,14 +546,12 @@ int fwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
 // bf16 with dk <= 128: a warp's share of the state fits its registers.
 bool mma_supported(int dk) { return dk <= 128; }
 
-size_t mma_fwd_workspace(const Shape &p) {
-    return (size_t)chunk_slots(total_rows(p), p.nseq, kC) * p.H * sizeof(FwdRecord);
-}
+size_t mma_fwd_workspace(const Shape &p) { return record_bytes(p) + plan_segments(p).total; }
 
 int mma_fwd(const Shape &p, const void *q, const void *k, const void *v, const void *g, const void *beta,
             const float *h0, void *out, float *hT, void *ws, cudaStream_t st) {
 #define GLA_CALL(KT) \
-    return fwd_kt<KT>(p, (const bf16 *)q, (const bf16 *)k, (const bf16 *)v, g, beta, h0, (bf16 *)out, hT, (FwdRecord *)ws, st)
+    return fwd_kt<KT>(p, (const bf16 *)q, (const bf16 *)k, (const bf16 *)v, g, beta, h0, (bf16 *)out, hT, (char *)ws, st)
     GLA_BY_KT(p.dk, GLA_CALL);
 #undef GLA_CALL
 }

@@ -104,6 +104,7 @@ struct Walk {           // one block's share of a chain
     int groups;         // warpgroups that hold those tiles; one more fetches
     int vrow;           // bytes of a staged row of V, an odd number of 16-byte units
     int stages, stage_bytes;
+    int segment;        // tokens per segment of a chain (a multiple of kC), or 0: a block walks the whole chain
 };
 
 // A block is launched with 128 registers a thread; the fetching warpgroup gives back 72 of them and each of the
@@ -116,15 +117,14 @@ __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.
 constexpr int kOutRow = 48;  // bytes of a staged row of 16 output columns: an odd number of 16-byte units
 
 // Blocks per chain: one where the chains fill the GPU (the fewest reads of K and Q), else as many as fill it.
-// B8 T2048 H16 dk96 dv192 (128 chains, 152 SMs) runs one block of 12 column tiles to a chain; B1 (16 chains) six
-// blocks of two.
+// B8 T2048 H16 dk96 dv192 (128 chains, 152 SMs) runs one block of 12 column tiles to a chain.
+// walks: chains, or segments of them; tiles: column tiles of 16 of one
 template <int KT, class Rec>
-Walk make_walk(const Shape &p, bool with_q) {
+Walk make_walk(long long walks, int tiles, bool with_q) {
     Walk w{};
-    const int tiles = (p.dv + 15) / 16, sms = device_info().sm_count;
-    const long long chains = (long long)p.nseq * p.H;
+    const int sms = device_info().sm_count;
     int splits = (tiles + kMaxWarps - 1) / kMaxWarps;
-    if (chains * splits < sms) splits = (int)min((long long)tiles, sms / chains);
+    if (walks * splits < sms) splits = (int)min((long long)tiles, sms / walks);
     w.warps = (tiles + splits - 1) / splits;
     w.splits = (tiles + w.warps - 1) / w.warps;
     w.groups = (w.warps + 3) / 4;
@@ -143,25 +143,49 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const v
 // Who a block and a thread are, and the shared memory: barriers, the warps' output tiles, the stages (K | Q | V |
 // record).
 struct Frame {
-    int lane, warp, chain, s, h, hk, col0, width, nch;
-    SeqRange r;
-    bool bad;  // the sequence's offsets are invalid
-    int64_t slot0;
+    int lane, warp, s, h, hk, col0, width, nch;
+    int walk;       // (sequence or segment's slot) * H + head
+    bool bad;       // the sequence's offsets are invalid
+    bool exists;    // whether a segment has this slot
+    bool first, last;  // of its sequence's segments
+    SeqRange r;     // the rows that this block walks over
+    int64_t slot0;  // slot of its first chunk
     uint32_t full, empty, outs, ring;
     volatile int *abort_flag;
 
     __device__ __forceinline__ Frame(const Shape &p, const Walk &w, unsigned block, char *sm) {
         lane = threadIdx.x & 31;
         warp = threadIdx.x >> 5;
-        chain = (int)(block / (unsigned)w.splits);
-        s = chain / p.H;
-        h = chain % p.H;
+        walk = (int)(block / (unsigned)w.splits);
+        s = walk / p.H;
+        h = walk % p.H;
         hk = h / p.group();
         col0 = (int)(block % (unsigned)w.splits) * w.warps * 16;  // first column of the block
-        width = min(w.warps * 16, p.dv - col0);                        // its columns, a multiple of 8
-        bad = !seq_range(s, p.T, p.cu, r);
+        width = min(w.warps * 16, p.dv - col0);                   // its columns of v, a multiple of 8 (none: <= 0)
+        exists = first = last = true;
+        if (w.segment == 0) {
+            bad = !seq_range(s, p.T, p.cu, r);
+            slot0 = r.start / kC + s;
+        } else {
+            // segment i of sequence s has the slot start_s / segment + s + i
+            const int slot = s;
+            int lo = 0, hi = p.nseq - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                const int start = p.cu == nullptr ? mid * p.T : __ldg(p.cu + mid);
+                if (start / w.segment + mid <= slot) lo = mid; else hi = mid - 1;
+            }
+            s = lo;
+            bad = !seq_range(s, p.T, p.cu, r);
+            const int i = slot - ((int)r.start / w.segment + s);
+            exists = i >= 0 && (int64_t)i * w.segment < r.len;  // an empty sequence has none: delta_join_kernel's
+            first = i == 0;
+            last = (int64_t)(i + 1) * w.segment >= r.len;
+            slot0 = r.start / kC + s + (int64_t)i * (w.segment / kC);
+            r.start += (int64_t)i * w.segment;
+            r.len = min((int64_t)w.segment, r.len - (int64_t)i * w.segment);
+        }
         nch = (int)((r.len + kC - 1) / kC);
-        slot0 = r.start / kC + s;
         full = ptx::smem_u32(sm);
         empty = full + 8 * w.stages;
         abort_flag = reinterpret_cast<volatile int *>(sm + 16 * w.stages);
@@ -228,30 +252,30 @@ __device__ __forceinline__ void fetch(const Shape &p, const Walk &w, const Frame
     }
 }
 
-// A warp's 16 columns of a state [dk][dv] in f32 as the accumulators of S^T (16 x dk).
+// A warp's 16 columns of a state [dk][cols] in f32 as the accumulators of S^T (16 x dk).
 template <int KT>
-__device__ __forceinline__ void load_state(float (&S)[2 * KT][4], const float *from, const Shape &p, int chain, int col,
+__device__ __forceinline__ void load_state(float (&S)[2 * KT][4], const float *from, int64_t state, int dk, int cols, int col,
                                            int lane) {
-    const int64_t at = (int64_t)chain * p.dk * p.dv + col + (lane >> 2);
+    const int64_t at = state * dk * cols + col + (lane >> 2);
 #pragma unroll
     for (int n = 0; n < 2 * KT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int row = n * 8 + 2 * (lane & 3) + (e & 1);
-            const bool has = from != nullptr && row < p.dk && col + (e >> 1) * 8 < p.dv;
-            S[n][e] = has ? from[at + (int64_t)row * p.dv + (e >> 1) * 8] : 0.f;
+            const bool has = from != nullptr && row < dk && col + (e >> 1) * 8 < cols;
+            S[n][e] = has ? from[at + (int64_t)row * cols + (e >> 1) * 8] : 0.f;
         }
 }
 template <int KT>
-__device__ __forceinline__ void store_state(float *to, const float (&S)[2 * KT][4], const Shape &p, int chain, int col,
+__device__ __forceinline__ void store_state(float *to, const float (&S)[2 * KT][4], int64_t state, int dk, int cols, int col,
                                             int lane) {
-    const int64_t at = (int64_t)chain * p.dk * p.dv + col + (lane >> 2);
+    const int64_t at = state * dk * cols + col + (lane >> 2);
 #pragma unroll
     for (int n = 0; n < 2 * KT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int row = n * 8 + 2 * (lane & 3) + (e & 1);
-            if (row < p.dk && col + (e >> 1) * 8 < p.dv) to[at + (int64_t)row * p.dv + (e >> 1) * 8] = S[n][e];
+            if (row < dk && col + (e >> 1) * 8 < cols) to[at + (int64_t)row * cols + (e >> 1) * 8] = S[n][e];
         }
 }
 

@@ -378,3 +378,31 @@ def test_refusals():
         gla.delta_decode_step(**dict(s, state=s["state"][:1].contiguous()))
     with pytest.raises(ValueError):
         gla.delta_decode_step(**s, slots=torch.zeros(3, dtype=torch.int32, device="cuda"))
+
+
+# ---- few long chains: the forward walks segments of them ------------------------------------------------------
+
+@pytest.mark.parametrize("T,H,Hk,dk,dv,h0", [(1100, 2, 1, 64, 64, True), (1025, 1, 1, 96, 192, False), (2100, 1, 1, 24, 40, True),
+                                             (1500, 2, 2, 128, 128, True), (1290, 3, 1, 72, 104, True)])
+def test_forward_of_few_long_chains(T, H, Hk, dk, dv, h0):
+    before = gla.gla_kernel_launches()
+    check_forward(make(1, T, H, Hk, dk, dv, seed=T, h0=h0, g_scale=0.02))
+    assert gla.gla_kernel_launches() - before == 4  # chunks, segments, their join, the walk
+
+
+def test_forward_of_few_long_packed_chains_with_resets():
+    d = make(0, 0, 2, 1, 64, 128, lengths=[0, 1400, 1, 3001, 0, 255], seed=11, g_scale=0.02)
+    d["g"][0, 300], d["g"][0, 1300:1310] = -float("inf"), -80.0
+    before = gla.gla_kernel_launches()
+    check_forward(d)
+    assert gla.gla_kernel_launches() - before == 4
+
+
+def test_bad_offsets_of_long_chains_are_reported_and_skipped():
+    d = make(0, 0, 1, 1, 64, 64, lengths=[3000, 600], seed=12)
+    cu = torch.tensor([0, 3000, 10], dtype=torch.int32, device="cuda")
+    out, hT = gla.delta_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["beta"], d["h0"], cu)
+    assert gla.STATUS[gla.gla_last_device_status()] == "GLA_ERR_DEVICE_ARG"
+    good = torch.tensor([0, 3000, 3000], dtype=torch.int32, device="cuda")
+    ref, h_ref = gla.delta_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["beta"], d["h0"], good)
+    assert torch.equal(hT, h_ref) and torch.equal(out[:, :3000], ref[:, :3000])
