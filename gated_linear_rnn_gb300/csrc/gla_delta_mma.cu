@@ -29,6 +29,7 @@
 // a short chunk is computed like a whole one) and the chunk's M, P, c and d beta by one bulk copy into a ring of
 // stages; a row's stride is an odd number of 16-byte units, so that ldmatrix meets no bank twice.
 #include "gla_delta_mma.cuh"
+#include "gla_pairs.cuh"
 
 GLA_DEFINE_STATUS(delta_mma)
 
@@ -38,10 +39,12 @@ namespace {
 
 // ---- what does not depend on the state -----------------------------------------------------------------------
 //
-// One warp per chunk and value head.  K K^T and Q K^T by mma.sync (their inputs are exact, their sums f32); then
-// lane j owns column j: D as a running product of the decays (no difference of logarithms, so a decay of zero is
-// as exact as any), and column j of the inverse by substitution, t_i = [i = j] - sum_{l < i} L_il beta_l t_l, with
-// L's rows broadcast from shared memory.
+// One warp per chunk and value head.  K K^T and Q K^T by mma.sync (their inputs are exact, their sums f32).  Lane j
+// then owns column j: first of D, as a running product of the decays (no difference of logarithms, so a decay of zero is
+// as exact as any), which meets both products where their accumulators lie; then of the inverse by substitution,
+// t_i = [i = j] - sum_{l < i} L_il beta_l t_l, with L's rows broadcast from shared memory and two l to an instruction.
+// P's accumulators are the B operand of the walk as they are; the inverse goes through shared memory once more.
+// The kernel is bound by issued instructions: 2,500 a chunk with Q K^T and D kept in shared memory as well.
 constexpr int kPrepWarps = 4;
 constexpr int kLd = 36;  // f32 row stride of the 32 x 32 tiles: rows 16-byte aligned, columns on different banks
 
@@ -61,38 +64,27 @@ __device__ __forceinline__ void fetch_rows(uint32_t dst, const bf16 *src, int64_
     }
 }
 
-// column `lane` of (I + L diag(beta))^-1 in t
+// Column `lane` of (I + L diag(beta))^-1 (kLeft: of (I + diag(beta) L)^-1) in t.  L holds anything finite on its
+// diagonal: what it multiplies there is still zero.
+template <bool kLeft>
 __device__ __forceinline__ void invert(const float *L, float be, int lane, float (&t)[kC]) {
-    float s[kC];  // beta t
+    Pair s[kC / 2];  // t, or beta t
+#pragma unroll
+    for (int i = 0; i < kC / 2; ++i) s[i] = both(0.f);
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
-        float x0 = i == lane ? 1.f : 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
+        Pair x = both(0.f), y = both(0.f);
 #pragma unroll
         for (int l = 0; l < i; l += 4) {
-            const float4 row = *reinterpret_cast<const float4 *>(L + i * kLd + l);
-            x0 = fmaf(-row.x, s[l], x0);
-            if (l + 1 < i) x1 = fmaf(-row.y, s[l + 1], x1);
-            if (l + 2 < i) x2 = fmaf(-row.z, s[l + 2], x2);
-            if (l + 3 < i) x3 = fmaf(-row.w, s[l + 3], x3);
+            const ulonglong2 row = *reinterpret_cast<const ulonglong2 *>(L + i * kLd + l);
+            x = fma(Pair{row.x}, s[l / 2], x);
+            y = fma(Pair{row.y}, s[l / 2 + 1], y);
         }
-        t[i] = (x0 + x1) + (x2 + x3);
-        s[i] = t[i] * __shfl_sync(0xffffffffu, be, i);
-    }
-}
-// column `lane` of (I + diag(beta) L)^-1 in t
-__device__ __forceinline__ void invert_left(const float *L, float be, int lane, float (&t)[kC]) {
-#pragma unroll
-    for (int i = 0; i < kC; ++i) {
-        float x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
-#pragma unroll
-        for (int l = 0; l < i; l += 4) {
-            const float4 row = *reinterpret_cast<const float4 *>(L + i * kLd + l);
-            x0 = fmaf(row.x, t[l], x0);
-            if (l + 1 < i) x1 = fmaf(row.y, t[l + 1], x1);
-            if (l + 2 < i) x2 = fmaf(row.z, t[l + 2], x2);
-            if (l + 3 < i) x3 = fmaf(row.w, t[l + 3], x3);
-        }
-        t[i] = (i == lane ? 1.f : 0.f) - __shfl_sync(0xffffffffu, be, i) * ((x0 + x1) + (x2 + x3));
+        const float own = i == lane ? 1.f : 0.f, b = __shfl_sync(0xffffffffu, be, i), sum = total(x + y);
+        t[i] = kLeft ? fmaf(-b, sum, own) : own - sum;
+        const float v = kLeft ? t[i] : b * t[i];
+        const float2 f = parts(s[i / 2]);
+        s[i / 2] = i & 1 ? pair(f.x, v) : pair(v, 0.f);
     }
 }
 
@@ -109,7 +101,7 @@ delta_prep_kernel(Shape p, unsigned units, const bf16 *__restrict__ q, const bf1
     ChunkAt at;
     if (!chunk_of_slot<kC>((int)(unit / (unsigned)p.H), p, at)) return;
     char *ks = sm_raw + warp * prep_warp_bytes<KT>(), *qs = ks + kC * row_bytes<KT>();
-    float *kap = reinterpret_cast<float *>(ks), *qk = kap + kC * kLd;
+    float *L = reinterpret_cast<float *>(ks), *D = L + kC * kLd;  // in the rows' place once these are read
     const uint32_t ka = ptx::smem_u32(ks), qa = ptx::smem_u32(qs);
     fetch_rows<KT>(ka, k + (at.row * p.Hk + hk) * p.dk, (int64_t)p.Hk * p.dk, at.len, p.dk, lane);
     fetch_rows<KT>(qa, q + (at.row * p.Hk + hk) * p.dk, (int64_t)p.Hk * p.dk, at.len, p.dk, lane);
@@ -121,7 +113,7 @@ delta_prep_kernel(Shape p, unsigned units, const bf16 *__restrict__ q, const bf1
     cp_async_wait_all();
     __syncwarp();
     const int m8 = lane >> 3, r8 = lane & 7;
-    float kk[2][4][4] = {}, qq[2][4][4] = {};
+    float kk[2][4][4] = {}, qq[2][4][4] = {};  // tiles on and below the diagonal
 #pragma unroll
     for (int s = 0; s < KT; ++s) {
         uint32_t b[2][4], ak[2][4], aq[2][4];
@@ -135,26 +127,15 @@ delta_prep_kernel(Shape p, unsigned units, const bf16 *__restrict__ q, const bf1
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int t = 0; t <= i; ++t) {  // tiles on and below the diagonal
+            for (int t = 0; t <= i; ++t) {
                 mma(kk[i][2 * t], ak[i], b[t][0], b[t][1]);
                 mma(kk[i][2 * t + 1], ak[i], b[t][2], b[t][3]);
                 mma(qq[i][2 * t], aq[i], b[t][0], b[t][1]);
                 mma(qq[i][2 * t + 1], aq[i], b[t][2], b[t][3]);
             }
     }
-    __syncwarp();  // the tiles are read: their place takes kappa and Q K^T
-    const int gr = lane >> 2, tg = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int at0 = (i * 16 + gr) * kLd + t * 8 + 2 * tg;
-            *reinterpret_cast<float2 *>(kap + at0) = make_float2(kk[i][t][0], kk[i][t][1]);
-            *reinterpret_cast<float2 *>(kap + at0 + 8 * kLd) = make_float2(kk[i][t][2], kk[i][t][3]);
-            *reinterpret_cast<float2 *>(qk + at0) = make_float2(qq[i][t][0], qq[i][t][1]);
-            *reinterpret_cast<float2 *>(qk + at0 + 8 * kLd) = make_float2(qq[i][t][2], qq[i][t][3]);
-        }
     __syncwarp();
+    const int gr = lane >> 2, tg = lane & 3;
     float f = 0.f, run = 1.f, c = 1.f;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
@@ -162,61 +143,74 @@ delta_prep_kernel(Shape p, unsigned units, const bf16 *__restrict__ q, const bf1
         run *= ai;
         if (i == lane) c = run;
         f = i == lane ? 1.f : f * ai;
-        const int e = i * kLd + lane;
-        kap[e] = i > lane ? f * kap[e] : 0.f;
-        qk[e] = i >= lane ? f * qk[e] * (kGrad ? 1.f : be) : 0.f;
+        D[i * kLd + lane] = f;
     }
+    __syncwarp();
+    // L = D o K K^T to shared memory (anything on the diagonal); P = D o Q K^T (diag(beta)) stays where it is
+    uint32_t pp[4][4];  // [tile of 8 rows][tile of 8 columns]
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (t > n) {
+                pp[n][t] = 0;
+                if (t <= (n | 1)) *reinterpret_cast<float2 *>(L + (n * 8 + gr) * kLd + t * 8 + 2 * tg) = make_float2(0.f, 0.f);
+                continue;
+            }
+            const int at0 = (n * 8 + gr) * kLd + t * 8 + 2 * tg, i = n >> 1, e = (n & 1) * 2;
+            const float2 d = *reinterpret_cast<const float2 *>(D + at0);
+            *reinterpret_cast<float2 *>(L + at0) = make_float2(d.x * kk[i][t][e], d.y * kk[i][t][e + 1]);
+            float x = d.x * qq[i][t][e], y = d.y * qq[i][t][e + 1];
+            if (!kGrad) {
+                x *= __shfl_sync(0xffffffffu, be, t * 8 + 2 * tg);
+                y *= __shfl_sync(0xffffffffu, be, t * 8 + 2 * tg + 1);
+            }
+            pp[n][t] = pack(x, y);
+        }
     __syncwarp();
     float t[kC];
     if (kGrad) {
-        // (I + diag(beta) L)^-1 goes out first; L stays for the other inverse
-        float left[kC];
-        invert_left(kap, be, lane, left);
-        invert(kap, be, lane, t);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < kC; ++i) kap[i * kLd + lane] = left[i];
-        __syncwarp();
         BwdRecord *rec = back + unit;
+        float left[kC];
+        invert<true>(L, be, lane, left);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            uint32_t mm[4], pp[4];
+        for (int i = 0; i < kC; ++i) D[i * kLd + lane] = left[i];
+        __syncwarp();
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {  // as B operands over the rows (k = i, n = j)
+            uint32_t mm[4], pt[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int at0 = (e * 8 + 2 * tg) * kLd + n * 8 + gr;
-                mm[e] = pack(kap[at0], kap[at0 + kLd]);
-                pp[e] = pack(qk[at0], qk[at0 + kLd]);
+                mm[e] = e >= n ? pack(D[at0], D[at0 + kLd]) : 0;
+                pt[e] = e >= n ? transpose8(pp[e][n]) : 0;
             }
             rec->m[n][lane] = make_uint4(mm[0], mm[1], mm[2], mm[3]);
-            rec->p[n][lane] = make_uint4(pp[0], pp[1], pp[2], pp[3]);
+            rec->p[n][lane] = make_uint4(pt[0], pt[1], pt[2], pt[3]);
         }
         rec->c[lane] = c;
         rec->d[lane] = f;
         rec->b[lane] = be;
-    } else {
-        invert(kap, be, lane, t);
+        __syncwarp();
     }
-    __syncwarp();
+    invert<false>(L, be, lane, t);
 #pragma unroll
-    for (int i = 0; i < kC; ++i) kap[i * kLd + lane] = t[i];
+    for (int i = 0; i < kC; ++i) D[i * kLd + lane] = t[i];
     __syncwarp();
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-        uint32_t hi[4], lo[4], pp[4];
+        uint32_t hi[4] = {}, lo[4] = {};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int at0 = (n * 8 + gr) * kLd + e * 8 + 2 * tg;
-            const float2 m = *reinterpret_cast<const float2 *>(kap + at0);
-            const float2 x = *reinterpret_cast<const float2 *>(qk + at0);
+        for (int e = 0; e <= n; ++e) {
+            const float2 m = *reinterpret_cast<const float2 *>(D + (n * 8 + gr) * kLd + e * 8 + 2 * tg);
             split(m.x, m.y, hi[e], lo[e]);
-            pp[e] = pack(x.x, x.y);
         }
         if (kGrad) {
             again[unit].mhi[n][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         } else {
             records[unit].mhi[n][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             records[unit].mlo[n][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            records[unit].p[n][lane] = make_uint4(pp[0], pp[1], pp[2], pp[3]);
+            records[unit].p[n][lane] = make_uint4(pp[n][0], pp[n][1], pp[n][2], pp[n][3]);
         }
     }
     (kGrad ? again[unit].c : records[unit].c)[lane] = c;
@@ -406,64 +400,67 @@ delta_fwd_kernel(Shape p, Walk w, FwdArgs a) {
 }
 
 // The state before every segment of a chain, S_{i+1} = M_i S_i + N_i from h0, for 32 columns of a head: 256 threads, a
-// column and an eighth of the rows each; M's rows come through shared memory, the state stays there.  A sequence
-// without tokens (or with bad offsets) has no segments: its final state is written here.
+// column and every eighth row each.  The state and M (the next segment's while one is used) lie in shared memory; an
+// element of S read there serves all of a thread's rows.  A sequence without tokens (or with bad offsets) has no
+// segments: its final state is written here.
 constexpr int kJoinCols = 32;
+inline int join_bytes(int dk) { return (2 * dk * dk + dk * kJoinCols) * (int)sizeof(float); }
+
 __global__ void __launch_bounds__(256)
 delta_join_kernel(Shape p, int segment, const float *__restrict__ M, const float *__restrict__ N,
                   const float *__restrict__ h0, float *__restrict__ starts, float *__restrict__ hT) {
-    __shared__ float S[128][kJoinCols];
-    __shared__ __align__(16) float m[8][128];
-    const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, col = blockIdx.y * kJoinCols + (threadIdx.x & 31);
-    const int part = threadIdx.x >> 5;
+    extern __shared__ __align__(128) char sm_raw[];
+    const int dk = p.dk, c = threadIdx.x & 31, part = threadIdx.x >> 5;
+    float *m = reinterpret_cast<float *>(sm_raw), *S = m + 2 * dk * dk;  // [2][dk][dk], [dk][32]
+    const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, col = blockIdx.y * kJoinCols + c;
     const bool live = col < p.dv;
     SeqRange r;
     if (!seq_range(s, p.T, p.cu, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
     const int64_t slot0 = r.start / segment + s;
     const int n = (int)((r.len + segment - 1) / segment);
-    const int64_t h_at = ((int64_t)s * p.H + h) * p.dk * p.dv + col;
+    const int64_t h_at = ((int64_t)s * p.H + h) * dk * p.dv + col;
     if (n == 0) {
         if (hT != nullptr && live)
-            for (int i = part; i < p.dk; i += 8) hT[h_at + (int64_t)i * p.dv] = h0 != nullptr ? h0[h_at + (int64_t)i * p.dv] : 0.f;
+            for (int i = part; i < dk; i += 8) hT[h_at + (int64_t)i * p.dv] = h0 != nullptr ? h0[h_at + (int64_t)i * p.dv] : 0.f;
         return;
     }
-    for (int i = part; i < p.dk; i += 8) S[i][threadIdx.x & 31] = live && h0 != nullptr ? h0[h_at + (int64_t)i * p.dv] : 0.f;
+    const auto fetch_m = [&](int g) {
+        const float *from = M + ((slot0 + g) * p.H + h) * dk * dk;
+        const uint32_t to = ptx::smem_u32(m + (g & 1) * dk * dk);
+        for (int i = threadIdx.x; i < dk * dk / 4; i += 256) cp_async16(to + i * 16, from + i * 4, true);
+    };
+    if (n > 1) fetch_m(0);
+    for (int i = part; i < dk; i += 8) S[i * kJoinCols + c] = live && h0 != nullptr ? h0[h_at + (int64_t)i * p.dv] : 0.f;
     for (int g = 0; g < n; ++g) {
-        const int64_t at = (slot0 + g) * p.H + h;
+        const int64_t at = ((slot0 + g) * p.H + h) * dk * p.dv + col;
         float next[16] = {};  // rows part, part + 8, ...
+        cp_async_wait_all();
         __syncthreads();
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
             const int i = x * 8 + part;
-            if (i < p.dk && live) {
-                starts[at * p.dk * p.dv + (int64_t)i * p.dv + col] = S[i][threadIdx.x & 31];
-                if (g + 1 < n) next[x] = N[at * p.dk * p.dv + (int64_t)i * p.dv + col];
+            if (i < dk && live) {
+                starts[at + (int64_t)i * p.dv] = S[i * kJoinCols + c];
+                if (g + 1 < n) next[x] = __ldg(N + at + (int64_t)i * p.dv);
             }
         }
         if (g + 1 == n) break;
+        if (g + 2 < n) fetch_m(g + 1);
+        const float *mg = m + (g & 1) * dk * dk + part * dk;
+        for (int j = 0; j < dk; j += 4) {
+            const float s0 = S[j * kJoinCols + c], s1 = S[(j + 1) * kJoinCols + c], s2 = S[(j + 2) * kJoinCols + c],
+                        s3 = S[(j + 3) * kJoinCols + c];
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-            if (x * 8 >= p.dk) break;
-            __syncwarp();  // a warp's row of M: row x * 8 + part
-            for (int j = threadIdx.x & 31; j < p.dk; j += 32)
-                m[part][j] = x * 8 + part < p.dk ? M[at * p.dk * p.dk + (int64_t)(x * 8 + part) * p.dk + j] : 0.f;
-            __syncwarp();
-            float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-            for (int j = 0; j < p.dk; j += 4) {
-                const float4 t = *reinterpret_cast<const float4 *>(&m[part][j]);
-                a0 = fmaf(t.x, S[j][threadIdx.x & 31], a0);
-                a1 = fmaf(t.y, S[j + 1][threadIdx.x & 31], a1);
-                a2 = fmaf(t.z, S[j + 2][threadIdx.x & 31], a2);
-                a3 = fmaf(t.w, S[j + 3][threadIdx.x & 31], a3);
-            }
-            next[x] += (a0 + a1) + (a2 + a3);
+            for (int x = 0; x < 16; ++x)
+                if (x * 8 < dk) {  // dk is a multiple of 8
+                    const float4 t = *reinterpret_cast<const float4 *>(mg + x * 8 * dk + j);
+                    next[x] = fmaf(t.x, s0, fmaf(t.y, s1, fmaf(t.z, s2, fmaf(t.w, s3, next[x]))));
+                }
         }
         __syncthreads();
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-            const int i = x * 8 + part;
-            if (i < p.dk) S[i][threadIdx.x & 31] = next[x];
-        }
+        for (int x = 0; x < 16; ++x)
+            if (x * 8 < dk) S[(x * 8 + part) * kJoinCols + c] = next[x];
     }
 }
 
@@ -524,7 +521,9 @@ int fwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
     Walk w = make_walk<KT, FwdRecord>(walks, tiles, true), ws_ = make_walk<KT, FwdRecord>(walks, tiles + KT, false);
     w.segment = ws_.segment = sg.tokens;
     if (walks * max(w.splits, ws_.splits) > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
-    if (!allow_smem<delta_fwd_kernel<KT, false>>() || !allow_smem<delta_fwd_kernel<KT, true>>()) return GLA_ERR_LAUNCH;
+    if (!allow_smem<delta_fwd_kernel<KT, false>>() || !allow_smem<delta_fwd_kernel<KT, true>>() ||
+        !allow_smem<delta_join_kernel>())
+        return GLA_ERR_LAUNCH;
     FwdRecord *records = (FwdRecord *)ws;
     int rc = launch_prep<KT, false>(p, q, k, g, beta, records, nullptr, nullptr, st);
     if (rc != GLA_OK) return rc;
@@ -533,7 +532,7 @@ int fwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
     if (sg.tokens) {
         delta_fwd_kernel<KT, true><<<(unsigned)(walks * ws_.splits), (ws_.groups + 1) * 128, walk_bytes(ws_), st>>>(p, ws_, a);
         const dim3 grid((unsigned)(p.nseq * p.H), (unsigned)((p.dv + kJoinCols - 1) / kJoinCols));
-        delta_join_kernel<<<grid, 256, 0, st>>>(p, sg.tokens, a.M, a.N, h0, (float *)(seg + sg.starts), hT);
+        delta_join_kernel<<<grid, 256, join_bytes(p.dk), st>>>(p, sg.tokens, a.M, a.N, h0, (float *)(seg + sg.starts), hT);
         count_launches(2);
     }
     delta_fwd_kernel<KT, false><<<(unsigned)(walks * w.splits), (w.groups + 1) * 128, walk_bytes(w), st>>>(p, w, a);
