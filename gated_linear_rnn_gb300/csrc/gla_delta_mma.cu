@@ -404,8 +404,9 @@ delta_fwd_kernel(Shape p, Walk w, FwdArgs a) {
 // element of S read there serves all of a thread's rows.  A sequence without tokens (or with bad offsets) has no
 // segments: its final state is written here.
 constexpr int kJoinCols = 32;
-inline int join_bytes(int dk) { return (2 * dk * dk + dk * kJoinCols) * (int)sizeof(float); }
+inline int join_bytes(int dk) { return (2 * dk * dk + dk * kJoinCols) * (int)sizeof(float); }  // >= (KT * 16 + dk) dk
 
+template <int KT>
 __global__ void __launch_bounds__(256)
 delta_join_kernel(Shape p, int segment, const float *__restrict__ M, const float *__restrict__ N,
                   const float *__restrict__ h0, float *__restrict__ starts, float *__restrict__ hT) {
@@ -433,33 +434,32 @@ delta_join_kernel(Shape p, int segment, const float *__restrict__ M, const float
     for (int i = part; i < dk; i += 8) S[i * kJoinCols + c] = live && h0 != nullptr ? h0[h_at + (int64_t)i * p.dv] : 0.f;
     for (int g = 0; g < n; ++g) {
         const int64_t at = ((slot0 + g) * p.H + h) * dk * p.dv + col;
-        float next[16] = {};  // rows part, part + 8, ...
+        float next[2 * KT];  // rows part, part + 8, ...
         cp_async_wait_all();
         __syncthreads();
+        const bool go_on = g + 1 < n;
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
+        for (int x = 0; x < 2 * KT; ++x) {
             const int i = x * 8 + part;
-            if (i < dk && live) {
-                starts[at + (int64_t)i * p.dv] = S[i * kJoinCols + c];
-                if (g + 1 < n) next[x] = __ldg(N + at + (int64_t)i * p.dv);
-            }
+            const bool has = i < dk && live;
+            if (has) starts[at + (int64_t)i * p.dv] = S[i * kJoinCols + c];
+            next[x] = has && go_on ? __ldg(N + at + (int64_t)i * p.dv) : 0.f;
         }
-        if (g + 1 == n) break;
+        if (!go_on) break;
         if (g + 2 < n) fetch_m(g + 1);
-        const float *mg = m + (g & 1) * dk * dk + part * dk;
+        const float *mg = m + (g & 1) * dk * dk + part * dk;  // rows past dk read what lies behind, for no one
         for (int j = 0; j < dk; j += 4) {
             const float s0 = S[j * kJoinCols + c], s1 = S[(j + 1) * kJoinCols + c], s2 = S[(j + 2) * kJoinCols + c],
                         s3 = S[(j + 3) * kJoinCols + c];
 #pragma unroll
-            for (int x = 0; x < 16; ++x)
-                if (x * 8 < dk) {  // dk is a multiple of 8
-                    const float4 t = *reinterpret_cast<const float4 *>(mg + x * 8 * dk + j);
-                    next[x] = fmaf(t.x, s0, fmaf(t.y, s1, fmaf(t.z, s2, fmaf(t.w, s3, next[x]))));
-                }
+            for (int x = 0; x < 2 * KT; ++x) {
+                const float4 t = *reinterpret_cast<const float4 *>(mg + x * 8 * dk + j);
+                next[x] = fmaf(t.x, s0, fmaf(t.y, s1, fmaf(t.z, s2, fmaf(t.w, s3, next[x]))));
+            }
         }
         __syncthreads();
 #pragma unroll
-        for (int x = 0; x < 16; ++x)
+        for (int x = 0; x < 2 * KT; ++x)
             if (x * 8 < dk) S[(x * 8 + part) * kJoinCols + c] = next[x];
     }
 }
@@ -522,7 +522,7 @@ int fwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
     w.segment = ws_.segment = sg.tokens;
     if (walks * max(w.splits, ws_.splits) > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
     if (!allow_smem<delta_fwd_kernel<KT, false>>() || !allow_smem<delta_fwd_kernel<KT, true>>() ||
-        !allow_smem<delta_join_kernel>())
+        !allow_smem<delta_join_kernel<KT>>())
         return GLA_ERR_LAUNCH;
     FwdRecord *records = (FwdRecord *)ws;
     int rc = launch_prep<KT, false>(p, q, k, g, beta, records, nullptr, nullptr, st);
@@ -532,7 +532,7 @@ int fwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
     if (sg.tokens) {
         delta_fwd_kernel<KT, true><<<(unsigned)(walks * ws_.splits), (ws_.groups + 1) * 128, walk_bytes(ws_), st>>>(p, ws_, a);
         const dim3 grid((unsigned)(p.nseq * p.H), (unsigned)((p.dv + kJoinCols - 1) / kJoinCols));
-        delta_join_kernel<<<grid, 256, join_bytes(p.dk), st>>>(p, sg.tokens, a.M, a.N, h0, (float *)(seg + sg.starts), hT);
+        delta_join_kernel<KT><<<grid, 256, join_bytes(p.dk), st>>>(p, sg.tokens, a.M, a.N, h0, (float *)(seg + sg.starts), hT);
         count_launches(2);
     }
     delta_fwd_kernel<KT, false><<<(unsigned)(walks * w.splits), (w.groups + 1) * 128, walk_bytes(w), st>>>(p, w, a);
