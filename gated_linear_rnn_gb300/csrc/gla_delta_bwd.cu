@@ -45,7 +45,7 @@ __device__ __forceinline__ int64_t image_at(const Shape &p, int64_t slot, int h,
     return ((slot * p.H + h) * ((p.dv + 15) / 16) + tile) * KT * 32;
 }
 
-// acc[t] += S^T K^T over the chunk's 32 tokens (t: tiles of 8 tokens), S rounded to bf16
+// acc[t] = S^T K^T over the chunk's 32 tokens (t: tiles of 8 tokens), S rounded to bf16
 template <int KT>
 __device__ __forceinline__ void state_times_rows(float (&acc)[4][4], const float (&S)[2 * KT][4], uint32_t rows, int lane) {
     const uint32_t off = (((lane >> 3) >> 1) * 8 + (lane & 7)) * row_bytes<KT>() + ((lane >> 3) & 1) * 16;
@@ -56,10 +56,17 @@ __device__ __forceinline__ void state_times_rows(float (&acc)[4][4], const float
         for (int e = 0; e < 4; ++e) a[e] = pack(S[2 * i + (e >> 1)][(e & 1) * 2], S[2 * i + (e >> 1)][(e & 1) * 2 + 1]);
         ldsm4(b0, rows + off + i * 32);
         ldsm4(b1, rows + off + 16 * row_bytes<KT>() + i * 32);
-        mma(acc[0], a, b0[0], b0[1]);
-        mma(acc[1], a, b0[2], b0[3]);
-        mma(acc[2], a, b1[0], b1[1]);
-        mma(acc[3], a, b1[2], b1[3]);
+        if (i == 0) {
+            mma0(acc[0], a, b0[0], b0[1]);
+            mma0(acc[1], a, b0[2], b0[3]);
+            mma0(acc[2], a, b1[0], b1[1]);
+            mma0(acc[3], a, b1[2], b1[3]);
+        } else {
+            mma(acc[0], a, b0[0], b0[1]);
+            mma(acc[1], a, b0[2], b0[3]);
+            mma(acc[2], a, b1[0], b1[1]);
+            mma(acc[3], a, b1[2], b1[3]);
+        }
     }
 }
 // S^T += U rows for U (16 columns x 32 tokens) as A operands
@@ -112,7 +119,7 @@ __device__ __forceinline__ void walk_again(const Shape &p, const Walk &w, unsign
         if ((c & 1) == 0 && live) write_image<KT>(images + image_at<KT>(p, slot64 + c / 2, f.h, col / 16), S, lane);
         const uint32_t ks = f.ring + sg * w.stage_bytes, vs = ks + kTile + f.warp * 32, rec = ks + kTile + kC * w.vrow;
         const uint32_t vec = rec + (uint32_t)offsetof(AgainRecord, c) + 8 * tg;
-        float Y[4][4] = {};
+        float Y[4][4];
         state_times_rows<KT>(Y, S, ks, lane);
         uint32_t x[2][4], xl[2][4];
 #pragma unroll
@@ -128,12 +135,12 @@ __device__ __forceinline__ void walk_again(const Shape &p, const Walk &w, unsign
                       x[t][2 * u + 1], xl[t][2 * u + 1]);
             }
         }
-        float R[4][4] = {};
+        float R[4][4];
         uint4 m[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) m[n] = lds128(rec + n * 512 + lane * 16);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) mma(R[n], x[0], m[n].x, m[n].y);
+        for (int n = 0; n < 4; ++n) mma0(R[n], x[0], m[n].x, m[n].y);
 #pragma unroll
         for (int n = 0; n < 4; ++n) mma(R[n], xl[0], m[n].x, m[n].y);
         mma(R[2], x[1], m[2].z, m[2].w);
@@ -149,9 +156,7 @@ __device__ __forceinline__ void walk_again(const Shape &p, const Walk &w, unsign
         }
         const float last = lds_f2(rec + (uint32_t)offsetof(AgainRecord, c) + 8 * 15).y;
 #pragma unroll
-        for (int n = 0; n < 2 * KT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[n][e] *= last;
+        for (int n = 0; n < 2 * KT; ++n) scale(S[n], both(last));
         add_outer<KT>(S, u, ks, lane);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(f.empty + 8 * sg);
@@ -202,13 +207,13 @@ __device__ __forceinline__ void walk_back(const Shape &p, const Walk &w, unsigne
 #pragma unroll
         for (int t = 0; t < 2; ++t) ldsm4t(a[t], vs + (t * 16 + (m8 >> 1) * 8 + r8) * w.vrow + (m8 & 1) * 16);
         // dU^T = dS^T K^T diag(d) + dO^T P: P is lower triangular, its first 16 rows reach the first 16 columns only
-        float U[4][4] = {};
+        float U[4][4];
         state_times_rows<KT>(U, S, ks, lane);
         uint4 m[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const float2 d = lds_f2(vec + 4 * kC + n * 32);
-            U[n][0] *= d.x; U[n][1] *= d.y; U[n][2] *= d.x; U[n][3] *= d.y;
+            scale(U[n], pair(d.x, d.y));
             m[n] = lds128(rec + n * 512 + lane * 16);
         }
 #pragma unroll
@@ -222,9 +227,9 @@ __device__ __forceinline__ void walk_back(const Shape &p, const Walk &w, unsigne
             split(U[n][2], U[n][3], u[n >> 1][(n & 1) * 2 + 1], ul[n >> 1][(n & 1) * 2 + 1]);
             m[n] = lds128(rec + 2048 + n * 512 + lane * 16);
         }
-        float Y[4][4] = {};
+        float Y[4][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) mma(Y[n], u[1], m[n].z, m[n].w);
+        for (int n = 0; n < 4; ++n) mma0(Y[n], u[1], m[n].z, m[n].w);
 #pragma unroll
         for (int n = 0; n < 4; ++n) mma(Y[n], ul[1], m[n].z, m[n].w);
         mma(Y[0], u[0], m[0].x, m[0].y);
@@ -246,9 +251,7 @@ __device__ __forceinline__ void walk_back(const Shape &p, const Walk &w, unsigne
         }
         const float last = lds_f2(rec + (uint32_t)offsetof(BwdRecord, c) + 8 * 15).y;
 #pragma unroll
-        for (int n = 0; n < 2 * KT; ++n)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) S[n][x] *= last;
+        for (int n = 0; n < 2 * KT; ++n) scale(S[n], both(last));
         add_outer<KT>(S, a, qs, lane);
         add_outer<KT>(S, e, ks, lane);
         __syncwarp();

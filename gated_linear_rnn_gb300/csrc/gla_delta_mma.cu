@@ -29,7 +29,6 @@
 // a short chunk is computed like a whole one) and the chunk's M, P, c and d beta by one bulk copy into a ring of
 // stages; a row's stride is an odd number of 16-byte units, so that ldmatrix meets no bank twice.
 #include "gla_delta_mma.cuh"
-#include "gla_pairs.cuh"
 
 GLA_DEFINE_STATUS(delta_mma)
 
@@ -275,7 +274,7 @@ delta_fwd_kernel(Shape p, Walk w, FwdArgs a) {
                        rec = ks + kV + kC * w.vrow;
         const uint32_t vec = rec + (uint32_t)offsetof(FwdRecord, c) + 8 * tg;
         // Y = S^T K^T
-        float Y[4][4] = {};
+        float Y[4][4];
         const uint32_t row_off = ((m8 >> 1) * 8 + r8) * kRow + (m8 & 1) * 16;
 #pragma unroll
         for (int i = 0; i < KT; ++i) {
@@ -287,10 +286,17 @@ delta_fwd_kernel(Shape p, Walk w, FwdArgs a) {
             uint32_t b0[4], b1[4];
             ldsm4(b0, ks + row_off + i * 32);
             ldsm4(b1, ks + row_off + 16 * kRow + i * 32);
-            mma(Y[0], ah, b0[0], b0[1]);
-            mma(Y[1], ah, b0[2], b0[3]);
-            mma(Y[2], ah, b1[0], b1[1]);
-            mma(Y[3], ah, b1[2], b1[3]);
+            if (i == 0) {
+                mma0(Y[0], ah, b0[0], b0[1]);
+                mma0(Y[1], ah, b0[2], b0[3]);
+                mma0(Y[2], ah, b1[0], b1[1]);
+                mma0(Y[3], ah, b1[2], b1[3]);
+            } else {
+                mma(Y[0], ah, b0[0], b0[1]);
+                mma(Y[1], ah, b0[2], b0[3]);
+                mma(Y[2], ah, b1[0], b1[1]);
+                mma(Y[3], ah, b1[2], b1[3]);
+            }
             mma(Y[0], al, b0[0], b0[1]);
             mma(Y[1], al, b0[2], b0[3]);
             mma(Y[2], al, b1[0], b1[1]);
@@ -312,13 +318,13 @@ delta_fwd_kernel(Shape p, Walk w, FwdArgs a) {
             }
         }
         // R^T = X^T M^T: M is lower triangular, so the first 16 rows meet the first 16 columns only
-        float R[4][4] = {};
+        float R[4][4];
         {
             uint4 m[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) m[n] = lds128(rec + n * 512 + lane * 16);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) mma(R[n], xh[0], m[n].x, m[n].y);
+            for (int n = 0; n < 4; ++n) mma0(R[n], xh[0], m[n].x, m[n].y);
 #pragma unroll
             for (int n = 0; n < 4; ++n) mma(R[n], xl[0], m[n].x, m[n].y);
             mma(R[2], xh[1], m[2].z, m[2].w);
@@ -343,7 +349,7 @@ delta_fwd_kernel(Shape p, Walk w, FwdArgs a) {
             split(R[n][0] * db.x, R[n][1] * db.y, uh[t][u], ul[t][u]);
             split(R[n][2] * db.x, R[n][3] * db.y, uh[t][u + 1], ul[t][u + 1]);
         }
-        float O[4][4] = {};
+        float O[4][4];
         if (!kSegment) {
 #pragma unroll
         for (int i = 0; i < KT; ++i) {
@@ -354,14 +360,19 @@ delta_fwd_kernel(Shape p, Walk w, FwdArgs a) {
             for (int t = 0; t < 2; ++t) {
                 uint32_t b[4];
                 ldsm4(b, qs + row_off + t * 16 * kRow + i * 32);
-                mma(O[2 * t], a, b[0], b[1]);
-                mma(O[2 * t + 1], a, b[2], b[3]);
+                if (i == 0) {
+                    mma0(O[2 * t], a, b[0], b[1]);
+                    mma0(O[2 * t + 1], a, b[2], b[3]);
+                } else {
+                    mma(O[2 * t], a, b[0], b[1]);
+                    mma(O[2 * t + 1], a, b[2], b[3]);
+                }
             }
         }
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const float2 cc = lds_f2(vec + n * 32);
-            O[n][0] *= cc.x; O[n][1] *= cc.y; O[n][2] *= cc.x; O[n][3] *= cc.y;
+            scale(O[n], pair(cc.x, cc.y));
             const uint4 pp = lds128(rec + 4096 + n * 512 + lane * 16);
             mma(O[n], rh[0], pp.x, pp.y);
             if (n >= 2) mma(O[n], rh[1], pp.z, pp.w);
@@ -375,8 +386,7 @@ delta_fwd_kernel(Shape p, Walk w, FwdArgs a) {
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 ldsm4t(b[m], ks + lane * kRow + (n + m) * 16);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S[n + m][e] *= last;
+                scale(S[n + m], both(last));
             }
 #pragma unroll
             for (int m = 0; m < 4; ++m) mma(S[n + m], uh[0], b[m][0], b[m][1]);

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "gla_delta.cuh"
+#include "gla_pairs.cuh"
 #include "sm100_ptx.cuh"
 
 namespace gla {
@@ -38,6 +39,16 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// the same from zero
+__device__ __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void scale(float (&d)[4], Pair by) {
+    const float2 x = parts(pair(d[0], d[1]) * by), y = parts(pair(d[2], d[3]) * by);
+    d[0] = x.x; d[1] = x.y; d[2] = y.x; d[3] = y.y;
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -85,7 +96,8 @@ __device__ __forceinline__ float hi_f(uint32_t p) { return __uint_as_float(p & 0
 // x, y as hi + lo parts of 8 bits each
 __device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &lo) {
     hi = pack(x, y);
-    lo = pack(x - lo_f(hi), y - hi_f(hi));
+    const float2 rest = parts(fma(pair(lo_f(hi), hi_f(hi)), both(-1.f), pair(x, y)));  // exact
+    lo = pack(rest.x, rest.y);
 }
 
 // 8 x 8 b16 values, a row's pair in each lane, transposed within the warp
