@@ -29,15 +29,17 @@ namespace {
 
 constexpr int kG = 64;  // tokens of a chunk of the gradient kernel: two chunks of a walk
 
-// S^T's 16 columns as bf16 B operands (k = the 16 columns, n = dk): [KT][32 lanes] x 16 bytes for each column tile,
-// so that a warp of the gradient kernel reads 512 neighbouring bytes at a time.
+// S^T's 16 columns rounded to bf16, as 8 x 8 matrices (rows: columns of S) of 128 bytes each, [KT][4] of them for each
+// column tile: rows 0-7 and 8-15 of dk's columns 16 i .., then of 16 i + 8 ...  Read with ldmatrix (transposed) they are
+// B operands (k = the 16 columns, n = dk).
 template <int KT>
-__device__ __forceinline__ void write_image(uint4 *to, const float (&S)[2 * KT][4], int lane) {
+__device__ __forceinline__ void write_image(uint4 *image, const float (&S)[2 * KT][4], int lane) {
+    uint32_t *to = reinterpret_cast<uint32_t *>(image) + lane;
 #pragma unroll
-    for (int i = 0; i < KT; ++i)
-        to[i * 32 + lane] = make_uint4(transpose8(pack(S[2 * i][0], S[2 * i][1])), transpose8(pack(S[2 * i][2], S[2 * i][3])),
-                                       transpose8(pack(S[2 * i + 1][0], S[2 * i + 1][1])),
-                                       transpose8(pack(S[2 * i + 1][2], S[2 * i + 1][3])));
+    for (int n = 0; n < 2 * KT; ++n) {
+        to[n * 64] = pack(S[n][0], S[n][1]);
+        to[n * 64 + 32] = pack(S[n][2], S[n][3]);
+    }
 }
 // the image of column tile `tile` of the state of (slot of 64 tokens, head)
 template <int KT>
@@ -95,14 +97,13 @@ __device__ __forceinline__ void walk_again(const Shape &p, const Walk &w, unsign
     if (f.bad && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
     if (f.warp >= w.groups * 4) {
         give_registers();
-        fetch<KT, false, false>(p, w, f, k, k, v, records);
+        fetch<KT, false, false, 1>(p, w, f, k, k, v, records, resid, nullptr);
         return;
     }
     take_registers();
     if (f.warp >= w.warps) return;
     const int lane = f.lane, tg = lane & 3, m8 = lane >> 3, r8 = lane & 7;
     const int col = f.col0 + f.warp * 16;
-    const uint32_t tile = f.outs + f.warp * kC * kOutRow;
     const int64_t slot64 = f.r.start / kG + f.s;
     const bool live = col < p.dv;
     float S[2 * KT][4];
@@ -158,9 +159,9 @@ __device__ __forceinline__ void walk_again(const Shape &p, const Walk &w, unsign
 #pragma unroll
         for (int n = 0; n < 2 * KT; ++n) scale(S[n], both(last));
         add_outer<KT>(S, u, ks, lane);
+        put_tile(R, vs, w.vrow, lane);  // in the place of this warp's columns of V
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(f.empty + 8 * sg);
-        write_tile(resid, R, p, f, c, col, tile);
     }
 }
 
@@ -176,14 +177,13 @@ __device__ __forceinline__ void walk_back(const Shape &p, const Walk &w, unsigne
     if (f.bad && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
     if (f.warp >= w.groups * 4) {
         give_registers();
-        fetch<KT, true, true>(p, w, f, q, k, dout, records);
+        fetch<KT, true, true, 2>(p, w, f, q, k, dout, records, ys, dv);
         return;
     }
     take_registers();
     if (f.warp >= w.warps) return;
     const int lane = f.lane, tg = lane & 3, m8 = lane >> 3, r8 = lane & 7;
     const int col = f.col0 + f.warp * 16;
-    const uint32_t tile = f.outs + f.warp * kC * kOutRow;
     const int64_t slot64 = f.r.start / kG + f.s;
     const bool live = col < p.dv;
     float S[2 * KT][4];
@@ -254,10 +254,10 @@ __device__ __forceinline__ void walk_back(const Shape &p, const Walk &w, unsigne
         for (int n = 0; n < 2 * KT; ++n) scale(S[n], both(last));
         add_outer<KT>(S, a, qs, lane);
         add_outer<KT>(S, e, ks, lane);
+        put_tile(Y, vs, w.vrow, lane);  // in the place of this warp's columns of dO
+        put_tile(D, rec + (uint32_t)sizeof(BwdRecord) + f.warp * 32, w.vrow, lane);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(f.empty + 8 * sg);
-        write_tile(ys, Y, p, f, c, col, tile);
-        write_tile(dv, D, p, f, c, col, tile);
     }
     if (dh0 != nullptr) store_state<KT>(dh0, S, f.walk, p.dk, p.dv, col, lane);
 }
@@ -331,17 +331,6 @@ template <int KT> struct GradPlan {
 };
 
 __device__ __forceinline__ void compute_sync() { ptx::named_bar_sync(1, kGradWarps * 32); }
-// the same, and whether any of the threads brings a failure: all of them leave together or none
-__device__ __forceinline__ bool compute_sync_any(bool failed) {
-    uint32_t any;
-    asm volatile("{\n\t.reg .pred p, r;\n\t"
-                 "setp.ne.u32 p, %1, 0;\n\t"
-                 "barrier.cta.red.or.pred r, 1, %2, p;\n\t"
-                 "selp.u32 %0, 1, 0, r;\n\t}"
-                 : "=r"(any) : "r"((uint32_t)failed), "n"(kGradWarps * 32) : "memory");
-    return any != 0;
-}
-
 // acc (16 rows x KT * 16) += A (16 x 16) times 16 rows of a tile
 template <int KT>
 __device__ __forceinline__ void add_rows(float (&acc)[2 * KT][4], const uint32_t (&a)[4], uint32_t rows, int lane) {
@@ -545,7 +534,7 @@ delta_grad_kernel(Shape p, GradArgs a) {
             const uint32_t slab = base + P::kOffSlab + sg * P::kSlab;
             const uint32_t a_at = slab + (role * kG + rt * 16 + (m8 & 1) * 8 + r8) * kSlabRow + (m8 >> 1) * 16;
             const uint32_t b_at = slab + (2 * kG + (m8 >> 1) * 8 + r8) * kSlabRow + (m8 & 1) * 16;
-            const uint32_t image = slab + 3 * kG * kSlabRow + (role == 2 ? P::kImage : 0) + lane * 16;
+            const uint32_t image = slab + 3 * kG * kSlabRow + (role == 2 ? P::kImage : 0) + lane * 16;  // matrix lane / 8, row lane % 8
             const int here = min(2, tiles - 2 * s);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -554,9 +543,10 @@ delta_grad_kernel(Shape p, GradArgs a) {
                 ldsm4(f, a_at + x * 32);
 #pragma unroll
                 for (int i = 0; i < KT; ++i) {
-                    const uint4 b = lds128(image + (x * KT + i) * 512);
-                    mma(A[2 * i], f, b.x, b.y);
-                    mma(A[2 * i + 1], f, b.z, b.w);
+                    uint32_t b[4];
+                    ldsm4t(b, image + (x * KT + i) * 512);
+                    mma(A[2 * i], f, b[0], b[1]);
+                    mma(A[2 * i + 1], f, b[2], b[3]);
                 }
                 if (role < 2) {
 #pragma unroll
@@ -648,7 +638,7 @@ delta_grad_kernel(Shape p, GradArgs a) {
                 if (row0 + 8 < at.len) store_gate<bf16>(a.dbeta, (at.row + row0 + 8) * p.H + h, p.gate_f32, own1);
             }
         }
-        if (compute_sync_any(!ok)) return;  // R' and N are whole
+        if (any_of<1, kGradWarps * 32>(!ok)) return;  // R' and N are whole
         {
             float acc[2 * KT][4] = {};
             if (role < 2) {  // R' K or N K
@@ -800,7 +790,8 @@ int bwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
     const long long rows = total_rows(p), slots = chunk_slots(rows, p.nseq, kG);
     const long long chains = (long long)p.nseq * p.H;
     const int tiles = (p.dv + 15) / 16;
-    const Walk wa = make_walk<KT, AgainRecord>(chains, tiles, false), wb = make_walk<KT, BwdRecord>(chains, tiles, true);
+    const Walk wa = make_walk<KT, AgainRecord>(chains, tiles, false, 1),
+               wb = make_walk<KT, BwdRecord>(chains, tiles, true, 2);
     const int grad_bytes = GradPlan<KT>::kTotal;
     const long long blocks = chains * wa.splits;
     if (2 * blocks > 0x7fffffffLL || slots * p.H > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;

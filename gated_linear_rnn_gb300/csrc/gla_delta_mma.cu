@@ -240,7 +240,7 @@ delta_fwd_kernel(Shape p, Walk w, FwdArgs a) {
     if (!f.exists || (kSegment && f.last)) return;  // nothing starts where a sequence ends
     if (f.warp >= w.groups * 4) {
         give_registers();
-        fetch<KT, !kSegment, false>(p, w, f, a.q, a.k, a.v, a.records);
+        fetch<KT, !kSegment, false, kSegment ? 0 : 1>(p, w, f, a.q, a.k, a.v, a.records, a.out, nullptr);
         return;
     }
     take_registers();
@@ -248,7 +248,6 @@ delta_fwd_kernel(Shape p, Walk w, FwdArgs a) {
     const int lane = f.lane, tg = lane & 3, m8 = lane >> 3, r8 = lane & 7;
     const int col = f.col0 + f.warp * 16;
     const int mcol = col - (p.dv + 15) / 16 * 16;  // kSegment: column of M, or negative
-    const uint32_t o_tile = f.outs + f.warp * kC * kOutRow;
     float S[2 * KT][4];
     if (kSegment) {
 #pragma unroll
@@ -397,9 +396,9 @@ delta_fwd_kernel(Shape p, Walk w, FwdArgs a) {
 #pragma unroll
             for (int m = 0; m < 4; ++m) mma(S[n + m], ul[1], b[m][2], b[m][3]);
         }
+        if (!kSegment) put_tile(O, vs, w.vrow, lane);  // in the place of this warp's columns of V
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(f.empty + 8 * sg);
-        if (!kSegment) write_tile(a.out, O, p, f, c, col, o_tile);
     }
     if (kSegment) {
         if (mcol < 0) store_state<KT>(a.N, S, f.walk, p.dk, p.dv, col, lane);
@@ -528,7 +527,7 @@ int fwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
     const Segments sg = plan_segments(p);
     const int tiles = (p.dv + 15) / 16;
     const long long walks = sg.tokens ? (long long)sg.slots * p.H : (long long)p.nseq * p.H;
-    Walk w = make_walk<KT, FwdRecord>(walks, tiles, true), ws_ = make_walk<KT, FwdRecord>(walks, tiles + KT, false);
+    Walk w = make_walk<KT, FwdRecord>(walks, tiles, true, 1), ws_ = make_walk<KT, FwdRecord>(walks, tiles + KT, false, 0);
     w.segment = ws_.segment = sg.tokens;
     if (walks * max(w.splits, ws_.splits) > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
     if (!allow_smem<delta_fwd_kernel<KT, false>>() || !allow_smem<delta_fwd_kernel<KT, true>>() ||

@@ -126,13 +126,12 @@ static_assert(kMaxWarps == 12, "three warpgroups of column tiles: 3 * 152 + 56 =
 __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
 __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 152;"); }
 
-constexpr int kOutRow = 48;  // bytes of a staged row of 16 output columns: an odd number of 16-byte units
-
 // Blocks per chain: one where the chains fill the GPU (the fewest reads of K and Q), else as many as fill it.
 // B8 T2048 H16 dk96 dv192 (128 chains, 152 SMs) runs one block of 12 column tiles to a chain.
-// walks: chains, or segments of them; tiles: column tiles of 16 of one
+// walks: chains, or segments of them; tiles: column tiles of 16 of one; outputs: tiles of 32 x its columns that leave a
+// stage, the first in V's place
 template <int KT, class Rec>
-Walk make_walk(long long walks, int tiles, bool with_q) {
+Walk make_walk(long long walks, int tiles, bool with_q, int outputs) {
     Walk w{};
     const int sms = device_info().sm_count;
     int splits = (tiles + kMaxWarps - 1) / kMaxWarps;
@@ -141,19 +140,30 @@ Walk make_walk(long long walks, int tiles, bool with_q) {
     w.splits = (tiles + w.warps - 1) / w.warps;
     w.groups = (w.warps + 3) / 4;
     w.vrow = (w.warps * 2 | 1) * 16;
-    w.stage_bytes = (with_q ? 2 : 1) * kC * row_bytes<KT>() + kC * w.vrow + (int)sizeof(Rec);
-    w.stages = 4;
+    w.stage_bytes = (with_q ? 2 : 1) * kC * row_bytes<KT>() + kC * w.vrow * (outputs > 1 ? outputs : 1) + (int)sizeof(Rec);
+    w.stages = 4 * w.stage_bytes + 128 <= device_info().max_smem_optin ? 4 : 3;
     return w;
 }
-inline int walk_bytes(const Walk &w) { return 128 + w.warps * kC * kOutRow + w.stages * w.stage_bytes; }
+inline int walk_bytes(const Walk &w) { return 128 + w.stages * w.stage_bytes; }
 
 // A bounded wait of a whole warp: all lanes learn the same.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
     return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort_flag, kWaitNs));
 }
 
-// Who a block and a thread are, and the shared memory: barriers, the warps' output tiles, the stages (K | Q | V |
-// record).
+// A barrier of some of the block's warps that tells all of them whether any brings a failure, so that all of them leave
+// together or none.
+template <int kBarrier, int kThreads> __device__ __forceinline__ bool any_of(bool failed) {
+    uint32_t any;
+    asm volatile("{\n\t.reg .pred p, r;\n\t"
+                 "setp.ne.u32 p, %1, 0;\n\t"
+                 "barrier.cta.red.or.pred r, %2, %3, p;\n\t"
+                 "selp.u32 %0, 1, 0, r;\n\t}"
+                 : "=r"(any) : "r"((uint32_t)failed), "n"(kBarrier), "n"(kThreads) : "memory");
+    return any != 0;
+}
+
+// Who a block and a thread are, and the shared memory: barriers, the stages (K | Q | V | record | a second output).
 struct Frame {
     int lane, warp, s, h, hk, col0, width, nch;
     int walk;       // (sequence or segment's slot) * H + head
@@ -162,7 +172,7 @@ struct Frame {
     bool first, last;  // of its sequence's segments
     SeqRange r;     // the rows that this block walks over
     int64_t slot0;  // slot of its first chunk
-    uint32_t full, empty, outs, ring;
+    uint32_t full, empty, ring;
     volatile int *abort_flag;
 
     __device__ __forceinline__ Frame(const Shape &p, const Walk &w, unsigned block, char *sm) {
@@ -201,8 +211,7 @@ struct Frame {
         full = ptx::smem_u32(sm);
         empty = full + 8 * w.stages;
         abort_flag = reinterpret_cast<volatile int *>(sm + 16 * w.stages);
-        outs = full + 128;
-        ring = outs + w.warps * kC * kOutRow;
+        ring = full + 128;
         if (threadIdx.x == 0) {
             for (int i = 0; i < w.stages; ++i) {
                 ptx::mbar_init(full + 8 * i, 129);  // the fetching threads, and the record
@@ -215,10 +224,29 @@ struct Frame {
     }
 };
 
-// The fetching warpgroup: four threads to a token's row.  kBack walks the chunks from the last to the first.
-template <int KT, bool kQ, bool kBack, class Rec>
+// The outputs of a stage, rows of the block's columns as the other warps left them, to rows of `out` and `out2` [rows, H,
+// dv]; neighbouring threads write neighbouring bytes.
+template <int kOut>
+__device__ __forceinline__ void write_rows(const Shape &p, const Walk &w, const Frame &f, int c, uint32_t v, uint32_t second,
+                                           bf16 *out, bf16 *out2) {
+    const int units = f.width / 8, id = threadIdx.x - w.groups * 128;
+    const int rows = (int)min((int64_t)kC, f.r.len - (int64_t)c * kC);
+    const unsigned inv = (65536 + units - 1) / units;  // e / units for e < 32 * 24 by a product
+    const int64_t at = ((f.r.start + (int64_t)c * kC) * p.H + f.h) * p.dv + f.col0;
+    for (int e = id; e < rows * units; e += 128) {
+        const int t = (int)(((unsigned)e * inv) >> 16), u = e - t * units;
+        const int64_t to = at + (int64_t)t * p.H * p.dv + u * 8;
+        *reinterpret_cast<uint4 *>(out + to) = lds128(v + t * w.vrow + u * 16);
+        if (kOut > 1) *reinterpret_cast<uint4 *>(out2 + to) = lds128(second + t * w.vrow + u * 16);
+    }
+}
+
+// The fetching warpgroup: four threads to a token's row.  kBack walks the chunks from the last to the first.  A stage
+// that comes back holds its chunk's outputs (kOut of them), which go out before it is filled again: the
+// other warps neither store to global memory nor wait for it.
+template <int KT, bool kQ, bool kBack, int kOut, class Rec>
 __device__ __forceinline__ void fetch(const Shape &p, const Walk &w, const Frame &f, const bf16 *q, const bf16 *k,
-                                      const bf16 *v, const Rec *records) {
+                                      const bf16 *v, const Rec *records, bf16 *out, bf16 *out2) {
     constexpr int kRow = row_bytes<KT>(), kTile = kC * kRow, kV = (kQ ? 2 : 1) * kTile;
     const int id = threadIdx.x - w.groups * 128, t = id >> 2, u0 = id & 3;
     const int vunits = w.warps * 2, vlive = f.width / 8, kunits = p.dk / 8;
@@ -228,12 +256,25 @@ __device__ __forceinline__ void fetch(const Shape &p, const Walk &w, const Frame
                *vr = v + row0 * vstride + (int64_t)f.h * p.dv + f.col0 + u0 * 8;
     const uint32_t kdst = f.ring + t * kRow + u0 * 16, vdst = f.ring + kV + t * w.vrow + u0 * 16;
     bool ok = true;
-    for (int i = 0; i < f.nch; ++i) {
-        const int c = kBack ? f.nch - 1 - i : i, sg = i % w.stages;
-        ok = i < w.stages || warp_wait(f.empty + 8 * sg, (i / w.stages + 1) & 1, f.abort_flag);
-        if (!ok) break;
-        const bool row = c * kC + t < f.r.len;  // a short chunk's missing rows are zero, and not read
+    for (int i = 0; i < f.nch + w.stages; ++i) {
+        const int sg = i % w.stages;
         const uint32_t at = sg * w.stage_bytes;
+        if (i >= w.stages) {
+            if (i >= f.nch && kOut == 0) break;  // nothing is left to bring in or out
+            ok = warp_wait(f.empty + 8 * sg, (i / w.stages + 1) & 1, f.abort_flag);
+            if (kOut > 0) {
+                const int done = i - w.stages;
+                const uint32_t from = f.ring + at + kV;
+                if (ok)
+                    write_rows<kOut>(p, w, f, kBack ? f.nch - 1 - done : done, from,
+                                     from + kC * w.vrow + (uint32_t)sizeof(Rec), out, out2);
+                ok = !any_of<3, 128>(!ok);  // the rows are read before any thread's copies may land on them
+            }
+            if (!ok) break;
+        }
+        if (i >= f.nch) continue;
+        const int c = kBack ? f.nch - 1 - i : i;
+        const bool row = c * kC + t < f.r.len;  // a short chunk's missing rows are zero, and not read
         if (id == 0) {
             ptx::mbar_expect_tx(f.full + 8 * sg, (uint32_t)sizeof(Rec));
             ptx::bulk_load_g2s(f.ring + at + kV + kC * w.vrow, records + (f.slot0 + c) * p.H + f.h, sizeof(Rec),
@@ -291,24 +332,13 @@ __device__ __forceinline__ void store_state(float *to, const float (&S)[2 * KT][
         }
 }
 
-// O^T (16 columns x 32 tokens) through the warp's tile to rows of 32 bytes of `out` [rows, H, dv].
-__device__ __forceinline__ void write_tile(bf16 *out, const float (&O)[4][4], const Shape &p, const Frame &f, int c, int col,
-                                           uint32_t tile) {
-    const int lane = f.lane, m8 = lane >> 3, r8 = lane & 7;
-    const uint32_t to = tile + ((m8 >> 1) * 8 + r8) * kOutRow + (m8 & 1) * 16;
+// O^T (16 columns x 32 tokens) rounded to bf16 into the warp's columns of a stage's rows.
+__device__ __forceinline__ void put_tile(const float (&O)[4][4], uint32_t cols, int vrow, int lane) {
+    const uint32_t to = cols + ((lane >> 4) * 8 + (lane & 7)) * vrow + ((lane >> 3) & 1) * 16;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
-        stsm4t(to + t * 16 * kOutRow, pack(O[2 * t][0], O[2 * t][1]), pack(O[2 * t][2], O[2 * t][3]),
+        stsm4t(to + t * 16 * vrow, pack(O[2 * t][0], O[2 * t][1]), pack(O[2 * t][2], O[2 * t][3]),
                pack(O[2 * t + 1][0], O[2 * t + 1][1]), pack(O[2 * t + 1][2], O[2 * t + 1][3]));
-    __syncwarp();
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int i = t * 16 + (lane >> 1), cc = col + (lane & 1) * 8;
-        const int64_t tok = (int64_t)c * kC + i;
-        const uint4 x = lds128(tile + i * kOutRow + (lane & 1) * 16);
-        if (tok < f.r.len && cc < p.dv) *reinterpret_cast<uint4 *>(out + ((f.r.start + tok) * p.H + f.h) * p.dv + cc) = x;
-    }
-    __syncwarp();
 }
 
 }  // namespace
