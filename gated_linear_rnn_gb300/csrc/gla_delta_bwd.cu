@@ -274,7 +274,7 @@ struct WalkArgs {
 
 // Both walks in one launch, since neither needs the other: the blocks of the longer one, backwards, come first.
 template <int KT>
-__global__ void __launch_bounds__(kMaxThreads)
+__global__ void __launch_bounds__(kMaxThreads, 1)
 delta_walks_kernel(Shape p, Walk again, Walk back, unsigned blocks, WalkArgs a) {
     extern __shared__ __align__(128) char sm_raw[];
     if (blockIdx.x < blocks)
@@ -296,74 +296,58 @@ delta_walks_kernel(Shape p, Walk again, Walk back, unsigned blocks, WalkArgs a) 
 //     m = rows of k . (R'^T Q + N^T K - N K) - q . (R' K):
 // the crossing products in the chunk, summed from the left (a token's reads leave, its writes enter), so that both
 // ends of a product carry the same rounding and cancel to f32.
-// D_ij comes from products of decays alone (a decay of zero is as good as any): within 16 tokens as a table, across
-// them as (from the tile's start to i)(whole tiles between)(from j to its tile's end).
+// D_ij comes from products of decays alone (a decay of zero is as good as any).
 //
-// One block per SM walks over units.  Twelve warps compute, in three roles of four (16 tokens each): dO's side (T = dO
-// R^T, dO S0^T, R' K -> dq), Y's (Y R^T, Y S0^T, N K) and R's (R dS1^T, R'^T Q + N^T K); the last two meet in
-// shared memory -> dk.  A fourth warpgroup fetches ahead: K, Q and the decay products of the next unit, and
-// slabs of 32 columns of dO, Y, R and of both states through a ring.  With one block per unit that loaded its whole
-// share first and read the states from L2 between products, the kernel took 489 us on the layer's gradient.
-constexpr int kGradWarps = 12;
-constexpr int kGradThreads = (kGradWarps + 4) * 32;
-constexpr int kMRow = kG * 2 + 16;  // bytes of a row of R' and N
-constexpr int kSlabRow = 80;        // bytes of a row of 32 columns: an odd number of 16-byte units
+// All products run on tcgen05 with accumulators in TMEM, 128 rows at a time: rows 0-63 are the query's side of the
+// unit's tokens, rows 64-127 the key's, so that everything that meets in one row of dq or dk lies in one TMEM lane
+// and one thread:
+//     D1 = [dO; Y] S0^T,  D2 = [Y; R] dS1^T,  D3 = [dO; Y] R^T,  D4 = [R'; N] K,  D5 = [.; R'^T Q + N^T K]
+// One block per SM walks over units with four kinds of warps: four fetch (slabs of 32 columns of dO, Y, R and of both
+// states through a ring; K, Q and the decays of a unit), one thread issues the products, three warps form
+// <S0, dS1> from the slabs, and two warpgroups take turns as epilogues: D3 becomes R' and N (a thread's row of D is a
+// running product along the row) in shared memory for D4 and D5, the others are scaled, summed and written.  D4 and D5
+// take the columns of D1 and D2 once these are in registers; with two sets of columns (dk <= 96) the products of
+// one unit run under the epilogue of the other.  As mma.sync with its operands through ldmatrix (every state
+// element loaded by four warps) the kernel took 308 us on the layer's gradient, bound by shared memory and by the
+// sequence of its phases.
+//
+// Operand tiles are without swizzle: 16-byte units [unit][row], whose 8 x 16-byte blocks are core matrices either way (rows
+// as M or N with K along the units, or rows as K).
+constexpr int kGradThreads = 512;      // 2 epilogue warpgroups, 1 fetching, 1 with the issuer and the inner products
+constexpr int kInnerWarps = 3;
+constexpr uint32_t kTmemCols = 512;
+static_assert(2 * 200 + 2 * 56 == 4 * 128, "the epilogues take what the others give back");
 
-struct Decays {                     // of one unit
-    float diag[4][256];             // D within a tile of 16 tokens
-    float pre[kG], suf[kG], c[kG], d[kG], beta[kG], whole[4], pad[4];
+struct Decays {                        // of one unit
+    float alpha[kG + 4], beta[kG], c[kG], d[kG];  // alpha[64] = 1 stands behind the last
 };
-struct Sums {                       // per token
-    float wq[kG], wk[kG], x[kG], mq[kG], my[kG], mr[kG], inner[kGradWarps], pad[4];
+struct Sums {                          // per token
+    float wq[kG], wk[kG], x[kG], mq[kG], mk[kG];
 };
 template <int KT> struct GradPlan {
-    static constexpr int kTile = kG * row_bytes<KT>();
+    static constexpr int kN = KT * 16;
+    static constexpr int kTile = kG * kN * 2;                                      // K or Q: [2 KT units][64 rows] x 16 bytes
     static constexpr int kHead = 2 * kTile + (int)sizeof(Decays);                  // K | Q | decays, two of them
+    static constexpr int kRows = 3 * kG * 64;                                      // dO | Y | R: [4 units][192 rows] x 16 bytes
     static constexpr int kImage = 2 * KT * 512;                                    // two column tiles of a state
-    static constexpr int kSlab = 3 * kG * kSlabRow + 2 * kImage;                   // dO | Y | R | S0 | dS1
+    static constexpr int kSlab = kRows + 2 * kImage;                               // rows | S0 | dS1
     static constexpr int kStages = KT <= 6 ? 3 : 2;
-    static constexpr int kXRow = KT * 16 + 4;                                      // f32 row of the exchange tile
-    static constexpr int kOffHead = 128, kOffSlab = kOffHead + 2 * kHead, kOffM = kOffSlab + kStages * kSlab,
-                         kOffX = kOffM + 2 * kG * kMRow, kOffSums = kOffX + kG * kXRow * 4,
-                         kTotal = kOffSums + 2 * (int)sizeof(Sums);
+    static constexpr int kOwn = 2 * kG * 128;                                      // [R'; N]: [8 units][128 rows] x 16 bytes
+    static constexpr int kFlip = 3 * kG * 128;                                     // N | R' | N: [24 units][64 rows] x 16 bytes
+    static constexpr int kOffHead = 256, kOffSlab = kOffHead + 2 * kHead, kOffT = kOffSlab + kStages * kSlab,
+                         kOffSums = kOffT + 2 * (kOwn + kFlip), kOffInner = kOffSums + 4 * (int)sizeof(Sums),
+                         kTotal = kOffInner + 2 * 16;
+    static constexpr int kSets = KT <= 6 ? 2 : 1;                                  // of accumulators
+    static constexpr uint32_t kSetCols = 2 * kN + kG;                              // D1 (D4) | D2 (D5) | D3
     static_assert(kTotal <= 227 * 1024, "shared memory of a block");
-    static_assert(kTile % 16 == 0 && kHead % 16 == 0 && kSlab % 16 == 0 && kOffX % 16 == 0, "16-byte copies");
+    static_assert(kSets * kSetCols <= kTmemCols, "TMEM");
+    static_assert(kHead % 16 == 0 && kSlab % 16 == 0 && kOffInner % 16 == 0 && sizeof(Decays) % 16 == 0, "16-byte copies");
+    // barriers
+    static constexpr int kHFull = 0, kHEmpty = 16, kFull = 32, kEmpty = kFull + 8 * 3, kAccFull = kEmpty + 8 * 3,
+                         kAccFree = kAccFull + 16, kReady = kAccFree + 16, kInFull = kReady + 16, kInner = kInFull + 16,
+                         kAbort = kInner + 16, kTmem = kAbort + 4;
+    static_assert(kTmem + 4 <= kOffHead, "barriers");
 };
-
-__device__ __forceinline__ void compute_sync() { ptx::named_bar_sync(1, kGradWarps * 32); }
-// acc (16 rows x KT * 16) += A (16 x 16) times 16 rows of a tile
-template <int KT>
-__device__ __forceinline__ void add_rows(float (&acc)[2 * KT][4], const uint32_t (&a)[4], uint32_t rows, int lane) {
-    const uint32_t at = rows + (((lane >> 3) & 1) * 8 + (lane & 7)) * row_bytes<KT>() + ((lane >> 3) >> 1) * 16;
-#pragma unroll
-    for (int i = 0; i < KT; ++i) {
-        uint32_t b[4];
-        ldsm4t(b, at + i * 32);
-        mma(acc[2 * i], a, b[0], b[1]);
-        mma(acc[2 * i + 1], a, b[2], b[3]);
-    }
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-    uint32_t x;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
-    return x;
-}
-// sums over dk of acc's two rows of this lane with the rows of a tile: lo for row gr, hi for row gr + 8
-template <int KT>
-__device__ __forceinline__ void row_dots(const float (&acc)[2 * KT][4], uint32_t rows, int lane, float &lo, float &hi) {
-    const uint32_t at = rows + (lane >> 2) * row_bytes<KT>() + (lane & 3) * 4;
-    lo = hi = 0.f;
-#pragma unroll
-    for (int n = 0; n < 2 * KT; ++n) {
-        const uint32_t x = lds32(at + n * 16), y = lds32(at + 8 * row_bytes<KT>() + n * 16);
-        lo = fmaf(acc[n][0], lo_f(x), fmaf(acc[n][1], hi_f(x), lo));
-        hi = fmaf(acc[n][2], lo_f(y), fmaf(acc[n][3], hi_f(y), hi));
-    }
-    lo += __shfl_xor_sync(0xffffffffu, lo, 1);
-    hi += __shfl_xor_sync(0xffffffffu, hi, 1);
-    lo += __shfl_xor_sync(0xffffffffu, lo, 2);
-    hi += __shfl_xor_sync(0xffffffffu, hi, 2);
-}
 
 struct GradArgs {
     const bf16 *q, *k, *dout;
@@ -376,368 +360,464 @@ struct GradArgs {
     unsigned units;         // slots * H
 };
 
+// The units that a block walks over, in the same order for all of its warps.
+struct Units {
+    unsigned unit;
+    int slot, h, n;  // n: how many came before
+    ChunkAt at;
+    __device__ __forceinline__ Units() : unit(blockIdx.x), n(-1) {}
+    __device__ __forceinline__ bool next(const Shape &p, unsigned units) {
+        if (n >= 0) unit += gridDim.x;
+        for (; unit < units; unit += gridDim.x) {
+            slot = (int)(unit / (unsigned)p.H);
+            h = (int)(unit % (unsigned)p.H);
+            if (chunk_of_slot<kG>(slot, p, at)) {
+                ++n;
+                return true;
+            }
+        }
+        return false;
+    }
+};
+
 template <int KT>
 __device__ __forceinline__ void grad_fetch(const Shape &p, const GradArgs &a, char *sm) {
     using P = GradPlan<KT>;
     const uint32_t base = ptx::smem_u32(sm);
-    const uint32_t hfull = base, hempty = base + 16, full = base + 32, empty = full + 8 * P::kStages;
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + 120);
-    const int id = threadIdx.x - kGradWarps * 32;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + P::kAbort);
+    const int id = threadIdx.x & 127;
     const int tiles = (p.dv + 15) / 16, slabs = (tiles + 1) / 2;
-    int n = 0, ns = 0;  // units and slabs so far
+    const int64_t vst = (int64_t)p.H * p.dv;
+    int ns = 0;          // slabs so far
+    int head_of = -1;    // a head that goes out with the last slab issued
     bool ok = true;
-    for (unsigned unit = blockIdx.x; ok && unit < a.units; unit += gridDim.x) {
-        const int slot = (int)(unit / (unsigned)p.H), h = (int)(unit % (unsigned)p.H), hk = h / p.group();
-        ChunkAt at;
-        if (!chunk_of_slot<kG>(slot, p, at)) continue;
-        const int hb = n & 1;
-        if (n >= 2 && !(ok = warp_wait(hempty + 8 * hb, (n / 2 + 1) & 1, abort_flag))) break;
-        ++n;
-        char *head = sm + P::kOffHead + hb * P::kHead;
+    // copies of the slab before the last one have landed (or all): they are made visible to the tensor cores
+    const auto publish = [&](int slab, int head) {
+        ptx::fence_async_shared();
+        ptx::mbar_arrive(base + P::kFull + 8 * (slab % P::kStages));
+        if (head >= 0) ptx::mbar_arrive(base + P::kHFull + 8 * head);
+    };
+    for (Units u; ok && u.next(p, a.units);) {
+        const int hb = u.n & 1, hk = u.h / p.group();
+        if (u.n >= 2 && !(ok = warp_wait(base + P::kHEmpty + 8 * hb, (u.n / 2 + 1) & 1, abort_flag))) break;
         const uint32_t ka = base + P::kOffHead + hb * P::kHead;
         {
-            const int t = id >> 1;  // two threads to a row
-            const bf16 *kr = a.k + ((at.row + t) * p.Hk + hk) * p.dk, *qr = a.q + ((at.row + t) * p.Hk + hk) * p.dk;
-            for (int u = id & 1; u < KT * 2; u += 2) {
-                const bool has = t < at.len && u * 8 < p.dk;
-                cp_async16(ka + t * row_bytes<KT>() + u * 16, has ? kr + u * 8 : a.k, has);
-                cp_async16(ka + P::kTile + t * row_bytes<KT>() + u * 16, has ? qr + u * 8 : a.q, has);
+            const int t = id & 63;  // two threads to a row, neighbouring rows in a warp
+            const bf16 *kr = a.k + ((u.at.row + t) * p.Hk + hk) * p.dk, *qr = a.q + ((u.at.row + t) * p.Hk + hk) * p.dk;
+            for (int x = id >> 6; x < KT * 2; x += 2) {
+                const bool has = t < u.at.len && x * 8 < p.dk;
+                cp_async16(ka + x * kG * 16 + t * 16, has ? kr + x * 8 : a.k, has);
+                cp_async16(ka + P::kTile + x * kG * 16 + t * 16, has ? qr + x * 8 : a.q, has);
             }
-            cp_async_arrive(hfull + 8 * hb);
         }
-        // the decays: thread j < 64 is column j of its tile of 16; both warps take all 64 tokens' decays
-        Decays &dc = *reinterpret_cast<Decays *>(head + 2 * P::kTile);
-        if (id < kG) {
-            const int lane = id & 31, b = id >> 4, j = id & 15;
-            float al[2];
+        Decays &dc = *reinterpret_cast<Decays *>(sm + P::kOffHead + hb * P::kHead + 2 * P::kTile);
+        if (id < 32) {  // products of decays up to and behind each token: lane owns tokens lane and 32 + lane
+            float al[2], up[2], down[2];
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                const int tok = m * 32 + lane;
-                al[m] = tok < at.len ? expf(load_gate<bf16>(a.g, (at.row + tok) * p.H + h, p.gate_f32)) : 1.f;
-            }
-            dc.beta[id] = id < at.len ? load_gate<bf16>(a.beta, (at.row + id) * p.H + h, p.gate_f32) : 0.f;
-            const float mine = id < 32 ? al[0] : al[1];
-            float f = 0.f, run = 1.f, pre = 1.f, whole0 = 1.f, whole1 = 1.f;
+                const int tok = m * 32 + id;
+                const bool live = tok < u.at.len;
+                al[m] = live ? expf(load_gate<bf16>(a.g, (u.at.row + tok) * p.H + u.h, p.gate_f32)) : 1.f;
+                dc.alpha[tok] = al[m];
+                dc.beta[tok] = live ? load_gate<bf16>(a.beta, (u.at.row + tok) * p.H + u.h, p.gate_f32) : 0.f;
+                up[m] = al[m];
+                const float behind = __shfl_down_sync(0xffffffffu, al[m], 1);
+                down[m] = id < 31 ? behind : 1.f;  // the product of the next ones, from this one's neighbour on
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float y = __shfl_sync(0xffffffffu, mine, i, 16);
-                run *= y;
-                if (i == j) pre = run;
-                f = i == j ? 1.f : f * y;
-                dc.diag[b][i * 16 + j] = f;
-                whole0 *= __shfl_sync(0xffffffffu, al[0], i, 16);
-                whole1 *= __shfl_sync(0xffffffffu, al[1], i, 16);
+                for (int w = 1; w < 32; w <<= 1) {
+                    const float x = __shfl_up_sync(0xffffffffu, up[m], w), y = __shfl_down_sync(0xffffffffu, down[m], w);
+                    if (id >= w) up[m] *= x;
+                    if (id + w < 32) down[m] *= y;
+                }
             }
-            float before = 1.f, after = 1.f;
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const float x = __shfl_sync(0xffffffffu, t < 2 ? whole0 : whole1, (t & 1) * 16);
-                if (t < b) before *= x;
-                if (t > b) after *= x;
-                if (id == 0) dc.whole[t] = x;
-            }
-            dc.pre[id] = pre;
-            dc.suf[id] = f;
-            dc.c[id] = before * pre;
-            dc.d[id] = f * after;
+            dc.alpha[kG + (id & 3)] = 1.f;
+            const float first = __shfl_sync(0xffffffffu, up[0], 31), second = __shfl_sync(0xffffffffu, up[1], 31);
+            dc.c[id] = up[0];
+            dc.c[32 + id] = first * up[1];
+            dc.d[id] = down[0] * second;
+            dc.d[32 + id] = down[1];
         }
-        ptx::mbar_arrive(hfull + 8 * hb);
-        const int64_t vst = (int64_t)p.H * p.dv;
-        const int t = id >> 1, u0 = (id & 1) * 2;  // two threads to a slab's row, two units each
-        const int64_t vat = (at.row + t) * vst + (int64_t)h * p.dv + u0 * 8;
-        const uint4 *s0 = a.s_images + image_at<KT>(p, slot, h, 0), *s1 = a.ds_images + image_at<KT>(p, slot, h, 0);
+        const uint4 *s0 = a.s_images + image_at<KT>(p, u.slot, u.h, 0), *s1 = a.ds_images + image_at<KT>(p, u.slot, u.h, 0);
         for (int s = 0; s < slabs; ++s, ++ns) {
             const int sg = ns % P::kStages;
-            if (ns >= P::kStages && !(ok = warp_wait(empty + 8 * sg, (ns / P::kStages + 1) & 1, abort_flag))) break;
+            if (ns >= P::kStages && !(ok = warp_wait(base + P::kEmpty + 8 * sg, (ns / P::kStages + 1) & 1, abort_flag))) break;
             const uint32_t to = base + P::kOffSlab + sg * P::kSlab;
             const int here = min(2, tiles - 2 * s) * KT * 512;
             if (id == 0) {
-                ptx::mbar_expect_tx(full + 8 * sg, 2 * here);
-                ptx::bulk_load_g2s(to + 3 * kG * kSlabRow, s0 + s * 2 * KT * 32, here, full + 8 * sg);
-                ptx::bulk_load_g2s(to + 3 * kG * kSlabRow + P::kImage, s1 + s * 2 * KT * 32, here, full + 8 * sg);
+                ptx::mbar_expect_tx(base + P::kFull + 8 * sg, 2 * here);
+                ptx::bulk_load_g2s(to + P::kRows, s0 + s * 2 * KT * 32, here, base + P::kFull + 8 * sg);
+                ptx::bulk_load_g2s(to + P::kRows + P::kImage, s1 + s * 2 * KT * 32, here, base + P::kFull + 8 * sg);
             }
+            // four threads to a row of 64 bytes, eight rows to a warp's copy
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const bool has = t < at.len && s * 32 + (u0 + u) * 8 < p.dv;
-                const int64_t off = has ? vat + s * 32 + u * 8 : 0;
-                const uint32_t dst = to + t * kSlabRow + (u0 + u) * 16;
+            for (int x = 0; x < 2; ++x) {
+                const int t = x * 32 + (id >> 2), w = id & 3;
+                const bool has = t < u.at.len && s * 32 + w * 8 < p.dv;
+                const int64_t off = has ? (u.at.row + t) * vst + (int64_t)u.h * p.dv + s * 32 + w * 8 : 0;
+                const uint32_t dst = to + w * 3 * kG * 16 + t * 16;
                 cp_async16(dst, a.dout + off, has);
-                cp_async16(dst + kG * kSlabRow, a.ys + off, has);
-                cp_async16(dst + 2 * kG * kSlabRow, a.resid + off, has);
+                cp_async16(dst + kG * 16, a.ys + off, has);
+                cp_async16(dst + 2 * kG * 16, a.resid + off, has);
             }
-            cp_async_arrive(full + 8 * sg);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (ns > 0) {
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                publish(ns - 1, head_of);
+            }
+            head_of = s == 0 ? hb : -1;
         }
     }
-    // nothing may be in flight into a block that ends early; a whole walk over units has waited for every stage
     cp_async_wait_all();
-    if (!ok) {
+    if (ok && ns > 0) publish(ns - 1, head_of);
+    if (!ok) {  // nothing may be in flight into a block that ends early
         *abort_flag = 1;
         for (int i = 0; i < P::kStages; ++i)
-            for (int par = 0; par < 2; ++par) ptx::mbar_wait(full + 8 * i, par, nullptr, kWaitNs / 1000);
+            for (int par = 0; par < 2; ++par) ptx::mbar_wait(base + P::kFull + 8 * i, par, nullptr, kWaitNs / 1000);
     }
 }
 
+// One thread: the products of the slabs into D1, D2 and D3, and of R' and N into D4 and D5 as soon as an epilogue has
+// them ready.
 template <int KT>
-__global__ void __launch_bounds__(kGradThreads)
-delta_grad_kernel(Shape p, GradArgs a) {
+__device__ __forceinline__ bool grad_issue(const Shape &p, const GradArgs &a, char *sm, uint32_t tmem) {
     using P = GradPlan<KT>;
-    extern __shared__ __align__(128) char sm_raw[];
-    const uint32_t base = ptx::smem_u32(sm_raw);
-    const uint32_t hfull = base, hempty = base + 16, full = base + 32, empty = full + 8 * P::kStages;
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm_raw + 120);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(hfull + 8 * i, 256);  // the fetching threads' copies, and their decays
-            ptx::mbar_init(hempty + 8 * i, kGradWarps);
-        }
-        for (int i = 0; i < P::kStages; ++i) {
-            ptx::mbar_init(full + 8 * i, 129);
-            ptx::mbar_init(empty + 8 * i, kGradWarps);
-        }
-        *abort_flag = 0;
-        ptx::fence_mbar_init();
-    }
-    __syncthreads();
-    if (warp >= kGradWarps) {
-        give_registers();
-        grad_fetch<KT>(p, a, sm_raw);
-        return;
-    }
-    take_registers();
-    // A tile of 16 tokens costs the more the further down it lies (T, R', N are triangular); the four SM quarters
-    // take warps in turn, so Y's tiles run against dO's.
-    const int role = warp >> 2, rt = role == 1 ? 3 - (warp & 3) : warp & 3;
-    const int gr = lane >> 2, tg = lane & 3, m8 = lane >> 3, r8 = lane & 7;
-    const int row0 = rt * 16 + gr;  // this lane's rows: row0 and row0 + 8
+    const uint32_t base = ptx::smem_u32(sm);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + P::kAbort);
     const int tiles = (p.dv + 15) / 16, slabs = (tiles + 1) / 2;
-    const uint32_t mt = base + P::kOffM, nt = mt + kG * kMRow;
-    float *exchange = reinterpret_cast<float *>(sm_raw + P::kOffX);
-    int n = 0, ns = 0;
-    for (unsigned unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
-        const int slot = (int)(unit / (unsigned)p.H), h = (int)(unit % (unsigned)p.H);
-        ChunkAt at;
-        if (!chunk_of_slot<kG>(slot, p, at)) continue;
-        const int hb = n & 1;
-        // a warp whose wait runs out goes on to the next barrier, where all learn of it and leave together
-        bool ok = warp_wait(hfull + 8 * hb, (n / 2) & 1, abort_flag);
-        Sums &sums = *reinterpret_cast<Sums *>(sm_raw + P::kOffSums + hb * sizeof(Sums));
-        ++n;
-        const uint32_t ks = base + P::kOffHead + hb * P::kHead, qs = ks + P::kTile;
-        const Decays &dc = *reinterpret_cast<const Decays *>(sm_raw + P::kOffHead + hb * P::kHead + 2 * P::kTile);
-        // T = do_i . r_j (or y_i . r_j) on and below the diagonal; A: this role's product with a state
-        float T[8][4] = {}, A[2 * KT][4] = {}, inner = 0.f;
+    constexpr uint32_t i_state = ptx::idesc_bf16(128, P::kN, 0, 1), i_rows = ptx::idesc_bf16(128, kG, 0, 0),
+                       i_flip = ptx::idesc_bf16(128, P::kN, 1, 1);
+    const auto inside = [&](int n) {  // D4 and D5 of unit n
+        ptx::tc_fence_after();
+        const uint32_t d = tmem + (n % P::kSets) * P::kSetCols, head = base + P::kOffHead + (n & 1) * P::kHead;
+        const uint32_t own = base + P::kOffT + (n & 1) * (P::kOwn + P::kFlip), flip = own + P::kOwn;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const uint64_t kd = ptx::smem_desc(head + s * 256, 128, kG * 16, ptx::kSwizzleNone),
+                           qd = ptx::smem_desc(head + P::kTile + s * 256, 128, kG * 16, ptx::kSwizzleNone);
+            ptx::mma_ss(d, ptx::smem_desc(own + s * 2 * 2 * kG * 16, 2 * kG * 16, 128, ptx::kSwizzleNone), kd, i_state, s > 0);
+            ptx::mma_ss(d + P::kN, ptx::smem_desc(flip + s * 256, 128, kG * 16, ptx::kSwizzleNone), qd, i_flip, s > 0);
+            ptx::mma_ss(d + P::kN, ptx::smem_desc(flip + 8 * kG * 16 + s * 256, 128, kG * 16, ptx::kSwizzleNone), kd, i_flip, 1);
+        }
+        ptx::mma_commit(base + P::kInFull + 8 * (n & 1));
+    };
+    int ns = 0, waiting = -1;  // a unit whose R' and N are still to come
+    const auto ready = [&](int n) { return base + P::kReady + 8 * (n & 1); };
+    for (Units u; u.next(p, a.units);) {
+        const int set = u.n % P::kSets;
+        if (u.n >= P::kSets &&
+            !ptx::mbar_wait(base + P::kAccFree + 8 * set, (u.n / P::kSets + 1) & 1, abort_flag, kWaitNs))
+            return false;
+        const uint32_t d = tmem + set * P::kSetCols;
         for (int s = 0; s < slabs; ++s, ++ns) {
             const int sg = ns % P::kStages;
-            ok = ok && warp_wait(full + 8 * sg, (ns / P::kStages) & 1, abort_flag);
-            if (!ok) break;
-            const uint32_t slab = base + P::kOffSlab + sg * P::kSlab;
-            const uint32_t a_at = slab + (role * kG + rt * 16 + (m8 & 1) * 8 + r8) * kSlabRow + (m8 >> 1) * 16;
-            const uint32_t b_at = slab + (2 * kG + (m8 >> 1) * 8 + r8) * kSlabRow + (m8 & 1) * 16;
-            const uint32_t image = slab + 3 * kG * kSlabRow + (role == 2 ? P::kImage : 0) + lane * 16;  // matrix lane / 8, row lane % 8
-            const int here = min(2, tiles - 2 * s);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (x >= here) break;
-                uint32_t f[4];
-                ldsm4(f, a_at + x * 32);
-#pragma unroll
-                for (int i = 0; i < KT; ++i) {
-                    uint32_t b[4];
-                    ldsm4t(b, image + (x * KT + i) * 512);
-                    mma(A[2 * i], f, b[0], b[1]);
-                    mma(A[2 * i + 1], f, b[2], b[3]);
+            // Until the slab is there, R' and N of the unit before may become ready; they do not wait for it, since the
+            // slab may be waiting for them (a head is free once its epilogue is done).
+            const uint64_t t0 = ptx::globaltimer();
+            while (!ptx::mbar_try_wait(base + P::kFull + 8 * sg, (ns / P::kStages) & 1)) {
+                if (waiting >= 0 && ptx::mbar_try_wait(ready(waiting), (waiting / 2) & 1)) {
+                    inside(waiting);
+                    waiting = -1;
                 }
-                if (role < 2) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        if (t <= rt) {
-                            uint32_t b[4];
-                            ldsm4(b, b_at + t * 16 * kSlabRow + x * 32);
-                            mma(T[2 * t], f, b[0], b[1]);
-                            mma(T[2 * t + 1], f, b[2], b[3]);
-                        }
-                }
+                if (*abort_flag || ptx::globaltimer() - t0 > kWaitNs) return false;
             }
-            for (int i = tid; i < here * KT * 32; i += kGradWarps * 32) {  // <S0, dS1>
-                const uint4 x = lds128(slab + 3 * kG * kSlabRow + i * 16),
-                            y = lds128(slab + 3 * kG * kSlabRow + P::kImage + i * 16);
+            ptx::tc_fence_after();
+            const uint32_t rows = base + P::kOffSlab + sg * P::kSlab, image = rows + P::kRows;
+            for (int x = 0; x < min(2, tiles - 2 * s); ++x) {
+                constexpr uint32_t kUnit = 3 * kG * 16;
+                const uint32_t r = rows + x * 2 * kUnit, i = image + x * KT * 512;
+                const uint32_t more = s > 0 || x > 0;
+                const uint64_t top = ptx::smem_desc(r, kUnit, 128, ptx::kSwizzleNone);
+                ptx::mma_ss(d, top, ptx::smem_desc(i, 128, 256, ptx::kSwizzleNone), i_state, more);
+                ptx::mma_ss(d + P::kN, ptx::smem_desc(r + kG * 16, kUnit, 128, ptx::kSwizzleNone),
+                            ptx::smem_desc(i + P::kImage, 128, 256, ptx::kSwizzleNone), i_state, more);
+                ptx::mma_ss(d + 2 * P::kN, top, ptx::smem_desc(r + 2 * kG * 16, kUnit, 128, ptx::kSwizzleNone), i_rows, more);
+            }
+            ptx::mma_commit(base + P::kEmpty + 8 * sg);
+            if (waiting >= 0 && ptx::mbar_try_wait(ready(waiting), (waiting / 2) & 1)) {
+                inside(waiting);
+                waiting = -1;
+            }
+        }
+        ptx::mma_commit(base + P::kAccFull + 8 * set);
+        if (waiting >= 0) {
+            if (!ptx::mbar_wait(ready(waiting), (waiting / 2) & 1, abort_flag, kWaitNs)) return false;
+            inside(waiting);
+        }
+        waiting = u.n;
+        if (P::kSets == 1) {  // the next unit's products need this one's accumulators
+            if (!ptx::mbar_wait(ready(waiting), (waiting / 2) & 1, abort_flag, kWaitNs)) return false;
+            inside(waiting);
+            waiting = -1;
+        }
+    }
+    if (waiting >= 0) {
+        if (!ptx::mbar_wait(ready(waiting), (waiting / 2) & 1, abort_flag, kWaitNs)) return false;
+        inside(waiting);
+    }
+    return true;
+}
+
+// Three warps: <S0, dS1> of each unit, as the slabs come by.
+template <int KT>
+__device__ __forceinline__ bool grad_inner(const Shape &p, const GradArgs &a, char *sm, int warp, int lane) {
+    using P = GradPlan<KT>;
+    const uint32_t base = ptx::smem_u32(sm);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + P::kAbort);
+    const int tiles = (p.dv + 15) / 16, slabs = (tiles + 1) / 2;
+    int ns = 0;
+    for (Units u; u.next(p, a.units);) {
+        // a unit's head comes once the epilogue two units before, which reads this sum's place, is done
+        if (!warp_wait(base + P::kHFull + 8 * (u.n & 1), (u.n / 2) & 1, abort_flag)) return false;
+        float inner = 0.f;
+        for (int s = 0; s < slabs; ++s, ++ns) {
+            const int sg = ns % P::kStages;
+            if (!warp_wait(base + P::kFull + 8 * sg, (ns / P::kStages) & 1, abort_flag)) return false;
+            const uint32_t image = base + P::kOffSlab + sg * P::kSlab + P::kRows;
+            for (int i = warp * 32 + lane; i < min(2, tiles - 2 * s) * KT * 32; i += kInnerWarps * 32) {
+                const uint4 x = lds128(image + i * 16), y = lds128(image + P::kImage + i * 16);
                 const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) inner = fmaf(lo_f(xw[e]), lo_f(yw[e]), fmaf(hi_f(xw[e]), hi_f(yw[e]), inner));
             }
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(empty + 8 * sg);
-        }
-        if (!ok && lane == 0) {
-            *abort_flag = 1;
-            record_status(GLA_ERR_TIMEOUT);
+            if (lane == 0) ptx::mbar_arrive(base + P::kEmpty + 8 * sg);
         }
         for (int m = 16; m > 0; m >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, m);
-        if (lane == 0) sums.inner[warp] = inner;
-        float lo, hi;
-        // the state's part of dq and dk, and its share of dg
-        {
-            const float *v = role == 2 ? dc.d : dc.c;
-            float f0 = v[row0], f1 = v[row0 + 8];
-            if (role > 0) {
-                f0 *= role == 1 ? -dc.beta[row0] : dc.beta[row0];
-                f1 *= role == 1 ? -dc.beta[row0 + 8] : dc.beta[row0 + 8];
-            }
-#pragma unroll
-            for (int i = 0; i < 2 * KT; ++i) {
-                A[i][0] *= f0; A[i][1] *= f0; A[i][2] *= f1; A[i][3] *= f1;
-            }
-            row_dots<KT>(A, (role ? ks : qs) + rt * 16 * row_bytes<KT>(), lane, lo, hi);
-            float *to = role == 0 ? sums.wq : role == 1 ? sums.wk : sums.x;
-            if (tg == 0) {
-                to[row0] = lo;
-                to[row0 + 8] = hi;
-            }
+        if (lane == 0) {
+            reinterpret_cast<float *>(sm + P::kOffInner)[(u.n & 1) * 4 + warp] = inner;
+            ptx::mbar_arrive(base + P::kInner + 8 * (u.n & 1));
         }
-        if (role < 2) {  // R' or N
-            float between[4];  // whole tiles strictly between tile t and this warp's
+    }
+    return true;
+}
+
+// a row of the unit's K or Q tile, eight elements at a time
+__device__ __forceinline__ void row8(uint32_t tile, int row, int unit, float (&x)[8]) {
+    const uint4 t = lds128(tile + unit * kG * 16 + row * 16);
+    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                float f = 1.f;
-                for (int m = t + 1; m < rt; ++m) f *= dc.whole[m];
-                between[t] = f;
-            }
-            float own0 = 0.f, own1 = 0.f;  // the diagonal's two elements, where tg == gr / 2
-            const float p0 = dc.pre[row0], p1 = dc.pre[row0 + 8];
-            const float g0 = role ? -dc.beta[row0] : 1.f, g1 = role ? -dc.beta[row0 + 8] : 1.f;
+    for (int e = 0; e < 4; ++e) {
+        x[2 * e] = lo_f(w[e]);
+        x[2 * e + 1] = hi_f(w[e]);
+    }
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// A warpgroup: every second unit; thread = row of 128 (token row % 64 on the query's or the key's side).
+template <int KT>
+__device__ __forceinline__ bool grad_epilogue(const Shape &p, const GradArgs &a, char *sm, uint32_t tmem, int group) {
+    using P = GradPlan<KT>;
+    const uint32_t base = ptx::smem_u32(sm);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + P::kAbort);
+    const int id = threadIdx.x & 127, warp = id >> 5, lane = id & 31, i = id & 63;
+    const bool key = id >= kG;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;  // this warp's TMEM lanes
+    int turn = 0;
+    for (Units u; u.next(p, a.units);) {
+        if ((u.n & 1) != group) continue;
+        const int set = u.n % P::kSets;
+        Sums &sums = reinterpret_cast<Sums *>(sm + P::kOffSums)[group * 2 + (turn++ & 1)];
+        const uint32_t head = base + P::kOffHead + group * P::kHead, mine = head + (key ? 0 : P::kTile);
+        const Decays &dc = *reinterpret_cast<const Decays *>(sm + P::kOffHead + group * P::kHead + 2 * P::kTile);
+        const uint32_t d = tmem + set * P::kSetCols + lanes;
+        bool ok = warp_wait(base + P::kHFull + 8 * group, (u.n / 2) & 1, abort_flag) &&
+                  warp_wait(base + P::kAccFull + 8 * set, (u.n / P::kSets) & 1, abort_flag);
+        float A[P::kN], w = 0.f, x = 0.f;
+        if (ok) {
+            ptx::tc_fence_after();
+            const float be = dc.beta[i], f1 = key ? -dc.c[i] * be : dc.c[i], f2 = dc.d[i] * be;
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
-                if (t <= 2 * rt + 1) {
-                    const int j = t * 8 + 2 * tg;
-                    const float b0 = dc.beta[j], b1 = dc.beta[j + 1];
-                    float x[4];
-                    if ((t >> 1) == rt) {
-                        const float *D = dc.diag[rt] + gr * 16 + (j & 15);
-                        const float2 u = *reinterpret_cast<const float2 *>(D), v = *reinterpret_cast<const float2 *>(D + 128);
-                        const int i0 = row0, i1 = row0 + 8, off = role;  // N leaves the diagonal out
-                        if (t == 2 * rt) own0 = gr & 1 ? T[t][1] : T[t][0];
-                        else own1 = gr & 1 ? T[t][3] : T[t][2];
-                        x[0] = j + off <= i0 ? g0 * b0 * u.x * T[t][0] : 0.f;
-                        x[1] = j + 1 + off <= i0 ? g0 * b1 * u.y * T[t][1] : 0.f;
-                        x[2] = j + off <= i1 ? g1 * b0 * v.x * T[t][2] : 0.f;
-                        x[3] = j + 1 + off <= i1 ? g1 * b1 * v.y * T[t][3] : 0.f;
-                    } else {
-                        const float m = between[t >> 1], s0 = m * dc.suf[j] * b0, s1 = m * dc.suf[j + 1] * b1;
-                        x[0] = g0 * p0 * s0 * T[t][0];
-                        x[1] = g0 * p0 * s1 * T[t][1];
-                        x[2] = g1 * p1 * s0 * T[t][2];
-                        x[3] = g1 * p1 * s1 * T[t][3];
+            for (int b = 0; b < P::kN; b += 32) {
+                uint32_t r[32];
+                ptx::tmem_ld32(d + b, r);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) A[b + e] = f1 * __uint_as_float(r[e]);
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    float m[8];
+                    row8(mine, i, (b + e) / 8, m);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) w = fmaf(m[y], A[b + e + y], w);
+                }
+                if (key) {
+                    ptx::tmem_ld32(d + P::kN + b, r);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        float m[8];
+                        row8(mine, i, (b + e) / 8, m);
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            const float v = f2 * __uint_as_float(r[e + y]);
+                            x = fmaf(m[y], v, x);
+                            A[b + e + y] += v;
+                        }
                     }
-                    char *to = sm_raw + P::kOffM + (role * kG + row0) * kMRow + j * 2;
-                    *reinterpret_cast<uint32_t *>(to) = pack(x[0], x[1]);
-                    *reinterpret_cast<uint32_t *>(to + 8 * kMRow) = pack(x[2], x[3]);
-                }
-            if (role && tg == gr >> 1) {
-                if (row0 < at.len) store_gate<bf16>(a.dbeta, (at.row + row0) * p.H + h, p.gate_f32, own0);
-                if (row0 + 8 < at.len) store_gate<bf16>(a.dbeta, (at.row + row0 + 8) * p.H + h, p.gate_f32, own1);
-            }
-        }
-        if (any_of<1, kGradWarps * 32>(!ok)) return;  // R' and N are whole
-        {
-            float acc[2 * KT][4] = {};
-            if (role < 2) {  // R' K or N K
-                const uint32_t own = (role ? nt : mt) + (rt * 16 + (m8 & 1) * 8 + r8) * kMRow + (m8 >> 1) * 16;
-                for (int t = 0; t <= rt; ++t) {
-                    uint32_t f[4];
-                    ldsm4(f, own + t * 32);
-                    add_rows<KT>(acc, f, ks + t * 16 * row_bytes<KT>(), lane);
-                }
-            } else {  // R'^T Q + N^T K
-                const uint32_t flip = ((m8 >> 1) * 8 + r8) * kMRow + rt * 32 + (m8 & 1) * 16;
-                for (int t = rt; t < 4; ++t) {
-                    uint32_t f[4];
-                    ldsm4t(f, mt + flip + t * 16 * kMRow);
-                    add_rows<KT>(acc, f, qs + t * 16 * row_bytes<KT>(), lane);
-                    ldsm4t(f, nt + flip + t * 16 * kMRow);
-                    add_rows<KT>(acc, f, ks + t * 16 * row_bytes<KT>(), lane);
                 }
             }
-            row_dots<KT>(acc, (role ? ks : qs) + rt * 16 * row_bytes<KT>(), lane, lo, hi);
-            float *to = role == 0 ? sums.mq : role == 1 ? sums.my : sums.mr;
-            if (tg == 0) {
-                to[row0] = role == 2 ? lo : -lo;
-                to[row0 + 8] = role == 2 ? hi : -hi;
-            }
-#pragma unroll
-            for (int i = 0; i < 2 * KT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) A[i][e] += acc[i][e];
-        }
-        if (role == 2) {
-#pragma unroll
-            for (int i = 0; i < 2 * KT; ++i) {
-                *reinterpret_cast<float2 *>(exchange + row0 * P::kXRow + i * 8 + 2 * tg) = make_float2(A[i][0], A[i][1]);
-                *reinterpret_cast<float2 *>(exchange + (row0 + 8) * P::kXRow + i * 8 + 2 * tg) = make_float2(A[i][2], A[i][3]);
-            }
-        }
-        compute_sync();  // R's part of dk and all sums are there; K, Q and the decays are read
-        if (role == 1) {
-#pragma unroll
-            for (int i = 0; i < 2 * KT; ++i) {
-                const float2 u = *reinterpret_cast<const float2 *>(exchange + row0 * P::kXRow + i * 8 + 2 * tg);
-                const float2 v = *reinterpret_cast<const float2 *>(exchange + (row0 + 8) * P::kXRow + i * 8 + 2 * tg);
-                A[i][0] += u.x; A[i][1] += u.y; A[i][2] += v.x; A[i][3] += v.y;
-            }
-        }
-        if (role < 2 && a.dq_part == nullptr) {
-            // 64 columns at a time through this warp's own 16 rows of R' or N, which the barrier has left free
-            const uint32_t tile = (role ? nt : mt) + rt * 16 * kMRow;
-            bf16 *to = (role ? a.dk : a.dq) + ((at.row + rt * 16) * p.H + h) * p.dk;
-#pragma unroll
-            for (int i0 = 0; i0 < 2 * KT; i0 += 8) {
-                __syncwarp();
-#pragma unroll
-                for (int i = i0; i < (i0 + 8 < 2 * KT ? i0 + 8 : 2 * KT); i += 2)
-                    stsm4(tile + ((m8 & 1) * 8 + r8) * kMRow + (i - i0 + (m8 >> 1)) * 16, pack(A[i][0], A[i][1]),
-                          pack(A[i][2], A[i][3]), pack(A[i + 1][0], A[i + 1][1]), pack(A[i + 1][2], A[i + 1][3]));
-                __syncwarp();
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int row = x * 4 + (lane >> 3), u = i0 + (lane & 7);
-                    if (rt * 16 + row < at.len && u * 8 < p.dk)
-                        *reinterpret_cast<uint4 *>(to + (int64_t)row * p.H * p.dk + u * 8) =
-                            lds128(tile + row * kMRow + (lane & 7) * 16);
-                }
-            }
-            __syncwarp();
-        } else if (role < 2) {
-            float *to = (role ? a.dk_part : a.dq_part) + ((at.row + row0) * p.H + h) * p.dk + 2 * tg;
-            const int64_t far = (int64_t)8 * p.H * p.dk;
-#pragma unroll
-            for (int i = 0; i < 2 * KT; ++i)
-                if (i * 8 < p.dk) {
-                    if (row0 < at.len) *reinterpret_cast<float2 *>(to + i * 8) = make_float2(A[i][0], A[i][1]);
-                    if (row0 + 8 < at.len) *reinterpret_cast<float2 *>(to + far + i * 8) = make_float2(A[i][2], A[i][3]);
-                }
-        }
-        if (warp == 8) {  // dg: lane owns tokens 2 lane and 2 lane + 1
+            (key ? sums.wk : sums.wq)[i] = w;
+            if (key) sums.x[i] = x;
+            // R' (query) or N (key), from the row's end: f = D_ij, zero for j > i
+            const uint32_t own = base + P::kOffT + group * (P::kOwn + P::kFlip), flip = own + P::kOwn;
+            const float g = key ? -be : 1.f;
             float f = 0.f;
 #pragma unroll
-            for (int m = 0; m < kGradWarps; ++m) f += sums.inner[m];
-            f *= dc.c[kG - 1];
-            const int i = 2 * lane;
-            const float w0 = sums.wq[i] + sums.wk[i], w1 = sums.wq[i + 1] + sums.wk[i + 1];
-            const float x0 = sums.x[i] + (sums.mq[i] + sums.my[i] + sums.mr[i]),
-                        x1 = sums.x[i + 1] + (sums.mq[i + 1] + sums.my[i + 1] + sums.mr[i + 1]);
+            for (int b = 32; b >= 0; b -= 32) {
+                uint32_t r[32];
+                ptx::tmem_ld32(d + 2 * P::kN + b, r);
+                ptx::tmem_wait_ld();
+                if (key && i >= b && i < b + 32) {
+                    float own_beta = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (b + e == i) own_beta = __uint_as_float(r[e]);
+                    if (i < u.at.len) store_gate<bf16>(a.dbeta, (u.at.row + i) * p.H + u.h, p.gate_f32, own_beta);
+                }
+#pragma unroll
+                for (int e0 = 24; e0 >= 0; e0 -= 8) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 7; e >= 0; --e) {
+                        const int j = b + e0 + e;
+                        f = j == i ? 1.f : f * dc.alpha[j + 1];
+                        const float z = f * dc.beta[j] * g * __uint_as_float(r[e0 + e]);
+                        v[e] = key && j == i ? 0.f : z;
+                    }
+                    const uint32_t q0 = pack(v[0], v[1]), q1 = pack(v[2], v[3]), q2 = pack(v[4], v[5]), q3 = pack(v[6], v[7]);
+                    const uint32_t unit = (b + e0) / 8;
+                    sts128(own + unit * 2 * kG * 16 + id * 16, q0, q1, q2, q3);
+                    if (key) {
+                        sts128(flip + unit * kG * 16 + i * 16, q0, q1, q2, q3);
+                        sts128(flip + (16 + unit) * kG * 16 + i * 16, q0, q1, q2, q3);
+                    } else {
+                        sts128(flip + (8 + unit) * kG * 16 + i * 16, q0, q1, q2, q3);
+                    }
+                }
+            }
+            ptx::fence_async_shared();
+            ptx::tc_fence_before();
+        }
+        ptx::mbar_arrive(base + P::kReady + 8 * group);
+        ok = ok && warp_wait(base + P::kInFull + 8 * group, (u.n / 2) & 1, abort_flag);
+        if (ok) {
+            ptx::tc_fence_after();
+            float m = 0.f;
+#pragma unroll
+            for (int b = 0; b < P::kN; b += 32) {
+                uint32_t r[32], t[32];
+                ptx::tmem_ld32(d + b, r);
+                if (key) ptx::tmem_ld32(d + P::kN + b, t);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    float v[8];
+                    row8(mine, i, (b + e) / 8, v);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        const float n = __uint_as_float(r[e + y]), o = key ? __uint_as_float(t[e + y]) : 0.f;
+                        m = fmaf(v[y], o - n, m);
+                        A[b + e + y] += n + o;
+                    }
+                }
+            }
+            ptx::tc_fence_before();
+            (key ? sums.mk : sums.mq)[i] = m;
+        }
+        ptx::mbar_arrive(base + P::kAccFree + 8 * set);
+        if (ok && i < u.at.len) {
+            const int64_t to = ((u.at.row + i) * p.H + u.h) * p.dk;
+            if (a.dq_part == nullptr) {
+                uint4 *out = reinterpret_cast<uint4 *>((key ? a.dk : a.dq) + to);
+#pragma unroll
+                for (int e = 0; e < P::kN; e += 8)
+                    if (e < p.dk)
+                        out[e / 8] = make_uint4(pack(A[e], A[e + 1]), pack(A[e + 2], A[e + 3]), pack(A[e + 4], A[e + 5]),
+                                                pack(A[e + 6], A[e + 7]));
+            } else {
+                float4 *out = reinterpret_cast<float4 *>((key ? a.dk_part : a.dq_part) + to);
+#pragma unroll
+                for (int e = 0; e < P::kN; e += 4)
+                    if (e < p.dk) out[e / 4] = make_float4(A[e], A[e + 1], A[e + 2], A[e + 3]);
+            }
+        }
+        ok = ok && warp_wait(base + P::kInner + 8 * group, (u.n / 2) & 1, abort_flag);
+        // all sums of the unit are there
+        if (group == 0 ? any_of<1, 128>(!ok) : any_of<2, 128>(!ok)) return false;
+        if (warp == 0) {  // dg: lane owns tokens 2 lane and 2 lane + 1
+            const float *in = reinterpret_cast<const float *>(sm + P::kOffInner) + (u.n & 1) * 4;
+            const float f = ((in[0] + in[1]) + in[2]) * dc.c[kG - 1];
+            const int j = 2 * lane;
+            const float w0 = sums.wq[j] + sums.wk[j], w1 = sums.wq[j + 1] + sums.wk[j + 1];
+            const float x0 = sums.x[j] + (sums.mq[j] + sums.mk[j]), x1 = sums.x[j + 1] + (sums.mq[j + 1] + sums.mk[j + 1]);
             float pre = x0 + x1, suf = w0 + w1;
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
-                const float u = __shfl_up_sync(0xffffffffu, pre, m), v = __shfl_down_sync(0xffffffffu, suf, m);
-                if (lane >= m) pre += u;
-                if (lane + m < 32) suf += v;
+                const float y = __shfl_up_sync(0xffffffffu, pre, m), z = __shfl_down_sync(0xffffffffu, suf, m);
+                if (lane >= m) pre += y;
+                if (lane + m < 32) suf += z;
             }
             const float left = pre - (x0 + x1);  // tokens before 2 lane
-            if (i < at.len) store_gate<bf16>(a.dg, (at.row + i) * p.H + h, p.gate_f32, f + left + suf);
-            if (i + 1 < at.len) store_gate<bf16>(a.dg, (at.row + i + 1) * p.H + h, p.gate_f32, f + left + x0 + (suf - w0));
+            if (j < u.at.len) store_gate<bf16>(a.dg, (u.at.row + j) * p.H + u.h, p.gate_f32, f + left + suf);
+            if (j + 1 < u.at.len) store_gate<bf16>(a.dg, (u.at.row + j + 1) * p.H + u.h, p.gate_f32, f + left + x0 + (suf - w0));
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(hempty + 8 * hb);
+        if (lane == 0) ptx::mbar_arrive(base + P::kHEmpty + 8 * group);
+    }
+    return true;
+}
+
+template <int KT>
+__global__ void __launch_bounds__(kGradThreads, 1)
+delta_grad_kernel(Shape p, GradArgs a) {
+    using P = GradPlan<KT>;
+    extern __shared__ __align__(128) char sm_raw[];
+    const uint32_t base = ptx::smem_u32(sm_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(base + P::kHFull + 8 * i, 128);
+            ptx::mbar_init(base + P::kHEmpty + 8 * i, 4);
+            ptx::mbar_init(base + P::kAccFull + 8 * i, 1);
+            ptx::mbar_init(base + P::kAccFree + 8 * i, 128);
+            ptx::mbar_init(base + P::kReady + 8 * i, 128);
+            ptx::mbar_init(base + P::kInFull + 8 * i, 1);
+            ptx::mbar_init(base + P::kInner + 8 * i, kInnerWarps);
+        }
+        for (int i = 0; i < P::kStages; ++i) {
+            ptx::mbar_init(base + P::kFull + 8 * i, 129);   // the fetching threads, and the states' bytes
+            ptx::mbar_init(base + P::kEmpty + 8 * i, 1 + kInnerWarps);
+        }
+        *reinterpret_cast<volatile int *>(sm_raw + P::kAbort) = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 12) ptx::tmem_alloc(base + P::kTmem, kTmemCols);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm_raw + P::kTmem);
+    bool ok = true;
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        ok = grad_epilogue<KT>(p, a, sm_raw, tmem, warp >> 2);
+    } else {
+        give_registers();
+        if (warp < 12) grad_fetch<KT>(p, a, sm_raw);
+        else if (warp == 12) { if (lane == 0) ok = grad_issue<KT>(p, a, sm_raw, tmem); }
+        else ok = grad_inner<KT>(p, a, sm_raw, warp - 13, lane);
+    }
+    if (!ok) {
+        *reinterpret_cast<volatile int *>(sm_raw + P::kAbort) = 1;
+        record_status(GLA_ERR_TIMEOUT);
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();  // every wait above is bounded, so all warps come here
+    if (warp == 12) {
+        ptx::tmem_relinquish();
+        ptx::tmem_dealloc(tmem, kTmemCols);
     }
 }
 

@@ -231,7 +231,7 @@ struct FwdArgs {
 };
 
 template <int KT, bool kSegment>
-__global__ void __launch_bounds__(kMaxThreads)
+__global__ void __launch_bounds__(kMaxThreads, 1)
 delta_fwd_kernel(Shape p, Walk w, FwdArgs a) {
     extern __shared__ __align__(128) char sm_raw[];
     constexpr int kRow = row_bytes<KT>(), kTile = kC * kRow, kV = (kSegment ? 1 : 2) * kTile;
