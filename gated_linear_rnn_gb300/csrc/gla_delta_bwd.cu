@@ -331,11 +331,11 @@ template <int KT> struct GradPlan {
     static constexpr int kRows = 3 * kG * 64;                                      // dO | Y | R: [4 units][192 rows] x 16 bytes
     static constexpr int kImage = 2 * KT * 512;                                    // two column tiles of a state
     static constexpr int kSlab = kRows + 2 * kImage;                               // rows | S0 | dS1
-    static constexpr int kStages = KT <= 6 ? 3 : 2;
+    static constexpr int kStages = KT <= 6 ? 5 : 4;
     static constexpr int kOwn = 2 * kG * 128;                                      // [R'; N]: [8 units][128 rows] x 16 bytes
     static constexpr int kFlip = 3 * kG * 128;                                     // N | R' | N: [24 units][64 rows] x 16 bytes
     static constexpr int kOffHead = 256, kOffSlab = kOffHead + 2 * kHead, kOffT = kOffSlab + kStages * kSlab,
-                         kOffSums = kOffT + 2 * (kOwn + kFlip), kOffInner = kOffSums + 4 * (int)sizeof(Sums),
+                         kOffSums = kOffT + kOwn + kFlip, kOffInner = kOffSums + 4 * (int)sizeof(Sums),
                          kTotal = kOffInner + 2 * 16;
     static constexpr int kSets = KT <= 6 ? 2 : 1;                                  // of accumulators
     static constexpr uint32_t kSetCols = 2 * kN + kG;                              // D1 (D4) | D2 (D5) | D3
@@ -343,7 +343,7 @@ template <int KT> struct GradPlan {
     static_assert(kSets * kSetCols <= kTmemCols, "TMEM");
     static_assert(kHead % 16 == 0 && kSlab % 16 == 0 && kOffInner % 16 == 0 && sizeof(Decays) % 16 == 0, "16-byte copies");
     // barriers
-    static constexpr int kHFull = 0, kHEmpty = 16, kFull = 32, kEmpty = kFull + 8 * 3, kAccFull = kEmpty + 8 * 3,
+    static constexpr int kHFull = 0, kHEmpty = 16, kFull = 32, kEmpty = kFull + 8 * kStages, kAccFull = kEmpty + 8 * kStages,
                          kAccFree = kAccFull + 16, kReady = kAccFree + 16, kInFull = kReady + 16, kInner = kInFull + 16,
                          kAbort = kInner + 16, kTmem = kAbort + 4;
     static_assert(kTmem + 4 <= kOffHead, "barriers");
@@ -388,18 +388,30 @@ __device__ __forceinline__ void grad_fetch(const Shape &p, const GradArgs &a, ch
     const int id = threadIdx.x & 127;
     const int tiles = (p.dv + 15) / 16, slabs = (tiles + 1) / 2;
     const int64_t vst = (int64_t)p.H * p.dv;
-    int ns = 0;          // slabs so far
-    int head_of = -1;    // a head that goes out with the last slab issued
+    // Three slabs are on their way at a time (and the head that came before one of them): 74 KB, which is what a latency
+    // of two microseconds takes at this SM's share of the bandwidth.
+    constexpr int kAhead = 3;
+    int ns = 0, out = 0;   // slabs issued, and made known
+    uint32_t heads = 0;    // 2 bits for each of the last slabs, the newest lowest: 1 + the head that came before it
     bool ok = true;
-    // copies of the slab before the last one have landed (or all): they are made visible to the tensor cores
-    const auto publish = [&](int slab, int head) {
+    // the copies of slab `out` have landed: they are made visible to the tensor cores
+    const auto publish = [&]() {
+        const uint32_t head = (heads >> (2 * (ns - 1 - out))) & 3;
         ptx::fence_async_shared();
-        ptx::mbar_arrive(base + P::kFull + 8 * (slab % P::kStages));
-        if (head >= 0) ptx::mbar_arrive(base + P::kHFull + 8 * head);
+        ptx::mbar_arrive(base + P::kFull + 8 * (out % P::kStages));
+        if (head) ptx::mbar_arrive(base + P::kHFull + 8 * (head - 1));
+        ++out;
     };
     for (Units u; ok && u.next(p, a.units);) {
         const int hb = u.n & 1, hk = u.h / p.group();
-        if (u.n >= 2 && !(ok = warp_wait(base + P::kHEmpty + 8 * hb, (u.n / 2 + 1) & 1, abort_flag))) break;
+        if (u.n >= 2) {
+            // before a wait, what has been asked for goes out whole: the others need it to come to its end
+            if (!__all_sync(0xffffffffu, ptx::mbar_try_wait(base + P::kHEmpty + 8 * hb, (u.n / 2 + 1) & 1))) {
+                cp_async_wait_all();
+                while (out < ns) publish();
+            }
+            if (!(ok = warp_wait(base + P::kHEmpty + 8 * hb, (u.n / 2 + 1) & 1, abort_flag))) break;
+        }
         const uint32_t ka = base + P::kOffHead + hb * P::kHead;
         {
             const int t = id & 63;  // two threads to a row, neighbouring rows in a warp
@@ -438,7 +450,7 @@ __device__ __forceinline__ void grad_fetch(const Shape &p, const GradArgs &a, ch
             dc.d[32 + id] = down[1];
         }
         const uint4 *s0 = a.s_images + image_at<KT>(p, u.slot, u.h, 0), *s1 = a.ds_images + image_at<KT>(p, u.slot, u.h, 0);
-        for (int s = 0; s < slabs; ++s, ++ns) {
+        for (int s = 0; s < slabs; ++s) {
             const int sg = ns % P::kStages;
             if (ns >= P::kStages && !(ok = warp_wait(base + P::kEmpty + 8 * sg, (ns / P::kStages + 1) & 1, abort_flag))) break;
             const uint32_t to = base + P::kOffSlab + sg * P::kSlab;
@@ -460,15 +472,15 @@ __device__ __forceinline__ void grad_fetch(const Shape &p, const GradArgs &a, ch
                 cp_async16(dst + 2 * kG * 16, a.resid + off, has);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
-            if (ns > 0) {
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-                publish(ns - 1, head_of);
+            heads = heads << 2 | (s == 0 ? 1 + hb : 0);
+            if (++ns - out > kAhead) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+                publish();
             }
-            head_of = s == 0 ? hb : -1;
         }
     }
     cp_async_wait_all();
-    if (ok && ns > 0) publish(ns - 1, head_of);
+    while (ok && out < ns) publish();
     if (!ok) {  // nothing may be in flight into a block that ends early
         *abort_flag = 1;
         for (int i = 0; i < P::kStages; ++i)
@@ -489,7 +501,7 @@ __device__ __forceinline__ bool grad_issue(const Shape &p, const GradArgs &a, ch
     const auto inside = [&](int n) {  // D4 and D5 of unit n
         ptx::tc_fence_after();
         const uint32_t d = tmem + (n % P::kSets) * P::kSetCols, head = base + P::kOffHead + (n & 1) * P::kHead;
-        const uint32_t own = base + P::kOffT + (n & 1) * (P::kOwn + P::kFlip), flip = own + P::kOwn;
+        const uint32_t own = base + P::kOffT, flip = own + P::kOwn;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const uint64_t kd = ptx::smem_desc(head + s * 256, 128, kG * 16, ptx::kSwizzleNone),
@@ -661,8 +673,10 @@ __device__ __forceinline__ bool grad_epilogue(const Shape &p, const GradArgs &a,
             (key ? sums.wk : sums.wq)[i] = w;
             if (key) sums.x[i] = x;
             // R' (query) or N (key), from the row's end: f = D_ij, zero for j > i
-            const uint32_t own = base + P::kOffT + group * (P::kOwn + P::kFlip), flip = own + P::kOwn;
+            const uint32_t own = base + P::kOffT, flip = own + P::kOwn;
             const float g = key ? -be : 1.f;
+            // the products of the unit before have read their R' and N
+            if (u.n > 0) ok = warp_wait(base + P::kInFull + 8 * (1 - group), ((u.n - 1) / 2) & 1, abort_flag);
             float f = 0.f;
 #pragma unroll
             for (int b = 32; b >= 0; b -= 32) {
