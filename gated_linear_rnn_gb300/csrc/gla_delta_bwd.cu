@@ -380,6 +380,8 @@ struct Units {
     }
 };
 
+// Slabs of a unit, then its K and Q: the products over the states need the slabs alone, so they run ahead of the
+// epilogue that frees K's and Q's place.
 template <int KT>
 __device__ __forceinline__ void grad_fetch(const Shape &p, const GradArgs &a, char *sm) {
     using P = GradPlan<KT>;
@@ -388,71 +390,43 @@ __device__ __forceinline__ void grad_fetch(const Shape &p, const GradArgs &a, ch
     const int id = threadIdx.x & 127;
     const int tiles = (p.dv + 15) / 16, slabs = (tiles + 1) / 2;
     const int64_t vst = (int64_t)p.H * p.dv;
-    // Three slabs are on their way at a time (and the head that came before one of them): 74 KB, which is what a latency
-    // of two microseconds takes at this SM's share of the bandwidth.
-    constexpr int kAhead = 3;
-    int ns = 0, out = 0;   // slabs issued, and made known
-    uint32_t heads = 0;    // 2 bits for each of the last slabs, the newest lowest: 1 + the head that came before it
-    bool ok = true;
-    // the copies of slab `out` have landed: they are made visible to the tensor cores
-    const auto publish = [&]() {
-        const uint32_t head = (heads >> (2 * (ns - 1 - out))) & 3;
+    // Up to four groups of copies (a slab, or K and Q) are on their way at a time, some 90 KB: what a latency of two
+    // microseconds takes at this SM's share of the bandwidth.  Groups become known in order, once they have landed.
+    constexpr int kAhead = 4;
+    int ns = 0, out = 0, groups = 0;  // slabs issued and made known, groups on their way
+    uint32_t kinds = 0;               // 2 bits for each, the newest lowest: 0 a slab, else 1 + the head's place
+    const auto publish = [&]() {      // the oldest group's copies, which have landed, to the tensor cores
+        const uint32_t head = (kinds >> (2 * --groups)) & 3;
         ptx::fence_async_shared();
-        ptx::mbar_arrive(base + P::kFull + 8 * (out % P::kStages));
-        if (head) ptx::mbar_arrive(base + P::kHFull + 8 * (head - 1));
-        ++out;
+        ptx::mbar_arrive(base + (head ? P::kHFull + 8 * (head - 1) : P::kFull + 8 * (out++ % P::kStages)));
     };
+    const auto issued = [&](uint32_t kind) {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        kinds = kinds << 2 | kind;
+        if (++groups > kAhead) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+            publish();
+        }
+    };
+    // before a wait, everything asked for becomes known: the others may need it to come to what is waited for
+    const auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) {
+            cp_async_wait_all();
+            while (groups > 0) publish();
+        }
+        return warp_wait(bar, parity, abort_flag);
+    };
+    bool ok = true;
     for (Units u; ok && u.next(p, a.units);) {
-        const int hb = u.n & 1, hk = u.h / p.group();
-        if (u.n >= 2) {
-            // before a wait, what has been asked for goes out whole: the others need it to come to its end
-            if (!__all_sync(0xffffffffu, ptx::mbar_try_wait(base + P::kHEmpty + 8 * hb, (u.n / 2 + 1) & 1))) {
-                cp_async_wait_all();
-                while (out < ns) publish();
-            }
-            if (!(ok = warp_wait(base + P::kHEmpty + 8 * hb, (u.n / 2 + 1) & 1, abort_flag))) break;
-        }
-        const uint32_t ka = base + P::kOffHead + hb * P::kHead;
-        {
-            const int t = id & 63;  // two threads to a row, neighbouring rows in a warp
-            const bf16 *kr = a.k + ((u.at.row + t) * p.Hk + hk) * p.dk, *qr = a.q + ((u.at.row + t) * p.Hk + hk) * p.dk;
-            for (int x = id >> 6; x < KT * 2; x += 2) {
-                const bool has = t < u.at.len && x * 8 < p.dk;
-                cp_async16(ka + x * kG * 16 + t * 16, has ? kr + x * 8 : a.k, has);
-                cp_async16(ka + P::kTile + x * kG * 16 + t * 16, has ? qr + x * 8 : a.q, has);
-            }
-        }
-        Decays &dc = *reinterpret_cast<Decays *>(sm + P::kOffHead + hb * P::kHead + 2 * P::kTile);
-        if (id < 32) {  // products of decays up to and behind each token: lane owns tokens lane and 32 + lane
-            float al[2], up[2], down[2];
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int tok = m * 32 + id;
-                const bool live = tok < u.at.len;
-                al[m] = live ? expf(load_gate<bf16>(a.g, (u.at.row + tok) * p.H + u.h, p.gate_f32)) : 1.f;
-                dc.alpha[tok] = al[m];
-                dc.beta[tok] = live ? load_gate<bf16>(a.beta, (u.at.row + tok) * p.H + u.h, p.gate_f32) : 0.f;
-                up[m] = al[m];
-                const float behind = __shfl_down_sync(0xffffffffu, al[m], 1);
-                down[m] = id < 31 ? behind : 1.f;  // the product of the next ones, from this one's neighbour on
-#pragma unroll
-                for (int w = 1; w < 32; w <<= 1) {
-                    const float x = __shfl_up_sync(0xffffffffu, up[m], w), y = __shfl_down_sync(0xffffffffu, down[m], w);
-                    if (id >= w) up[m] *= x;
-                    if (id + w < 32) down[m] *= y;
-                }
-            }
-            dc.alpha[kG + (id & 3)] = 1.f;
-            const float first = __shfl_sync(0xffffffffu, up[0], 31), second = __shfl_sync(0xffffffffu, up[1], 31);
-            dc.c[id] = up[0];
-            dc.c[32 + id] = first * up[1];
-            dc.d[id] = down[0] * second;
-            dc.d[32 + id] = down[1];
-        }
         const uint4 *s0 = a.s_images + image_at<KT>(p, u.slot, u.h, 0), *s1 = a.ds_images + image_at<KT>(p, u.slot, u.h, 0);
-        for (int s = 0; s < slabs; ++s) {
+        const bf16 *rows[2];  // four threads to a row of 64 bytes, eight rows to a warp's copy
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            rows[x] = a.dout + (u.at.row + x * 32 + (id >> 2)) * vst + (int64_t)u.h * p.dv + (id & 3) * 8;
+        const int64_t y_off = a.ys - a.dout, r_off = a.resid - a.dout;
+        for (int s = 0; s < slabs; ++s, ++ns) {
             const int sg = ns % P::kStages;
-            if (ns >= P::kStages && !(ok = warp_wait(base + P::kEmpty + 8 * sg, (ns / P::kStages + 1) & 1, abort_flag))) break;
+            if (ns >= P::kStages && !(ok = wait(base + P::kEmpty + 8 * sg, (ns / P::kStages + 1) & 1))) break;
             const uint32_t to = base + P::kOffSlab + sg * P::kSlab;
             const int here = min(2, tiles - 2 * s) * KT * 512;
             if (id == 0) {
@@ -460,27 +434,33 @@ __device__ __forceinline__ void grad_fetch(const Shape &p, const GradArgs &a, ch
                 ptx::bulk_load_g2s(to + P::kRows, s0 + s * 2 * KT * 32, here, base + P::kFull + 8 * sg);
                 ptx::bulk_load_g2s(to + P::kRows + P::kImage, s1 + s * 2 * KT * 32, here, base + P::kFull + 8 * sg);
             }
-            // four threads to a row of 64 bytes, eight rows to a warp's copy
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int t = x * 32 + (id >> 2), w = id & 3;
                 const bool has = t < u.at.len && s * 32 + w * 8 < p.dv;
-                const int64_t off = has ? (u.at.row + t) * vst + (int64_t)u.h * p.dv + s * 32 + w * 8 : 0;
+                const bf16 *from = has ? rows[x] + s * 32 : a.dout;
                 const uint32_t dst = to + w * 3 * kG * 16 + t * 16;
-                cp_async16(dst, a.dout + off, has);
-                cp_async16(dst + kG * 16, a.ys + off, has);
-                cp_async16(dst + 2 * kG * 16, a.resid + off, has);
+                cp_async16(dst, from, has);
+                cp_async16(dst + kG * 16, has ? from + y_off : a.ys, has);
+                cp_async16(dst + 2 * kG * 16, has ? from + r_off : a.resid, has);
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            heads = heads << 2 | (s == 0 ? 1 + hb : 0);
-            if (++ns - out > kAhead) {
-                asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
-                publish();
-            }
+            issued(0);
         }
+        if (!ok) break;
+        const int hb = u.n & 1, hk = u.h / p.group();
+        if (u.n >= 2 && !(ok = wait(base + P::kHEmpty + 8 * hb, (u.n / 2 + 1) & 1))) break;
+        const uint32_t ka = base + P::kOffHead + hb * P::kHead;
+        const int t = id & 63;  // two threads to a row, neighbouring rows in a warp
+        const bf16 *kr = a.k + ((u.at.row + t) * p.Hk + hk) * p.dk, *qr = a.q + ((u.at.row + t) * p.Hk + hk) * p.dk;
+        for (int x = id >> 6; x < KT * 2; x += 2) {
+            const bool has = t < u.at.len && x * 8 < p.dk;
+            cp_async16(ka + x * kG * 16 + t * 16, has ? kr + x * 8 : a.k, has);
+            cp_async16(ka + P::kTile + x * kG * 16 + t * 16, has ? qr + x * 8 : a.q, has);
+        }
+        issued(1 + hb);
     }
     cp_async_wait_all();
-    while (ok && out < ns) publish();
+    while (ok && groups > 0) publish();
     if (!ok) {  // nothing may be in flight into a block that ends early
         *abort_flag = 1;
         for (int i = 0; i < P::kStages; ++i)
@@ -569,7 +549,7 @@ __device__ __forceinline__ bool grad_issue(const Shape &p, const GradArgs &a, ch
     return true;
 }
 
-// Three warps: <S0, dS1> of each unit, as the slabs come by.
+// Three warps: <S0, dS1> of each unit, as the slabs come by; the first also the products of the unit's decays.
 template <int KT>
 __device__ __forceinline__ bool grad_inner(const Shape &p, const GradArgs &a, char *sm, int warp, int lane) {
     using P = GradPlan<KT>;
@@ -578,8 +558,14 @@ __device__ __forceinline__ bool grad_inner(const Shape &p, const GradArgs &a, ch
     const int tiles = (p.dv + 15) / 16, slabs = (tiles + 1) / 2;
     int ns = 0;
     for (Units u; u.next(p, a.units);) {
-        // a unit's head comes once the epilogue two units before, which reads this sum's place, is done
-        if (!warp_wait(base + P::kHFull + 8 * (u.n & 1), (u.n / 2) & 1, abort_flag)) return false;
+        float al[2] = {1.f, 1.f}, be[2] = {0.f, 0.f};  // lane owns tokens lane and 32 + lane
+        if (warp == 0)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+                if (m * 32 + lane < u.at.len) {
+                    al[m] = load_gate<bf16>(a.g, (u.at.row + m * 32 + lane) * p.H + u.h, p.gate_f32);
+                    be[m] = load_gate<bf16>(a.beta, (u.at.row + m * 32 + lane) * p.H + u.h, p.gate_f32);
+                }
         float inner = 0.f;
         for (int s = 0; s < slabs; ++s, ++ns) {
             const int sg = ns % P::kStages;
@@ -595,10 +581,38 @@ __device__ __forceinline__ bool grad_inner(const Shape &p, const GradArgs &a, ch
             if (lane == 0) ptx::mbar_arrive(base + P::kEmpty + 8 * sg);
         }
         for (int m = 16; m > 0; m >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, m);
-        if (lane == 0) {
-            reinterpret_cast<float *>(sm + P::kOffInner)[(u.n & 1) * 4 + warp] = inner;
-            ptx::mbar_arrive(base + P::kInner + 8 * (u.n & 1));
+        // the epilogue of two units before has read its sums and decays
+        const int hb = u.n & 1;
+        if (u.n >= 2 && !warp_wait(base + P::kHEmpty + 8 * hb, (u.n / 2 + 1) & 1, abort_flag)) return false;
+        if (lane == 0) reinterpret_cast<float *>(sm + P::kOffInner)[hb * 4 + warp] = inner;
+        if (warp == 0) {
+            Decays &dc = *reinterpret_cast<Decays *>(sm + P::kOffHead + hb * P::kHead + 2 * P::kTile);
+            float up[2], down[2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int tok = m * 32 + lane;
+                al[m] = tok < u.at.len ? expf(al[m]) : 1.f;
+                dc.alpha[tok] = al[m];
+                dc.beta[tok] = be[m];
+                up[m] = al[m];
+                const float behind = __shfl_down_sync(0xffffffffu, al[m], 1);
+                down[m] = lane < 31 ? behind : 1.f;  // the product of the next ones, from this one's neighbour on
+#pragma unroll
+                for (int w = 1; w < 32; w <<= 1) {
+                    const float x = __shfl_up_sync(0xffffffffu, up[m], w), y = __shfl_down_sync(0xffffffffu, down[m], w);
+                    if (lane >= w) up[m] *= x;
+                    if (lane + w < 32) down[m] *= y;
+                }
+            }
+            dc.alpha[kG + (lane & 3)] = 1.f;
+            const float first = __shfl_sync(0xffffffffu, up[0], 31), second = __shfl_sync(0xffffffffu, up[1], 31);
+            dc.c[lane] = up[0];
+            dc.c[32 + lane] = first * up[1];
+            dc.d[lane] = down[0] * second;
+            dc.d[32 + lane] = down[1];
         }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(base + P::kInner + 8 * hb);
     }
     return true;
 }
@@ -634,8 +648,9 @@ __device__ __forceinline__ bool grad_epilogue(const Shape &p, const GradArgs &a,
         const uint32_t head = base + P::kOffHead + group * P::kHead, mine = head + (key ? 0 : P::kTile);
         const Decays &dc = *reinterpret_cast<const Decays *>(sm + P::kOffHead + group * P::kHead + 2 * P::kTile);
         const uint32_t d = tmem + set * P::kSetCols + lanes;
-        bool ok = warp_wait(base + P::kHFull + 8 * group, (u.n / 2) & 1, abort_flag) &&
-                  warp_wait(base + P::kAccFull + 8 * set, (u.n / P::kSets) & 1, abort_flag);
+        bool ok = warp_wait(base + P::kAccFull + 8 * set, (u.n / P::kSets) & 1, abort_flag) &&
+                  warp_wait(base + P::kInner + 8 * group, (u.n / 2) & 1, abort_flag) &&
+                  warp_wait(base + P::kHFull + 8 * group, (u.n / 2) & 1, abort_flag);
         float A[P::kN], w = 0.f, x = 0.f;
         if (ok) {
             ptx::tc_fence_after();
@@ -757,7 +772,6 @@ __device__ __forceinline__ bool grad_epilogue(const Shape &p, const GradArgs &a,
                     if (e < p.dk) out[e / 4] = make_float4(A[e], A[e + 1], A[e + 2], A[e + 3]);
             }
         }
-        ok = ok && warp_wait(base + P::kInner + 8 * group, (u.n / 2) & 1, abort_flag);
         // all sums of the unit are there
         if (group == 0 ? any_of<1, 128>(!ok) : any_of<2, 128>(!ok)) return false;
         if (warp == 0) {  // dg: lane owns tokens 2 lane and 2 lane + 1
