@@ -296,58 +296,80 @@ delta_walks_kernel(Shape p, Walk again, Walk back, unsigned blocks, WalkArgs a) 
 //     m = rows of k . (R'^T Q + N^T K - N K) - q . (R' K):
 // the crossing products in the chunk, summed from the left (a token's reads leave, its writes enter), so that both
 // ends of a product carry the same rounding and cancel to f32.
-// D_ij comes from products of decays alone (a decay of zero is as good as any).
+// D_ij comes from products of decays alone (a decay of zero is as good as any): within 16 tokens as a table, across
+// them as (from the tile's start to i)(whole tiles between)(from j to its tile's end).
 //
-// All products run on tcgen05 with accumulators in TMEM, 128 rows at a time: rows 0-63 are the query's side of the
-// unit's tokens, rows 64-127 the key's, so that everything that meets in one row of dq or dk lies in one TMEM lane
-// and one thread:
-//     D1 = [dO; Y] S0^T,  D2 = [Y; R] dS1^T,  D3 = [dO; Y] R^T,  D4 = [R'; N] K,  D5 = [.; R'^T Q + N^T K]
-// One block per SM walks over units with four kinds of warps: four fetch (slabs of 32 columns of dO, Y, R and of both
-// states through a ring; K, Q and the decays of a unit), one thread issues the products, three warps form
-// <S0, dS1> from the slabs, and two warpgroups take turns as epilogues: D3 becomes R' and N (a thread's row of D is a
-// running product along the row) in shared memory for D4 and D5, the others are scaled, summed and written.  D4 and D5
-// take the columns of D1 and D2 once these are in registers; with two sets of columns (dk <= 96) the products of
-// one unit run under the epilogue of the other.  As mma.sync with its operands through ldmatrix (every state
-// element loaded by four warps) the kernel took 308 us on the layer's gradient, bound by shared memory and by the
-// sequence of its phases.
-//
-// Operand tiles are without swizzle: 16-byte units [unit][row], whose 8 x 16-byte blocks are core matrices either way (rows
-// as M or N with K along the units, or rows as K).
-constexpr int kGradThreads = 512;      // 2 epilogue warpgroups, 1 fetching, 1 with the issuer and the inner products
-constexpr int kInnerWarps = 3;
-constexpr uint32_t kTmemCols = 512;
-static_assert(2 * 200 + 2 * 56 == 4 * 128, "the epilogues take what the others give back");
+// One block per SM walks over units.  Twelve warps compute, in three roles of four (16 tokens each): dO's side (T = dO
+// R^T, dO S0^T, R' K -> dq), Y's (Y R^T, Y S0^T, N K) and R's (R dS1^T, R'^T Q + N^T K); the last two meet in
+// shared memory -> dk.  A fourth warpgroup fetches ahead: K, Q and the decay products of the next unit, and
+// slabs of 64 columns (32 for dk > 96) of dO, Y, R and of both states through a ring.
+// On the layer's gradient (4,096 units of 64 x 96 x 192, 790 MB): 269 us, of which the slabs' products are about 115,
+// T with R' and N 70 and the products inside the unit 50: the phases of a unit follow one another, and shared memory
+// carries every state element to four warps.  One block per unit with its states read from L2 between products
+// took 489 us, slabs of 32 columns 275, and the same unit with all products on tcgen05 (128 rows of TMEM, one thread
+// per row of dq and dk, two epilogues in turn) 281: its products took no time, but its unit waited through more
+// hands, each of a microsecond, than its two sets of accumulators could cover.
+constexpr int kGradWarps = 12;
+constexpr int kGradThreads = (kGradWarps + 4) * 32;
+constexpr int kMRow = kG * 2 + 16;  // bytes of a row of R' and N
 
-struct Decays {                        // of one unit
-    float alpha[kG + 4], beta[kG], c[kG], d[kG];  // alpha[64] = 1 stands behind the last
+struct Decays {                     // of one unit
+    float diag[4][256];             // D within a tile of 16 tokens
+    float pre[kG], suf[kG], c[kG], d[kG], beta[kG], whole[4], pad[4];
 };
-struct Sums {                          // per token
-    float wq[kG], wk[kG], x[kG], mq[kG], mk[kG];
+struct Sums {                       // per token
+    float wq[kG], wk[kG], x[kG], mq[kG], my[kG], mr[kG], inner[kGradWarps], pad[4];
 };
 template <int KT> struct GradPlan {
-    static constexpr int kN = KT * 16;
-    static constexpr int kTile = kG * kN * 2;                                      // K or Q: [2 KT units][64 rows] x 16 bytes
+    static constexpr int kTile = kG * row_bytes<KT>();
     static constexpr int kHead = 2 * kTile + (int)sizeof(Decays);                  // K | Q | decays, two of them
-    static constexpr int kRows = 3 * kG * 64;                                      // dO | Y | R: [4 units][192 rows] x 16 bytes
-    static constexpr int kImage = 2 * KT * 512;                                    // two column tiles of a state
-    static constexpr int kSlab = kRows + 2 * kImage;                               // rows | S0 | dS1
-    static constexpr int kStages = KT <= 6 ? 5 : 4;
-    static constexpr int kOwn = 2 * kG * 128;                                      // [R'; N]: [8 units][128 rows] x 16 bytes
-    static constexpr int kFlip = 3 * kG * 128;                                     // N | R' | N: [24 units][64 rows] x 16 bytes
-    static constexpr int kOffHead = 256, kOffSlab = kOffHead + 2 * kHead, kOffT = kOffSlab + kStages * kSlab,
-                         kOffSums = kOffT + kOwn + kFlip, kOffInner = kOffSums + 4 * (int)sizeof(Sums),
-                         kTotal = kOffInner + 2 * 16;
-    static constexpr int kSets = KT <= 6 ? 2 : 1;                                  // of accumulators
-    static constexpr uint32_t kSetCols = 2 * kN + kG;                              // D1 (D4) | D2 (D5) | D3
+    static constexpr int kTiles = KT <= 6 ? 4 : 2;                                 // column tiles of 16 in a slab
+    static constexpr int kSlabRow = kTiles * 32 + 16;                              // an odd number of 16-byte units
+    static constexpr int kImage = kTiles * KT * 512;                               // its column tiles of a state
+    static constexpr int kSlab = 3 * kG * kSlabRow + 2 * kImage;                   // dO | Y | R | S0 | dS1
+    static constexpr int kStages = 2;
+    static constexpr int kXRow = KT * 16 + 4;                                      // f32 row of the exchange tile
+    static constexpr int kOffHead = 128, kOffSlab = kOffHead + 2 * kHead, kOffM = kOffSlab + kStages * kSlab,
+                         kOffX = kOffM + 2 * kG * kMRow, kOffSums = kOffX + kG * kXRow * 4,
+                         kTotal = kOffSums + 2 * (int)sizeof(Sums);
     static_assert(kTotal <= 227 * 1024, "shared memory of a block");
-    static_assert(kSets * kSetCols <= kTmemCols, "TMEM");
-    static_assert(kHead % 16 == 0 && kSlab % 16 == 0 && kOffInner % 16 == 0 && sizeof(Decays) % 16 == 0, "16-byte copies");
-    // barriers
-    static constexpr int kHFull = 0, kHEmpty = 16, kFull = 32, kEmpty = kFull + 8 * kStages, kAccFull = kEmpty + 8 * kStages,
-                         kAccFree = kAccFull + 16, kReady = kAccFree + 16, kInFull = kReady + 16, kInner = kInFull + 16,
-                         kAbort = kInner + 16, kTmem = kAbort + 4;
-    static_assert(kTmem + 4 <= kOffHead, "barriers");
+    static_assert(kTile % 16 == 0 && kHead % 16 == 0 && kSlab % 16 == 0 && kOffX % 16 == 0, "16-byte copies");
 };
+
+__device__ __forceinline__ void compute_sync() { ptx::named_bar_sync(1, kGradWarps * 32); }
+// acc (16 rows x KT * 16) += A (16 x 16) times 16 rows of a tile
+template <int KT>
+__device__ __forceinline__ void add_rows(float (&acc)[2 * KT][4], const uint32_t (&a)[4], uint32_t rows, int lane) {
+    const uint32_t at = rows + (((lane >> 3) & 1) * 8 + (lane & 7)) * row_bytes<KT>() + ((lane >> 3) >> 1) * 16;
+#pragma unroll
+    for (int i = 0; i < KT; ++i) {
+        uint32_t b[4];
+        ldsm4t(b, at + i * 32);
+        mma(acc[2 * i], a, b[0], b[1]);
+        mma(acc[2 * i + 1], a, b[2], b[3]);
+    }
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t x;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+    return x;
+}
+// sums over dk of acc's two rows of this lane with the rows of a tile: lo for row gr, hi for row gr + 8
+template <int KT>
+__device__ __forceinline__ void row_dots(const float (&acc)[2 * KT][4], uint32_t rows, int lane, float &lo, float &hi) {
+    const uint32_t at = rows + (lane >> 2) * row_bytes<KT>() + (lane & 3) * 4;
+    lo = hi = 0.f;
+#pragma unroll
+    for (int n = 0; n < 2 * KT; ++n) {
+        const uint32_t x = lds32(at + n * 16), y = lds32(at + 8 * row_bytes<KT>() + n * 16);
+        lo = fmaf(acc[n][0], lo_f(x), fmaf(acc[n][1], hi_f(x), lo));
+        hi = fmaf(acc[n][2], lo_f(y), fmaf(acc[n][3], hi_f(y), hi));
+    }
+    lo += __shfl_xor_sync(0xffffffffu, lo, 1);
+    hi += __shfl_xor_sync(0xffffffffu, hi, 1);
+    lo += __shfl_xor_sync(0xffffffffu, lo, 2);
+    hi += __shfl_xor_sync(0xffffffffu, hi, 2);
+}
 
 struct GradArgs {
     const bf16 *q, *k, *dout;
@@ -360,441 +382,107 @@ struct GradArgs {
     unsigned units;         // slots * H
 };
 
-// The units that a block walks over, in the same order for all of its warps.
-struct Units {
-    unsigned unit;
-    int slot, h, n;  // n: how many came before
-    ChunkAt at;
-    __device__ __forceinline__ Units() : unit(blockIdx.x), n(-1) {}
-    __device__ __forceinline__ bool next(const Shape &p, unsigned units) {
-        if (n >= 0) unit += gridDim.x;
-        for (; unit < units; unit += gridDim.x) {
-            slot = (int)(unit / (unsigned)p.H);
-            h = (int)(unit % (unsigned)p.H);
-            if (chunk_of_slot<kG>(slot, p, at)) {
-                ++n;
-                return true;
-            }
-        }
-        return false;
-    }
-};
-
-// Slabs of a unit, then its K and Q: the products over the states need the slabs alone, so they run ahead of the
-// epilogue that frees K's and Q's place.
 template <int KT>
 __device__ __forceinline__ void grad_fetch(const Shape &p, const GradArgs &a, char *sm) {
     using P = GradPlan<KT>;
     const uint32_t base = ptx::smem_u32(sm);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + P::kAbort);
-    const int id = threadIdx.x & 127;
-    const int tiles = (p.dv + 15) / 16, slabs = (tiles + 1) / 2;
-    const int64_t vst = (int64_t)p.H * p.dv;
-    // Up to four groups of copies (a slab, or K and Q) are on their way at a time, some 90 KB: what a latency of two
-    // microseconds takes at this SM's share of the bandwidth.  Groups become known in order, once they have landed.
-    constexpr int kAhead = 4;
-    int ns = 0, out = 0, groups = 0;  // slabs issued and made known, groups on their way
-    uint32_t kinds = 0;               // 2 bits for each, the newest lowest: 0 a slab, else 1 + the head's place
-    const auto publish = [&]() {      // the oldest group's copies, which have landed, to the tensor cores
-        const uint32_t head = (kinds >> (2 * --groups)) & 3;
-        ptx::fence_async_shared();
-        ptx::mbar_arrive(base + (head ? P::kHFull + 8 * (head - 1) : P::kFull + 8 * (out++ % P::kStages)));
-    };
-    const auto issued = [&](uint32_t kind) {
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        kinds = kinds << 2 | kind;
-        if (++groups > kAhead) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
-            publish();
-        }
-    };
-    // before a wait, everything asked for becomes known: the others may need it to come to what is waited for
-    const auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (!__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) {
-            cp_async_wait_all();
-            while (groups > 0) publish();
-        }
-        return warp_wait(bar, parity, abort_flag);
-    };
+    const uint32_t hfull = base, hempty = base + 16, full = base + 32, empty = full + 8 * P::kStages;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + 120);
+    const int id = threadIdx.x - kGradWarps * 32;
+    const int tiles = (p.dv + 15) / 16, slabs = (tiles + P::kTiles - 1) / P::kTiles;
+    int n = 0, ns = 0;  // units and slabs so far
     bool ok = true;
-    for (Units u; ok && u.next(p, a.units);) {
-        const uint4 *s0 = a.s_images + image_at<KT>(p, u.slot, u.h, 0), *s1 = a.ds_images + image_at<KT>(p, u.slot, u.h, 0);
-        const bf16 *rows[2];  // four threads to a row of 64 bytes, eight rows to a warp's copy
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-            rows[x] = a.dout + (u.at.row + x * 32 + (id >> 2)) * vst + (int64_t)u.h * p.dv + (id & 3) * 8;
-        const int64_t y_off = a.ys - a.dout, r_off = a.resid - a.dout;
-        for (int s = 0; s < slabs; ++s, ++ns) {
-            const int sg = ns % P::kStages;
-            if (ns >= P::kStages && !(ok = wait(base + P::kEmpty + 8 * sg, (ns / P::kStages + 1) & 1))) break;
-            const uint32_t to = base + P::kOffSlab + sg * P::kSlab;
-            const int here = min(2, tiles - 2 * s) * KT * 512;
-            if (id == 0) {
-                ptx::mbar_expect_tx(base + P::kFull + 8 * sg, 2 * here);
-                ptx::bulk_load_g2s(to + P::kRows, s0 + s * 2 * KT * 32, here, base + P::kFull + 8 * sg);
-                ptx::bulk_load_g2s(to + P::kRows + P::kImage, s1 + s * 2 * KT * 32, here, base + P::kFull + 8 * sg);
-            }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int t = x * 32 + (id >> 2), w = id & 3;
-                const bool has = t < u.at.len && s * 32 + w * 8 < p.dv;
-                const bf16 *from = has ? rows[x] + s * 32 : a.dout;
-                const uint32_t dst = to + w * 3 * kG * 16 + t * 16;
-                cp_async16(dst, from, has);
-                cp_async16(dst + kG * 16, has ? from + y_off : a.ys, has);
-                cp_async16(dst + 2 * kG * 16, has ? from + r_off : a.resid, has);
-            }
-            issued(0);
-        }
-        if (!ok) break;
-        const int hb = u.n & 1, hk = u.h / p.group();
-        if (u.n >= 2 && !(ok = wait(base + P::kHEmpty + 8 * hb, (u.n / 2 + 1) & 1))) break;
+    for (unsigned unit = blockIdx.x; ok && unit < a.units; unit += gridDim.x) {
+        const int slot = (int)(unit / (unsigned)p.H), h = (int)(unit % (unsigned)p.H), hk = h / p.group();
+        ChunkAt at;
+        if (!chunk_of_slot<kG>(slot, p, at)) continue;
+        const int hb = n & 1;
+        if (n >= 2 && !(ok = warp_wait(hempty + 8 * hb, (n / 2 + 1) & 1, abort_flag))) break;
+        ++n;
+        char *head = sm + P::kOffHead + hb * P::kHead;
         const uint32_t ka = base + P::kOffHead + hb * P::kHead;
-        const int t = id & 63;  // two threads to a row, neighbouring rows in a warp
-        const bf16 *kr = a.k + ((u.at.row + t) * p.Hk + hk) * p.dk, *qr = a.q + ((u.at.row + t) * p.Hk + hk) * p.dk;
-        for (int x = id >> 6; x < KT * 2; x += 2) {
-            const bool has = t < u.at.len && x * 8 < p.dk;
-            cp_async16(ka + x * kG * 16 + t * 16, has ? kr + x * 8 : a.k, has);
-            cp_async16(ka + P::kTile + x * kG * 16 + t * 16, has ? qr + x * 8 : a.q, has);
-        }
-        issued(1 + hb);
-    }
-    cp_async_wait_all();
-    while (ok && groups > 0) publish();
-    if (!ok) {  // nothing may be in flight into a block that ends early
-        *abort_flag = 1;
-        for (int i = 0; i < P::kStages; ++i)
-            for (int par = 0; par < 2; ++par) ptx::mbar_wait(base + P::kFull + 8 * i, par, nullptr, kWaitNs / 1000);
-    }
-}
-
-// One thread: the products of the slabs into D1, D2 and D3, and of R' and N into D4 and D5 as soon as an epilogue has
-// them ready.
-template <int KT>
-__device__ __forceinline__ bool grad_issue(const Shape &p, const GradArgs &a, char *sm, uint32_t tmem) {
-    using P = GradPlan<KT>;
-    const uint32_t base = ptx::smem_u32(sm);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + P::kAbort);
-    const int tiles = (p.dv + 15) / 16, slabs = (tiles + 1) / 2;
-    constexpr uint32_t i_state = ptx::idesc_bf16(128, P::kN, 0, 1), i_rows = ptx::idesc_bf16(128, kG, 0, 0),
-                       i_flip = ptx::idesc_bf16(128, P::kN, 1, 1);
-    const auto inside = [&](int n) {  // D4 and D5 of unit n
-        ptx::tc_fence_after();
-        const uint32_t d = tmem + (n % P::kSets) * P::kSetCols, head = base + P::kOffHead + (n & 1) * P::kHead;
-        const uint32_t own = base + P::kOffT, flip = own + P::kOwn;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const uint64_t kd = ptx::smem_desc(head + s * 256, 128, kG * 16, ptx::kSwizzleNone),
-                           qd = ptx::smem_desc(head + P::kTile + s * 256, 128, kG * 16, ptx::kSwizzleNone);
-            ptx::mma_ss(d, ptx::smem_desc(own + s * 2 * 2 * kG * 16, 2 * kG * 16, 128, ptx::kSwizzleNone), kd, i_state, s > 0);
-            ptx::mma_ss(d + P::kN, ptx::smem_desc(flip + s * 256, 128, kG * 16, ptx::kSwizzleNone), qd, i_flip, s > 0);
-            ptx::mma_ss(d + P::kN, ptx::smem_desc(flip + 8 * kG * 16 + s * 256, 128, kG * 16, ptx::kSwizzleNone), kd, i_flip, 1);
-        }
-        ptx::mma_commit(base + P::kInFull + 8 * (n & 1));
-    };
-    int ns = 0, waiting = -1;  // a unit whose R' and N are still to come
-    const auto ready = [&](int n) { return base + P::kReady + 8 * (n & 1); };
-    for (Units u; u.next(p, a.units);) {
-        const int set = u.n % P::kSets;
-        if (u.n >= P::kSets &&
-            !ptx::mbar_wait(base + P::kAccFree + 8 * set, (u.n / P::kSets + 1) & 1, abort_flag, kWaitNs))
-            return false;
-        const uint32_t d = tmem + set * P::kSetCols;
-        for (int s = 0; s < slabs; ++s, ++ns) {
-            const int sg = ns % P::kStages;
-            // Until the slab is there, R' and N of the unit before may become ready; they do not wait for it, since the
-            // slab may be waiting for them (a head is free once its epilogue is done).
-            const uint64_t t0 = ptx::globaltimer();
-            while (!ptx::mbar_try_wait(base + P::kFull + 8 * sg, (ns / P::kStages) & 1)) {
-                if (waiting >= 0 && ptx::mbar_try_wait(ready(waiting), (waiting / 2) & 1)) {
-                    inside(waiting);
-                    waiting = -1;
-                }
-                if (*abort_flag || ptx::globaltimer() - t0 > kWaitNs) return false;
+        {
+            const int t = id >> 1;  // two threads to a row
+            const bf16 *kr = a.k + ((at.row + t) * p.Hk + hk) * p.dk, *qr = a.q + ((at.row + t) * p.Hk + hk) * p.dk;
+            for (int u = id & 1; u < KT * 2; u += 2) {
+                const bool has = t < at.len && u * 8 < p.dk;
+                cp_async16(ka + t * row_bytes<KT>() + u * 16, has ? kr + u * 8 : a.k, has);
+                cp_async16(ka + P::kTile + t * row_bytes<KT>() + u * 16, has ? qr + u * 8 : a.q, has);
             }
-            ptx::tc_fence_after();
-            const uint32_t rows = base + P::kOffSlab + sg * P::kSlab, image = rows + P::kRows;
-            for (int x = 0; x < min(2, tiles - 2 * s); ++x) {
-                constexpr uint32_t kUnit = 3 * kG * 16;
-                const uint32_t r = rows + x * 2 * kUnit, i = image + x * KT * 512;
-                const uint32_t more = s > 0 || x > 0;
-                const uint64_t top = ptx::smem_desc(r, kUnit, 128, ptx::kSwizzleNone);
-                ptx::mma_ss(d, top, ptx::smem_desc(i, 128, 256, ptx::kSwizzleNone), i_state, more);
-                ptx::mma_ss(d + P::kN, ptx::smem_desc(r + kG * 16, kUnit, 128, ptx::kSwizzleNone),
-                            ptx::smem_desc(i + P::kImage, 128, 256, ptx::kSwizzleNone), i_state, more);
-                ptx::mma_ss(d + 2 * P::kN, top, ptx::smem_desc(r + 2 * kG * 16, kUnit, 128, ptx::kSwizzleNone), i_rows, more);
-            }
-            ptx::mma_commit(base + P::kEmpty + 8 * sg);
-            if (waiting >= 0 && ptx::mbar_try_wait(ready(waiting), (waiting / 2) & 1)) {
-                inside(waiting);
-                waiting = -1;
-            }
+            cp_async_arrive(hfull + 8 * hb);
         }
-        ptx::mma_commit(base + P::kAccFull + 8 * set);
-        if (waiting >= 0) {
-            if (!ptx::mbar_wait(ready(waiting), (waiting / 2) & 1, abort_flag, kWaitNs)) return false;
-            inside(waiting);
-        }
-        waiting = u.n;
-        if (P::kSets == 1) {  // the next unit's products need this one's accumulators
-            if (!ptx::mbar_wait(ready(waiting), (waiting / 2) & 1, abort_flag, kWaitNs)) return false;
-            inside(waiting);
-            waiting = -1;
-        }
-    }
-    if (waiting >= 0) {
-        if (!ptx::mbar_wait(ready(waiting), (waiting / 2) & 1, abort_flag, kWaitNs)) return false;
-        inside(waiting);
-    }
-    return true;
-}
-
-// Three warps: <S0, dS1> of each unit, as the slabs come by; the first also the products of the unit's decays.
-template <int KT>
-__device__ __forceinline__ bool grad_inner(const Shape &p, const GradArgs &a, char *sm, int warp, int lane) {
-    using P = GradPlan<KT>;
-    const uint32_t base = ptx::smem_u32(sm);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + P::kAbort);
-    const int tiles = (p.dv + 15) / 16, slabs = (tiles + 1) / 2;
-    int ns = 0;
-    for (Units u; u.next(p, a.units);) {
-        float al[2] = {1.f, 1.f}, be[2] = {0.f, 0.f};  // lane owns tokens lane and 32 + lane
-        if (warp == 0)
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-                if (m * 32 + lane < u.at.len) {
-                    al[m] = load_gate<bf16>(a.g, (u.at.row + m * 32 + lane) * p.H + u.h, p.gate_f32);
-                    be[m] = load_gate<bf16>(a.beta, (u.at.row + m * 32 + lane) * p.H + u.h, p.gate_f32);
-                }
-        float inner = 0.f;
-        for (int s = 0; s < slabs; ++s, ++ns) {
-            const int sg = ns % P::kStages;
-            if (!warp_wait(base + P::kFull + 8 * sg, (ns / P::kStages) & 1, abort_flag)) return false;
-            const uint32_t image = base + P::kOffSlab + sg * P::kSlab + P::kRows;
-            for (int i = warp * 32 + lane; i < min(2, tiles - 2 * s) * KT * 32; i += kInnerWarps * 32) {
-                const uint4 x = lds128(image + i * 16), y = lds128(image + P::kImage + i * 16);
-                const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) inner = fmaf(lo_f(xw[e]), lo_f(yw[e]), fmaf(hi_f(xw[e]), hi_f(yw[e]), inner));
-            }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(base + P::kEmpty + 8 * sg);
-        }
-        for (int m = 16; m > 0; m >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, m);
-        // the epilogue of two units before has read its sums and decays
-        const int hb = u.n & 1;
-        if (u.n >= 2 && !warp_wait(base + P::kHEmpty + 8 * hb, (u.n / 2 + 1) & 1, abort_flag)) return false;
-        if (lane == 0) reinterpret_cast<float *>(sm + P::kOffInner)[hb * 4 + warp] = inner;
-        if (warp == 0) {
-            Decays &dc = *reinterpret_cast<Decays *>(sm + P::kOffHead + hb * P::kHead + 2 * P::kTile);
-            float up[2], down[2];
+        // the decays: thread j < 64 is column j of its tile of 16; both warps take all 64 tokens' decays
+        Decays &dc = *reinterpret_cast<Decays *>(head + 2 * P::kTile);
+        if (id < kG) {
+            const int lane = id & 31, b = id >> 4, j = id & 15;
+            float al[2];
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 const int tok = m * 32 + lane;
-                al[m] = tok < u.at.len ? expf(al[m]) : 1.f;
-                dc.alpha[tok] = al[m];
-                dc.beta[tok] = be[m];
-                up[m] = al[m];
-                const float behind = __shfl_down_sync(0xffffffffu, al[m], 1);
-                down[m] = lane < 31 ? behind : 1.f;  // the product of the next ones, from this one's neighbour on
-#pragma unroll
-                for (int w = 1; w < 32; w <<= 1) {
-                    const float x = __shfl_up_sync(0xffffffffu, up[m], w), y = __shfl_down_sync(0xffffffffu, down[m], w);
-                    if (lane >= w) up[m] *= x;
-                    if (lane + w < 32) down[m] *= y;
-                }
+                al[m] = tok < at.len ? expf(load_gate<bf16>(a.g, (at.row + tok) * p.H + h, p.gate_f32)) : 1.f;
             }
-            dc.alpha[kG + (lane & 3)] = 1.f;
-            const float first = __shfl_sync(0xffffffffu, up[0], 31), second = __shfl_sync(0xffffffffu, up[1], 31);
-            dc.c[lane] = up[0];
-            dc.c[32 + lane] = first * up[1];
-            dc.d[lane] = down[0] * second;
-            dc.d[32 + lane] = down[1];
+            dc.beta[id] = id < at.len ? load_gate<bf16>(a.beta, (at.row + id) * p.H + h, p.gate_f32) : 0.f;
+            const float mine = id < 32 ? al[0] : al[1];
+            float f = 0.f, run = 1.f, pre = 1.f, whole0 = 1.f, whole1 = 1.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float y = __shfl_sync(0xffffffffu, mine, i, 16);
+                run *= y;
+                if (i == j) pre = run;
+                f = i == j ? 1.f : f * y;
+                dc.diag[b][i * 16 + j] = f;
+                whole0 *= __shfl_sync(0xffffffffu, al[0], i, 16);
+                whole1 *= __shfl_sync(0xffffffffu, al[1], i, 16);
+            }
+            float before = 1.f, after = 1.f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const float x = __shfl_sync(0xffffffffu, t < 2 ? whole0 : whole1, (t & 1) * 16);
+                if (t < b) before *= x;
+                if (t > b) after *= x;
+                if (id == 0) dc.whole[t] = x;
+            }
+            dc.pre[id] = pre;
+            dc.suf[id] = f;
+            dc.c[id] = before * pre;
+            dc.d[id] = f * after;
         }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(base + P::kInner + 8 * hb);
+        ptx::mbar_arrive(hfull + 8 * hb);
+        const int64_t vst = (int64_t)p.H * p.dv;
+        // neighbouring threads to neighbouring units of a row: 2 kTiles of them
+        constexpr int kUnits = 2 * P::kTiles, kStep = 128 / kUnits;
+        const int t0 = id / kUnits, u0 = id % kUnits;
+        const int64_t vat = (at.row + t0) * vst + (int64_t)h * p.dv + u0 * 8;
+        const uint4 *s0 = a.s_images + image_at<KT>(p, slot, h, 0), *s1 = a.ds_images + image_at<KT>(p, slot, h, 0);
+        for (int s = 0; s < slabs; ++s, ++ns) {
+            const int sg = ns % P::kStages;
+            if (ns >= P::kStages && !(ok = warp_wait(empty + 8 * sg, (ns / P::kStages + 1) & 1, abort_flag))) break;
+            const uint32_t to = base + P::kOffSlab + sg * P::kSlab;
+            const int here = min(P::kTiles, tiles - P::kTiles * s) * KT * 512;
+            if (id == 0) {
+                ptx::mbar_expect_tx(full + 8 * sg, 2 * here);
+                ptx::bulk_load_g2s(to + 3 * kG * P::kSlabRow, s0 + s * P::kTiles * KT * 32, here, full + 8 * sg);
+                ptx::bulk_load_g2s(to + 3 * kG * P::kSlabRow + P::kImage, s1 + s * P::kTiles * KT * 32, here, full + 8 * sg);
+            }
+#pragma unroll 4
+            for (int t = t0; t < kG; t += kStep) {
+                const bool has = t < at.len && s * P::kTiles * 16 + u0 * 8 < p.dv;
+                const int64_t off = has ? vat + (t - t0) * vst + s * P::kTiles * 16 : 0;
+                const uint32_t dst = to + t * P::kSlabRow + u0 * 16;
+                cp_async16(dst, a.dout + off, has);
+                cp_async16(dst + kG * P::kSlabRow, a.ys + off, has);
+                cp_async16(dst + 2 * kG * P::kSlabRow, a.resid + off, has);
+            }
+            cp_async_arrive(full + 8 * sg);
+        }
     }
-    return true;
-}
-
-// a row of the unit's K or Q tile, eight elements at a time
-__device__ __forceinline__ void row8(uint32_t tile, int row, int unit, float (&x)[8]) {
-    const uint4 t = lds128(tile + unit * kG * 16 + row * 16);
-    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        x[2 * e] = lo_f(w[e]);
-        x[2 * e + 1] = hi_f(w[e]);
+    // nothing may be in flight into a block that ends early; a whole walk over units has waited for every stage
+    cp_async_wait_all();
+    if (!ok) {
+        *abort_flag = 1;
+        for (int i = 0; i < P::kStages; ++i)
+            for (int par = 0; par < 2; ++par) ptx::mbar_wait(full + 8 * i, par, nullptr, kWaitNs / 1000);
     }
-}
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-// A warpgroup: every second unit; thread = row of 128 (token row % 64 on the query's or the key's side).
-template <int KT>
-__device__ __forceinline__ bool grad_epilogue(const Shape &p, const GradArgs &a, char *sm, uint32_t tmem, int group) {
-    using P = GradPlan<KT>;
-    const uint32_t base = ptx::smem_u32(sm);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + P::kAbort);
-    const int id = threadIdx.x & 127, warp = id >> 5, lane = id & 31, i = id & 63;
-    const bool key = id >= kG;
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;  // this warp's TMEM lanes
-    int turn = 0;
-    for (Units u; u.next(p, a.units);) {
-        if ((u.n & 1) != group) continue;
-        const int set = u.n % P::kSets;
-        Sums &sums = reinterpret_cast<Sums *>(sm + P::kOffSums)[group * 2 + (turn++ & 1)];
-        const uint32_t head = base + P::kOffHead + group * P::kHead, mine = head + (key ? 0 : P::kTile);
-        const Decays &dc = *reinterpret_cast<const Decays *>(sm + P::kOffHead + group * P::kHead + 2 * P::kTile);
-        const uint32_t d = tmem + set * P::kSetCols + lanes;
-        bool ok = warp_wait(base + P::kAccFull + 8 * set, (u.n / P::kSets) & 1, abort_flag) &&
-                  warp_wait(base + P::kInner + 8 * group, (u.n / 2) & 1, abort_flag) &&
-                  warp_wait(base + P::kHFull + 8 * group, (u.n / 2) & 1, abort_flag);
-        float A[P::kN], w = 0.f, x = 0.f;
-        if (ok) {
-            ptx::tc_fence_after();
-            const float be = dc.beta[i], f1 = key ? -dc.c[i] * be : dc.c[i], f2 = dc.d[i] * be;
-#pragma unroll
-            for (int b = 0; b < P::kN; b += 32) {
-                uint32_t r[32];
-                ptx::tmem_ld32(d + b, r);
-                ptx::tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) A[b + e] = f1 * __uint_as_float(r[e]);
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    float m[8];
-                    row8(mine, i, (b + e) / 8, m);
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) w = fmaf(m[y], A[b + e + y], w);
-                }
-                if (key) {
-                    ptx::tmem_ld32(d + P::kN + b, r);
-                    ptx::tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        float m[8];
-                        row8(mine, i, (b + e) / 8, m);
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            const float v = f2 * __uint_as_float(r[e + y]);
-                            x = fmaf(m[y], v, x);
-                            A[b + e + y] += v;
-                        }
-                    }
-                }
-            }
-            (key ? sums.wk : sums.wq)[i] = w;
-            if (key) sums.x[i] = x;
-            // R' (query) or N (key), from the row's end: f = D_ij, zero for j > i
-            const uint32_t own = base + P::kOffT, flip = own + P::kOwn;
-            const float g = key ? -be : 1.f;
-            // the products of the unit before have read their R' and N
-            if (u.n > 0) ok = warp_wait(base + P::kInFull + 8 * (1 - group), ((u.n - 1) / 2) & 1, abort_flag);
-            float f = 0.f;
-#pragma unroll
-            for (int b = 32; b >= 0; b -= 32) {
-                uint32_t r[32];
-                ptx::tmem_ld32(d + 2 * P::kN + b, r);
-                ptx::tmem_wait_ld();
-                if (key && i >= b && i < b + 32) {
-                    float own_beta = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (b + e == i) own_beta = __uint_as_float(r[e]);
-                    if (i < u.at.len) store_gate<bf16>(a.dbeta, (u.at.row + i) * p.H + u.h, p.gate_f32, own_beta);
-                }
-#pragma unroll
-                for (int e0 = 24; e0 >= 0; e0 -= 8) {
-                    float v[8];
-#pragma unroll
-                    for (int e = 7; e >= 0; --e) {
-                        const int j = b + e0 + e;
-                        f = j == i ? 1.f : f * dc.alpha[j + 1];
-                        const float z = f * dc.beta[j] * g * __uint_as_float(r[e0 + e]);
-                        v[e] = key && j == i ? 0.f : z;
-                    }
-                    const uint32_t q0 = pack(v[0], v[1]), q1 = pack(v[2], v[3]), q2 = pack(v[4], v[5]), q3 = pack(v[6], v[7]);
-                    const uint32_t unit = (b + e0) / 8;
-                    sts128(own + unit * 2 * kG * 16 + id * 16, q0, q1, q2, q3);
-                    if (key) {
-                        sts128(flip + unit * kG * 16 + i * 16, q0, q1, q2, q3);
-                        sts128(flip + (16 + unit) * kG * 16 + i * 16, q0, q1, q2, q3);
-                    } else {
-                        sts128(flip + (8 + unit) * kG * 16 + i * 16, q0, q1, q2, q3);
-                    }
-                }
-            }
-            ptx::fence_async_shared();
-            ptx::tc_fence_before();
-        }
-        ptx::mbar_arrive(base + P::kReady + 8 * group);
-        ok = ok && warp_wait(base + P::kInFull + 8 * group, (u.n / 2) & 1, abort_flag);
-        if (ok) {
-            ptx::tc_fence_after();
-            float m = 0.f;
-#pragma unroll
-            for (int b = 0; b < P::kN; b += 32) {
-                uint32_t r[32], t[32];
-                ptx::tmem_ld32(d + b, r);
-                if (key) ptx::tmem_ld32(d + P::kN + b, t);
-                ptx::tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    float v[8];
-                    row8(mine, i, (b + e) / 8, v);
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        const float n = __uint_as_float(r[e + y]), o = key ? __uint_as_float(t[e + y]) : 0.f;
-                        m = fmaf(v[y], o - n, m);
-                        A[b + e + y] += n + o;
-                    }
-                }
-            }
-            ptx::tc_fence_before();
-            (key ? sums.mk : sums.mq)[i] = m;
-        }
-        ptx::mbar_arrive(base + P::kAccFree + 8 * set);
-        if (ok && i < u.at.len) {
-            const int64_t to = ((u.at.row + i) * p.H + u.h) * p.dk;
-            if (a.dq_part == nullptr) {
-                uint4 *out = reinterpret_cast<uint4 *>((key ? a.dk : a.dq) + to);
-#pragma unroll
-                for (int e = 0; e < P::kN; e += 8)
-                    if (e < p.dk)
-                        out[e / 8] = make_uint4(pack(A[e], A[e + 1]), pack(A[e + 2], A[e + 3]), pack(A[e + 4], A[e + 5]),
-                                                pack(A[e + 6], A[e + 7]));
-            } else {
-                float4 *out = reinterpret_cast<float4 *>((key ? a.dk_part : a.dq_part) + to);
-#pragma unroll
-                for (int e = 0; e < P::kN; e += 4)
-                    if (e < p.dk) out[e / 4] = make_float4(A[e], A[e + 1], A[e + 2], A[e + 3]);
-            }
-        }
-        // all sums of the unit are there
-        if (group == 0 ? any_of<1, 128>(!ok) : any_of<2, 128>(!ok)) return false;
-        if (warp == 0) {  // dg: lane owns tokens 2 lane and 2 lane + 1
-            const float *in = reinterpret_cast<const float *>(sm + P::kOffInner) + (u.n & 1) * 4;
-            const float f = ((in[0] + in[1]) + in[2]) * dc.c[kG - 1];
-            const int j = 2 * lane;
-            const float w0 = sums.wq[j] + sums.wk[j], w1 = sums.wq[j + 1] + sums.wk[j + 1];
-            const float x0 = sums.x[j] + (sums.mq[j] + sums.mk[j]), x1 = sums.x[j + 1] + (sums.mq[j + 1] + sums.mk[j + 1]);
-            float pre = x0 + x1, suf = w0 + w1;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const float y = __shfl_up_sync(0xffffffffu, pre, m), z = __shfl_down_sync(0xffffffffu, suf, m);
-                if (lane >= m) pre += y;
-                if (lane + m < 32) suf += z;
-            }
-            const float left = pre - (x0 + x1);  // tokens before 2 lane
-            if (j < u.at.len) store_gate<bf16>(a.dg, (u.at.row + j) * p.H + u.h, p.gate_f32, f + left + suf);
-            if (j + 1 < u.at.len) store_gate<bf16>(a.dg, (u.at.row + j + 1) * p.H + u.h, p.gate_f32, f + left + x0 + (suf - w0));
-        }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(base + P::kHEmpty + 8 * group);
-    }
-    return true;
 }
 
 template <int KT>
@@ -803,49 +491,261 @@ delta_grad_kernel(Shape p, GradArgs a) {
     using P = GradPlan<KT>;
     extern __shared__ __align__(128) char sm_raw[];
     const uint32_t base = ptx::smem_u32(sm_raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
+    const uint32_t hfull = base, hempty = base + 16, full = base + 32, empty = full + 8 * P::kStages;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm_raw + 120);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(base + P::kHFull + 8 * i, 128);
-            ptx::mbar_init(base + P::kHEmpty + 8 * i, 4);
-            ptx::mbar_init(base + P::kAccFull + 8 * i, 1);
-            ptx::mbar_init(base + P::kAccFree + 8 * i, 128);
-            ptx::mbar_init(base + P::kReady + 8 * i, 128);
-            ptx::mbar_init(base + P::kInFull + 8 * i, 1);
-            ptx::mbar_init(base + P::kInner + 8 * i, kInnerWarps);
+            ptx::mbar_init(hfull + 8 * i, 256);  // the fetching threads' copies, and their decays
+            ptx::mbar_init(hempty + 8 * i, kGradWarps);
         }
         for (int i = 0; i < P::kStages; ++i) {
-            ptx::mbar_init(base + P::kFull + 8 * i, 129);   // the fetching threads, and the states' bytes
-            ptx::mbar_init(base + P::kEmpty + 8 * i, 1 + kInnerWarps);
+            ptx::mbar_init(full + 8 * i, 129);
+            ptx::mbar_init(empty + 8 * i, kGradWarps);
         }
-        *reinterpret_cast<volatile int *>(sm_raw + P::kAbort) = 0;
+        *abort_flag = 0;
         ptx::fence_mbar_init();
     }
-    if (warp == 12) ptx::tmem_alloc(base + P::kTmem, kTmemCols);
-    ptx::tc_fence_before();
     __syncthreads();
-    ptx::tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm_raw + P::kTmem);
-    bool ok = true;
-    if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        ok = grad_epilogue<KT>(p, a, sm_raw, tmem, warp >> 2);
-    } else {
+    if (warp >= kGradWarps) {
         give_registers();
-        if (warp < 12) grad_fetch<KT>(p, a, sm_raw);
-        else if (warp == 12) { if (lane == 0) ok = grad_issue<KT>(p, a, sm_raw, tmem); }
-        else ok = grad_inner<KT>(p, a, sm_raw, warp - 13, lane);
+        grad_fetch<KT>(p, a, sm_raw);
+        return;
     }
-    if (!ok) {
-        *reinterpret_cast<volatile int *>(sm_raw + P::kAbort) = 1;
-        record_status(GLA_ERR_TIMEOUT);
-    }
-    __syncwarp();
-    ptx::tc_fence_before();
-    __syncthreads();  // every wait above is bounded, so all warps come here
-    if (warp == 12) {
-        ptx::tmem_relinquish();
-        ptx::tmem_dealloc(tmem, kTmemCols);
+    take_registers();
+    // A tile of 16 tokens costs the more the further down it lies (T, R', N are triangular); the four SM quarters
+    // take warps in turn, so Y's tiles run against dO's.
+    const int role = warp >> 2, rt = role == 1 ? 3 - (warp & 3) : warp & 3;
+    const int gr = lane >> 2, tg = lane & 3, m8 = lane >> 3, r8 = lane & 7;
+    const int row0 = rt * 16 + gr;  // this lane's rows: row0 and row0 + 8
+    const int tiles = (p.dv + 15) / 16, slabs = (tiles + P::kTiles - 1) / P::kTiles;
+    const uint32_t mt = base + P::kOffM, nt = mt + kG * kMRow;
+    float *exchange = reinterpret_cast<float *>(sm_raw + P::kOffX);
+    int n = 0, ns = 0;
+    for (unsigned unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
+        const int slot = (int)(unit / (unsigned)p.H), h = (int)(unit % (unsigned)p.H);
+        ChunkAt at;
+        if (!chunk_of_slot<kG>(slot, p, at)) continue;
+        const int hb = n & 1;
+        // a warp whose wait runs out goes on to the next barrier, where all learn of it and leave together
+        bool ok = warp_wait(hfull + 8 * hb, (n / 2) & 1, abort_flag);
+        Sums &sums = *reinterpret_cast<Sums *>(sm_raw + P::kOffSums + hb * sizeof(Sums));
+        ++n;
+        const uint32_t ks = base + P::kOffHead + hb * P::kHead, qs = ks + P::kTile;
+        const Decays &dc = *reinterpret_cast<const Decays *>(sm_raw + P::kOffHead + hb * P::kHead + 2 * P::kTile);
+        // T = do_i . r_j (or y_i . r_j) on and below the diagonal; A: this role's product with a state
+        float T[8][4] = {}, A[2 * KT][4] = {}, inner = 0.f;
+        for (int s = 0; s < slabs; ++s, ++ns) {
+            const int sg = ns % P::kStages;
+            ok = ok && warp_wait(full + 8 * sg, (ns / P::kStages) & 1, abort_flag);
+            if (!ok) break;
+            const uint32_t slab = base + P::kOffSlab + sg * P::kSlab;
+            const uint32_t a_at = slab + (role * kG + rt * 16 + (m8 & 1) * 8 + r8) * P::kSlabRow + (m8 >> 1) * 16;
+            const uint32_t b_at = slab + (2 * kG + (m8 >> 1) * 8 + r8) * P::kSlabRow + (m8 & 1) * 16;
+            const uint32_t image = slab + 3 * kG * P::kSlabRow + (role == 2 ? P::kImage : 0) + lane * 16;  // matrix lane / 8, row lane % 8
+            const int here = min(P::kTiles, tiles - P::kTiles * s);
+#pragma unroll
+            for (int x = 0; x < P::kTiles; ++x) {
+                if (x >= here) break;
+                uint32_t f[4];
+                ldsm4(f, a_at + x * 32);
+#pragma unroll
+                for (int i = 0; i < KT; ++i) {
+                    uint32_t b[4];
+                    ldsm4t(b, image + (x * KT + i) * 512);
+                    mma(A[2 * i], f, b[0], b[1]);
+                    mma(A[2 * i + 1], f, b[2], b[3]);
+                }
+                if (role < 2) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        if (t <= rt) {
+                            uint32_t b[4];
+                            ldsm4(b, b_at + t * 16 * P::kSlabRow + x * 32);
+                            mma(T[2 * t], f, b[0], b[1]);
+                            mma(T[2 * t + 1], f, b[2], b[3]);
+                        }
+                }
+            }
+            for (int i = tid; i < here * KT * 32; i += kGradWarps * 32) {  // <S0, dS1>
+                const uint4 x = lds128(slab + 3 * kG * P::kSlabRow + i * 16),
+                            y = lds128(slab + 3 * kG * P::kSlabRow + P::kImage + i * 16);
+                const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) inner = fmaf(lo_f(xw[e]), lo_f(yw[e]), fmaf(hi_f(xw[e]), hi_f(yw[e]), inner));
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(empty + 8 * sg);
+        }
+        if (!ok && lane == 0) {
+            *abort_flag = 1;
+            record_status(GLA_ERR_TIMEOUT);
+        }
+        for (int m = 16; m > 0; m >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, m);
+        if (lane == 0) sums.inner[warp] = inner;
+        float lo, hi;
+        // the state's part of dq and dk, and its share of dg
+        {
+            const float *v = role == 2 ? dc.d : dc.c;
+            float f0 = v[row0], f1 = v[row0 + 8];
+            if (role > 0) {
+                f0 *= role == 1 ? -dc.beta[row0] : dc.beta[row0];
+                f1 *= role == 1 ? -dc.beta[row0 + 8] : dc.beta[row0 + 8];
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * KT; ++i) {
+                A[i][0] *= f0; A[i][1] *= f0; A[i][2] *= f1; A[i][3] *= f1;
+            }
+            row_dots<KT>(A, (role ? ks : qs) + rt * 16 * row_bytes<KT>(), lane, lo, hi);
+            float *to = role == 0 ? sums.wq : role == 1 ? sums.wk : sums.x;
+            if (tg == 0) {
+                to[row0] = lo;
+                to[row0 + 8] = hi;
+            }
+        }
+        if (role < 2) {  // R' or N
+            float between[4];  // whole tiles strictly between tile t and this warp's
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                float f = 1.f;
+                for (int m = t + 1; m < rt; ++m) f *= dc.whole[m];
+                between[t] = f;
+            }
+            float own0 = 0.f, own1 = 0.f;  // the diagonal's two elements, where tg == gr / 2
+            const float p0 = dc.pre[row0], p1 = dc.pre[row0 + 8];
+            const float g0 = role ? -dc.beta[row0] : 1.f, g1 = role ? -dc.beta[row0 + 8] : 1.f;
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+                if (t <= 2 * rt + 1) {
+                    const int j = t * 8 + 2 * tg;
+                    const float b0 = dc.beta[j], b1 = dc.beta[j + 1];
+                    float x[4];
+                    if ((t >> 1) == rt) {
+                        const float *D = dc.diag[rt] + gr * 16 + (j & 15);
+                        const float2 u = *reinterpret_cast<const float2 *>(D), v = *reinterpret_cast<const float2 *>(D + 128);
+                        const int i0 = row0, i1 = row0 + 8, off = role;  // N leaves the diagonal out
+                        if (t == 2 * rt) own0 = gr & 1 ? T[t][1] : T[t][0];
+                        else own1 = gr & 1 ? T[t][3] : T[t][2];
+                        x[0] = j + off <= i0 ? g0 * b0 * u.x * T[t][0] : 0.f;
+                        x[1] = j + 1 + off <= i0 ? g0 * b1 * u.y * T[t][1] : 0.f;
+                        x[2] = j + off <= i1 ? g1 * b0 * v.x * T[t][2] : 0.f;
+                        x[3] = j + 1 + off <= i1 ? g1 * b1 * v.y * T[t][3] : 0.f;
+                    } else {
+                        const float m = between[t >> 1], s0 = m * dc.suf[j] * b0, s1 = m * dc.suf[j + 1] * b1;
+                        x[0] = g0 * p0 * s0 * T[t][0];
+                        x[1] = g0 * p0 * s1 * T[t][1];
+                        x[2] = g1 * p1 * s0 * T[t][2];
+                        x[3] = g1 * p1 * s1 * T[t][3];
+                    }
+                    char *to = sm_raw + P::kOffM + (role * kG + row0) * kMRow + j * 2;
+                    *reinterpret_cast<uint32_t *>(to) = pack(x[0], x[1]);
+                    *reinterpret_cast<uint32_t *>(to + 8 * kMRow) = pack(x[2], x[3]);
+                }
+            if (role && tg == gr >> 1) {
+                if (row0 < at.len) store_gate<bf16>(a.dbeta, (at.row + row0) * p.H + h, p.gate_f32, own0);
+                if (row0 + 8 < at.len) store_gate<bf16>(a.dbeta, (at.row + row0 + 8) * p.H + h, p.gate_f32, own1);
+            }
+        }
+        if (any_of<1, kGradWarps * 32>(!ok)) return;  // R' and N are whole
+        {
+            float acc[2 * KT][4] = {};
+            if (role < 2) {  // R' K or N K
+                const uint32_t own = (role ? nt : mt) + (rt * 16 + (m8 & 1) * 8 + r8) * kMRow + (m8 >> 1) * 16;
+                for (int t = 0; t <= rt; ++t) {
+                    uint32_t f[4];
+                    ldsm4(f, own + t * 32);
+                    add_rows<KT>(acc, f, ks + t * 16 * row_bytes<KT>(), lane);
+                }
+            } else {  // R'^T Q + N^T K
+                const uint32_t flip = ((m8 >> 1) * 8 + r8) * kMRow + rt * 32 + (m8 & 1) * 16;
+                for (int t = rt; t < 4; ++t) {
+                    uint32_t f[4];
+                    ldsm4t(f, mt + flip + t * 16 * kMRow);
+                    add_rows<KT>(acc, f, qs + t * 16 * row_bytes<KT>(), lane);
+                    ldsm4t(f, nt + flip + t * 16 * kMRow);
+                    add_rows<KT>(acc, f, ks + t * 16 * row_bytes<KT>(), lane);
+                }
+            }
+            row_dots<KT>(acc, (role ? ks : qs) + rt * 16 * row_bytes<KT>(), lane, lo, hi);
+            float *to = role == 0 ? sums.mq : role == 1 ? sums.my : sums.mr;
+            if (tg == 0) {
+                to[row0] = role == 2 ? lo : -lo;
+                to[row0 + 8] = role == 2 ? hi : -hi;
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * KT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) A[i][e] += acc[i][e];
+        }
+        if (role == 2) {
+#pragma unroll
+            for (int i = 0; i < 2 * KT; ++i) {
+                *reinterpret_cast<float2 *>(exchange + row0 * P::kXRow + i * 8 + 2 * tg) = make_float2(A[i][0], A[i][1]);
+                *reinterpret_cast<float2 *>(exchange + (row0 + 8) * P::kXRow + i * 8 + 2 * tg) = make_float2(A[i][2], A[i][3]);
+            }
+        }
+        compute_sync();  // R's part of dk and all sums are there; K, Q and the decays are read
+        if (role == 1) {
+#pragma unroll
+            for (int i = 0; i < 2 * KT; ++i) {
+                const float2 u = *reinterpret_cast<const float2 *>(exchange + row0 * P::kXRow + i * 8 + 2 * tg);
+                const float2 v = *reinterpret_cast<const float2 *>(exchange + (row0 + 8) * P::kXRow + i * 8 + 2 * tg);
+                A[i][0] += u.x; A[i][1] += u.y; A[i][2] += v.x; A[i][3] += v.y;
+            }
+        }
+        if (role < 2 && a.dq_part == nullptr) {
+            // 64 columns at a time through this warp's own 16 rows of R' or N, which the barrier has left free
+            const uint32_t tile = (role ? nt : mt) + rt * 16 * kMRow;
+            bf16 *to = (role ? a.dk : a.dq) + ((at.row + rt * 16) * p.H + h) * p.dk;
+#pragma unroll
+            for (int i0 = 0; i0 < 2 * KT; i0 += 8) {
+                __syncwarp();
+#pragma unroll
+                for (int i = i0; i < (i0 + 8 < 2 * KT ? i0 + 8 : 2 * KT); i += 2)
+                    stsm4(tile + ((m8 & 1) * 8 + r8) * kMRow + (i - i0 + (m8 >> 1)) * 16, pack(A[i][0], A[i][1]),
+                          pack(A[i][2], A[i][3]), pack(A[i + 1][0], A[i + 1][1]), pack(A[i + 1][2], A[i + 1][3]));
+                __syncwarp();
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int row = x * 4 + (lane >> 3), u = i0 + (lane & 7);
+                    if (rt * 16 + row < at.len && u * 8 < p.dk)
+                        *reinterpret_cast<uint4 *>(to + (int64_t)row * p.H * p.dk + u * 8) =
+                            lds128(tile + row * kMRow + (lane & 7) * 16);
+                }
+            }
+            __syncwarp();
+        } else if (role < 2) {
+            float *to = (role ? a.dk_part : a.dq_part) + ((at.row + row0) * p.H + h) * p.dk + 2 * tg;
+            const int64_t far = (int64_t)8 * p.H * p.dk;
+#pragma unroll
+            for (int i = 0; i < 2 * KT; ++i)
+                if (i * 8 < p.dk) {
+                    if (row0 < at.len) *reinterpret_cast<float2 *>(to + i * 8) = make_float2(A[i][0], A[i][1]);
+                    if (row0 + 8 < at.len) *reinterpret_cast<float2 *>(to + far + i * 8) = make_float2(A[i][2], A[i][3]);
+                }
+        }
+        if (warp == 8) {  // dg: lane owns tokens 2 lane and 2 lane + 1
+            float f = 0.f;
+#pragma unroll
+            for (int m = 0; m < kGradWarps; ++m) f += sums.inner[m];
+            f *= dc.c[kG - 1];
+            const int i = 2 * lane;
+            const float w0 = sums.wq[i] + sums.wk[i], w1 = sums.wq[i + 1] + sums.wk[i + 1];
+            const float x0 = sums.x[i] + (sums.mq[i] + sums.my[i] + sums.mr[i]),
+                        x1 = sums.x[i + 1] + (sums.mq[i + 1] + sums.my[i + 1] + sums.mr[i + 1]);
+            float pre = x0 + x1, suf = w0 + w1;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const float u = __shfl_up_sync(0xffffffffu, pre, m), v = __shfl_down_sync(0xffffffffu, suf, m);
+                if (lane >= m) pre += u;
+                if (lane + m < 32) suf += v;
+            }
+            const float left = pre - (x0 + x1);  // tokens before 2 lane
+            if (i < at.len) store_gate<bf16>(a.dg, (at.row + i) * p.H + h, p.gate_f32, f + left + suf);
+            if (i + 1 < at.len) store_gate<bf16>(a.dg, (at.row + i + 1) * p.H + h, p.gate_f32, f + left + x0 + (suf - w0));
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(hempty + 8 * hb);
     }
 }
 
