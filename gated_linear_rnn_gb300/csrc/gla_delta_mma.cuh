@@ -163,6 +163,26 @@ template <int kBarrier, int kThreads> __device__ __forceinline__ bool any_of(boo
     return any != 0;
 }
 
+// The sequence of a packed batch that is the rank-th longest (the first of equals first), by all threads of a block.  Blocks
+// start in their order, so the longest chains start first and the last ones to end are short: 301 us against 353 in the
+// batch's own order at 24 sequences of up to 2,048 tokens (16 heads, 96/192).
+// Up to 256 sequences, since each thread ranks one by looking at all lengths; more are many waves of blocks anyway.
+constexpr int kMostRanked = 256;
+__device__ __forceinline__ int ranked_sequence(const Shape &p, int rank, volatile int *place) {
+    for (int t = threadIdx.x; t < p.nseq; t += blockDim.x) {
+        SeqRange r, o;
+        seq_range(t, p.T, p.cu, r);
+        int before = 0;
+        for (int i = 0; i < p.nseq; ++i) {
+            seq_range(i, p.T, p.cu, o);
+            before += o.len > r.len || (o.len == r.len && i < t);
+        }
+        if (before == rank) *place = t;
+    }
+    __syncthreads();
+    return *place;
+}
+
 // Who a block and a thread are, and the shared memory: barriers, the stages (K | Q | V | record | a second output).
 struct Frame {
     int lane, warp, s, h, hk, col0, width, nch;
@@ -186,6 +206,10 @@ struct Frame {
         width = min(w.warps * 16, p.dv - col0);                   // its columns of v, a multiple of 8 (none: <= 0)
         exists = first = last = true;
         if (w.segment == 0) {
+            if (p.cu != nullptr && p.nseq > 1 && p.nseq <= kMostRanked) {
+                s = ranked_sequence(p, s, reinterpret_cast<volatile int *>(sm + 16 * w.stages + 4));
+                walk = s * p.H + h;
+            }
             bad = !seq_range(s, p.T, p.cu, r);
             slot0 = r.start / kC + s;
         } else {
