@@ -15,6 +15,11 @@
 // forward's state needs; states and all sums are f32.  One rounding to bf16 is 1.7e-3 of a vector's norm, and
 // they add in squares: X and dU, which every residual and every Y are made of, keep their lo parts (six products of
 // 16 x 8 x 16 a chunk each), which takes dbeta, a product of both, from 4.7e-3 to 4e-3.
+//
+// Eight sequences of 2,048 tokens, 16 heads of 96/192: 552 us: preparation 55, both walks 225 (260 before the fetching
+// warps gave registers to the computing ones), gradient kernel 269.  The walks run in one launch since neither fills
+// the GPU alone on a small batch; on a large one shared
+// memory's pipe (71% busy) and mma.sync's (54%) bound them.
 #include "gla_delta_mma.cuh"
 
 GLA_DEFINE_STATUS(delta_bwd)

@@ -163,9 +163,9 @@ template <int kBarrier, int kThreads> __device__ __forceinline__ bool any_of(boo
     return any != 0;
 }
 
-// The sequence of a packed batch that is the rank-th longest (the first of equals first), by all threads of a block.  Blocks
-// start in their order, so the longest chains start first and the last ones to end are short: 301 us against 353 in the
-// batch's own order at 24 sequences of up to 2,048 tokens (16 heads, 96/192).
+// The sequence of a packed batch that is the rank-th longest (the first of equals first), by all threads of a block.
+// Blocks start in their order, so the longest chains start first and the last ones to end are short: 301 us against
+// 353 in the batch's own order at 24 sequences of up to 2,048 tokens (16 heads, 96/192).
 // Up to 256 sequences, since each thread ranks one by looking at all lengths; more are many waves of blocks anyway.
 constexpr int kMostRanked = 256;
 __device__ __forceinline__ int ranked_sequence(const Shape &p, int rank, volatile int *place) {

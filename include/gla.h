@@ -452,6 +452,9 @@ GLA_API int gla_conv1d_silu_step(const void *x, const float *weight, const float
  *   gate_dtype  GLA_F32, or dtype: g, beta and their gradients.  (With bf16 inputs the gradients carry the
  *               rounding of bf16 products, about 2e-3 of their size, in either type.)
  * All states and sums are f32.  Sizes: 16 <= dk <= 256, 16 <= dv <= 512, both multiples of 8.
+ * bf16 sequences run in chunks: a NaN or an infinity at a token may reach the other tokens of its chain within
+ * the 32 around it (64 in the gradients) as well as all later ones (earlier ones, in the gradients), and no
+ * other chain.  f32 sequences run token by token.
  */
 
 /*
