@@ -19,7 +19,7 @@
 // Eight sequences of 2,048 tokens, 16 heads of 96/192: 552 us: preparation 55, both walks 225 (260 before the fetching
 // warps gave registers to the computing ones), gradient kernel 269.  The walks run in one launch since neither fills
 // the GPU alone on a small batch; on a large one shared
-// memory's pipe (71% busy) and mma.sync's (54%) bound them.
+// memory's pipe (70% busy) and mma.sync's (54%) bound them.
 #include "gla_delta_mma.cuh"
 
 GLA_DEFINE_STATUS(delta_bwd)

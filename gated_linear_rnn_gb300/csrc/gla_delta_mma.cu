@@ -31,12 +31,12 @@
 // twice.  (One warp in its place was what the walk waited for: 360 us against 246 at the sizes below.)
 //
 // Eight sequences of 2,048 tokens, 16 heads of 96/192: 213 us, preparation 45 and walk 163.  That is 1.5 TB/s of the
-// inputs and outputs: the walk keeps mma.sync's pipe 62% busy with one block of 128 registers a thread on an SM, and
-// 24% of its warps; HBM would need 46 us.
+// inputs and outputs: the walk keeps mma.sync's pipe 71% busy with one block of 128 registers a thread on an SM, and
+// a quarter of its warps; HBM would need 46 us.
 //
 // A third and a fourth kernel serve few long chains, cut into segments (segment_tokens): a walk over each segment's
 // map S -> M S + N, delta_join_kernel over the maps, then the walk of every segment from its own state.  32,768
-// tokens of 16 heads: 874 us (preparation 78, maps 450, join 48, walk 300), against 1,416 as whole chains.
+// tokens of 16 heads: 867 us (preparation 78, maps 450, join 48, walk 300), against 1,416 as whole chains.
 #include "gla_delta_mma.cuh"
 
 GLA_DEFINE_STATUS(delta_mma)
