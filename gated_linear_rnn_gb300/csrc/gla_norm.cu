@@ -29,12 +29,13 @@ constexpr int kThreads = 256;
 
 enum Act { kNone = GLA_ACT_NONE, kSilu = GLA_ACT_SILU, kSigmoid = GLA_ACT_SIGMOID };
 
-// q = 1 / (1 + e^-x) and rest = 1 - q, each to a few units in its last place: rest is e^-x q (1 - q would leave 2^-24
-// of one where q is near 1, which SiLU's slope multiplies by x).  Below x = -80 q stays at e^-80: the product
-// of an infinite e^-x with 0 would not be a number.
+// q = 1 / (1 + e^-x) and rest = 1 - q, each to 2 + |x| units of 2^-24 (the rounding of e^-x's argument), and a NaN where x
+// is one.  rest is e^-x q (1 - q would leave 2^-24 of one where q is near 1, which SiLU's slope multiplies by x).  Below
+// x = -87 e^-x runs into infinity and q into 0, which is the limit; rest is 1 to the last bit from x = -20 on and is not
+// taken from their product there.
 __device__ __forceinline__ void sigmoid(Pair x, Pair &q, Pair &rest) {
     const float2 f = parts(x);
-    const float2 t = parts(pair(fmaxf(f.x, -80.f), fmaxf(f.y, -80.f)) * both(-1.4426950408889634f));
+    const float2 t = parts(x * both(-1.4426950408889634f));
     float e0, e1, q0, q1;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t.y));
@@ -43,7 +44,8 @@ __device__ __forceinline__ void sigmoid(Pair x, Pair &q, Pair &rest) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q0) : "f"(d.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q1) : "f"(d.y));
     q = pair(q0, q1);
-    rest = e * q;
+    const float2 r = parts(e * q);
+    rest = pair(f.x < -20.f ? 1.f : r.x, f.y < -20.f ? 1.f : r.y);
 }
 
 // Lanes per group (a power of two, whole warps above 32) and vectors of four channels per lane.
@@ -235,7 +237,7 @@ norm_fwd_kernel(const T *__restrict__ x, const float *__restrict__ weight, const
                     Pair q, rest;
                     if (kAct != kNone) sigmoid(t, q, rest);
                     if (kAct == kNone) y[e] = kGate ? z * t : z;
-                    else if (kAct == kSilu) y[e] = (kGate ? z * t : z) * q;
+                    else if (kAct == kSilu) y[e] = kGate ? z * (t * q) : z * q;  // t q first: z t may overflow where q is 0
                     else y[e] = kGate ? z * q : q;
                 }
                 Vec<T>::put(out + row * C + pl.channel + j * pl.stride, y);
