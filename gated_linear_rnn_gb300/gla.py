@@ -525,7 +525,8 @@ def _allocating_on(stream, device):
     if stream is None:
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        # torch takes a null handle for no handle, and would make another stream of its own
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
     return torch.cuda.stream(stream)
 
 
