@@ -451,14 +451,29 @@ def gla_conv1d_silu_step(x, weight, bias, state_inout, y, stream=None) -> None:
 ACT_NONE, ACT_SILU, ACT_SIGMOID = 0, 1, 2  # gla_act
 
 
-def _arg(t: Optional[torch.Tensor], name: str, dtype, shape, allow_none: bool = False):
-    """The device pointer of a contiguous CUDA tensor of this type and shape (None for an absent one)."""
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _device(t: torch.Tensor, name: str) -> int:
+    """The device of a call's first tensor, which has to be the current one: the library launches there."""
+    at = t.get_device()
+    if at < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if at != _current_device():
+        raise ValueError(f"{name} lies on device {at}, which is not the current device, {_current_device()}")
+    return at
+
+
+def _arg(t: Optional[torch.Tensor], name: str, dtype, shape, device: int, allow_none: bool = False):
+    """The device pointer of a contiguous tensor of this type and shape on ``device`` (None for an absent one)."""
     if t is None:
         if not allow_none:
             raise ValueError(f"{name} is required")
         return None
-    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()):
         _check(t, name, dtype, shape)
+        raise ValueError(f"{name} must lie on device {device}, got {t.device}")
     return t.data_ptr()
 
 
@@ -494,18 +509,18 @@ def _delta_args(q, k, v, g, beta, h0, out, hT, cu_seqlens):
     B, T, Hk, dk = q.shape
     _, _, H, dv = v.shape
     dtype, gates = _delta_types(q, g, H, Hk)
+    at = _device(q, "q")
     nseq = B
     cu = None
     if cu_seqlens is not None:
         if B != 1:
             raise ValueError("a packed batch has leading dimension 1")
-        _check(cu_seqlens, "cu_seqlens", torch.int32)
-        nseq, cu = cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
+        nseq, cu = cu_seqlens.numel() - 1, _arg(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, at)
     qs, vs, gs, hs = q.shape, (B, T, H, dv), (B, T, H), (nseq, H, dk, dv)
     t, gt = q.dtype, g.dtype
-    ptrs = (_arg(q, "q", t, qs), _arg(k, "k", t, qs), _arg(v, "v", t, vs), _arg(g, "g", gt, gs),
-            _arg(beta, "beta", gt, gs), _arg(h0, "h0", torch.float32, hs, True), _arg(out, "out", t, vs),
-            _arg(hT, "hT", torch.float32, hs, True))
+    ptrs = (_arg(q, "q", t, qs, at), _arg(k, "k", t, qs, at), _arg(v, "v", t, vs, at), _arg(g, "g", gt, gs, at),
+            _arg(beta, "beta", gt, gs, at), _arg(h0, "h0", torch.float32, hs, at, True), _arg(out, "out", t, vs, at),
+            _arg(hT, "hT", torch.float32, hs, at, True))
     return ptrs, (nseq, T, H, Hk, dk, dv, dtype, gates), cu
 
 
@@ -533,8 +548,8 @@ def _allocating_on(stream, device):
 def _workspace(given, need: int, device, stream):
     """(tensor, pointer, bytes) of the caller's workspace, or of one from torch's allocator on ``stream``."""
     if given is not None:
-        if not given.is_cuda or not given.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
+        if given.device != device or not given.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
         return given, given.data_ptr(), given.numel() * given.element_size()
     if need == 0:
         return None, None, 0
@@ -558,13 +573,14 @@ def gla_delta_chunk_bwd(q, k, v, g, beta, dout, h0, dhT, dq, dk, dv, dg, dbeta, 
     """Gradients of gla_delta_chunk_fwd: writes dq, dk, dv, dg, dbeta and (if given) dh0.  See include/gla.h."""
     ptrs, sizes, cu = _delta_args(q, k, v, g, beta, h0, dout, dhT, cu_seqlens)
     nseq, _, H, _, dk_, dv_ = sizes[:6]
-    grads = (_arg(dq, "dq", q.dtype, q.shape), _arg(dk, "dk", q.dtype, q.shape), _arg(dv, "dv", q.dtype, v.shape),
-             _arg(dg, "dg", g.dtype, g.shape), _arg(dbeta, "dbeta", g.dtype, g.shape),
-             _arg(dh0, "dh0", torch.float32, (nseq, H, dk_, dv_), True))
+    t, gt, at = q.dtype, g.dtype, q.get_device()
+    grads = (_arg(dq, "dq", t, q.shape, at), _arg(dk, "dk", t, q.shape, at), _arg(dv, "dv", t, v.shape, at),
+             _arg(dg, "dg", gt, g.shape, at), _arg(dbeta, "dbeta", gt, g.shape, at),
+             _arg(dh0, "dh0", torch.float32, (nseq, H, dk_, dv_), at, True))
     need = gla_delta_workspace_bytes(OP_BACKWARD, *sizes[:7], cu is not None)
-    ws, at, n = _workspace(workspace, need, q.device, stream)
+    ws, ws_at, n = _workspace(workspace, need, q.device, stream)
     p = ptrs
-    rc = load().gla_delta_chunk_bwd(p[0], p[1], p[2], p[3], p[4], p[6], p[5], p[7], *grads, *sizes, cu, at, n,
+    rc = load().gla_delta_chunk_bwd(p[0], p[1], p[2], p[3], p[4], p[6], p[5], p[7], *grads, *sizes, cu, ws_at, n,
                                     _raw_stream(stream, q.device))
     _raise(rc, "gla_delta_chunk_bwd")
 
@@ -578,11 +594,12 @@ def gla_delta_decode_step(q, k, v, g, beta, state, out, slots=None, stream=None)
     _, H, dv = v.shape
     dtype, gates = _delta_types(q, g, H, Hk)
     pages = state.shape[0] if slots is not None else N
-    qs, vs, gs, t, gt = q.shape, (N, H, dv), (N, H), q.dtype, g.dtype
+    qs, vs, gs, t, gt, at = q.shape, (N, H, dv), (N, H), q.dtype, g.dtype, _device(q, "q")
     rc = load().gla_delta_decode_step(
-        _arg(q, "q", t, qs), _arg(k, "k", t, qs), _arg(v, "v", t, vs), _arg(g, "g", gt, gs), _arg(beta, "beta", gt, gs),
-        _arg(state, "state", torch.float32, (pages, H, dk, dv)), _arg(slots, "slots", torch.int32, (N,), True), pages,
-        _arg(out, "out", t, vs), N, H, Hk, dk, dv, dtype, gates, _raw_stream(stream, q.device))
+        _arg(q, "q", t, qs, at), _arg(k, "k", t, qs, at), _arg(v, "v", t, vs, at), _arg(g, "g", gt, gs, at),
+        _arg(beta, "beta", gt, gs, at), _arg(state, "state", torch.float32, (pages, H, dk, dv), at),
+        _arg(slots, "slots", torch.int32, (N,), at, True), pages, _arg(out, "out", t, vs, at), N, H, Hk, dk, dv, dtype,
+        gates, _raw_stream(stream, q.device))
     if rc:
         raise GLAError(rc, "gla_delta_decode_step")
 
@@ -592,10 +609,10 @@ def _norm_args(x, weight, bias, groups, gate, out):
     if groups <= 0 or C % groups or C == 0:
         raise ValueError("the last dimension of x must be a multiple of groups")
     dtype = _dtype(x, "x")
-    t, s = x.dtype, x.shape
-    ptrs = (_arg(x, "x", t, s), _arg(weight, "weight", torch.float32, (C,), True),
-            _arg(bias, "bias", torch.float32, (C,), True), _arg(gate, "gate", t, s, True))
-    return ptrs, _arg(out, "out", t, s), x.numel() // C, C // groups, dtype
+    t, s, at = x.dtype, x.shape, _device(x, "x")
+    ptrs = (_arg(x, "x", t, s, at), _arg(weight, "weight", torch.float32, (C,), at, True),
+            _arg(bias, "bias", torch.float32, (C,), at, True), _arg(gate, "gate", t, s, at, True))
+    return ptrs, _arg(out, "out", t, s, at), x.numel() // C, C // groups, dtype
 
 
 def gla_group_norm(x, weight, bias, groups: int, out, gate=None, act: int = ACT_SILU, eps: float = 1e-5,
@@ -620,12 +637,12 @@ def gla_group_norm_bwd(dout, x, weight, bias, groups: int, dx, dweight, dbias, d
                        act: int = ACT_SILU, eps: float = 1e-5, workspace=None, stream=None) -> None:
     """Gradients of gla_group_norm: writes dx, dweight, dbias and (with a gate) dgate.  See include/gla.h."""
     ptrs, to, rows, width, dtype = _norm_args(x, weight, bias, groups, gate, dx)
-    C = (x.shape[-1],)
-    grads = (_arg(dweight, "dweight", torch.float32, C, True), _arg(dbias, "dbias", torch.float32, C, True),
-             _arg(dgate, "dgate", x.dtype, x.shape, gate is None))
-    ws, at, n = _workspace(workspace, gla_group_norm_workspace_bytes(rows, groups, width), x.device, stream)
-    rc = load().gla_group_norm_bwd(_arg(dout, "dout", x.dtype, x.shape), *ptrs, act, eps, to, *grads, rows, groups, width,
-                                   dtype, at, n, _raw_stream(stream, x.device))
+    C, t, at = (x.shape[-1],), x.dtype, x.get_device()
+    grads = (_arg(dweight, "dweight", torch.float32, C, at, True), _arg(dbias, "dbias", torch.float32, C, at, True),
+             _arg(dgate, "dgate", t, x.shape, at, gate is None))
+    ws, ws_at, n = _workspace(workspace, gla_group_norm_workspace_bytes(rows, groups, width), x.device, stream)
+    rc = load().gla_group_norm_bwd(_arg(dout, "dout", t, x.shape, at), *ptrs, act, eps, to, *grads, rows, groups, width,
+                                   dtype, ws_at, n, _raw_stream(stream, x.device))
     _raise(rc, "gla_group_norm_bwd")
 
 
