@@ -65,7 +65,7 @@ int simt_fwd(const Shape &, const T *, const T *, const T *, const void *, const
              cudaStream_t);
 size_t simt_bwd_workspace(const Shape &);
 template <typename T>
-int simt_bwd(const Shape &, const T *, const T *, const T *, const void *, const void *, const T *, const float *,
+int simt_bwd(Shape, const T *, const T *, const T *, const void *, const void *, const T *, const float *,
              const float *, T *, T *, T *, void *, void *, float *, void *, cudaStream_t);
 bool mma_supported(int dk);
 bool mma_bwd_supported(int dk);

@@ -345,7 +345,9 @@ delta_rec_fwd_kernel(Shape p, const T *__restrict__ q, const T *__restrict__ k, 
     __shared__ __align__(16) St sm[2];
     const Lane<kRpl> ln(p);
     SeqRange r;
-    if (!seq_range(ln.s, p.T, p.cu, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
+    if (!checked_rows(p, offsets_in_order(p), ln.s, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
+    if (p.rows != nullptr && ln.h == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+        p.rows[ln.s] = make_int2((int)r.start, (int)r.len);
     Pair S[kRpl / 2];
     ln.load(S, h0, p);
     const int64_t slot0 = r.start / 64 + ln.s;
@@ -407,8 +409,7 @@ delta_rec_bwd_kernel(Shape p, const T *__restrict__ q, const T *__restrict__ k, 
     constexpr int kTok = St::kTok;
     __shared__ __align__(16) St sm[2];
     const Lane<kRpl> ln(p);
-    SeqRange r;
-    if (!seq_range(ln.s, p.T, p.cu, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
+    const SeqRange r = rows_of(p, ln.s);
     Pair S[kRpl / 2];
     ln.load(S, dhT, p);
     const int64_t slot0 = r.start / 64 + ln.s, last = r.len > 0 ? (r.len - 1) / kTok * kTok : -1;
@@ -685,7 +686,7 @@ int rec_fwd(const Shape &p, const T *q, const T *k, const T *v, const void *g, c
 size_t simt_bwd_workspace(const Shape &p) {
     const size_t rows = (size_t)total_rows(p) * p.H * p.dv;
     const size_t state = (size_t)chunk_slots(total_rows(p), p.nseq, kG) * p.H * p.dk * p.dv;
-    return 2 * (rows + state) * sizeof(float);
+    return rows_bytes(p) + 2 * (rows + state) * sizeof(float);
 }
 
 template <typename T>
@@ -695,13 +696,14 @@ int simt_fwd(const Shape &p, const T *q, const T *k, const T *v, const void *g, 
 }
 
 template <typename T>
-int simt_bwd(const Shape &p, const T *q, const T *k, const T *v, const void *g, const void *beta, const T *dout,
+int simt_bwd(Shape p, const T *q, const T *k, const T *v, const void *g, const void *beta, const T *dout,
              const float *h0, const float *dhT, T *dq, T *dk, T *dv, void *dg, void *dbeta, float *dh0, void *ws,
              cudaStream_t st) {
     const long long rows = total_rows(p), slots = chunk_slots(rows, p.nseq, kG);
     if (slots * p.Hk > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
     const size_t state = (size_t)slots * p.H * p.dk * p.dv;
-    float *s0 = (float *)ws, *ds1 = s0 + state, *resid = ds1 + state, *ys = resid + (size_t)rows * p.H * p.dv;
+    p.rows = p.cu ? (int2 *)ws : nullptr;
+    float *s0 = (float *)((char *)ws + rows_bytes(p)), *ds1 = s0 + state, *resid = ds1 + state, *ys = resid + (size_t)rows * p.H * p.dv;
     int rc = rec_fwd<T>(p, q, k, v, g, beta, h0, nullptr, nullptr, resid, s0, st);
     if (rc != GLA_OK) return rc;
     const dim3 grid((unsigned)((long long)p.nseq * p.H), (unsigned)((p.dv + kCols - 1) / kCols));
@@ -722,10 +724,10 @@ template int simt_fwd<float>(const Shape &, const float *, const float *, const 
                              const float *, float *, float *, cudaStream_t);
 template int simt_fwd<__nv_bfloat16>(const Shape &, const __nv_bfloat16 *, const __nv_bfloat16 *, const __nv_bfloat16 *,
                                      const void *, const void *, const float *, __nv_bfloat16 *, float *, cudaStream_t);
-template int simt_bwd<float>(const Shape &, const float *, const float *, const float *, const void *, const void *,
+template int simt_bwd<float>(Shape, const float *, const float *, const float *, const void *, const void *,
                              const float *, const float *, const float *, float *, float *, float *, void *, void *,
                              float *, void *, cudaStream_t);
-template int simt_bwd<__nv_bfloat16>(const Shape &, const __nv_bfloat16 *, const __nv_bfloat16 *,
+template int simt_bwd<__nv_bfloat16>(Shape, const __nv_bfloat16 *, const __nv_bfloat16 *,
                                      const __nv_bfloat16 *, const void *, const void *, const __nv_bfloat16 *,
                                      const float *, const float *, __nv_bfloat16 *, __nv_bfloat16 *, __nv_bfloat16 *,
                                      void *, void *, float *, void *, cudaStream_t);

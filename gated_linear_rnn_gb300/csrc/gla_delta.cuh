@@ -16,6 +16,7 @@ struct Shape {
     int nseq, T, H, Hk, dk, dv;
     int gate_f32;
     const int32_t *cu;
+    int2 *rows;  // packed: first row and number of rows of each sequence, which the first kernel of a call writes
     __host__ __device__ int group() const { return H / Hk; }
 };
 
@@ -24,35 +25,100 @@ __host__ inline long long total_rows(const Shape &s) { return s.cu ? (long long)
 // Chunks of C tokens restart at every sequence start.  Chunk c of sequence s has the slot
 // start_s / C + s + c; slots of different chunks differ, and all are below slots(rows, nseq, C).
 __host__ inline long long chunk_slots(long long rows, int nseq, int C) { return rows / C + nseq + 1; }
+__host__ inline size_t rows_bytes(const Shape &s) { return s.cu ? ((size_t)s.nseq * sizeof(int2) + 255) / 256 * 256 : 0; }
+
+// ---- packed batches: offsets as they come ------------------------------------------------------------------------
+//
+// A batch is in order where its offsets lie in 0 .. T and never fall.  Elsewhere the sequences that have such an offset
+// are bad, and so is one that starts before the end of an earlier one, whose rows and slots it would share; all others
+// are what they are alone.  A call's first kernel looks at the offsets and leaves the rows of every sequence to the
+// others: a bad one has none, at the end of those before it, so that the starts rise and can be bisected.
+
+// By a whole warp.
+__device__ __forceinline__ bool offsets_in_order(const Shape &p) {
+    bool ok = true;
+    if (p.cu != nullptr)
+        for (unsigned i = threadIdx.x & 31; i < (unsigned)p.nseq; i += 32) {
+            const int32_t a = __ldg(p.cu + i), b = __ldg(p.cu + i + 1);
+            ok = ok && a >= 0 && a <= b && b <= p.T;
+        }
+    return __all_sync(0xffffffffu, ok);
+}
+
+// The rows of sequence s; false for a bad one.
+__device__ __forceinline__ bool checked_rows(const Shape &p, bool in_order, int s, SeqRange &r) {
+    bool good = seq_range(s, p.T, p.cu, r);
+    if (!in_order) {
+        int64_t end = 0;  // of the sequences before it
+        for (int j = 0; j < s; ++j) {
+            SeqRange o;
+            if (seq_range(j, p.T, p.cu, o)) end = max(end, o.start + o.len);
+        }
+        if (r.start < end) good = false;
+        if (!good) {
+            r.start = end;
+            r.len = 0;
+        }
+    }
+    return good;
+}
+
+// ---- sequences and chunks ------------------------------------------------------------------------------------------
+
+__device__ __forceinline__ SeqRange rows_of(const Shape &p, int s) {
+    if (p.cu == nullptr) return {(int64_t)s * p.T, p.T};
+    const int2 t = __ldg(p.rows + s);
+    return {t.x, t.y};
+}
+
+// The largest s with start_s / C + s <= slot, whose chunk of C tokens it is if it is any sequence's.  Slots and rows are
+// below 2^31 (the entry points see to it).
+template <class F>
+__device__ __forceinline__ int bisect_slots(const Shape &p, int slot, int C, F packed_start) {
+    int lo = 0, hi = p.nseq - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        const int start = p.cu == nullptr ? mid * p.T : packed_start(mid);
+        if (start / C + mid <= slot) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
 
 struct ChunkAt {
     int64_t row;   // first row of the chunk
     int len;       // its tokens, 1 .. C
-    int seq;
-    bool first, last;  // first / last chunk of its sequence
 };
-
-// The chunk that owns a slot; false for slots that no chunk has (and for sequences with bad offsets).  Slots and
-// rows are below 2^31 (the entry points see to it).
+// Chunk of sequence s in this slot; false if it has none there.
 template <int C>
-__device__ __forceinline__ bool chunk_of_slot(int slot, const Shape &p, ChunkAt &at) {
-    int lo = 0, hi = p.nseq - 1;  // the largest s with start_s / C + s <= slot
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        const int start = p.cu == nullptr ? mid * p.T : __ldg(p.cu + mid);
-        if (start / C + mid <= slot) lo = mid; else hi = mid - 1;
-    }
-    SeqRange r;
-    if (!seq_range(lo, p.T, p.cu, r)) return false;
-    const int start = (int)r.start, len = (int)r.len;
-    const int c = slot - (start / C + lo);
+__device__ __forceinline__ bool chunk_at(int slot, int s, const SeqRange &r, ChunkAt &at) {
+    const int start = (int)r.start, len = (int)r.len, c = slot - (start / C + s);
     if (c < 0 || c >= (len + C - 1) / C) return false;
     at.row = start + c * C;
     at.len = min(len - c * C, C);
-    at.seq = lo;
-    at.first = c == 0;
-    at.last = c == (len + C - 1) / C - 1;
     return true;
+}
+
+// The chunk that owns a slot; false for slots that no chunk has.
+template <int C>
+__device__ __forceinline__ bool chunk_of_slot(int slot, const Shape &p, ChunkAt &at) {
+    const int s = bisect_slots(p, slot, C, [&](int i) { return __ldg(p.rows + i).x; });
+    return chunk_at<C>(slot, s, rows_of(p, s), at);
+}
+// The same by the offsets themselves.
+template <int C>
+__device__ __forceinline__ bool checked_chunk_of_slot(int slot, const Shape &p, bool in_order, ChunkAt &at) {
+    SeqRange r;
+    if (in_order) {
+        const int s = bisect_slots(p, slot, C, [&](int i) { return __ldg(p.cu + i); });
+        return seq_range(s, p.T, p.cu, r) && chunk_at<C>(slot, s, r, at);
+    }
+    int64_t end = 0;
+    for (int s = 0; s < p.nseq; ++s) {
+        if (!seq_range(s, p.T, p.cu, r)) continue;
+        if (r.start >= end && chunk_at<C>(slot, s, r, at)) return true;
+        end = max(end, r.start + r.len);
+    }
+    return false;
 }
 
 // g and beta come in f32 or in the type of q.

@@ -99,7 +99,6 @@ __device__ __forceinline__ void walk_again(const Shape &p, const Walk &w, unsign
                                            bf16 *__restrict__ resid, uint4 *__restrict__ images) {
     constexpr int kTile = kC * row_bytes<KT>();
     const Frame f(p, w, block, sm_raw);
-    if (f.bad && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
     if (f.warp >= w.groups * 4) {
         give_registers();
         fetch<KT, false, false, 1>(p, w, f, k, k, v, records, resid, nullptr);
@@ -179,7 +178,6 @@ __device__ __forceinline__ void walk_back(const Shape &p, const Walk &w, unsigne
                                           uint4 *__restrict__ images, float *__restrict__ dh0) {
     constexpr int kTile = kC * row_bytes<KT>();
     const Frame f(p, w, block, sm_raw);
-    if (f.bad && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
     if (f.warp >= w.groups * 4) {
         give_registers();
         fetch<KT, true, true, 2>(p, w, f, q, k, dout, records, ys, dv);
@@ -772,7 +770,7 @@ delta_heads_kernel(const float *__restrict__ dq_part, const float *__restrict__ 
 }
 
 struct Workspace {
-    size_t again, back, s_images, ds_images, resid, ys, dq_part, dk_part, total;
+    size_t rows, again, back, s_images, ds_images, resid, ys, dq_part, dk_part, total;
 };
 template <int KT> Workspace workspace_kt(const Shape &p) {
     const long long rows = total_rows(p);
@@ -782,6 +780,7 @@ template <int KT> Workspace workspace_kt(const Shape &p) {
     Workspace w{};
     size_t at = 0;
     const auto take = [&at](size_t n) { const size_t x = at; at += (n + 255) / 256 * 256; return x; };
+    w.rows = take(rows_bytes(p));
     w.again = take(units * sizeof(AgainRecord));
     w.back = take(units * sizeof(BwdRecord));
     w.s_images = take(image);
@@ -796,10 +795,11 @@ template <int KT> Workspace workspace_kt(const Shape &p) {
 }
 
 template <int KT>
-int bwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const void *g, const void *beta,
+int bwd_kt(Shape p, const bf16 *q, const bf16 *k, const bf16 *v, const void *g, const void *beta,
            const bf16 *dout, const float *h0, const float *dhT, bf16 *dq, bf16 *dk, bf16 *dv, void *dg, void *dbeta,
            float *dh0, char *ws, cudaStream_t st) {
     const Workspace at = workspace_kt<KT>(p);
+    p.rows = (int2 *)(ws + at.rows);
     const long long rows = total_rows(p), slots = chunk_slots(rows, p.nseq, kG);
     const long long chains = (long long)p.nseq * p.H;
     const int tiles = (p.dv + 15) / 16;

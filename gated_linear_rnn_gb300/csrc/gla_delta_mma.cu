@@ -106,8 +106,17 @@ delta_prep_kernel(Shape p, unsigned units, const bf16 *__restrict__ q, const bf1
     const unsigned unit = blockIdx.x * kPrepWarps + warp;  // slot * H + h
     if (unit >= units) return;
     const int h = (int)(unit % (unsigned)p.H), hk = h / p.group();
+    const bool in_order = offsets_in_order(p);
+    if (p.cu != nullptr && unit < (unsigned)p.nseq) {  // the rows of every sequence, for the kernels that follow
+        SeqRange r;
+        const bool good = checked_rows(p, in_order, (int)unit, r);
+        if (lane == 0) {
+            p.rows[unit] = make_int2((int)r.start, (int)r.len);
+            if (!good) record_status(GLA_ERR_DEVICE_ARG);
+        }
+    }
     ChunkAt at;
-    if (!chunk_of_slot<kC>((int)(unit / (unsigned)p.H), p, at)) return;
+    if (!checked_chunk_of_slot<kC>((int)(unit / (unsigned)p.H), p, in_order, at)) return;
     char *ks = sm_raw + warp * prep_warp_bytes<KT>(), *qs = ks + kC * row_bytes<KT>();
     float *L = reinterpret_cast<float *>(ks), *D = L + kC * kLd;  // in the rows' place once these are read
     const uint32_t ka = ptx::smem_u32(ks), qa = ptx::smem_u32(qs);
@@ -245,7 +254,6 @@ delta_fwd_kernel(Shape p, Walk w, FwdArgs a) {
     extern __shared__ __align__(128) char sm_raw[];
     constexpr int kRow = row_bytes<KT>(), kTile = kC * kRow, kV = (kSegment ? 1 : 2) * kTile;
     const Frame f(p, w, blockIdx.x, sm_raw);
-    if (f.bad && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
     if (!f.exists || (kSegment && f.last)) return;  // nothing starts where a sequence ends
     if (f.warp >= w.groups * 4) {
         give_registers();
@@ -433,8 +441,7 @@ delta_join_kernel(Shape p, int segment, const float *__restrict__ M, const float
     float *m = reinterpret_cast<float *>(sm_raw), *S = m + 2 * dk * dk;  // [2][dk][dk], [dk][32]
     const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, col = blockIdx.y * kJoinCols + c;
     const bool live = col < p.dv;
-    SeqRange r;
-    if (!seq_range(s, p.T, p.cu, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
+    const SeqRange r = rows_of(p, s);
     const int64_t slot0 = r.start / segment + s;
     const int n = (int)((r.len + segment - 1) / segment);
     const int64_t h_at = ((int64_t)s * p.H + h) * dk * p.dv + col;
@@ -526,12 +533,13 @@ int launch_prep(const Shape &p, const bf16 *q, const bf16 *k, const void *g, con
     return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
 }
 
+// The workspace: the sequences' rows, the records, and the segments' maps and states.
 size_t record_bytes(const Shape &p) {
     return ((size_t)chunk_slots(total_rows(p), p.nseq, kC) * p.H * sizeof(FwdRecord) + 255) / 256 * 256;
 }
 
 template <int KT>
-int fwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const void *g, const void *beta,
+int fwd_kt(Shape p, const bf16 *q, const bf16 *k, const bf16 *v, const void *g, const void *beta,
            const float *h0, bf16 *out, float *hT, char *ws, cudaStream_t st) {
     const Segments sg = plan_segments(p);
     const int tiles = (p.dv + 15) / 16;
@@ -542,6 +550,8 @@ int fwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
     if (!allow_smem<delta_fwd_kernel<KT, false>>() || !allow_smem<delta_fwd_kernel<KT, true>>() ||
         !allow_smem<delta_join_kernel<KT>>())
         return GLA_ERR_LAUNCH;
+    p.rows = (int2 *)ws;
+    ws += rows_bytes(p);
     FwdRecord *records = (FwdRecord *)ws;
     int rc = launch_prep<KT, false>(p, q, k, g, beta, records, nullptr, nullptr, st);
     if (rc != GLA_OK) return rc;
@@ -563,7 +573,7 @@ int fwd_kt(const Shape &p, const bf16 *q, const bf16 *k, const bf16 *v, const vo
 // bf16 with dk <= 128: a warp's share of the state fits its registers.
 bool mma_supported(int dk) { return dk <= 128; }
 
-size_t mma_fwd_workspace(const Shape &p) { return record_bytes(p) + plan_segments(p).total; }
+size_t mma_fwd_workspace(const Shape &p) { return rows_bytes(p) + record_bytes(p) + plan_segments(p).total; }
 
 int mma_fwd(const Shape &p, const void *q, const void *k, const void *v, const void *g, const void *beta,
             const float *h0, void *out, float *hT, void *ws, cudaStream_t st) {

@@ -170,12 +170,11 @@ template <int kBarrier, int kThreads> __device__ __forceinline__ bool any_of(boo
 constexpr int kMostRanked = 256;
 __device__ __forceinline__ int ranked_sequence(const Shape &p, int rank, volatile int *place) {
     for (int t = threadIdx.x; t < p.nseq; t += blockDim.x) {
-        SeqRange r, o;
-        seq_range(t, p.T, p.cu, r);
+        const int len = __ldg(p.rows + t).y;
         int before = 0;
         for (int i = 0; i < p.nseq; ++i) {
-            seq_range(i, p.T, p.cu, o);
-            before += o.len > r.len || (o.len == r.len && i < t);
+            const int other = __ldg(p.rows + i).y;
+            before += other > len || (other == len && i < t);
         }
         if (before == rank) *place = t;
     }
@@ -187,9 +186,8 @@ __device__ __forceinline__ int ranked_sequence(const Shape &p, int rank, volatil
 struct Frame {
     int lane, warp, s, h, hk, col0, width, nch;
     int walk;       // (sequence or segment's slot) * H + head
-    bool bad;       // the sequence's offsets are invalid
     bool exists;    // whether a segment has this slot
-    bool first, last;  // of its sequence's segments
+    bool last;      // of its sequence's segments
     SeqRange r;     // the rows that this block walks over
     int64_t slot0;  // slot of its first chunk
     uint32_t full, empty, ring;
@@ -204,28 +202,21 @@ struct Frame {
         hk = h / p.group();
         col0 = (int)(block % (unsigned)w.splits) * w.warps * 16;  // first column of the block
         width = min(w.warps * 16, p.dv - col0);                   // its columns of v, a multiple of 8 (none: <= 0)
-        exists = first = last = true;
+        exists = last = true;
         if (w.segment == 0) {
             if (p.cu != nullptr && p.nseq > 1 && p.nseq <= kMostRanked) {
                 s = ranked_sequence(p, s, reinterpret_cast<volatile int *>(sm + 16 * w.stages + 4));
                 walk = s * p.H + h;
             }
-            bad = !seq_range(s, p.T, p.cu, r);
+            r = rows_of(p, s);
             slot0 = r.start / kC + s;
         } else {
             // segment i of sequence s has the slot start_s / segment + s + i
             const int slot = s;
-            int lo = 0, hi = p.nseq - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                const int start = p.cu == nullptr ? mid * p.T : __ldg(p.cu + mid);
-                if (start / w.segment + mid <= slot) lo = mid; else hi = mid - 1;
-            }
-            s = lo;
-            bad = !seq_range(s, p.T, p.cu, r);
+            s = bisect_slots(p, slot, w.segment, [&](int i) { return __ldg(p.rows + i).x; });
+            r = rows_of(p, s);
             const int i = slot - ((int)r.start / w.segment + s);
-            exists = i >= 0 && (int64_t)i * w.segment < r.len;  // an empty sequence has none: delta_join_kernel's
-            first = i == 0;
+            exists = i >= 0 && (int64_t)i * w.segment < r.len;  // a sequence without rows has none: delta_join_kernel's
             last = (int64_t)(i + 1) * w.segment >= r.len;
             slot0 = r.start / kC + s + (int64_t)i * (w.segment / kC);
             r.start += (int64_t)i * w.segment;

@@ -470,8 +470,9 @@ GLA_API long long gla_delta_workspace_bytes(int op, int B, int T, int H, int Hk,
  *   q, k        [B, T, Hk, dk];  v, out [B, T, H, dv] (out written);  g, beta [B, T, H]
  *   h0, hT      [B, H, dk, dv] f32: initial state or NULL (zeros); final state, written, or NULL to skip
  *   cu_seqlens  NULL, or a DEVICE int32 [B+1] of offsets into packed [1, T, ...] tensors, as gla_chunk_fwd
- *               (an empty sequence gets hT = h0; a sequence with bad offsets is skipped and
- *               GLA_ERR_DEVICE_ARG recorded); T = 0 (packed) leaves only empty sequences
+ *               (an empty sequence gets hT = h0).  A sequence with offsets outside 0 .. T, with falling ones, or that
+ *               starts before the end of an earlier one is taken as empty and GLA_ERR_DEVICE_ARG recorded; the
+ *               others are what they are without it.  T = 0 (packed) leaves only empty sequences
  *   ws, ws_bytes  workspace of at least gla_delta_workspace_bytes(GLA_OP_FORWARD, ...) bytes (else
  *               GLA_ERR_ARG); NULL where that is 0
  * bf16 out is rounded once; hT comes from f32 sums over unrounded products (f32 accuracy) in both types.

@@ -68,7 +68,6 @@ def check(cu, T, H, Hk, dk, dv, dtype, backward=True):
     x = inputs(T, n, H, Hk, dk, dv, dtype)
     rows, states = run(x, cu, T, n, H, Hk, dk, dv, dtype, backward)
     assert gla.STATUS[gla.gla_last_device_status()] == "GLA_ERR_DEVICE_ARG"
-    left = torch.ones(T, dtype=torch.bool)
     for s, a, b in good(cu, T):
         # the sequence as the only one with tokens of a batch of the same sizes, so that the same kernels run
         one = [0] * (s + 1) + [b - a] * (n - s)
@@ -80,9 +79,6 @@ def check(cu, T, H, Hk, dk, dv, dtype, backward=True):
             assert torch.equal(t[:, a:b], want_rows[name][:, :b - a]), (name, s)
         for name, t in states.items():
             assert torch.equal(t[s], want_states[name][s]), (name, s)
-        left[a:b] = False
-    for name, t in rows.items():
-        assert bool((t[0, left.cuda()] == 7.0).all()), name  # no row of a skipped sequence is written
 
 
 BAD = {
