@@ -347,7 +347,7 @@ delta_rec_fwd_kernel(Shape p, const T *__restrict__ q, const T *__restrict__ k, 
     SeqRange r;
     if (!checked_rows(p, offsets_in_order(p), ln.s, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
     if (p.rows != nullptr && ln.h == 0 && blockIdx.y == 0 && threadIdx.x == 0)
-        p.rows[ln.s] = make_int2((int)r.start, (int)r.len);
+        p.rows[ln.s] = make_int2((int)r.start, (int)r.len);  // no kernel after this one asks for the span
     Pair S[kRpl / 2];
     ln.load(S, h0, p);
     const int64_t slot0 = r.start / 64 + ln.s;

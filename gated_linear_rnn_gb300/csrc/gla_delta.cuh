@@ -16,7 +16,9 @@ struct Shape {
     int nseq, T, H, Hk, dk, dv;
     int gate_f32;
     const int32_t *cu;
-    int2 *rows;  // packed: first row and number of rows of each sequence, which the first kernel of a call writes
+    // packed, [nseq + 1], which the first kernel of a call writes: the first row and the number of rows of each sequence,
+    // then the rows that all of them have together, or a negative number of them where the batch is not in order
+    int2 *rows;
     __host__ __device__ int group() const { return H / Hk; }
 };
 
@@ -25,7 +27,7 @@ __host__ inline long long total_rows(const Shape &s) { return s.cu ? (long long)
 // Chunks of C tokens restart at every sequence start.  Chunk c of sequence s has the slot
 // start_s / C + s + c; slots of different chunks differ, and all are below slots(rows, nseq, C).
 __host__ inline long long chunk_slots(long long rows, int nseq, int C) { return rows / C + nseq + 1; }
-__host__ inline size_t rows_bytes(const Shape &s) { return s.cu ? ((size_t)s.nseq * sizeof(int2) + 255) / 256 * 256 : 0; }
+__host__ inline size_t rows_bytes(const Shape &s) { return s.cu ? (((size_t)s.nseq + 1) * sizeof(int2) + 255) / 256 * 256 : 0; }
 
 // ---- packed batches: offsets as they come ------------------------------------------------------------------------
 //
@@ -63,6 +65,11 @@ __device__ __forceinline__ bool checked_rows(const Shape &p, bool in_order, int 
     return good;
 }
 
+__device__ __forceinline__ int2 span_of(const Shape &p, bool in_order) {
+    const int first = __ldg(p.cu);
+    return in_order ? make_int2(first, __ldg(p.cu + p.nseq) - first) : make_int2(0, -1);
+}
+
 // ---- sequences and chunks ------------------------------------------------------------------------------------------
 
 __device__ __forceinline__ SeqRange rows_of(const Shape &p, int s) {
@@ -82,6 +89,23 @@ __device__ __forceinline__ int bisect_slots(const Shape &p, int slot, int C, F p
         if (start / C + mid <= slot) lo = mid; else hi = mid - 1;
     }
     return lo;
+}
+
+// Whether element i of rows of `width` elements lies in any sequence's row: where the batch is in order, all rows from
+// the first sequence's to the last one's are; else the last that starts at or before a row is the only one that can have
+// it.
+__device__ __forceinline__ bool in_some_sequence(const Shape &p, int64_t i, int64_t width) {
+    if (p.cu == nullptr) return true;
+    const int2 span = __ldg(p.rows + p.nseq);
+    if (span.y >= 0) return i >= span.x * width && i < (span.x + (int64_t)span.y) * width;
+    const int row = (int)(i / width);
+    int lo = 0, hi = p.nseq - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(p.rows + mid).x <= row) lo = mid; else hi = mid - 1;
+    }
+    const int2 t = __ldg(p.rows + lo);
+    return row >= t.x && row - t.x < t.y;
 }
 
 struct ChunkAt {

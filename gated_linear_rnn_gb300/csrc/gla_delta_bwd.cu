@@ -752,25 +752,29 @@ delta_grad_kernel(Shape p, GradArgs a) {
     }
 }
 
-// dq and dk of a key head: the sum over its value heads' parts, four elements a thread, in a fixed order.
+// dq and dk of a key head: the sum over its value heads' parts, four elements a thread, in a fixed order.  Rows of a
+// packed batch that are no sequence's have no parts, and stay as they are.
 __global__ void __launch_bounds__(256)
-delta_heads_kernel(const float *__restrict__ dq_part, const float *__restrict__ dk_part, bf16 *__restrict__ dq,
-                   bf16 *__restrict__ dk_out, int64_t n, int dk, int group) {
+delta_heads_kernel(Shape p, const float *__restrict__ dq_part, const float *__restrict__ dk_part, bf16 *__restrict__ dq,
+                   bf16 *__restrict__ dk_out, int64_t n) {
+    const int dk = p.dk, group = p.group();
     const float *part = blockIdx.y ? dk_part : dq_part;
     bf16 *out = blockIdx.y ? dk_out : dq;
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;  // element of [rows, Hk, dk]
     if (i >= n) return;
+    const bool has = in_some_sequence(p, i, (int64_t)p.Hk * dk);
     const float *from = part + (i / dk) * group * dk + i % dk;
     float4 s = *reinterpret_cast<const float4 *>(from);
     for (int m = 1; m < group; ++m) {
         const float4 x = *reinterpret_cast<const float4 *>(from + (int64_t)m * dk);
         s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
     }
+    if (!has) return;  // asked for after the loads, which the answer does not hold up
     *reinterpret_cast<uint2 *>(out + i) = make_uint2(pack(s.x, s.y), pack(s.z, s.w));
 }
 
 struct Workspace {
-    size_t rows, again, back, s_images, ds_images, resid, ys, dq_part, dk_part, total;
+    size_t again, back, s_images, ds_images, resid, ys, dq_part, dk_part, rows, total;
 };
 template <int KT> Workspace workspace_kt(const Shape &p) {
     const long long rows = total_rows(p);
@@ -780,7 +784,6 @@ template <int KT> Workspace workspace_kt(const Shape &p) {
     Workspace w{};
     size_t at = 0;
     const auto take = [&at](size_t n) { const size_t x = at; at += (n + 255) / 256 * 256; return x; };
-    w.rows = take(rows_bytes(p));
     w.again = take(units * sizeof(AgainRecord));
     w.back = take(units * sizeof(BwdRecord));
     w.s_images = take(image);
@@ -790,6 +793,7 @@ template <int KT> Workspace workspace_kt(const Shape &p) {
     const size_t parts = p.H == p.Hk ? 0 : (size_t)rows * p.H * p.dk * sizeof(float);
     w.dq_part = take(parts);
     w.dk_part = take(parts);
+    w.rows = take(rows_bytes(p));
     w.total = at;
     return w;
 }
@@ -830,7 +834,7 @@ int bwd_kt(Shape p, const bf16 *q, const bf16 *k, const bf16 *v, const void *g, 
         if (!single) {
             const int64_t n = (int64_t)rows * p.Hk * p.dk;
             const dim3 grid((unsigned)((n / 4 + 255) / 256), 2);
-            delta_heads_kernel<<<grid, 256, 0, st>>>(a.dq_part, a.dk_part, dq, dk, n, p.dk, p.group());
+            delta_heads_kernel<<<grid, 256, 0, st>>>(p, a.dq_part, a.dk_part, dq, dk, n);
             count_launches(1);
         }
     }

@@ -112,6 +112,7 @@ delta_prep_kernel(Shape p, unsigned units, const bf16 *__restrict__ q, const bf1
         const bool good = checked_rows(p, in_order, (int)unit, r);
         if (lane == 0) {
             p.rows[unit] = make_int2((int)r.start, (int)r.len);
+            if (unit == 0) p.rows[p.nseq] = span_of(p, in_order);
             if (!good) record_status(GLA_ERR_DEVICE_ARG);
         }
     }

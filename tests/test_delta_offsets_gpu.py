@@ -68,6 +68,7 @@ def check(cu, T, H, Hk, dk, dv, dtype, backward=True):
     x = inputs(T, n, H, Hk, dk, dv, dtype)
     rows, states = run(x, cu, T, n, H, Hk, dk, dv, dtype, backward)
     assert gla.STATUS[gla.gla_last_device_status()] == "GLA_ERR_DEVICE_ARG"
+    left = torch.ones(T, dtype=torch.bool)
     for s, a, b in good(cu, T):
         # the sequence as the only one with tokens of a batch of the same sizes, so that the same kernels run
         one = [0] * (s + 1) + [b - a] * (n - s)
@@ -79,6 +80,9 @@ def check(cu, T, H, Hk, dk, dv, dtype, backward=True):
             assert torch.equal(t[:, a:b], want_rows[name][:, :b - a]), (name, s)
         for name, t in states.items():
             assert torch.equal(t[s], want_states[name][s]), (name, s)
+        left[a:b] = False
+    for name, t in rows.items():
+        assert bool((t[0, left.cuda()] == 7.0).all()), name  # no row of a skipped sequence is written
 
 
 BAD = {
@@ -139,3 +143,16 @@ def check_many(cu, T, dtype):
     bar = 1e-2 if dtype == torch.bfloat16 else 5e-5  # as for the other results of this operator
     assert float((rows["out"][0][a].double() - o).abs().max()) <= bar * float(o.abs().max())
     assert float((states["hT"][s].double() - S).abs().max()) <= 5e-5 * float(S.abs().max())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("H,Hk", [(2, 2), (4, 2)])
+def test_rows_of_no_sequence_are_left_as_they_are(dtype, H, Hk):
+    """Rows ahead of the first sequence and behind the last: offsets in order, and nothing to report."""
+    T, cu, sizes = 200, [7, 60, 60, 135], (H, Hk, 64, 40, dtype)
+    x = inputs(T, 3, H, Hk, 64, 40, dtype)
+    rows, _ = run(x, cu, T, 3, *sizes, True)
+    assert gla.gla_last_device_status() == 0
+    for name, t in rows.items():
+        assert bool((t[0, :7] == 7.0).all()) and bool((t[0, 135:] == 7.0).all()), name
+        assert bool(t[0, 7:135].isfinite().all()), name
