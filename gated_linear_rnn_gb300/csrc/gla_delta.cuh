@@ -19,6 +19,10 @@ struct Shape {
     // packed, [nseq + 1], which the first kernel of a call writes: the first row and the number of rows of each sequence,
     // then the rows that all of them have together, or a negative number of them where the batch is not in order
     int2 *rows;
+    // [nseq], likewise, what the walks over chains take in turn: first row, number of rows, sequence; the longest first
+    // where `ranked`, else as the batch has them
+    int4 *walks;
+    int ranked;
     __host__ __device__ int group() const { return H / Hk; }
 };
 
@@ -27,7 +31,9 @@ __host__ inline long long total_rows(const Shape &s) { return s.cu ? (long long)
 // Chunks of C tokens restart at every sequence start.  Chunk c of sequence s has the slot
 // start_s / C + s + c; slots of different chunks differ, and all are below slots(rows, nseq, C).
 __host__ inline long long chunk_slots(long long rows, int nseq, int C) { return rows / C + nseq + 1; }
-__host__ inline size_t rows_bytes(const Shape &s) { return s.cu ? (((size_t)s.nseq + 1) * sizeof(int2) + 255) / 256 * 256 : 0; }
+__host__ inline size_t rows_bytes(const Shape &s) {
+    return s.cu ? ((size_t)s.nseq * sizeof(int4) + ((size_t)s.nseq + 1) * sizeof(int2) + 255) / 256 * 256 : 0;
+}
 
 // ---- packed batches: offsets as they come ------------------------------------------------------------------------
 //
@@ -93,10 +99,8 @@ __device__ __forceinline__ int bisect_slots(const Shape &p, int slot, int C, F p
 
 // Whether element i of rows of `width` elements lies in any sequence's row: where the batch is in order, all rows from
 // the first sequence's to the last one's are; else the last that starts at or before a row is the only one that can have
-// it.
-__device__ __forceinline__ bool in_some_sequence(const Shape &p, int64_t i, int64_t width) {
-    if (p.cu == nullptr) return true;
-    const int2 span = __ldg(p.rows + p.nseq);
+// it.  span: rows[nseq], which the caller may load ahead.
+__device__ __forceinline__ bool in_some_sequence(const Shape &p, int2 span, int64_t i, int64_t width) {
     if (span.y >= 0) return i >= span.x * width && i < (span.x + (int64_t)span.y) * width;
     const int row = (int)(i / width);
     int lo = 0, hi = p.nseq - 1;

@@ -762,14 +762,14 @@ delta_heads_kernel(Shape p, const float *__restrict__ dq_part, const float *__re
     bf16 *out = blockIdx.y ? dk_out : dq;
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;  // element of [rows, Hk, dk]
     if (i >= n) return;
-    const bool has = in_some_sequence(p, i, (int64_t)p.Hk * dk);
+    const int2 span = __ldg(p.cu != nullptr ? p.rows + p.nseq : reinterpret_cast<const int2 *>(part));  // on its way with the parts
     const float *from = part + (i / dk) * group * dk + i % dk;
     float4 s = *reinterpret_cast<const float4 *>(from);
     for (int m = 1; m < group; ++m) {
         const float4 x = *reinterpret_cast<const float4 *>(from + (int64_t)m * dk);
         s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
     }
-    if (!has) return;  // asked for after the loads, which the answer does not hold up
+    if (p.cu != nullptr && !in_some_sequence(p, span, i, (int64_t)p.Hk * dk)) return;
     *reinterpret_cast<uint2 *>(out + i) = make_uint2(pack(s.x, s.y), pack(s.z, s.w));
 }
 
@@ -803,7 +803,6 @@ int bwd_kt(Shape p, const bf16 *q, const bf16 *k, const bf16 *v, const void *g, 
            const bf16 *dout, const float *h0, const float *dhT, bf16 *dq, bf16 *dk, bf16 *dv, void *dg, void *dbeta,
            float *dh0, char *ws, cudaStream_t st) {
     const Workspace at = workspace_kt<KT>(p);
-    p.rows = (int2 *)(ws + at.rows);
     const long long rows = total_rows(p), slots = chunk_slots(rows, p.nseq, kG);
     const long long chains = (long long)p.nseq * p.H;
     const int tiles = (p.dv + 15) / 16;
@@ -812,6 +811,7 @@ int bwd_kt(Shape p, const bf16 *q, const bf16 *k, const bf16 *v, const void *g, 
     const int grad_bytes = GradPlan<KT>::kTotal;
     const long long blocks = chains * wa.splits;
     if (2 * blocks > 0x7fffffffLL || slots * p.H > 0x7fffffffLL) return GLA_ERR_UNSUPPORTED;
+    place_rows(p, ws + at.rows, 2 * blocks);
     const int walks_bytes = max(walk_bytes(wa), walk_bytes(wb));
     if (!allow_smem<delta_walks_kernel<KT>>() || !allow_smem<delta_grad_kernel<KT>>())
         return GLA_ERR_LAUNCH;

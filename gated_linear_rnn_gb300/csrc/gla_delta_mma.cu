@@ -107,12 +107,16 @@ delta_prep_kernel(Shape p, unsigned units, const bf16 *__restrict__ q, const bf1
     if (unit >= units) return;
     const int h = (int)(unit % (unsigned)p.H), hk = h / p.group();
     const bool in_order = offsets_in_order(p);
-    if (p.cu != nullptr && unit < (unsigned)p.nseq) {  // the rows of every sequence, for the kernels that follow
+    // the rows of every sequence, for the kernels that follow, by the last units: they have the fewest chunks
+    const unsigned seq = units - 1 - unit;
+    if (p.cu != nullptr && seq < (unsigned)p.nseq) {
         SeqRange r;
-        const bool good = checked_rows(p, in_order, (int)unit, r);
+        const bool good = checked_rows(p, in_order, (int)seq, r);
+        const int turn = p.ranked ? rank_of(p, (int)seq, lane) : (int)seq;
         if (lane == 0) {
-            p.rows[unit] = make_int2((int)r.start, (int)r.len);
-            if (unit == 0) p.rows[p.nseq] = span_of(p, in_order);
+            p.rows[seq] = make_int2((int)r.start, (int)r.len);
+            p.walks[turn] = make_int4((int)r.start, (int)r.len, (int)seq, 0);
+            if (seq == 0) p.rows[p.nseq] = span_of(p, in_order);
             if (!good) record_status(GLA_ERR_DEVICE_ARG);
         }
     }
@@ -551,7 +555,7 @@ int fwd_kt(Shape p, const bf16 *q, const bf16 *k, const bf16 *v, const void *g, 
     if (!allow_smem<delta_fwd_kernel<KT, false>>() || !allow_smem<delta_fwd_kernel<KT, true>>() ||
         !allow_smem<delta_join_kernel<KT>>())
         return GLA_ERR_LAUNCH;
-    p.rows = (int2 *)ws;
+    place_rows(p, ws, sg.tokens ? 0 : walks * w.splits);
     ws += rows_bytes(p);
     FwdRecord *records = (FwdRecord *)ws;
     int rc = launch_prep<KT, false>(p, q, k, g, beta, records, nullptr, nullptr, st);

@@ -163,23 +163,29 @@ template <int kBarrier, int kThreads> __device__ __forceinline__ bool any_of(boo
     return any != 0;
 }
 
-// The sequence of a packed batch that is the rank-th longest (the first of equals first), by all threads of a block.
-// Blocks start in their order, so the longest chains start first and the last ones to end are short: 301 us against
-// 353 in the batch's own order at 24 sequences of up to 2,048 tokens (16 heads, 96/192).
-// Up to 256 sequences, since each thread ranks one by looking at all lengths; more are many waves of blocks anyway.
-constexpr int kMostRanked = 256;
-__device__ __forceinline__ int ranked_sequence(const Shape &p, int rank, volatile int *place) {
-    for (int t = threadIdx.x; t < p.nseq; t += blockDim.x) {
-        const int len = __ldg(p.rows + t).y;
-        int before = 0;
-        for (int i = 0; i < p.nseq; ++i) {
-            const int other = __ldg(p.rows + i).y;
-            before += other > len || (other == len && i < t);
-        }
-        if (before == rank) *place = t;
+// The walks over a packed batch start in the order of their lengths, the longest first, so that the last ones to end are
+// short, where their blocks run in two to eight waves.  The preparation finds each sequence's rank, by a warp that looks
+// at all lengths.  16 heads of 96/192, in this order and in the batch's own: 24 sequences of 0..256 tokens 52 and 58 us,
+// of 0..1,024 148 and 160, 64 of 0..1,024 381 and 416; of 64 equal lengths 58 and 56.  In one wave all start at once, and
+// in many the order is nothing but its cost: 8 of 0..1,024 77 and 75 us, 128 of 0..256 262 and 262, 256 of them 513 and 498.
+constexpr int kRankedWaves = 8;
+// rows_bytes at `at`; blocks: of the launch whose blocks walk over whole chains, or 0
+inline void place_rows(Shape &p, char *at, long long blocks) {
+    const long long sms = device_info().sm_count;
+    p.walks = reinterpret_cast<int4 *>(at);
+    p.rows = reinterpret_cast<int2 *>(p.walks + p.nseq);
+    p.ranked = blocks > sms && blocks <= kRankedWaves * sms;
+}
+// How many sequences start before s: the longer ones, and of equals the first.  (A bad one's length is only an order here.)
+__device__ __forceinline__ int rank_of(const Shape &p, int s, int lane) {
+    SeqRange own, r;
+    seq_range(s, p.T, p.cu, own);
+    int before = 0;
+    for (int i = lane; i < p.nseq; i += 32) {
+        seq_range(i, p.T, p.cu, r);
+        before += r.len > own.len || (r.len == own.len && i < s);
     }
-    __syncthreads();
-    return *place;
+    return __reduce_add_sync(0xffffffffu, before);
 }
 
 // Who a block and a thread are, and the shared memory: barriers, the stages (K | Q | V | record | a second output).
@@ -204,11 +210,14 @@ struct Frame {
         width = min(w.warps * 16, p.dv - col0);                   // its columns of v, a multiple of 8 (none: <= 0)
         exists = last = true;
         if (w.segment == 0) {
-            if (p.cu != nullptr && p.nseq > 1 && p.nseq <= kMostRanked) {
-                s = ranked_sequence(p, s, reinterpret_cast<volatile int *>(sm + 16 * w.stages + 4));
+            if (p.cu != nullptr) {
+                const int4 t = __ldg(p.walks + s);
+                r = {t.x, t.y};
+                s = t.z;
                 walk = s * p.H + h;
+            } else {
+                r = {(int64_t)s * p.T, p.T};
             }
-            r = rows_of(p, s);
             slot0 = r.start / kC + s;
         } else {
             // segment i of sequence s has the slot start_s / segment + s + i
