@@ -494,20 +494,32 @@ delta_join_kernel(Shape p, int segment, const float *__restrict__ M, const float
     }
 }
 
-// Tokens per segment, or 0 for whole chains.  A walk is one product after another, so few chains leave most of the
-// GPU idle: B1 T32768 H16 dk96 dv192 took 1,416 us as 16 chains.  Segments cost their map first (dk more columns than
-// dv, without the output: some 1.2 walks), which pays off from about six of them on; so chains are cut where a
-// sixth of the GPU's column tiles (12 to an SM) would do for all of them, into as many segments as fill it, none
-// shorter than 256 tokens, where that makes four of a sequence (of a packed batch, whose lengths only the device
-// knows, four in all: a sequence of one segment costs nothing more).
+// Tokens per segment, or 0 for whole chains.  A walk is one product after another, so few chains leave most of the GPU
+// idle: B1 T32768 H16 dk96 dv192 takes 1,416 us as 16 chains and 867 cut.  Chains are cut into as many segments as fill
+// the GPU (12 column tiles to an SM), none shorter than 256 tokens, where that is the cheaper way.  Counted in steps of a
+// walk (a chunk of a chain, some 0.16 us times KT), with n segments to a sequence,
+//     saved  the steps of n - 1 segments
+//     paid   0.375 for each chunk that has to give a map, head and column tile of it (dv / 16 + KT) per SM, 4 for each
+//            segment in the join's row (3 where dk <= 64), and 6 for two more launches
+// At 248 sizes with both ways measured (1 to 32 heads of 24/40 to 128/256, 1 to 4 sequences of 256 to 32,768 tokens) this
+// loses 0.4% against the better one, 11% at most.  Whole and cut, us: 4 x 2,048, 8 heads of 128/128 102 and 179; 1 x 4,096, 16
+// heads of 96/192 146 and 163; 1 x 8,192 288 and 266; 1 x 2,048, 4 heads of 64/64 59 and 44.
+// Of several packed sequences only the device knows the lengths, and the longest one decides: 1 of 5,200 and 5 of 100
+// tokens, 6 heads of 24/40, 122 whole and 46 cut; 6 of 1,300, 24 heads of 32/32, 56 and 88.  They are cut where a sixth
+// of the GPU's tiles would do for all chains, and where there are four segments in all; over 60 such batches that loses
+// 5% on equal lengths and 1% on uneven ones.
 int segment_tokens(const Shape &p) {
-    const long long rows = total_rows(p), tiles = (p.dv + 15) / 16, chains = (long long)p.nseq * p.H;
-    const long long room = (long long)device_info().sm_count * kMaxWarps;
-    if (rows == 0 || chains * tiles * 6 > room) return 0;
-    const long long segments = max(1LL, room / (p.H * tiles));
-    const long long tokens = max(256LL, (rows + segments - 1) / segments);
-    if (rows < 4 * tokens * (p.cu ? 1 : p.nseq)) return 0;
-    return (int)((tokens + kC - 1) / kC * kC);
+    const long long rows = total_rows(p), tiles = (p.dv + 15) / 16, sms = device_info().sm_count;
+    if (rows == 0 || sms == 0) return 0;
+    const long long segments = max(1LL, sms * kMaxWarps / (p.H * tiles));
+    const long long tokens = (max(256LL, (rows + segments - 1) / segments) + kC - 1) / kC * kC;
+    if (p.cu && p.nseq > 1)
+        return (long long)p.nseq * p.H * tiles * 6 <= sms * kMaxWarps && rows >= 4 * tokens ? (int)tokens : 0;
+    if (p.T <= tokens) return 0;
+    const int kt = p.dk <= 32 ? 2 : p.dk <= 64 ? 4 : p.dk <= 96 ? 6 : 8;
+    const double n = (double)p.T / (double)tokens, kept = 1.0 - 1.0 / n;
+    const double maps = 0.375 * (double)rows / kC * kept * (double)(p.H * (tiles + kt)) / (double)sms;
+    return (double)p.T / kC * kept > maps + (p.dk <= 64 ? 3.0 : 4.0) * n + 6.0 ? (int)tokens : 0;
 }
 struct Segments {
     int tokens;
