@@ -189,8 +189,8 @@ int check_delta_sizes(int B, int T, int H, int Hk, int dk, int dv, int dtype, in
     if (B <= 0 || T < 0 || H <= 0 || Hk <= 0 || dk <= 0 || dv <= 0 || H % Hk) return GLA_ERR_ARG;
     if (dk < 16 || dk > 256 || dv < 16 || dv > 512 || dk % 8 || dv % 8) return GLA_ERR_UNSUPPORTED;
     const long long rows = packed ? (long long)T : (long long)B * T;
-    // block indexes (chains, and chunks of 32 tokens of all heads) and row offsets of packed batches are 32-bit
-    if (rows > 0x7fffffffLL || (long long)B * H > 0x7fffffffLL || (rows / 32 + B + 1) * H > 0x7fffffffLL)
+    // block indexes (chains, and chunks of 32 tokens of all heads) and rows, up to the end of a chunk, are 32-bit
+    if (rows > 0x7fffff00LL || (long long)B * H > 0x7fffffffLL || (rows / 32 + B + 1) * H > 0x7fffffffLL)
         return GLA_ERR_UNSUPPORTED;
     return GLA_OK;
 }

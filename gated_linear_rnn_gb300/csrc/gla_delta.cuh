@@ -44,12 +44,12 @@ __host__ inline size_t rows_bytes(const Shape &s) {
 
 // By a whole warp.
 __device__ __forceinline__ bool offsets_in_order(const Shape &p) {
+    if (p.cu == nullptr) return true;
     bool ok = true;
-    if (p.cu != nullptr)
-        for (unsigned i = threadIdx.x & 31; i < (unsigned)p.nseq; i += 32) {
-            const int32_t a = __ldg(p.cu + i), b = __ldg(p.cu + i + 1);
-            ok = ok && a >= 0 && a <= b && b <= p.T;
-        }
+    for (unsigned i = threadIdx.x & 31; i < (unsigned)p.nseq; i += 32) {
+        const int32_t a = __ldg(p.cu + i), b = __ldg(p.cu + i + 1);
+        ok = ok && a >= 0 && a <= b && b <= p.T;
+    }
     return __all_sync(0xffffffffu, ok);
 }
 

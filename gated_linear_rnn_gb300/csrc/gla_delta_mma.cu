@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 delta_fwd_kernel(Shape p, Walk w, FwdArgs a) {
     extern __shared__ __align__(128) char sm_raw[];
     constexpr int kRow = row_bytes<KT>(), kTile = kC * kRow, kV = (kSegment ? 1 : 2) * kTile;
-    const Frame f(p, w, blockIdx.x, sm_raw);
+    const Frame f(p, w, blockIdx.x, sm_raw, kSegment || w.segment != 0);
     if (!f.exists || (kSegment && f.last)) return;  // nothing starts where a sequence ends
     if (f.warp >= w.groups * 4) {
         give_registers();
