@@ -5,6 +5,8 @@
 //     u = beta (v - a k S),   S <- a S + k^T u,   o = q S.
 // Every column of S (one of the dv) obeys this map by itself: only k, q, a and beta are shared.  So the
 // columns of a chain are split over threads, warps and blocks without any exchange between them.
+#include <type_traits>
+
 #include "gla_delta.cuh"
 #include "gla_pairs.cuh"
 
@@ -656,14 +658,16 @@ int check_launch(int n) {
     return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
 }
 
-// rows of the state a lane holds: a quarter of dk, rounded up to what the kernels are built for
-#define GLA_BY_ROWS(dk, CALL)      \
-    do {                           \
-        if (dk <= 32) { CALL(8); } \
-        else if (dk <= 64) { CALL(16); } \
-        else if (dk <= 96) { CALL(24); } \
-        else if (dk <= 128) { CALL(32); } \
-        else { CALL(64); }         \
+// rows of the state a lane holds: a quarter of dk, rounded up to what the kernels are built for; bf16 comes here with dk
+// above 128 alone
+#define GLA_BY_ROWS(T, dk, CALL)                                     \
+    do {                                                             \
+        if constexpr (!std::is_same<T, float>::value) { CALL(64); }  \
+        else if (dk <= 32) { CALL(8); }                              \
+        else if (dk <= 64) { CALL(16); }                             \
+        else if (dk <= 96) { CALL(24); }                             \
+        else if (dk <= 128) { CALL(32); }                            \
+        else { CALL(64); }                                           \
     } while (0)
 
 // out null: the residuals and states instead
@@ -676,7 +680,7 @@ int rec_fwd(const Shape &p, const T *q, const T *k, const T *v, const void *g, c
         delta_rec_fwd_kernel<T, R, false><<<grid, 128, 0, st>>>(p, q, k, v, g, beta, h0, out, hT, resid, states);   \
     else                                                                                                           \
         delta_rec_fwd_kernel<T, R, true><<<grid, 128, 0, st>>>(p, q, k, v, g, beta, h0, out, hT, resid, states)
-    GLA_BY_ROWS(p.dk, GLA_CALL);
+    GLA_BY_ROWS(T, p.dk, GLA_CALL);
 #undef GLA_CALL
     return check_launch(1);
 }
@@ -709,7 +713,7 @@ int simt_bwd(Shape p, const T *q, const T *k, const T *v, const void *g, const v
     const dim3 grid((unsigned)((long long)p.nseq * p.H), (unsigned)((p.dv + kCols - 1) / kCols));
 #define GLA_CALL(R) \
     delta_rec_bwd_kernel<T, R><<<grid, 128, 0, st>>>(p, q, k, dout, g, beta, dhT, dv, ys, ds1, dh0)
-    GLA_BY_ROWS(p.dk, GLA_CALL);
+    GLA_BY_ROWS(T, p.dk, GLA_CALL);
 #undef GLA_CALL
     rc = check_launch(1);
     if (rc != GLA_OK || rows == 0) return rc;
