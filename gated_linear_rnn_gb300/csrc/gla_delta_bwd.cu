@@ -16,7 +16,7 @@
 // they add in squares: X and dU, which every residual and every Y are made of, keep their lo parts (six products of
 // 16 x 8 x 16 a chunk each), which takes dbeta, a product of both, from 4.7e-3 to 4e-3.
 //
-// Eight sequences of 2,048 tokens, 16 heads of 96/192: 552 us: preparation 55, both walks 225 (260 before the fetching
+// Eight sequences of 2,048 tokens, 16 heads of 96/192: 550 us: preparation 54, both walks 223 (260 before the fetching
 // warps gave registers to the computing ones), gradient kernel 269.  The walks run in one launch since neither fills
 // the GPU alone on a small batch; on a large one shared
 // memory's pipe (70% busy) and mma.sync's (54%) bound them.
@@ -306,7 +306,7 @@ delta_walks_kernel(Shape p, Walk again, Walk back, unsigned blocks, WalkArgs a) 
 // R^T, dO S0^T, R' K -> dq), Y's (Y R^T, Y S0^T, N K) and R's (R dS1^T, R'^T Q + N^T K); the last two meet in
 // shared memory -> dk.  A fourth warpgroup fetches ahead: K, Q and the decay products of the next unit, and
 // slabs of 64 columns (32 for dk > 96) of dO, Y, R and of both states through a ring.
-// On the layer's gradient (4,096 units of 64 x 96 x 192, 790 MB): 269 us, of which the slabs' products are about 115,
+// On the layer's gradient (4,096 units of 64 x 96 x 192, 790 MB): 266 us, of which the slabs' products are about 115,
 // T with R' and N 70 and the products inside the unit 50: the phases of a unit follow one another, and shared memory
 // carries every state element to four warps.  One block per unit with its states read from L2 between products
 // took 489 us, slabs of 32 columns 275, and the same unit with all products on tcgen05 (128 rows of TMEM, one thread

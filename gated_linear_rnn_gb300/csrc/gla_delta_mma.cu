@@ -16,27 +16,27 @@
 //     Y = S^T K^T,  X^T = V^T - Y diag(c),  R^T = X^T M^T,  O^T = S^T Q^T diag(c) + R^T P^T,
 //     S^T = c_31 S^T + (R^T diag(d beta)) K.
 // A step of a chain is three products long, without a barrier or a trip through memory between them; that, and
-// not the rate of the tensor cores, is what a walk over a long sequence is made of.  tcgen05 runs four times the
-// rate of mma.sync (1,020 multiply-adds a clock and SM, measured) but its accumulators would have to go through
-// the registers and back to shared memory, split in two, between any two of the products.
+// not the rate of the tensor cores, is what a walk over a long sequence is made of.  mma.sync runs at 1,020 multiply-adds
+// a clock and SM (measured), a quarter of tcgen05's rate.  A walk on tcgen05 could keep S^T, X^T and R^T as A operands in
+// TMEM, through the registers between any two products for their scaling and splitting; it has not been built.
 //
 // Precision: q, k and v are bf16 and so exact as operands.  S, X, M and R are f32 values; where a product with
 // them reaches the state, each is taken as two bf16 parts, hi + lo, whose sum holds 16 bits of it (2^-17 relative);
-// M X takes three products, the others two.  So hT has f32 accuracy.  O, itself rounded to bf16, takes the hi
-// parts alone.
+// M X takes three products, the others two.  hT is within 6e-6 of its norm, where f32 arithmetic alone would leave 2e-7.
+// O, itself rounded to bf16, takes the hi parts alone: 3e-3 of its norm, where its own rounding leaves 1.7e-3.
 //
 // A warpgroup of its own, four threads to a row, fetches the rows of K, Q and V by 16-byte asynchronous copies (zero
 // past a sequence's end, so a short chunk is computed like a whole one) and the chunk's M, P, c and d beta by one
 // bulk copy into a ring of stages; a row's stride is an odd number of 16-byte units, so that ldmatrix meets no bank
 // twice.  (One warp in its place was what the walk waited for: 360 us against 246 at the sizes below.)
 //
-// Eight sequences of 2,048 tokens, 16 heads of 96/192: 213 us, preparation 45 and walk 163.  That is 1.5 TB/s of the
+// Eight sequences of 2,048 tokens, 16 heads of 96/192: 215 us, preparation 46 and walk 164.  That is 1.5 TB/s of the
 // inputs and outputs: the walk keeps mma.sync's pipe 71% busy with one block of 128 registers a thread on an SM, and
 // a quarter of its warps; HBM would need 46 us.
 //
 // A third and a fourth kernel serve few long chains, cut into segments (segment_tokens): a walk over each segment's
 // map S -> M S + N, delta_join_kernel over the maps, then the walk of every segment from its own state.  32,768
-// tokens of 16 heads: 867 us (preparation 78, maps 450, join 48, walk 300), against 1,416 as whole chains.
+// tokens of 16 heads: 876 us (preparation 80, maps 456, join 47, walk 288), against 1,416 as whole chains.
 #include "gla_delta_mma.cuh"
 
 GLA_DEFINE_STATUS(delta_mma)
@@ -495,7 +495,7 @@ delta_join_kernel(Shape p, int segment, const float *__restrict__ M, const float
 }
 
 // Tokens per segment, or 0 for whole chains.  A walk is one product after another, so few chains leave most of the GPU
-// idle: B1 T32768 H16 dk96 dv192 takes 1,416 us as 16 chains and 867 cut.  Chains are cut into as many segments as fill
+// idle: B1 T32768 H16 dk96 dv192 takes 1,416 us as 16 chains and 876 cut.  Chains are cut into as many segments as fill
 // the GPU (12 column tiles to an SM), none shorter than 256 tokens, where that is the cheaper way.  Counted in steps of a
 // walk (a chunk of a chain, some 0.16 us times KT), with n segments to a sequence,
 //     saved  the steps of n - 1 segments

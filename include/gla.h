@@ -444,17 +444,24 @@ GLA_API int gla_conv1d_silu_step(const void *x, const float *weight, const float
  * state already answers to k_t:
  *     u_t = beta_t (v_t - a_t k_t S_{t-1}),  S_t = a_t S_{t-1} + k_t^T u_t,  o_t = q_t S_t,  a_t = exp(g_t)
  * There is no extra scale or normalisation of q and k: both belong to the caller (the recurrence is stable
- * where beta_t |k_t|^2 <= 2 and g_t <= 0).  g_t = -inf (a_t = 0) is a full reset of the state.
+ * where beta_t |k_t|^2 <= 2 and g_t <= 0).  g_t = -inf (a_t = 0) is a full reset of a finite state.
  *
  * Heads: q and k have Hk heads, v, g, beta, out and the states H; Hk divides H, and value head h reads query
  * and key head h / (H / Hk).  The gradients of q and k are sums over the value heads that read them.
  *   dtype       GLA_BF16 or GLA_F32: q, k, v, out and their gradients
- *   gate_dtype  GLA_F32, or dtype: g, beta and their gradients.  (With bf16 inputs the gradients carry the
- *               rounding of bf16 products, about 2e-3 of their size, in either type.)
- * All states and sums are f32.  Sizes: 16 <= dk <= 256, 16 <= dv <= 512, both multiples of 8.
- * bf16 sequences run in chunks: a NaN or an infinity at a token may reach the other tokens of its chain within
- * the 32 around it (64 in the gradients) as well as all later ones (earlier ones, in the gradients), and no
- * other chain.  f32 sequences run token by token.
+ *   gate_dtype  GLA_F32, or dtype: g, beta and their gradients
+ * Sizes: 16 <= dk <= 256, 16 <= dv <= 512, both multiples of 8.
+ *
+ * Kernels: bf16 with dk <= 128 runs in chunks of 32 tokens on the tensor cores; f32, and bf16 with dk > 128, token by
+ * token in f32 arithmetic, several times to thirty times slower.  (gla_chunk_kernel does not speak of these calls.)
+ * Precision: states and sums are f32.  On the tensor cores operands are rounded.  As the norm of an error over the
+ * norm of what it is in, of a head: states and X are multiplied as two bf16 parts, 2^-17 an operand, and hT comes out
+ * within 6e-6; out, of which the other operands are bf16, within 3.5e-3, of which its own rounding is 1.7e-3.  The gradients'
+ * products take bf16 operands: 4e-3 to 5e-3, up to 1.6e-2 for dg where its sums cancel, and no better in dg, dbeta
+ * and dh0 where these are f32.  Token by token all are within 4e-6 before they are rounded to their type.
+ * A NaN or an infinity reaches what the formulas carry it to.  On the tensor cores it may also reach the other tokens of
+ * its chain in its chunk of 32 (in the gradients, of either type, of 64; chunks are counted from the sequence's start),
+ * earlier ones among them.  It reaches no other chain.
  */
 
 /*
@@ -475,7 +482,6 @@ GLA_API long long gla_delta_workspace_bytes(int op, int B, int T, int H, int Hk,
  *               others are what they are without it.  T = 0 (packed) leaves only empty sequences
  *   ws, ws_bytes  workspace of at least gla_delta_workspace_bytes(GLA_OP_FORWARD, ...) bytes (else
  *               GLA_ERR_ARG); NULL where that is 0
- * bf16 out is rounded once; hT comes from f32 sums over unrounded products (f32 accuracy) in both types.
  * Returns a gla_status.
  */
 GLA_API int gla_delta_chunk_fwd(const void *q, const void *k, const void *v, const void *g, const void *beta,
@@ -486,7 +492,7 @@ GLA_API int gla_delta_chunk_fwd(const void *q, const void *k, const void *v, con
 /*
  * gla_delta_chunk_bwd — its gradients, with L = sum(dout .* out) + sum(dhT .* hT).  With dS_t the gradient
  * with respect to S_t, backwards in time from dS_T = dhT + q_T^T dout_T:
- *     y_t = k_t dS_t,  dv_t = beta_t y_t,  dbeta_t = y_t . u_t / beta_t,  dq_t = dout_t S_t^T,
+ *     y_t = k_t dS_t,  dv_t = beta_t y_t,  dbeta_t = y_t . (v_t - a_t k_t S_{t-1}),  dq_t = dout_t S_t^T,
  *     dk_t = u_t dS_t^T - dv_t (a_t S_{t-1})^T,  dg_t = <dS_t - k_t^T dv_t, a_t S_{t-1}>,
  *     dS_{t-1} = a_t (dS_t - k_t^T dv_t) + q_{t-1}^T dout_{t-1},  dh0 = a_1 (dS_1 - k_1^T dv_1)
  * The states are recomputed; nothing is kept from the forward.
@@ -494,7 +500,7 @@ GLA_API int gla_delta_chunk_fwd(const void *q, const void *k, const void *v, con
  *   dq, dk_out  as q, k;  dv_out as v;  dg, dbeta as g, beta: written
  *   dh0         [B, H, dk, dv] f32, written; NULL to skip
  *   ws, ws_bytes  workspace of at least gla_delta_workspace_bytes(GLA_OP_BACKWARD, ...) bytes
- * No array may alias another.  Returns a gla_status.
+ * Rows of a packed batch that are no sequence's are not written.  No array may alias another.  Returns a gla_status.
  */
 GLA_API int gla_delta_chunk_bwd(const void *q, const void *k, const void *v, const void *g, const void *beta,
                                 const void *dout, const float *h0, const float *dhT, void *dq, void *dk_out,
@@ -526,7 +532,8 @@ GLA_API int gla_delta_decode_step(const void *q, const void *k, const void *v, c
  *   weight, bias  [groups * width] f32, NULL for ones / zeros
  *   act           a gla_act;  eps > 0
  *   width         a multiple of 8, 8 <= width <= 2048; groups * width <= 1048576; rows >= 0
- * Statistics and arithmetic are f32; out is rounded once.  Returns a gla_status.
+ * Statistics and arithmetic are f32; out is rounded once.  A sigmoid of x is good to 2 + |x| units of 2^-24, and 0 where
+ * it is below the smallest normal number: a gate of the type's lowest value gives 0.  Returns a gla_status.
  */
 typedef enum { GLA_ACT_NONE = 0, GLA_ACT_SILU = 1, GLA_ACT_SIGMOID = 2 } gla_act;
 GLA_API int gla_group_norm(const void *x, const float *weight, const float *bias, const void *gate, int act, float eps,
@@ -553,7 +560,7 @@ GLA_API int gla_group_norm_bwd(const void *dout, const void *x, const float *wei
 GLA_API int gla_last_device_status(void *stream);
 
 /*
- * gla_chunk_kernel — which kernel a chunked entry point runs for these sizes on
+ * gla_chunk_kernel — which kernel a chunked entry point (not of the gated delta rule) runs for these sizes on
  * the current device (a host-side query; launches nothing).
  *   op     GLA_OP_FORWARD (gla_chunk_fwd and its _noalloc, _host and _save
  *          forms), GLA_OP_FORWARD_GATED (gla_chunk_fwd_gated) or GLA_OP_BACKWARD
