@@ -19,10 +19,7 @@ struct Shape {
     // packed, [nseq + 1], which the first kernel of a call writes: the first row and the number of rows of each sequence,
     // then the rows that all of them have together, or a negative number of them where the batch is not in order
     int2 *rows;
-    // [nseq], likewise, what the walks over chains take in turn: first row, number of rows, sequence; the longest first
-    // where `ranked`, else as the batch has them
-    int4 *walks;
-    int ranked;
+    int *order;  // [nseq], likewise: the sequences, the longest first; null where the walks take them as they come
     __host__ __device__ int group() const { return H / Hk; }
 };
 
@@ -32,7 +29,7 @@ __host__ inline long long total_rows(const Shape &s) { return s.cu ? (long long)
 // start_s / C + s + c; slots of different chunks differ, and all are below slots(rows, nseq, C).
 __host__ inline long long chunk_slots(long long rows, int nseq, int C) { return rows / C + nseq + 1; }
 __host__ inline size_t rows_bytes(const Shape &s) {
-    return s.cu ? ((size_t)s.nseq * sizeof(int4) + ((size_t)s.nseq + 1) * sizeof(int2) + 255) / 256 * 256 : 0;
+    return s.cu ? (((size_t)s.nseq + 1) * sizeof(int2) + (size_t)s.nseq * sizeof(int) + 255) / 256 * 256 : 0;
 }
 
 // ---- packed batches: offsets as they come ------------------------------------------------------------------------

@@ -98,7 +98,7 @@ __device__ __forceinline__ void walk_again(const Shape &p, const Walk &w, unsign
                                            const AgainRecord *__restrict__ records, const float *__restrict__ h0,
                                            bf16 *__restrict__ resid, uint4 *__restrict__ images) {
     constexpr int kTile = kC * row_bytes<KT>();
-    const Frame f(p, w, block, sm_raw, false);
+    const Frame f(p, w, block, sm_raw);
     if (f.warp >= w.groups * 4) {
         give_registers();
         fetch<KT, false, false, 1>(p, w, f, k, k, v, records, resid, nullptr);
@@ -108,7 +108,7 @@ __device__ __forceinline__ void walk_again(const Shape &p, const Walk &w, unsign
     if (f.warp >= w.warps) return;
     const int lane = f.lane, tg = lane & 3, m8 = lane >> 3, r8 = lane & 7;
     const int col = f.col0 + f.warp * 16;
-    const int64_t slot64 = f.start / kG + f.s;
+    const int64_t slot64 = f.r.start / kG + f.s;
     const bool live = col < p.dv;
     float S[2 * KT][4];
     load_state<KT>(S, h0, f.walk, p.dk, p.dv, col, lane);
@@ -177,7 +177,7 @@ __device__ __forceinline__ void walk_back(const Shape &p, const Walk &w, unsigne
                                           const float *__restrict__ dhT, bf16 *__restrict__ ys, bf16 *__restrict__ dv,
                                           uint4 *__restrict__ images, float *__restrict__ dh0) {
     constexpr int kTile = kC * row_bytes<KT>();
-    const Frame f(p, w, block, sm_raw, false);
+    const Frame f(p, w, block, sm_raw);
     if (f.warp >= w.groups * 4) {
         give_registers();
         fetch<KT, true, true, 2>(p, w, f, q, k, dout, records, ys, dv);
@@ -187,7 +187,7 @@ __device__ __forceinline__ void walk_back(const Shape &p, const Walk &w, unsigne
     if (f.warp >= w.warps) return;
     const int lane = f.lane, tg = lane & 3, m8 = lane >> 3, r8 = lane & 7;
     const int col = f.col0 + f.warp * 16;
-    const int64_t slot64 = f.start / kG + f.s;
+    const int64_t slot64 = f.r.start / kG + f.s;
     const bool live = col < p.dv;
     float S[2 * KT][4];
     load_state<KT>(S, dhT, f.walk, p.dk, p.dv, col, lane);

@@ -112,10 +112,10 @@ delta_prep_kernel(Shape p, unsigned units, const bf16 *__restrict__ q, const bf1
     if (p.cu != nullptr && seq < (unsigned)p.nseq) {
         SeqRange r;
         const bool good = checked_rows(p, in_order, (int)seq, r);
-        const int turn = p.ranked ? rank_of(p, (int)seq, lane) : (int)seq;
+        const int turn = p.order != nullptr ? rank_of(p, (int)seq, lane) : 0;
         if (lane == 0) {
             p.rows[seq] = make_int2((int)r.start, (int)r.len);
-            p.walks[turn] = make_int4((int)r.start, (int)r.len, (int)seq, 0);
+            if (p.order != nullptr) p.order[turn] = (int)seq;
             if (seq == 0) p.rows[p.nseq] = span_of(p, in_order);
             if (!good) record_status(GLA_ERR_DEVICE_ARG);
         }
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 delta_fwd_kernel(Shape p, Walk w, FwdArgs a) {
     extern __shared__ __align__(128) char sm_raw[];
     constexpr int kRow = row_bytes<KT>(), kTile = kC * kRow, kV = (kSegment ? 1 : 2) * kTile;
-    const Frame f(p, w, blockIdx.x, sm_raw, kSegment || w.segment != 0);
+    const Frame f(p, w, blockIdx.x, sm_raw);
     if (!f.exists || (kSegment && f.last)) return;  // nothing starts where a sequence ends
     if (f.warp >= w.groups * 4) {
         give_registers();

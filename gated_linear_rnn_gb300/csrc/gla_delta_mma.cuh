@@ -172,9 +172,8 @@ constexpr int kRankedWaves = 8;
 // rows_bytes at `at`; blocks: of the launch whose blocks walk over whole chains, or 0
 inline void place_rows(Shape &p, char *at, long long blocks) {
     const long long sms = device_info().sm_count;
-    p.walks = reinterpret_cast<int4 *>(at);
-    p.rows = reinterpret_cast<int2 *>(p.walks + p.nseq);
-    p.ranked = blocks > sms && blocks <= kRankedWaves * sms;
+    p.rows = reinterpret_cast<int2 *>(at);
+    p.order = p.cu != nullptr && blocks > sms && blocks <= kRankedWaves * sms ? reinterpret_cast<int *>(p.rows + p.nseq + 1) : nullptr;
 }
 // How many sequences start before s: the longer ones, and of equals the first.  (A bad one's length is only an order here.)
 __device__ __forceinline__ int rank_of(const Shape &p, int s, int lane) {
@@ -194,13 +193,12 @@ struct Frame {
     int walk;       // (sequence or segment's slot) * H + head
     bool exists;    // whether a segment has this slot
     bool last;      // of its sequence's segments
-    int start, len;    // the rows that this block walks over
-    int slot0;         // slot of its first chunk
+    SeqRange r;     // the rows that this block walks over
+    int64_t slot0;  // slot of its first chunk
     uint32_t full, empty, ring;
     volatile int *abort_flag;
 
-    // cut: whether the block walks over a segment of a chain; a constant where the kernel only does one or the other
-    __device__ __forceinline__ Frame(const Shape &p, const Walk &w, unsigned block, char *sm, bool cut) {
+    __device__ __forceinline__ Frame(const Shape &p, const Walk &w, unsigned block, char *sm) {
         lane = threadIdx.x & 31;
         warp = threadIdx.x >> 5;
         walk = (int)(block / (unsigned)w.splits);
@@ -210,35 +208,30 @@ struct Frame {
         col0 = (int)(block % (unsigned)w.splits) * w.warps * 16;  // first column of the block
         width = min(w.warps * 16, p.dv - col0);                   // its columns of v, a multiple of 8 (none: <= 0)
         exists = last = true;
-        if (!cut) {
-            if (p.cu != nullptr) {
-                const int4 t = __ldg(p.walks + s);
-                start = t.x;
-                len = t.y;
-                s = t.z;
+        if (w.segment == 0) {
+            if (p.order != nullptr) {
+                // through shared memory: the walk is 163 us for 160.5 at 8 x 2,048 tokens where each thread loads it
+                volatile int *turn = reinterpret_cast<volatile int *>(sm + 16 * w.stages + 4);
+                if (threadIdx.x == 0) *turn = __ldg(p.order + s);
+                __syncthreads();
+                s = *turn;
                 walk = s * p.H + h;
-            } else {
-                start = s * p.T;
-                len = p.T;
             }
-            slot0 = start / kC + s;
+            r = rows_of(p, s);
+            slot0 = r.start / kC + s;
         } else {
             // segment i of sequence s has the slot start_s / segment + s + i
             const int slot = s;
             s = bisect_slots(p, slot, w.segment, [&](int i) { return __ldg(p.rows + i).x; });
-            const SeqRange r = rows_of(p, s);
-            start = (int)r.start;
-            len = (int)r.len;
-            const int i = slot - (start / w.segment + s);
-            exists = i >= 0 && (int64_t)i * w.segment < len;  // a sequence without rows has none: delta_join_kernel's
-            const int before = exists ? i * w.segment : 0;
-            slot0 = (start / kC) + s + before / kC;
-            start += before;
-            len -= before;
-            last = len <= w.segment;
-            len = min(len, w.segment);
+            r = rows_of(p, s);
+            const int i = slot - ((int)r.start / w.segment + s);
+            exists = i >= 0 && (int64_t)i * w.segment < r.len;  // a sequence without rows has none: delta_join_kernel's
+            last = (int64_t)(i + 1) * w.segment >= r.len;
+            slot0 = r.start / kC + s + (int64_t)i * (w.segment / kC);
+            r.start += (int64_t)i * w.segment;
+            r.len = min((int64_t)w.segment, r.len - (int64_t)i * w.segment);
         }
-        nch = (len + kC - 1) / kC;
+        nch = (int)((r.len + kC - 1) / kC);
         full = ptx::smem_u32(sm);
         empty = full + 8 * w.stages;
         abort_flag = reinterpret_cast<volatile int *>(sm + 16 * w.stages);
@@ -261,9 +254,9 @@ template <int kOut>
 __device__ __forceinline__ void write_rows(const Shape &p, const Walk &w, const Frame &f, int c, uint32_t v, uint32_t second,
                                            bf16 *out, bf16 *out2) {
     const int units = f.width / 8, id = threadIdx.x - w.groups * 128;
-    const int rows = min(kC, f.len - c * kC);
+    const int rows = (int)min((int64_t)kC, f.r.len - (int64_t)c * kC);
     const unsigned inv = (65536 + units - 1) / units;  // e / units for e < 32 * 24 by a product
-    const int64_t at = ((int64_t)(f.start + c * kC) * p.H + f.h) * p.dv + f.col0;
+    const int64_t at = ((f.r.start + (int64_t)c * kC) * p.H + f.h) * p.dv + f.col0;
     for (int e = id; e < rows * units; e += 128) {
         const int t = (int)(((unsigned)e * inv) >> 16), u = e - t * units;
         const int64_t to = at + (int64_t)t * p.H * p.dv + u * 8;
@@ -282,7 +275,7 @@ __device__ __forceinline__ void fetch(const Shape &p, const Walk &w, const Frame
     const int id = threadIdx.x - w.groups * 128, t = id >> 2, u0 = id & 3;
     const int vunits = w.warps * 2, vlive = f.width / 8, kunits = p.dk / 8;
     const int64_t kstride = (int64_t)p.Hk * p.dk, vstride = (int64_t)p.H * p.dv;
-    const int64_t row0 = (int64_t)f.start + t + (kBack ? (f.nch - 1) * kC : 0);
+    const int64_t row0 = f.r.start + t + (kBack ? (int64_t)(f.nch - 1) * kC : 0);
     const bf16 *kr = k + row0 * kstride + f.hk * p.dk + u0 * 8, *qr = q + row0 * kstride + f.hk * p.dk + u0 * 8,
                *vr = v + row0 * vstride + (int64_t)f.h * p.dv + f.col0 + u0 * 8;
     const uint32_t kdst = f.ring + t * kRow + u0 * 16, vdst = f.ring + kV + t * w.vrow + u0 * 16;
@@ -305,10 +298,10 @@ __device__ __forceinline__ void fetch(const Shape &p, const Walk &w, const Frame
         }
         if (i >= f.nch) continue;
         const int c = kBack ? f.nch - 1 - i : i;
-        const bool row = c * kC + t < f.len;  // a short chunk's missing rows are zero, and not read
+        const bool row = c * kC + t < f.r.len;  // a short chunk's missing rows are zero, and not read
         if (id == 0) {
             ptx::mbar_expect_tx(f.full + 8 * sg, (uint32_t)sizeof(Rec));
-            ptx::bulk_load_g2s(f.ring + at + kV + kC * w.vrow, records + (int64_t)(f.slot0 + c) * p.H + f.h, sizeof(Rec),
+            ptx::bulk_load_g2s(f.ring + at + kV + kC * w.vrow, records + (f.slot0 + c) * p.H + f.h, sizeof(Rec),
                                f.full + 8 * sg);
         }
 #pragma unroll
