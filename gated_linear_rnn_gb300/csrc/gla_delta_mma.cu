@@ -30,13 +30,13 @@
 // bulk copy into a ring of stages; a row's stride is an odd number of 16-byte units, so that ldmatrix meets no bank
 // twice.  (One warp in its place was what the walk waited for: 360 us against 246 at the sizes below.)
 //
-// Eight sequences of 2,048 tokens, 16 heads of 96/192: 215 us, preparation 46 and walk 164.  That is 1.5 TB/s of the
+// Eight sequences of 2,048 tokens, 16 heads of 96/192: 212 us, preparation 45 and walk 161.  That is 1.5 TB/s of the
 // inputs and outputs: the walk keeps mma.sync's pipe 71% busy with one block of 128 registers a thread on an SM, and
 // a quarter of its warps; HBM would need 46 us.
 //
 // A third and a fourth kernel serve few long chains, cut into segments (segment_tokens): a walk over each segment's
 // map S -> M S + N, delta_join_kernel over the maps, then the walk of every segment from its own state.  32,768
-// tokens of 16 heads: 876 us (preparation 80, maps 456, join 47, walk 288), against 1,416 as whole chains.
+// tokens of 16 heads: 865 us (preparation 80, maps 447, join 47, walk 281), against 1,416 as whole chains.
 #include "gla_delta_mma.cuh"
 
 GLA_DEFINE_STATUS(delta_mma)
@@ -495,7 +495,7 @@ delta_join_kernel(Shape p, int segment, const float *__restrict__ M, const float
 }
 
 // Tokens per segment, or 0 for whole chains.  A walk is one product after another, so few chains leave most of the GPU
-// idle: B1 T32768 H16 dk96 dv192 takes 1,416 us as 16 chains and 876 cut.  Chains are cut into as many segments as fill
+// idle: B1 T32768 H16 dk96 dv192 takes 1,416 us as 16 chains and 865 cut.  Chains are cut into as many segments as fill
 // the GPU (12 column tiles to an SM), none shorter than 256 tokens, where that is the cheaper way.  Counted in steps of a
 // walk (a chunk of a chain, some 0.16 us times KT), with n segments to a sequence,
 //     saved  the steps of n - 1 segments
