@@ -347,9 +347,15 @@ delta_rec_fwd_kernel(Shape p, const T *__restrict__ q, const T *__restrict__ k, 
     __shared__ __align__(16) St sm[2];
     const Lane<kRpl> ln(p);
     SeqRange r;
-    if (!checked_rows(p, offsets_in_order(p), ln.s, r) && threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
-    if (p.rows != nullptr && ln.h == 0 && blockIdx.y == 0 && threadIdx.x == 0)
-        p.rows[ln.s] = make_int2((int)r.start, (int)r.len);  // no kernel after this one asks for the span
+    const bool good = good_sequence(p, ln.s, r);
+    if (!good) {
+        r.start = r.len = 0;
+        if (threadIdx.x == 0) record_status(GLA_ERR_DEVICE_ARG);
+    }
+    if (p.rows != nullptr && ln.h == 0 && blockIdx.y == 0 && threadIdx.x < 32) {  // no later kernel asks for the span
+        const int start = good ? (int)r.start : end_before(p, ln.s);
+        if (threadIdx.x == 0) p.rows[ln.s] = make_int2(start, (int)r.len);
+    }
     Pair S[kRpl / 2];
     ln.load(S, h0, p);
     const int64_t slot0 = r.start / 64 + ln.s;

@@ -20,6 +20,7 @@ struct Shape {
     // then the rows that all of them have together, or a negative number of them where the batch is not in order
     int2 *rows;
     int *order;  // [nseq], likewise: the sequences, the longest first; null where the walks take them as they come
+    int planned;  // whether a kernel of its own has written rows, ahead of the preparation
     __host__ __device__ int group() const { return H / Hk; }
 };
 
@@ -39,26 +40,46 @@ __host__ inline size_t rows_bytes(const Shape &s) {
 // are what they are alone.  A call's first kernel looks at the offsets and leaves the rows of every sequence to the
 // others: a bad one has none, at the end of those before it, so that the starts rise and can be bisected.
 
+// Every warp that asks for a sequence or a chunk by the offsets looks at all of them: up to so many.  More are planned.
+constexpr int kMostChecked = 256;
+
 // By a whole warp.
 __device__ __forceinline__ bool offsets_in_order(const Shape &p) {
-    if (p.cu == nullptr) return true;
     bool ok = true;
-    for (unsigned i = threadIdx.x & 31; i < (unsigned)p.nseq; i += 32) {
+    for (int i = threadIdx.x & 31; i < p.nseq; i += 32) {
         const int32_t a = __ldg(p.cu + i), b = __ldg(p.cu + i + 1);
         ok = ok && a >= 0 && a <= b && b <= p.T;
     }
     return __all_sync(0xffffffffu, ok);
 }
 
-// The rows of sequence s; false for a bad one.
+// Whether sequence s is good, by all threads of a block: what a kernel that takes sequences, not chunks, has to know.
+__device__ __forceinline__ bool good_sequence(const Shape &p, int s, SeqRange &r) {
+    const bool own = seq_range(s, p.T, p.cu, r);
+    if (p.cu == nullptr) return true;
+    bool shared = false;  // rows of an earlier one
+    for (int j = threadIdx.x; j < s; j += blockDim.x) {
+        SeqRange o;
+        if (seq_range(j, p.T, p.cu, o) && o.start + o.len > r.start) shared = true;
+    }
+    return !__syncthreads_or(shared) && own;
+}
+
+// The largest end of the sequences before s, by a whole warp.
+__device__ __forceinline__ int end_before(const Shape &p, int s) {
+    int end = 0;
+    for (int j = threadIdx.x & 31; j < s; j += 32) {
+        SeqRange r;
+        if (seq_range(j, p.T, p.cu, r)) end = max(end, (int)(r.start + r.len));
+    }
+    return __reduce_max_sync(0xffffffffu, end);
+}
+
+// The rows of sequence s, by a whole warp; false for a bad one.
 __device__ __forceinline__ bool checked_rows(const Shape &p, bool in_order, int s, SeqRange &r) {
     bool good = seq_range(s, p.T, p.cu, r);
     if (!in_order) {
-        int64_t end = 0;  // of the sequences before it
-        for (int j = 0; j < s; ++j) {
-            SeqRange o;
-            if (seq_range(j, p.T, p.cu, o)) end = max(end, o.start + o.len);
-        }
+        const int end = end_before(p, s);
         if (r.start < end) good = false;
         if (!good) {
             r.start = end;

@@ -106,22 +106,35 @@ delta_prep_kernel(Shape p, unsigned units, const bf16 *__restrict__ q, const bf1
     const unsigned unit = blockIdx.x * kPrepWarps + warp;  // slot * H + h
     if (unit >= units) return;
     const int h = (int)(unit % (unsigned)p.H), hk = h / p.group();
-    const bool in_order = offsets_in_order(p);
-    // the rows of every sequence, for the kernels that follow, by the last units: they have the fewest chunks
-    const unsigned seq = units - 1 - unit;
-    if (p.cu != nullptr && seq < (unsigned)p.nseq) {
-        SeqRange r;
-        const bool good = checked_rows(p, in_order, (int)seq, r);
-        const int turn = p.order != nullptr ? rank_of(p, (int)seq, lane) : 0;
-        if (lane == 0) {
-            p.rows[seq] = make_int2((int)r.start, (int)r.len);
-            if (p.order != nullptr) p.order[turn] = (int)seq;
-            if (seq == 0) p.rows[p.nseq] = span_of(p, in_order);
-            if (!good) record_status(GLA_ERR_DEVICE_ARG);
+    const int slot = (int)(unit / (unsigned)p.H);
+    ChunkAt at;
+    bool has;
+    if (p.cu == nullptr) {
+        has = chunk_of_slot<kC>(slot, p, at);
+    } else {
+        // what the kernels that follow need of every sequence, by the last units: they have the fewest chunks
+        const unsigned seq = units - 1 - unit;
+        if (p.order != nullptr && seq < (unsigned)p.nseq) {
+            const int turn = rank_of(p, (int)seq, lane);
+            if (lane == 0) p.order[turn] = (int)seq;
+        }
+        if (p.planned) {
+            has = chunk_of_slot<kC>(slot, p, at);
+        } else {
+            const bool in_order = offsets_in_order(p);
+            if (seq < (unsigned)p.nseq) {
+                SeqRange r;
+                const bool good = checked_rows(p, in_order, (int)seq, r);
+                if (lane == 0) {
+                    p.rows[seq] = make_int2((int)r.start, (int)r.len);
+                    if (seq == 0) p.rows[p.nseq] = span_of(p, in_order);
+                    if (!good) record_status(GLA_ERR_DEVICE_ARG);
+                }
+            }
+            has = checked_chunk_of_slot<kC>(slot, p, in_order, at);
         }
     }
-    ChunkAt at;
-    if (!checked_chunk_of_slot<kC>((int)(unit / (unsigned)p.H), p, in_order, at)) return;
+    if (!has) return;
     char *ks = sm_raw + warp * prep_warp_bytes<KT>(), *qs = ks + kC * row_bytes<KT>();
     float *L = reinterpret_cast<float *>(ks), *D = L + kC * kLd;  // in the rows' place once these are read
     const uint32_t ka = ptx::smem_u32(ks), qa = ptx::smem_u32(qs);
@@ -538,12 +551,52 @@ Segments plan_segments(const Shape &p) {
     return g;
 }
 
+// The rows of every sequence of a batch of more than kMostChecked, by one block.
+constexpr int kPlanThreads = 1024;
+__global__ void __launch_bounds__(kPlanThreads) delta_plan_kernel(Shape p) {
+    __shared__ int ends[kPlanThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int end = 0;  // of the sequences so far
+    bool all_good = true;
+    for (int64_t s0 = 0; s0 < p.nseq; s0 += kPlanThreads) {
+        const int64_t s = s0 + threadIdx.x;
+        SeqRange r{0, 0};
+        const bool own = s < p.nseq && seq_range((int)s, p.T, p.cu, r);
+        int upto = own ? (int)(r.start + r.len) : 0;  // the largest end of this warp's sequences up to this one
+        for (int m = 1; m < 32; m <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, m);
+            if (lane >= m) upto = max(upto, x);
+        }
+        if (lane == 31) ends[warp] = upto;
+        __syncthreads();
+        int before = __shfl_up_sync(0xffffffffu, upto, 1);
+        before = max(end, lane > 0 ? before : 0);
+        for (int i = 0; i < kPlanThreads / 32; ++i) {
+            if (i < warp) before = max(before, ends[i]);
+            end = max(end, ends[i]);
+        }
+        if (s < p.nseq) {
+            const bool good = own && r.start >= before;
+            p.rows[s] = good ? make_int2((int)r.start, (int)r.len) : make_int2(before, 0);
+            if (!good) record_status(GLA_ERR_DEVICE_ARG);
+            all_good = all_good && good;
+        }
+        __syncthreads();
+    }
+    if (!__syncthreads_and(all_good)) all_good = false;
+    if (threadIdx.x == 0) p.rows[p.nseq] = span_of(p, all_good);
+}
+
 template <int KT, bool kGrad>
 int launch_prep(const Shape &p, const bf16 *q, const bf16 *k, const void *g, const void *beta, FwdRecord *records,
                 AgainRecord *again, BwdRecord *back, cudaStream_t st) {
     const unsigned units = (unsigned)(chunk_slots(total_rows(p), p.nseq, kC) * p.H);
     const int bytes = kPrepWarps * prep_warp_bytes<KT>();
     if (!allow_smem<delta_prep_kernel<KT, kGrad>>()) return GLA_ERR_LAUNCH;
+    if (p.planned) {
+        delta_plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
+        count_launches(1);
+    }
     delta_prep_kernel<KT, kGrad><<<(units + kPrepWarps - 1) / kPrepWarps, kPrepWarps * 32, bytes, st>>>(
         p, units, q, k, g, beta, records, again, back);
     count_launches(1);

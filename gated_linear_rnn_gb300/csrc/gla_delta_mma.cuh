@@ -164,7 +164,7 @@ template <int kBarrier, int kThreads> __device__ __forceinline__ bool any_of(boo
 }
 
 // The walks over a packed batch start in the order of their lengths, the longest first, so that the last ones to end are
-// short, where their blocks run in two to eight waves.  The preparation finds each sequence's rank, by a warp that looks
+// short, where their blocks run in more than one and at most eight waves.  The preparation finds each sequence's rank, by a warp that looks
 // at all lengths.  16 heads of 96/192, in this order and in the batch's own: 24 sequences of 0..256 tokens 52 and 58 us,
 // of 0..1,024 148 and 160, 64 of 0..1,024 381 and 416; of 64 equal lengths 58 and 56.  In one wave all start at once, and
 // in many the order is nothing but its cost: 8 of 0..1,024 77 and 75 us, 128 of 0..256 262 and 262, 256 of them 513 and 498.
@@ -173,6 +173,7 @@ constexpr int kRankedWaves = 8;
 inline void place_rows(Shape &p, char *at, long long blocks) {
     const long long sms = device_info().sm_count;
     p.rows = reinterpret_cast<int2 *>(at);
+    p.planned = p.cu != nullptr && p.nseq > kMostChecked;
     p.order = p.cu != nullptr && blocks > sms && blocks <= kRankedWaves * sms ? reinterpret_cast<int *>(p.rows + p.nseq + 1) : nullptr;
 }
 // How many sequences start before s: the longer ones, and of equals the first.  (A bad one's length is only an order here.)

@@ -124,6 +124,37 @@ def test_a_bad_offset_among_many_sequences(dtype):
     check_many(cu, 1600, dtype)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [255, 256, 257, 1024, 1025, 5000])
+def test_bad_offsets_among_more_and_more_sequences(dtype, n):
+    """Few sequences are checked where they are asked for, many by a kernel of their own, a thousand at a time."""
+    cu = list(range(0, n + 1))
+    cu[n // 3], cu[n - 7] = -5, n // 2
+    check_many(cu, n, dtype)
+
+
+@pytest.mark.parametrize("n", [256, 257, 3000])
+def test_gradients_beside_a_bad_offset_among_many_sequences(n):
+    """All kernels of a gradient agree on the sequences: what a good one gets is what it gets in a batch in order."""
+    T, sizes = 2 * n + 40, (4, 2, 32, 16, torch.bfloat16)
+    x = inputs(T, n, 4, 2, 32, 16, torch.bfloat16)
+    cu = list(range(0, 2 * n + 1, 2))
+    cu[-1] = T  # the last sequence is the longest
+    want_rows, want_states = run(x, cu, T, n, *sizes, True)
+    assert gla.gla_last_device_status() == 0
+    spoilt = list(cu)
+    spoilt[n // 2] = 10 ** 6
+    rows, states = run(x, spoilt, T, n, *sizes, True)
+    assert gla.STATUS[gla.gla_last_device_status()] == "GLA_ERR_DEVICE_ARG"
+    first, last = cu[n // 2 - 1], cu[n // 2 + 1]
+    for name, t in rows.items():
+        assert torch.equal(t[:, :first], want_rows[name][:, :first]) and torch.equal(t[:, last:], want_rows[name][:, last:]), name
+        assert bool((t[:, first:last] == 7.0).all()), name
+    for name, t in states.items():
+        keep = [i for i in range(n) if i not in (n // 2 - 1, n // 2)]
+        assert torch.equal(t[keep], want_states[name][keep]), name
+
+
 def check_many(cu, T, dtype):
     """One token each, so that out, hT and the gradients have a short form: S = exp(g) h0, u = beta (v - k S), o = q (S + k^T u)."""
     n, H, dk, dv = len(cu) - 1, 1, 16, 16
