@@ -40,8 +40,10 @@ __host__ inline size_t rows_bytes(const Shape &s) {
 // are what they are alone.  A call's first kernel looks at the offsets and leaves the rows of every sequence to the
 // others: a bad one has none, at the end of those before it, so that the starts rise and can be bisected.
 
-// Every warp that asks for a sequence or a chunk by the offsets looks at all of them: up to so many.  More are planned.
-constexpr int kMostChecked = 256;
+// Up to so many sequences, every warp that asks for a chunk by the offsets looks at all of them; more are planned by a
+// kernel ahead.  Sequences of 8 tokens, 4 heads of 96/192, forward, us, checked and planned: 24 of them 13.9 and 15.8, 1,024
+// 198 and 201, 4,096 790 and 774, 16,384 3,462 and 3,066.
+constexpr int kMostChecked = 1024;
 
 // By a whole warp.
 __device__ __forceinline__ bool offsets_in_order(const Shape &p) {
