@@ -400,7 +400,7 @@ def _run_own(s):
         return [out, s["state"]]
     if c["op"] == "fwd":
         return list(gla.scan_fwd(s["x"], s["g"], form, gate=s["gate"], act=act, h0=s["h0"], cu_seqlens=s["cu"]))
-    states = gla.scan_states(s["x"])  # what the forward keeps for the gradient
+    states = gla.scan_states(s["x"], s["cu"])  # what the forward keeps for the gradient
     out, _ = gla.scan_fwd(s["x"], s["g"], form, gate=s["gate"], act=act, h0=s["h0"], cu_seqlens=s["cu"],
                           final_state=False, states=states)
     grads = gla.scan_bwd(s["x"], s["g"], form, s["dout"], gate=s["gate"], act=act, h0=s["h0"], dhT=s["dhT"],
