@@ -19,34 +19,13 @@
 // 16,384 tokens of 16 groups of 192, bf16 with a gate: 55 us (302 MB, 5.5 TB/s, 0.81 of a copy's rate); gradient
 // 100 us (503 MB, 5.0 TB/s, 0.74), of which 9 are the second kernel.  Scalar arithmetic took 71 and 209; pairs with
 // fewer blocks on an SM 66 and 103.
-#include "gla_pairs.cuh"
+#include "gla_act.cuh"
 
 namespace gla {
 namespace norm {
 namespace {
 
 constexpr int kThreads = 256;
-
-enum Act { kNone = GLA_ACT_NONE, kSilu = GLA_ACT_SILU, kSigmoid = GLA_ACT_SIGMOID };
-
-// q = 1 / (1 + e^-x) and rest = 1 - q, each to 2 + |x| units of 2^-24 (the rounding of e^-x's argument), and a NaN where x
-// is one.  rest is e^-x q (1 - q would leave 2^-24 of one where q is near 1, which SiLU's slope multiplies by x).  Below
-// x = -87 e^-x runs into infinity and q into 0, which is the limit; rest is 1 to the last bit from x = -20 on and is not
-// taken from their product there.
-__device__ __forceinline__ void sigmoid(Pair x, Pair &q, Pair &rest) {
-    const float2 f = parts(x);
-    const float2 t = parts(x * both(-1.4426950408889634f));
-    float e0, e1, q0, q1;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t.x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t.y));
-    const Pair e = pair(e0, e1);
-    const float2 d = parts(e + both(1.f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q0) : "f"(d.x));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q1) : "f"(d.y));
-    q = pair(q0, q1);
-    const float2 r = parts(e * q);
-    rest = pair(f.x < -20.f ? 1.f : r.x, f.y < -20.f ? 1.f : r.y);
-}
 
 // Lanes per group (a power of two, whole warps above 32) and vectors of four channels per lane.
 struct Plan {
