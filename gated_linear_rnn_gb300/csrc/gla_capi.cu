@@ -8,6 +8,7 @@
 
 #include "gla_common.cuh"
 #include "gla_delta.cuh"
+#include "gla_scan.cuh"
 
 namespace gla {
 
@@ -85,6 +86,16 @@ int group_norm(const void *, const float *, const float *, const void *, int, fl
 int group_norm_bwd(const void *, const void *, const float *, const float *, const void *, int, float, void *, float *,
                    float *, void *, void *, int64_t, int, int, int, cudaStream_t);
 }  // namespace norm
+namespace scan {
+int64_t workspace(int, const Shape &);
+int fwd(const Shape &, const void *, const void *, const void *, const float *, void *, float *, float *, int, int, void *,
+        cudaStream_t);
+int bwd(const Shape &, const void *, const void *, const void *, const void *, const float *, const float *, const float *,
+        void *, void *, void *, float *, int, int, void *, cudaStream_t);
+int step(const void *, const void *, const void *, float *, const int32_t *, int, void *, int, int, int, int, int, int,
+         cudaStream_t);
+}  // namespace scan
+int take_status_scan(cudaStream_t);
 int take_status_delta(cudaStream_t);
 int take_status_delta_mma(cudaStream_t);
 int take_status_delta_bwd(cudaStream_t);
@@ -238,6 +249,40 @@ int check_norm(const void *x, const float *weight, const float *bias, const void
     if (width % 8 || width > 2048 || (long long)groups * width > (1 << 20) || rows > (1LL << 40))
         return GLA_ERR_UNSUPPORTED;
     if (!aligned16(x) || !aligned16(weight) || !aligned16(bias) || !aligned16(gate) || !aligned16(out))
+        return GLA_ERR_ALIGN;
+    if (!device_info().ok) return GLA_ERR_UNSUPPORTED;
+    return GLA_OK;
+}
+
+// Sizes of the gated recurrence's entry points over whole sequences.
+int check_scan_sizes(int B, int T, int D, int packed) {
+    if (B <= 0 || T < 0 || D <= 0) return GLA_ERR_ARG;
+    if (D % 8) return GLA_ERR_UNSUPPORTED;
+    const long long rows = packed ? (long long)T : (long long)B * T;
+    // rows, and blocks of 64 channels of a chunk or a sequence, are 32-bit
+    const long long parts = (D + 63) / 64;
+    if (rows > 0x7fffff00LL || (rows / scan::kChunk + B + 1) * parts > 0x7fffffffLL || (long long)B * parts > 0x7fffffffLL)
+        return GLA_ERR_UNSUPPORTED;
+    return GLA_OK;
+}
+
+int check_scan_kind(int form, int act, int dtype, int g_dtype) {
+    if (dtype != GLA_BF16 && dtype != GLA_F32) return GLA_ERR_ARG;
+    if (g_dtype != GLA_F32 && g_dtype != dtype) return GLA_ERR_ARG;
+    if (form < GLA_SCAN_LOG || form > GLA_SCAN_SIGMOID_LEAK) return GLA_ERR_ARG;
+    if (act != GLA_ACT_NONE && act != GLA_ACT_SILU && act != GLA_ACT_SIGMOID) return GLA_ERR_ARG;
+    return GLA_OK;
+}
+
+int check_scan(const void *x, const void *g, const void *gate, const float *h0, const void *out, const float *hT,
+               const float *states, int B, int T, int D, int form, int act, int dtype, int g_dtype, const int32_t *cu,
+               const void *ws) {
+    int rc = check_scan_sizes(B, T, D, cu != nullptr);
+    if (!rc) rc = check_scan_kind(form, act, dtype, g_dtype);
+    if (rc) return rc;
+    if (T > 0 && (!x || !g || !out)) return GLA_ERR_ARG;
+    if (!aligned16(x) || !aligned16(g) || !aligned16(gate) || !aligned16(h0) || !aligned16(out) || !aligned16(hT) ||
+        !aligned16(states) || !aligned16(cu) || !aligned16(ws))
         return GLA_ERR_ALIGN;
     if (!device_info().ok) return GLA_ERR_UNSUPPORTED;
     return GLA_OK;
@@ -546,12 +591,65 @@ int gla_group_norm_bwd(const void *dout, const void *x, const float *weight, con
                                 width, dtype, (cudaStream_t)stream);
 }
 
+long long gla_scan_workspace_bytes(int op, int B, int T, int D, int packed) {
+    if (op != GLA_OP_FORWARD && op != GLA_OP_BACKWARD) return GLA_ERR_ARG;
+    int rc = check_scan_sizes(B, T, D, packed);
+    if (rc) return rc;
+    static const int32_t some = 0;  // only whether offsets are given matters here
+    return (long long)scan::workspace(op, {B, T, D, 0, 0, packed ? &some : nullptr});
+}
+
+long long gla_scan_states_bytes(int B, int T, int D, int packed) {
+    int rc = check_scan_sizes(B, T, D, packed);
+    if (rc) return rc;
+    static const int32_t some = 0;
+    return (long long)scan::states_bytes({B, T, D, 0, 0, packed ? &some : nullptr});
+}
+
+int gla_scan_fwd(const void *x, const void *g, const void *gate, const float *h0, void *out, float *hT, float *states, int B,
+                 int T, int D, int form, int act, int dtype, int g_dtype, const int32_t *cu_seqlens, void *ws,
+                 long long ws_bytes, void *stream) {
+    int rc = check_scan(x, g, gate, h0, out, hT, states, B, T, D, form, act, dtype, g_dtype, cu_seqlens, ws);
+    if (rc) return rc;
+    const scan::Shape p{B, T, D, form, act, cu_seqlens};
+    const int64_t need = scan::workspace(GLA_OP_FORWARD, p);
+    if (need > 0 && (!ws || ws_bytes < need)) return GLA_ERR_ARG;
+    return scan::fwd(p, x, g, gate, h0, out, hT, states, dtype, g_dtype, ws, (cudaStream_t)stream);
+}
+
+int gla_scan_bwd(const void *x, const void *g, const void *gate, const void *dout, const float *h0, const float *dhT,
+                 const float *states, void *dx, void *dg, void *dgate, float *dh0, int B, int T, int D, int form, int act,
+                 int dtype, int g_dtype, const int32_t *cu_seqlens, void *ws, long long ws_bytes, void *stream) {
+    int rc = check_scan(x, g, gate, h0, dout, dhT, states, B, T, D, form, act, dtype, g_dtype, cu_seqlens, ws);
+    if (rc) return rc;
+    if (T > 0 && (!dx || !dg || (gate != nullptr) != (dgate != nullptr))) return GLA_ERR_ARG;
+    if (!aligned16(dx) || !aligned16(dg) || !aligned16(dgate) || !aligned16(dh0)) return GLA_ERR_ALIGN;
+    const scan::Shape p{B, T, D, form, act, cu_seqlens};
+    const int64_t need = scan::workspace(GLA_OP_BACKWARD, p);
+    if (need > 0 && (!ws || ws_bytes < need)) return GLA_ERR_ARG;
+    return scan::bwd(p, x, g, gate, dout, h0, dhT, states, dx, dg, dgate, dh0, dtype, g_dtype, ws, (cudaStream_t)stream);
+}
+
+int gla_scan_step(const void *x, const void *g, const void *gate, float *state, const int32_t *slots, int nslots, void *out,
+                  int N, int D, int form, int act, int dtype, int g_dtype, void *stream) {
+    int rc = check_scan_kind(form, act, dtype, g_dtype);
+    if (rc) return rc;
+    if (N < 0 || D <= 0 || (slots && nslots <= 0)) return GLA_ERR_ARG;
+    if (D % 8 || (long long)N * D > (1LL << 40)) return GLA_ERR_UNSUPPORTED;
+    if (N == 0) return GLA_OK;
+    if (!x || !g || !state || !out) return GLA_ERR_ARG;
+    if (!aligned16(x) || !aligned16(g) || !aligned16(gate) || !aligned16(state) || !aligned16(slots) || !aligned16(out))
+        return GLA_ERR_ALIGN;
+    if (!device_info().ok) return GLA_ERR_UNSUPPORTED;
+    return scan::step(x, g, gate, state, slots, nslots, out, N, D, form, act, dtype, g_dtype, (cudaStream_t)stream);
+}
+
 int gla_last_device_status(void *stream) {
     cudaStream_t st = (cudaStream_t)stream;
     int result = GLA_OK;
-    const int parts[8] = {take_status_simt(st), take_status_decode(st), take_status_tc(st), take_status_bwd(st),
+    const int parts[] = {take_status_simt(st), take_status_decode(st), take_status_tc(st), take_status_bwd(st),
                           take_status_conv(st), take_status_delta(st), take_status_delta_mma(st),
-                          take_status_delta_bwd(st)};
+                          take_status_delta_bwd(st), take_status_scan(st)};
     for (int p : parts) {
         if (p == GLA_ERR_LAUNCH) return GLA_ERR_LAUNCH;
         if (result == GLA_OK && p != 0) result = p;

@@ -1,0 +1,182 @@
+// gla_scan.cu — the gated recurrence: forward, gradient and the step for single tokens.
+//
+//     h_t = a_t h_{t-1} + w_t x_t,   out_t = h_t act(gate_t);   a_t = exp(g_t) or sigmoid(g_t),   w_t = 1 or 1 - a_t
+//
+// Gradient, backwards in time with D_T = dhT:
+//     dh_t = dout_t act(gate_t) + D_t,   D_{t-1} = a_t dh_t,   dh0 = D_0,   dx_t = w_t dh_t,
+//     da_t = dh_t (h_{t-1} - x_t) where the input leaks, dh_t h_{t-1} elsewhere,   dg_t = da_t a_t, times 1 - a_t for a sigmoid,
+//     dgate_t = dout_t h_t act'(gate_t)
+#include "gla_scan.cuh"
+
+GLA_DEFINE_STATUS(scan)
+
+namespace gla {
+namespace scan {
+namespace {
+
+constexpr int kThreads = 128;  // two channels each
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t *__restrict__ cu, int nseq, int T, int2 *rows) {
+    if (plan_rows(cu, nseq, T, rows)) record_status(GLA_ERR_DEVICE_ARG);
+}
+
+// A thread takes two channels of a sequence from its first token to its last.
+template <typename T, typename TG, int kForm, bool kGate>
+__global__ void __launch_bounds__(kThreads)
+walk_fwd_kernel(const T *__restrict__ x, const TG *__restrict__ g, const T *__restrict__ gate, const float *__restrict__ h0,
+                T *__restrict__ out, float *__restrict__ hT, float *__restrict__ states, Sequences q, int D, int act, int parts_of_row) {
+    const int s = blockIdx.x / parts_of_row, d = ((blockIdx.x % parts_of_row) * kThreads + (int)threadIdx.x) * 2;
+    if (d >= D) return;
+    const int2 r = rows_of(q, s);
+    Pair h = h0 != nullptr ? load_state(h0 + (int64_t)s * D + d) : both(0.f);
+    const int64_t slot = (int64_t)r.x / kChunk + s;
+    for (int t = 0; t < r.y; ++t) {
+        const int64_t at = (int64_t)(r.x + t) * D + d;
+        if (states != nullptr && t % kChunk == 0) store_state(states + (slot + t / kChunk) * D + d, h);
+        const Decay a = decay<kForm>(load_two(g + at));
+        h = decayed(a, h, input<kForm>(a, load_two(x + at)));
+        if (out != nullptr) store_two(out + at, kGate ? h * activation(load_two(gate + at), act) : h);
+    }
+    if (hT != nullptr) store_state(hT + (int64_t)s * D + d, h);
+}
+
+template <typename T, typename TG, int kForm, bool kGate>
+__global__ void __launch_bounds__(kThreads)
+walk_bwd_kernel(const T *__restrict__ x, const TG *__restrict__ g, const T *__restrict__ gate, const T *__restrict__ dout,
+                const float *__restrict__ dhT, const float *__restrict__ states, T *__restrict__ dx, TG *__restrict__ dg,
+                T *__restrict__ dgate, float *__restrict__ dh0, Sequences q, int D, int act, int parts_of_row) {
+    const int s = blockIdx.x / parts_of_row, d = ((blockIdx.x % parts_of_row) * kThreads + (int)threadIdx.x) * 2;
+    if (d >= D) return;
+    const int2 r = rows_of(q, s);
+    Pair back = dhT != nullptr ? load_state(dhT + (int64_t)s * D + d) : both(0.f);
+    const int64_t slot = (int64_t)r.x / kChunk + s;
+    Pair before[kChunk];
+    for (int c = (r.y + kChunk - 1) / kChunk - 1; c >= 0; --c) {
+        const int n = min(kChunk, r.y - c * kChunk);
+        const int64_t first = (int64_t)(r.x + c * kChunk) * D + d;
+        Pair h = load_state(states + (slot + c) * D + d);
+        for (int t = 0; t < n; ++t) {
+            before[t] = h;
+            const Decay a = decay<kForm>(load_two(g + first + (int64_t)t * D));
+            h = decayed(a, h, input<kForm>(a, load_two(x + first + (int64_t)t * D)));
+        }
+        for (int t = n - 1; t >= 0; --t) {
+            const int64_t at = first + (int64_t)t * D;
+            const Decay a = decay<kForm>(load_two(g + at));
+            const Pair xt = load_two(x + at), up = load_two(dout + at);
+            Pair dh = up;
+            if (kGate) {
+                Pair slope;
+                dh = up * activation(load_two(gate + at), act, slope);
+                store_two(dgate + at, up * decayed(a, before[t], input<kForm>(a, xt)) * slope);
+            }
+            dh = dh + back;
+            Pair da = leaks(kForm) ? before[t] + xt * both(-1.f) : before[t];
+            da = dh * da * a.a;
+            if (kForm == GLA_SCAN_SIGMOID || kForm == GLA_SCAN_SIGMOID_LEAK) da = da * (a.m * both(-1.f));
+            store_two(dg + at, da);
+            store_two(dx + at, input<kForm>(a, dh));
+            back = decayed(a, dh, both(0.f));
+        }
+    }
+    if (dh0 != nullptr) store_state(dh0 + (int64_t)s * D + d, back);
+}
+
+// One token of N sequences, four channels a thread.
+template <typename T, typename TG, int kForm, bool kGate>
+__global__ void __launch_bounds__(256)
+step_kernel(const T *__restrict__ x, const TG *__restrict__ g, const T *__restrict__ gate, float *__restrict__ state,
+            const int32_t *__restrict__ slots, int nslots, T *__restrict__ out, int64_t total, int D, int act) {
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= total) return;
+    const int64_t n = i * 4 / D, at = i * 4;
+    int64_t page = n;
+    if (slots != nullptr) {
+        page = __ldg(slots + n);
+        if (page >= nslots) {
+            record_status(GLA_ERR_DEVICE_ARG);
+            page = -1;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+        if (page < 0) {
+            store_two(out + at + e, both(0.f));
+            continue;
+        }
+        float *to = state + page * D + (at - n * D) + e;
+        const Decay a = decay<kForm>(load_two(g + at + e));
+        const Pair h = decayed(a, load_state(to), input<kForm>(a, load_two(x + at + e)));
+        store_state(to, h);
+        store_two(out + at + e, kGate ? h * activation(load_two(gate + at + e), act) : h);
+    }
+}
+
+int status() { return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH; }
+
+Sequences plan(const Shape &p, void *ws, cudaStream_t st) {
+    if (p.cu == nullptr) return {p.nseq, p.T, nullptr};
+    plan_kernel<<<1, kPlanThreads, 0, st>>>(p.cu, p.nseq, p.T, (int2 *)ws);
+    count_launches(1);
+    return {p.nseq, p.T, (const int2 *)ws};
+}
+
+void run_fwd(const Shape &p, const void *x, const void *g, const void *gate, const float *h0, void *out, float *hT,
+             float *states, int dtype, int g_dtype, const Sequences &q, cudaStream_t st) {
+    const int parts = (p.D + 2 * kThreads - 1) / (2 * kThreads);
+#define GLA_RUN(T, TG, F, G)                                                                                                \
+    walk_fwd_kernel<T, TG, F, G><<<(unsigned)(p.nseq * parts), kThreads, 0, st>>>(                                          \
+        (const T *)x, (const TG *)g, (const T *)gate, h0, (T *)out, hT, states, q, p.D, p.act, parts)
+    GLA_SCAN_DISPATCH(dtype, g_dtype, gate != nullptr, GLA_RUN)
+#undef GLA_RUN
+    count_launches(1);
+}
+
+}  // namespace
+
+int64_t workspace(int op, const Shape &p) {
+    return rows_bytes(p.nseq, p.cu != nullptr) + (op == GLA_OP_BACKWARD ? states_bytes(p) : 0);
+}
+
+int fwd(const Shape &p, const void *x, const void *g, const void *gate, const float *h0, void *out, float *hT, float *states,
+        int dtype, int g_dtype, void *ws, cudaStream_t st) {
+    const Sequences q = plan(p, ws, st);
+    run_fwd(p, x, g, gate, h0, out, hT, states, dtype, g_dtype, q, st);
+    return status();
+}
+
+int bwd(const Shape &p, const void *x, const void *g, const void *gate, const void *dout, const float *h0, const float *dhT,
+        const float *states, void *dx, void *dg, void *dgate, float *dh0, int dtype, int g_dtype, void *ws, cudaStream_t st) {
+    const Sequences q = plan(p, ws, st);
+    if (states == nullptr) {
+        float *own = reinterpret_cast<float *>((uint8_t *)ws + rows_bytes(p.nseq, p.cu != nullptr));
+        run_fwd(p, x, g, nullptr, h0, nullptr, nullptr, own, dtype, g_dtype, q, st);
+        states = own;
+    }
+    const int parts = (p.D + 2 * kThreads - 1) / (2 * kThreads);
+#define GLA_RUN(T, TG, F, G)                                                                                                \
+    walk_bwd_kernel<T, TG, F, G><<<(unsigned)(p.nseq * parts), kThreads, 0, st>>>(                                          \
+        (const T *)x, (const TG *)g, (const T *)gate, (const T *)dout, dhT, states, (T *)dx, (TG *)dg, (T *)dgate, dh0, q,  \
+        p.D, p.act, parts)
+    GLA_SCAN_DISPATCH(dtype, g_dtype, gate != nullptr, GLA_RUN)
+#undef GLA_RUN
+    count_launches(1);
+    return status();
+}
+
+int step(const void *x, const void *g, const void *gate, float *state, const int32_t *slots, int nslots, void *out, int N,
+         int D, int form, int act, int dtype, int g_dtype, cudaStream_t st) {
+    const int64_t total = (int64_t)N * D / 4;
+    const int64_t blocks = (total + 255) / 256;
+    const Shape p{N, 1, D, form, act, nullptr};
+#define GLA_RUN(T, TG, F, G)                                                                                                \
+    step_kernel<T, TG, F, G><<<(unsigned)blocks, 256, 0, st>>>((const T *)x, (const TG *)g, (const T *)gate, state, slots,  \
+                                                               nslots, (T *)out, total, D, act)
+    GLA_SCAN_DISPATCH(dtype, g_dtype, gate != nullptr, GLA_RUN)
+#undef GLA_RUN
+    count_launches(1);
+    return status();
+}
+
+}  // namespace scan
+}  // namespace gla

@@ -1,0 +1,147 @@
+// gla_scan.cuh — what the kernels of the gated recurrence share.
+//
+//     h_t = a_t h_{t-1} + w_t x_t,   out_t = h_t act(gate_t)
+//
+// on one number a channel, with a_t = exp(g_t) or sigmoid(g_t) and w_t = 1 or 1 - a_t.
+#pragma once
+
+#include "gla_act.cuh"
+#include "gla_seq.cuh"
+
+namespace gla {
+namespace scan {
+
+// Rows of a chunk: the state before each one is what a forward keeps for the gradient.
+constexpr int kChunk = 128;
+
+struct Shape {
+    int nseq, T, D;
+    int form, act;
+    const int32_t *cu;
+};
+__host__ inline int64_t total_rows(const Shape &p) { return p.cu ? (int64_t)p.T : (int64_t)p.nseq * p.T; }
+__host__ inline int64_t slots(const Shape &p) { return chunk_slots(total_rows(p), p.nseq, kChunk); }
+__host__ inline int64_t states_bytes(const Shape &p) { return slots(p) * p.D * (int64_t)sizeof(float); }
+
+// ---- two neighbouring channels of one row ------------------------------------------------------------------------
+template <typename T> struct Two;
+template <> struct Two<__nv_bfloat16> {
+    using Raw = uint32_t;
+    static __device__ __forceinline__ Pair open(Raw w) {
+        return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    static __device__ __forceinline__ Raw close(Pair x) {
+        const float2 f = parts(x);
+        const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+};
+template <> struct Two<float> {
+    using Raw = float2;
+    static __device__ __forceinline__ Pair open(Raw w) { return pair(w.x, w.y); }
+    static __device__ __forceinline__ Raw close(Pair x) { return parts(x); }
+};
+template <typename T> __device__ __forceinline__ Pair load_two(const T *p) {
+    return Two<T>::open(__ldg(reinterpret_cast<const typename Two<T>::Raw *>(p)));
+}
+template <typename T> __device__ __forceinline__ void store_two(T *p, Pair x) {
+    *reinterpret_cast<typename Two<T>::Raw *>(p) = Two<T>::close(x);
+}
+__device__ __forceinline__ Pair load_state(const float *p) {
+    const float2 f = *reinterpret_cast<const float2 *>(p);
+    return pair(f.x, f.y);
+}
+__device__ __forceinline__ void store_state(float *p, Pair x) { *reinterpret_cast<float2 *>(p) = parts(x); }
+
+// ---- the decay ---------------------------------------------------------------------------------------------------
+//
+// Long memories need 1 - a more than a: an a of 1 - 1e-4 that is rounded to 2^-25 has 3e-4 of its decay rounded away, and
+// all tokens' alike where g is.  So the decay is held as m = a - 1 where it is near 1, good to a few units of its own last
+// place, and h a is h + m h in one rounding; elsewhere a itself is, so that a strong decay keeps its digits too.
+struct Decay {
+    Pair a, m;      // a, and a - 1
+    bool lo, hi;    // for either channel, whether a is near 1
+};
+
+template <int kForm>
+__device__ __forceinline__ Decay decay(Pair g) {
+    Decay d;
+    const float2 f = parts(g);
+    if (kForm == GLA_SCAN_LOG || kForm == GLA_SCAN_LOG_LEAK) {
+        float a0, a1;
+        const float2 t = parts(g * both(1.4426950408889634f));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a0) : "f"(t.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a1) : "f"(t.y));
+        d.a = pair(a0, a1);
+        // e^g - 1 by its series: behind g^6 / 6! the next term is below 2^-24 of the sum for |g| < 0.25
+        Pair s = fma(g, both(1.f / 720.f), both(1.f / 120.f));
+        s = fma(g, s, both(1.f / 24.f));
+        s = fma(g, s, both(1.f / 6.f));
+        s = fma(g, s, both(0.5f));
+        s = fma(g, s, both(1.f));
+        const float2 m = parts(s * g);
+        d.lo = fabsf(f.x) < 0.25f;
+        d.hi = fabsf(f.y) < 0.25f;
+        d.m = pair(d.lo ? m.x : a0 - 1.f, d.hi ? m.y : a1 - 1.f);
+    } else {
+        Pair rest;
+        sigmoid(g, d.a, rest);
+        d.m = rest * both(-1.f);
+        d.lo = f.x > 1.f;
+        d.hi = f.y > 1.f;
+    }
+    return d;
+}
+__host__ __device__ constexpr bool leaks(int form) { return form == GLA_SCAN_LOG_LEAK || form == GLA_SCAN_SIGMOID_LEAK; }
+
+// a h + b
+__device__ __forceinline__ Pair decayed(const Decay &d, Pair h, Pair b) {
+    const float2 a = parts(d.a), m = parts(d.m), f = parts(h);
+    const Pair c = pair(d.lo ? m.x : a.x, d.hi ? m.y : a.y);
+    const Pair base = pair(d.lo ? f.x : 0.f, d.hi ? f.y : 0.f);
+    return fma(c, h, base) + b;
+}
+// the input's part of h
+template <int kForm>
+__device__ __forceinline__ Pair input(const Decay &d, Pair x) {
+    return leaks(kForm) ? x * (d.m * both(-1.f)) : x;
+}
+
+// act(x) and its slope
+__device__ __forceinline__ Pair activation(Pair x, int act) {
+    if (act == kNone) return x;
+    Pair q, rest;
+    sigmoid(x, q, rest);
+    return act == kSilu ? x * q : q;
+}
+__device__ __forceinline__ Pair activation(Pair x, int act, Pair &slope) {
+    slope = both(1.f);
+    if (act == kNone) return x;
+    Pair q, rest;
+    sigmoid(x, q, rest);
+    slope = act == kSilu ? q * fma(x, rest, both(1.f)) : q * rest;
+    return act == kSilu ? x * q : q;
+}
+
+// Calls RUN(T, TG, kForm, kGate) for a call's types, form and gate.
+#define GLA_SCAN_BY_FORM(T, TG, G, RUN)                                   \
+    switch (p.form) {                                                     \
+        case GLA_SCAN_LOG: RUN(T, TG, GLA_SCAN_LOG, G); break;            \
+        case GLA_SCAN_LOG_LEAK: RUN(T, TG, GLA_SCAN_LOG_LEAK, G); break;  \
+        case GLA_SCAN_SIGMOID: RUN(T, TG, GLA_SCAN_SIGMOID, G); break;    \
+        default: RUN(T, TG, GLA_SCAN_SIGMOID_LEAK, G); break;             \
+    }
+#define GLA_SCAN_DISPATCH(dtype, g_dtype, gated, RUN)                                                            \
+    if (dtype == GLA_F32) {                                                                                      \
+        if (gated) { GLA_SCAN_BY_FORM(float, float, true, RUN) }                                                 \
+        else { GLA_SCAN_BY_FORM(float, float, false, RUN) }                                                      \
+    } else if (g_dtype == GLA_F32) {                                                                             \
+        if (gated) { GLA_SCAN_BY_FORM(__nv_bfloat16, float, true, RUN) }                                         \
+        else { GLA_SCAN_BY_FORM(__nv_bfloat16, float, false, RUN) }                                              \
+    } else {                                                                                                     \
+        if (gated) { GLA_SCAN_BY_FORM(__nv_bfloat16, __nv_bfloat16, true, RUN) }                                 \
+        else { GLA_SCAN_BY_FORM(__nv_bfloat16, __nv_bfloat16, false, RUN) }                                      \
+    }
+
+}  // namespace scan
+}  // namespace gla

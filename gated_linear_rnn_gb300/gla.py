@@ -53,6 +53,11 @@ SIGNATURES = {
     "gla_group_norm": ([_P, _P, _P, _P, _I, _F, _P, _L, _I, _I, _I, _P], _I),
     "gla_group_norm_workspace_bytes": ([_L, _I, _I], _L),
     "gla_group_norm_bwd": ([_P, _P, _P, _P, _P, _I, _F, _P, _P, _P, _P, _L, _I, _I, _I, _P, _L, _P], _I),
+    "gla_scan_workspace_bytes": ([_I] * 5, _L),
+    "gla_scan_states_bytes": ([_I] * 4, _L),
+    "gla_scan_fwd": ([_P] * 7 + [_I] * 7 + [_P, _P, _L, _P], _I),
+    "gla_scan_bwd": ([_P] * 11 + [_I] * 7 + [_P, _P, _L, _P], _I),
+    "gla_scan_step": ([_P] * 5 + [_I, _P] + [_I] * 6 + [_P], _I),
     "gla_last_device_status": ([_P], _I),
     "gla_status_str": ([_I], ctypes.c_char_p),
     "gla_chunk_kernel": ([_I, _I, _I, _I, _I], _I),
@@ -646,6 +651,103 @@ def gla_group_norm_bwd(dout, x, weight, bias, groups: int, dx, dweight, dbias, d
     _raise(rc, "gla_group_norm_bwd")
 
 
+# ---- gated recurrence -------------------------------------------------------------------------------
+
+SCAN_LOG, SCAN_LOG_LEAK, SCAN_SIGMOID, SCAN_SIGMOID_LEAK = 0, 1, 2, 3  # gla_scan_form
+
+
+def _scan_types(x, g):
+    dtype, gates = _dtype(x, "x"), _dtype(g, "g")
+    if gates != F32 and gates != dtype:
+        raise ValueError("g must be torch.float32 or of the type of x")
+    return dtype, gates
+
+
+def _scan_args(x, g, gate, h0, out, hT, cu_seqlens):
+    """Checks shared by gla_scan_fwd and gla_scan_bwd; returns the pointers, the sizes and types, and the offsets."""
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, D] (packed: [1, T, D])")
+    B, T, D = x.shape
+    types = _scan_types(x, g)
+    at = _device(x, "x")
+    nseq, cu = B, None
+    if cu_seqlens is not None:
+        if B != 1:
+            raise ValueError("a packed batch has leading dimension 1")
+        nseq, cu = cu_seqlens.numel() - 1, _arg(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, at)
+    t, s, hs = x.dtype, x.shape, (nseq, D)
+    ptrs = (_arg(x, "x", t, s, at), _arg(g, "g", g.dtype, s, at), _arg(gate, "gate", t, s, at, True),
+            _arg(h0, "h0", torch.float32, hs, at, True), _arg(out, "out", t, s, at),
+            _arg(hT, "hT", torch.float32, hs, at, True))
+    return ptrs, (nseq, T, D), types, cu
+
+
+def gla_scan_workspace_bytes(op: int, B: int, T: int, D: int, packed: bool) -> int:
+    """Workspace bytes of gla_scan_fwd (OP_FORWARD) or gla_scan_bwd (OP_BACKWARD)."""
+    n = load().gla_scan_workspace_bytes(int(op), int(B), int(T), int(D), int(bool(packed)))
+    if n < 0:
+        raise GLAError(n, "gla_scan_workspace_bytes")
+    return n
+
+
+def gla_scan_states_bytes(B: int, T: int, D: int, packed: bool) -> int:
+    """Bytes of the states that gla_scan_fwd keeps for gla_scan_bwd."""
+    n = load().gla_scan_states_bytes(int(B), int(T), int(D), int(bool(packed)))
+    if n < 0:
+        raise GLAError(n, "gla_scan_states_bytes")
+    return n
+
+
+def _scan_states(states, sizes, packed, device):
+    if states is None:
+        return None
+    return _arg(states, "states", torch.float32, (gla_scan_states_bytes(*sizes, packed) // 4,), device)
+
+
+def gla_scan_fwd(x, g, form: int, h0, out, hT, gate=None, act: int = ACT_SILU, states=None, cu_seqlens=None,
+                 workspace=None, stream=None) -> None:
+    """Gated recurrence over whole sequences: writes ``out`` and (if given) ``hT`` and ``states``.  See include/gla.h."""
+    p, sizes, types, cu = _scan_args(x, g, gate, h0, out, hT, cu_seqlens)
+    kept = _scan_states(states, sizes, cu is not None, x.get_device())
+    ws, ws_at, n = _workspace(workspace, gla_scan_workspace_bytes(OP_FORWARD, *sizes, cu is not None), x.device, stream)
+    rc = load().gla_scan_fwd(*p, kept, *sizes, form, act, *types, cu, ws_at, n, _raw_stream(stream, x.device))
+    _raise(rc, "gla_scan_fwd")
+
+
+def gla_scan_bwd(x, g, form: int, dout, h0, dhT, dx, dg, dh0, gate=None, dgate=None, act: int = ACT_SILU, states=None,
+                 cu_seqlens=None, workspace=None, stream=None) -> None:
+    """Gradients of gla_scan_fwd: writes dx, dg, (with a gate) dgate and (if given) dh0.  See include/gla.h."""
+    p, sizes, types, cu = _scan_args(x, g, gate, h0, dout, dhT, cu_seqlens)
+    at, t = x.get_device(), x.dtype
+    if gate is None and dgate is not None:
+        raise ValueError("dgate without a gate")
+    grads = (_arg(dx, "dx", t, x.shape, at), _arg(dg, "dg", g.dtype, x.shape, at),
+             _arg(dgate, "dgate", t, x.shape, at, gate is None),
+             _arg(dh0, "dh0", torch.float32, (sizes[0], sizes[2]), at, True))
+    kept = _scan_states(states, sizes, cu is not None, at)
+    ws, ws_at, n = _workspace(workspace, gla_scan_workspace_bytes(OP_BACKWARD, *sizes, cu is not None), x.device, stream)
+    rc = load().gla_scan_bwd(p[0], p[1], p[2], p[4], p[3], p[5], kept, *grads, *sizes, form, act, *types, cu, ws_at, n,
+                             _raw_stream(stream, x.device))
+    _raise(rc, "gla_scan_bwd")
+
+
+def gla_scan_step(x, g, form: int, state, out, gate=None, act: int = ACT_SILU, slots=None, stream=None) -> None:
+    """One token of the gated recurrence for N sequences, in place on ``state`` [N, D], or with ``slots`` on pages of a
+    pool [nslots, D] (negative slot: padding row, zero out).  See include/gla.h."""
+    if x.dim() != 2 or state.dim() != 2:
+        raise ValueError("x must be [N, D] and state [.., D]")
+    N, D = x.shape
+    types = _scan_types(x, g)
+    t, s, at = x.dtype, x.shape, _device(x, "x")
+    pages = state.shape[0] if slots is not None else N
+    rc = load().gla_scan_step(
+        _arg(x, "x", t, s, at), _arg(g, "g", g.dtype, s, at), _arg(gate, "gate", t, s, at, True),
+        _arg(state, "state", torch.float32, (pages, D), at), _arg(slots, "slots", torch.int32, (N,), at, True), pages,
+        _arg(out, "out", t, s, at), N, D, form, act, *types, _raw_stream(stream, x.device))
+    if rc:
+        raise GLAError(rc, "gla_scan_step")
+
+
 def gla_last_device_status(stream=None) -> int:
     """Synchronise the stream; return and clear the library's device status word."""
     return int(load().gla_last_device_status(_stream(stream)))
@@ -755,3 +857,40 @@ def group_norm_bwd(dout, x, weight, bias, groups: int, gate=None, act: int = ACT
         dweight, dbias = (torch.empty(x.shape[-1], dtype=torch.float32, device=x.device) for _ in range(2))
     gla_group_norm_bwd(dout, x, weight, bias, groups, dx, dweight, dbias, dgate, gate, act, eps, None, stream)
     return dx, dweight, dbias, dgate
+
+
+def scan_states(x, cu_seqlens=None):
+    """Allocate the states that scan_fwd keeps for scan_bwd, for inputs like ``x``."""
+    nseq = x.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+    n = gla_scan_states_bytes(nseq, x.shape[1], x.shape[2], cu_seqlens is not None) // 4
+    return torch.empty(n, dtype=torch.float32, device=x.device)
+
+
+def scan_fwd(x, g, form: int, gate=None, act: int = ACT_SILU, h0=None, cu_seqlens=None, final_state: bool = True,
+             states=None, stream=None):
+    """Allocate ``out`` (and ``hT``) and run the gated recurrence; returns (out, hT or None).  ``states``: from
+    scan_states, to be kept for scan_bwd."""
+    nseq = x.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+    with _allocating_on(stream, x.device):
+        out = torch.empty_like(x)
+        hT = torch.empty((nseq, x.shape[-1]), dtype=torch.float32, device=x.device) if final_state else None
+    gla_scan_fwd(x, g, form, h0, out, hT, gate, act, states, cu_seqlens, None, stream)
+    return out, hT
+
+
+def scan_bwd(x, g, form: int, dout, gate=None, act: int = ACT_SILU, h0=None, dhT=None, states=None, cu_seqlens=None,
+             stream=None):
+    """Allocate and return (dx, dg, dgate, dh0) of the gated recurrence; dgate is None without a gate, dh0 without h0."""
+    with _allocating_on(stream, x.device):
+        dx, dg = torch.empty_like(x), torch.empty_like(g)
+        dgate, dh0 = None if gate is None else torch.empty_like(gate), None if h0 is None else torch.empty_like(h0)
+    gla_scan_bwd(x, g, form, dout, h0, dhT, dx, dg, dh0, gate, dgate, act, states, cu_seqlens, None, stream)
+    return dx, dg, dgate, dh0
+
+
+def scan_step(x, g, form: int, state, gate=None, act: int = ACT_SILU, slots=None, stream=None):
+    """Run one step of the gated recurrence in place on ``state`` (or on pages ``slots`` of it); returns the new ``out``."""
+    with _allocating_on(stream, x.device):
+        out = torch.empty_like(x)
+    gla_scan_step(x, g, form, state, out, gate, act, slots, stream)
+    return out

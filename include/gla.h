@@ -552,6 +552,77 @@ GLA_API int gla_group_norm_bwd(const void *dout, const void *x, const float *wei
                                long long ws_bytes, void *stream);
 
 /*
+ * The gated recurrence: one number per sequence and channel,
+ *     h_t = a_t h_{t-1} + w_t x_t,   out_t = h_t, or h_t act(gate_t) with a gate (act: a gla_act)
+ * with a decay a_t of its own for every token and channel, by form:
+ *     GLA_SCAN_LOG           a = exp(g),      w = 1          GLA_SCAN_LOG_LEAK      a = exp(g),      w = 1 - a
+ *     GLA_SCAN_SIGMOID       a = sigmoid(g),  w = 1          GLA_SCAN_SIGMOID_LEAK  a = sigmoid(g),  w = 1 - a
+ * A log decay is at most 0 where the recurrence is to be stable.  g = -inf is a full reset of a finite state; a sigmoid's
+ * g = +inf keeps it (and a leaking one then takes nothing of x).
+ *
+ * x, g, gate and out are [B, T, D], or packed [1, T, D] with cu_seqlens (then B is the number of sequences); states and
+ * their gradients [B, D] f32.
+ *   dtype    GLA_BF16 or GLA_F32: x, gate, out and their gradients
+ *   g_dtype  GLA_F32, or dtype: g and its gradient
+ *   D % 8 == 0; all rows together below 2^31 - 256
+ * States, decays and sums are f32; a decay near 1 is held as its distance from 1.  Results are rounded once.  A sequence's
+ * results do not depend on what else is in the batch, as long as the batch's sizes (B, T, D) are the same.  A NaN or an
+ * infinity reaches what the formulas carry it to, and in its own channel and sequence also other tokens of its chunk of 128
+ * where a decay or a product of decays is 0 (0 times it is a NaN).  It reaches no other channel or sequence.
+ */
+typedef enum { GLA_SCAN_LOG = 0, GLA_SCAN_LOG_LEAK = 1, GLA_SCAN_SIGMOID = 2, GLA_SCAN_SIGMOID_LEAK = 3 } gla_scan_form;
+
+/*
+ * gla_scan_workspace_bytes — bytes of the workspace that gla_scan_fwd (op GLA_OP_FORWARD) or gla_scan_bwd (op
+ * GLA_OP_BACKWARD) needs for these sizes (packed: nonzero with cu_seqlens), 0 if none; gla_scan_states_bytes — bytes of the
+ * states that a forward may keep for its gradient.  Negative: a gla_status for sizes that the calls reject.  The caller owns
+ * both (device, 16-byte aligned); the workspace may be used for anything else once the call's work on its stream is done.
+ */
+GLA_API long long gla_scan_workspace_bytes(int op, int B, int T, int D, int packed);
+GLA_API long long gla_scan_states_bytes(int B, int T, int D, int packed);
+
+/*
+ * gla_scan_fwd — the gated recurrence over whole sequences (prefill, training forward).
+ *   gate        like x, or NULL (act is then not used)
+ *   h0, hT      initial state or NULL (zeros); final state, written, or NULL to skip
+ *   states      gla_scan_states_bytes bytes, written, for gla_scan_bwd; NULL to skip
+ *   cu_seqlens  NULL, or a DEVICE int32 [B+1] of offsets, as gla_delta_chunk_fwd: an empty sequence gets hT = h0; bad
+ *               ones are taken as empty and GLA_ERR_DEVICE_ARG recorded, the others are what they are without them
+ *   ws, ws_bytes  at least gla_scan_workspace_bytes(GLA_OP_FORWARD, ...) bytes (else GLA_ERR_ARG); NULL where that is 0
+ * Rows of a packed batch that are no sequence's are not written.  Returns a gla_status.
+ */
+GLA_API int gla_scan_fwd(const void *x, const void *g, const void *gate, const float *h0, void *out, float *hT,
+                         float *states, int B, int T, int D, int form, int act, int dtype, int g_dtype,
+                         const int32_t *cu_seqlens, void *ws, long long ws_bytes, void *stream);
+
+/*
+ * gla_scan_bwd — its gradients, with L = sum(dout .* out) + sum(dhT .* hT).  Backwards in time from D_T = dhT:
+ *     dh_t = dout_t act(gate_t) + D_t,  D_{t-1} = a_t dh_t,  dh0 = D_0,  dx_t = w_t dh_t,  dgate_t = dout_t h_t act'(gate_t),
+ *     da_t = dh_t (h_{t-1} - x_t) where the input leaks, else dh_t h_{t-1},  dg_t = da_t a_t (1 - a_t for a sigmoid, else 1)
+ *   dhT         [B, D] f32 or NULL (zeros);  states: what the forward with the same x, g, h0, sizes and offsets wrote, or NULL
+ *               (they are then computed again, for one more pass over x and g, from h0)
+ *   dx, dgate   like x (dgate with a gate, else NULL);  dg like g;  dh0 [B, D] f32, NULL to skip: written
+ *   ws, ws_bytes  at least gla_scan_workspace_bytes(GLA_OP_BACKWARD, ...) bytes
+ * Rows of a packed batch that are no sequence's are not written.  No array may alias another.  Returns a gla_status.
+ */
+GLA_API int gla_scan_bwd(const void *x, const void *g, const void *gate, const void *dout, const float *h0,
+                         const float *dhT, const float *states, void *dx, void *dg, void *dgate, float *dh0, int B, int T,
+                         int D, int form, int act, int dtype, int g_dtype, const int32_t *cu_seqlens, void *ws,
+                         long long ws_bytes, void *stream);
+
+/*
+ * gla_scan_step — one token of N sequences, in place on their states.
+ *   x, g, gate, out  [N, D] (out written; gate may be NULL)
+ *   state       [N, D] f32; with slots: a pool [nslots, D] of pages, as gla_delta_decode_step (a negative slot is a padding
+ *               row: zero out, no page touched; >= nslots: the same, and GLA_ERR_DEVICE_ARG is recorded).  Two rows must
+ *               not name the same page
+ *   N = 0 does nothing
+ * Makes no allocation or synchronisation: it can be captured in a CUDA graph.  Returns a gla_status.
+ */
+GLA_API int gla_scan_step(const void *x, const void *g, const void *gate, float *state, const int32_t *slots, int nslots,
+                          void *out, int N, int D, int form, int act, int dtype, int g_dtype, void *stream);
+
+/*
  * gla_last_device_status — synchronise `stream`, then return and clear the
  * device status word: GLA_OK, GLA_ERR_TIMEOUT or GLA_ERR_DEVICE_ARG for the
  * first failure recorded by any kernel of this library on the current device

@@ -1,0 +1,59 @@
+"""The checks of the gated recurrence's entry points that need no device."""
+import ctypes
+
+import pytest
+
+from gated_linear_rnn_gb300 import build as B
+from gated_linear_rnn_gb300 import gla
+
+FAKE, ODD = ctypes.c_void_p(4096), ctypes.c_void_p(4096 + 8)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build_library()
+    return gla.load()
+
+
+def fwd(lib, x=FAKE, g=FAKE, gate=None, out=FAKE, B=1, T=8, D=64, form=0, act=1, dtype=0, g_dtype=1, cu=None, ws=None, n=0):
+    return lib.gla_scan_fwd(x, g, gate, None, out, None, None, B, T, D, form, act, dtype, g_dtype, cu, ws, n, None)
+
+
+def test_forward_refuses(lib):
+    assert fwd(lib, x=None) == fwd(lib, g=None) == fwd(lib, out=None) == -1
+    assert fwd(lib, B=0) == fwd(lib, T=-1) == fwd(lib, D=0) == -1
+    assert fwd(lib, form=4) == fwd(lib, form=-1) == fwd(lib, act=3) == fwd(lib, dtype=2) == -1
+    assert fwd(lib, dtype=1, g_dtype=0) == -1  # bf16 decays beside f32 inputs
+    assert fwd(lib, D=60) == -2
+    assert fwd(lib, B=1 << 20, T=1 << 12) == -2  # more rows than 2^31 - 256
+    assert fwd(lib, x=ODD) == fwd(lib, g=ODD) == fwd(lib, gate=ODD) == fwd(lib, out=ODD) == fwd(lib, cu=ODD) == -3
+
+
+def test_backward_refuses(lib):
+    def bwd(dx=FAKE, dg=FAKE, gate=None, dgate=None, dout=FAKE):
+        return lib.gla_scan_bwd(FAKE, FAKE, gate, dout, None, None, None, dx, dg, dgate, None, 1, 8, 64, 0, 1, 0, 1, None, None,
+                                0, None)
+    assert bwd(dout=None) == -1
+    # with a device of another kind, or none, the last check refuses every call
+    assert {bwd(dx=None), bwd(dg=None), bwd(gate=FAKE), bwd(dgate=FAKE), bwd()} <= {-1, -2}
+
+
+def test_step_refuses(lib):
+    def step(x=FAKE, g=FAKE, gate=None, state=FAKE, slots=None, nslots=0, out=FAKE, N=1, D=64, form=0, act=1):
+        return lib.gla_scan_step(x, g, gate, state, slots, nslots, out, N, D, form, act, 0, 1, None)
+    assert step(x=None) == step(g=None) == step(state=None) == step(out=None) == -1
+    assert step(N=-1) == step(D=0) == step(slots=FAKE) == step(form=4) == step(act=-1) == -1
+    assert step(D=12) == -2
+    assert step(x=ODD) == step(gate=ODD) == step(state=ODD) == step(slots=ODD, nslots=1) == -3
+    assert step(N=0, x=None) == 0
+
+
+def test_sizes(lib):
+    assert lib.gla_scan_workspace_bytes(3, 1, 8, 64, 0) == lib.gla_scan_workspace_bytes(0, 0, 8, 64, 0) == -1
+    assert lib.gla_scan_workspace_bytes(0, 1, 8, 60, 0) == lib.gla_scan_states_bytes(1, 8, 60, 0) == -2
+    assert lib.gla_scan_workspace_bytes(0, 1 << 20, 1 << 12, 64, 0) == -2
+    # a state before every 128 tokens of every sequence
+    assert gla.gla_scan_states_bytes(3, 300, 64, False) >= 3 * 3 * 64 * 4
+    assert gla.gla_scan_workspace_bytes(gla.OP_BACKWARD, 3, 300, 64, False) >= gla.gla_scan_states_bytes(3, 300, 64, False)
+    with pytest.raises(gla.GLAError):
+        gla.gla_scan_states_bytes(1, 8, 60, False)
