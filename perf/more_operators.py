@@ -388,7 +388,7 @@ def _run_own(s):
         block = dict(kind=kind, gate=s["gate"], act=act, scale=s["scale"], post=c["post"], post_weight=s["post_weight"],
                      post_bias=s["post_bias"], eps=EPS)
         if c["op"] == "norm":
-            r, out = gla.residual_norm(s["x"], s["y"], s["weight"], s["bias"], **block)
+            r, out = gla.residual_norm(s["x"], s["y"], s["weight"], s["bias"], dtype=_dtype(c), **block)
             return [r, out] if c["y"] else [out]
         got = gla.residual_norm_bwd(s["dr"], s["dout"], s["x"], s["y"], s["weight"], s["bias"], **block)
         return [t for t in (got.dx, got.dweight, got.dbias, got.dscale, got.dgate, got.dpost_weight, got.dpost_bias, got.dy)
