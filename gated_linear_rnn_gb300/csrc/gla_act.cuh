@@ -26,4 +26,20 @@ __device__ __forceinline__ void sigmoid(Pair x, Pair &q, Pair &rest) {
     rest = pair(f.x < -20.f ? 1.f : r.x, f.y < -20.f ? 1.f : r.y);
 }
 
+// act(x), a gate's factor, and its slope
+__device__ __forceinline__ Pair activation(Pair x, int act) {
+    if (act == kNone) return x;
+    Pair q, rest;
+    sigmoid(x, q, rest);
+    return act == kSilu ? x * q : q;
+}
+__device__ __forceinline__ Pair activation(Pair x, int act, Pair &slope) {
+    slope = both(1.f);
+    if (act == kNone) return x;
+    Pair q, rest;
+    sigmoid(x, q, rest);
+    slope = act == kSilu ? q * fma(x, rest, both(1.f)) : q * rest;
+    return act == kSilu ? x * q : q;
+}
+
 }  // namespace gla

@@ -95,6 +95,20 @@ int bwd(const Shape &, const void *, const void *, const void *, const void *, c
 int step(const void *, const void *, const void *, float *, const int32_t *, int, void *, int, int, int, int, int, int,
          cudaStream_t);
 }  // namespace scan
+namespace resnorm {
+int64_t workspace(int64_t, int);
+int fwd(const void *, const void *, const void *, const float *, const float *, const float *, const float *, const float *,
+        int, int, int, float, void *, void *, int64_t, int, int, int, cudaStream_t);
+int bwd(const void *, const void *, const void *, const void *, const void *, const float *, const float *, const float *,
+        const float *, int, int, int, float, void *, void *, void *, float *, float *, float *, float *, float *, int64_t, int,
+        int, int, void *, cudaStream_t);
+}  // namespace resnorm
+namespace convbwd {
+int64_t workspace(int, int, int, bool);
+int bwd(const void *, const void *, const float *, const float *, const float *, const float *, void *, float *, float *, float *,
+        int, int, int, int, const int32_t *, void *, cudaStream_t);
+}  // namespace convbwd
+int take_status_conv_bwd(cudaStream_t);
 int take_status_scan(cudaStream_t);
 int take_status_delta(cudaStream_t);
 int take_status_delta_mma(cudaStream_t);
@@ -285,6 +299,34 @@ int check_scan(const void *x, const void *g, const void *gate, const float *h0, 
         !aligned16(states) || !aligned16(cu) || !aligned16(ws))
         return GLA_ERR_ALIGN;
     if (!device_info().ok) return GLA_ERR_UNSUPPORTED;
+    return GLA_OK;
+}
+
+int check_conv_bwd_sizes(int B, int T, int D, int packed) {
+    if (B <= 0 || T < 0 || D <= 0) return GLA_ERR_ARG;
+    const long long rows = packed ? (long long)T : (long long)B * T;
+    // rows are 32-bit, and slabs of 128 channels a dimension of the grid
+    if (D % 8 || rows > 0x7fffff00LL || D > 65535 * 128) return GLA_ERR_UNSUPPORTED;
+    return GLA_OK;
+}
+
+// What both residual norm calls have: y's parts only with y, the norm's parameters only with its output.
+int check_resnorm(const void *y, const void *gate, const float *scale, const float *post_weight, const float *post_bias,
+                  const float *weight, const float *bias, bool normed, int kind, int post, int act, float eps, long long rows,
+                  int D, int dtype, int stream_dtype) {
+    if (dtype != GLA_BF16 && dtype != GLA_F32) return GLA_ERR_ARG;
+    if (stream_dtype != GLA_F32 && stream_dtype != dtype) return GLA_ERR_ARG;
+    if (kind != GLA_NORM_LAYER && kind != GLA_NORM_RMS) return GLA_ERR_ARG;
+    if (act != GLA_ACT_NONE && act != GLA_ACT_SILU && act != GLA_ACT_SIGMOID) return GLA_ERR_ARG;
+    if (rows < 0 || D <= 0 || !(eps > 0.f)) return GLA_ERR_ARG;
+    if (!normed && (weight || bias)) return GLA_ERR_ARG;
+    if (!post && (post_weight || post_bias)) return GLA_ERR_ARG;
+    // an empty tensor has no address: without rows an absent y is not told from a present one
+    if (rows > 0 && !y && (gate || scale || post)) return GLA_ERR_ARG;
+    if (D % 8 || D > 16384 || rows > (1LL << 40)) return GLA_ERR_UNSUPPORTED;
+    if (!aligned16(y) || !aligned16(gate) || !aligned16(scale) || !aligned16(post_weight) || !aligned16(post_bias) ||
+        !aligned16(weight) || !aligned16(bias))
+        return GLA_ERR_ALIGN;
     return GLA_OK;
 }
 
@@ -498,6 +540,28 @@ int gla_conv1d_silu_step(const void *x, const float *weight, const float *bias, 
     return conv1d_silu_step_bf16(x, weight, bias, state_inout, y, N, D, (cudaStream_t)stream);
 }
 
+long long gla_conv1d_silu_bwd_workspace_bytes(int B, int T, int D, int packed) {
+    int rc = check_conv_bwd_sizes(B, T, D, packed);
+    return rc ? rc : (long long)convbwd::workspace(B, T, D, packed != 0);
+}
+
+int gla_conv1d_silu_bwd(const void *dy, const void *x, const float *weight, const float *bias, const float *state_in,
+                        const float *dstate_out, void *dx, float *dweight, float *dbias, float *dstate_in, int B, int T, int D,
+                        int dtype, const int32_t *cu_seqlens, void *ws, long long ws_bytes, void *stream) {
+    if (dtype != GLA_BF16 && dtype != GLA_F32) return GLA_ERR_ARG;
+    int rc = check_conv_bwd_sizes(B, T, D, cu_seqlens != nullptr);
+    if (rc) return rc;
+    if (!weight || (T > 0 && (!dy || !x || !dx))) return GLA_ERR_ARG;
+    if (!ws || ws_bytes < (long long)convbwd::workspace(B, T, D, cu_seqlens != nullptr)) return GLA_ERR_ARG;
+    if (!aligned16(dy) || !aligned16(x) || !aligned16(weight) || !aligned16(bias) || !aligned16(state_in) ||
+        !aligned16(dstate_out) || !aligned16(dx) || !aligned16(dweight) || !aligned16(dbias) || !aligned16(dstate_in) ||
+        !aligned16(cu_seqlens) || !aligned16(ws))
+        return GLA_ERR_ALIGN;
+    if (!device_info().ok) return GLA_ERR_UNSUPPORTED;
+    return convbwd::bwd(dy, x, weight, bias, state_in, dstate_out, dx, dweight, dbias, dstate_in, B, T, D, dtype, cu_seqlens, ws,
+                        (cudaStream_t)stream);
+}
+
 long long gla_delta_workspace_bytes(int op, int B, int T, int H, int Hk, int dk, int dv, int dtype, int packed) {
     if (op != GLA_OP_FORWARD && op != GLA_OP_BACKWARD) return GLA_ERR_ARG;
     int rc = check_delta_sizes(B, T, H, Hk, dk, dv, dtype, packed);
@@ -644,12 +708,53 @@ int gla_scan_step(const void *x, const void *g, const void *gate, float *state, 
     return scan::step(x, g, gate, state, slots, nslots, out, N, D, form, act, dtype, g_dtype, (cudaStream_t)stream);
 }
 
+int gla_residual_norm(const void *x, const void *y, const void *gate, const float *scale, const float *post_weight,
+                      const float *post_bias, const float *weight, const float *bias, int kind, int post, int act, float eps,
+                      void *r, void *out, long long rows, int D, int dtype, int stream_dtype, void *stream) {
+    int rc = check_resnorm(y, gate, scale, post_weight, post_bias, weight, bias, out != nullptr || rows == 0, kind, post, act,
+                           eps, rows, D, dtype, stream_dtype);
+    if (rc) return rc;
+    if (rows > 0 && (!x || (y != nullptr) != (r != nullptr) || (!y && !out))) return GLA_ERR_ARG;
+    if (!aligned16(x) || !aligned16(r) || !aligned16(out)) return GLA_ERR_ALIGN;
+    if (!device_info().ok) return GLA_ERR_UNSUPPORTED;
+    return resnorm::fwd(x, y, gate, scale, post_weight, post_bias, weight, bias, kind, post, act, eps, r, out, rows, D, dtype,
+                        stream_dtype, (cudaStream_t)stream);
+}
+
+long long gla_residual_norm_workspace_bytes(long long rows, int D) {
+    if (rows < 0 || D <= 0) return GLA_ERR_ARG;
+    if (D % 8 || D > 16384 || rows > (1LL << 40)) return GLA_ERR_UNSUPPORTED;
+    return (long long)resnorm::workspace(rows, D);
+}
+
+int gla_residual_norm_bwd(const void *dr, const void *dout, const void *r, const void *y, const void *gate, const float *scale,
+                          const float *post_weight, const float *post_bias, const float *weight, int kind, int post, int act,
+                          float eps, void *dx, void *dy, void *dgate, float *dscale, float *dpost_weight, float *dpost_bias,
+                          float *dweight, float *dbias, long long rows, int D, int dtype, int stream_dtype, void *ws,
+                          long long ws_bytes, void *stream) {
+    int rc = check_resnorm(y, gate, scale, post_weight, post_bias, weight, nullptr, dout != nullptr || rows == 0, kind, post, act,
+                           eps, rows, D, dtype, stream_dtype);
+    if (rc) return rc;
+    if (rows > 0 && (!r || !dx || (!dr && !dout) || (y != nullptr) != (dy != nullptr) || (gate != nullptr) != (dgate != nullptr)))
+        return GLA_ERR_ARG;
+    if ((dscale && !scale) || ((dpost_weight || dpost_bias) && !post) || (rows > 0 && !dout && (dweight || dbias)))
+        return GLA_ERR_ARG;
+    if (!ws || ws_bytes < (long long)resnorm::workspace(rows, D)) return GLA_ERR_ARG;
+    if (!aligned16(dr) || !aligned16(dout) || !aligned16(r) || !aligned16(dx) || !aligned16(dy) || !aligned16(dgate) ||
+        !aligned16(dscale) || !aligned16(dpost_weight) || !aligned16(dpost_bias) || !aligned16(dweight) || !aligned16(dbias) ||
+        !aligned16(ws))
+        return GLA_ERR_ALIGN;
+    if (!device_info().ok) return GLA_ERR_UNSUPPORTED;
+    return resnorm::bwd(dr, dout, r, y, gate, scale, post_weight, post_bias, weight, kind, post, act, eps, dx, dy, dgate, dscale,
+                        dpost_weight, dpost_bias, dweight, dbias, rows, D, dtype, stream_dtype, ws, (cudaStream_t)stream);
+}
+
 int gla_last_device_status(void *stream) {
     cudaStream_t st = (cudaStream_t)stream;
     int result = GLA_OK;
     const int parts[] = {take_status_simt(st), take_status_decode(st), take_status_tc(st), take_status_bwd(st),
                           take_status_conv(st), take_status_delta(st), take_status_delta_mma(st),
-                          take_status_delta_bwd(st), take_status_scan(st)};
+                          take_status_delta_bwd(st), take_status_scan(st), take_status_conv_bwd(st)};
     for (int p : parts) {
         if (p == GLA_ERR_LAUNCH) return GLA_ERR_LAUNCH;
         if (result == GLA_OK && p != 0) result = p;

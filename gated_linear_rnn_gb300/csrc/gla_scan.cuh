@@ -107,22 +107,6 @@ __device__ __forceinline__ Pair input(const Decay &d, Pair x) {
     return leaks(kForm) ? x * (d.m * both(-1.f)) : x;
 }
 
-// act(x) and its slope
-__device__ __forceinline__ Pair activation(Pair x, int act) {
-    if (act == kNone) return x;
-    Pair q, rest;
-    sigmoid(x, q, rest);
-    return act == kSilu ? x * q : q;
-}
-__device__ __forceinline__ Pair activation(Pair x, int act, Pair &slope) {
-    slope = both(1.f);
-    if (act == kNone) return x;
-    Pair q, rest;
-    sigmoid(x, q, rest);
-    slope = act == kSilu ? q * fma(x, rest, both(1.f)) : q * rest;
-    return act == kSilu ? x * q : q;
-}
-
 // Calls RUN(T, TG, kForm, kGate) for a call's types, form and gate.
 #define GLA_SCAN_BY_FORM(T, TG, G, RUN)                                   \
     switch (p.form) {                                                     \

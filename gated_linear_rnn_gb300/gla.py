@@ -14,7 +14,7 @@ import contextlib
 import ctypes
 import os
 import threading
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -46,6 +46,8 @@ SIGNATURES = {
     "gla_conv1d_silu": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P], _I),
     "gla_conv1d_silu_f32": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P], _I),
     "gla_conv1d_silu_step": ([_P, _P, _P, _P, _P, _I, _I, _P], _I),
+    "gla_conv1d_silu_bwd_workspace_bytes": ([_I] * 4, _L),
+    "gla_conv1d_silu_bwd": ([_P] * 10 + [_I] * 4 + [_P, _P, _L, _P], _I),
     "gla_delta_workspace_bytes": ([_I] * 9, _L),
     "gla_delta_chunk_fwd": ([_P] * 8 + [_I] * 8 + [_P, _P, _L, _P], _I),
     "gla_delta_chunk_bwd": ([_P] * 14 + [_I] * 8 + [_P, _P, _L, _P], _I),
@@ -58,6 +60,9 @@ SIGNATURES = {
     "gla_scan_fwd": ([_P] * 7 + [_I] * 7 + [_P, _P, _L, _P], _I),
     "gla_scan_bwd": ([_P] * 11 + [_I] * 7 + [_P, _P, _L, _P], _I),
     "gla_scan_step": ([_P] * 5 + [_I, _P] + [_I] * 6 + [_P], _I),
+    "gla_residual_norm": ([_P] * 8 + [_I, _I, _I, _F, _P, _P, _L, _I, _I, _I, _P], _I),
+    "gla_residual_norm_workspace_bytes": ([_L, _I], _L),
+    "gla_residual_norm_bwd": ([_P] * 9 + [_I, _I, _I, _F] + [_P] * 8 + [_L, _I, _I, _I, _P, _L, _P], _I),
     "gla_last_device_status": ([_P], _I),
     "gla_status_str": ([_I], ctypes.c_char_p),
     "gla_chunk_kernel": ([_I, _I, _I, _I, _I], _I),
@@ -651,6 +656,39 @@ def gla_group_norm_bwd(dout, x, weight, bias, groups: int, dx, dweight, dbias, d
     _raise(rc, "gla_group_norm_bwd")
 
 
+def gla_conv1d_silu_bwd_workspace_bytes(B: int, T: int, D: int, packed: bool) -> int:
+    """Workspace bytes of gla_conv1d_silu_bwd."""
+    n = load().gla_conv1d_silu_bwd_workspace_bytes(int(B), int(T), int(D), int(bool(packed)))
+    if n < 0:
+        raise GLAError(n, "gla_conv1d_silu_bwd_workspace_bytes")
+    return n
+
+
+def gla_conv1d_silu_bwd(dy, x, weight, bias, state_in, dstate_out, dx, dweight, dbias, dstate_in, cu_seqlens=None,
+                        workspace=None, stream=None) -> None:
+    """Gradients of gla_conv1d_silu (bf16) and gla_conv1d_silu_f32: writes dx and, if given, dweight, dbias and dstate_in.
+    See include/gla.h."""
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, D] (packed: [1, T, D])")
+    B, T, D = x.shape
+    dtype, at, f, t = _dtype(x, "x"), _device(x, "x"), torch.float32, x.dtype
+    nseq, cu = B, None
+    if cu_seqlens is not None:
+        if B != 1:
+            raise ValueError("a packed batch has leading dimension 1")
+        nseq, cu = cu_seqlens.numel() - 1, _arg(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, at)
+    ss = (nseq, D, 3)
+    p = (_arg(dy, "dy", t, x.shape, at), _arg(x, "x", t, x.shape, at), _arg(weight, "weight", f, (D, 4), at),
+         _arg(bias, "bias", f, (D,), at, True), _arg(state_in, "state_in", f, ss, at, True),
+         _arg(dstate_out, "dstate_out", f, ss, at, True), _arg(dx, "dx", t, x.shape, at),
+         _arg(dweight, "dweight", f, (D, 4), at, True), _arg(dbias, "dbias", f, (D,), at, True),
+         _arg(dstate_in, "dstate_in", f, ss, at, True))
+    need = gla_conv1d_silu_bwd_workspace_bytes(nseq, T, D, cu is not None)
+    ws, ws_at, n = _workspace(workspace, need, x.device, stream)
+    rc = load().gla_conv1d_silu_bwd(*p, nseq, T, D, dtype, cu, ws_at, n, _raw_stream(stream, x.device))
+    _raise(rc, "gla_conv1d_silu_bwd")
+
+
 # ---- gated recurrence -------------------------------------------------------------------------------
 
 SCAN_LOG, SCAN_LOG_LEAK, SCAN_SIGMOID, SCAN_SIGMOID_LEAK = 0, 1, 2, 3  # gla_scan_form
@@ -746,6 +784,78 @@ def gla_scan_step(x, g, form: int, state, out, gate=None, act: int = ACT_SILU, s
         _arg(out, "out", t, s, at), N, D, form, act, *types, _raw_stream(stream, x.device))
     if rc:
         raise GLAError(rc, "gla_scan_step")
+
+
+# ---- residual sum with the norms around it --------------------------------------------------------------
+
+NORM_LAYER, NORM_RMS = 0, 1  # gla_norm_kind
+
+
+def _resnorm_args(x, y, gate, scale, post_weight, post_bias, weight, act_dtype):
+    """Checks shared by both residual norm calls; returns the pointers, rows, D, the types and the device."""
+    if x.dim() < 1:
+        raise ValueError("the residual stream must be [..., D]")
+    D, s, at = x.shape[-1], x.shape, _device(x, "x")
+    if act_dtype not in _DTYPES or _dtype(x, "x") != F32 and x.dtype != act_dtype:
+        raise ValueError(f"the residual stream must be torch.float32 or of the type of y and out, got {x.dtype} beside {act_dtype}")
+    if y is None and (gate is not None or scale is not None or post_weight is not None or post_bias is not None):
+        raise ValueError("gate, scale and the norm behind a block need y")
+    f, v = torch.float32, (D,)
+    ptrs = (_arg(y, "y", act_dtype, s, at, True), _arg(gate, "gate", act_dtype, s, at, True),
+            _arg(scale, "scale", f, v, at, True), _arg(post_weight, "post_weight", f, v, at, True),
+            _arg(post_bias, "post_bias", f, v, at, True), _arg(weight, "weight", f, v, at, True))
+    rows = x.numel() // D if D else 0
+    return ptrs, rows, D, (_DTYPES[act_dtype], _DTYPES[x.dtype]), at
+
+
+def gla_residual_norm(x, y, weight, bias, r, out, kind: int = NORM_RMS, gate=None, act: int = ACT_SILU, scale=None,
+                      post: bool = False, post_weight=None, post_bias=None, eps: float = 1e-5, stream=None) -> None:
+    """The sum r = x + scale act(gate) u with u = y or its norm, and out, the norm of r: writes ``r`` (with y) and ``out``
+    (if given).  See include/gla.h."""
+    if y is None and (post or r is not None or out is None) or y is not None and r is None:
+        raise ValueError("r is written where y is given; without y there is nothing but out, and no norm behind a block")
+    if out is None and (weight is not None or bias is not None):
+        raise ValueError("weight and bias are those of out")
+    act_dtype = y.dtype if y is not None else out.dtype
+    p, rows, D, types, at = _resnorm_args(x, y, gate, scale, post_weight, post_bias, weight, act_dtype)
+    rc = load().gla_residual_norm(_arg(x, "x", x.dtype, x.shape, at), *p,
+                                  _arg(bias, "bias", torch.float32, (D,), at, True), kind, bool(post), act, eps,
+                                  _arg(r, "r", x.dtype, x.shape, at, True), _arg(out, "out", act_dtype, x.shape, at, True),
+                                  rows, D, *types, _raw_stream(stream, x.device))
+    if rc:
+        raise GLAError(rc, "gla_residual_norm")
+
+
+def gla_residual_norm_workspace_bytes(rows: int, D: int) -> int:
+    """Workspace bytes of gla_residual_norm_bwd."""
+    n = load().gla_residual_norm_workspace_bytes(int(rows), int(D))
+    if n < 0:
+        raise GLAError(n, "gla_residual_norm_workspace_bytes")
+    return n
+
+
+def gla_residual_norm_bwd(dr, dout, r, y, weight, dx, dy, dgate=None, dscale=None, dpost_weight=None, dpost_bias=None,
+                          dweight=None, dbias=None, kind: int = NORM_RMS, gate=None, act: int = ACT_SILU, scale=None,
+                          post: bool = False, post_weight=None, post_bias=None, eps: float = 1e-5, workspace=None,
+                          stream=None) -> None:
+    """Gradients of gla_residual_norm at the sum ``r`` (x itself without y): writes dx, and of the others those that are
+    given (dy with y and dgate with a gate are required).  See include/gla.h."""
+    if dr is None and dout is None:
+        raise ValueError("dr or dout is required")
+    if y is None and (post or dy is not None) or gate is None and dgate is not None:
+        raise ValueError("dy and the norm behind a block need y, dgate a gate")
+    act_dtype = dout.dtype if dout is not None else r.dtype if y is None else y.dtype
+    p, rows, D, types, at = _resnorm_args(r, y, gate, scale, post_weight, post_bias, weight, act_dtype)
+    st, s, f, v = r.dtype, r.shape, torch.float32, (D,)
+    grads = (_arg(dx, "dx", st, s, at), _arg(dy, "dy", act_dtype, s, at, y is None),
+             _arg(dgate, "dgate", act_dtype, s, at, gate is None), _arg(dscale, "dscale", f, v, at, True),
+             _arg(dpost_weight, "dpost_weight", f, v, at, True), _arg(dpost_bias, "dpost_bias", f, v, at, True),
+             _arg(dweight, "dweight", f, v, at, True), _arg(dbias, "dbias", f, v, at, True))
+    ws, ws_at, n = _workspace(workspace, gla_residual_norm_workspace_bytes(rows, D), r.device, stream)
+    rc = load().gla_residual_norm_bwd(_arg(dr, "dr", st, s, at, True), _arg(dout, "dout", act_dtype, s, at, True),
+                                      _arg(r, "r", st, s, at), *p, kind, bool(post), act, eps, *grads, rows, D, *types, ws_at,
+                                      n, _raw_stream(stream, r.device))
+    _raise(rc, "gla_residual_norm_bwd")
 
 
 def gla_last_device_status(stream=None) -> int:
@@ -859,6 +969,16 @@ def group_norm_bwd(dout, x, weight, bias, groups: int, gate=None, act: int = ACT
     return dx, dweight, dbias, dgate
 
 
+def conv1d_silu_bwd(dy, x, weight, bias=None, state_in=None, dstate_out=None, cu_seqlens=None, stream=None):
+    """Allocate and return (dx, dweight, dbias, dstate_in) of the causal convolution with SiLU; dbias is None without a
+    bias, dstate_in without state_in."""
+    like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
+    with _allocating_on(stream, x.device):
+        dx, dweight, dbias, dstate = torch.empty_like(x), torch.empty_like(weight), like(bias), like(state_in)
+    gla_conv1d_silu_bwd(dy, x, weight, bias, state_in, dstate_out, dx, dweight, dbias, dstate, cu_seqlens, None, stream)
+    return dx, dweight, dbias, dstate
+
+
 def scan_states(x, cu_seqlens=None):
     """Allocate the states that scan_fwd keeps for scan_bwd, for inputs like ``x``."""
     nseq = x.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
@@ -894,3 +1014,40 @@ def scan_step(x, g, form: int, state, gate=None, act: int = ACT_SILU, slots=None
         out = torch.empty_like(x)
     gla_scan_step(x, g, form, state, out, gate, act, slots, stream)
     return out
+
+
+def residual_norm(x, y=None, weight=None, bias=None, kind: int = NORM_RMS, gate=None, act: int = ACT_SILU, scale=None,
+                  post: bool = False, post_weight=None, post_bias=None, eps: float = 1e-5, norm: bool = True, dtype=None,
+                  stream=None):
+    """Allocate and return (r, out): the residual sum of the stream ``x`` and a block's result ``y`` and the norm of it; r is
+    None without y, out without ``norm``.  ``dtype``: that of out where there is no y (else y's), None for that of x."""
+    with _allocating_on(stream, x.device):
+        r = None if y is None else torch.empty_like(x)
+        out = torch.empty_like(x, dtype=(dtype or x.dtype) if y is None else y.dtype) if norm else None
+    gla_residual_norm(x, y, weight, bias, r, out, kind, gate, act, scale, post, post_weight, post_bias, eps, stream)
+    return r, out
+
+
+class ResidualNormGrads(NamedTuple):
+    """Gradients of residual_norm; those of absent parts are None."""
+    dx: torch.Tensor
+    dy: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    dscale: Optional[torch.Tensor]
+    dpost_weight: Optional[torch.Tensor]
+    dpost_bias: Optional[torch.Tensor]
+    dweight: Optional[torch.Tensor]
+    dbias: Optional[torch.Tensor]
+
+
+def residual_norm_bwd(dr, dout, r, y=None, weight=None, bias=None, kind: int = NORM_RMS, gate=None, act: int = ACT_SILU,
+                      scale=None, post: bool = False, post_weight=None, post_bias=None, eps: float = 1e-5, stream=None):
+    """Allocate and return the gradients of residual_norm at the sum ``r`` (x itself without y), of every part that is
+    given.  ``dr``: what reaches r besides out, or None; ``dout``: None where the forward had no norm."""
+    like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
+    with _allocating_on(stream, r.device):
+        g = ResidualNormGrads(torch.empty_like(r), like(y), like(gate), like(scale), like(post_weight), like(post_bias),
+                              like(weight), like(bias))
+    gla_residual_norm_bwd(dr, dout, r, y, weight, g.dx, g.dy, g.dgate, g.dscale, g.dpost_weight, g.dpost_bias, g.dweight,
+                          g.dbias, kind, gate, act, scale, post, post_weight, post_bias, eps, None, stream)
+    return g

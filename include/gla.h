@@ -439,6 +439,24 @@ GLA_API int gla_conv1d_silu_step(const void *x, const float *weight, const float
                                  void *y, int N, int D, void *stream);
 
 /*
+ * gla_conv1d_silu_bwd — the gradients of gla_conv1d_silu (of dtype GLA_BF16) or gla_conv1d_silu_f32 (GLA_F32), with
+ * L = sum(dy .* y) + sum(dstate_out .* state_out); nothing is kept from the forward:
+ *     dz_t = dy_t SiLU'(z_t),  dx_v = sum_{k=0..3} weight[k] dz_{v+3-k} (dz is 0 behind a sequence's end), plus dstate_out for
+ *     a sequence's last three inputs,  dweight[k] = sum over tokens of dz_t x_{t-3+k},  dbias = sum over tokens of dz_t
+ *   dy, dx      like x (dx written);  dweight [D, 4] and dbias [D] f32, written, either may be NULL
+ *   state_in, dstate_out, dstate_in  [B|N, D, 3] f32 or NULL (zeros; dstate_in is then not written)
+ *   cu_seqlens  as gla_delta_chunk_fwd: bad sequences are taken as empty and GLA_ERR_DEVICE_ARG recorded; rows that are no
+ *               sequence's are not written
+ *   ws, ws_bytes  at least gla_conv1d_silu_bwd_workspace_bytes(...) bytes (device): the blocks' sums of dweight and dbias,
+ *               which are added up in a fixed order
+ *   D % 8 == 0; all rows together below 2^31 - 256; pointers 16-byte aligned.  Arithmetic is f32.  Returns a gla_status.
+ */
+GLA_API long long gla_conv1d_silu_bwd_workspace_bytes(int B, int T, int D, int packed);
+GLA_API int gla_conv1d_silu_bwd(const void *dy, const void *x, const float *weight, const float *bias, const float *state_in,
+                                const float *dstate_out, void *dx, float *dweight, float *dbias, float *dstate_in, int B, int T,
+                                int D, int dtype, const int32_t *cu_seqlens, void *ws, long long ws_bytes, void *stream);
+
+/*
  * The gated delta rule.  Every (sequence, value head) chain keeps a dk x dv matrix state S like the mixer
  * above, with a decay and a write strength per token, and writes the difference between v_t and what the
  * state already answers to k_t:
@@ -621,6 +639,44 @@ GLA_API int gla_scan_bwd(const void *x, const void *g, const void *gate, const v
  */
 GLA_API int gla_scan_step(const void *x, const void *g, const void *gate, float *state, const int32_t *slots, int nslots,
                           void *out, int N, int D, int form, int act, int dtype, int g_dtype, void *stream);
+
+/*
+ * gla_residual_norm — the sum between two blocks of a model with the norms on both of its sides, for each token's D channels:
+ *     u = n(y) post_weight + post_bias where post is nonzero, else y        (the norm behind a block)
+ *     r = x + scale act(gate) u                                             (the residual stream; gate or scale may be absent)
+ *     out = n(r) weight + bias                                              (the norm in front of the next block)
+ *     n(v) = (v - mean) / sqrt(variance + eps) for GLA_NORM_LAYER, v / sqrt(mean square + eps) for GLA_NORM_RMS
+ *   x, r         [rows, D] of stream_dtype: the residual stream before and after (r written)
+ *   y, gate, out [rows, D] of dtype (out written); gate NULL: no factor; act: a gla_act
+ *   y NULL       nothing is added: out = n(x) weight + bias, and r, gate, scale, post and its parameters must be absent
+ *   out NULL     the sum alone; weight and bias must be NULL
+ *   scale, weight, bias, post_weight, post_bias  [D] f32; NULL for ones / zeros
+ *   dtype        GLA_BF16 or GLA_F32;  stream_dtype  dtype, or GLA_F32
+ *   D            a multiple of 8, 8 <= D <= 16384;  rows >= 0;  eps > 0
+ * Statistics and arithmetic are f32, out is of the sum before it is rounded to r.  Returns a gla_status.
+ */
+typedef enum { GLA_NORM_LAYER = 0, GLA_NORM_RMS = 1 } gla_norm_kind;
+GLA_API int gla_residual_norm(const void *x, const void *y, const void *gate, const float *scale, const float *post_weight,
+                              const float *post_bias, const float *weight, const float *bias, int kind, int post, int act,
+                              float eps, void *r, void *out, long long rows, int D, int dtype, int stream_dtype,
+                              void *stream);
+
+/*
+ * gla_residual_norm_bwd — its gradients, at the sum r that the forward left (the x of a call without y).
+ *   dr           [rows, D] of stream_dtype: what reaches r besides out; NULL for zeros
+ *   dout         like out; NULL where the forward had no out (then dweight and dbias must be NULL).  One of both is given
+ *   dx           like x, dy and dgate like y and gate: written (dgate with a gate, dy with y, else NULL)
+ *   dscale, dpost_weight, dpost_bias, dweight, dbias  [D] f32, written; any may be NULL, and those of an absent part must be
+ *   ws           device workspace of at least gla_residual_norm_workspace_bytes(rows, D) bytes for the blocks' sums of these
+ *                five, which are added up in a fixed order
+ * Returns a gla_status.
+ */
+GLA_API long long gla_residual_norm_workspace_bytes(long long rows, int D);
+GLA_API int gla_residual_norm_bwd(const void *dr, const void *dout, const void *r, const void *y, const void *gate,
+                                  const float *scale, const float *post_weight, const float *post_bias, const float *weight,
+                                  int kind, int post, int act, float eps, void *dx, void *dy, void *dgate, float *dscale,
+                                  float *dpost_weight, float *dpost_bias, float *dweight, float *dbias, long long rows, int D,
+                                  int dtype, int stream_dtype, void *ws, long long ws_bytes, void *stream);
 
 /*
  * gla_last_device_status — synchronise `stream`, then return and clear the
