@@ -110,6 +110,8 @@ int bwd(const void *, const void *, const float *, const float *, const float *,
 }  // namespace convbwd
 int take_status_conv_bwd(cudaStream_t);
 int take_status_scan(cudaStream_t);
+int take_status_scan_fwd(cudaStream_t);
+int take_status_scan_bwd(cudaStream_t);
 int take_status_delta(cudaStream_t);
 int take_status_delta_mma(cudaStream_t);
 int take_status_delta_bwd(cudaStream_t);
@@ -275,7 +277,7 @@ int check_scan_sizes(int B, int T, int D, int packed) {
     const long long rows = packed ? (long long)T : (long long)B * T;
     // rows, and blocks of 64 channels of a chunk or a sequence, are 32-bit
     const long long parts = (D + 63) / 64;
-    if (rows > 0x7fffff00LL || (rows / scan::kChunk + B + 1) * parts > 0x7fffffffLL || (long long)B * parts > 0x7fffffffLL)
+    if (rows > 0x7fffff00LL || (rows / scan::kChunk + B + 1) * parts > 0x7fff0000LL || (long long)B * parts > 0x7fffffffLL)
         return GLA_ERR_UNSUPPORTED;
     return GLA_OK;
 }
@@ -754,7 +756,8 @@ int gla_last_device_status(void *stream) {
     int result = GLA_OK;
     const int parts[] = {take_status_simt(st), take_status_decode(st), take_status_tc(st), take_status_bwd(st),
                           take_status_conv(st), take_status_delta(st), take_status_delta_mma(st),
-                          take_status_delta_bwd(st), take_status_scan(st), take_status_conv_bwd(st)};
+                          take_status_delta_bwd(st), take_status_scan(st), take_status_scan_fwd(st),
+                          take_status_scan_bwd(st), take_status_conv_bwd(st)};
     for (int p : parts) {
         if (p == GLA_ERR_LAUNCH) return GLA_ERR_LAUNCH;
         if (result == GLA_OK && p != 0) result = p;

@@ -343,7 +343,9 @@ sum_kernel(const float *__restrict__ part, int nblocks, int D, Sums sums) {
 }
 
 int blocks(const Plan &pl, int64_t rows, int per_sm) {
-    const int64_t need = (rows + pl.rows - 1) / pl.rows, most = (int64_t)device_info().sm_count * per_sm;
+    const int64_t need = (rows + pl.rows - 1) / pl.rows;
+    int64_t most = (int64_t)device_info().sm_count * per_sm;
+    if (most < 1) most = 1;
     return (int)(need < most ? need : most);
 }
 int fwd_per_sm(const Plan &pl) { return 2048 / pl.threads < 1 ? 1 : 2048 / pl.threads; }

@@ -6,18 +6,29 @@
 //     dh_t = dout_t act(gate_t) + D_t,   D_{t-1} = a_t dh_t,   dh0 = D_0,   dx_t = w_t dh_t,
 //     da_t = dh_t (h_{t-1} - x_t) where the input leaks, dh_t h_{t-1} elsewhere,   dg_t = da_t a_t, times 1 - a_t for a sigmoid,
 //     dgate_t = dout_t h_t act'(gate_t)
-#include "gla_scan.cuh"
+#include "gla_scan_tiles.cuh"
 
 GLA_DEFINE_STATUS(scan)
 
 namespace gla {
 namespace scan {
+
+bool tiles_fwd(const Shape &, const Tiles &, const Chain &, const void *, const void *, const void *, const float *, void *, float *,
+               float *, int, int, cudaStream_t);
+bool tiles_bwd(const Shape &, const Tiles &, const Chain &, const void *, const void *, const void *, const void *, const float *,
+               const float *, void *, void *, void *, float *, int, int, cudaStream_t);
+
 namespace {
 
 constexpr int kThreads = 128;  // two channels each
+constexpr int kWalked = 16;    // tokens of a sequence, see walks()
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t *__restrict__ cu, int nseq, int T, int2 *rows) {
-    if (plan_rows(cu, nseq, T, rows)) record_status(GLA_ERR_DEVICE_ARG);
+// What has to be there before the others start: the rows of a packed batch's sequences, and the words of the chains unset.
+__global__ void __launch_bounds__(kPlanThreads)
+prepare_kernel(const int32_t *__restrict__ cu, int nseq, int T, int2 *rows, uint4 *unset, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * kPlanThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kPlanThreads)
+        unset[i] = make_uint4(kUnset, kUnset, kUnset, kUnset);
+    if (blockIdx.x == 0 && cu != nullptr && plan_rows(cu, nseq, T, rows)) record_status(GLA_ERR_DEVICE_ARG);
 }
 
 // A thread takes two channels of a sequence from its first token to its last.
@@ -114,15 +125,8 @@ step_kernel(const T *__restrict__ x, const TG *__restrict__ g, const T *__restri
 
 int status() { return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH; }
 
-Sequences plan(const Shape &p, void *ws, cudaStream_t st) {
-    if (p.cu == nullptr) return {p.nseq, p.T, nullptr};
-    plan_kernel<<<1, kPlanThreads, 0, st>>>(p.cu, p.nseq, p.T, (int2 *)ws);
-    count_launches(1);
-    return {p.nseq, p.T, (const int2 *)ws};
-}
-
-void run_fwd(const Shape &p, const void *x, const void *g, const void *gate, const float *h0, void *out, float *hT,
-             float *states, int dtype, int g_dtype, const Sequences &q, cudaStream_t st) {
+void walk_fwd(const Shape &p, const void *x, const void *g, const void *gate, const float *h0, void *out, float *hT,
+              float *states, int dtype, int g_dtype, const Sequences &q, cudaStream_t st) {
     const int parts = (p.D + 2 * kThreads - 1) / (2 * kThreads);
 #define GLA_RUN(T, TG, F, G)                                                                                                \
     walk_fwd_kernel<T, TG, F, G><<<(unsigned)(p.nseq * parts), kThreads, 0, st>>>(                                          \
@@ -132,27 +136,9 @@ void run_fwd(const Shape &p, const void *x, const void *g, const void *gate, con
     count_launches(1);
 }
 
-}  // namespace
-
-int64_t workspace(int op, const Shape &p) {
-    return rows_bytes(p.nseq, p.cu != nullptr) + (op == GLA_OP_BACKWARD ? states_bytes(p) : 0);
-}
-
-int fwd(const Shape &p, const void *x, const void *g, const void *gate, const float *h0, void *out, float *hT, float *states,
-        int dtype, int g_dtype, void *ws, cudaStream_t st) {
-    const Sequences q = plan(p, ws, st);
-    run_fwd(p, x, g, gate, h0, out, hT, states, dtype, g_dtype, q, st);
-    return status();
-}
-
-int bwd(const Shape &p, const void *x, const void *g, const void *gate, const void *dout, const float *h0, const float *dhT,
-        const float *states, void *dx, void *dg, void *dgate, float *dh0, int dtype, int g_dtype, void *ws, cudaStream_t st) {
-    const Sequences q = plan(p, ws, st);
-    if (states == nullptr) {
-        float *own = reinterpret_cast<float *>((uint8_t *)ws + rows_bytes(p.nseq, p.cu != nullptr));
-        run_fwd(p, x, g, nullptr, h0, nullptr, nullptr, own, dtype, g_dtype, q, st);
-        states = own;
-    }
+void walk_bwd(const Shape &p, const void *x, const void *g, const void *gate, const void *dout, const float *dhT,
+              const float *states, void *dx, void *dg, void *dgate, float *dh0, int dtype, int g_dtype, const Sequences &q,
+              cudaStream_t st) {
     const int parts = (p.D + 2 * kThreads - 1) / (2 * kThreads);
 #define GLA_RUN(T, TG, F, G)                                                                                                \
     walk_bwd_kernel<T, TG, F, G><<<(unsigned)(p.nseq * parts), kThreads, 0, st>>>(                                          \
@@ -161,6 +147,81 @@ int bwd(const Shape &p, const void *x, const void *g, const void *gate, const vo
     GLA_SCAN_DISPATCH(dtype, g_dtype, gate != nullptr, GLA_RUN)
 #undef GLA_RUN
     count_launches(1);
+}
+
+// A call's workspace: the rows of a packed batch's sequences, a counter and a chain for each direction, and (of a gradient that
+// is not given them) the states.
+struct Layout {
+    int64_t rows, counters, chains, states, total;
+};
+constexpr int64_t kCounterBytes = 256;
+bool chained(const Shape &p) { return p.cu != nullptr || p.T > kChunk; }
+Layout layout(int op, const Shape &p) {
+    Layout l{};
+    const int64_t chain = chained(p) ? (chain_floats(p) * (int64_t)sizeof(float) + 255) / 256 * 256 : 0;
+    const int dirs = op == GLA_OP_BACKWARD ? 2 : 1;
+    l.counters = rows_bytes(p.nseq, p.cu != nullptr);
+    l.chains = l.counters + (chain > 0 ? dirs * kCounterBytes : 0);
+    l.states = l.chains + dirs * chain;
+    l.total = l.states + (op == GLA_OP_BACKWARD ? states_bytes(p) : 0);
+    return l;
+}
+Chain chain_at(const Layout &l, const Shape &p, void *ws, int dir) {
+    uint8_t *b = (uint8_t *)ws;
+    Chain c;
+    c.next = (unsigned *)(b + l.counters + dir * kCounterBytes);
+    c.effect = (float *)(b + l.chains + dir * ((chain_floats(p) * (int64_t)sizeof(float) + 255) / 256 * 256));
+    c.result = c.effect + slots(p) * p.D * 2;
+    return c;
+}
+
+// dirs: how many of the chains are used
+Sequences prepare(const Shape &p, const Layout &l, void *ws, int dirs, cudaStream_t st) {
+    if (!chained(p)) return {p.nseq, p.T, nullptr};
+    uint8_t *b = (uint8_t *)ws;
+    const int64_t bytes = l.chains - l.counters + dirs * ((chain_floats(p) * (int64_t)sizeof(float) + 255) / 256 * 256);
+    const int64_t n = bytes / 16, need = (n + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+    const int64_t most = 2 * (int64_t)device_info().sm_count;
+    prepare_kernel<<<(unsigned)(need < most ? need : most), kPlanThreads, 0, st>>>(p.cu, p.nseq, p.T, (int2 *)ws,
+                                                                                 (uint4 *)(b + l.counters), n);
+    count_launches(1);
+    return {p.nseq, p.T, p.cu ? (const int2 *)ws : nullptr};
+}
+
+// Sequences this short on average are walked by a thread for two channels each.
+bool walks(const Shape &p) { return total_rows(p) <= (int64_t)kWalked * p.nseq; }
+
+}  // namespace
+
+int64_t workspace(int op, const Shape &p) { return layout(op, p).total; }
+
+int fwd(const Shape &p, const void *x, const void *g, const void *gate, const float *h0, void *out, float *hT, float *states,
+        int dtype, int g_dtype, void *ws, cudaStream_t st) {
+    const Layout l = layout(GLA_OP_FORWARD, p);
+    const Sequences q = prepare(p, l, ws, 1, st);
+    if (walks(p)) walk_fwd(p, x, g, gate, h0, out, hT, states, dtype, g_dtype, q, st);
+    else if (!tiles_fwd(p, make_tiles(p, q), chain_at(l, p, ws, 0), x, g, gate, h0, out, hT, states, dtype, g_dtype, st))
+        return GLA_ERR_LAUNCH;
+    return status();
+}
+
+int bwd(const Shape &p, const void *x, const void *g, const void *gate, const void *dout, const float *h0, const float *dhT,
+        const float *states, void *dx, void *dg, void *dgate, float *dh0, int dtype, int g_dtype, void *ws, cudaStream_t st) {
+    const Layout l = layout(GLA_OP_BACKWARD, p);
+    const Sequences q = prepare(p, l, ws, states == nullptr ? 2 : 1, st);
+    float *own = reinterpret_cast<float *>((uint8_t *)ws + l.states);
+    const Tiles t = make_tiles(p, q);
+    if (walks(p)) {
+        if (states == nullptr) walk_fwd(p, x, g, nullptr, h0, nullptr, nullptr, own, dtype, g_dtype, q, st);
+        walk_bwd(p, x, g, gate, dout, dhT, states != nullptr ? states : own, dx, dg, dgate, dh0, dtype, g_dtype, q, st);
+        return status();
+    }
+    if (states == nullptr &&
+        !tiles_fwd(p, t, chain_at(l, p, ws, 1), x, g, nullptr, h0, nullptr, nullptr, own, dtype, g_dtype, st))
+        return GLA_ERR_LAUNCH;
+    if (!tiles_bwd(p, t, chain_at(l, p, ws, 0), x, g, gate, dout, dhT, states != nullptr ? states : own, dx, dg, dgate, dh0,
+                   dtype, g_dtype, st))
+        return GLA_ERR_LAUNCH;
     return status();
 }
 

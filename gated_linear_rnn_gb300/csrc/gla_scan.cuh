@@ -12,7 +12,7 @@ namespace gla {
 namespace scan {
 
 // Rows of a chunk: the state before each one is what a forward keeps for the gradient.
-constexpr int kChunk = 128;
+constexpr int kChunk = 64;
 
 struct Shape {
     int nseq, T, D;

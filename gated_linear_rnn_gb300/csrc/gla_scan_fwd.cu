@@ -1,0 +1,180 @@
+// gla_scan_fwd.cu — the gated recurrence over chunks (see gla_scan_tiles.cuh): one pass over x, g and gate.
+#include "gla_scan_tiles.cuh"
+
+GLA_DEFINE_STATUS(scan_fwd)
+
+namespace gla {
+namespace scan {
+namespace {
+
+constexpr int kPerSm = 1024 / kTileThreads;  // blocks that the registers allow
+
+template <typename T, typename TG, bool kGate> struct Ring {
+    static constexpr int x = 0, g = tile_bytes<T>(), z = g + tile_bytes<TG>();
+    static constexpr int bytes = z + (kGate ? tile_bytes<T>() : 0);
+};
+
+template <typename T, typename TG, int kForm, bool kGate>
+__global__ void __launch_bounds__(kTileThreads, kPerSm)
+tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
+                 const __grid_constant__ CUtensorMap mz, const float *__restrict__ h0, T *__restrict__ out,
+                 float *__restrict__ hT, float *__restrict__ states, Tiles t, Chain chain, int act, int stages) {
+    using namespace ptx;
+    using R = Ring<T, TG, kGate>;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float4 effects[kWarps][32];
+    __shared__ float2 enters[32];
+    __shared__ Tile tiles[kMaxStages];
+    __shared__ __align__(8) uint64_t full[kMaxStages];
+    __shared__ int gave_up;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = t.D;
+    const uint32_t base = smem_u32(ring), bar = smem_u32(full);
+    unsigned own = blockIdx.x;
+
+    auto order = [&](int st) {  // by one thread
+        tiles[st] = next_tile<true>(t, chain, own);
+        const Tile &o = tiles[st];
+        if (o.row < 0) return;
+        const uint32_t to = base + (uint32_t)(st * R::bytes), b = bar + 8u * (uint32_t)st;
+        mbar_expect_tx(b, R::bytes);
+        tma_load_2d(to + R::x, &mx, o.col, o.row, b);
+        tma_load_2d(to + R::g, &mg, o.col, o.row, b);
+        if (kGate) tma_load_2d(to + R::z, &mz, o.col, o.row, b);
+    };
+    if (threadIdx.x == 0) {
+        gave_up = 0;
+        for (int st = 0; st < stages; ++st) mbar_init(bar + 8u * (uint32_t)st, 1);
+        fence_mbar_init();
+        for (int st = 0; st < stages; ++st) order(st);
+    }
+    // sequences without tokens pass their state on
+    if (hT != nullptr)
+        for (int s = blockIdx.x; s < t.q.nseq; s += gridDim.x)
+            if (rows_of(t.q, s).y == 0)
+                for (int d = threadIdx.x; d < D; d += kTileThreads)
+                    hT[(int64_t)s * D + d] = h0 != nullptr ? __ldg(h0 + (int64_t)s * D + d) : 0.f;
+    __syncthreads();
+
+    int st = 0;
+    uint32_t phase = 0;
+    for (bool first = true;; first = false) {
+        const Tile o = tiles[st];
+        if (o.row < 0) break;
+        if (!mbar_wait(bar + 8u * (uint32_t)st, phase, nullptr, kWaitNs)) {
+            record_status(GLA_ERR_TIMEOUT);
+            gave_up = 1;
+        }
+        const uint8_t *stage = ring + st * R::bytes;
+        const int d = o.col + 2 * lane, n = min(kLane, o.len - warp * kLane);  // the warp's rows, none or fewer where n < 8
+        // the warp's rows from a zero state: h, and the product of the decays up to each
+        Pair h[kLane], P[kLane], hh = both(0.f), PP = both(1.f);
+#pragma unroll
+        for (int i = 0; i < kLane; ++i) {
+            if (i < n) {
+                const int at = (warp * kLane + i) * kSlab + 2 * lane;
+                const Decay a = decay<kForm>(staged<TG>(stage + R::g, at));
+                hh = decayed(a, hh, input<kForm>(a, staged<T>(stage + R::x, at)));
+                PP = decayed(a, PP, both(0.f));
+            }
+            h[i] = hh;
+            P[i] = PP;
+        }
+        {
+            const float2 a = parts(PP), b = parts(hh);
+            effects[warp][lane] = make_float4(a.x, a.y, b.x, b.y);
+        }
+        __syncthreads();
+        // the tile of the round before is done: its stage takes the next one
+        if (threadIdx.x == 0 && !first) order(st == 0 ? stages - 1 : st - 1);
+        Pair A = both(1.f), H = both(0.f);  // the effect of the warps before this one
+        for (int w = 0; w < warp; ++w) {
+            const float4 f = effects[w][lane];
+            const Pair a = pair(f.x, f.y);
+            H = fma(a, H, pair(f.z, f.w));
+            A = A * a;
+        }
+        if (warp == kWarps - 1) {
+            const Pair tA = A * PP, tH = fma(PP, H, hh);
+            const int64_t at = (int64_t)o.slot * D + d;
+            const bool on = d < D;
+            Pair S = both(0.f);
+            if (o.chunk == 0) {
+                if (on && h0 != nullptr) S = load_state(h0 + (int64_t)o.seq * D + d);
+            } else {
+                if (on && o.behind > 0) publish_effect(chain, at, tA, tH);
+                if (!look_back<-1>(chain, o.slot, D, d, o.chunk, S)) {
+                    record_status(GLA_ERR_TIMEOUT);
+                    gave_up = 1;
+                }
+            }
+            const Pair end = fma(tA, S, tH);
+            if (on) {
+                if (o.behind > 0) publish_result(chain, at, end);
+                else if (hT != nullptr) store_state(hT + (int64_t)o.seq * D + d, end);
+                if (states != nullptr) store_state(states + at, S);
+            }
+            enters[lane] = parts(S);
+        }
+        __syncthreads();
+        if (gave_up) break;
+        if (out != nullptr && d < D) {
+            const float2 e = enters[lane];
+            const Pair S = fma(A, pair(e.x, e.y), H);
+            T *to = out + (int64_t)(o.row + warp * kLane) * D + d;
+#pragma unroll
+            for (int i = 0; i < kLane; ++i) {
+                if (i < n) {
+                    Pair y = fma(P[i], S, h[i]);
+                    if (kGate) y = y * activation(staged<T>(stage + R::z, (warp * kLane + i) * kSlab + 2 * lane), act);
+                    store_two(to + (int64_t)i * D, y);
+                }
+            }
+        }
+        if (++st == stages) {
+            st = 0;
+            phase ^= 1;
+        }
+    }
+    // a block that gave up waits for what it has ordered
+    if (gave_up && threadIdx.x == 0)
+        for (int i = 0; i < stages; ++i) {
+            if (++st == stages) {
+                st = 0;
+                phase ^= 1;
+            }
+            if (i + 1 < stages && tiles[st].row >= 0) mbar_wait(bar + 8u * (uint32_t)st, phase, nullptr, kWaitNs);
+        }
+}
+
+template <typename T, typename TG, int kForm, bool kGate>
+bool launch(const Shape &p, const Tiles &t, const Chain &chain, const T *x, const TG *g, const T *gate, const float *h0, T *out,
+            float *hT, float *states, cudaStream_t st) {
+    using R = Ring<T, TG, kGate>;
+    constexpr Room room = room_for(R::bytes, kPerSm);
+    constexpr int bytes = room.stages * R::bytes;
+    constexpr auto kKernel = tiles_fwd_kernel<T, TG, kForm, kGate>;
+    CUtensorMap mx, mg, mz;
+    if (!tile_map(&mx, x, p) || !tile_map(&mg, g, p) || !tile_map(&mz, kGate ? gate : x, p)) return false;
+    if (!allow_dynamic<kKernel>(bytes)) return false;
+    int64_t grid = (int64_t)device_info().sm_count * room.per_sm;
+    if (grid > (int64_t)t.total) grid = t.total;
+    if (grid < 1) grid = 1;
+    kKernel<<<(unsigned)grid, kTileThreads, bytes, st>>>(mx, mg, mz, h0, out, hT, states, t, chain, p.act, room.stages);
+    count_launches(1);
+    return true;
+}
+
+}  // namespace
+
+bool tiles_fwd(const Shape &p, const Tiles &t, const Chain &chain, const void *x, const void *g, const void *gate,
+               const float *h0, void *out, float *hT, float *states, int dtype, int g_dtype, cudaStream_t st) {
+    bool ok = false;
+#define GLA_RUN(T, TG, F, G)                                                                                              \
+    ok = launch<T, TG, F, G>(p, t, chain, (const T *)x, (const TG *)g, (const T *)gate, h0, (T *)out, hT, states, st)
+    GLA_SCAN_DISPATCH(dtype, g_dtype, gate != nullptr, GLA_RUN)
+#undef GLA_RUN
+    return ok;
+}
+
+}  // namespace scan
+}  // namespace gla

@@ -1,0 +1,223 @@
+// gla_scan_tiles.cuh — what the chunked forward and gradient of the gated recurrence share.
+//
+// A block works on tiles of 64 channels of a chunk of kChunk rows of one sequence: a warp takes eight rows, a lane two
+// channels.  A tile's effect on a state is h -> A h + H.  Its warps find their rows' effects from a zero state, meet in shared
+// memory, and the tile's effect is published; the state that enters it is then found by looking back over the effects of the
+// tiles before it, to the nearest one whose own result is published.  The look back folds from that result on, one tile after
+// the other, which is the same arithmetic wherever it starts: the results do not depend on who was first.
+//
+// What is published is its own flag: a word that holds kUnset has not been written yet.
+//
+// Tiles are handed out by a counter in an order in which a tile comes after all that it waits for, so that a waiting block
+// waits only for blocks that run.  Rows come in by TMA, some tiles ahead.
+#pragma once
+
+#include <cuda.h>
+
+#include "gla_scan.cuh"
+#include "sm100_ptx.cuh"
+
+namespace gla {
+bool make_map_2d(CUtensorMap *m, CUtensorMapDataType dtype, uint32_t elem_bytes, const void *base, uint64_t cols,
+                 uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle sw);
+namespace scan {
+
+constexpr int kLane = 8;                     // rows of a warp
+constexpr int kWarps = kChunk / kLane;
+constexpr int kTileThreads = kWarps * 32;
+constexpr int kSlab = 64;                    // channels of a tile
+constexpr uint32_t kUnset = 0xffffffffu;     // a NaN that no result is: one that would be is stored as another
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s a wait
+constexpr int kBack = 4;                     // tiles that a look back reads at once
+
+// The chunks' effects and results, for one direction.
+struct Chain {
+    float *effect;   // [slots, D, 2]: A, H
+    float *result;   // [slots, D]
+    unsigned *next;  // the counter of tiles, and behind it whether a wait gave up
+};
+__host__ inline int64_t chain_floats(const Shape &p) { return slots(p) * p.D * 3; }
+
+struct Tiles {
+    Sequences q;
+    int D, slabs, nslots, per_seq;  // per_seq: chunks of a sequence of a dense batch
+    unsigned total;
+    int chained;                    // whether any sequence may have more than one chunk
+};
+__host__ inline Tiles make_tiles(const Shape &p, const Sequences &q) {
+    Tiles t{q, p.D, (p.D + kSlab - 1) / kSlab, (int)slots(p), (p.T + kChunk - 1) / kChunk, 0, 1};
+    t.total = p.cu ? (unsigned)t.nslots * (unsigned)t.slabs : (unsigned)t.per_seq * (unsigned)p.nseq * (unsigned)t.slabs;
+    t.chained = p.cu != nullptr || p.T > kChunk;
+    return t;
+}
+
+struct Tile {
+    int row, len, chunk, behind, seq, slot, col;  // behind: its sequence's chunks after it; col: its first channel
+};
+
+// Tile k in the order of a direction; false for slots that no chunk has.  A dense batch goes through all sequences' first
+// chunks, then their second ones and so on: what a tile waits for is then mostly done.
+template <bool kForth>
+__device__ __forceinline__ bool tile_at(const Tiles &t, unsigned k, Tile &o) {
+    o.col = (int)(k % (unsigned)t.slabs) * kSlab;
+    unsigned r = k / (unsigned)t.slabs;
+    int2 rows;
+    if (t.q.rows == nullptr) {
+        o.seq = (int)(r % (unsigned)t.q.nseq);
+        o.chunk = (int)(r / (unsigned)t.q.nseq);
+        if (!kForth) o.chunk = t.per_seq - 1 - o.chunk;
+        rows = rows_of(t.q, o.seq);
+        o.slot = rows.x / kChunk + o.seq + o.chunk;
+    } else {
+        o.slot = kForth ? (int)r : t.nslots - 1 - (int)r;
+        o.seq = sequence_of_slot(t.q, o.slot, kChunk);
+        rows = rows_of(t.q, o.seq);
+        o.chunk = o.slot - (rows.x / kChunk + o.seq);
+        if (o.chunk < 0 || (int64_t)o.chunk * kChunk >= rows.y) return false;
+    }
+    o.row = rows.x + o.chunk * kChunk;
+    o.len = min(kChunk, rows.y - o.chunk * kChunk);
+    o.behind = (rows.y - 1) / kChunk - o.chunk;
+    return true;
+}
+
+// The next tile of a block, by one thread; row < 0 when there are no more.
+template <bool kForth>
+__device__ __forceinline__ Tile next_tile(const Tiles &t, const Chain &c, unsigned &own) {
+    Tile o;
+    for (;;) {
+        unsigned k = own;
+        if (t.chained) k = atomicAdd(c.next, 1u) + 1u;  // the counter starts at kUnset
+        else own += gridDim.x;
+        if (k >= t.total) {
+            o.row = -1;
+            return o;
+        }
+        if (tile_at<kForth>(t, k, o)) return o;
+    }
+}
+
+// ---- launches --------------------------------------------------------------------------------------------------------
+
+// Blocks of an SM and stages of a block: as many blocks as the threads' registers allow and two stages each leave room for.
+struct Room {
+    int per_sm, stages;
+};
+constexpr int kMaxStages = 4;
+constexpr Room room_for(int stage_bytes, int most) {
+    const int room = 225 * 1024, fixed = kWarps * 512 * 2 + 1024;
+    int per_sm = room / (2 * stage_bytes + fixed);
+    per_sm = per_sm > most ? most : per_sm;
+    int stages = (room / per_sm - fixed) / stage_bytes;
+    return {per_sm, stages > kMaxStages ? kMaxStages : stages};
+}
+
+// The map of an array [rows, D] for boxes of a tile.
+template <typename T> bool tile_map(CUtensorMap *m, const T *at, const Shape &p) {
+    return make_map_2d(m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                       (uint32_t)sizeof(T), at, (uint64_t)p.D, (uint64_t)total_rows(p), kSlab, kChunk,
+                       CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// Lets a kernel use so many bytes of dynamic shared memory; asked of the runtime once per kernel and device.
+template <auto kKernel> bool allow_dynamic(int bytes) {
+    constexpr int kDevices = 64;
+    static std::atomic<bool> allowed[kDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < kDevices && allowed[dev].load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    if (dev < kDevices) allowed[dev].store(true, std::memory_order_release);
+    return true;
+}
+
+// two channels of a staged tile
+template <typename T> __device__ __forceinline__ Pair staged(const uint8_t *tile, int at) {
+    return Two<T>::open(*reinterpret_cast<const typename Two<T>::Raw *>(tile + at * (int)sizeof(T)));
+}
+template <typename T> constexpr int tile_bytes() { return kChunk * kSlab * (int)sizeof(T); }
+
+// ---- what is published -----------------------------------------------------------------------------------------------
+__device__ __forceinline__ float settled(float x) { return __float_as_uint(x) == kUnset ? __uint_as_float(0x7fffffffu) : x; }
+__device__ __forceinline__ bool is_set(float x) { return __float_as_uint(x) != kUnset; }
+
+__device__ __forceinline__ void publish_effect(const Chain &c, int64_t at, Pair A, Pair H) {
+    const float2 a = parts(A), h = parts(H);
+    asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(c.effect + at * 2), "f"(settled(a.x)),
+                 "f"(settled(h.x)), "f"(settled(a.y)), "f"(settled(h.y))
+                 : "memory");
+}
+__device__ __forceinline__ void publish_result(const Chain &c, int64_t at, Pair S) {
+    const float2 s = parts(S);
+    asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(c.result + at), "f"(settled(s.x)), "f"(settled(s.y))
+                 : "memory");
+}
+__device__ __forceinline__ float4 read_effect(const Chain &c, int64_t at) {
+    float4 f;
+    asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+                 : "l"(c.effect + at * 2)
+                 : "memory");
+    return f;
+}
+__device__ __forceinline__ float2 read_result(const Chain &c, int64_t at) {
+    float2 f;
+    asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(f.x), "=f"(f.y) : "l"(c.result + at) : "memory");
+    return f;
+}
+
+// The state that enters a tile from the `behind` tiles on its chain's other side (at > 0), by a whole warp; kStep is how far
+// a neighbour's slot lies off.  A channel past the last has nothing to wait for.  False when the wait gave up.
+template <int kStep>
+__device__ __forceinline__ bool look_back(const Chain &c, int64_t slot, int D, int d, int behind, Pair &S) {
+    const bool on = d < D;
+    uint64_t since = 0;
+    for (unsigned tries = 0;; ++tries) {
+        float2 res[kBack];
+        float4 eff[kBack];
+        const int n = min(behind, kBack);
+#pragma unroll
+        for (int j = 0; j < kBack; ++j) {
+            res[j] = make_float2(0.f, 0.f);
+            eff[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (on && j < n) {
+                res[j] = read_result(c, (slot + (int64_t)kStep * (j + 1)) * D + d);
+                if (j + 1 < n) eff[j] = read_effect(c, (slot + (int64_t)kStep * (j + 1)) * D + d);
+            }
+        }
+        // the nearest tile whose result is there, and whether the effects of those between are
+        int from = -1;
+        bool open = true;
+#pragma unroll
+        for (int j = 0; j < kBack; ++j) {
+            if (j < n && open && from < 0) {
+                if (__all_sync(0xffffffffu, is_set(res[j].x) && is_set(res[j].y))) from = j;
+                else if (j + 1 == n ||
+                         !__all_sync(0xffffffffu, is_set(eff[j].x) && is_set(eff[j].y) && is_set(eff[j].z) && is_set(eff[j].w)))
+                    open = false;
+            }
+        }
+        if (from >= 0) {
+            S = both(0.f);
+#pragma unroll
+            for (int j = kBack - 1; j >= 0; --j) {
+                if (j == from) S = pair(res[j].x, res[j].y);
+                if (j < from) S = fma(pair(eff[j].x, eff[j].z), S, pair(eff[j].y, eff[j].w));
+            }
+            return true;
+        }
+        if ((tries & 63u) == 63u) {
+            unsigned gave_up;
+            asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(gave_up) : "l"(c.next + 1) : "memory");
+            const uint64_t now = ptx::globaltimer();
+            if (since == 0) since = now;
+            if (__any_sync(0xffffffffu, gave_up != kUnset || now - since > kWaitNs)) {
+                if ((threadIdx.x & 31) == 0) atomicExch(c.next + 1, 1u);
+                return false;
+            }
+        }
+    }
+}
+
+}  // namespace scan
+}  // namespace gla

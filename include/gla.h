@@ -585,7 +585,7 @@ GLA_API int gla_group_norm_bwd(const void *dout, const void *x, const float *wei
  *   D % 8 == 0; all rows together below 2^31 - 256
  * States, decays and sums are f32; a decay near 1 is held as its distance from 1.  Results are rounded once.  A sequence's
  * results do not depend on what else is in the batch, as long as the batch's sizes (B, T, D) are the same.  A NaN or an
- * infinity reaches what the formulas carry it to, and in its own channel and sequence also other tokens of its chunk of 128
+ * infinity reaches what the formulas carry it to, and in its own channel and sequence also other tokens of its chunk of 64
  * where a decay or a product of decays is 0 (0 times it is a NaN).  It reaches no other channel or sequence.
  */
 typedef enum { GLA_SCAN_LOG = 0, GLA_SCAN_LOG_LEAK = 1, GLA_SCAN_SIGMOID = 2, GLA_SCAN_SIGMOID_LEAK = 3 } gla_scan_form;
