@@ -83,11 +83,11 @@ walk_bwd_kernel(const T *__restrict__ x, const TG *__restrict__ g, const T *__re
             }
             dh = dh + back;
             Pair da = leaks(kForm) ? before[t] + xt * both(-1.f) : before[t];
-            da = dh * da * a.a;
-            if (kForm == GLA_SCAN_SIGMOID || kForm == GLA_SCAN_SIGMOID_LEAK) da = da * (a.m * both(-1.f));
+            da = dh * da * whole(a);
+            if (!is_log(kForm)) da = da * rest(a);
             store_two(dg + at, da);
             store_two(dx + at, input<kForm>(a, dh));
-            back = decayed(a, dh, both(0.f));
+            back = decayed(a, dh);
         }
     }
     if (dh0 != nullptr) store_state(dh0 + (int64_t)s * D + d, back);

@@ -56,23 +56,22 @@ __device__ __forceinline__ void store_state(float *p, Pair x) { *reinterpret_cas
 // ---- the decay ---------------------------------------------------------------------------------------------------
 //
 // Long memories need 1 - a more than a: an a of 1 - 1e-4 that is rounded to 2^-25 has 3e-4 of its decay rounded away, and
-// all tokens' alike where g is.  So the decay is held as m = a - 1 where it is near 1, good to a few units of its own last
-// place, and h a is h + m h in one rounding; elsewhere a itself is, so that a strong decay keeps its digits too.
+// all tokens' alike where g is.  So a decay is held as c + k: c = a - 1, good to a few units of its own last place, and k = 1
+// where a is near 1; c = a, so that a strong decay keeps its digits too, and k = 0 elsewhere.  (k h is a NaN where h is an
+// infinity and k = 0; choosing h or 0 instead costs twice the instructions, of which the chunked kernels have few to spare.)
 struct Decay {
-    Pair a, m;      // a, and a - 1
-    bool lo, hi;    // for either channel, whether a is near 1
+    Pair c, k;
 };
 
 template <int kForm>
 __device__ __forceinline__ Decay decay(Pair g) {
-    Decay d;
     const float2 f = parts(g);
+    float c0, c1;
+    bool lo, hi;
     if (kForm == GLA_SCAN_LOG || kForm == GLA_SCAN_LOG_LEAK) {
-        float a0, a1;
         const float2 t = parts(g * both(1.4426950408889634f));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a0) : "f"(t.x));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a1) : "f"(t.y));
-        d.a = pair(a0, a1);
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(c0) : "f"(t.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(c1) : "f"(t.y));
         // e^g - 1 by its series: behind g^6 / 6! the next term is below 2^-24 of the sum for |g| < 0.25
         Pair s = fma(g, both(1.f / 720.f), both(1.f / 120.f));
         s = fma(g, s, both(1.f / 24.f));
@@ -80,31 +79,40 @@ __device__ __forceinline__ Decay decay(Pair g) {
         s = fma(g, s, both(0.5f));
         s = fma(g, s, both(1.f));
         const float2 m = parts(s * g);
-        d.lo = fabsf(f.x) < 0.25f;
-        d.hi = fabsf(f.y) < 0.25f;
-        d.m = pair(d.lo ? m.x : a0 - 1.f, d.hi ? m.y : a1 - 1.f);
+        lo = fabsf(f.x) < 0.25f;
+        hi = fabsf(f.y) < 0.25f;
+        c0 = lo ? m.x : c0;
+        c1 = hi ? m.y : c1;
     } else {
-        Pair rest;
-        sigmoid(g, d.a, rest);
-        d.m = rest * both(-1.f);
-        d.lo = f.x > 1.f;
-        d.hi = f.y > 1.f;
+        // 1 / (1 + e^-g), and 1 less that as e^-g / (1 + e^-g), where e^-g is small
+        float e0, e1;
+        const float2 t = parts(g * both(-1.4426950408889634f));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t.y));
+        const Pair e = pair(e0, e1);
+        const float2 d = parts(e + both(1.f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(c0) : "f"(d.x));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(c1) : "f"(d.y));
+        const float2 r = parts(e * pair(c0, c1));
+        lo = f.x > 1.f;
+        hi = f.y > 1.f;
+        c0 = lo ? -r.x : c0;
+        c1 = hi ? -r.y : c1;
     }
-    return d;
+    return {pair(c0, c1), pair(lo ? 1.f : 0.f, hi ? 1.f : 0.f)};
 }
 __host__ __device__ constexpr bool leaks(int form) { return form == GLA_SCAN_LOG_LEAK || form == GLA_SCAN_SIGMOID_LEAK; }
+__host__ __device__ constexpr bool is_log(int form) { return form == GLA_SCAN_LOG || form == GLA_SCAN_LOG_LEAK; }
 
-// a h + b
-__device__ __forceinline__ Pair decayed(const Decay &d, Pair h, Pair b) {
-    const float2 a = parts(d.a), m = parts(d.m), f = parts(h);
-    const Pair c = pair(d.lo ? m.x : a.x, d.hi ? m.y : a.y);
-    const Pair base = pair(d.lo ? f.x : 0.f, d.hi ? f.y : 0.f);
-    return fma(c, h, base) + b;
-}
+// a h + b, a h, a and 1 - a
+__device__ __forceinline__ Pair decayed(const Decay &d, Pair h, Pair b) { return fma(d.c, h, fma(d.k, h, b)); }
+__device__ __forceinline__ Pair decayed(const Decay &d, Pair h) { return fma(d.c, h, d.k * h); }
+__device__ __forceinline__ Pair whole(const Decay &d) { return d.c + d.k; }
+__device__ __forceinline__ Pair rest(const Decay &d) { return fma(d.c, both(-1.f), fma(d.k, both(-1.f), both(1.f))); }
 // the input's part of h
 template <int kForm>
 __device__ __forceinline__ Pair input(const Decay &d, Pair x) {
-    return leaks(kForm) ? x * (d.m * both(-1.f)) : x;
+    return leaks(kForm) ? x * rest(d) : x;
 }
 
 // Calls RUN(T, TG, kForm, kGate) for a call's types, form and gate.

@@ -2,6 +2,8 @@
 //
 // Of a tile, the states h come from the one before its chunk, and dh from the tiles behind it: dh_t = up_t + D_t with up_t =
 // dout_t act(gate_t) and D_{t-1} = a_t dh_t, an effect D -> A D + C of a row, a warp's rows and a tile like the forward's.
+#include <type_traits>
+
 #include "gla_scan_tiles.cuh"
 
 GLA_DEFINE_STATUS(scan_bwd)
@@ -26,12 +28,12 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
     using namespace ptx;
     using R = Ring<T, TG, kGate>;
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ float4 forth[kWarps][32];   // A, H of each warp's rows
-    __shared__ float2 back[kWarps][32];    // C (A is the same both ways)
+    __shared__ float4 forths[2][kWarps][32];  // A, H of each warp's rows, of this tile and the one before
+    __shared__ float2 backs[2][kWarps][32];   // C (A is the same both ways)
     __shared__ float2 enters[32];
+    __shared__ Window win;
     __shared__ Tile tiles[kMaxStages];
     __shared__ __align__(8) uint64_t full[kMaxStages];
-    __shared__ int gave_up;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = t.D;
     const uint32_t base = smem_u32(ring), bar = smem_u32(full);
     unsigned own = blockIdx.x;
@@ -47,9 +49,9 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
         tma_load_2d(to + R::u, &mu, o.col, o.row, b);
         if (kGate) tma_load_2d(to + R::z, &mz, o.col, o.row, b);
     };
-    const bool orders = threadIdx.x == kTileThreads - 32;  // not of the warp that looks back
+    const bool orders = threadIdx.x == kTileThreads - 32;  // not of the warp that folds what is looked back over
     if (orders) {
-        gave_up = 0;
+        win.gave_up = 0;
         for (int st = 0; st < stages; ++st) mbar_init(bar + 8u * (uint32_t)st, 1);
         fence_mbar_init();
         for (int st = 0; st < stages; ++st) order(st);
@@ -62,73 +64,65 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
                     dh0[(int64_t)s * D + d] = dhT != nullptr ? __ldg(dhT + (int64_t)s * D + d) : 0.f;
     __syncthreads();
 
-    int st = 0;
+    int st = 0, half = 0;
     uint32_t phase = 0;
-    for (bool first = true;; first = false) {
+    bool ok = true;
+    for (bool first = true;; first = false, half ^= 1) {
         const Tile o = tiles[st];
         if (o.row < 0) break;
         const int d = o.col + 2 * lane, n = min(kLane, o.len - warp * kLane);
         const bool on = d < D;
         const int64_t slot_at = (int64_t)o.slot * D + d;
         const Pair begin = on ? load_state(states + slot_at) : both(0.f);
-        if (!mbar_wait(bar + 8u * (uint32_t)st, phase, nullptr, kWaitNs)) {
-            record_status(GLA_ERR_TIMEOUT);
-            gave_up = 1;
-        }
-        const uint8_t *stage = ring + st * R::bytes;
+        if (!mbar_wait(bar + 8u * (uint32_t)st, phase, nullptr, kWaitNs)) win.gave_up = 1;
+        const uint8_t *stage = ring + st * R::bytes + (warp * kLane * kSlab + 2 * lane) * (int)sizeof(T);
+        const uint8_t *stage_g = ring + st * R::bytes + R::g + (warp * kLane * kSlab + 2 * lane) * (int)sizeof(TG);
+        auto &forth = forths[half];
+        auto &back = backs[half];
         // the warp's rows: their decays, dout times the gate's factor and slope, and the rows' effects both ways
         Decay a[kLane];
         Pair up[kLane], us[kGate ? kLane : 1];
-        Pair H = both(0.f), A = both(1.f), C = both(0.f);
+        auto local = [&](auto whole_run, int kind) {
+            Pair H = both(0.f), A = both(1.f), C = both(0.f);
 #pragma unroll
-        for (int i = 0; i < kLane; ++i)
-            if (i < n) {
-                const int at = (warp * kLane + i) * kSlab + 2 * lane;
-                a[i] = decay<kForm>(staged<TG>(stage + R::g, at));
-                H = decayed(a[i], H, input<kForm>(a[i], staged<T>(stage + R::x, at)));
-                A = decayed(a[i], A, both(0.f));
-                up[i] = staged<T>(stage + R::u, at);
-                if (kGate) {
-                    Pair slope;
-                    const Pair f = activation(staged<T>(stage + R::z, at), act, slope);
-                    us[i] = up[i] * slope;
-                    up[i] = up[i] * f;
+            for (int i = 0; i < kLane; ++i)
+                if (whole_run.value || i < n) {
+                    a[i] = decay<kForm>(staged<TG>(stage_g, i * kSlab));
+                    const Pair b = input<kForm>(a[i], staged<T>(stage + R::x, i * kSlab));
+                    H = i == 0 ? b : decayed(a[i], H, b);
+                    A = i == 0 ? whole(a[i]) : decayed(a[i], A);
+                    up[i] = staged<T>(stage + R::u, i * kSlab);
+                    if (kGate) {
+                        Pair slope;
+                        const Pair f = activation(staged<T>(stage + R::z, i * kSlab), kind, slope);
+                        us[i] = up[i] * slope;
+                        up[i] = up[i] * f;
+                    }
                 }
-            }
 #pragma unroll
-        for (int i = kLane - 1; i >= 0; --i)
-            if (i < n) C = decayed(a[i], up[i] + C, both(0.f));
-        {
+            for (int i = kLane - 1; i >= 0; --i)
+                if (whole_run.value || i < n) C = decayed(a[i], up[i] + C);
             const float2 p = parts(A), q = parts(H);
             forth[warp][lane] = make_float4(p.x, p.y, q.x, q.y);
             back[warp][lane] = parts(C);
-        }
+        };
+        if (n < kLane) local(std::false_type{}, act);
+        else if (!kGate || act == kSilu) local(std::true_type{}, kSilu);
+        else if (act == kSigmoid) local(std::true_type{}, kSigmoid);
+        else local(std::true_type{}, kNone);
         __syncthreads();
         if (orders && !first) order(st == 0 ? stages - 1 : st - 1);
-        if (warp == 0) {  // the tile's effect on what comes from behind it, and what does
-            Pair tA = both(1.f), tC = both(0.f);
+        constexpr int kWho = 0;
+        Pair S = both(0.f), tA = both(1.f), tC = both(0.f);
+        if (warp == kWho) {  // the tile's effect on what comes from behind it
             for (int w = kWarps - 1; w >= 0; --w) {
                 const float4 f = forth[w][lane];
                 const float2 c = back[w][lane];
                 tC = fma(pair(f.x, f.y), tC, pair(c.x, c.y));
                 tA = tA * pair(f.x, f.y);
             }
-            Pair S = both(0.f);
-            if (o.behind == 0) {
-                if (on && dhT != nullptr) S = load_state(dhT + (int64_t)o.seq * D + d);
-            } else {
-                if (on && o.chunk > 0) publish_effect(chain, slot_at, tA, tC);
-                if (!look_back<1>(chain, o.slot, D, d, o.behind, S)) {
-                    record_status(GLA_ERR_TIMEOUT);
-                    gave_up = 1;
-                }
-            }
-            const Pair end = fma(tA, S, tC);
-            if (on) {
-                if (o.chunk > 0) publish_result(chain, slot_at, end);
-                else if (dh0 != nullptr) store_state(dh0 + (int64_t)o.seq * D + d, end);
-            }
-            enters[lane] = parts(S);
+            if (on && o.behind > 0 && o.chunk > 0) publish_effect(chain, slot_at, tA, tC);
+            if (on && o.behind == 0 && dhT != nullptr) S = load_state(dhT + (int64_t)o.seq * D + d);
         }
         // the states before the warp's rows
         Pair before[kLane], h = begin;
@@ -137,15 +131,33 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
             h = fma(pair(f.x, f.y), h, pair(f.z, f.w));
         }
         const int64_t out_at = (int64_t)(o.row + warp * kLane) * D + d;
+        auto forwards = [&](auto whole_run) {
+            T *to = kGate ? dgate + out_at : nullptr;
 #pragma unroll
-        for (int i = 0; i < kLane; ++i)
-            if (i < n) {
-                before[i] = h;
-                h = decayed(a[i], h, input<kForm>(a[i], staged<T>(stage + R::x, (warp * kLane + i) * kSlab + 2 * lane)));
-                if (kGate && on) store_two(dgate + out_at + (int64_t)i * D, us[i] * h);
+            for (int i = 0; i < kLane; ++i)
+                if (whole_run.value || i < n) {
+                    before[i] = h;
+                    if (kGate || i + 1 < kLane) h = decayed(a[i], h, input<kForm>(a[i], staged<T>(stage + R::x, i * kSlab)));
+                    if (kGate) {
+                        if (on) store_two(to, us[i] * h);
+                        to += D;
+                    }
+                }
+        };
+        if (n == kLane) forwards(std::true_type{});
+        else forwards(std::false_type{});
+        if (o.behind > 0) ok = look_back<1, kWho>(chain, win, o.slot, D, d, min(o.behind, t.window), S);
+        if (warp == kWho) {
+            const Pair end = fma(tA, S, tC);
+            if (on) {
+                if (o.chunk > 0) publish_result(chain, slot_at, end);
+                else if (dh0 != nullptr) store_state(dh0 + (int64_t)o.seq * D + d, end);
             }
+            enters[lane] = parts(S);
+        }
         __syncthreads();
-        if (gave_up) break;
+        ok = ok && !win.gave_up;
+        if (!ok) break;
         const float2 e = enters[lane];
         Pair K = pair(e.x, e.y);
         for (int w = kWarps - 1; w > warp; --w) {
@@ -153,43 +165,55 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
             const float2 c = back[w][lane];
             K = fma(pair(f.x, f.y), K, pair(c.x, c.y));
         }
+        auto backwards = [&](auto whole_run) {
+            const int64_t last = out_at + (int64_t)(kLane - 1) * D;
+            T *to = dx + last;
+            TG *to_g = dg + last;
 #pragma unroll
-        for (int i = kLane - 1; i >= 0; --i)
-            if (i < n) {
-                const Pair dh = up[i] + K;
-                Pair da = before[i];
-                if (leaks(kForm)) da = da + staged<T>(stage + R::x, (warp * kLane + i) * kSlab + 2 * lane) * both(-1.f);
-                da = dh * da * a[i].a;
-                if (kForm == GLA_SCAN_SIGMOID || kForm == GLA_SCAN_SIGMOID_LEAK) da = da * (a[i].m * both(-1.f));
-                if (on) {
-                    store_two(dg + out_at + (int64_t)i * D, da);
-                    store_two(dx + out_at + (int64_t)i * D, input<kForm>(a[i], dh));
+            for (int i = kLane - 1; i >= 0; --i) {
+                if (whole_run.value || i < n) {
+                    const Pair dh = up[i] + K, w = rest(a[i]);
+                    Pair da = before[i];
+                    if (leaks(kForm)) da = fma(staged<T>(stage + R::x, i * kSlab), both(-1.f), da);
+                    da = dh * da * whole(a[i]);
+                    if (!is_log(kForm)) da = da * w;
+                    if (on) {
+                        store_two(to_g, da);
+                        store_two(to, leaks(kForm) ? w * dh : dh);
+                    }
+                    if (i > 0) K = decayed(a[i], dh);
                 }
-                K = decayed(a[i], dh, both(0.f));
+                to -= D;
+                to_g -= D;
             }
-        __syncthreads();  // forth and back are written again
+        };
+        if (n == kLane) backwards(std::true_type{});
+        else backwards(std::false_type{});
         if (++st == stages) {
             st = 0;
             phase ^= 1;
         }
     }
     // a block that gave up waits for what it has ordered
-    if (gave_up && threadIdx.x == 0)
-        for (int i = 0; i < stages; ++i) {
+    if (!ok && threadIdx.x == 0) {
+        record_status(GLA_ERR_TIMEOUT);
+        for (int i = 1; i < stages; ++i) {
             if (++st == stages) {
                 st = 0;
                 phase ^= 1;
             }
-            if (i + 1 < stages && tiles[st].row >= 0) mbar_wait(bar + 8u * (uint32_t)st, phase, nullptr, kWaitNs);
+            if (tiles[st].row >= 0) mbar_wait(bar + 8u * (uint32_t)st, phase, nullptr, kWaitNs);
         }
+    }
 }
 
 template <typename T, typename TG, int kForm, bool kGate>
-bool launch(const Shape &p, const Tiles &t, const Chain &chain, const T *x, const TG *g, const T *gate, const T *dout,
+bool launch(const Shape &p, Tiles t, const Chain &chain, const T *x, const TG *g, const T *gate, const T *dout,
             const float *dhT, const float *states, T *dx, TG *dg, T *dgate, float *dh0, cudaStream_t st) {
     using R = Ring<T, TG, kGate>;
     constexpr Room room = room_for(R::bytes, kPerSm);
     constexpr int bytes = room.stages * R::bytes;
+    static_assert(room.stages >= 2, "a stage is refilled while the next one is read");
     constexpr auto kKernel = tiles_bwd_kernel<T, TG, kForm, kGate>;
     CUtensorMap mx, mg, mu, mz;
     if (!tile_map(&mx, x, p) || !tile_map(&mg, g, p) || !tile_map(&mu, dout, p) || !tile_map(&mz, kGate ? gate : x, p)) return false;
@@ -197,6 +221,7 @@ bool launch(const Shape &p, const Tiles &t, const Chain &chain, const T *x, cons
     int64_t grid = (int64_t)device_info().sm_count * room.per_sm;
     if (grid > (int64_t)t.total) grid = t.total;
     if (grid < 1) grid = 1;
+    t.window = window_for(t, grid);
     kKernel<<<(unsigned)grid, kTileThreads, bytes, st>>>(mx, mg, mu, mz, dhT, states, dx, dg, dgate, dh0, t, chain, p.act,
                                                          room.stages);
     count_launches(1);

@@ -1,4 +1,6 @@
 // gla_scan_fwd.cu — the gated recurrence over chunks (see gla_scan_tiles.cuh): one pass over x, g and gate.
+#include <type_traits>
+
 #include "gla_scan_tiles.cuh"
 
 GLA_DEFINE_STATUS(scan_fwd)
@@ -7,7 +9,7 @@ namespace gla {
 namespace scan {
 namespace {
 
-constexpr int kPerSm = 1024 / kTileThreads;  // blocks that the registers allow
+constexpr int kPerSm = 768 / kTileThreads;  // blocks that the registers allow
 
 template <typename T, typename TG, bool kGate> struct Ring {
     static constexpr int x = 0, g = tile_bytes<T>(), z = g + tile_bytes<TG>();
@@ -24,9 +26,9 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ float4 effects[kWarps][32];
     __shared__ float2 enters[32];
+    __shared__ Window win;
     __shared__ Tile tiles[kMaxStages];
     __shared__ __align__(8) uint64_t full[kMaxStages];
-    __shared__ int gave_up;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = t.D;
     const uint32_t base = smem_u32(ring), bar = smem_u32(full);
     unsigned own = blockIdx.x;
@@ -37,12 +39,12 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
         if (o.row < 0) return;
         const uint32_t to = base + (uint32_t)(st * R::bytes), b = bar + 8u * (uint32_t)st;
         mbar_expect_tx(b, R::bytes);
-        tma_load_2d(to + R::x, &mx, o.col, o.row, b);
         tma_load_2d(to + R::g, &mg, o.col, o.row, b);
+        tma_load_2d(to + R::x, &mx, o.col, o.row, b);
         if (kGate) tma_load_2d(to + R::z, &mz, o.col, o.row, b);
     };
     if (threadIdx.x == 0) {
-        gave_up = 0;
+        win.gave_up = 0;
         for (int st = 0; st < stages; ++st) mbar_init(bar + 8u * (uint32_t)st, 1);
         fence_mbar_init();
         for (int st = 0; st < stages; ++st) order(st);
@@ -57,30 +59,34 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
 
     int st = 0;
     uint32_t phase = 0;
+    bool ok = true;
     for (bool first = true;; first = false) {
         const Tile o = tiles[st];
         if (o.row < 0) break;
-        if (!mbar_wait(bar + 8u * (uint32_t)st, phase, nullptr, kWaitNs)) {
-            record_status(GLA_ERR_TIMEOUT);
-            gave_up = 1;
-        }
-        const uint8_t *stage = ring + st * R::bytes;
+        if (!mbar_wait(bar + 8u * (uint32_t)st, phase, nullptr, kWaitNs)) win.gave_up = 1;
+        const uint8_t *stage = ring + st * R::bytes + (warp * kLane * kSlab + 2 * lane) * (int)sizeof(T);
+        const uint8_t *stage_g = ring + st * R::bytes + R::g + (warp * kLane * kSlab + 2 * lane) * (int)sizeof(TG);
         const int d = o.col + 2 * lane, n = min(kLane, o.len - warp * kLane);  // the warp's rows, none or fewer where n < 8
         // the warp's rows from a zero state: h, and the product of the decays up to each
-        Pair h[kLane], P[kLane], hh = both(0.f), PP = both(1.f);
+        Pair h[kLane], P[kLane];
+        auto local = [&](auto whole_run) {
+            Pair hh = both(0.f), PP = both(1.f);
 #pragma unroll
-        for (int i = 0; i < kLane; ++i) {
-            if (i < n) {
-                const int at = (warp * kLane + i) * kSlab + 2 * lane;
-                const Decay a = decay<kForm>(staged<TG>(stage + R::g, at));
-                hh = decayed(a, hh, input<kForm>(a, staged<T>(stage + R::x, at)));
-                PP = decayed(a, PP, both(0.f));
+            for (int i = 0; i < kLane; ++i) {
+                if (whole_run.value || i < n) {
+                    const Decay a = decay<kForm>(staged<TG>(stage_g, i * kSlab));
+                    const Pair b = input<kForm>(a, staged<T>(stage + R::x, i * kSlab));
+                    hh = i == 0 ? b : decayed(a, hh, b);
+                    PP = i == 0 ? whole(a) : decayed(a, PP);
+                }
+                h[i] = hh;
+                P[i] = PP;
             }
-            h[i] = hh;
-            P[i] = PP;
-        }
+        };
+        if (n == kLane) local(std::true_type{});
+        else local(std::false_type{});
         {
-            const float2 a = parts(PP), b = parts(hh);
+            const float2 a = parts(P[kLane - 1]), b = parts(h[kLane - 1]);
             effects[warp][lane] = make_float4(a.x, a.y, b.x, b.y);
         }
         __syncthreads();
@@ -93,22 +99,19 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
             H = fma(a, H, pair(f.z, f.w));
             A = A * a;
         }
-        if (warp == kWarps - 1) {
-            const Pair tA = A * PP, tH = fma(PP, H, hh);
-            const int64_t at = (int64_t)o.slot * D + d;
-            const bool on = d < D;
-            Pair S = both(0.f);
-            if (o.chunk == 0) {
-                if (on && h0 != nullptr) S = load_state(h0 + (int64_t)o.seq * D + d);
-            } else {
-                if (on && o.behind > 0) publish_effect(chain, at, tA, tH);
-                if (!look_back<-1>(chain, o.slot, D, d, o.chunk, S)) {
-                    record_status(GLA_ERR_TIMEOUT);
-                    gave_up = 1;
-                }
-            }
+        const int64_t at = (int64_t)o.slot * D + d;
+        constexpr int kWho = kWarps - 1;  // the warp that has all of the tile's effect
+        const Pair tA = A * P[kLane - 1], tH = fma(P[kLane - 1], H, h[kLane - 1]);
+        Pair S = both(0.f);
+        if (o.chunk > 0) {
+            if (warp == kWho && d < D && o.behind > 0) publish_effect(chain, at, tA, tH);
+            ok = look_back<-1, kWho>(chain, win, o.slot, D, d, min(o.chunk, t.window), S);
+        } else if (warp == kWho && d < D && h0 != nullptr) {
+            S = load_state(h0 + (int64_t)o.seq * D + d);
+        }
+        if (warp == kWho) {
             const Pair end = fma(tA, S, tH);
-            if (on) {
+            if (d < D) {
                 if (o.behind > 0) publish_result(chain, at, end);
                 else if (hT != nullptr) store_state(hT + (int64_t)o.seq * D + d, end);
                 if (states != nullptr) store_state(states + at, S);
@@ -116,19 +119,26 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
             enters[lane] = parts(S);
         }
         __syncthreads();
-        if (gave_up) break;
+        ok = ok && !win.gave_up;
+        if (!ok) break;
         if (out != nullptr && d < D) {
             const float2 e = enters[lane];
-            const Pair S = fma(A, pair(e.x, e.y), H);
+            S = fma(A, pair(e.x, e.y), H);
             T *to = out + (int64_t)(o.row + warp * kLane) * D + d;
+            auto emit = [&](auto whole_run, int kind) {
 #pragma unroll
-            for (int i = 0; i < kLane; ++i) {
-                if (i < n) {
-                    Pair y = fma(P[i], S, h[i]);
-                    if (kGate) y = y * activation(staged<T>(stage + R::z, (warp * kLane + i) * kSlab + 2 * lane), act);
-                    store_two(to + (int64_t)i * D, y);
-                }
-            }
+                for (int i = 0; i < kLane; ++i)
+                    if (whole_run.value || i < n) {
+                        Pair y = fma(P[i], S, h[i]);
+                        if (kGate) y = y * activation(staged<T>(stage + R::z, i * kSlab), kind);
+                        store_two(to, y);
+                        to += D;
+                    }
+            };
+            if (n < kLane) emit(std::false_type{}, act);
+            else if (!kGate || act == kSilu) emit(std::true_type{}, kSilu);
+            else if (act == kSigmoid) emit(std::true_type{}, kSigmoid);
+            else emit(std::true_type{}, kNone);
         }
         if (++st == stages) {
             st = 0;
@@ -136,22 +146,25 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
         }
     }
     // a block that gave up waits for what it has ordered
-    if (gave_up && threadIdx.x == 0)
-        for (int i = 0; i < stages; ++i) {
+    if (!ok && threadIdx.x == 0) {
+        record_status(GLA_ERR_TIMEOUT);
+        for (int i = 1; i < stages; ++i) {
             if (++st == stages) {
                 st = 0;
                 phase ^= 1;
             }
-            if (i + 1 < stages && tiles[st].row >= 0) mbar_wait(bar + 8u * (uint32_t)st, phase, nullptr, kWaitNs);
+            if (tiles[st].row >= 0) mbar_wait(bar + 8u * (uint32_t)st, phase, nullptr, kWaitNs);
         }
+    }
 }
 
 template <typename T, typename TG, int kForm, bool kGate>
-bool launch(const Shape &p, const Tiles &t, const Chain &chain, const T *x, const TG *g, const T *gate, const float *h0, T *out,
+bool launch(const Shape &p, Tiles t, const Chain &chain, const T *x, const TG *g, const T *gate, const float *h0, T *out,
             float *hT, float *states, cudaStream_t st) {
     using R = Ring<T, TG, kGate>;
     constexpr Room room = room_for(R::bytes, kPerSm);
     constexpr int bytes = room.stages * R::bytes;
+    static_assert(room.stages >= 2, "a stage is refilled while the next one is read");
     constexpr auto kKernel = tiles_fwd_kernel<T, TG, kForm, kGate>;
     CUtensorMap mx, mg, mz;
     if (!tile_map(&mx, x, p) || !tile_map(&mg, g, p) || !tile_map(&mz, kGate ? gate : x, p)) return false;
@@ -159,6 +172,7 @@ bool launch(const Shape &p, const Tiles &t, const Chain &chain, const T *x, cons
     int64_t grid = (int64_t)device_info().sm_count * room.per_sm;
     if (grid > (int64_t)t.total) grid = t.total;
     if (grid < 1) grid = 1;
+    t.window = window_for(t, grid);
     kKernel<<<(unsigned)grid, kTileThreads, bytes, st>>>(mx, mg, mz, h0, out, hT, states, t, chain, p.act, room.stages);
     count_launches(1);
     return true;

@@ -28,7 +28,7 @@ constexpr int kTileThreads = kWarps * 32;
 constexpr int kSlab = 64;                    // channels of a tile
 constexpr uint32_t kUnset = 0xffffffffu;     // a NaN that no result is: one that would be is stored as another
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s a wait
-constexpr int kBack = 4;                     // tiles that a look back reads at once
+constexpr int kBack = 2 * kWarps;            // tiles that a look back reads at once, at most
 
 // The chunks' effects and results, for one direction.
 struct Chain {
@@ -43,9 +43,10 @@ struct Tiles {
     int D, slabs, nslots, per_seq;  // per_seq: chunks of a sequence of a dense batch
     unsigned total;
     int chained;                    // whether any sequence may have more than one chunk
+    int window;                     // tiles that a look back reads at once
 };
 __host__ inline Tiles make_tiles(const Shape &p, const Sequences &q) {
-    Tiles t{q, p.D, (p.D + kSlab - 1) / kSlab, (int)slots(p), (p.T + kChunk - 1) / kChunk, 0, 1};
+    Tiles t{q, p.D, (p.D + kSlab - 1) / kSlab, (int)slots(p), (p.T + kChunk - 1) / kChunk, 0, 1, 1};
     t.total = p.cu ? (unsigned)t.nslots * (unsigned)t.slabs : (unsigned)t.per_seq * (unsigned)p.nseq * (unsigned)t.slabs;
     t.chained = p.cu != nullptr || p.T > kChunk;
     return t;
@@ -97,40 +98,6 @@ __device__ __forceinline__ Tile next_tile(const Tiles &t, const Chain &c, unsign
     }
 }
 
-// ---- launches --------------------------------------------------------------------------------------------------------
-
-// Blocks of an SM and stages of a block: as many blocks as the threads' registers allow and two stages each leave room for.
-struct Room {
-    int per_sm, stages;
-};
-constexpr int kMaxStages = 4;
-constexpr Room room_for(int stage_bytes, int most) {
-    const int room = 225 * 1024, fixed = kWarps * 512 * 2 + 1024;
-    int per_sm = room / (2 * stage_bytes + fixed);
-    per_sm = per_sm > most ? most : per_sm;
-    int stages = (room / per_sm - fixed) / stage_bytes;
-    return {per_sm, stages > kMaxStages ? kMaxStages : stages};
-}
-
-// The map of an array [rows, D] for boxes of a tile.
-template <typename T> bool tile_map(CUtensorMap *m, const T *at, const Shape &p) {
-    return make_map_2d(m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                       (uint32_t)sizeof(T), at, (uint64_t)p.D, (uint64_t)total_rows(p), kSlab, kChunk,
-                       CU_TENSOR_MAP_SWIZZLE_NONE);
-}
-
-// Lets a kernel use so many bytes of dynamic shared memory; asked of the runtime once per kernel and device.
-template <auto kKernel> bool allow_dynamic(int bytes) {
-    constexpr int kDevices = 64;
-    static std::atomic<bool> allowed[kDevices];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    if (dev < kDevices && allowed[dev].load(std::memory_order_acquire)) return true;
-    if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-    if (dev < kDevices) allowed[dev].store(true, std::memory_order_release);
-    return true;
-}
-
 // two channels of a staged tile
 template <typename T> __device__ __forceinline__ Pair staged(const uint8_t *tile, int at) {
     return Two<T>::open(*reinterpret_cast<const typename Two<T>::Raw *>(tile + at * (int)sizeof(T)));
@@ -166,57 +133,112 @@ __device__ __forceinline__ float2 read_result(const Chain &c, int64_t at) {
     return f;
 }
 
-// The state that enters a tile from the `behind` tiles on its chain's other side (at > 0), by a whole warp; kStep is how far
-// a neighbour's slot lies off.  A channel past the last has nothing to wait for.  False when the wait gave up.
-template <int kStep>
-__device__ __forceinline__ bool look_back(const Chain &c, int64_t slot, int D, int d, int behind, Pair &S) {
-    const bool on = d < D;
+// The state that enters a tile from the `n` tiles that are looked back over, by the whole block; kStep is how far a
+// neighbour's slot lies off.  Each warp reads two of them at most, so that one trip to memory serves all.  Warp kWho has the
+// state; a channel past the last has nothing to wait for.  False, for all threads, when the wait gave up.
+struct Window {
+    float4 effect[kBack][32];
+    float2 result[kBack][32];
+    int ready[kBack];  // 1: the result, 2: the effect
+    int gave_up;
+};
+template <int kStep, int kWho>
+__device__ __forceinline__ bool look_back(const Chain &c, Window &win, int64_t slot, int D, int d, int n, Pair &S) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint64_t since = 0;
     for (unsigned tries = 0;; ++tries) {
-        float2 res[kBack];
-        float4 eff[kBack];
-        const int n = min(behind, kBack);
+        float2 res[2] = {};
+        float4 eff[2] = {};
 #pragma unroll
-        for (int j = 0; j < kBack; ++j) {
-            res[j] = make_float2(0.f, 0.f);
-            eff[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (on && j < n) {
-                res[j] = read_result(c, (slot + (int64_t)kStep * (j + 1)) * D + d);
-                if (j + 1 < n) eff[j] = read_effect(c, (slot + (int64_t)kStep * (j + 1)) * D + d);
+        for (int i = 0; i < 2; ++i) {
+            const int j = warp + i * kWarps;
+            if (j < n && d < D) {
+                const int64_t at = (slot + (int64_t)kStep * (j + 1)) * D + d;
+                res[i] = read_result(c, at);
+                if (j + 1 < n) eff[i] = read_effect(c, at);
             }
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = warp + i * kWarps;
+            if (j < n) {
+                win.result[j][lane] = res[i];
+                win.effect[j][lane] = eff[i];
+                const bool r = __all_sync(0xffffffffu, is_set(res[i].x) && is_set(res[i].y));
+                const bool e = __all_sync(0xffffffffu, is_set(eff[i].x) && is_set(eff[i].y) && is_set(eff[i].z) && is_set(eff[i].w));
+                if (lane == 0) win.ready[j] = (r ? 1 : 0) + (e ? 2 : 0);
+            }
+        }
+        __syncthreads();
         // the nearest tile whose result is there, and whether the effects of those between are
-        int from = -1;
-        bool open = true;
-#pragma unroll
-        for (int j = 0; j < kBack; ++j) {
-            if (j < n && open && from < 0) {
-                if (__all_sync(0xffffffffu, is_set(res[j].x) && is_set(res[j].y))) from = j;
-                else if (j + 1 == n ||
-                         !__all_sync(0xffffffffu, is_set(eff[j].x) && is_set(eff[j].y) && is_set(eff[j].z) && is_set(eff[j].w)))
-                    open = false;
-            }
-        }
-        if (from >= 0) {
-            S = both(0.f);
-#pragma unroll
-            for (int j = kBack - 1; j >= 0; --j) {
-                if (j == from) S = pair(res[j].x, res[j].y);
-                if (j < from) S = fma(pair(eff[j].x, eff[j].z), S, pair(eff[j].y, eff[j].w));
+        const int word = lane < n ? win.ready[lane] : 0;
+        const unsigned r = __ballot_sync(0xffffffffu, word & 1), e = __ballot_sync(0xffffffffu, word & 2);
+        const unsigned between = (r & (0u - r)) - 1u;
+        if (r != 0 && (e & between) == between) {
+            if (warp == kWho) {
+                int j = __ffs(r) - 1;
+                const float2 f = win.result[j][lane];
+                S = pair(f.x, f.y);
+                for (--j; j >= 0; --j) {
+                    const float4 t = win.effect[j][lane];
+                    S = fma(pair(t.x, t.z), S, pair(t.y, t.w));
+                }
             }
             return true;
         }
-        if ((tries & 63u) == 63u) {
+        if (threadIdx.x == 0 && (tries & 63u) == 63u) {
             unsigned gave_up;
             asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(gave_up) : "l"(c.next + 1) : "memory");
             const uint64_t now = ptx::globaltimer();
             if (since == 0) since = now;
-            if (__any_sync(0xffffffffu, gave_up != kUnset || now - since > kWaitNs)) {
-                if ((threadIdx.x & 31) == 0) atomicExch(c.next + 1, 1u);
-                return false;
+            if (gave_up != kUnset || now - since > kWaitNs) {
+                atomicExch(c.next + 1, 1u);
+                win.gave_up = 1;
             }
         }
+        __syncthreads();
+        if (win.gave_up) return false;
     }
+}
+
+// ---- launches --------------------------------------------------------------------------------------------------------
+
+// Blocks of an SM and stages of a block: as many blocks as the threads' registers allow and two stages each leave room for.
+struct Room {
+    int per_sm, stages;
+};
+constexpr int kMaxStages = 4;
+constexpr Room room_for(int stage_bytes, int most) {
+    const int room = 225 * 1024, fixed = (int)sizeof(Window) + kWarps * 1536 + 2048;  // beside the stages
+    int per_sm = room / (2 * stage_bytes + fixed);
+    per_sm = per_sm > most ? most : per_sm;
+    int stages = (room / per_sm - fixed) / stage_bytes;
+    return {per_sm, stages > kMaxStages ? kMaxStages : stages};
+}
+
+// The map of an array [rows, D] for boxes of a tile.
+template <typename T> bool tile_map(CUtensorMap *m, const T *at, const Shape &p) {
+    return make_map_2d(m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                       (uint32_t)sizeof(T), at, (uint64_t)p.D, (uint64_t)total_rows(p), kSlab, kChunk,
+                       CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// Tiles that a look back reads at once: about those of its chain that are worked on at the same time.
+inline int window_for(const Tiles &t, int64_t grid) {
+    const int64_t chains = t.q.rows == nullptr ? (int64_t)t.q.nseq * t.slabs : t.slabs, w = grid / chains + 2;
+    return (int)(w < kBack ? w : kBack);
+}
+
+// Lets a kernel use so many bytes of dynamic shared memory; asked of the runtime once per kernel and device.
+template <auto kKernel> bool allow_dynamic(int bytes) {
+    constexpr int kDevices = 64;
+    static std::atomic<bool> allowed[kDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < kDevices && allowed[dev].load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    if (dev < kDevices) allowed[dev].store(true, std::memory_order_release);
+    return true;
 }
 
 }  // namespace scan
