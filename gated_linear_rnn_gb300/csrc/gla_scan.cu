@@ -40,10 +40,9 @@ walk_fwd_kernel(const T *__restrict__ x, const TG *__restrict__ g, const T *__re
     if (d >= D) return;
     const int2 r = rows_of(q, s);
     Pair h = h0 != nullptr ? load_state(h0 + (int64_t)s * D + d) : both(0.f);
-    const int64_t slot = (int64_t)r.x / kChunk + s;
     for (int t = 0; t < r.y; ++t) {
         const int64_t at = (int64_t)(r.x + t) * D + d;
-        if (states != nullptr && t % kChunk == 0) store_state(states + (slot + t / kChunk) * D + d, h);
+        if (states != nullptr && t % kRun == 0) store_state(states + state_slot(r.x, s, t) * D + d, h);
         const Decay a = decay<kForm>(load_two(g + at));
         h = decayed(a, h, input<kForm>(a, load_two(x + at)));
         if (out != nullptr) store_two(out + at, kGate ? h * activation(load_two(gate + at), act) : h);
@@ -60,35 +59,39 @@ walk_bwd_kernel(const T *__restrict__ x, const TG *__restrict__ g, const T *__re
     if (d >= D) return;
     const int2 r = rows_of(q, s);
     Pair back = dhT != nullptr ? load_state(dhT + (int64_t)s * D + d) : both(0.f);
-    const int64_t slot = (int64_t)r.x / kChunk + s;
-    Pair before[kChunk];
-    for (int c = (r.y + kChunk - 1) / kChunk - 1; c >= 0; --c) {
-        const int n = min(kChunk, r.y - c * kChunk);
-        const int64_t first = (int64_t)(r.x + c * kChunk) * D + d;
-        Pair h = load_state(states + (slot + c) * D + d);
-        for (int t = 0; t < n; ++t) {
-            before[t] = h;
-            const Decay a = decay<kForm>(load_two(g + first + (int64_t)t * D));
-            h = decayed(a, h, input<kForm>(a, load_two(x + first + (int64_t)t * D)));
-        }
-        for (int t = n - 1; t >= 0; --t) {
-            const int64_t at = first + (int64_t)t * D;
-            const Decay a = decay<kForm>(load_two(g + at));
-            const Pair xt = load_two(x + at), up = load_two(dout + at);
-            Pair dh = up;
-            if (kGate) {
-                Pair slope;
-                dh = up * activation(load_two(gate + at), act, slope);
-                store_two(dgate + at, up * decayed(a, before[t], input<kForm>(a, xt)) * slope);
+    for (int c = (r.y + kRun - 1) / kRun - 1; c >= 0; --c) {
+        const int n = min(kRun, r.y - c * kRun);
+        const int64_t first = (int64_t)(r.x + c * kRun) * D + d;
+        Pair h = load_state(states + state_slot(r.x, s, c * kRun) * D + d), before[kRun], in[kRun];
+        Decay a[kRun];
+#pragma unroll
+        for (int t = 0; t < kRun; ++t)
+            if (t < n) {
+                const int64_t at = first + (int64_t)t * D;
+                a[t] = decay<kForm>(load_two(g + at));
+                in[t] = load_two(x + at);
+                before[t] = h;
+                h = decayed(a[t], h, input<kForm>(a[t], in[t]));
             }
-            dh = dh + back;
-            Pair da = leaks(kForm) ? before[t] + xt * both(-1.f) : before[t];
-            da = dh * da * whole(a);
-            if (!is_log(kForm)) da = da * rest(a);
-            store_two(dg + at, da);
-            store_two(dx + at, input<kForm>(a, dh));
-            back = decayed(a, dh);
-        }
+#pragma unroll
+        for (int t = kRun - 1; t >= 0; --t)
+            if (t < n) {
+                const int64_t at = first + (int64_t)t * D;
+                const Pair up = load_two(dout + at);
+                Pair dh = up;
+                if (kGate) {
+                    Pair slope;
+                    dh = up * activation(load_two(gate + at), act, slope);
+                    store_two(dgate + at, up * slope * decayed(a[t], before[t], input<kForm>(a[t], in[t])));
+                }
+                dh = dh + back;
+                Pair da = leaks(kForm) ? fma(in[t], both(-1.f), before[t]) : before[t];
+                da = dh * (da * whole(a[t]));
+                if (!is_log(kForm)) da = da * rest(a[t]);
+                store_two(dg + at, da);
+                store_two(dx + at, input<kForm>(a[t], dh));
+                back = decayed(a[t], dh);
+            }
     }
     if (dh0 != nullptr) store_state(dh0 + (int64_t)s * D + d, back);
 }

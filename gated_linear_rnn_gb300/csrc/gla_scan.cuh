@@ -11,8 +11,10 @@
 namespace gla {
 namespace scan {
 
-// Rows of a chunk: the state before each one is what a forward keeps for the gradient.
-constexpr int kChunk = 64;
+constexpr int kChunk = 64;  // rows of a chunk
+// Rows of a run.  The state before every run is what a forward keeps for the gradient: half a byte for each element, for which
+// the gradient's kernel needs neither the states before a chunk nor a second walk through its rows.
+constexpr int kRun = 8;
 
 struct Shape {
     int nseq, T, D;
@@ -21,7 +23,11 @@ struct Shape {
 };
 __host__ inline int64_t total_rows(const Shape &p) { return p.cu ? (int64_t)p.T : (int64_t)p.nseq * p.T; }
 __host__ inline int64_t slots(const Shape &p) { return chunk_slots(total_rows(p), p.nseq, kChunk); }
-__host__ inline int64_t states_bytes(const Shape &p) { return slots(p) * p.D * (int64_t)sizeof(float); }
+__host__ inline int64_t states_bytes(const Shape &p) {
+    return chunk_slots(total_rows(p), p.nseq, kRun) * p.D * (int64_t)sizeof(float);
+}
+// where the state before a sequence's rows t .. t + kRun - 1 is kept; start: the sequence's first row
+__device__ __forceinline__ int64_t state_slot(int start, int seq, int t) { return (int64_t)(start / kRun) + seq + t / kRun; }
 
 // ---- two neighbouring channels of one row ------------------------------------------------------------------------
 template <typename T> struct Two;

@@ -1,7 +1,8 @@
-// gla_scan_bwd.cu — the gradient of the gated recurrence over chunks (see gla_scan_tiles.cuh), from the states before them.
+// gla_scan_bwd.cu — the gradient of the gated recurrence over chunks (see gla_scan_tiles.cuh), from the states before runs.
 //
-// Of a tile, the states h come from the one before its chunk, and dh from the tiles behind it: dh_t = up_t + D_t with up_t =
+// A warp's states h come from the one before its rows, and dh from what is behind them: dh_t = up_t + D_t with up_t =
 // dout_t act(gate_t) and D_{t-1} = a_t dh_t, an effect D -> A D + C of a row, a warp's rows and a tile like the forward's.
+// Everything but dh is found on the way there, so that little is left for the rows once it is known.
 #include <type_traits>
 
 #include "gla_scan_tiles.cuh"
@@ -28,18 +29,17 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
     using namespace ptx;
     using R = Ring<T, TG, kGate>;
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ float4 forths[2][kWarps][32];  // A, H of each warp's rows, of this tile and the one before
-    __shared__ float2 backs[2][kWarps][32];   // C (A is the same both ways)
+    __shared__ float4 both_effects[2][kWarps][32];  // of this tile and the one before
     __shared__ float2 enters[32];
     __shared__ Window win;
     __shared__ Tile tiles[kMaxStages];
     __shared__ __align__(8) uint64_t full[kMaxStages];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = t.D;
     const uint32_t base = smem_u32(ring), bar = smem_u32(full);
-    unsigned own = blockIdx.x;
+    Turns<false> turns;
 
     auto order = [&](int st) {  // by one thread
-        tiles[st] = next_tile<false>(t, chain, own);
+        tiles[st] = turns.next(t, chain);
         const Tile &o = tiles[st];
         if (o.row < 0) return;
         const uint32_t to = base + (uint32_t)(st * R::bytes), b = bar + 8u * (uint32_t)st;
@@ -52,6 +52,7 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
     const bool orders = threadIdx.x == kTileThreads - 32;  // not of the warp that folds what is looked back over
     if (orders) {
         win.gave_up = 0;
+        turns.start(t, chain);
         for (int st = 0; st < stages; ++st) mbar_init(bar + 8u * (uint32_t)st, 1);
         fence_mbar_init();
         for (int st = 0; st < stages; ++st) order(st);
@@ -64,93 +65,85 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
                     dh0[(int64_t)s * D + d] = dhT != nullptr ? __ldg(dhT + (int64_t)s * D + d) : 0.f;
     __syncthreads();
 
+    // the state before the warp's rows of a tile, asked for a tile ahead
+    auto state_of = [&](const Tile &o) {
+        const int d = o.col + 2 * lane, t = warp * kLane;
+        if (o.row < 0 || d >= D || t >= o.len) return both(0.f);
+        return load_state(states + state_slot(o.start(), o.seq, o.chunk * kChunk + t) * D + d);
+    };
     int st = 0, half = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (bool first = true;; first = false, half ^= 1) {
+    Pair next = state_of(tiles[0]);
+    for (;; half ^= 1) {
         const Tile o = tiles[st];
         if (o.row < 0) break;
         const int d = o.col + 2 * lane, n = min(kLane, o.len - warp * kLane);
         const bool on = d < D;
-        const int64_t slot_at = (int64_t)o.slot * D + d;
-        const Pair begin = on ? load_state(states + slot_at) : both(0.f);
+        const int64_t at = (int64_t)o.slot * D + d, out_at = (int64_t)(o.row + warp * kLane) * D + d;
+        Pair h = next;
         if (!mbar_wait(bar + 8u * (uint32_t)st, phase, nullptr, kWaitNs)) win.gave_up = 1;
         const uint8_t *stage = ring + st * R::bytes + (warp * kLane * kSlab + 2 * lane) * (int)sizeof(T);
         const uint8_t *stage_g = ring + st * R::bytes + R::g + (warp * kLane * kSlab + 2 * lane) * (int)sizeof(TG);
-        auto &forth = forths[half];
-        auto &back = backs[half];
-        // the warp's rows: their decays, dout times the gate's factor and slope, and the rows' effects both ways
+        auto &effects = both_effects[half];
+        // the warp's rows: their decays, dout times the gate's factor, dg without dh, and the rows' effect
         Decay a[kLane];
-        Pair up[kLane], us[kGate ? kLane : 1];
+        Pair up[kLane], da[kLane];
         auto local = [&](auto whole_run, int kind) {
-            Pair H = both(0.f), A = both(1.f), C = both(0.f);
+            T *to = kGate ? dgate + out_at : nullptr;
+            Pair A = both(1.f), C = both(0.f);
 #pragma unroll
             for (int i = 0; i < kLane; ++i)
                 if (whole_run.value || i < n) {
                     a[i] = decay<kForm>(staged<TG>(stage_g, i * kSlab));
-                    const Pair b = input<kForm>(a[i], staged<T>(stage + R::x, i * kSlab));
-                    H = i == 0 ? b : decayed(a[i], H, b);
+                    const Pair x = staged<T>(stage + R::x, i * kSlab), w = rest(a[i]);
                     A = i == 0 ? whole(a[i]) : decayed(a[i], A);
+                    da[i] = whole(a[i]) * (leaks(kForm) ? fma(x, both(-1.f), h) : h);
+                    if (!is_log(kForm)) da[i] = da[i] * w;
+                    h = decayed(a[i], h, leaks(kForm) ? w * x : x);
                     up[i] = staged<T>(stage + R::u, i * kSlab);
                     if (kGate) {
                         Pair slope;
                         const Pair f = activation(staged<T>(stage + R::z, i * kSlab), kind, slope);
-                        us[i] = up[i] * slope;
+                        if (on) store_two(to, up[i] * slope * h);
                         up[i] = up[i] * f;
+                        to += D;
                     }
                 }
 #pragma unroll
             for (int i = kLane - 1; i >= 0; --i)
                 if (whole_run.value || i < n) C = decayed(a[i], up[i] + C);
-            const float2 p = parts(A), q = parts(H);
-            forth[warp][lane] = make_float4(p.x, p.y, q.x, q.y);
-            back[warp][lane] = parts(C);
+            const float2 p = parts(A), q = parts(C);
+            effects[warp][lane] = make_float4(p.x, p.y, q.x, q.y);
         };
         if (n < kLane) local(std::false_type{}, act);
         else if (!kGate || act == kSilu) local(std::true_type{}, kSilu);
         else if (act == kSigmoid) local(std::true_type{}, kSigmoid);
         else local(std::true_type{}, kNone);
         __syncthreads();
-        if (orders && !first) order(st == 0 ? stages - 1 : st - 1);
+        if (orders) order(st);  // all of the stage is read
         constexpr int kWho = 0;
-        Pair S = both(0.f), tA = both(1.f), tC = both(0.f);
-        if (warp == kWho) {  // the tile's effect on what comes from behind it
-            for (int w = kWarps - 1; w >= 0; --w) {
-                const float4 f = forth[w][lane];
-                const float2 c = back[w][lane];
-                tC = fma(pair(f.x, f.y), tC, pair(c.x, c.y));
-                tA = tA * pair(f.x, f.y);
+        Pair bA = both(1.f), bC = both(0.f), S = both(0.f);  // the effect of the warps behind this one, and what enters the tile
+#pragma unroll
+        for (int w = kWarps - 1; w > 0; --w)
+            if (w > warp) {
+                const float4 f = effects[w][lane];
+                bC = fma(pair(f.x, f.y), bC, pair(f.z, f.w));
+                bA = bA * pair(f.x, f.y);
             }
-            if (on && o.behind > 0 && o.chunk > 0) publish_effect(chain, slot_at, tA, tC);
+        Pair tA, tC;
+        if (warp == kWho) {  // the tile's effect
+            const float4 f = effects[kWho][lane];
+            tC = fma(pair(f.x, f.y), bC, pair(f.z, f.w));
+            tA = bA * pair(f.x, f.y);
+            if (on && o.behind > 0 && o.chunk > 0) publish_effect(chain, at, tA, tC);
             if (on && o.behind == 0 && dhT != nullptr) S = load_state(dhT + (int64_t)o.seq * D + d);
         }
-        // the states before the warp's rows
-        Pair before[kLane], h = begin;
-        for (int w = 0; w < warp; ++w) {
-            const float4 f = forth[w][lane];
-            h = fma(pair(f.x, f.y), h, pair(f.z, f.w));
-        }
-        const int64_t out_at = (int64_t)(o.row + warp * kLane) * D + d;
-        auto forwards = [&](auto whole_run) {
-            T *to = kGate ? dgate + out_at : nullptr;
-#pragma unroll
-            for (int i = 0; i < kLane; ++i)
-                if (whole_run.value || i < n) {
-                    before[i] = h;
-                    if (kGate || i + 1 < kLane) h = decayed(a[i], h, input<kForm>(a[i], staged<T>(stage + R::x, i * kSlab)));
-                    if (kGate) {
-                        if (on) store_two(to, us[i] * h);
-                        to += D;
-                    }
-                }
-        };
-        if (n == kLane) forwards(std::true_type{});
-        else forwards(std::false_type{});
         if (o.behind > 0) ok = look_back<1, kWho>(chain, win, o.slot, D, d, min(o.behind, t.window), S);
         if (warp == kWho) {
             const Pair end = fma(tA, S, tC);
             if (on) {
-                if (o.chunk > 0) publish_result(chain, slot_at, end);
+                if (o.chunk > 0) publish_result(chain, at, end);
                 else if (dh0 != nullptr) store_state(dh0 + (int64_t)o.seq * D + d, end);
             }
             enters[lane] = parts(S);
@@ -159,36 +152,25 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
         ok = ok && !win.gave_up;
         if (!ok) break;
         const float2 e = enters[lane];
-        Pair K = pair(e.x, e.y);
-        for (int w = kWarps - 1; w > warp; --w) {
-            const float4 f = forth[w][lane];
-            const float2 c = back[w][lane];
-            K = fma(pair(f.x, f.y), K, pair(c.x, c.y));
-        }
+        Pair K = fma(bA, pair(e.x, e.y), bC);
+        next = state_of(tiles[st + 1 == stages ? 0 : st + 1]);
         auto backwards = [&](auto whole_run) {
-            const int64_t last = out_at + (int64_t)(kLane - 1) * D;
-            T *to = dx + last;
-            TG *to_g = dg + last;
+            T *to = dx + out_at + (int64_t)(kLane - 1) * D;
+            TG *to_g = dg + out_at + (int64_t)(kLane - 1) * D;
 #pragma unroll
             for (int i = kLane - 1; i >= 0; --i) {
                 if (whole_run.value || i < n) {
-                    const Pair dh = up[i] + K, w = rest(a[i]);
-                    Pair da = before[i];
-                    if (leaks(kForm)) da = fma(staged<T>(stage + R::x, i * kSlab), both(-1.f), da);
-                    da = dh * da * whole(a[i]);
-                    if (!is_log(kForm)) da = da * w;
-                    if (on) {
-                        store_two(to_g, da);
-                        store_two(to, leaks(kForm) ? w * dh : dh);
-                    }
+                    const Pair dh = up[i] + K;
+                    store_two(to_g, dh * da[i]);
+                    store_two(to, input<kForm>(a[i], dh));
                     if (i > 0) K = decayed(a[i], dh);
                 }
                 to -= D;
                 to_g -= D;
             }
         };
-        if (n == kLane) backwards(std::true_type{});
-        else backwards(std::false_type{});
+        if (on && n == kLane) backwards(std::true_type{});
+        else if (on && n > 0) backwards(std::false_type{});
         if (++st == stages) {
             st = 0;
             phase ^= 1;
@@ -197,7 +179,7 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
     // a block that gave up waits for what it has ordered
     if (!ok && threadIdx.x == 0) {
         record_status(GLA_ERR_TIMEOUT);
-        for (int i = 1; i < stages; ++i) {
+        for (int i = 0; i < stages; ++i) {
             if (++st == stages) {
                 st = 0;
                 phase ^= 1;
@@ -213,7 +195,7 @@ bool launch(const Shape &p, Tiles t, const Chain &chain, const T *x, const TG *g
     using R = Ring<T, TG, kGate>;
     constexpr Room room = room_for(R::bytes, kPerSm);
     constexpr int bytes = room.stages * R::bytes;
-    static_assert(room.stages >= 2, "a stage is refilled while the next one is read");
+    static_assert(room.stages >= 2, "a tile is worked on while the next one comes in");
     constexpr auto kKernel = tiles_bwd_kernel<T, TG, kForm, kGate>;
     CUtensorMap mx, mg, mu, mz;
     if (!tile_map(&mx, x, p) || !tile_map(&mg, g, p) || !tile_map(&mu, dout, p) || !tile_map(&mz, kGate ? gate : x, p)) return false;

@@ -24,30 +24,41 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
     using namespace ptx;
     using R = Ring<T, TG, kGate>;
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ float4 effects[kWarps][32];
+    __shared__ float4 both_effects[2][kWarps][32];  // of this tile and the one before
     __shared__ float2 enters[32];
     __shared__ Window win;
     __shared__ Tile tiles[kMaxStages];
     __shared__ __align__(8) uint64_t full[kMaxStages];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = t.D;
     const uint32_t base = smem_u32(ring), bar = smem_u32(full);
-    unsigned own = blockIdx.x;
+    Turns<true> turns;
 
-    auto order = [&](int st) {  // by one thread
-        tiles[st] = next_tile<true>(t, chain, own);
+    // by one thread: the next tile into a stage; its gate, which a tile's last part reads, later than the rest
+    auto order = [&](int st) {
+        tiles[st] = turns.next(t, chain);
         const Tile &o = tiles[st];
         if (o.row < 0) return;
         const uint32_t to = base + (uint32_t)(st * R::bytes), b = bar + 8u * (uint32_t)st;
-        mbar_expect_tx(b, R::bytes);
+        mbar_expect_tx(b, R::z);
         tma_load_2d(to + R::g, &mg, o.col, o.row, b);
         tma_load_2d(to + R::x, &mx, o.col, o.row, b);
-        if (kGate) tma_load_2d(to + R::z, &mz, o.col, o.row, b);
+    };
+    auto order_gate = [&](int st) {
+        const Tile &o = tiles[st];
+        if (!kGate || o.row < 0) return;
+        const uint32_t b = bar + 8u * (uint32_t)st;
+        mbar_expect_tx(b, R::bytes - R::z);
+        tma_load_2d(base + (uint32_t)(st * R::bytes + R::z), &mz, o.col, o.row, b);
     };
     if (threadIdx.x == 0) {
         win.gave_up = 0;
-        for (int st = 0; st < stages; ++st) mbar_init(bar + 8u * (uint32_t)st, 1);
+        turns.start(t, chain);
+        for (int st = 0; st < stages; ++st) mbar_init(bar + 8u * (uint32_t)st, kGate ? 2 : 1);
         fence_mbar_init();
-        for (int st = 0; st < stages; ++st) order(st);
+        for (int st = 0; st < stages; ++st) {
+            order(st);
+            order_gate(st);
+        }
     }
     // sequences without tokens pass their state on
     if (hT != nullptr)
@@ -57,16 +68,17 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
                     hT[(int64_t)s * D + d] = h0 != nullptr ? __ldg(h0 + (int64_t)s * D + d) : 0.f;
     __syncthreads();
 
-    int st = 0;
+    int st = 0, half = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (bool first = true;; first = false) {
+    for (bool first = true;; first = false, half ^= 1) {
         const Tile o = tiles[st];
         if (o.row < 0) break;
         if (!mbar_wait(bar + 8u * (uint32_t)st, phase, nullptr, kWaitNs)) win.gave_up = 1;
         const uint8_t *stage = ring + st * R::bytes + (warp * kLane * kSlab + 2 * lane) * (int)sizeof(T);
         const uint8_t *stage_g = ring + st * R::bytes + R::g + (warp * kLane * kSlab + 2 * lane) * (int)sizeof(TG);
         const int d = o.col + 2 * lane, n = min(kLane, o.len - warp * kLane);  // the warp's rows, none or fewer where n < 8
+        auto &effects = both_effects[half];
         // the warp's rows from a zero state: h, and the product of the decays up to each
         Pair h[kLane], P[kLane];
         auto local = [&](auto whole_run) {
@@ -90,40 +102,41 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
             effects[warp][lane] = make_float4(a.x, a.y, b.x, b.y);
         }
         __syncthreads();
-        // the tile of the round before is done: its stage takes the next one
-        if (threadIdx.x == 0 && !first) order(st == 0 ? stages - 1 : st - 1);
-        Pair A = both(1.f), H = both(0.f);  // the effect of the warps before this one
-        for (int w = 0; w < warp; ++w) {
-            const float4 f = effects[w][lane];
-            const Pair a = pair(f.x, f.y);
-            H = fma(a, H, pair(f.z, f.w));
-            A = A * a;
+        // x and g are read, and the tile of the round before is done
+        if (threadIdx.x == 0) {
+            order(st);
+            if (!first) order_gate(st == 0 ? stages - 1 : st - 1);
         }
         const int64_t at = (int64_t)o.slot * D + d;
-        constexpr int kWho = kWarps - 1;  // the warp that has all of the tile's effect
-        const Pair tA = A * P[kLane - 1], tH = fma(P[kLane - 1], H, h[kLane - 1]);
-        Pair S = both(0.f);
-        if (o.chunk > 0) {
-            if (warp == kWho && d < D && o.behind > 0) publish_effect(chain, at, tA, tH);
-            ok = look_back<-1, kWho>(chain, win, o.slot, D, d, min(o.chunk, t.window), S);
-        } else if (warp == kWho && d < D && h0 != nullptr) {
-            S = load_state(h0 + (int64_t)o.seq * D + d);
+        constexpr int kWho = kWarps - 1;
+        Pair A = both(1.f), H = both(0.f), S = both(0.f);  // the effect of the warps before this one, and what enters the tile
+        for (int w = 0; w < warp; ++w) {
+            const float4 f = effects[w][lane];
+            H = fma(pair(f.x, f.y), H, pair(f.z, f.w));
+            A = A * pair(f.x, f.y);
         }
+        const Pair tA = A * P[kLane - 1], tH = fma(P[kLane - 1], H, h[kLane - 1]);
+        if (warp == kWho && d < D) {  // tA and tH are the tile's effect
+            if (o.chunk > 0 && o.behind > 0) publish_effect(chain, at, tA, tH);
+            if (o.chunk == 0 && h0 != nullptr) S = load_state(h0 + (int64_t)o.seq * D + d);
+        }
+        if (o.chunk > 0) ok = look_back<-1, kWho>(chain, win, o.slot, D, d, min(o.chunk, t.window), S);
         if (warp == kWho) {
             const Pair end = fma(tA, S, tH);
             if (d < D) {
                 if (o.behind > 0) publish_result(chain, at, end);
                 else if (hT != nullptr) store_state(hT + (int64_t)o.seq * D + d, end);
-                if (states != nullptr) store_state(states + at, S);
             }
             enters[lane] = parts(S);
         }
         __syncthreads();
         ok = ok && !win.gave_up;
         if (!ok) break;
-        if (out != nullptr && d < D) {
+        if (d < D && n > 0) {
             const float2 e = enters[lane];
             S = fma(A, pair(e.x, e.y), H);
+            if (states != nullptr)
+                store_state(states + state_slot(o.start(), o.seq, o.chunk * kChunk + warp * kLane) * D + d, S);
             T *to = out + (int64_t)(o.row + warp * kLane) * D + d;
             auto emit = [&](auto whole_run, int kind) {
 #pragma unroll
@@ -135,7 +148,8 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
                         to += D;
                     }
             };
-            if (n < kLane) emit(std::false_type{}, act);
+            if (out == nullptr) {
+            } else if (n < kLane) emit(std::false_type{}, act);
             else if (!kGate || act == kSilu) emit(std::true_type{}, kSilu);
             else if (act == kSigmoid) emit(std::true_type{}, kSigmoid);
             else emit(std::true_type{}, kNone);
@@ -148,7 +162,8 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
     // a block that gave up waits for what it has ordered
     if (!ok && threadIdx.x == 0) {
         record_status(GLA_ERR_TIMEOUT);
-        for (int i = 1; i < stages; ++i) {
+        order_gate(st);
+        for (int i = 0; i < stages; ++i) {
             if (++st == stages) {
                 st = 0;
                 phase ^= 1;
@@ -164,7 +179,7 @@ bool launch(const Shape &p, Tiles t, const Chain &chain, const T *x, const TG *g
     using R = Ring<T, TG, kGate>;
     constexpr Room room = room_for(R::bytes, kPerSm);
     constexpr int bytes = room.stages * R::bytes;
-    static_assert(room.stages >= 2, "a stage is refilled while the next one is read");
+    static_assert(room.stages >= 2, "a tile is worked on while the next one comes in");
     constexpr auto kKernel = tiles_fwd_kernel<T, TG, kForm, kGate>;
     CUtensorMap mx, mg, mz;
     if (!tile_map(&mx, x, p) || !tile_map(&mg, g, p) || !tile_map(&mz, kGate ? gate : x, p)) return false;

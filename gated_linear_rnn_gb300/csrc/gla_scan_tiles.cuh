@@ -22,7 +22,7 @@ bool make_map_2d(CUtensorMap *m, CUtensorMapDataType dtype, uint32_t elem_bytes,
                  uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle sw);
 namespace scan {
 
-constexpr int kLane = 8;                     // rows of a warp
+constexpr int kLane = kRun;                  // rows of a warp
 constexpr int kWarps = kChunk / kLane;
 constexpr int kTileThreads = kWarps * 32;
 constexpr int kSlab = 64;                    // channels of a tile
@@ -54,6 +54,7 @@ __host__ inline Tiles make_tiles(const Shape &p, const Sequences &q) {
 
 struct Tile {
     int row, len, chunk, behind, seq, slot, col;  // behind: its sequence's chunks after it; col: its first channel
+    __device__ int start() const { return row - chunk * kChunk; }  // its sequence's first row
 };
 
 // Tile k in the order of a direction; false for slots that no chunk has.  A dense batch goes through all sequences' first
@@ -82,21 +83,31 @@ __device__ __forceinline__ bool tile_at(const Tiles &t, unsigned k, Tile &o) {
     return true;
 }
 
-// The next tile of a block, by one thread; row < 0 when there are no more.
+// A block's tiles, by one thread.  The number of the tile after the next one is asked for ahead: the counter takes as long to
+// answer as memory does.
 template <bool kForth>
-__device__ __forceinline__ Tile next_tile(const Tiles &t, const Chain &c, unsigned &own) {
-    Tile o;
-    for (;;) {
-        unsigned k = own;
-        if (t.chained) k = atomicAdd(c.next, 1u) + 1u;  // the counter starts at kUnset
-        else own += gridDim.x;
-        if (k >= t.total) {
-            o.row = -1;
-            return o;
-        }
-        if (tile_at<kForth>(t, k, o)) return o;
+struct Turns {
+    unsigned ahead;
+    __device__ __forceinline__ void take(const Tiles &t, const Chain &c) {
+        if (t.chained) ahead = atomicAdd(c.next, 1u) + 1u;  // the counter starts at kUnset
+        else ahead += gridDim.x;
     }
-}
+    __device__ __forceinline__ void start(const Tiles &t, const Chain &c) {
+        ahead = blockIdx.x;
+        if (t.chained) take(t, c);
+    }
+    // the next tile; row < 0 when there are no more
+    __device__ __forceinline__ Tile next(const Tiles &t, const Chain &c) {
+        Tile o;
+        for (;;) {
+            const unsigned k = ahead;
+            o.row = -1;
+            if (k >= t.total) return o;
+            take(t, c);
+            if (tile_at<kForth>(t, k, o)) return o;
+        }
+    }
+};
 
 // two channels of a staged tile
 template <typename T> __device__ __forceinline__ Pair staged(const uint8_t *tile, int at) {
