@@ -9,40 +9,50 @@
 //     e = du post_weight,   dy = uq (e - mean(e) - uh mean(e uh)), or du
 //     dweight = sum of dout h, dbias = sum of dout, dpost_weight = sum of du uh, dpost_bias = sum of du
 //
-// A row is one block's, or a part of a warp's where it is short; a thread keeps the same channels for all of its rows, so the
-// sums over tokens stay in registers until its last row.
+// Both are bound by HBM.  A row is one block's, or a part of a warp's where it is short; a thread takes four neighbouring
+// channels at a time and keeps the same ones for all of its rows, so the gradient's sums over tokens stay in registers until
+// its last row.  Rows come into shared memory by bulk copies, some rows ahead, and are read from there by each step that needs
+// them: what is in flight and what a later step needs costs no registers, of which the sums take most.  Rows that two stages
+// have no room for are read from memory each time.
 #include "gla_act.cuh"
+#include "sm100_ptx.cuh"
+
+GLA_DEFINE_STATUS(resnorm)
 
 namespace gla {
 namespace resnorm {
 namespace {
 
 constexpr int kSums = 5;  // dscale, dpost_weight, dpost_bias, dweight, dbias
+constexpr int kMaxStages = 6;
+constexpr int kRowsThreads = 256;  // of a block with several rows
+constexpr uint64_t kWaitNs = 2000000000ull;
 
-// Threads to a row (whole warps above 32) and vectors of four channels to a thread.
+// Threads to a row (whole warps above 32), vectors of four channels to a thread, rows of a block at a time.
 struct Plan {
-    int lanes, vecs, rows, threads;  // rows: of a block at a time
+    int lanes, vecs, rows, threads;
 };
 
-Plan make_plan(int D) {
+Plan make_plan(int D, int vecs) {
     const int nv = D / 4;
     Plan p{};
-    p.vecs = nv <= 2048 ? (nv <= 32 ? 1 : 2) : 4;
+    p.vecs = (nv + vecs - 1) / vecs <= 1024 ? vecs : 4;
     const int need = (nv + p.vecs - 1) / p.vecs;
     p.lanes = 1;
     if (need <= 32)
         while (p.lanes < need) p.lanes *= 2;
     else
         p.lanes = (need + 31) / 32 * 32;
-    p.rows = p.lanes <= 32 ? 128 / p.lanes : 1;
+    p.rows = p.lanes <= 32 ? kRowsThreads / p.lanes : 1;
     p.threads = p.lanes * p.rows;
     return p;
 }
+constexpr int kFwdVecs = 4, kBwdVecs = 2;
 
 template <typename T> struct Four;  // four channels of one row
 template <> struct Four<__nv_bfloat16> {
     using Raw = uint2;
-    static __device__ __forceinline__ void open(Raw w, Pair (&x)[2]) {
+    static __device__ __forceinline__ void open(Pair (&x)[2], Raw w) {
         x[0] = pair(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u));
         x[1] = pair(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
     }
@@ -54,7 +64,7 @@ template <> struct Four<__nv_bfloat16> {
 };
 template <> struct Four<float> {
     using Raw = float4;
-    static __device__ __forceinline__ void open(Raw w, Pair (&x)[2]) {
+    static __device__ __forceinline__ void open(Pair (&x)[2], Raw w) {
         x[0] = pair(w.x, w.y);
         x[1] = pair(w.z, w.w);
     }
@@ -63,6 +73,9 @@ template <> struct Four<float> {
         return make_float4(f.x, f.y, g.x, g.y);
     }
 };
+template <typename T> __device__ __forceinline__ void put(T *to, const Pair (&x)[2]) {
+    __stcs(reinterpret_cast<typename Four<T>::Raw *>(to), Four<T>::close(x));
+}
 
 // A thread's place: its row in the block, its first channel and how many of its vectors exist.
 struct Place {
@@ -76,25 +89,10 @@ struct Place {
     }
 };
 
-template <typename T, int kVec>
-__device__ __forceinline__ void fetch(Pair (&v)[kVec][2], const T *from, int64_t at, const Place &pl, bool has) {
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-        if (has && j < pl.count)
-            Four<T>::open(__ldcs(reinterpret_cast<const typename Four<T>::Raw *>(from + at + pl.channel + j * pl.stride)), v[j]);
-        else v[j][0] = v[j][1] = both(0.f);
-    }
-}
-template <typename T>
-__device__ __forceinline__ void put(T *to, int64_t at, const Place &pl, int j, const Pair (&x)[2]) {
-    __stcs(reinterpret_cast<typename Four<T>::Raw *>(to + at + pl.channel + j * pl.stride), Four<T>::close(x));
-}
-// four parameters of vector j, or a constant where there are none
-__device__ __forceinline__ void param(Pair (&v)[2], const float *from, const Place &pl, int j, float otherwise) {
-    float4 f = make_float4(otherwise, otherwise, otherwise, otherwise);
-    if (from != nullptr && j < pl.count) f = __ldg(reinterpret_cast<const float4 *>(from + pl.channel + j * pl.stride));
-    v[0] = pair(f.x, f.y);
-    v[1] = pair(f.z, f.w);
+// Four parameters, or a constant where there are none.
+__device__ __forceinline__ void param(Pair (&v)[2], const float *from, int channel, float otherwise) {
+    if (from != nullptr) Four<float>::open(v, __ldg(reinterpret_cast<const float4 *>(from + channel)));
+    else v[0] = v[1] = both(otherwise);
 }
 
 // Two sums over a row's threads at once.  Rows of more than a warp meet in shared memory, in one half of it after the other,
@@ -103,200 +101,383 @@ struct Meeting {
     float2 at[2][32];
 };
 __device__ __forceinline__ float2 row_sum(float2 s, int lanes, Meeting &m, int &half) {
-    for (int d = min(lanes, 32) >> 1; d > 0; d >>= 1) {
-        s.x += __shfl_xor_sync(0xffffffffu, s.x, d);
-        s.y += __shfl_xor_sync(0xffffffffu, s.y, d);
-    }
-    if (lanes > 32) {
-        if ((threadIdx.x & 31) == 0) m.at[half][threadIdx.x >> 5] = s;
-        __syncthreads();
-        s = make_float2(0.f, 0.f);
-        for (int w = 0; w < lanes >> 5; ++w) {
-            s.x += m.at[half][w].x;
-            s.y += m.at[half][w].y;
+    if (lanes < 32) {
+        for (int d = lanes >> 1; d > 0; d >>= 1) {
+            s.x += __shfl_xor_sync(0xffffffffu, s.x, d);
+            s.y += __shfl_xor_sync(0xffffffffu, s.y, d);
         }
-        half ^= 1;
+        return s;
     }
+    // one half of the warp adds the one sum up, the other half the other
+    const bool upper = threadIdx.x & 16;
+    float v = (upper ? s.y : s.x) + __shfl_xor_sync(0xffffffffu, upper ? s.x : s.y, 16);
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if (lanes == 32) {
+        const float o = __shfl_xor_sync(0xffffffffu, v, 16);
+        return upper ? make_float2(o, v) : make_float2(v, o);
+    }
+    if ((threadIdx.x & 15) == 0) reinterpret_cast<float *>(&m.at[half][threadIdx.x >> 5])[upper] = v;
+    __syncthreads();
+    s = make_float2(0.f, 0.f);
+    const int warps = lanes >> 5;
+#pragma unroll 4
+    for (int w = 0; w < warps; w += 2) {  // the one past an odd number is zero
+        const float4 f = *reinterpret_cast<const float4 *>(&m.at[half][w]);
+        s.x += f.x + f.z;
+        s.y += f.y + f.w;
+    }
+    half ^= 1;
     return s;
 }
+__device__ __forceinline__ void clear(Meeting &m) {
+    if (threadIdx.x < 32) m.at[0][threadIdx.x] = m.at[1][threadIdx.x] = make_float2(0.f, 0.f);
+}
 
-// v becomes n(v) without its root; returns the root's reciprocal.  An absent vector stays zero.
-template <int kVec>
-__device__ __forceinline__ float centre(Pair (&v)[kVec][2], const Place &pl, int kind, float inv, float eps, int lanes,
-                                        Meeting &m, int &half) {
-    if (kind == GLA_NORM_LAYER) {
-        Pair s = both(0.f);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) s = s + (v[j][0] + v[j][1]);
-        const float mean = row_sum(make_float2(total(s), 0.f), lanes, m, half).x * inv;
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            const Pair less = both(j < pl.count ? -mean : 0.f);
-            v[j][0] = v[j][0] + less;
-            v[j][1] = v[j][1] + less;
+// Arrays whose rows come in, and the stages that they come into: a block's rows of each array at a time.
+template <int kArrays> struct Inputs {
+    const void *from[kArrays];  // null: absent
+    int row_bytes[kArrays], at[kArrays];
+    int stage_bytes, stages;
+};
+
+// The rows of a block, one item (its rows at a time) after the other.
+template <bool kStage, int kArrays>
+struct Rows {
+    const Inputs<kArrays> &in;
+    uint8_t *ring;
+    uint64_t *full;
+    int *failed;
+    int64_t rows, items, item;
+    int step, st;
+    uint32_t phase;
+    bool first;
+    __device__ __forceinline__ Rows(const Inputs<kArrays> &in_, uint8_t *ring_, uint64_t *full_, int *failed_, int64_t rows_, int lanes)
+        : in(in_), ring(ring_), full(full_), failed(failed_), rows(rows_), item(blockIdx.x), step(blockDim.x / lanes), st(0), phase(0),
+          first(true) {
+        items = (rows + step - 1) / step;
+        if (!kStage) return;
+        if (threadIdx.x == 0) {
+            *failed = 0;
+            for (int i = 0; i < in.stages; ++i) ptx::mbar_init(ptx::smem_u32(full + i), 1);
+            ptx::fence_mbar_init();
+            for (int i = 0; i < in.stages; ++i) order(i, item + i * (int64_t)gridDim.x);
         }
     }
-    Pair s = both(0.f);
+    // by one thread
+    __device__ __forceinline__ void order(int to_stage, int64_t k) const {
+        if (k >= items) return;
+        const uint32_t b = ptx::smem_u32(full + to_stage), to = ptx::smem_u32(ring) + (uint32_t)(to_stage * in.stage_bytes);
+        const int n = (int)min((int64_t)step, rows - k * step);
+        uint32_t bytes = 0;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) s = fma(v[j][0], v[j][0], fma(v[j][1], v[j][1], s));
-    return rsqrtf(fmaf(row_sum(make_float2(total(s), 0.f), lanes, m, half).x, inv, eps));
-}
+        for (int i = 0; i < kArrays; ++i)
+            if (in.from[i] != nullptr) bytes += (uint32_t)(n * in.row_bytes[i]);
+        ptx::mbar_expect_tx(b, bytes);
+#pragma unroll
+        for (int i = 0; i < kArrays; ++i)
+            if (in.from[i] != nullptr)
+                ptx::bulk_load_g2s(to + (uint32_t)in.at[i], (const uint8_t *)in.from[i] + k * step * in.row_bytes[i],
+                                   (uint32_t)(n * in.row_bytes[i]), b);
+    }
+    __device__ __forceinline__ bool more() const { return item < items; }
+    __device__ __forceinline__ void arrive() const {
+        if (kStage && !ptx::mbar_wait(ptx::smem_u32(full + st), phase, failed, kWaitNs)) *(volatile int *)failed = 1;
+    }
+    // All threads of the block are past the item before: its stage takes another one.
+    __device__ __forceinline__ void refill() const {
+        if (kStage && threadIdx.x == 0 && !first) order(st == 0 ? in.stages - 1 : st - 1, item + (in.stages - 1) * (int64_t)gridDim.x);
+    }
+    __device__ __forceinline__ void next() {
+        first = false;
+        item += gridDim.x;
+        if (kStage && ++st == in.stages) {
+            st = 0;
+            phase ^= 1u;
+        }
+    }
+    // what a block that gave up has ordered still comes in
+    __device__ __forceinline__ void end() const {
+        if (kStage && threadIdx.x == 0 && *(volatile int *)failed) {
+            record_status(GLA_ERR_TIMEOUT);
+            for (int i = 0; i < in.stages; ++i) ptx::mbar_wait(ptx::smem_u32(full + i), phase ^ (uint32_t)(i < st), nullptr, kWaitNs);
+        }
+    }
+    // four channels of array i
+    template <typename T> __device__ __forceinline__ void get(Pair (&v)[2], int i, int row_in_item, int D, int channel) const {
+        using Raw = typename Four<T>::Raw;
+        if (kStage)
+            Four<T>::open(v, *reinterpret_cast<const Raw *>(ring + st * in.stage_bytes + in.at[i] +
+                                                            (row_in_item * D + channel) * (int)sizeof(T)));
+        else
+            Four<T>::open(v, __ldg(reinterpret_cast<const Raw *>((const T *)in.from[i] + (item * step + row_in_item) * D + channel)));
+    }
+};
 
 struct Weights {
     const float *scale, *post_weight, *post_bias, *weight, *bias;
 };
 
-template <typename T, typename TS, int kVec>
-__global__ void __launch_bounds__(1024)
-fwd_kernel(const TS *__restrict__ x, const T *__restrict__ y, const T *__restrict__ gate, Weights w, int kind, int post, int act,
-           float eps, TS *__restrict__ r, T *__restrict__ out, int64_t rows, int D, int lanes) {
-    __shared__ Meeting meet;
+// The mean (of a layer norm; else 0) and the reciprocal root of one or two arrays' rows: GET(0 or 1, j, v) reads vector j.
+template <int kVec, class Get>
+__device__ __forceinline__ void statistics(Get get, bool one, bool two, int count, int kind, float inv, float eps, int lanes, Meeting &m,
+                                           int &half, float2 &mean, float2 &root) {
+    mean = make_float2(0.f, 0.f);
+    if (kind == GLA_NORM_LAYER) {
+        Pair s = both(0.f), t = both(0.f), v[2];
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (j < count) {
+                if (one) get(0, j, v), s = s + (v[0] + v[1]);
+                if (two) get(1, j, v), t = t + (v[0] + v[1]);
+            }
+        mean = row_sum(make_float2(total(s), total(t)), lanes, m, half);
+        mean.x *= inv, mean.y *= inv;
+    }
+    Pair s = both(0.f), t = both(0.f), v[2];
+    const Pair a = both(-mean.x), b = both(-mean.y);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+        if (j < count) {
+            if (one) {
+                get(0, j, v);
+                v[0] = v[0] + a, v[1] = v[1] + a;
+                s = fma(v[0], v[0], fma(v[1], v[1], s));
+            }
+            if (two) {
+                get(1, j, v);
+                v[0] = v[0] + b, v[1] = v[1] + b;
+                t = fma(v[0], v[0], fma(v[1], v[1], t));
+            }
+        }
+    root = row_sum(make_float2(total(s), total(t)), lanes, m, half);
+    root.x = rsqrtf(fmaf(root.x, inv, eps)), root.y = rsqrtf(fmaf(root.y, inv, eps));
+}
+
+template <typename T, typename TS, int kVec, bool kStage, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads <= 256 ? 3 : 1)
+fwd_kernel(Inputs<3> in, Weights w, int kind, int post, int act, float eps, TS *__restrict__ r, T *__restrict__ out, int64_t rows,
+           int D, int lanes) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ uint64_t full[kMaxStages];
+    __shared__ int failed;
+    __shared__ __align__(16) Meeting meet;
     int half = 0;
     const Place pl(D, lanes);
-    const int step = blockDim.x / lanes;
     const float inv = 1.f / (float)D;
-    for (int64_t r0 = (int64_t)blockIdx.x * step; r0 < rows; r0 += (int64_t)gridDim.x * step) {
-        const int64_t row = r0 + pl.row, at = row * D;
-        const bool on = row < rows;
+    const bool has_y = in.from[1] != nullptr, has_gate = in.from[2] != nullptr;
+    const bool meets = lanes > 32 && (post || out != nullptr);
+    Rows<kStage, 3> it(in, ring, full, &failed, rows, lanes);
+    clear(meet);
+    __syncthreads();
+    for (; it.more(); it.next()) {
+        if (!meets) {
+            __syncthreads();
+            it.refill();
+        }
+        it.arrive();
+        const int64_t row = it.item * it.step + pl.row, at = row * D + pl.channel;
+        const int count = row < rows ? pl.count : 0;
+        Pair q = both(1.f), m = both(0.f);
+        if (post) {
+            float2 mean, root;
+            statistics<kVec>([&](int, int j, Pair (&v)[2]) { it.template get<T>(v, 1, pl.row, D, pl.channel + j * pl.stride); }, true,
+                             false, count, kind, inv, eps, lanes, meet, half, mean, root);
+            q = both(root.x), m = both(-mean.x);
+            if (meets) it.refill();
+        }
         Pair v[kVec][2];
-        fetch<TS, kVec>(v, x, at, pl, on);
-        if (y != nullptr) {
-            Pair u[kVec][2], g[kVec][2];
-            fetch<T, kVec>(u, y, at, pl, on);
-            if (gate != nullptr) fetch<T, kVec>(g, gate, at, pl, on);
-            Pair q = both(1.f);
-            if (post) q = both(centre<kVec>(u, pl, kind, inv, eps, lanes, meet, half));
+        if (has_y) {
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
-                Pair pw[2], pb[2], sc[2];
-                param(pw, w.post_weight, pl, j, 1.f);
-                param(pb, w.post_bias, pl, j, 0.f);
-                param(sc, w.scale, pl, j, 1.f);
+                v[j][0] = v[j][1] = both(0.f);
+                if (j < count) {
+                    const int c = pl.channel + j * pl.stride;
+                    Pair u[2], g[2], a[2], b[2];
+                    it.template get<TS>(v[j], 0, pl.row, D, c);
+                    it.template get<T>(u, 1, pl.row, D, c);
+                    if (post) {
+                        param(a, w.post_weight, c, 1.f);
+                        param(b, w.post_bias, c, 0.f);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (post) u[j][e] = fma(u[j][e] * q, pw[e], pb[e]);
-                    if (gate != nullptr) u[j][e] = u[j][e] * activation(g[j][e], act);
-                    v[j][e] = w.scale != nullptr ? fma(u[j][e], sc[e], v[j][e]) : v[j][e] + u[j][e];
+                        for (int e = 0; e < 2; ++e) u[e] = fma((u[e] + m) * q, a[e], b[e]);
+                    }
+                    if (has_gate) {
+                        it.template get<T>(g, 2, pl.row, D, c);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) u[e] = u[e] * activation(g[e], act);
+                    }
+                    param(a, w.scale, c, 1.f);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) v[j][e] = fma(u[e], a[e], v[j][e]);
+                    put<TS>(r + at + j * pl.stride, v[j]);
                 }
-                if (on && j < pl.count) put<TS>(r, at, pl, j, v[j]);
-                if (j >= pl.count) v[j][0] = v[j][1] = both(0.f);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                v[j][0] = v[j][1] = both(0.f);
+                if (j < count) it.template get<TS>(v[j], 0, pl.row, D, pl.channel + j * pl.stride);
             }
         }
         if (out != nullptr) {
-            const Pair q = both(centre<kVec>(v, pl, kind, inv, eps, lanes, meet, half));
+            float2 mean, root;
+            statistics<kVec>([&](int, int j, Pair (&x)[2]) { x[0] = v[j][0], x[1] = v[j][1]; }, true, false, count, kind, inv, eps,
+                             lanes, meet, half, mean, root);
+            if (meets && !post) it.refill();
+            q = both(root.x), m = both(-mean.x);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                Pair pw[2], pb[2];
-                param(pw, w.weight, pl, j, 1.f);
-                param(pb, w.bias, pl, j, 0.f);
+            for (int j = 0; j < kVec; ++j)
+                if (j < count) {
+                    const int c = pl.channel + j * pl.stride;
+                    Pair a[2], b[2];
+                    param(a, w.weight, c, 1.f);
+                    param(b, w.bias, c, 0.f);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) v[j][e] = fma(v[j][e] * q, pw[e], pb[e]);
-                if (on && j < pl.count) put<T>(out, at, pl, j, v[j]);
-            }
+                    for (int e = 0; e < 2; ++e) a[e] = fma((v[j][e] + m) * q, a[e], b[e]);
+                    put<T>(out + at + j * pl.stride, a);
+                }
         }
     }
+    it.end();
 }
 
-template <typename T, typename TS, int kVec>
-__global__ void __launch_bounds__(1024)
-bwd_kernel(const TS *__restrict__ dr, const T *__restrict__ dout, const TS *__restrict__ r, const T *__restrict__ y,
-           const T *__restrict__ gate, Weights w, int kind, int post, int act, float eps, TS *__restrict__ dx,
-           T *__restrict__ dy, T *__restrict__ dgate, float *__restrict__ part, int64_t rows, int D, int lanes) {
-    __shared__ Meeting meet;
-    __shared__ float4 tops[128];
+template <typename T, typename TS, int kVec, bool kStage, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads <= 320 ? 640 / kThreads : 1)
+bwd_kernel(Inputs<5> in, Weights w, int kind, int post, int act, float eps, TS *__restrict__ dx, T *__restrict__ dy,
+           T *__restrict__ dgate, float *__restrict__ part, int64_t rows, int D, int lanes) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ uint64_t full[kMaxStages];
+    __shared__ int failed;
+    __shared__ __align__(16) Meeting meet;
+    __shared__ float4 tops[kRowsThreads];
     int half = 0;
     const Place pl(D, lanes);
-    const int step = blockDim.x / lanes;
     const float inv = 1.f / (float)D;
+    const bool has_dr = in.from[0] != nullptr, has_out = in.from[1] != nullptr, has_y = in.from[3] != nullptr,
+               has_gate = in.from[4] != nullptr;
+    const bool meets = lanes > 32 && (post || has_out);
     Pair sums[kSums][kVec][2];
 #pragma unroll
     for (int i = 0; i < kSums; ++i)
 #pragma unroll
         for (int j = 0; j < kVec; ++j) sums[i][j][0] = sums[i][j][1] = both(0.f);
-    for (int64_t r0 = (int64_t)blockIdx.x * step; r0 < rows; r0 += (int64_t)gridDim.x * step) {
-        const int64_t row = r0 + pl.row, at = row * D;
-        const bool on = row < rows;
-        Pair d[kVec][2];
-        fetch<TS, kVec>(d, dr, at, pl, on && dr != nullptr);
-        if (dout != nullptr) {
-            Pair h[kVec][2], up[kVec][2];
-            fetch<TS, kVec>(h, r, at, pl, on);
-            fetch<T, kVec>(up, dout, at, pl, on);
-            const float q = centre<kVec>(h, pl, kind, inv, eps, lanes, meet, half);
+    Rows<kStage, 5> it(in, ring, full, &failed, rows, lanes);
+    clear(meet);
+    __syncthreads();
+    for (; it.more(); it.next()) {
+        if (!meets) {
+            __syncthreads();
+            it.refill();
+        }
+        it.arrive();
+        const int64_t row = it.item * it.step + pl.row, at = row * D + pl.channel;
+        const int count = row < rows ? pl.count : 0;
+        float2 mean, root;  // of r, and of y
+        if (has_out || post) {
+            statistics<kVec>(
+                [&](int which, int j, Pair (&v)[2]) {
+                    if (which == 0) it.template get<TS>(v, 2, pl.row, D, pl.channel + j * pl.stride);
+                    else it.template get<T>(v, 3, pl.row, D, pl.channel + j * pl.stride);
+                },
+                has_out, post, count, kind, inv, eps, lanes, meet, half, mean, root);
+            if (meets) it.refill();
+        }
+        const Pair q = both(root.x), m = both(-mean.x), uq = both(root.y), um = both(-mean.y);
+        Pair m1 = both(0.f), m2 = both(0.f);
+        if (has_out) {
             Pair s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                Pair pw[2];
-                param(pw, w.weight, pl, j, 1.f);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    h[j][e] = h[j][e] * both(q);
-                    sums[3][j][e] = fma(up[j][e], h[j][e], sums[3][j][e]);
-                    sums[4][j][e] = sums[4][j][e] + up[j][e];
-                    up[j][e] = up[j][e] * pw[e];
-                    s1 = s1 + up[j][e];
-                    s2 = fma(up[j][e], h[j][e], s2);
-                }
-            }
-            const float2 s = row_sum(make_float2(total(s1), total(s2)), lanes, meet, half);
-            const Pair m1 = both(kind == GLA_NORM_LAYER ? -s.x * inv : 0.f), m2 = both(-s.y * inv);
-#pragma unroll
             for (int j = 0; j < kVec; ++j)
+                if (j < count) {
+                    const int c = pl.channel + j * pl.stride;
+                    Pair up[2], h[2], wt[2];
+                    it.template get<T>(up, 1, pl.row, D, c);
+                    it.template get<TS>(h, 2, pl.row, D, c);
+                    param(wt, w.weight, c, 1.f);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) d[j][e] = fma(fma(h[j][e], m2, up[j][e] + m1), both(q), d[j][e]);
+                    for (int e = 0; e < 2; ++e) {
+                        h[e] = (h[e] + m) * q;
+                        sums[3][j][e] = fma(up[e], h[e], sums[3][j][e]);
+                        sums[4][j][e] = sums[4][j][e] + up[e];
+                        const Pair t = up[e] * wt[e];
+                        s1 = s1 + t;
+                        s2 = fma(t, h[e], s2);
+                    }
+                }
+            const float2 s = row_sum(make_float2(total(s1), total(s2)), lanes, meet, half);
+            m1 = both(kind == GLA_NORM_LAYER ? -s.x * inv : 0.f), m2 = both(-s.y * inv);
         }
+        Pair d[kVec][2], s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
         for (int j = 0; j < kVec; ++j)
-            if (on && j < pl.count) put<TS>(dx, at, pl, j, d[j]);
-        if (y == nullptr) continue;
-        Pair u[kVec][2], g[kVec][2];
-        fetch<T, kVec>(u, y, at, pl, on);
-        if (gate != nullptr) fetch<T, kVec>(g, gate, at, pl, on);
-        float uq = 1.f;
-        if (post) uq = centre<kVec>(u, pl, kind, inv, eps, lanes, meet, half);
-        Pair s1 = both(0.f), s2 = both(0.f);
+            if (j < count) {
+                const int c = pl.channel + j * pl.stride;
+                d[j][0] = d[j][1] = both(0.f);
+                if (has_dr) it.template get<TS>(d[j], 0, pl.row, D, c);
+                if (has_out) {
+                    Pair up[2], h[2], wt[2];
+                    it.template get<T>(up, 1, pl.row, D, c);
+                    it.template get<TS>(h, 2, pl.row, D, c);
+                    param(wt, w.weight, c, 1.f);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            Pair pw[2], pb[2], sc[2];
-            param(pw, w.post_weight, pl, j, 1.f);
-            param(pb, w.post_bias, pl, j, 0.f);
-            param(sc, w.scale, pl, j, 1.f);
-            const bool has = on && j < pl.count;
+                    for (int e = 0; e < 2; ++e) d[j][e] = fma(fma((h[e] + m) * q, m2, fma(up[e], wt[e], m1)), q, d[j][e]);
+                }
+                put<TS>(dx + at + j * pl.stride, d[j]);
+                if (has_y) {
+                    Pair u[2], g[2], pw[2], pb[2], sc[2];
+                    it.template get<T>(u, 3, pl.row, D, c);
+                    param(sc, w.scale, c, 1.f);
+                    if (post) {
+                        param(pw, w.post_weight, c, 1.f);
+                        param(pb, w.post_bias, c, 0.f);
+                    }
+                    if (has_gate) it.template get<T>(g, 4, pl.row, D, c);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (!has) d[j][e] = both(0.f);
-                if (post) u[j][e] = u[j][e] * both(uq);
-                const Pair z = post ? fma(u[j][e], pw[e], pb[e]) : u[j][e];
-                Pair slope = both(0.f), f = both(1.f);
-                if (gate != nullptr) f = activation(g[j][e], act, slope);
-                const Pair df = d[j][e] * f;
-                sums[0][j][e] = fma(df, z, sums[0][j][e]);
-                if (gate != nullptr) g[j][e] = d[j][e] * sc[e] * z * slope;
-                d[j][e] = df * sc[e];
-                if (post) {
-                    sums[1][j][e] = fma(d[j][e], u[j][e], sums[1][j][e]);
-                    sums[2][j][e] = sums[2][j][e] + d[j][e];
-                    d[j][e] = d[j][e] * pw[e];
-                    s1 = s1 + d[j][e];
-                    s2 = fma(d[j][e], u[j][e], s2);
+                    for (int e = 0; e < 2; ++e) {
+                        Pair z = u[e], df = d[j][e];
+                        if (post) {
+                            u[e] = (u[e] + um) * uq;
+                            z = fma(u[e], pw[e], pb[e]);
+                        }
+                        if (has_gate) {
+                            Pair slope;
+                            df = df * activation(g[e], act, slope);
+                            g[e] = d[j][e] * sc[e] * z * slope;
+                        }
+                        sums[0][j][e] = fma(df, z, sums[0][j][e]);
+                        df = df * sc[e];
+                        if (post) {
+                            sums[1][j][e] = fma(df, u[e], sums[1][j][e]);
+                            sums[2][j][e] = sums[2][j][e] + df;
+                            df = df * pw[e];
+                            s1 = s1 + df;
+                            s2 = fma(df, u[e], s2);
+                        }
+                        d[j][e] = df;
+                    }
+                    if (has_gate) put<T>(dgate + at + j * pl.stride, g);
+                    if (!post) put<T>(dy + at + j * pl.stride, d[j]);
                 }
             }
-            if (gate != nullptr && has) put<T>(dgate, at, pl, j, g[j]);
-        }
         if (post) {
             const float2 s = row_sum(make_float2(total(s1), total(s2)), lanes, meet, half);
-            const Pair m1 = both(kind == GLA_NORM_LAYER ? -s.x * inv : 0.f), m2 = both(-s.y * inv);
+            m1 = both(kind == GLA_NORM_LAYER ? -s.x * inv : 0.f), m2 = both(-s.y * inv);
 #pragma unroll
             for (int j = 0; j < kVec; ++j)
+                if (j < count) {
+                    Pair u[2];
+                    it.template get<T>(u, 3, pl.row, D, pl.channel + j * pl.stride);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) d[j][e] = fma(u[j][e], m2, d[j][e] + m1) * both(uq);
+                    for (int e = 0; e < 2; ++e) d[j][e] = fma((u[e] + um) * uq, m2, d[j][e] + m1) * uq;
+                    put<T>(dy + at + j * pl.stride, d[j]);
+                }
         }
-#pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            if (on && j < pl.count) put<T>(dy, at, pl, j, d[j]);
     }
+    it.end();
     // the block's rows of one channel set meet in shared memory; one writer per channel
     float *to = part + (int64_t)blockIdx.x * kSums * D;
+    const int step = blockDim.x / lanes;
 #pragma unroll
     for (int i = 0; i < kSums; ++i)
 #pragma unroll
@@ -348,55 +529,111 @@ int blocks(const Plan &pl, int64_t rows, int per_sm) {
     if (most < 1) most = 1;
     return (int)(need < most ? need : most);
 }
-int fwd_per_sm(const Plan &pl) { return 2048 / pl.threads < 1 ? 1 : 2048 / pl.threads; }
-int bwd_per_sm(const Plan &pl) { return 512 / pl.threads < 1 ? 1 : 512 / pl.threads; }
+// Blocks of an SM: as many as the threads' registers allow, 85 a thread of the forward and 102 of the gradient.
+int per_sm(const Plan &pl, int threads) {
+    const int n = threads / pl.threads;
+    return n < 1 ? 1 : n;
+}
+constexpr int kFwdThreads = 768, kBwdThreads = 640;
 
-#define GLA_BY_VEC(RUN, T, TS)            \
-    switch (pl.vecs) {                    \
-        case 1: RUN(T, TS, 1); break;     \
-        case 2: RUN(T, TS, 2); break;     \
-        default: RUN(T, TS, 4); break;    \
+constexpr int kMostShared = 220 * 1024;
+
+// The stages of a block: rows of each array one behind the other.
+template <int kArrays> int lay_out(Inputs<kArrays> &in, const Plan &pl, int per_sm) {
+    int at = 0;
+    for (int i = 0; i < kArrays; ++i) {
+        in.at[i] = at;
+        if (in.from[i] != nullptr) at += (pl.rows * in.row_bytes[i] + 127) / 128 * 128;
     }
+    in.stage_bytes = at;
+    const int room = 190 * 1024 / per_sm - 6144;  // what is left caches the parameters
+    in.stages = room / at;
+    if (in.stages < 2 && per_sm == 1) in.stages = kMostShared / at;
+    if (in.stages > kMaxStages) in.stages = kMaxStages;
+    if (in.stages < 2) in.stages = 0;
+    return in.stages * at;
+}
+
+// RUN(T, TS, kVec, kStage, kThreads) for a call's types and plan; kSmall: threads of the kernels that share an SM.
+#define GLA_BY_STAGE(RUN, T, TS, V, N)                 \
+    if (staged) { RUN(T, TS, V, true, N) }             \
+    else { RUN(T, TS, V, false, N) }
+#define GLA_BY_PLAN(RUN, T, TS)                                                     \
+    if (pl.vecs == kVecs && pl.threads <= kSmall) { GLA_BY_STAGE(RUN, T, TS, kVecs, kSmall) } \
+    else if (pl.vecs == kVecs && pl.threads <= 512) { GLA_BY_STAGE(RUN, T, TS, kVecs, 512) }  \
+    else if (pl.vecs == kVecs) { GLA_BY_STAGE(RUN, T, TS, kVecs, 1024) }            \
+    else { GLA_BY_STAGE(RUN, T, TS, 4, 1024) }
 #define GLA_BY_TYPE(RUN)                                                                          \
-    if (dtype == GLA_F32) { GLA_BY_VEC(RUN, float, float) }                                       \
-    else if (stream_dtype == GLA_F32) { GLA_BY_VEC(RUN, __nv_bfloat16, float) }                   \
-    else { GLA_BY_VEC(RUN, __nv_bfloat16, __nv_bfloat16) }
+    if (dtype == GLA_F32) { GLA_BY_PLAN(RUN, float, float) }                                      \
+    else if (stream_dtype == GLA_F32) { GLA_BY_PLAN(RUN, __nv_bfloat16, float) }                  \
+    else { GLA_BY_PLAN(RUN, __nv_bfloat16, __nv_bfloat16) }
+
+// Lets a kernel use as much shared memory as any call may ask for; asked of the runtime once per kernel and device.
+template <auto kKernel> bool allow_most() {
+    constexpr int kDevices = 64;
+    static std::atomic<bool> allowed[kDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < kDevices && allowed[dev].load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared) != cudaSuccess) return false;
+    if (dev < kDevices) allowed[dev].store(true, std::memory_order_release);
+    return true;
+}
 
 }  // namespace
 
 int64_t workspace(int64_t rows, int D) {
-    const Plan pl = make_plan(D);
-    return (int64_t)blocks(pl, rows < 1 ? 1 : rows, bwd_per_sm(pl)) * kSums * D * (int64_t)sizeof(float);
+    const Plan pl = make_plan(D, kBwdVecs);
+    return (int64_t)blocks(pl, rows < 1 ? 1 : rows, per_sm(pl, kBwdThreads)) * kSums * D * (int64_t)sizeof(float);
 }
 
 int fwd(const void *x, const void *y, const void *gate, const float *scale, const float *post_weight, const float *post_bias,
         const float *weight, const float *bias, int kind, int post, int act, float eps, void *r, void *out, int64_t rows, int D,
         int dtype, int stream_dtype, cudaStream_t st) {
     if (rows == 0) return GLA_OK;
-    const Plan pl = make_plan(D);
+    constexpr int kVecs = kFwdVecs, kSmall = 256;
+    const Plan pl = make_plan(D, kVecs);
     const Weights w{scale, post_weight, post_bias, weight, bias};
-    const unsigned grid = (unsigned)blocks(pl, rows, fwd_per_sm(pl));
-#define GLA_RUN(T, TS, V)                                                                                             \
-    fwd_kernel<T, TS, V><<<grid, pl.threads, 0, st>>>((const TS *)x, (const T *)y, (const T *)gate, w, kind, post,    \
-                                                      act, eps, (TS *)r, (T *)out, rows, D, pl.lanes)
+    const int e = dtype == GLA_F32 ? 4 : 2, es = stream_dtype == GLA_F32 ? 4 : 2, n = per_sm(pl, kFwdThreads);
+    Inputs<3> in{{x, y, gate}, {D * es, D * e, D * e}, {}, 0, 0};
+    const int bytes = lay_out(in, pl, n);
+    const bool staged = in.stages > 0;
+    const unsigned grid = (unsigned)blocks(pl, rows, n);
+    bool ok = false;
+#define GLA_RUN(T, TS, V, S, N)                                                                                            \
+    {                                                                                                                      \
+        constexpr auto kKernel = fwd_kernel<T, TS, V, S, N>;                                                               \
+        ok = allow_most<kKernel>();                                                                                        \
+        if (ok) kKernel<<<grid, pl.threads, bytes, st>>>(in, w, kind, post, act, eps, (TS *)r, (T *)out, rows, D, pl.lanes); \
+    }
     GLA_BY_TYPE(GLA_RUN)
 #undef GLA_RUN
     count_launches(1);
-    return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
+    return ok && cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
 }
 
 int bwd(const void *dr, const void *dout, const void *r, const void *y, const void *gate, const float *scale,
         const float *post_weight, const float *post_bias, const float *weight, int kind, int post, int act, float eps, void *dx,
         void *dy, void *dgate, float *dscale, float *dpost_weight, float *dpost_bias, float *dweight, float *dbias, int64_t rows,
         int D, int dtype, int stream_dtype, void *ws, cudaStream_t st) {
-    const Plan pl = make_plan(D);
+    constexpr int kVecs = kBwdVecs, kSmall = 320;
+    const Plan pl = make_plan(D, kVecs);
     const Weights w{scale, post_weight, post_bias, weight, nullptr};
-    const int nb = rows > 0 ? blocks(pl, rows, bwd_per_sm(pl)) : 0;
+    const int n = per_sm(pl, kBwdThreads), nb = rows > 0 ? blocks(pl, rows, n) : 0;
+    bool ok = true;
     if (nb > 0) {
-#define GLA_RUN(T, TS, V)                                                                                                   \
-    bwd_kernel<T, TS, V><<<(unsigned)nb, pl.threads, 0, st>>>((const TS *)dr, (const T *)dout, (const TS *)r, (const T *)y, \
-                                                              (const T *)gate, w, kind, post, act, eps, (TS *)dx, (T *)dy,  \
-                                                              (T *)dgate, (float *)ws, rows, D, pl.lanes)
+        const int e = dtype == GLA_F32 ? 4 : 2, es = stream_dtype == GLA_F32 ? 4 : 2;
+        Inputs<5> in{{dr, dout, dout != nullptr ? r : nullptr, y, gate}, {D * es, D * e, D * es, D * e, D * e}, {}, 0, 0};
+        const int bytes = lay_out(in, pl, n);
+        const bool staged = in.stages > 0;
+#define GLA_RUN(T, TS, V, S, N)                                                                                            \
+        {                                                                                                                  \
+            constexpr auto kKernel = bwd_kernel<T, TS, V, S, N>;                                                           \
+            ok = allow_most<kKernel>();                                                                                    \
+            if (ok)                                                                                                        \
+                kKernel<<<(unsigned)nb, pl.threads, bytes, st>>>(in, w, kind, post, act, eps, (TS *)dx, (T *)dy,           \
+                                                                 (T *)dgate, (float *)ws, rows, D, pl.lanes);              \
+        }
         GLA_BY_TYPE(GLA_RUN)
 #undef GLA_RUN
         count_launches(1);
@@ -406,7 +643,7 @@ int bwd(const void *dr, const void *dout, const void *r, const void *y, const vo
         sum_kernel<<<dim3((unsigned)((D + 31) / 32), kSums), 256, 0, st>>>((const float *)ws, nb, D, sums);
         count_launches(1);
     }
-    return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
+    return ok && cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
 }
 
 }  // namespace resnorm
