@@ -326,7 +326,7 @@ int check_resnorm(const void *y, const void *gate, const float *scale, const flo
     if (!post && (post_weight || post_bias)) return GLA_ERR_ARG;
     // an empty tensor has no address: without rows an absent y is not told from a present one
     if (rows > 0 && !y && (gate || scale || post)) return GLA_ERR_ARG;
-    if (D % 8 || D > 16384 || rows > (1LL << 40)) return GLA_ERR_UNSUPPORTED;
+    if (D % 8 || D > 16384 || rows > 0x7fffff00LL) return GLA_ERR_UNSUPPORTED;
     if (!aligned16(y) || !aligned16(gate) || !aligned16(scale) || !aligned16(post_weight) || !aligned16(post_bias) ||
         !aligned16(weight) || !aligned16(bias))
         return GLA_ERR_ALIGN;
@@ -726,7 +726,7 @@ int gla_residual_norm(const void *x, const void *y, const void *gate, const floa
 
 long long gla_residual_norm_workspace_bytes(long long rows, int D) {
     if (rows < 0 || D <= 0) return GLA_ERR_ARG;
-    if (D % 8 || D > 16384 || rows > (1LL << 40)) return GLA_ERR_UNSUPPORTED;
+    if (D % 8 || D > 16384 || rows > 0x7fffff00LL) return GLA_ERR_UNSUPPORTED;
     return (long long)resnorm::workspace(rows, D);
 }
 

@@ -11,9 +11,11 @@
 //
 // Both are bound by HBM.  A row is one block's, or a part of a warp's where it is short; a thread takes four neighbouring
 // channels at a time and keeps the same ones for all of its rows, so the gradient's sums over tokens stay in registers until
-// its last row.  Rows come into shared memory by bulk copies, some rows ahead, and are read from there by each step that needs
-// them: what is in flight and what a later step needs costs no registers, of which the sums take most.  Rows that two stages
-// have no room for are read from memory each time.
+// its last row.  An SM has several blocks, so that one row's barriers wait beside another's work.  Rows come into shared memory
+// by bulk copies, some rows ahead, and are read from there by each step: what is in flight costs no registers.  Rows that two
+// stages have no room for are read from memory.  Statistics are taken in two steps, a mean and then centred squares.
+#include <type_traits>
+
 #include "gla_act.cuh"
 #include "sm100_ptx.cuh"
 
@@ -25,29 +27,29 @@ namespace {
 
 constexpr int kSums = 5;  // dscale, dpost_weight, dpost_bias, dweight, dbias
 constexpr int kMaxStages = 6;
-constexpr int kRowsThreads = 256;  // of a block with several rows
+constexpr int kThreads = 256;  // of a block with several rows
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// Threads to a row (whole warps above 32), vectors of four channels to a thread, rows of a block at a time.
+// Threads to a row (whole warps above 32), rows of a block at a time.  A thread's vectors are kStride channels apart, so that
+// those of a warp are neighbours and a vector's place is a constant away from the thread's first.
 struct Plan {
     int lanes, vecs, rows, threads;
 };
+constexpr int kStride = 128;
+constexpr int kFwdVecs = 4, kBwdVecs = 2, kWideVecs = 4;
 
 Plan make_plan(int D, int vecs) {
-    const int nv = D / 4;
     Plan p{};
-    p.vecs = (nv + vecs - 1) / vecs <= 1024 ? vecs : 4;
-    const int need = (nv + p.vecs - 1) / p.vecs;
+    p.vecs = D <= kStride ? 1 : D <= 2 * kStride ? 2 : D <= 1024 * 4 * vecs ? vecs : kWideVecs;
     p.lanes = 1;
-    if (need <= 32)
-        while (p.lanes < need) p.lanes *= 2;
+    if (D <= kStride)
+        while (p.lanes < D / 4) p.lanes *= 2;
     else
-        p.lanes = (need + 31) / 32 * 32;
-    p.rows = p.lanes <= 32 ? kRowsThreads / p.lanes : 1;
+        p.lanes = (D + kStride * p.vecs - 1) / (kStride * p.vecs) * 32;
+    p.rows = p.lanes <= 32 ? kThreads / p.lanes : 1;
     p.threads = p.lanes * p.rows;
     return p;
 }
-constexpr int kFwdVecs = 4, kBwdVecs = 2;
 
 template <typename T> struct Four;  // four channels of one row
 template <> struct Four<__nv_bfloat16> {
@@ -77,98 +79,169 @@ template <typename T> __device__ __forceinline__ void put(T *to, const Pair (&x)
     __stcs(reinterpret_cast<typename Four<T>::Raw *>(to), Four<T>::close(x));
 }
 
-// A thread's place: its row in the block, its first channel and how many of its vectors exist.
-struct Place {
-    int row, channel, count, stride;
-    __device__ __forceinline__ Place(int D, int lanes) {
-        const int lane = threadIdx.x % lanes, nv = D >> 2;
-        row = threadIdx.x / lanes;
-        channel = lane * 4;
-        stride = lanes * 4;
-        count = lane < nv ? (nv - lane + lanes - 1) / lanes : 0;
+// A thread's vectors: fetch reads them (zero where there are none), times and plus take parameters that may be absent, for all
+// of them or none.  kAll: every thread has all of its vectors.
+template <int kVec, bool kAll> struct Vectors {
+    using V = Pair[kVec][2];
+    int count;
+    __device__ __forceinline__ bool has(int j) const { return kAll || j < count; }
+    template <typename T> __device__ __forceinline__ void fetch(V &v, const T *p) const {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            if (!kAll) v[j][0] = v[j][1] = both(0.f);
+            if (has(j)) Four<T>::open(v[j], *reinterpret_cast<const typename Four<T>::Raw *>(p + j * kStride));
+        }
+    }
+    template <typename T> __device__ __forceinline__ void store(T *p, const V &v) const {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (has(j)) put<T>(p + j * kStride, v[j]);
+    }
+    template <class F> __device__ __forceinline__ void with(const float *p, F f) const {  // f(j, parameters), where there are any
+        if (p == nullptr) return;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            Pair a[2] = {both(0.f), both(0.f)};
+            if (has(j)) Four<float>::open(a, *reinterpret_cast<const float4 *>(p + j * kStride));
+            f(j, a);
+        }
+    }
+    __device__ __forceinline__ void times(V &v, const float *p) const {
+        with(p, [&](int j, const Pair (&a)[2]) { v[j][0] = v[j][0] * a[0], v[j][1] = v[j][1] * a[1]; });
+    }
+    __device__ __forceinline__ void plus(V &v, const float *p) const {
+        with(p, [&](int j, const Pair (&a)[2]) { v[j][0] = v[j][0] + a[0], v[j][1] = v[j][1] + a[1]; });
+    }
+    __device__ __forceinline__ void times(V &v, float by) const {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[j][0] = v[j][0] * both(by), v[j][1] = v[j][1] * both(by);
+    }
+    __device__ __forceinline__ void shift(V &v, float by) const {  // those that there are
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            const Pair b = both(has(j) ? by : 0.f);
+            v[j][0] = v[j][0] + b, v[j][1] = v[j][1] + b;
+        }
+    }
+    __device__ __forceinline__ void clear(V &v) const {  // those that there are not
+        if (kAll) return;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (!has(j)) v[j][0] = v[j][1] = both(0.f);
+    }
+    static __device__ __forceinline__ float sum(const V &v) {
+        Pair s = v[0][0] + v[0][1];
+#pragma unroll
+        for (int j = 1; j < kVec; ++j) s = s + (v[j][0] + v[j][1]);
+        return total(s);
+    }
+    static __device__ __forceinline__ float squares(const V &v) {
+        Pair s = v[0][0] * v[0][0];
+        s = fma(v[0][1], v[0][1], s);
+#pragma unroll
+        for (int j = 1; j < kVec; ++j) s = fma(v[j][0], v[j][0], fma(v[j][1], v[j][1], s));
+        return total(s);
+    }
+    static __device__ __forceinline__ float product(const V &v, const V &u) {
+        Pair s = v[0][0] * u[0][0];
+        s = fma(v[0][1], u[0][1], s);
+#pragma unroll
+        for (int j = 1; j < kVec; ++j) s = fma(v[j][0], u[j][0], fma(v[j][1], u[j][1], s));
+        return total(s);
+    }
+    // g becomes act(g), and slope act's slope: one choice for all vectors
+    template <int kAct> static __device__ __forceinline__ void gate(V &g) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) g[j][0] = activation(g[j][0], kAct), g[j][1] = activation(g[j][1], kAct);
+    }
+    template <int kAct> static __device__ __forceinline__ void gate(V &g, V &slope) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            g[j][0] = activation(g[j][0], kAct, slope[j][0]);
+            g[j][1] = activation(g[j][1], kAct, slope[j][1]);
+        }
     }
 };
 
-// Four parameters, or a constant where there are none.
-__device__ __forceinline__ void param(Pair (&v)[2], const float *from, int channel, float otherwise) {
-    if (from != nullptr) Four<float>::open(v, __ldg(reinterpret_cast<const float4 *>(from + channel)));
-    else v[0] = v[1] = both(otherwise);
-}
-
-// Two sums over a row's threads at once.  Rows of more than a warp meet in shared memory, in one half of it after the other,
-// so that one barrier a sum is enough; every thread of the block calls this.
+// Two sums over a row's threads at once.  The warps of a row meet in shared memory, in one half of it after the other, so that
+// one barrier a sum is enough; every thread of the block calls this.
 struct Meeting {
-    float2 at[2][32];
+    float at[2][2][32];  // the first sum's parts by warp, and the second's
 };
-__device__ __forceinline__ float2 row_sum(float2 s, int lanes, Meeting &m, int &half) {
+__device__ __forceinline__ float2 row_sum(float a, float b, int lanes, Meeting &m, int &half) {
     if (lanes < 32) {
         for (int d = lanes >> 1; d > 0; d >>= 1) {
-            s.x += __shfl_xor_sync(0xffffffffu, s.x, d);
-            s.y += __shfl_xor_sync(0xffffffffu, s.y, d);
+            a += __shfl_xor_sync(0xffffffffu, a, d);
+            b += __shfl_xor_sync(0xffffffffu, b, d);
         }
-        return s;
+        return make_float2(a, b);
     }
-    // one half of the warp adds the one sum up, the other half the other
-    const bool upper = threadIdx.x & 16;
-    float v = (upper ? s.y : s.x) + __shfl_xor_sync(0xffffffffu, upper ? s.x : s.y, 16);
+    // one half of the warp adds the one sum up, the other half the other; then the warps' parts likewise
+    const int lane = threadIdx.x & 31, upper = lane >> 4;
+    float v = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    if (lanes == 32) {
-        const float o = __shfl_xor_sync(0xffffffffu, v, 16);
-        return upper ? make_float2(o, v) : make_float2(v, o);
+    if (lanes > 32) {
+        float(&at)[2][32] = m.at[half];
+        if ((lane & 15) == 0) at[upper][threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = at[upper][lane & 15];
+        if (lanes > 512) v += at[upper][16 + (lane & 15)];
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        half ^= 1;
     }
-    if ((threadIdx.x & 15) == 0) reinterpret_cast<float *>(&m.at[half][threadIdx.x >> 5])[upper] = v;
-    __syncthreads();
-    s = make_float2(0.f, 0.f);
-    const int warps = lanes >> 5;
-#pragma unroll 4
-    for (int w = 0; w < warps; w += 2) {  // the one past an odd number is zero
-        const float4 f = *reinterpret_cast<const float4 *>(&m.at[half][w]);
-        s.x += f.x + f.z;
-        s.y += f.y + f.w;
-    }
-    half ^= 1;
-    return s;
+    const float o = __shfl_xor_sync(0xffffffffu, v, 16);
+    return upper ? make_float2(o, v) : make_float2(v, o);
 }
-__device__ __forceinline__ void clear(Meeting &m) {
-    if (threadIdx.x < 32) m.at[0][threadIdx.x] = m.at[1][threadIdx.x] = make_float2(0.f, 0.f);
+__device__ __forceinline__ void clear(Meeting &m) {  // warps that there are not add nothing
+    for (int i = threadIdx.x; i < 128; i += blockDim.x) (&m.at[0][0][0])[i] = 0.f;
 }
 
-// Arrays whose rows come in, and the stages that they come into: a block's rows of each array at a time.
+// Arrays whose rows come in, and the stages that they come into: the rows of an item, of each array.
 template <int kArrays> struct Inputs {
     const void *from[kArrays];  // null: absent
     int row_bytes[kArrays], at[kArrays];
-    int stage_bytes, stages;
+    int stage_bytes, stages, passes;
 };
 
-// The rows of a block, one item (its rows at a time) after the other.
+// The rows of a block, an item (`passes` rows for each of its threads) after the other.
+struct Bars {
+    uint64_t full[kMaxStages], read[kMaxStages];
+    int failed;
+};
 template <bool kStage, int kArrays>
 struct Rows {
     const Inputs<kArrays> &in;
     uint8_t *ring;
-    uint64_t *full;
-    int *failed;
-    int64_t rows, items, item;
-    int step, st;
+    Bars &bars;
+    int64_t rows, row;               // row: the thread's
+    int item, items, at_once, step, mine, st;  // rows at once and of an item; the thread's row in its item
     uint32_t phase;
-    bool first;
-    __device__ __forceinline__ Rows(const Inputs<kArrays> &in_, uint8_t *ring_, uint64_t *full_, int *failed_, int64_t rows_, int lanes)
-        : in(in_), ring(ring_), full(full_), failed(failed_), rows(rows_), item(blockIdx.x), step(blockDim.x / lanes), st(0), phase(0),
-          first(true) {
-        items = (rows + step - 1) / step;
+    bool late;  // whether the stage of the item before is still to be refilled
+    __device__ __forceinline__ Rows(const Inputs<kArrays> &in_, uint8_t *ring_, Bars &bars_, int64_t rows_, int lanes)
+        : in(in_), ring(ring_), bars(bars_), rows(rows_), item(blockIdx.x), at_once(blockDim.x / lanes), st(0), phase(0), late(false) {
+        step = at_once * in.passes;
+        mine = threadIdx.x / lanes;
+        items = (int)((rows + step - 1) / step);
+        row = (int64_t)item * step + mine;
         if (!kStage) return;
         if (threadIdx.x == 0) {
-            *failed = 0;
-            for (int i = 0; i < in.stages; ++i) ptx::mbar_init(ptx::smem_u32(full + i), 1);
+            bars.failed = 0;
+            for (int i = 0; i < in.stages; ++i) {
+                ptx::mbar_init(ptx::smem_u32(bars.full + i), 1);
+                ptx::mbar_init(ptx::smem_u32(bars.read + i), (blockDim.x + 31) / 32);
+            }
             ptx::fence_mbar_init();
-            for (int i = 0; i < in.stages; ++i) order(i, item + i * (int64_t)gridDim.x);
+            for (int i = 0; i < in.stages; ++i) order(i, item + i * (int)gridDim.x);
         }
     }
     // by one thread
-    __device__ __forceinline__ void order(int to_stage, int64_t k) const {
+    __device__ __forceinline__ void order(int to_stage, int k) const {
         if (k >= items) return;
-        const uint32_t b = ptx::smem_u32(full + to_stage), to = ptx::smem_u32(ring) + (uint32_t)(to_stage * in.stage_bytes);
-        const int n = (int)min((int64_t)step, rows - k * step);
+        const uint32_t b = ptx::smem_u32(bars.full + to_stage), to = ptx::smem_u32(ring) + (uint32_t)(to_stage * in.stage_bytes);
+        const int64_t first = (int64_t)k * step;
+        const int n = (int)min((int64_t)step, rows - first);
         uint32_t bytes = 0;
 #pragma unroll
         for (int i = 0; i < kArrays; ++i)
@@ -177,324 +250,361 @@ struct Rows {
 #pragma unroll
         for (int i = 0; i < kArrays; ++i)
             if (in.from[i] != nullptr)
-                ptx::bulk_load_g2s(to + (uint32_t)in.at[i], (const uint8_t *)in.from[i] + k * step * in.row_bytes[i],
+                ptx::bulk_load_g2s(to + (uint32_t)in.at[i], (const uint8_t *)in.from[i] + first * in.row_bytes[i],
                                    (uint32_t)(n * in.row_bytes[i]), b);
     }
-    __device__ __forceinline__ bool more() const { return item < items; }
-    __device__ __forceinline__ void arrive() const {
-        if (kStage && !ptx::mbar_wait(ptx::smem_u32(full + st), phase, failed, kWaitNs)) *(volatile int *)failed = 1;
+    __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity) const {
+        if (!ptx::mbar_wait(ptx::smem_u32(bar), parity, &bars.failed, kWaitNs)) *(volatile int *)&bars.failed = 1;
     }
-    // All threads of the block are past the item before: its stage takes another one.
-    __device__ __forceinline__ void refill() const {
-        if (kStage && threadIdx.x == 0 && !first) order(st == 0 ? in.stages - 1 : st - 1, item + (in.stages - 1) * (int64_t)gridDim.x);
+    // The thread's next row; false when the block has no more.  meets: a barrier of the row's sums is followed by refill().
+    __device__ __forceinline__ bool begin(bool meets) {
+        if (item >= items) return false;
+        if (kStage && mine < at_once) {
+            if (!meets) {
+                if (threadIdx.x == 0 && late) wait(bars.read + (st == 0 ? in.stages - 1 : st - 1), st == 0 ? phase ^ 1u : phase);
+                refill();
+            }
+            wait(bars.full + st, phase);
+        }
+        return true;
+    }
+    // All threads are past the item before: its stage takes another one.
+    __device__ __forceinline__ void refill() {
+        if (kStage && late && threadIdx.x == 0) order(st == 0 ? in.stages - 1 : st - 1, item + (in.stages - 1) * (int)gridDim.x);
+        late = false;
+        __syncwarp();
     }
     __device__ __forceinline__ void next() {
-        first = false;
-        item += gridDim.x;
-        if (kStage && ++st == in.stages) {
-            st = 0;
-            phase ^= 1u;
+        mine += at_once;
+        row += at_once;
+        if (mine < step) return;
+        mine -= step;
+        row += ((int64_t)gridDim.x - 1) * step;
+        if (kStage) {
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(ptx::smem_u32(bars.read + st));
+            late = true;
+            if (++st == in.stages) {
+                st = 0;
+                phase ^= 1u;
+            }
         }
+        item += gridDim.x;
     }
     // what a block that gave up has ordered still comes in
     __device__ __forceinline__ void end() const {
-        if (kStage && threadIdx.x == 0 && *(volatile int *)failed) {
+        if (kStage && threadIdx.x == 0 && *(volatile int *)&bars.failed) {
             record_status(GLA_ERR_TIMEOUT);
-            for (int i = 0; i < in.stages; ++i) ptx::mbar_wait(ptx::smem_u32(full + i), phase ^ (uint32_t)(i < st), nullptr, kWaitNs);
+            for (int i = 0; i < in.stages; ++i) ptx::mbar_wait(ptx::smem_u32(bars.full + i), phase ^ (uint32_t)(i < st), nullptr, kWaitNs);
         }
     }
-    // four channels of array i
-    template <typename T> __device__ __forceinline__ void get(Pair (&v)[2], int i, int row_in_item, int D, int channel) const {
-        using Raw = typename Four<T>::Raw;
-        if (kStage)
-            Four<T>::open(v, *reinterpret_cast<const Raw *>(ring + st * in.stage_bytes + in.at[i] +
-                                                            (row_in_item * D + channel) * (int)sizeof(T)));
-        else
-            Four<T>::open(v, __ldg(reinterpret_cast<const Raw *>((const T *)in.from[i] + (item * step + row_in_item) * D + channel)));
+    // a channel of the thread's row of array i, staged or in memory
+    template <typename T> __device__ __forceinline__ const T *at(int i, int D, int channel) const {
+        if (kStage) return reinterpret_cast<const T *>(ring + st * in.stage_bytes + in.at[i]) + mine * D + channel;
+        return (const T *)in.from[i] + row * D + channel;
+    }
+};
+
+// A thread's place: its first channel and how many of its vectors exist.
+template <int kVec> struct Place {
+    int channel, count;
+    __device__ __forceinline__ Place(int D, int lanes) {
+        const int lane = threadIdx.x % lanes;
+        channel = lanes < 32 ? lane * 4 : (lane >> 5) * (kStride * kVec) + (lane & 31) * 4;
+        count = channel >= D ? 0 : lanes < 32 ? 1 : min(kVec, (D - channel + kStride - 1) / kStride);
     }
 };
 
 struct Weights {
     const float *scale, *post_weight, *post_bias, *weight, *bias;
+    __device__ __forceinline__ Weights from(int channel) const {
+        auto at = [&](const float *p) { return p == nullptr ? nullptr : p + channel; };
+        return {at(scale), at(post_weight), at(post_bias), at(weight), at(bias)};
+    }
+    // those that there are, in shared memory, by the whole block
+    __device__ __forceinline__ Weights shared(float *to, int D) const {
+        auto copy = [&](const float *p) -> const float * {
+            if (p == nullptr) return nullptr;
+            for (int i = threadIdx.x; i < D / 4; i += blockDim.x)
+                reinterpret_cast<float4 *>(to)[i] = __ldg(reinterpret_cast<const float4 *>(p) + i);
+            const float *const there = to;
+            to += D;
+            return there;
+        };
+        const float *const a = copy(scale), *const b = copy(post_weight), *const c = copy(post_bias), *const d = copy(weight);
+        return {a, b, c, d, copy(bias)};
+    }
 };
 
-// The mean (of a layer norm; else 0) and the reciprocal root of one or two arrays' rows: GET(0 or 1, j, v) reads vector j.
-template <int kVec, class Get>
-__device__ __forceinline__ void statistics(Get get, bool one, bool two, int count, int kind, float inv, float eps, int lanes, Meeting &m,
-                                           int &half, float2 &mean, float2 &root) {
-    mean = make_float2(0.f, 0.f);
-    if (kind == GLA_NORM_LAYER) {
-        Pair s = both(0.f), t = both(0.f), v[2];
-#pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            if (j < count) {
-                if (one) get(0, j, v), s = s + (v[0] + v[1]);
-                if (two) get(1, j, v), t = t + (v[0] + v[1]);
-            }
-        mean = row_sum(make_float2(total(s), total(t)), lanes, m, half);
-        mean.x *= inv, mean.y *= inv;
-    }
-    Pair s = both(0.f), t = both(0.f), v[2];
-    const Pair a = both(-mean.x), b = both(-mean.y);
-#pragma unroll
-    for (int j = 0; j < kVec; ++j)
-        if (j < count) {
-            if (one) {
-                get(0, j, v);
-                v[0] = v[0] + a, v[1] = v[1] + a;
-                s = fma(v[0], v[0], fma(v[1], v[1], s));
-            }
-            if (two) {
-                get(1, j, v);
-                v[0] = v[0] + b, v[1] = v[1] + b;
-                t = fma(v[0], v[0], fma(v[1], v[1], t));
-            }
-        }
-    root = row_sum(make_float2(total(s), total(t)), lanes, m, half);
-    root.x = rsqrtf(fmaf(root.x, inv, eps)), root.y = rsqrtf(fmaf(root.y, inv, eps));
-}
-
-template <typename T, typename TS, int kVec, bool kStage, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads <= 256 ? 3 : 1)
-fwd_kernel(Inputs<3> in, Weights w, int kind, int post, int act, float eps, TS *__restrict__ r, T *__restrict__ out, int64_t rows,
-           int D, int lanes) {
+template <typename T, typename TS, int kVec, bool kStage, int kMost>
+__global__ void __launch_bounds__(kMost, kMost <= 256 ? 3 : 1)
+fwd_kernel(const Inputs<3> in, Weights weights, int kind, int post, int act, float eps, TS *__restrict__ r, T *__restrict__ out,
+           int64_t rows, int D, int lanes, int params_at) {
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ uint64_t full[kMaxStages];
-    __shared__ int failed;
+    __shared__ Bars bars;
     __shared__ __align__(16) Meeting meet;
-    int half = 0;
-    const Place pl(D, lanes);
+    const Place<kVec> pl(D, lanes);
     const float inv = 1.f / (float)D;
-    const bool has_y = in.from[1] != nullptr, has_gate = in.from[2] != nullptr;
-    const bool meets = lanes > 32 && (post || out != nullptr);
-    Rows<kStage, 3> it(in, ring, full, &failed, rows, lanes);
+    const bool has_y = in.from[1] != nullptr, has_gate = in.from[2] != nullptr, meets = lanes > 32 && (post || out != nullptr);
+    Rows<kStage, 3> it(in, ring, bars, rows, lanes);
     clear(meet);
+    const Weights w = (params_at >= 0 ? weights.shared(reinterpret_cast<float *>(ring + params_at), D) : weights).from(pl.channel);
     __syncthreads();
-    for (; it.more(); it.next()) {
-        if (!meets) {
-            __syncthreads();
-            it.refill();
-        }
-        it.arrive();
-        const int64_t row = it.item * it.step + pl.row, at = row * D + pl.channel;
-        const int count = row < rows ? pl.count : 0;
-        Pair q = both(1.f), m = both(0.f);
-        if (post) {
-            float2 mean, root;
-            statistics<kVec>([&](int, int j, Pair (&v)[2]) { it.template get<T>(v, 1, pl.row, D, pl.channel + j * pl.stride); }, true,
-                             false, count, kind, inv, eps, lanes, meet, half, mean, root);
-            q = both(root.x), m = both(-mean.x);
+    int half = 0;
+    auto row = [&](auto all) {
+        using Vs = Vectors<kVec, all.value>;
+        const Vs vs{it.row < rows ? pl.count : 0};
+        const int64_t at = it.row * D + pl.channel;
+        typename Vs::V v;
+        // v becomes n(v)
+        auto normalise = [&](typename Vs::V &x) {
+            if (kind == GLA_NORM_LAYER) vs.shift(x, -row_sum(Vs::sum(x), 0.f, lanes, meet, half).x * inv);
+            vs.times(x, rsqrtf(fmaf(row_sum(Vs::squares(x), 0.f, lanes, meet, half).x, inv, eps)));
             if (meets) it.refill();
-        }
-        Pair v[kVec][2];
+        };
         if (has_y) {
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                v[j][0] = v[j][1] = both(0.f);
-                if (j < count) {
-                    const int c = pl.channel + j * pl.stride;
-                    Pair u[2], g[2], a[2], b[2];
-                    it.template get<TS>(v[j], 0, pl.row, D, c);
-                    it.template get<T>(u, 1, pl.row, D, c);
-                    if (post) {
-                        param(a, w.post_weight, c, 1.f);
-                        param(b, w.post_bias, c, 0.f);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) u[e] = fma((u[e] + m) * q, a[e], b[e]);
-                    }
-                    if (has_gate) {
-                        it.template get<T>(g, 2, pl.row, D, c);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) u[e] = u[e] * activation(g[e], act);
-                    }
-                    param(a, w.scale, c, 1.f);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) v[j][e] = fma(u[e], a[e], v[j][e]);
-                    put<TS>(r + at + j * pl.stride, v[j]);
-                }
+            typename Vs::V u;
+            vs.fetch(u, it.template at<T>(1, D, pl.channel));
+            if (post) {
+                normalise(u);
+                vs.times(u, w.post_weight);
+                vs.plus(u, w.post_bias);
             }
+            if (has_gate) {
+                typename Vs::V g;
+                vs.fetch(g, it.template at<T>(2, D, pl.channel));
+                if (act == kSilu) Vs::template gate<kSilu>(g);
+                else if (act == kSigmoid) Vs::template gate<kSigmoid>(g);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) u[j][0] = u[j][0] * g[j][0], u[j][1] = u[j][1] * g[j][1];
+            }
+            vs.times(u, w.scale);
+            vs.fetch(v, it.template at<TS>(0, D, pl.channel));
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) v[j][0] = v[j][0] + u[j][0], v[j][1] = v[j][1] + u[j][1];
+            vs.store(r + at, v);
+            vs.clear(v);
         } else {
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                v[j][0] = v[j][1] = both(0.f);
-                if (j < count) it.template get<TS>(v[j], 0, pl.row, D, pl.channel + j * pl.stride);
-            }
+            vs.fetch(v, it.template at<TS>(0, D, pl.channel));
         }
         if (out != nullptr) {
-            float2 mean, root;
-            statistics<kVec>([&](int, int j, Pair (&x)[2]) { x[0] = v[j][0], x[1] = v[j][1]; }, true, false, count, kind, inv, eps,
-                             lanes, meet, half, mean, root);
-            if (meets && !post) it.refill();
-            q = both(root.x), m = both(-mean.x);
-#pragma unroll
-            for (int j = 0; j < kVec; ++j)
-                if (j < count) {
-                    const int c = pl.channel + j * pl.stride;
-                    Pair a[2], b[2];
-                    param(a, w.weight, c, 1.f);
-                    param(b, w.bias, c, 0.f);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) a[e] = fma((v[j][e] + m) * q, a[e], b[e]);
-                    put<T>(out + at + j * pl.stride, a);
-                }
+            normalise(v);
+            vs.times(v, w.weight);
+            vs.plus(v, w.bias);
+            vs.store(out + at, v);
         }
+    };
+    const bool full_rows = (lanes < 32 ? D == lanes * 4 : D % (kStride * kVec) == 0) && rows % it.step == 0;
+    for (; it.begin(meets); it.next()) {
+        if (full_rows) row(std::true_type{});
+        else row(std::false_type{});
     }
     it.end();
 }
 
-template <typename T, typename TS, int kVec, bool kStage, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads <= 320 ? 640 / kThreads : 1)
-bwd_kernel(Inputs<5> in, Weights w, int kind, int post, int act, float eps, TS *__restrict__ dx, T *__restrict__ dy,
-           T *__restrict__ dgate, float *__restrict__ part, int64_t rows, int D, int lanes) {
+// kMode: which parts there are, for the kernels built for one kind of call whose rows leave no thread without work; kAnyMode: all
+// of that is asked for at run time.  (Of 16,384 x 2,560 with all parts the latter takes a quarter more time.)
+enum Mode { kOut = 1, kY = 2, kPost = 4, kGated = 8, kGatedSigmoid = 16, kAnyMode = 32 };
+template <typename T, typename TS, int kVec, bool kStage, int kMost, int kMode>
+__global__ void __launch_bounds__(kMost, kMost <= 320 ? 2 : 1)
+bwd_kernel(const Inputs<5> in, Weights weights, int kind, int post_, int act, float eps, TS *__restrict__ dx, T *__restrict__ dy,
+           T *__restrict__ dgate, float *__restrict__ part, int64_t rows, int D, int lanes, int params_at) {
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ uint64_t full[kMaxStages];
-    __shared__ int failed;
+    __shared__ Bars bars;
     __shared__ __align__(16) Meeting meet;
-    __shared__ float4 tops[kRowsThreads];
-    int half = 0;
-    const Place pl(D, lanes);
+    const Place<kVec> pl(D, lanes);
     const float inv = 1.f / (float)D;
-    const bool has_dr = in.from[0] != nullptr, has_out = in.from[1] != nullptr, has_y = in.from[3] != nullptr,
-               has_gate = in.from[4] != nullptr;
+    constexpr bool kAny = kMode == kAnyMode;
+    const bool has_dr = in.from[0] != nullptr, layer = kind == GLA_NORM_LAYER;
+    const bool has_out = kAny ? in.from[1] != nullptr : (kMode & kOut) != 0, has_y = kAny ? in.from[3] != nullptr : (kMode & kY) != 0,
+               has_gate = kAny ? in.from[4] != nullptr : (kMode & (kGated | kGatedSigmoid)) != 0, post = kAny ? post_ != 0 : (kMode & kPost) != 0;
     const bool meets = lanes > 32 && (post || has_out);
     Pair sums[kSums][kVec][2];
 #pragma unroll
     for (int i = 0; i < kSums; ++i)
 #pragma unroll
         for (int j = 0; j < kVec; ++j) sums[i][j][0] = sums[i][j][1] = both(0.f);
-    Rows<kStage, 5> it(in, ring, full, &failed, rows, lanes);
+    Rows<kStage, 5> it(in, ring, bars, rows, lanes);
     clear(meet);
+    const Weights w = (params_at >= 0 ? weights.shared(reinterpret_cast<float *>(ring + params_at), D) : weights).from(pl.channel);
     __syncthreads();
-    for (; it.more(); it.next()) {
-        if (!meets) {
-            __syncthreads();
-            it.refill();
-        }
-        it.arrive();
-        const int64_t row = it.item * it.step + pl.row, at = row * D + pl.channel;
-        const int count = row < rows ? pl.count : 0;
-        float2 mean, root;  // of r, and of y
+    int half = 0;
+    // every step reads what it needs again: registers are what the sums leave
+    auto row = [&](auto all) {
+        using Vs = Vectors<kVec, all.value>;
+        const Vs vs{it.row < rows ? pl.count : 0};
+        const int64_t at = it.row * D + pl.channel;
+        const TS *const from_r = it.template at<TS>(2, D, pl.channel);
+        const T *const from_out = it.template at<T>(1, D, pl.channel), *const from_y = it.template at<T>(3, D, pl.channel);
+        // one vector of an array, or of parameters
+        auto vec = [&](Pair (&v)[2], const auto *p, int j) {
+            using E = std::remove_cv_t<std::remove_reference_t<decltype(*p)>>;
+            if (!all.value) v[0] = v[1] = both(0.f);
+            if (vs.has(j)) Four<E>::open(v, *reinterpret_cast<const typename Four<E>::Raw *>(p + j * kStride));
+        };
+        Pair q = both(1.f), qm = both(0.f), uq = both(1.f), uqm = both(0.f);  // n(v) is (v + qm) q
         if (has_out || post) {
-            statistics<kVec>(
-                [&](int which, int j, Pair (&v)[2]) {
-                    if (which == 0) it.template get<TS>(v, 2, pl.row, D, pl.channel + j * pl.stride);
-                    else it.template get<T>(v, 3, pl.row, D, pl.channel + j * pl.stride);
-                },
-                has_out, post, count, kind, inv, eps, lanes, meet, half, mean, root);
-            if (meets) it.refill();
-        }
-        const Pair q = both(root.x), m = both(-mean.x), uq = both(root.y), um = both(-mean.y);
-        Pair m1 = both(0.f), m2 = both(0.f);
-        if (has_out) {
-            Pair s1 = both(0.f), s2 = both(0.f);
+            float mr = 0.f, mu = 0.f;
+            Pair s = both(0.f), t = both(0.f), v[2];
+            if (layer) {
 #pragma unroll
-            for (int j = 0; j < kVec; ++j)
-                if (j < count) {
-                    const int c = pl.channel + j * pl.stride;
-                    Pair up[2], h[2], wt[2];
-                    it.template get<T>(up, 1, pl.row, D, c);
-                    it.template get<TS>(h, 2, pl.row, D, c);
-                    param(wt, w.weight, c, 1.f);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        h[e] = (h[e] + m) * q;
-                        sums[3][j][e] = fma(up[e], h[e], sums[3][j][e]);
-                        sums[4][j][e] = sums[4][j][e] + up[e];
-                        const Pair t = up[e] * wt[e];
-                        s1 = s1 + t;
-                        s2 = fma(t, h[e], s2);
-                    }
+                for (int j = 0; j < kVec; ++j) {
+                    if (has_out) vec(v, from_r, j), s = s + (v[0] + v[1]);
+                    if (post) vec(v, from_y, j), t = t + (v[0] + v[1]);
                 }
-            const float2 s = row_sum(make_float2(total(s1), total(s2)), lanes, meet, half);
-            m1 = both(kind == GLA_NORM_LAYER ? -s.x * inv : 0.f), m2 = both(-s.y * inv);
-        }
-        Pair d[kVec][2], s1 = both(0.f), s2 = both(0.f);
+                const float2 o = row_sum(total(s), total(t), lanes, meet, half);
+                mr = -o.x * inv, mu = -o.y * inv;
+                s = t = both(0.f);
+            }
 #pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            if (j < count) {
-                const int c = pl.channel + j * pl.stride;
-                d[j][0] = d[j][1] = both(0.f);
-                if (has_dr) it.template get<TS>(d[j], 0, pl.row, D, c);
+            for (int j = 0; j < kVec; ++j) {
                 if (has_out) {
-                    Pair up[2], h[2], wt[2];
-                    it.template get<T>(up, 1, pl.row, D, c);
-                    it.template get<TS>(h, 2, pl.row, D, c);
-                    param(wt, w.weight, c, 1.f);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) d[j][e] = fma(fma((h[e] + m) * q, m2, fma(up[e], wt[e], m1)), q, d[j][e]);
+                    vec(v, from_r, j);
+                    const Pair by = both(vs.has(j) ? mr : 0.f);
+                    v[0] = v[0] + by, v[1] = v[1] + by;
+                    s = fma(v[0], v[0], fma(v[1], v[1], s));
                 }
-                put<TS>(dx + at + j * pl.stride, d[j]);
-                if (has_y) {
-                    Pair u[2], g[2], pw[2], pb[2], sc[2];
-                    it.template get<T>(u, 3, pl.row, D, c);
-                    param(sc, w.scale, c, 1.f);
-                    if (post) {
-                        param(pw, w.post_weight, c, 1.f);
-                        param(pb, w.post_bias, c, 0.f);
-                    }
-                    if (has_gate) it.template get<T>(g, 4, pl.row, D, c);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        Pair z = u[e], df = d[j][e];
-                        if (post) {
-                            u[e] = (u[e] + um) * uq;
-                            z = fma(u[e], pw[e], pb[e]);
-                        }
-                        if (has_gate) {
-                            Pair slope;
-                            df = df * activation(g[e], act, slope);
-                            g[e] = d[j][e] * sc[e] * z * slope;
-                        }
-                        sums[0][j][e] = fma(df, z, sums[0][j][e]);
-                        df = df * sc[e];
-                        if (post) {
-                            sums[1][j][e] = fma(df, u[e], sums[1][j][e]);
-                            sums[2][j][e] = sums[2][j][e] + df;
-                            df = df * pw[e];
-                            s1 = s1 + df;
-                            s2 = fma(df, u[e], s2);
-                        }
-                        d[j][e] = df;
-                    }
-                    if (has_gate) put<T>(dgate + at + j * pl.stride, g);
-                    if (!post) put<T>(dy + at + j * pl.stride, d[j]);
+                if (post) {
+                    vec(v, from_y, j);
+                    const Pair by = both(vs.has(j) ? mu : 0.f);
+                    v[0] = v[0] + by, v[1] = v[1] + by;
+                    t = fma(v[0], v[0], fma(v[1], v[1], t));
                 }
             }
-        if (post) {
-            const float2 s = row_sum(make_float2(total(s1), total(s2)), lanes, meet, half);
-            m1 = both(kind == GLA_NORM_LAYER ? -s.x * inv : 0.f), m2 = both(-s.y * inv);
-#pragma unroll
-            for (int j = 0; j < kVec; ++j)
-                if (j < count) {
-                    Pair u[2];
-                    it.template get<T>(u, 3, pl.row, D, pl.channel + j * pl.stride);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) d[j][e] = fma((u[e] + um) * uq, m2, d[j][e] + m1) * uq;
-                    put<T>(dy + at + j * pl.stride, d[j]);
-                }
+            const float2 o = row_sum(total(s), total(t), lanes, meet, half);
+            if (meets) it.refill();
+            const float rr = rsqrtf(fmaf(o.x, inv, eps)), ru = rsqrtf(fmaf(o.y, inv, eps));
+            q = both(rr), qm = both(mr);
+            if (post) uq = both(ru), uqm = both(mu);
         }
-    }
+        Pair m1 = both(0.f), m2 = both(0.f);
+        if (has_out) {
+            Pair s = both(0.f), t = both(0.f);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                Pair up[2], h[2], wt[2] = {both(1.f), both(1.f)};
+                vec(up, from_out, j);
+                vec(h, from_r, j);
+                if (w.weight != nullptr) vec(wt, w.weight, j);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    h[e] = (h[e] + qm) * q;
+                    sums[3][j][e] = fma(up[e], h[e], sums[3][j][e]);
+                    sums[4][j][e] = sums[4][j][e] + up[e];
+                    up[e] = up[e] * wt[e];
+                    s = s + up[e];
+                    t = fma(up[e], h[e], t);
+                }
+            }
+            const float2 o = row_sum(layer ? total(s) : 0.f, total(t), lanes, meet, half);
+            m1 = both(-o.x * inv), m2 = both(-o.y * inv);
+        }
+        typename Vs::V d;
+        Pair s = both(0.f), t = both(0.f);
+        // dx, and from there on through the scale and the gate, one vector after the other
+        auto through = [&](auto kind_of_act) {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                d[j][0] = d[j][1] = both(0.f);
+                if (has_dr) vec(d[j], it.template at<TS>(0, D, pl.channel), j);
+                if (has_out) {
+                    Pair up[2], h[2], wt[2] = {both(1.f), both(1.f)};
+                    vec(up, from_out, j);
+                    vec(h, from_r, j);
+                    if (w.weight != nullptr) vec(wt, w.weight, j);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) d[j][e] = fma(fma((h[e] + qm) * q, m2, fma(up[e], wt[e], m1)), q, d[j][e]);
+                    if (!vs.has(j)) d[j][0] = d[j][1] = both(0.f);
+                }
+                if (vs.has(j)) put<TS>(dx + at + j * kStride, d[j]);
+                if (!has_y) continue;
+                Pair u[2], z[2], p[2];
+                vec(u, from_y, j);
+                if (post) u[0] = (u[0] + uqm) * uq, u[1] = (u[1] + uqm) * uq;
+                z[0] = u[0], z[1] = u[1];  // what the scale and the gate multiply
+                if (w.post_weight != nullptr) {
+                    vec(p, w.post_weight, j);
+                    z[0] = z[0] * p[0], z[1] = z[1] * p[1];
+                }
+                if (w.post_bias != nullptr) {
+                    vec(p, w.post_bias, j);
+                    z[0] = z[0] + p[0], z[1] = z[1] + p[1];
+                }
+                Pair sc[2] = {both(1.f), both(1.f)};
+                if (w.scale != nullptr) vec(sc, w.scale, j);
+                if (kind_of_act.value >= 0) {
+                    Pair g[2], slope;
+                    vec(g, it.template at<T>(4, D, pl.channel), j);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const Pair f = activation(g[e], kind_of_act.value, slope);
+                        g[e] = d[j][e] * sc[e] * z[e] * slope;
+                        d[j][e] = d[j][e] * f;
+                    }
+                    if (vs.has(j)) put<T>(dgate + at + j * kStride, g);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    sums[0][j][e] = fma(d[j][e], z[e], sums[0][j][e]);
+                    d[j][e] = d[j][e] * sc[e];
+                }
+                if (!post) {
+                    if (vs.has(j)) put<T>(dy + at + j * kStride, d[j]);
+                    continue;
+                }
+                if (w.post_weight != nullptr) vec(p, w.post_weight, j);
+                else p[0] = p[1] = both(1.f);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    sums[1][j][e] = fma(d[j][e], u[e], sums[1][j][e]);
+                    sums[2][j][e] = sums[2][j][e] + d[j][e];
+                    d[j][e] = d[j][e] * p[e];
+                    s = s + d[j][e];
+                    t = fma(d[j][e], u[e], t);
+                }
+            }
+        };
+        if (!kAny) through(std::integral_constant<int, (kMode & kGated) != 0 ? (int)kSilu : (kMode & kGatedSigmoid) != 0 ? (int)kSigmoid : -1>{});
+        else if (!has_gate) through(std::integral_constant<int, -1>{});
+        else if (act == kSilu) through(std::integral_constant<int, kSilu>{});
+        else if (act == kSigmoid) through(std::integral_constant<int, kSigmoid>{});
+        else through(std::integral_constant<int, kNone>{});
+        if (post) {
+            const float2 o = row_sum(layer ? total(s) : 0.f, total(t), lanes, meet, half);
+            m1 = both(-o.x * inv), m2 = both(-o.y * inv);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                Pair u[2];
+                vec(u, from_y, j);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) d[j][e] = fma((u[e] + uqm) * uq, m2, d[j][e] + m1) * uq;
+                if (vs.has(j)) put<T>(dy + at + j * kStride, d[j]);
+            }
+        }
+    };
+    for (; it.begin(meets); it.next()) row(std::integral_constant<bool, !kAny>{});
     it.end();
     // the block's rows of one channel set meet in shared memory; one writer per channel
     float *to = part + (int64_t)blockIdx.x * kSums * D;
-    const int step = blockDim.x / lanes;
+    const int at_once = blockDim.x / lanes, mine = threadIdx.x / lanes;
+    float4 *const tops = reinterpret_cast<float4 *>(ring);  // the stages are read
 #pragma unroll
     for (int i = 0; i < kSums; ++i)
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
             float4 v = Four<float>::close(sums[i][j]);
-            if (step > 1) {
+            if (at_once > 1) {
                 __syncthreads();
                 tops[threadIdx.x] = v;
                 __syncthreads();
-                if (pl.row == 0)
-                    for (int m = 1; m < step; ++m) {
+                if (mine == 0)
+                    for (int m = 1; m < at_once; ++m) {
                         const float4 o = tops[threadIdx.x + m * lanes];
                         v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
                     }
             }
-            if (pl.row == 0 && j < pl.count)
-                *reinterpret_cast<float4 *>(to + (int64_t)i * D + pl.channel + j * pl.stride) = v;
+            if (mine == 0 && j < pl.count)
+                *reinterpret_cast<float4 *>(to + (int64_t)i * D + pl.channel + j * kStride) = v;
         }
 }
 
@@ -523,46 +633,54 @@ sum_kernel(const float *__restrict__ part, int nblocks, int D, Sums sums) {
     }
 }
 
+// Blocks of an SM: as many as the threads' registers allow, 85 a thread of the forward and 102 of the gradient.
+constexpr int kFwdThreads = 768, kBwdThreads = 640;
+int per_sm(const Plan &pl, int threads) { return threads < pl.threads ? 1 : threads / pl.threads; }
 int blocks(const Plan &pl, int64_t rows, int per_sm) {
     const int64_t need = (rows + pl.rows - 1) / pl.rows;
     int64_t most = (int64_t)device_info().sm_count * per_sm;
     if (most < 1) most = 1;
     return (int)(need < most ? need : most);
 }
-// Blocks of an SM: as many as the threads' registers allow, 85 a thread of the forward and 102 of the gradient.
-int per_sm(const Plan &pl, int threads) {
-    const int n = threads / pl.threads;
-    return n < 1 ? 1 : n;
-}
-constexpr int kFwdThreads = 768, kBwdThreads = 640;
 
-constexpr int kMostShared = 220 * 1024;
+constexpr int kMostShared = 218 * 1024;
 
-// The stages of a block: rows of each array one behind the other.
-template <int kArrays> int lay_out(Inputs<kArrays> &in, const Plan &pl, int per_sm) {
-    int at = 0;
+// The stages of a block: an item's rows of each array one behind the other; behind them the parameters, `params` bytes, where
+// there is room (else params_at is negative: they are read from memory, and what shared memory leaves caches them).  Short rows
+// are taken some at a time, while there are enough for all blocks: an item's copies then serve several rows of a thread.
+template <int kArrays> int lay_out(Inputs<kArrays> &in, const Plan &pl, int64_t rows, int per_sm, int nblocks, int params, int &params_at) {
+    int row = 0, at = 0;
+    for (int i = 0; i < kArrays; ++i)
+        if (in.from[i] != nullptr) row += in.row_bytes[i];
+    in.passes = 1;
+    while (in.passes < 8 && 2 * in.passes * pl.rows * row <= 16 * 1024 && rows >= 4LL * in.passes * pl.rows * nblocks) in.passes *= 2;
     for (int i = 0; i < kArrays; ++i) {
         in.at[i] = at;
-        if (in.from[i] != nullptr) at += (pl.rows * in.row_bytes[i] + 127) / 128 * 128;
+        if (in.from[i] != nullptr) at += (in.passes * pl.rows * in.row_bytes[i] + 127) / 128 * 128;
     }
     in.stage_bytes = at;
-    const int room = 190 * 1024 / per_sm - 6144;  // what is left caches the parameters
-    in.stages = room / at;
-    if (in.stages < 2 && per_sm == 1) in.stages = kMostShared / at;
+    const int room = kMostShared / per_sm - (per_sm > 1 ? 2048 : 0);
+    const bool shared = params > 0 && 2 * at + params <= room;
+    in.stages = shared ? (room - params) / at : (room - (per_sm > 1 ? 28 * 1024 / per_sm : 0)) / at;
     if (in.stages > kMaxStages) in.stages = kMaxStages;
     if (in.stages < 2) in.stages = 0;
-    return in.stages * at;
+    int bytes = in.stages * at;
+    if (bytes < 16 * pl.threads) bytes = 16 * pl.threads;
+    params_at = in.stages > 0 && shared ? bytes : -1;
+    return bytes + (params_at >= 0 ? params : 0);
 }
 
-// RUN(T, TS, kVec, kStage, kThreads) for a call's types and plan; kSmall: threads of the kernels that share an SM.
+// RUN(T, TS, kVec, kStage, kMost) for a call's types and plan.
 #define GLA_BY_STAGE(RUN, T, TS, V, N)                 \
     if (staged) { RUN(T, TS, V, true, N) }             \
     else { RUN(T, TS, V, false, N) }
-#define GLA_BY_PLAN(RUN, T, TS)                                                     \
-    if (pl.vecs == kVecs && pl.threads <= kSmall) { GLA_BY_STAGE(RUN, T, TS, kVecs, kSmall) } \
-    else if (pl.vecs == kVecs && pl.threads <= 512) { GLA_BY_STAGE(RUN, T, TS, kVecs, 512) }  \
-    else if (pl.vecs == kVecs) { GLA_BY_STAGE(RUN, T, TS, kVecs, 1024) }            \
-    else { GLA_BY_STAGE(RUN, T, TS, 4, 1024) }
+#define GLA_BY_PLAN(RUN, T, TS)                                                                     \
+    if (pl.threads <= kSmall && pl.vecs == 1) { GLA_BY_STAGE(RUN, T, TS, 1, kSmall) }               \
+    else if (pl.threads <= kSmall && pl.vecs == 2) { GLA_BY_STAGE(RUN, T, TS, 2, kSmall) }          \
+    else if (pl.threads <= kSmall && pl.vecs == kVecs) { GLA_BY_STAGE(RUN, T, TS, kVecs, kSmall) }  \
+    else if (pl.threads <= 512 && pl.vecs == kVecs) { GLA_BY_STAGE(RUN, T, TS, kVecs, 512) }        \
+    else if (pl.vecs == kVecs) { GLA_BY_STAGE(RUN, T, TS, kVecs, 1024) }                            \
+    else { GLA_BY_STAGE(RUN, T, TS, kWideVecs, 1024) }
 #define GLA_BY_TYPE(RUN)                                                                          \
     if (dtype == GLA_F32) { GLA_BY_PLAN(RUN, float, float) }                                      \
     else if (stream_dtype == GLA_F32) { GLA_BY_PLAN(RUN, __nv_bfloat16, float) }                  \
@@ -594,17 +712,19 @@ int fwd(const void *x, const void *y, const void *gate, const float *scale, cons
     constexpr int kVecs = kFwdVecs, kSmall = 256;
     const Plan pl = make_plan(D, kVecs);
     const Weights w{scale, post_weight, post_bias, weight, bias};
-    const int e = dtype == GLA_F32 ? 4 : 2, es = stream_dtype == GLA_F32 ? 4 : 2, n = per_sm(pl, kFwdThreads);
-    Inputs<3> in{{x, y, gate}, {D * es, D * e, D * e}, {}, 0, 0};
-    const int bytes = lay_out(in, pl, n);
-    const bool staged = in.stages > 0;
+    const int e = dtype == GLA_F32 ? 4 : 2, es = stream_dtype == GLA_F32 ? 4 : 2;
+    Inputs<3> in{{x, y, gate}, {D * es, D * e, D * e}, {}, 0, 0, 1};
+    const int n = per_sm(pl, kFwdThreads);
     const unsigned grid = (unsigned)blocks(pl, rows, n);
+    int params_at;
+    const int bytes = lay_out(in, pl, rows, n, (int)grid, 0, params_at);
+    const bool staged = in.stages > 0;
     bool ok = false;
 #define GLA_RUN(T, TS, V, S, N)                                                                                            \
     {                                                                                                                      \
         constexpr auto kKernel = fwd_kernel<T, TS, V, S, N>;                                                               \
         ok = allow_most<kKernel>();                                                                                        \
-        if (ok) kKernel<<<grid, pl.threads, bytes, st>>>(in, w, kind, post, act, eps, (TS *)r, (T *)out, rows, D, pl.lanes); \
+        if (ok) kKernel<<<grid, pl.threads, bytes, st>>>(in, w, kind, post, act, eps, (TS *)r, (T *)out, rows, D, pl.lanes, params_at); \
     }
     GLA_BY_TYPE(GLA_RUN)
 #undef GLA_RUN
@@ -623,18 +743,41 @@ int bwd(const void *dr, const void *dout, const void *r, const void *y, const vo
     bool ok = true;
     if (nb > 0) {
         const int e = dtype == GLA_F32 ? 4 : 2, es = stream_dtype == GLA_F32 ? 4 : 2;
-        Inputs<5> in{{dr, dout, dout != nullptr ? r : nullptr, y, gate}, {D * es, D * e, D * es, D * e, D * e}, {}, 0, 0};
-        const int bytes = lay_out(in, pl, n);
+        Inputs<5> in{{dr, dout, dout != nullptr ? r : nullptr, y, gate}, {D * es, D * e, D * es, D * e, D * e}, {}, 0, 0, 1};
+        int params_at;
+        const int arrays = (scale != nullptr) + (post_weight != nullptr) + (post_bias != nullptr) + (weight != nullptr);
+        const int bytes = lay_out(in, pl, rows, n, nb, arrays * D * 4, params_at);
         const bool staged = in.stages > 0;
-#define GLA_RUN(T, TS, V, S, N)                                                                                            \
+        const int mode = (dout != nullptr ? kOut : 0) + (y != nullptr ? kY : 0) + (post ? kPost : 0) +
+                         (gate == nullptr ? 0 : act == kSilu ? kGated : act == kSigmoid ? kGatedSigmoid : kAnyMode);
+        const bool whole = staged && pl.vecs == kVecs && pl.threads <= kSmall && D % (kStride * kVecs) == 0 &&
+                           rows % ((int64_t)pl.rows * in.passes) == 0;
+#define GLA_MODE(T, TS, V, S, N, M)                                                                                        \
         {                                                                                                                  \
-            constexpr auto kKernel = bwd_kernel<T, TS, V, S, N>;                                                           \
+            constexpr auto kKernel = bwd_kernel<T, TS, V, S, N, M>;                                                        \
             ok = allow_most<kKernel>();                                                                                    \
             if (ok)                                                                                                        \
                 kKernel<<<(unsigned)nb, pl.threads, bytes, st>>>(in, w, kind, post, act, eps, (TS *)dx, (T *)dy,           \
-                                                                 (T *)dgate, (float *)ws, rows, D, pl.lanes);              \
+                                                                 (T *)dgate, (float *)ws, rows, D, pl.lanes, params_at);   \
         }
-        GLA_BY_TYPE(GLA_RUN)
+#define GLA_RUN(T, TS, V, S, N) GLA_MODE(T, TS, V, S, N, kAnyMode)
+#define GLA_WHOLE(T, TS)                                                                                                   \
+        if (mode == kOut + kY + kPost + kGated) GLA_MODE(T, TS, kVecs, true, kSmall, kOut + kY + kPost + kGated)           \
+        else if (mode == kOut + kY + kPost + kGatedSigmoid) GLA_MODE(T, TS, kVecs, true, kSmall, kOut + kY + kPost + kGatedSigmoid) \
+        else if (mode == kOut + kY + kPost) GLA_MODE(T, TS, kVecs, true, kSmall, kOut + kY + kPost)                        \
+        else if (mode == kOut + kY + kGated) GLA_MODE(T, TS, kVecs, true, kSmall, kOut + kY + kGated)                      \
+        else if (mode == kOut + kY + kGatedSigmoid) GLA_MODE(T, TS, kVecs, true, kSmall, kOut + kY + kGatedSigmoid)        \
+        else if (mode == kOut + kY) GLA_MODE(T, TS, kVecs, true, kSmall, kOut + kY)                                        \
+        else found = false;
+        bool found = whole;
+        if (whole) {
+            if (dtype == GLA_F32) { GLA_WHOLE(float, float) }
+            else if (stream_dtype == GLA_F32) { GLA_WHOLE(__nv_bfloat16, float) }
+            else { GLA_WHOLE(__nv_bfloat16, __nv_bfloat16) }
+        }
+        if (!found) { GLA_BY_TYPE(GLA_RUN) }
+#undef GLA_WHOLE
+#undef GLA_MODE
 #undef GLA_RUN
         count_launches(1);
     }

@@ -652,7 +652,7 @@ GLA_API int gla_scan_step(const void *x, const void *g, const void *gate, float 
  *   out NULL     the sum alone; weight and bias must be NULL
  *   scale, weight, bias, post_weight, post_bias  [D] f32; NULL for ones / zeros
  *   dtype        GLA_BF16 or GLA_F32;  stream_dtype  dtype, or GLA_F32
- *   D            a multiple of 8, 8 <= D <= 16384;  rows >= 0;  eps > 0
+ *   D            a multiple of 8, 8 <= D <= 16384;  0 <= rows < 2^31 - 256;  eps > 0
  * Statistics and arithmetic are f32, out is of the sum before it is rounded to r.  Returns a gla_status.
  */
 typedef enum { GLA_NORM_LAYER = 0, GLA_NORM_RMS = 1 } gla_norm_kind;
