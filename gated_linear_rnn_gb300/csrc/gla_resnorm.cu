@@ -25,7 +25,10 @@ namespace gla {
 namespace resnorm {
 namespace {
 
-constexpr int kSums = 5;  // dscale, dpost_weight, dpost_bias, dweight, dbias
+// Sums over tokens, with f = act(gate): of dx f n(y) and dx f, of dout h and dout.  They give dpost_weight and dpost_bias by the
+// factor scale, dscale = post_weight (the first) + post_bias (the second), dweight and dbias.  (Without the norm of y the
+// first is of dx f y, and dscale itself.)
+constexpr int kSums = 4;
 constexpr int kMaxStages = 6;
 constexpr int kThreads = 256;  // of a block with several rows
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -163,6 +166,29 @@ template <int kVec, bool kAll> struct Vectors {
     }
 };
 
+// Minus a value near a row's mean (is there a row): the mean of its first 8 channels in bf16, which every thread reads, of its
+// first 128 (all, where there are no more) in f32.  Sums of v + near and of its square then give the row's variance with a
+// loss of (their mean)^2 over the variance, which is below D / 8 or D / 128: at worst those channels alone are off from all
+// others.  That leaves 2^-13 and 2^-17 of the variance at 16,384 channels, and 2^-24 times a small number for common rows.
+template <typename E> __device__ __forceinline__ float near_mean(const E *row, int D, int lanes, bool is) {
+    if (sizeof(E) == 2) {
+        if (!is) return 0.f;
+        const uint4 w = *reinterpret_cast<const uint4 *>(row);
+        Pair v[2], u[2];
+        Four<__nv_bfloat16>::open(v, make_uint2(w.x, w.y));
+        Four<__nv_bfloat16>::open(u, make_uint2(w.z, w.w));
+        return total((v[0] + v[1]) + (u[0] + u[1])) * -0.125f;
+    }
+    const int n = min(D, kStride), c = (threadIdx.x % lanes & 31) * 4;
+    float s = 0.f;
+    if (is && c < n) {
+        const float4 w = *reinterpret_cast<const float4 *>(row + c);
+        s = (w.x + w.y) + (w.z + w.w);
+    }
+    for (int d = min(lanes, 32) >> 1; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    return s * (-1.f / (float)n);
+}
+
 // Two sums over a row's threads at once.  The warps of a row meet in shared memory, in one half of it after the other, so that
 // one barrier a sum is enough; every thread of the block calls this.
 struct Meeting {
@@ -194,8 +220,49 @@ __device__ __forceinline__ float2 row_sum(float a, float b, int lanes, Meeting &
     const float o = __shfl_xor_sync(0xffffffffu, v, 16);
     return upper ? make_float2(o, v) : make_float2(v, o);
 }
-__device__ __forceinline__ void clear(Meeting &m) {  // warps that there are not add nothing
-    for (int i = threadIdx.x; i < 128; i += blockDim.x) (&m.at[0][0][0])[i] = 0.f;
+
+// Six sums at once, each thread's parts given and the row's sums returned in v: three halvings leave a lane with one of them.
+// kMost: the block's threads at most.
+struct SixMeeting {
+    float at[2][32][8];  // by warp
+};
+template <int kMost> __device__ __forceinline__ void row_sums(float (&v)[6], int lanes, SixMeeting &m, int &half) {
+    if (lanes < 32) {
+        for (int d = lanes >> 1; d > 0; d >>= 1)
+#pragma unroll
+            for (int i = 0; i < 6; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    const bool b16 = (lane & 16) != 0, b8 = (lane & 8) != 0, b4 = (lane & 4) != 0;
+    float w[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) w[i] = (b16 ? v[i + 3] : v[i]) + __shfl_xor_sync(0xffffffffu, b16 ? v[i] : v[i + 3], 16);
+    float x = (b8 ? w[1] : w[0]) + __shfl_xor_sync(0xffffffffu, b8 ? w[0] : w[1], 8);
+    const float y = w[2] + __shfl_xor_sync(0xffffffffu, w[2], 8);
+    x = (b4 ? y : x) + __shfl_xor_sync(0xffffffffu, b4 ? x : y, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    // the sum that a lane has: 3 (bit 4 of it) + 2 where bit 2 is set, else bit 3
+    if (lanes == 32) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(0xffffffffu, x, i / 3 * 16 + (i % 3 == 2 ? 4 : i % 3 * 8));
+        return;
+    }
+    float(&at)[32][8] = m.at[half];
+    if ((lane & 3) == 0 && !(b4 && b8)) at[threadIdx.x >> 5][(b16 ? 3 : 0) + (b4 ? 2 : b8 ? 1 : 0)] = x;
+    __syncthreads();
+    x = at[lane >> 3][lane & 7];
+#pragma unroll
+    for (int i = 1; i < (kMost / 32 + 3) / 4; ++i) x += at[(lane >> 3) + 4 * i][lane & 7];
+    x += __shfl_xor_sync(0xffffffffu, x, 16);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+#pragma unroll
+    for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(0xffffffffu, x, i);
+    half ^= 1;
+}
+template <class M> __device__ __forceinline__ void clear(M &m) {  // warps that there are not add nothing
+    for (int i = threadIdx.x; i < (int)(sizeof(M) / sizeof(float)); i += blockDim.x) reinterpret_cast<float *>(&m)[i] = 0.f;
 }
 
 // Arrays whose rows come in, and the stages that they come into: the rows of an item, of each array.
@@ -404,7 +471,10 @@ fwd_kernel(const Inputs<3> in, Weights weights, int kind, int post, int act, flo
 
 // kMode: which parts there are, for the kernels built for one kind of call whose rows leave no thread without work; kAnyMode: all
 // of that is asked for at run time.  (Of 16,384 x 2,560 with all parts the latter takes a quarter more time.)
-enum Mode { kOut = 1, kY = 2, kPost = 4, kGated = 8, kGatedSigmoid = 16, kAnyMode = 32 };
+// kParams: the parameters are in shared memory, all that the parts could ask for (ones and zeros for those that there are not).
+enum Mode { kOut = 1, kY = 2, kPost = 4, kGated = 8, kGatedSigmoid = 16, kAnyMode = 32, kParams = 64 };
+enum Param { kWeight, kScale, kPostWeight, kPostBias };
+constexpr __host__ __device__ int params_of(int mode) { return mode & kPost ? 4 : mode & kY ? 2 : 1; }
 template <typename T, typename TS, int kVec, bool kStage, int kMost, int kMode>
 __global__ void __launch_bounds__(kMost, kMost <= 320 ? 2 : 1)
 bwd_kernel(const Inputs<5> in, Weights weights, int kind, int post_, int act, float eps, TS *__restrict__ dx, T *__restrict__ dy,
@@ -412,9 +482,10 @@ bwd_kernel(const Inputs<5> in, Weights weights, int kind, int post_, int act, fl
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ Bars bars;
     __shared__ __align__(16) Meeting meet;
+    __shared__ __align__(16) SixMeeting six;
     const Place<kVec> pl(D, lanes);
     const float inv = 1.f / (float)D;
-    constexpr bool kAny = kMode == kAnyMode;
+    constexpr bool kAny = (kMode & kAnyMode) != 0;
     const bool has_dr = in.from[0] != nullptr, layer = kind == GLA_NORM_LAYER;
     const bool has_out = kAny ? in.from[1] != nullptr : (kMode & kOut) != 0, has_y = kAny ? in.from[3] != nullptr : (kMode & kY) != 0,
                has_gate = kAny ? in.from[4] != nullptr : (kMode & (kGated | kGatedSigmoid)) != 0, post = kAny ? post_ != 0 : (kMode & kPost) != 0;
@@ -426,13 +497,24 @@ bwd_kernel(const Inputs<5> in, Weights weights, int kind, int post_, int act, fl
         for (int j = 0; j < kVec; ++j) sums[i][j][0] = sums[i][j][1] = both(0.f);
     Rows<kStage, 5> it(in, ring, bars, rows, lanes);
     clear(meet);
-    const Weights w = (params_at >= 0 ? weights.shared(reinterpret_cast<float *>(ring + params_at), D) : weights).from(pl.channel);
+    clear(six);
+    constexpr bool kShared = (kMode & kParams) != 0;
+    if (kShared)
+        for (int i = 0; i < params_of(kMode); ++i) {
+            const float *const from = i == kWeight ? weights.weight : i == kScale ? weights.scale : i == kPostWeight ? weights.post_weight : weights.post_bias;
+            const float fill = i == kPostBias ? 0.f : 1.f;
+            float4 *const to = reinterpret_cast<float4 *>(ring + params_at) + i * (D / 4);
+            for (int c = threadIdx.x; c < D / 4; c += blockDim.x)
+                to[c] = from ? __ldg(reinterpret_cast<const float4 *>(from) + c) : make_float4(fill, fill, fill, fill);
+        }
+    const Weights w = kShared ? weights : (params_at >= 0 ? weights.shared(reinterpret_cast<float *>(ring + params_at), D) : weights).from(pl.channel);
+    const float *const params = reinterpret_cast<const float *>(ring + params_at) + pl.channel;
     __syncthreads();
     int half = 0;
-    // every step reads what it needs again: registers are what the sums leave
     auto row = [&](auto all) {
         using Vs = Vectors<kVec, all.value>;
-        const Vs vs{it.row < rows ? pl.count : 0};
+        const bool there = all.value || it.row < rows;
+        const Vs vs{there ? pl.count : 0};
         const int64_t at = it.row * D + pl.channel;
         const TS *const from_r = it.template at<TS>(2, D, pl.channel);
         const T *const from_out = it.template at<T>(1, D, pl.channel), *const from_y = it.template at<T>(3, D, pl.channel);
@@ -442,62 +524,66 @@ bwd_kernel(const Inputs<5> in, Weights weights, int kind, int post_, int act, fl
             if (!all.value) v[0] = v[1] = both(0.f);
             if (vs.has(j)) Four<E>::open(v, *reinterpret_cast<const typename Four<E>::Raw *>(p + j * kStride));
         };
-        Pair q = both(1.f), qm = both(0.f), uq = both(1.f), uqm = both(0.f);  // n(v) is (v + qm) q
+        // vector j of a parameter; v as it is where there is none
+        auto param = [&](Pair (&v)[2], Param which, int j) {
+            const float *const p = which == kWeight ? w.weight : which == kScale ? w.scale : which == kPostWeight ? w.post_weight : w.post_bias;
+            if (kShared) vec(v, params + which * D, j);
+            else if (p != nullptr) vec(v, p, j);
+        };
+        // n(r) = r' q + qm and n(y) = y' uq + uqm, of r' = r + near_r and y' = y + near_y
+        typename Vs::V rc, yc;
+        Pair q = both(1.f), qm = both(0.f), uq = both(1.f), uqm = both(0.f), m1 = both(0.f), m2 = both(0.f);
+        float near_r = 0.f, near_y = 0.f;
         if (has_out || post) {
-            float mr = 0.f, mu = 0.f;
-            Pair s = both(0.f), t = both(0.f), v[2];
             if (layer) {
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    if (has_out) vec(v, from_r, j), s = s + (v[0] + v[1]);
-                    if (post) vec(v, from_y, j), t = t + (v[0] + v[1]);
-                }
-                const float2 o = row_sum(total(s), total(t), lanes, meet, half);
-                mr = -o.x * inv, mu = -o.y * inv;
-                s = t = both(0.f);
+                if (has_out) near_r = near_mean(it.template at<TS>(2, D, 0), D, lanes, there);
+                if (post) near_y = near_mean(it.template at<T>(3, D, 0), D, lanes, there);
             }
+            Pair s[6];
+#pragma unroll
+            for (int i = 0; i < 6; ++i) s[i] = both(0.f);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 if (has_out) {
-                    vec(v, from_r, j);
-                    const Pair by = both(vs.has(j) ? mr : 0.f);
-                    v[0] = v[0] + by, v[1] = v[1] + by;
-                    s = fma(v[0], v[0], fma(v[1], v[1], s));
+                    Pair up[2], wt[2] = {both(1.f), both(1.f)};
+                    vec(rc[j], from_r, j);
+                    vec(up, from_out, j);
+                    param(wt, kWeight, j);
+                    const Pair by = both(vs.has(j) ? near_r : 0.f);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (layer) rc[j][e] = rc[j][e] + by;
+                        up[e] = up[e] * wt[e];
+                        s[0] = s[0] + rc[j][e];
+                        s[1] = fma(rc[j][e], rc[j][e], s[1]);
+                        s[2] = s[2] + up[e];
+                        s[3] = fma(up[e], rc[j][e], s[3]);
+                    }
                 }
                 if (post) {
-                    vec(v, from_y, j);
-                    const Pair by = both(vs.has(j) ? mu : 0.f);
-                    v[0] = v[0] + by, v[1] = v[1] + by;
-                    t = fma(v[0], v[0], fma(v[1], v[1], t));
+                    vec(yc[j], from_y, j);
+                    const Pair by = both(vs.has(j) ? near_y : 0.f);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (layer) yc[j][e] = yc[j][e] + by;
+                        s[4] = s[4] + yc[j][e];
+                        s[5] = fma(yc[j][e], yc[j][e], s[5]);
+                    }
                 }
             }
-            const float2 o = row_sum(total(s), total(t), lanes, meet, half);
+            float o[6];
+#pragma unroll
+            for (int i = 0; i < 6; ++i) o[i] = total(s[i]);
+            row_sums<kMost>(o, lanes, six, half);
             if (meets) it.refill();
-            const float rr = rsqrtf(fmaf(o.x, inv, eps)), ru = rsqrtf(fmaf(o.y, inv, eps));
-            q = both(rr), qm = both(mr);
-            if (post) uq = both(ru), uqm = both(mu);
-        }
-        Pair m1 = both(0.f), m2 = both(0.f);
-        if (has_out) {
-            Pair s = both(0.f), t = both(0.f);
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                Pair up[2], h[2], wt[2] = {both(1.f), both(1.f)};
-                vec(up, from_out, j);
-                vec(h, from_r, j);
-                if (w.weight != nullptr) vec(wt, w.weight, j);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    h[e] = (h[e] + qm) * q;
-                    sums[3][j][e] = fma(up[e], h[e], sums[3][j][e]);
-                    sums[4][j][e] = sums[4][j][e] + up[e];
-                    up[e] = up[e] * wt[e];
-                    s = s + up[e];
-                    t = fma(up[e], h[e], t);
-                }
-            }
-            const float2 o = row_sum(layer ? total(s) : 0.f, total(t), lanes, meet, half);
-            m1 = both(-o.x * inv), m2 = both(-o.y * inv);
+            // (a variance below zero is rounding; a NaN stays)
+            const float mr = layer ? o[0] * inv : 0.f, mu = layer ? o[4] * inv : 0.f;
+            const float vr = fmaf(-mr, mr, o[1] * inv), vu = fmaf(-mu, mu, o[5] * inv);
+            const float rr = rsqrtf((vr < 0.f ? 0.f : vr) + eps), ru = rsqrtf((vu < 0.f ? 0.f : vu) + eps);
+            q = both(rr), qm = both(-mr * rr);
+            if (post) uq = both(ru), uqm = both(-mu * ru);
+            if (layer) m1 = both(-o[2] * inv);
+            m2 = both(-fmaf(-mr, o[2], o[3]) * rr * inv);
         }
         typename Vs::V d;
         Pair s = both(0.f), t = both(0.f);
@@ -508,32 +594,36 @@ bwd_kernel(const Inputs<5> in, Weights weights, int kind, int post_, int act, fl
                 d[j][0] = d[j][1] = both(0.f);
                 if (has_dr) vec(d[j], it.template at<TS>(0, D, pl.channel), j);
                 if (has_out) {
-                    Pair up[2], h[2], wt[2] = {both(1.f), both(1.f)};
+                    Pair up[2], wt[2] = {both(1.f), both(1.f)};
                     vec(up, from_out, j);
-                    vec(h, from_r, j);
-                    if (w.weight != nullptr) vec(wt, w.weight, j);
+                    param(wt, kWeight, j);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) d[j][e] = fma(fma((h[e] + qm) * q, m2, fma(up[e], wt[e], m1)), q, d[j][e]);
+                    for (int e = 0; e < 2; ++e) {
+                        const Pair h = fma(rc[j][e], q, qm);
+                        sums[2][j][e] = fma(up[e], h, sums[2][j][e]);
+                        sums[3][j][e] = sums[3][j][e] + up[e];
+                        d[j][e] = fma(fma(h, m2, fma(up[e], wt[e], m1)), q, d[j][e]);
+                    }
                     if (!vs.has(j)) d[j][0] = d[j][1] = both(0.f);
                 }
                 if (vs.has(j)) put<TS>(dx + at + j * kStride, d[j]);
                 if (!has_y) continue;
-                Pair u[2], z[2], p[2];
-                vec(u, from_y, j);
-                if (post) u[0] = (u[0] + uqm) * uq, u[1] = (u[1] + uqm) * uq;
-                z[0] = u[0], z[1] = u[1];  // what the scale and the gate multiply
-                if (w.post_weight != nullptr) {
-                    vec(p, w.post_weight, j);
-                    z[0] = z[0] * p[0], z[1] = z[1] * p[1];
-                }
-                if (w.post_bias != nullptr) {
-                    vec(p, w.post_bias, j);
-                    z[0] = z[0] + p[0], z[1] = z[1] + p[1];
-                }
+                Pair u[2], p[2];
+                if (post) u[0] = fma(yc[j][0], uq, uqm), u[1] = fma(yc[j][1], uq, uqm);
+                else vec(u, from_y, j);
                 Pair sc[2] = {both(1.f), both(1.f)};
-                if (w.scale != nullptr) vec(sc, w.scale, j);
+                param(sc, kScale, j);
                 if (kind_of_act.value >= 0) {
                     Pair g[2], slope;
+                    Pair z[2] = {u[0], u[1]};  // what the scale and the gate multiply
+                    if (post) {
+                        p[0] = p[1] = both(1.f);
+                        param(p, kPostWeight, j);
+                        z[0] = z[0] * p[0], z[1] = z[1] * p[1];
+                        p[0] = p[1] = both(0.f);
+                        param(p, kPostBias, j);
+                        z[0] = z[0] + p[0], z[1] = z[1] + p[1];
+                    }
                     vec(g, it.template at<T>(4, D, pl.channel), j);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -545,19 +635,18 @@ bwd_kernel(const Inputs<5> in, Weights weights, int kind, int post_, int act, fl
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    sums[0][j][e] = fma(d[j][e], z[e], sums[0][j][e]);
+                    sums[0][j][e] = fma(d[j][e], u[e], sums[0][j][e]);
+                    if (post) sums[1][j][e] = sums[1][j][e] + d[j][e];
                     d[j][e] = d[j][e] * sc[e];
                 }
                 if (!post) {
                     if (vs.has(j)) put<T>(dy + at + j * kStride, d[j]);
                     continue;
                 }
-                if (w.post_weight != nullptr) vec(p, w.post_weight, j);
-                else p[0] = p[1] = both(1.f);
+                p[0] = p[1] = both(1.f);
+                param(p, kPostWeight, j);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    sums[1][j][e] = fma(d[j][e], u[e], sums[1][j][e]);
-                    sums[2][j][e] = sums[2][j][e] + d[j][e];
                     d[j][e] = d[j][e] * p[e];
                     s = s + d[j][e];
                     t = fma(d[j][e], u[e], t);
@@ -574,10 +663,13 @@ bwd_kernel(const Inputs<5> in, Weights weights, int kind, int post_, int act, fl
             m1 = both(-o.x * inv), m2 = both(-o.y * inv);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
-                Pair u[2];
-                vec(u, from_y, j);
+                Pair y[2];
+                vec(y, from_y, j);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) d[j][e] = fma((u[e] + uqm) * uq, m2, d[j][e] + m1) * uq;
+                for (int e = 0; e < 2; ++e) {
+                    if (layer) y[e] = y[e] + both(near_y);
+                    d[j][e] = fma(fma(y[e], uq, uqm), m2, d[j][e] + m1) * uq;
+                }
                 if (vs.has(j)) put<T>(dy + at + j * kStride, d[j]);
             }
         }
@@ -609,28 +701,38 @@ bwd_kernel(const Inputs<5> in, Weights weights, int kind, int post_, int act, fl
 }
 
 struct Sums {
-    float *to[kSums];
+    float *dscale, *dpost_weight, *dpost_bias, *dweight, *dbias;
 };
 
-// The blocks' parts of every sum added up, 32 channels x 8 runs of blocks a block, in a fixed order.
+// The blocks' parts of two of the sums added up, 32 channels x 8 runs of blocks a block, in a fixed order.
 __global__ void __launch_bounds__(256)
-sum_kernel(const float *__restrict__ part, int nblocks, int D, Sums sums) {
-    __shared__ float sm[8][33];
-    float *to = sums.to[blockIdx.y];
-    if (to == nullptr) return;
+sum_kernel(const float *__restrict__ part, int nblocks, int D, bool post, Weights w, Sums to) {
+    __shared__ float sm[2][8][33];
+    if (blockIdx.y == 0 ? !to.dscale && !to.dpost_weight && !to.dpost_bias : !to.dweight && !to.dbias) return;
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
-    float s = 0.f;
+    float s = 0.f, t = 0.f;
     if (c < D)
 #pragma unroll 8
-        for (int i = run; i < nblocks; i += 8) s += __ldg(part + ((int64_t)i * kSums + blockIdx.y) * D + c);
-    sm[run][threadIdx.x & 31] = s;
+        for (int i = run; i < nblocks; i += 8) {
+            const float *from = part + ((int64_t)i * kSums + blockIdx.y * 2) * D + c;
+            s += __ldg(from), t += __ldg(from + D);
+        }
+    sm[0][run][threadIdx.x & 31] = s;
+    sm[1][run][threadIdx.x & 31] = t;
     __syncthreads();
-    if (run == 0 && c < D) {
-        s = 0.f;
+    if (run != 0 || c >= D) return;
+    s = t = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += sm[i][threadIdx.x & 31];
-        to[c] = s;
+    for (int i = 0; i < 8; ++i) s += sm[0][i][threadIdx.x & 31], t += sm[1][i][threadIdx.x & 31];
+    if (blockIdx.y == 1) {
+        if (to.dweight) to.dweight[c] = s;
+        if (to.dbias) to.dbias[c] = t;
+        return;
     }
+    const float scale = w.scale ? w.scale[c] : 1.f;
+    if (to.dscale) to.dscale[c] = post ? fmaf(w.post_weight ? w.post_weight[c] : 1.f, s, w.post_bias ? w.post_bias[c] * t : 0.f) : s;
+    if (to.dpost_weight) to.dpost_weight[c] = scale * s;
+    if (to.dpost_bias) to.dpost_bias[c] = scale * t;
 }
 
 // Blocks of an SM: as many as the threads' registers allow, 85 a thread of the forward and 102 of the gradient.
@@ -659,9 +761,10 @@ template <int kArrays> int lay_out(Inputs<kArrays> &in, const Plan &pl, int64_t 
         if (in.from[i] != nullptr) at += (in.passes * pl.rows * in.row_bytes[i] + 127) / 128 * 128;
     }
     in.stage_bytes = at;
-    const int room = kMostShared / per_sm - (per_sm > 1 ? 2048 : 0);
+    const int room = kMostShared / per_sm - (per_sm > 1 ? 3328 : 0);
     const bool shared = params > 0 && 2 * at + params <= room;
     in.stages = shared ? (room - params) / at : (room - (per_sm > 1 ? 28 * 1024 / per_sm : 0)) / at;
+    if (in.stages < 2 && 2 * at <= room) in.stages = 2;
     if (in.stages > kMaxStages) in.stages = kMaxStages;
     if (in.stages < 2) in.stages = 0;
     int bytes = in.stages * at;
@@ -745,13 +848,14 @@ int bwd(const void *dr, const void *dout, const void *r, const void *y, const vo
         const int e = dtype == GLA_F32 ? 4 : 2, es = stream_dtype == GLA_F32 ? 4 : 2;
         Inputs<5> in{{dr, dout, dout != nullptr ? r : nullptr, y, gate}, {D * es, D * e, D * es, D * e, D * e}, {}, 0, 0, 1};
         int params_at;
-        const int arrays = (scale != nullptr) + (post_weight != nullptr) + (post_bias != nullptr) + (weight != nullptr);
-        const int bytes = lay_out(in, pl, rows, n, nb, arrays * D * 4, params_at);
-        const bool staged = in.stages > 0;
+        int arrays = (scale != nullptr) + (post_weight != nullptr) + (post_bias != nullptr) + (weight != nullptr);
         const int mode = (dout != nullptr ? kOut : 0) + (y != nullptr ? kY : 0) + (post ? kPost : 0) +
                          (gate == nullptr ? 0 : act == kSilu ? kGated : act == kSigmoid ? kGatedSigmoid : kAnyMode);
-        const bool whole = staged && pl.vecs == kVecs && pl.threads <= kSmall && D % (kStride * kVecs) == 0 &&
-                           rows % ((int64_t)pl.rows * in.passes) == 0;
+        const bool even = pl.vecs == kVecs && pl.threads <= kSmall && D % (kStride * kVecs) == 0;
+        if (even && arrays < params_of(mode)) arrays = params_of(mode);
+        const int bytes = lay_out(in, pl, rows, n, nb, arrays * D * 4, params_at);
+        const bool staged = in.stages > 0;
+        const bool whole = staged && even && rows % ((int64_t)pl.rows * in.passes) == 0;
 #define GLA_MODE(T, TS, V, S, N, M)                                                                                        \
         {                                                                                                                  \
             constexpr auto kKernel = bwd_kernel<T, TS, V, S, N, M>;                                                        \
@@ -761,15 +865,20 @@ int bwd(const void *dr, const void *dout, const void *r, const void *y, const vo
                                                                  (T *)dgate, (float *)ws, rows, D, pl.lanes, params_at);   \
         }
 #define GLA_RUN(T, TS, V, S, N) GLA_MODE(T, TS, V, S, N, kAnyMode)
+#define GLA_WHOLE_MODE(T, TS, M)                                                                                           \
+        if (mode == (M)) {                                                                                                 \
+            found = true;                                                                                                  \
+            if (params_at >= 0) GLA_MODE(T, TS, kVecs, true, kSmall, (M) + kParams)                                        \
+            else GLA_MODE(T, TS, kVecs, true, kSmall, M)                                                                   \
+        }
 #define GLA_WHOLE(T, TS)                                                                                                   \
-        if (mode == kOut + kY + kPost + kGated) GLA_MODE(T, TS, kVecs, true, kSmall, kOut + kY + kPost + kGated)           \
-        else if (mode == kOut + kY + kPost + kGatedSigmoid) GLA_MODE(T, TS, kVecs, true, kSmall, kOut + kY + kPost + kGatedSigmoid) \
-        else if (mode == kOut + kY + kPost) GLA_MODE(T, TS, kVecs, true, kSmall, kOut + kY + kPost)                        \
-        else if (mode == kOut + kY + kGated) GLA_MODE(T, TS, kVecs, true, kSmall, kOut + kY + kGated)                      \
-        else if (mode == kOut + kY + kGatedSigmoid) GLA_MODE(T, TS, kVecs, true, kSmall, kOut + kY + kGatedSigmoid)        \
-        else if (mode == kOut + kY) GLA_MODE(T, TS, kVecs, true, kSmall, kOut + kY)                                        \
-        else found = false;
-        bool found = whole;
+        GLA_WHOLE_MODE(T, TS, kOut + kY + kPost + kGated)                                                                  \
+        GLA_WHOLE_MODE(T, TS, kOut + kY + kPost + kGatedSigmoid)                                                           \
+        GLA_WHOLE_MODE(T, TS, kOut + kY + kPost)                                                                           \
+        GLA_WHOLE_MODE(T, TS, kOut + kY + kGated)                                                                          \
+        GLA_WHOLE_MODE(T, TS, kOut + kY + kGatedSigmoid)                                                                   \
+        GLA_WHOLE_MODE(T, TS, kOut + kY)
+        bool found = false;
         if (whole) {
             if (dtype == GLA_F32) { GLA_WHOLE(float, float) }
             else if (stream_dtype == GLA_F32) { GLA_WHOLE(__nv_bfloat16, float) }
@@ -777,13 +886,14 @@ int bwd(const void *dr, const void *dout, const void *r, const void *y, const vo
         }
         if (!found) { GLA_BY_TYPE(GLA_RUN) }
 #undef GLA_WHOLE
+#undef GLA_WHOLE_MODE
 #undef GLA_MODE
 #undef GLA_RUN
         count_launches(1);
     }
     if (dscale || dpost_weight || dpost_bias || dweight || dbias) {
-        const Sums sums{{dscale, dpost_weight, dpost_bias, dweight, dbias}};
-        sum_kernel<<<dim3((unsigned)((D + 31) / 32), kSums), 256, 0, st>>>((const float *)ws, nb, D, sums);
+        const Sums sums{dscale, dpost_weight, dpost_bias, dweight, dbias};
+        sum_kernel<<<dim3((unsigned)((D + 31) / 32), kSums / 2), 256, 0, st>>>((const float *)ws, nb, D, post != 0, w, sums);
         count_launches(1);
     }
     return ok && cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
