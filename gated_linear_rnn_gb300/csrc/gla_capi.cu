@@ -110,6 +110,9 @@ int bwd(const void *, const void *, const float *, const float *, const float *,
 }  // namespace convbwd
 int take_status_conv_bwd(cudaStream_t);
 int take_status_resnorm(cudaStream_t);
+int take_status_resnorm_bwd_bf16(cudaStream_t);
+int take_status_resnorm_bwd_mixed(cudaStream_t);
+int take_status_resnorm_bwd_f32(cudaStream_t);
 int take_status_scan(cudaStream_t);
 int take_status_scan_fwd(cudaStream_t);
 int take_status_scan_bwd(cudaStream_t);
@@ -758,7 +761,8 @@ int gla_last_device_status(void *stream) {
     const int parts[] = {take_status_simt(st), take_status_decode(st), take_status_tc(st), take_status_bwd(st),
                           take_status_conv(st), take_status_delta(st), take_status_delta_mma(st),
                           take_status_delta_bwd(st), take_status_scan(st), take_status_scan_fwd(st),
-                          take_status_scan_bwd(st), take_status_conv_bwd(st), take_status_resnorm(st)};
+                          take_status_scan_bwd(st), take_status_conv_bwd(st), take_status_resnorm(st),
+                          take_status_resnorm_bwd_bf16(st), take_status_resnorm_bwd_mixed(st), take_status_resnorm_bwd_f32(st)};
     for (int p : parts) {
         if (p == GLA_ERR_LAUNCH) return GLA_ERR_LAUNCH;
         if (result == GLA_OK && p != 0) result = p;

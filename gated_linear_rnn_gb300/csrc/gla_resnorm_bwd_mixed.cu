@@ -1,0 +1,19 @@
+// gla_resnorm_bwd_mixed.cu — the residual norm's gradient in bf16 on an f32 stream, a translation unit of its own for the compiler's sake.
+#include "gla_common.cuh"
+
+GLA_DEFINE_STATUS(resnorm_bwd_mixed)
+
+#include "gla_resnorm_bwd.cuh"
+
+namespace gla {
+namespace resnorm {
+
+int bwd_mixed(const void *dr, const void *dout, const void *r, const void *y, const void *gate, const float *scale,
+              const float *post_weight, const float *post_bias, const float *weight, int kind, int post, int act, float eps,
+              void *dx, void *dy, void *dgate, float *part, int64_t rows, int D, cudaStream_t st) {
+    return launch_bwd<__nv_bfloat16, float>(dr, dout, r, y, gate, {scale, post_weight, post_bias, weight, nullptr}, kind, post, act, eps,
+                                 dx, dy, dgate, part, rows, D, st);
+}
+
+}  // namespace resnorm
+}  // namespace gla
