@@ -23,22 +23,53 @@ namespace {
 constexpr int kThreads = 128;  // two channels each
 constexpr int kWalked = 16;    // tokens of a sequence, see walks()
 
-// What has to be there before the others start: the rows of a packed batch's sequences, and the words of the chains unset.
+// What has to be there before the others start: the rows and the chunks of a packed batch's sequences of more than `walked`
+// tokens, and the words of the chains unset.  32 sequences, a warp's, have their first chunks listed, then their second ones.
 __global__ void __launch_bounds__(kPlanThreads)
-prepare_kernel(const int32_t *__restrict__ cu, int nseq, int T, int2 *rows, uint4 *unset, int64_t n) {
+prepare_kernel(const int32_t *__restrict__ cu, int nseq, int T, int walked, int2 *rows, int2 *tasks, int *ntasks, uint4 *unset, int64_t n) {
     for (int64_t i = (int64_t)blockIdx.x * kPlanThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kPlanThreads)
         unset[i] = make_uint4(kUnset, kUnset, kUnset, kUnset);
-    if (blockIdx.x == 0 && cu != nullptr && plan_rows(cu, nseq, T, rows)) record_status(GLA_ERR_DEVICE_ARG);
+    if (blockIdx.x != 0) return;
+    if (plan_rows(cu, nseq, T, rows)) record_status(GLA_ERR_DEVICE_ARG);
+    __shared__ int of_warp[kPlanThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int done = 0;  // tasks listed before
+    for (int first = 0; first < nseq; first += kPlanThreads) {
+        const int s = first + (int)threadIdx.x, len = s < nseq ? rows[s].y : 0;  // the thread's own from plan_rows
+        const int chunks = len > walked ? (len + kChunk - 1) / kChunk : 0;
+        const int mine = __reduce_add_sync(0xffffffffu, chunks);
+        if (lane == 0) of_warp[warp] = mine;
+        __syncthreads();
+        int at = done;
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            if (w < warp) at += of_warp[w];
+            done += of_warp[w];
+        }
+        for (int c = 0;; ++c) {
+            const unsigned have = __ballot_sync(0xffffffffu, chunks > c);
+            if (have == 0) break;
+            if ((have & (have - 1)) == 0) {  // the rest is one sequence's
+                const int who = __ffs(have) - 1, all = __shfl_sync(0xffffffffu, chunks, who), which = first + warp * 32 + who;
+                for (int i = c + lane; i < all; i += 32) tasks[at + i - c] = make_int2(which, i);
+                break;
+            }
+            if (chunks > c) tasks[at + __popc(have & ((1u << lane) - 1u))] = make_int2(s, c);
+            at += __popc(have);
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) *ntasks = done;
 }
 
-// A thread takes two channels of a sequence from its first token to its last.
+// A thread takes two channels of a sequence of `most` tokens at most from its first token to its last.
 template <typename T, typename TG, int kForm, bool kGate>
 __global__ void __launch_bounds__(kThreads)
 walk_fwd_kernel(const T *__restrict__ x, const TG *__restrict__ g, const T *__restrict__ gate, const float *__restrict__ h0,
-                T *__restrict__ out, float *__restrict__ hT, float *__restrict__ states, Sequences q, int D, int act, int parts_of_row) {
+                T *__restrict__ out, float *__restrict__ hT, float *__restrict__ states, Sequences q, int most, int D, int act, int parts_of_row) {
     const int s = blockIdx.x / parts_of_row, d = ((blockIdx.x % parts_of_row) * kThreads + (int)threadIdx.x) * 2;
     if (d >= D) return;
     const int2 r = rows_of(q, s);
+    if (r.y > most) return;
     Pair h = h0 != nullptr ? load_state(h0 + (int64_t)s * D + d) : both(0.f);
     for (int t = 0; t < r.y; ++t) {
         const int64_t at = (int64_t)(r.x + t) * D + d;
@@ -54,10 +85,11 @@ template <typename T, typename TG, int kForm, bool kGate>
 __global__ void __launch_bounds__(kThreads)
 walk_bwd_kernel(const T *__restrict__ x, const TG *__restrict__ g, const T *__restrict__ gate, const T *__restrict__ dout,
                 const float *__restrict__ dhT, const float *__restrict__ states, T *__restrict__ dx, TG *__restrict__ dg,
-                T *__restrict__ dgate, float *__restrict__ dh0, Sequences q, int D, int act, int parts_of_row) {
+                T *__restrict__ dgate, float *__restrict__ dh0, Sequences q, int most, int D, int act, int parts_of_row) {
     const int s = blockIdx.x / parts_of_row, d = ((blockIdx.x % parts_of_row) * kThreads + (int)threadIdx.x) * 2;
     if (d >= D) return;
     const int2 r = rows_of(q, s);
+    if (r.y > most) return;
     Pair back = dhT != nullptr ? load_state(dhT + (int64_t)s * D + d) : both(0.f);
     for (int c = (r.y + kRun - 1) / kRun - 1; c >= 0; --c) {
         const int n = min(kRun, r.y - c * kRun);
@@ -128,12 +160,14 @@ step_kernel(const T *__restrict__ x, const TG *__restrict__ g, const T *__restri
 
 int status() { return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH; }
 
+int most_walked(const Shape &p) { return p.cu != nullptr ? kChunk : p.T; }
+
 void walk_fwd(const Shape &p, const void *x, const void *g, const void *gate, const float *h0, void *out, float *hT,
               float *states, int dtype, int g_dtype, const Sequences &q, cudaStream_t st) {
     const int parts = (p.D + 2 * kThreads - 1) / (2 * kThreads);
 #define GLA_RUN(T, TG, F, G)                                                                                                \
     walk_fwd_kernel<T, TG, F, G><<<(unsigned)(p.nseq * parts), kThreads, 0, st>>>(                                          \
-        (const T *)x, (const TG *)g, (const T *)gate, h0, (T *)out, hT, states, q, p.D, p.act, parts)
+        (const T *)x, (const TG *)g, (const T *)gate, h0, (T *)out, hT, states, q, most_walked(p), p.D, p.act, parts)
     GLA_SCAN_DISPATCH(dtype, g_dtype, gate != nullptr, GLA_RUN)
 #undef GLA_RUN
     count_launches(1);
@@ -146,7 +180,7 @@ void walk_bwd(const Shape &p, const void *x, const void *g, const void *gate, co
 #define GLA_RUN(T, TG, F, G)                                                                                                \
     walk_bwd_kernel<T, TG, F, G><<<(unsigned)(p.nseq * parts), kThreads, 0, st>>>(                                          \
         (const T *)x, (const TG *)g, (const T *)gate, (const T *)dout, dhT, states, (T *)dx, (TG *)dg, (T *)dgate, dh0, q,  \
-        p.D, p.act, parts)
+        most_walked(p), p.D, p.act, parts)
     GLA_SCAN_DISPATCH(dtype, g_dtype, gate != nullptr, GLA_RUN)
 #undef GLA_RUN
     count_launches(1);
@@ -155,7 +189,7 @@ void walk_bwd(const Shape &p, const void *x, const void *g, const void *gate, co
 // A call's workspace: the rows of a packed batch's sequences, a counter and a chain for each direction, and (of a gradient that
 // is not given them) the states.
 struct Layout {
-    int64_t rows, counters, chains, states, total;
+    int64_t tasks, ntasks, counters, chains, states, total;  // (the rows are first)
 };
 constexpr int64_t kCounterBytes = 256;
 bool chained(const Shape &p) { return p.cu != nullptr || p.T > kChunk; }
@@ -163,7 +197,9 @@ Layout layout(int op, const Shape &p) {
     Layout l{};
     const int64_t chain = chained(p) ? (chain_floats(p) * (int64_t)sizeof(float) + 255) / 256 * 256 : 0;
     const int dirs = op == GLA_OP_BACKWARD ? 2 : 1;
-    l.counters = rows_bytes(p.nseq, p.cu != nullptr);
+    l.tasks = rows_bytes(p.nseq, p.cu != nullptr);
+    l.ntasks = l.tasks + (p.cu != nullptr ? (slots(p) * (int64_t)sizeof(int2) + 255) / 256 * 256 : 0);
+    l.counters = l.ntasks + (p.cu != nullptr ? kCounterBytes : 0);
     l.chains = l.counters + (chain > 0 ? dirs * kCounterBytes : 0);
     l.states = l.chains + dirs * chain;
     l.total = l.states + (op == GLA_OP_BACKWARD ? states_bytes(p) : 0);
@@ -178,21 +214,35 @@ Chain chain_at(const Layout &l, const Shape &p, void *ws, int dir) {
     return c;
 }
 
+// A tile has 64 rows, used or not.  Where sequences have kWalked tokens and fewer on average, a thread walks those of up to a
+// tile's rows; of a packed batch the tiles then take the others, if there are any (a decode step with a prompt in it).
+bool walks(const Shape &p) { return total_rows(p) <= (int64_t)kWalked * p.nseq; }
+
 // dirs: how many of the chains are used
 Sequences prepare(const Shape &p, const Layout &l, void *ws, int dirs, cudaStream_t st) {
     if (!chained(p)) return {p.nseq, p.T, nullptr};
     uint8_t *b = (uint8_t *)ws;
     const int64_t bytes = l.chains - l.counters + dirs * ((chain_floats(p) * (int64_t)sizeof(float) + 255) / 256 * 256);
+    if (p.cu == nullptr) {
+        cudaMemsetAsync(b + l.counters, 0xff, (size_t)bytes, st);
+        return {p.nseq, p.T, nullptr};
+    }
     const int64_t n = bytes / 16, need = (n + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
     const int64_t most = 2 * (int64_t)device_info().sm_count;
-    prepare_kernel<<<(unsigned)(need < most ? need : most), kPlanThreads, 0, st>>>(p.cu, p.nseq, p.T, (int2 *)ws,
-                                                                                 (uint4 *)(b + l.counters), n);
+    prepare_kernel<<<(unsigned)(need < most ? need : most), kPlanThreads, 0, st>>>(
+        p.cu, p.nseq, p.T, walks(p) ? kChunk : 0, (int2 *)ws, (int2 *)(b + l.tasks), (int *)(b + l.ntasks), (uint4 *)(b + l.counters), n);
     count_launches(1);
-    return {p.nseq, p.T, p.cu ? (const int2 *)ws : nullptr};
+    return {p.nseq, p.T, (const int2 *)ws};
 }
 
-// Sequences this short on average are walked by a thread for two channels each.
-bool walks(const Shape &p) { return total_rows(p) <= (int64_t)kWalked * p.nseq; }
+Tiles tiles_of(const Shape &p, const Sequences &q, const Layout &l, void *ws) {
+    Tiles t = make_tiles(p, q);
+    if (p.cu == nullptr) return t;
+    t.walked = walks(p);
+    t.tasks = (const int2 *)((uint8_t *)ws + l.tasks);
+    t.ntasks = (const int *)((uint8_t *)ws + l.ntasks);
+    return t;
+}
 
 }  // namespace
 
@@ -202,8 +252,11 @@ int fwd(const Shape &p, const void *x, const void *g, const void *gate, const fl
         int dtype, int g_dtype, void *ws, cudaStream_t st) {
     const Layout l = layout(GLA_OP_FORWARD, p);
     const Sequences q = prepare(p, l, ws, 1, st);
-    if (walks(p)) walk_fwd(p, x, g, gate, h0, out, hT, states, dtype, g_dtype, q, st);
-    else if (!tiles_fwd(p, make_tiles(p, q), chain_at(l, p, ws, 0), x, g, gate, h0, out, hT, states, dtype, g_dtype, st))
+    if (walks(p)) {
+        walk_fwd(p, x, g, gate, h0, out, hT, states, dtype, g_dtype, q, st);
+        if (p.cu == nullptr || p.T <= kChunk) return status();
+    }
+    if (!tiles_fwd(p, tiles_of(p, q, l, ws), chain_at(l, p, ws, 0), x, g, gate, h0, out, hT, states, dtype, g_dtype, st))
         return GLA_ERR_LAUNCH;
     return status();
 }
@@ -213,11 +266,11 @@ int bwd(const Shape &p, const void *x, const void *g, const void *gate, const vo
     const Layout l = layout(GLA_OP_BACKWARD, p);
     const Sequences q = prepare(p, l, ws, states == nullptr ? 2 : 1, st);
     float *own = reinterpret_cast<float *>((uint8_t *)ws + l.states);
-    const Tiles t = make_tiles(p, q);
+    const Tiles t = tiles_of(p, q, l, ws);
     if (walks(p)) {
         if (states == nullptr) walk_fwd(p, x, g, nullptr, h0, nullptr, nullptr, own, dtype, g_dtype, q, st);
         walk_bwd(p, x, g, gate, dout, dhT, states != nullptr ? states : own, dx, dg, dgate, dh0, dtype, g_dtype, q, st);
-        return status();
+        if (p.cu == nullptr || p.T <= kChunk) return status();
     }
     if (states == nullptr &&
         !tiles_fwd(p, t, chain_at(l, p, ws, 1), x, g, nullptr, h0, nullptr, nullptr, own, dtype, g_dtype, st))

@@ -28,6 +28,7 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
                  T *__restrict__ dgate, float *__restrict__ dh0, Tiles t, Chain chain, int act, int stages) {
     using namespace ptx;
     using R = Ring<T, TG, kGate>;
+    if (tiles_of(t) == 0 && t.walked) return;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ float4 both_effects[2][kWarps][32];  // of this tile and the one before
     __shared__ float2 enters[32];
@@ -58,7 +59,7 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
         for (int st = 0; st < stages; ++st) order(st);
     }
     // sequences without tokens pass the gradient of their state on
-    if (dh0 != nullptr)
+    if (dh0 != nullptr && !t.walked)
         for (int s = blockIdx.x; s < t.q.nseq; s += gridDim.x)
             if (rows_of(t.q, s).y == 0)
                 for (int d = threadIdx.x; d < D; d += kTileThreads)

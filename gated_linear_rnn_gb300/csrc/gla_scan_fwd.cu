@@ -23,6 +23,7 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
                  float *__restrict__ hT, float *__restrict__ states, Tiles t, Chain chain, int act, int stages) {
     using namespace ptx;
     using R = Ring<T, TG, kGate>;
+    if (tiles_of(t) == 0 && t.walked) return;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ float4 both_effects[2][kWarps][32];  // of this tile and the one before
     __shared__ float2 enters[32];
@@ -61,7 +62,7 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
         }
     }
     // sequences without tokens pass their state on
-    if (hT != nullptr)
+    if (hT != nullptr && !t.walked)
         for (int s = blockIdx.x; s < t.q.nseq; s += gridDim.x)
             if (rows_of(t.q, s).y == 0)
                 for (int d = threadIdx.x; d < D; d += kTileThreads)

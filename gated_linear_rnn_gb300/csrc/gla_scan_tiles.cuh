@@ -44,9 +44,15 @@ struct Tiles {
     unsigned total;
     int chained;                    // whether any sequence may have more than one chunk
     int window;                     // tiles that a look back reads at once
+    bool walked;                    // short sequences are walked by other kernels
+    const int2 *tasks;              // of a packed batch: sequence and chunk, in the forward's order
+    const int *ntasks;
 };
+__device__ __forceinline__ unsigned tiles_of(const Tiles &t) {
+    return t.tasks == nullptr ? t.total : (unsigned)__ldg(t.ntasks) * (unsigned)t.slabs;
+}
 __host__ inline Tiles make_tiles(const Shape &p, const Sequences &q) {
-    Tiles t{q, p.D, (p.D + kSlab - 1) / kSlab, (int)slots(p), (p.T + kChunk - 1) / kChunk, 0, 1, 1};
+    Tiles t{q, p.D, (p.D + kSlab - 1) / kSlab, (int)slots(p), (p.T + kChunk - 1) / kChunk, 0, 1, 1, false, nullptr, nullptr};
     t.total = p.cu ? (unsigned)t.nslots * (unsigned)t.slabs : (unsigned)t.per_seq * (unsigned)p.nseq * (unsigned)t.slabs;
     t.chained = p.cu != nullptr || p.T > kChunk;
     return t;
@@ -57,10 +63,10 @@ struct Tile {
     __device__ int start() const { return row - chunk * kChunk; }  // its sequence's first row
 };
 
-// Tile k in the order of a direction; false for slots that no chunk has.  A dense batch goes through all sequences' first
-// chunks, then their second ones and so on: what a tile waits for is then mostly done.
+// Tile k in the order of a direction, of n.  A dense batch goes through all sequences' first chunks, then their second ones and
+// so on: what a tile waits for is then mostly done.  A packed one does so with 32 sequences after the other.
 template <bool kForth>
-__device__ __forceinline__ bool tile_at(const Tiles &t, unsigned k, Tile &o) {
+__device__ __forceinline__ void tile_at(const Tiles &t, unsigned k, unsigned n, Tile &o) {
     o.col = (int)(k % (unsigned)t.slabs) * kSlab;
     unsigned r = k / (unsigned)t.slabs;
     int2 rows;
@@ -71,41 +77,40 @@ __device__ __forceinline__ bool tile_at(const Tiles &t, unsigned k, Tile &o) {
         rows = rows_of(t.q, o.seq);
         o.slot = rows.x / kChunk + o.seq + o.chunk;
     } else {
-        o.slot = kForth ? (int)r : t.nslots - 1 - (int)r;
-        o.seq = sequence_of_slot(t.q, o.slot, kChunk);
+        const int2 task = __ldg(t.tasks + (kForth ? r : n / (unsigned)t.slabs - 1 - r));
+        o.seq = task.x;
+        o.chunk = task.y;
         rows = rows_of(t.q, o.seq);
-        o.chunk = o.slot - (rows.x / kChunk + o.seq);
-        if (o.chunk < 0 || (int64_t)o.chunk * kChunk >= rows.y) return false;
+        o.slot = rows.x / kChunk + o.seq + o.chunk;
     }
     o.row = rows.x + o.chunk * kChunk;
     o.len = min(kChunk, rows.y - o.chunk * kChunk);
     o.behind = (rows.y - 1) / kChunk - o.chunk;
-    return true;
 }
 
 // A block's tiles, by one thread.  The number of the tile after the next one is asked for ahead: the counter takes as long to
 // answer as memory does.
 template <bool kForth>
 struct Turns {
-    unsigned ahead;
+    unsigned ahead, total;
     __device__ __forceinline__ void take(const Tiles &t, const Chain &c) {
         if (t.chained) ahead = atomicAdd(c.next, 1u) + 1u;  // the counter starts at kUnset
         else ahead += gridDim.x;
     }
     __device__ __forceinline__ void start(const Tiles &t, const Chain &c) {
         ahead = blockIdx.x;
+        total = tiles_of(t);
         if (t.chained) take(t, c);
     }
     // the next tile; row < 0 when there are no more
     __device__ __forceinline__ Tile next(const Tiles &t, const Chain &c) {
         Tile o;
-        for (;;) {
-            const unsigned k = ahead;
-            o.row = -1;
-            if (k >= t.total) return o;
-            take(t, c);
-            if (tile_at<kForth>(t, k, o)) return o;
-        }
+        const unsigned k = ahead;
+        o.row = -1;
+        if (k >= total) return o;
+        take(t, c);
+        tile_at<kForth>(t, k, total, o);
+        return o;
     }
 };
 

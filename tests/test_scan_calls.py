@@ -52,7 +52,7 @@ def test_sizes(lib):
     assert lib.gla_scan_workspace_bytes(3, 1, 8, 64, 0) == lib.gla_scan_workspace_bytes(0, 0, 8, 64, 0) == -1
     assert lib.gla_scan_workspace_bytes(0, 1, 8, 60, 0) == lib.gla_scan_states_bytes(1, 8, 60, 0) == -2
     assert lib.gla_scan_workspace_bytes(0, 1 << 20, 1 << 12, 64, 0) == -2
-    # a state before every 128 tokens of every sequence
+    # a state before every 8 tokens of every sequence
     assert gla.gla_scan_states_bytes(3, 300, 64, False) >= 3 * 3 * 64 * 4
     assert gla.gla_scan_workspace_bytes(gla.OP_BACKWARD, 3, 300, 64, False) >= gla.gla_scan_states_bytes(3, 300, 64, False)
     with pytest.raises(gla.GLAError):

@@ -112,6 +112,15 @@ def test_packed(cu, types):
     check(make((1, max(cu[-1], 1), 72), types, form, nseq=len(cu) - 1), form, cu=cu)
 
 
+@pytest.mark.parametrize("lengths", [[1] * 90 + [700, 0, 64, 65], [0, 0, 3, 129] + [2] * 60, [1] * 40, [300] + [1] * 300, [64, 1, 0, 16] * 4])
+@pytest.mark.parametrize("states", [False, True])
+def test_a_prompt_among_single_tokens(lengths, states):
+    """Sequences of a few tokens on average, some of them long."""
+    cu = np.concatenate([[0], np.cumsum(lengths)]).tolist()
+    check(make((1, cu[-1], 136), TYPES[len(lengths) % 3], gla.SCAN_SIGMOID_LEAK, nseq=len(lengths), seed=len(lengths)), gla.SCAN_SIGMOID_LEAK,
+          cu=cu, states=states)
+
+
 def test_packed_without_rows():
     t = make((1, 0, 64), TYPES[0], gla.SCAN_LOG, nseq=3)
     check(t, gla.SCAN_LOG, cu=[0, 0, 0, 0])
