@@ -148,6 +148,7 @@ int launch_fwd(const void *x, const void *y, const void *gate, const Weights &w,
     if (n > 1 && pl.threads > 256) in.stages = bytes = 0;
 #define GLA_RUN(V, S, N)                                                                                                   \
     return launch<fwd_kernel<T, TS, V, S, N>>(nu, 1, pl.threads, bytes, st, in, w, kind, post, act, eps, (TS *)r, (T *)out, rows, D, pl.lanes);
+    if (pl.vecs < kFwdVecs && in.stages < 2) return 0;  // (so few channels always have room)
     if (pl.vecs == 1) GLA_RUN(1, true, 256)
     if (pl.vecs == 2) GLA_RUN(2, true, 256)
     if (in.stages > 0) {

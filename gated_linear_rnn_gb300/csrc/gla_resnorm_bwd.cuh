@@ -246,7 +246,7 @@ template <typename T, typename TS>
 int launch_bwd(const void *dr, const void *dout, const void *r, const void *y, const void *gate, const Weights &w, int kind,
                 int post, int act, float eps, void *dx, void *dy, void *dgate, float *part, int64_t rows, int D, cudaStream_t st) {
     const Plan pl = make_plan(D, kBwdVecs, kWidest);
-    const int n = per_sm(pl, kBwdThreads), nu = units(pl, rows, n);
+    int n = per_sm(pl, kBwdThreads);
     constexpr int e = sizeof(T), es = sizeof(TS);
     Inputs<5> in{};
     const void *const from[5] = {dr, dout, dout != nullptr ? r : nullptr, y, gate};
@@ -262,7 +262,14 @@ int launch_bwd(const void *dr, const void *dout, const void *r, const void *y, c
     const bool known = mode == kOut + kY || mode == kOut + kY + kPost || (mode & ~(kPost | kGated | kGatedSigmoid)) == kOut + kY;
     const bool even = known && pl.vecs == kBwdVecs && D % pl.slice == 0 && pl.slice % (kStride * kBwdVecs) == 0;
     int params_at;
-    const int bytes = lay_out(in, pl, rows, n, nu, params_of(even ? mode : kAnyMode) * pl.slice * 4, params_at);
+    const int params = params_of(even ? mode : kAnyMode) * pl.slice * 4;
+    int bytes = lay_out(in, pl, rows, n, units(pl, rows, n), params, params_at);
+    while (in.stages < 2 && n > 1) {  // fewer blocks of an SM, with room for their stages (f32 rows of 512 channels or so)
+        --n;
+        bytes = lay_out(in, pl, rows, n, units(pl, rows, n), params, params_at);
+    }
+    if (in.stages < 2) return 0;
+    const int nu = units(pl, rows, n);
     const bool whole = even && rows % ((int64_t)pl.rows * in.passes) == 0 && (pl.ranks == 1 || params_at >= 0);
 #define GLA_RUN(V, W, M)                                                                                                   \
     return launch<bwd_kernel<T, TS, V, W, M>>(nu, pl.ranks, pl.threads, bytes, st, in, w, kind, post, act, eps, \
@@ -279,7 +286,10 @@ int launch_bwd(const void *dr, const void *dout, const void *r, const void *y, c
     GLA_WHOLE(kOut + kY + kGated)
     GLA_WHOLE(kOut + kY + kGatedSigmoid)
     GLA_WHOLE(kOut + kY)
-    if (pl.vecs == 1) GLA_RUN(1, false, kAnyMode + kParams)  // parameters of so few channels always have room
+    if (pl.vecs == 1) {
+        if (params_at < 0) return 0;  // (parameters of so few channels always have room)
+        GLA_RUN(1, false, kAnyMode + kParams)
+    }
     if (pl.ranks > 1) {
         if (params_at >= 0) GLA_RUN(kBwdVecs, true, kAnyMode + kParams)
         GLA_RUN(kBwdVecs, true, kAnyMode)

@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from gated_linear_rnn_gb300 import build as B
 from gated_linear_rnn_gb300 import gla
@@ -57,3 +58,50 @@ def test_conv_gradient_refuses(lib):
     assert bwd(dy=ODD) == bwd(x=ODD) == bwd(w=ODD) == bwd(state=ODD) == bwd(cu=ODD) == bwd(ws=ODD) == -3
     assert lib.gla_conv1d_silu_bwd_workspace_bytes(0, 8, 64, 0) == -1
     assert lib.gla_conv1d_silu_bwd_workspace_bytes(1, 8, 60, 0) == -2
+
+
+def recurrent_calls():
+    """Small calls of the recurrence, the residual norm and the convolution's gradient on the device."""
+    x, w = torch.zeros(1, 8, 32, device="cuda").bfloat16(), torch.ones(32, device="cuda")
+    one, state, taps = x[0], torch.zeros(8, 32, device="cuda"), torch.ones(32, 4, device="cuda")
+    return {
+        "scan_fwd": lambda **kw: gla.scan_fwd(x, x, gla.SCAN_LOG, **kw)[0],
+        "scan_bwd": lambda **kw: gla.scan_bwd(x, x, gla.SCAN_LOG, x, **kw)[0],
+        "scan_step": lambda **kw: gla.scan_step(one, one, gla.SCAN_LOG, state, **kw),
+        "residual_norm": lambda **kw: gla.residual_norm(x, x, w, w, **kw)[1],
+        "residual_norm_bwd": lambda **kw: gla.residual_norm_bwd(x, x, x, x, w, w, **kw).dx,
+        "conv1d_silu_bwd": lambda **kw: gla.conv1d_silu_bwd(x, x, taps, **kw)[0],
+    }
+
+
+NAMES = ["scan_fwd", "scan_bwd", "scan_step", "residual_norm", "residual_norm_bwd", "conv1d_silu_bwd"]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", NAMES)
+def test_tensors_of_another_device_than_the_current_one_are_refused(lib, name, monkeypatch):
+    call = recurrent_calls()[name]
+    call()
+    torch.cuda.synchronize()
+    before = gla.gla_kernel_launches()
+    with monkeypatch.context() as m:
+        m.setattr(gla, "_current_device", lambda: 1)
+        with pytest.raises(ValueError, match="current"):
+            call()
+    assert gla.gla_kernel_launches() == before
+    assert gla.gla_last_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", NAMES)
+def test_the_null_stream(lib, name):
+    """A raw handle of 0 is the default stream, for the call and for what it allocates."""
+    call = recurrent_calls()[name]
+    base = call()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = call(stream=0)
+    torch.cuda.default_stream().synchronize()
+    assert torch.equal(base, got)
+    assert gla.gla_last_device_status() == 0

@@ -240,3 +240,40 @@ def test_refusals_on_the_device():
         big = torch.zeros(1, 16392, device="cuda")
         gla.residual_norm(big)
     assert gla.gla_kernel_launches() == before
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("D", [512, 2560, 5120, 5128, 8192, 10240, 10248, 16384])
+@pytest.mark.parametrize("post,act", [(True, gla.ACT_SILU), (True, gla.ACT_SIGMOID), (True, None), (False, gla.ACT_SILU),
+                                      (False, gla.ACT_SIGMOID), (False, None), (True, gla.ACT_NONE)])
+def test_whole_rows_and_wide_ones(types, D, post, act):
+    """Widths that leave no thread without work, in one block and in several, and those beside them, of every kind of call."""
+    v, block = make((24, D), types, seed=D, gate=act is not None, post=post)
+    check(v, block, KINDS[D % 3 % 2], gla.ACT_SILU if act is None else act)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("D", [512, 2560])
+def test_first_channels_far_from_the_others(types, D):
+    """A row's variance is taken of values less the mean of its first channels, 8 in bf16 and 128 in f32, and loses (mean of
+    those)^2 / variance x 2^-24 of itself, here D / 8 or D / 128 x 2^-24 at worst: 2e-5 of it, 1e-5 of the norm, beside the bar."""
+    v, block = make((16, D), types, seed=1)
+    n = 8 if types[1] == torch.bfloat16 else 128
+    v["x"][:, :n] += 1000.0
+    v["y"][:, :8 if types[0] == torch.bfloat16 else 128] += 300.0
+    kw = dict(kind=gla.NORM_LAYER, **block)
+    r, _ = K.residual_norm(v["x"], v["y"], v["weight"], v["bias"], **kw)
+    r = torch.from_numpy(r).to(types[1]).cuda()
+    got = gla.residual_norm_bwd(v["dr"], v["dout"], r, v["y"], v["weight"], v["bias"], **kw)
+    want = K.residual_norm_bwd(v["dr"], v["dout"], r, v["y"], v["weight"], **kw)
+    for name, x in got._asdict().items():
+        close(x, want[name], 2 * F32 + 1e-5, name)
+
+
+@pytest.mark.parametrize("D", [72, 1160, 2560, 10240])
+def test_results_are_the_same_every_time(D):
+    v, block = make((900, D), TYPES[0])
+    run = lambda: gla.residual_norm_bwd(v["dr"], v["dout"], v["x"], v["y"], v["weight"], v["bias"], **block)  # noqa: E731
+    base = run()
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(base, run()))
