@@ -4,7 +4,7 @@
 
 Prefill runs the chunked operators over whole (packed) prompts; decode runs the one-token operators on the states that
 prefill left, in pages of a pool; the training step takes the gradients of the mixer's core back to q, k, v, the
-gates, the norm's parameters and the output gate.  Run it with  python examples/delta_mixer.py  on a GB300.
+gates, the norm's parameters and the output gate, or through the convolution to the mixer's input and all parameters.  Run it with  python examples/delta_mixer.py  on a GB300.
 """
 from __future__ import annotations
 
@@ -64,6 +64,18 @@ class Mixer:
         return y, dq, dk, dv, dg, dbeta, dgate, dweight, dbias
 
 
+    def train_step(self, x, g, beta, gate, dy):
+        """From the mixer's input on: (y, dx, dg, dbeta, dgate, and the gradients of the norm's and the conv's parameters)."""
+        z = torch.empty_like(x)
+        gla.gla_conv1d_silu(x, self.conv_weight, self.conv_bias, None, None, z)
+        leaf = z.detach().requires_grad_()
+        q, k, v = self.split(leaf)  # torch takes the gradient of the unit lengths
+        y, dq, dk, dv, dg, dbeta, dgate, dweight, dbias = self.core_step(q.detach(), k.detach(), v.detach(), g, beta, gate, dy)
+        dz, = torch.autograd.grad((q, k, v), leaf, (dq, dk, dv))
+        dx, dtaps, dtaps_bias, _ = gla.conv1d_silu_bwd(dz, x, self.conv_weight, self.conv_bias)
+        return y, dx, dg, dbeta, dgate, dweight, dbias, dtaps, dtaps_bias
+
+
 def inputs(shape, seed: int = 1, device: str = "cuda"):
     """Random x, g, beta and gate of a prompt of this shape."""
     gen = torch.Generator(device=device).manual_seed(seed)
@@ -90,6 +102,7 @@ def main(tokens: int = 200, prompt: int = 150) -> float:
     off = float((torch.cat(parts, 1).float() - whole.float()).abs().max() / whole.float().abs().max())
     q, k, v = m.split(x)
     grads = m.core_step(q, k, v, g.bfloat16(), beta.bfloat16(), gate, torch.randn_like(whole))
+    grads += m.train_step(x, g.bfloat16(), beta.bfloat16(), gate, torch.randn_like(whole))
     assert all(bool(t.isfinite().all()) for t in grads) and gla.gla_last_device_status() == 0
     print(f"prefill of {prompt} tokens and {tokens - prompt} steps against one prefill: {off:.1e} of the largest output")
     return off
