@@ -216,6 +216,8 @@ Chain chain_at(const Layout &l, const Shape &p, void *ws, int dir) {
 
 // A tile has 64 rows, used or not.  Where sequences have kWalked tokens and fewer on average, a thread walks those of up to a
 // tile's rows; of a packed batch the tiles then take the others, if there are any (a decode step with a prompt in it).
+// 16,384 x 2,560 bf16 as sequences of 16, walked: forward 102 us, gradient 293; of 17, by tiles: 160 and 266; of 4, walked: 103
+// and 312.  256 single tokens and a prompt of 2,048 in one batch: 25 us.
 bool walks(const Shape &p) { return total_rows(p) <= (int64_t)kWalked * p.nseq; }
 
 // dirs: how many of the chains are used

@@ -10,6 +10,13 @@
 //
 // Tiles are handed out by a counter in an order in which a tile comes after all that it waits for, so that a waiting block
 // waits only for blocks that run.  Rows come in by TMA, some tiles ahead.
+//
+// Each input is read once and each output written once.  Measured (bf16, sigmoid with a leak, gate): 8 x 2,048 x 2,560 forward
+// 80 us, gradient 127 (the bytes at the rate of a copy: 50 and 87); 256 x 64, without chains, 68 and 112.  What bounds it there
+// is the instructions of the decays and gates beside the wait for a tile's meeting; in few long sequences the look back, 0.3 us
+// from a tile to the next: 1 x 32,768 x 2,048 f32 log decays 151 and 215 (79 and 139).  Tiles of 64 x 64 in three blocks (two,
+// gradient) of an SM were measured against 128 x 32 (long 143 and 218, short sequences twice the time), clusters that hand the
+// state on in shared memory (8 x 2,048: 137) and a warp that only follows the chain (gradient 116, of long sequences 236).
 #pragma once
 
 #include <cuda.h>
