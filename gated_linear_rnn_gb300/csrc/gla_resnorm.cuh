@@ -96,8 +96,9 @@ template <int kVec, bool kAll> struct Vectors {
     template <typename T> __device__ __forceinline__ void fetch(V &v, const T *p) const {
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
-            if (!kAll) v[j][0] = v[j][1] = both(0.f);
-            if (has(j)) Four<T>::open(v[j], *reinterpret_cast<const typename Four<T>::Raw *>(p + j * kStride));
+            typename Four<T>::Raw raw{};
+            if (has(j)) raw = *reinterpret_cast<const typename Four<T>::Raw *>(p + j * kStride);
+            Four<T>::open(v[j], raw);
         }
     }
     template <typename T> __device__ __forceinline__ void store(T *p, const V &v) const {
@@ -480,18 +481,22 @@ int lay_out(Inputs<kArrays> &in, const Plan &pl, int64_t rows, int per_sm, int n
         if (in.from[i] != nullptr) row += in.row_bytes[i];
     in.passes = 1;
     while (!wide && in.passes < 8 && 2 * in.passes * pl.rows * row <= 16 * 1024 && rows >= 4LL * in.passes * pl.rows * nblocks) in.passes *= 2;
+    const int room = kMostShared / per_sm - (per_sm == 1 ? 0 : wide ? 6144 : 3328);
     auto place = [&](int bytes) {
         const int here = at;
         at += (bytes + 127) / 128 * 128;
         return here;
     };
-    for (int i = 0; i < kArrays; ++i) {
-        if (in.from[i] == nullptr) continue;
-        in.at[i] = place(wide ? in.slice_bytes[i] : in.passes * pl.rows * in.row_bytes[i]);
-        if (wide) in.head_at[i] = place(in.head_bytes[i]);
+    for (;; in.passes /= 2) {  // fewer, where that leaves the parameters their room
+        at = 0;
+        for (int i = 0; i < kArrays; ++i) {
+            if (in.from[i] == nullptr) continue;
+            in.at[i] = place(wide ? in.slice_bytes[i] : in.passes * pl.rows * in.row_bytes[i]);
+            if (wide) in.head_at[i] = place(in.head_bytes[i]);
+        }
+        if (in.passes == 1 || 2 * at + params <= room) break;
     }
     in.stage_bytes = at;
-    const int room = kMostShared / per_sm - (per_sm == 1 ? 0 : wide ? 6144 : 3328);
     const bool shared = params > 0 && 2 * at + params <= room;
     in.stages = shared ? (room - params) / at : (room - (per_sm > 1 ? 28 * 1024 / per_sm : 0)) / at;
     if (in.stages < 2 && 2 * at <= room) in.stages = 2;

@@ -10,10 +10,11 @@ namespace {
 constexpr int kBwdVecs = 2, kBwdMost = 640;
 constexpr int kBwdThreads = 640;  // of an SM, at 96 registers each
 
-// kMode: which parts there are, for the kernels built for one kind of call whose rows leave no thread without work; kAnyMode: all
-// of that is asked for at run time.  (Of 16,384 x 2,560 with all parts the latter takes a quarter more time.)
-// kParams: the parameters are in shared memory, all that the parts could ask for (ones and zeros for those that there are not).
-enum Mode { kOut = 1, kY = 2, kPost = 4, kGated = 8, kGatedSigmoid = 16, kAnyMode = 32, kParams = 64 };
+// kMode: which parts there are, for the kernels built for one kind of call; kAnyMode: all of that is asked for at run time.
+// (16,435 x 2,552 bf16: 212 us with all parts and 104 of a plain sum, asked at run time 318 and 211.)  kRagged: some threads have
+// vectors without channels.  (Whole rows of 2,560: 177 and 95.)  kParams: the parameters are in shared memory, all that the parts
+// could ask for (ones and zeros for those that there are not).
+enum Mode { kOut = 1, kY = 2, kPost = 4, kGated = 8, kGatedSigmoid = 16, kAnyMode = 32, kParams = 64, kRagged = 128 };
 enum Param { kWeight, kScale, kPostWeight, kPostBias };
 constexpr __host__ __device__ int params_of(int mode) { return mode & (kPost | kAnyMode) ? 4 : mode & kY ? 2 : 1; }
 template <typename T, typename TS, int kVec, bool kWide, int kMode>
@@ -62,8 +63,9 @@ bwd_kernel(const Inputs<5> in, Weights weights, int kind, int post_, int act, fl
         // one vector of an array, or of parameters
         auto vec = [&](Pair (&v)[2], const auto *p, int j) {
             using E = std::remove_cv_t<std::remove_reference_t<decltype(*p)>>;
-            if (!all.value) v[0] = v[1] = both(0.f);
-            if (vs.has(j)) Four<E>::open(v, *reinterpret_cast<const typename Four<E>::Raw *>(p + j * kStride));
+            typename Four<E>::Raw raw{};
+            if (vs.has(j)) raw = *reinterpret_cast<const typename Four<E>::Raw *>(p + j * kStride);
+            Four<E>::open(v, raw);
         };
         // vector j of a parameter; v as it is where there is none
         auto param = [&](Pair (&v)[2], Param which, int j) {
@@ -215,7 +217,7 @@ bwd_kernel(const Inputs<5> in, Weights weights, int kind, int post_, int act, fl
             }
         }
     };
-    for (; it.begin(meets); it.next()) row(std::integral_constant<bool, !kAny>{});
+    for (; it.begin(meets); it.next()) row(std::integral_constant<bool, (kMode & (kAnyMode | kRagged)) == 0>{});
     it.end();
     // the block's rows of one channel set meet in shared memory; one writer per channel
     float *to = part + (int64_t)(kWide ? blockIdx.x / cl.ranks : blockIdx.x) * kSums * D;
@@ -260,9 +262,9 @@ int launch_bwd(const void *dr, const void *dout, const void *r, const void *y, c
     const int mode = (dout != nullptr ? kOut : 0) + (y != nullptr ? kY : 0) + (post ? kPost : 0) +
                      (gate == nullptr ? 0 : act == kSilu ? kGated : act == kSigmoid ? kGatedSigmoid : kAnyMode);
     const bool known = mode == kOut + kY || mode == kOut + kY + kPost || (mode & ~(kPost | kGated | kGatedSigmoid)) == kOut + kY;
-    const bool even = known && pl.vecs == kBwdVecs && D % pl.slice == 0 && pl.slice % (kStride * kBwdVecs) == 0;
+    const bool even = D % pl.slice == 0 && pl.slice % (kStride * kBwdVecs) == 0;
     int params_at;
-    const int params = params_of(even ? mode : kAnyMode) * pl.slice * 4;
+    const int params = params_of(known && pl.vecs == kBwdVecs ? mode : kAnyMode) * pl.slice * 4;
     int bytes = lay_out(in, pl, rows, n, units(pl, rows, n), params, params_at);
     while (in.stages < 2 && n > 1) {  // fewer blocks of an SM, with room for their stages (f32 rows of 512 channels or so)
         --n;
@@ -270,15 +272,20 @@ int launch_bwd(const void *dr, const void *dout, const void *r, const void *y, c
     }
     if (in.stages < 2) return 0;
     const int nu = units(pl, rows, n);
-    const bool whole = even && rows % ((int64_t)pl.rows * in.passes) == 0 && (pl.ranks == 1 || params_at >= 0);
+    // kernels of a call's own parts: all but those of a row in several blocks that have no room for its parameters
+    const bool whole = even && rows % ((int64_t)pl.rows * in.passes) == 0;
+    const bool own = pl.vecs == kBwdVecs && (params_at >= 0 || pl.ranks == 1);
 #define GLA_RUN(V, W, M)                                                                                                   \
     return launch<bwd_kernel<T, TS, V, W, M>>(nu, pl.ranks, pl.threads, bytes, st, in, w, kind, post, act, eps, \
                                               (TS *)dx, (T *)dy, (T *)dgate, part, rows, D, pl.slice, pl.lanes, params_at);
 #define GLA_WHOLE(M)                                                                                                       \
-    if (whole && mode == (M)) {                                                                                            \
-        if (pl.ranks > 1) GLA_RUN(kBwdVecs, true, (M) + kParams)                                                           \
-        if (params_at >= 0) GLA_RUN(kBwdVecs, false, (M) + kParams)                                                        \
-        GLA_RUN(kBwdVecs, false, M)                                                                                        \
+    if (own && mode == (M)) {                                                                                              \
+        if (pl.ranks > 1 && whole) GLA_RUN(kBwdVecs, true, (M) + kParams)                                                  \
+        if (pl.ranks > 1) GLA_RUN(kBwdVecs, true, (M) + kParams + kRagged)                                                 \
+        if (params_at < 0 && whole) GLA_RUN(kBwdVecs, false, M)                                                            \
+        if (params_at < 0) GLA_RUN(kBwdVecs, false, (M) + kRagged)                                                         \
+        if (whole) GLA_RUN(kBwdVecs, false, (M) + kParams)                                                                 \
+        GLA_RUN(kBwdVecs, false, (M) + kParams + kRagged)                                                                  \
     }
     GLA_WHOLE(kOut + kY + kPost + kGated)
     GLA_WHOLE(kOut + kY + kPost + kGatedSigmoid)
