@@ -128,14 +128,15 @@ walk_bwd_kernel(const T *__restrict__ x, const TG *__restrict__ g, const T *__re
     if (dh0 != nullptr) store_state(dh0 + (int64_t)s * D + d, back);
 }
 
-// One token of N sequences, four channels a thread.
+// One token of N sequences, four channels a thread, 1 << shift threads to a row; a block has a part of 256 >> shift rows.
+constexpr int kStepThreads = 256;
 template <typename T, typename TG, int kForm, bool kGate>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kStepThreads)
 step_kernel(const T *__restrict__ x, const TG *__restrict__ g, const T *__restrict__ gate, float *__restrict__ state,
-            const int32_t *__restrict__ slots, int nslots, T *__restrict__ out, int64_t total, int D, int act) {
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= total) return;
-    const int64_t n = i * 4 / D, at = i * 4;
+            const int32_t *__restrict__ slots, int nslots, T *__restrict__ out, int N, int D, int shift, unsigned parts, int act) {
+    const int64_t n = (int64_t)(blockIdx.x / parts) * (kStepThreads >> shift) + (threadIdx.x >> shift);
+    const int c = (int)((blockIdx.x % parts) << shift | (threadIdx.x & ((1u << shift) - 1u))) * 4;
+    if (n >= N || c >= D) return;
     int64_t page = n;
     if (slots != nullptr) {
         page = __ldg(slots + n);
@@ -144,18 +145,27 @@ step_kernel(const T *__restrict__ x, const TG *__restrict__ g, const T *__restri
             page = -1;
         }
     }
+    const int64_t at = n * D + c;
+    Pair v[2], d[2], z[2], y[2] = {both(0.f), both(0.f)};
+    if (page >= 0) {
+        load_four(x + at, v);
+        load_four(g + at, d);
+        if (kGate) load_four(gate + at, z);
+        float4 *const to = reinterpret_cast<float4 *>(state + page * D + c);
+        const float4 s = *to;
+        const Pair h[2] = {pair(s.x, s.y), pair(s.z, s.w)};
 #pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-        if (page < 0) {
-            store_two(out + at + e, both(0.f));
-            continue;
+        for (int e = 0; e < 2; ++e) {
+            const Decay a = decay<kForm>(d[e]);
+            y[e] = decayed(a, h[e], input<kForm>(a, v[e]));
         }
-        float *to = state + page * D + (at - n * D) + e;
-        const Decay a = decay<kForm>(load_two(g + at + e));
-        const Pair h = decayed(a, load_state(to), input<kForm>(a, load_two(x + at + e)));
-        store_state(to, h);
-        store_two(out + at + e, kGate ? h * activation(load_two(gate + at + e), act) : h);
+        const float2 p = gla::parts(y[0]), q = gla::parts(y[1]);
+        *to = make_float4(p.x, p.y, q.x, q.y);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (kGate) y[e] = y[e] * activation(z[e], act);
     }
+    store_four(out + at, y);
 }
 
 int status() { return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH; }
@@ -285,12 +295,16 @@ int bwd(const Shape &p, const void *x, const void *g, const void *gate, const vo
 
 int step(const void *x, const void *g, const void *gate, float *state, const int32_t *slots, int nslots, void *out, int N,
          int D, int form, int act, int dtype, int g_dtype, cudaStream_t st) {
-    const int64_t total = (int64_t)N * D / 4;
-    const int64_t blocks = (total + 255) / 256;
+    int shift = 0;
+    while (shift < 8 && (4 << shift) < D) ++shift;
+    const int64_t parts = (D + (4 << shift) - 1) >> (shift + 2), rows = kStepThreads >> shift;
+    const int64_t items = (N + rows - 1) / rows * parts;
+    if (items > 0x7fffffff) return GLA_ERR_UNSUPPORTED;
     const Shape p{N, 1, D, form, act, nullptr};
 #define GLA_RUN(T, TG, F, G)                                                                                                \
-    step_kernel<T, TG, F, G><<<(unsigned)blocks, 256, 0, st>>>((const T *)x, (const TG *)g, (const T *)gate, state, slots,  \
-                                                               nslots, (T *)out, total, D, act)
+    step_kernel<T, TG, F, G><<<(unsigned)items, kStepThreads, 0, st>>>((const T *)x, (const TG *)g, (const T *)gate, state, \
+                                                                       slots, nslots, (T *)out, N, D, shift,                \
+                                                                       (unsigned)parts, act)
     GLA_SCAN_DISPATCH(dtype, g_dtype, gate != nullptr, GLA_RUN)
 #undef GLA_RUN
     count_launches(1);

@@ -53,6 +53,22 @@ template <typename T> __device__ __forceinline__ Pair load_two(const T *p) {
 template <typename T> __device__ __forceinline__ void store_two(T *p, Pair x) {
     *reinterpret_cast<typename Two<T>::Raw *>(p) = Two<T>::close(x);
 }
+// four of them
+__device__ __forceinline__ void load_four(const __nv_bfloat16 *p, Pair (&x)[2]) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
+    x[0] = Two<__nv_bfloat16>::open(w.x), x[1] = Two<__nv_bfloat16>::open(w.y);
+}
+__device__ __forceinline__ void load_four(const float *p, Pair (&x)[2]) {
+    const float4 w = __ldg(reinterpret_cast<const float4 *>(p));
+    x[0] = pair(w.x, w.y), x[1] = pair(w.z, w.w);
+}
+__device__ __forceinline__ void store_four(__nv_bfloat16 *p, const Pair (&x)[2]) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(Two<__nv_bfloat16>::close(x[0]), Two<__nv_bfloat16>::close(x[1]));
+}
+__device__ __forceinline__ void store_four(float *p, const Pair (&x)[2]) {
+    const float2 a = parts(x[0]), b = parts(x[1]);
+    *reinterpret_cast<float4 *>(p) = make_float4(a.x, a.y, b.x, b.y);
+}
 __device__ __forceinline__ Pair load_state(const float *p) {
     const float2 f = *reinterpret_cast<const float2 *>(p);
     return pair(f.x, f.y);
