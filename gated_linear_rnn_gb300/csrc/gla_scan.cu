@@ -20,7 +20,7 @@ bool tiles_bwd(const Shape &, const Tiles &, const Chain &, const void *, const 
 
 namespace {
 
-constexpr int kThreads = 128;  // two channels each
+constexpr int kThreads = 128;  // four channels each
 constexpr int kWalked = 16;    // tokens of a sequence, see walks()
 
 // What has to be there before the others start: the rows and the chunks of a packed batch's sequences of more than `walked`
@@ -61,71 +61,125 @@ prepare_kernel(const int32_t *__restrict__ cu, int nseq, int T, int walked, int2
     if (threadIdx.x == 0) *ntasks = done;
 }
 
-// A thread takes two channels of a sequence of `most` tokens at most from its first token to its last.
+// A thread takes four channels of a sequence of `most` tokens at most from its first token to its last, a run's loads at once.
 template <typename T, typename TG, int kForm, bool kGate>
 __global__ void __launch_bounds__(kThreads)
 walk_fwd_kernel(const T *__restrict__ x, const TG *__restrict__ g, const T *__restrict__ gate, const float *__restrict__ h0,
-                T *__restrict__ out, float *__restrict__ hT, float *__restrict__ states, Sequences q, int most, int D, int act, int parts_of_row) {
-    const int s = blockIdx.x / parts_of_row, d = ((blockIdx.x % parts_of_row) * kThreads + (int)threadIdx.x) * 2;
-    if (d >= D) return;
-    const int2 r = rows_of(q, s);
+                T *__restrict__ out, float *__restrict__ hT, float *__restrict__ states, Sequences q, int most, int D, int act, int shift,
+                unsigned parts_of_row) {
+    const int64_t s = (int64_t)(blockIdx.x / parts_of_row) * (kThreads >> shift) + (threadIdx.x >> shift);
+    const int d = (int)((blockIdx.x % parts_of_row) << shift | (threadIdx.x & ((1u << shift) - 1u))) * 4;
+    if (s >= q.nseq || d >= D) return;
+    const int2 r = rows_of(q, (int)s);
     if (r.y > most) return;
-    Pair h = h0 != nullptr ? load_state(h0 + (int64_t)s * D + d) : both(0.f);
-    for (int t = 0; t < r.y; ++t) {
-        const int64_t at = (int64_t)(r.x + t) * D + d;
-        if (states != nullptr && t % kRun == 0) store_state(states + state_slot(r.x, s, t) * D + d, h);
-        const Decay a = decay<kForm>(load_two(g + at));
-        h = decayed(a, h, input<kForm>(a, load_two(x + at)));
-        if (out != nullptr) store_two(out + at, kGate ? h * activation(load_two(gate + at), act) : h);
-    }
-    if (hT != nullptr) store_state(hT + (int64_t)s * D + d, h);
-}
-
-template <typename T, typename TG, int kForm, bool kGate>
-__global__ void __launch_bounds__(kThreads)
-walk_bwd_kernel(const T *__restrict__ x, const TG *__restrict__ g, const T *__restrict__ gate, const T *__restrict__ dout,
-                const float *__restrict__ dhT, const float *__restrict__ states, T *__restrict__ dx, TG *__restrict__ dg,
-                T *__restrict__ dgate, float *__restrict__ dh0, Sequences q, int most, int D, int act, int parts_of_row) {
-    const int s = blockIdx.x / parts_of_row, d = ((blockIdx.x % parts_of_row) * kThreads + (int)threadIdx.x) * 2;
-    if (d >= D) return;
-    const int2 r = rows_of(q, s);
-    if (r.y > most) return;
-    Pair back = dhT != nullptr ? load_state(dhT + (int64_t)s * D + d) : both(0.f);
-    for (int c = (r.y + kRun - 1) / kRun - 1; c >= 0; --c) {
-        const int n = min(kRun, r.y - c * kRun);
-        const int64_t first = (int64_t)(r.x + c * kRun) * D + d;
-        Pair h = load_state(states + state_slot(r.x, s, c * kRun) * D + d), before[kRun], in[kRun];
-        Decay a[kRun];
+    Pair h[2] = {both(0.f), both(0.f)};
+    if (h0 != nullptr) load_four(h0 + s * D + d, h);
+    for (int t0 = 0; t0 < r.y; t0 += kRun) {
+        if (states != nullptr) store_four(states + state_slot(r.x, (int)s, t0) * D + d, h);
+        const int n = min(kRun, r.y - t0);
+        const int64_t first = (int64_t)(r.x + t0) * D + d;
+        FourRaw<T> xs[kRun], zs[kGate ? kRun : 1];
+        FourRaw<TG> gs[kRun];
 #pragma unroll
         for (int t = 0; t < kRun; ++t)
             if (t < n) {
                 const int64_t at = first + (int64_t)t * D;
-                a[t] = decay<kForm>(load_two(g + at));
-                in[t] = load_two(x + at);
-                before[t] = h;
-                h = decayed(a[t], h, input<kForm>(a[t], in[t]));
+                gs[t].load(g + at), xs[t].load(x + at);
+                if (kGate && out != nullptr) zs[t].load(gate + at);
+            }
+#pragma unroll
+        for (int t = 0; t < kRun; ++t)
+            if (t < n) {
+                Pair v[2], a[2], z[2], y[2];
+                xs[t].open(v), gs[t].open(a);
+                if (kGate && out != nullptr) zs[t].open(z);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const Decay c = decay<kForm>(a[e]);
+                    h[e] = decayed(c, h[e], input<kForm>(c, v[e]));
+                    y[e] = kGate && out != nullptr ? h[e] * activation(z[e], act) : h[e];
+                }
+                if (out != nullptr) store_four(out + first + (int64_t)t * D, y);
+            }
+    }
+    if (hT != nullptr) store_four(hT + s * D + d, h);
+}
+
+// The states of a run of rows from the one before it, then backwards through the run.
+template <typename T, typename TG, int kForm, bool kGate>
+__global__ void __launch_bounds__(kThreads)
+walk_bwd_kernel(const T *__restrict__ x, const TG *__restrict__ g, const T *__restrict__ gate, const T *__restrict__ dout,
+                const float *__restrict__ dhT, const float *__restrict__ states, T *__restrict__ dx, TG *__restrict__ dg,
+                T *__restrict__ dgate, float *__restrict__ dh0, Sequences q, int most, int D, int act, int shift, unsigned parts_of_row) {
+    const int64_t s = (int64_t)(blockIdx.x / parts_of_row) * (kThreads >> shift) + (threadIdx.x >> shift);
+    const int d = (int)((blockIdx.x % parts_of_row) << shift | (threadIdx.x & ((1u << shift) - 1u))) * 4;
+    if (s >= q.nseq || d >= D) return;
+    const int2 r = rows_of(q, (int)s);
+    if (r.y > most) return;
+    Pair back[2] = {both(0.f), both(0.f)};
+    if (dhT != nullptr) load_four(dhT + s * D + d, back);
+    for (int c = (r.y + kRun - 1) / kRun - 1; c >= 0; --c) {
+        const int n = min(kRun, r.y - c * kRun);
+        const int64_t first = (int64_t)(r.x + c * kRun) * D + d;
+        Pair h[2], before[kRun][2];
+        FourRaw<T> xs[kRun], us[kRun], zs[kGate ? kRun : 1];
+        FourRaw<TG> gs[kRun];
+        load_four(states + state_slot(r.x, (int)s, c * kRun) * D + d, h);
+#pragma unroll
+        for (int t = 0; t < kRun; ++t)
+            if (t < n) {
+                const int64_t at = first + (int64_t)t * D;
+                gs[t].load(g + at), xs[t].load(x + at);
+            }
+#pragma unroll
+        for (int t = 0; t < kRun; ++t)
+            if (t < n) {
+                const int64_t at = first + (int64_t)t * D;
+                us[t].load(dout + at);
+                if (kGate) zs[t].load(gate + at);
+            }
+#pragma unroll
+        for (int t = 0; t < kRun; ++t)
+            if (t < n) {
+                Pair v[2], a[2];
+                xs[t].open(v), gs[t].open(a);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    before[t][e] = h[e];
+                    const Decay k = decay<kForm>(a[e]);
+                    h[e] = decayed(k, h[e], input<kForm>(k, v[e]));
+                }
             }
 #pragma unroll
         for (int t = kRun - 1; t >= 0; --t)
             if (t < n) {
                 const int64_t at = first + (int64_t)t * D;
-                const Pair up = load_two(dout + at);
-                Pair dh = up;
-                if (kGate) {
-                    Pair slope;
-                    dh = up * activation(load_two(gate + at), act, slope);
-                    store_two(dgate + at, up * slope * decayed(a[t], before[t], input<kForm>(a[t], in[t])));
+                Pair v[2], a[2], up[2], z[2];
+                xs[t].open(v), gs[t].open(a), us[t].open(up);
+                if (kGate) zs[t].open(z);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const Decay k = decay<kForm>(a[e]);
+                    Pair dh = up[e];
+                    if (kGate) {
+                        Pair slope;
+                        dh = up[e] * activation(z[e], act, slope);
+                        z[e] = up[e] * slope * decayed(k, before[t][e], input<kForm>(k, v[e]));
+                    }
+                    dh = dh + back[e];
+                    Pair da = leaks(kForm) ? fma(v[e], both(-1.f), before[t][e]) : before[t][e];
+                    da = dh * (da * whole(k));
+                    if (!is_log(kForm)) da = da * rest(k);
+                    a[e] = da;
+                    v[e] = input<kForm>(k, dh);
+                    back[e] = decayed(k, dh);
                 }
-                dh = dh + back;
-                Pair da = leaks(kForm) ? fma(in[t], both(-1.f), before[t]) : before[t];
-                da = dh * (da * whole(a[t]));
-                if (!is_log(kForm)) da = da * rest(a[t]);
-                store_two(dg + at, da);
-                store_two(dx + at, input<kForm>(a[t], dh));
-                back = decayed(a[t], dh);
+                if (kGate) store_four(dgate + at, z);
+                store_four(dg + at, a);
+                store_four(dx + at, v);
             }
     }
-    if (dh0 != nullptr) store_state(dh0 + (int64_t)s * D + d, back);
+    if (dh0 != nullptr) store_four(dh0 + s * D + d, back);
 }
 
 // One token of N sequences, four channels a thread, 1 << shift threads to a row; a block has a part of 256 >> shift rows.
@@ -172,12 +226,27 @@ int status() { return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNC
 
 int most_walked(const Shape &p) { return p.cu != nullptr ? kChunk : p.T; }
 
+// How rows of D channels go to blocks of so many threads, four channels each: 1 << shift threads to a row's part.
+struct Split {
+    int shift;
+    int64_t parts, blocks;
+};
+Split split(int64_t rows, int D, int threads) {
+    Split w{};
+    while ((1 << w.shift) < threads && (4 << w.shift) < D) ++w.shift;
+    const int64_t at_once = threads >> w.shift;
+    w.parts = (D + (4 << w.shift) - 1) >> (w.shift + 2);
+    w.blocks = (rows + at_once - 1) / at_once * w.parts;
+    return w;
+}
+
 void walk_fwd(const Shape &p, const void *x, const void *g, const void *gate, const float *h0, void *out, float *hT,
               float *states, int dtype, int g_dtype, const Sequences &q, cudaStream_t st) {
-    const int parts = (p.D + 2 * kThreads - 1) / (2 * kThreads);
+    const Split w = split(p.nseq, p.D, kThreads);
 #define GLA_RUN(T, TG, F, G)                                                                                                \
-    walk_fwd_kernel<T, TG, F, G><<<(unsigned)(p.nseq * parts), kThreads, 0, st>>>(                                          \
-        (const T *)x, (const TG *)g, (const T *)gate, h0, (T *)out, hT, states, q, most_walked(p), p.D, p.act, parts)
+    walk_fwd_kernel<T, TG, F, G><<<(unsigned)w.blocks, kThreads, 0, st>>>(                                                  \
+        (const T *)x, (const TG *)g, (const T *)gate, h0, (T *)out, hT, states, q, most_walked(p), p.D, p.act, w.shift,     \
+        (unsigned)w.parts)
     GLA_SCAN_DISPATCH(dtype, g_dtype, gate != nullptr, GLA_RUN)
 #undef GLA_RUN
     count_launches(1);
@@ -186,11 +255,11 @@ void walk_fwd(const Shape &p, const void *x, const void *g, const void *gate, co
 void walk_bwd(const Shape &p, const void *x, const void *g, const void *gate, const void *dout, const float *dhT,
               const float *states, void *dx, void *dg, void *dgate, float *dh0, int dtype, int g_dtype, const Sequences &q,
               cudaStream_t st) {
-    const int parts = (p.D + 2 * kThreads - 1) / (2 * kThreads);
+    const Split w = split(p.nseq, p.D, kThreads);
 #define GLA_RUN(T, TG, F, G)                                                                                                \
-    walk_bwd_kernel<T, TG, F, G><<<(unsigned)(p.nseq * parts), kThreads, 0, st>>>(                                          \
+    walk_bwd_kernel<T, TG, F, G><<<(unsigned)w.blocks, kThreads, 0, st>>>(                                                  \
         (const T *)x, (const TG *)g, (const T *)gate, (const T *)dout, dhT, states, (T *)dx, (TG *)dg, (T *)dgate, dh0, q,  \
-        most_walked(p), p.D, p.act, parts)
+        most_walked(p), p.D, p.act, w.shift, (unsigned)w.parts)
     GLA_SCAN_DISPATCH(dtype, g_dtype, gate != nullptr, GLA_RUN)
 #undef GLA_RUN
     count_launches(1);
@@ -295,16 +364,13 @@ int bwd(const Shape &p, const void *x, const void *g, const void *gate, const vo
 
 int step(const void *x, const void *g, const void *gate, float *state, const int32_t *slots, int nslots, void *out, int N,
          int D, int form, int act, int dtype, int g_dtype, cudaStream_t st) {
-    int shift = 0;
-    while (shift < 8 && (4 << shift) < D) ++shift;
-    const int64_t parts = (D + (4 << shift) - 1) >> (shift + 2), rows = kStepThreads >> shift;
-    const int64_t items = (N + rows - 1) / rows * parts;
-    if (items > 0x7fffffff) return GLA_ERR_UNSUPPORTED;
+    const Split w = split(N, D, kStepThreads);
+    if (w.blocks > 0x7fffffff) return GLA_ERR_UNSUPPORTED;
     const Shape p{N, 1, D, form, act, nullptr};
 #define GLA_RUN(T, TG, F, G)                                                                                                \
-    step_kernel<T, TG, F, G><<<(unsigned)items, kStepThreads, 0, st>>>((const T *)x, (const TG *)g, (const T *)gate, state, \
-                                                                       slots, nslots, (T *)out, N, D, shift,                \
-                                                                       (unsigned)parts, act)
+    step_kernel<T, TG, F, G><<<(unsigned)w.blocks, kStepThreads, 0, st>>>((const T *)x, (const TG *)g, (const T *)gate, state, \
+                                                                       slots, nslots, (T *)out, N, D, w.shift,              \
+                                                                       (unsigned)w.parts, act)
     GLA_SCAN_DISPATCH(dtype, g_dtype, gate != nullptr, GLA_RUN)
 #undef GLA_RUN
     count_launches(1);

@@ -53,14 +53,22 @@ template <typename T> __device__ __forceinline__ Pair load_two(const T *p) {
 template <typename T> __device__ __forceinline__ void store_two(T *p, Pair x) {
     *reinterpret_cast<typename Two<T>::Raw *>(p) = Two<T>::close(x);
 }
-// four of them
-__device__ __forceinline__ void load_four(const __nv_bfloat16 *p, Pair (&x)[2]) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
-    x[0] = Two<__nv_bfloat16>::open(w.x), x[1] = Two<__nv_bfloat16>::open(w.y);
-}
-__device__ __forceinline__ void load_four(const float *p, Pair (&x)[2]) {
-    const float4 w = __ldg(reinterpret_cast<const float4 *>(p));
-    x[0] = pair(w.x, w.y), x[1] = pair(w.z, w.w);
+// four of them, as they lie in memory
+template <typename T> struct FourRaw;
+template <> struct FourRaw<__nv_bfloat16> {
+    uint2 w;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = __ldg(reinterpret_cast<const uint2 *>(p)); }
+    __device__ __forceinline__ void open(Pair (&x)[2]) const { x[0] = Two<__nv_bfloat16>::open(w.x), x[1] = Two<__nv_bfloat16>::open(w.y); }
+};
+template <> struct FourRaw<float> {
+    float4 w;
+    __device__ __forceinline__ void load(const float *p) { w = __ldg(reinterpret_cast<const float4 *>(p)); }
+    __device__ __forceinline__ void open(Pair (&x)[2]) const { x[0] = pair(w.x, w.y), x[1] = pair(w.z, w.w); }
+};
+template <typename T> __device__ __forceinline__ void load_four(const T *p, Pair (&x)[2]) {
+    FourRaw<T> f;
+    f.load(p);
+    f.open(x);
 }
 __device__ __forceinline__ void store_four(__nv_bfloat16 *p, const Pair (&x)[2]) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(Two<__nv_bfloat16>::close(x[0]), Two<__nv_bfloat16>::close(x[1]));
