@@ -21,7 +21,7 @@ bool tiles_bwd(const Shape &, const Tiles &, const Chain &, const void *, const 
 namespace {
 
 constexpr int kThreads = 128;  // four channels each
-constexpr int kWalked = 16;    // tokens of a sequence, see walks()
+constexpr int kWalked = 8, kWalkedOfMany = 32;  // tokens of a sequence, see walks()
 
 // What has to be there before the others start: the rows and the chunks of a packed batch's sequences of more than `walked`
 // tokens, and the words of the chains unset.  32 sequences, a warp's, have their first chunks listed, then their second ones.
@@ -289,15 +289,20 @@ Chain chain_at(const Layout &l, const Shape &p, void *ws, int dir) {
     Chain c;
     c.next = (unsigned *)(b + l.counters + dir * kCounterBytes);
     c.effect = (float *)(b + l.chains + dir * ((chain_floats(p) * (int64_t)sizeof(float) + 255) / 256 * 256));
-    c.result = c.effect + slots(p) * p.D * 2;
+    c.result = c.effect + places(p) * p.D * 2;
     return c;
 }
 
-// A tile has 64 rows, used or not.  Where sequences have kWalked tokens and fewer on average, a thread walks those of up to a
-// tile's rows; of a packed batch the tiles then take the others, if there are any (a decode step with a prompt in it).
-// 16,384 x 2,560 bf16 as sequences of 16, walked: forward 102 us, gradient 293; of 17, by tiles: 160 and 266; of 4, walked: 103
-// and 312.  256 single tokens and a prompt of 2,048 in one batch: 25 us.
-bool walks(const Shape &p) { return total_rows(p) <= (int64_t)kWalked * p.nseq; }
+// A tile has 64 rows, used or not, and its meetings; a walk takes 0.25 us a token (0.4 the gradient's) and no less.  So sequences are
+// walked that have kWalked tokens and fewer on average, or kWalkedOfMany where there are tiles for several rounds of the blocks;
+// of a packed batch those of up to a tile's rows, and the tiles then take the others, if there are any (a decode step with a
+// prompt in it).  Forward and gradient of 16,384 x 2,560 bf16 in us, walked and by tiles: sequences of 17 tokens 63, 134 and 152,
+// 260; of 32 61, 126 and 98, 164; of 64 63, 129 and 66, 110; 8 sequences of 32 8, 13 and 4, 5; f32 256 x 32 52, 162 and 92, 146.
+bool walks(const Shape &p) {
+    const int64_t rows = total_rows(p), tiles = (int64_t)p.nseq * ((p.D + kSlab - 1) / kSlab);
+    return rows <= (int64_t)kWalked * p.nseq ||
+           (rows <= (int64_t)kWalkedOfMany * p.nseq && tiles >= 16 * (int64_t)device_info().sm_count);
+}
 
 // dirs: how many of the chains are used
 Sequences prepare(const Shape &p, const Layout &l, void *ws, int dirs, cudaStream_t st) {

@@ -39,11 +39,15 @@ constexpr int kBack = 2 * kWarps;            // tiles that a look back reads at 
 
 // The chunks' effects and results, for one direction.
 struct Chain {
-    float *effect;   // [slots, D, 2]: A, H
-    float *result;   // [slots, D]
+    float *effect;   // [places, D, 2]: A, H
+    float *result;   // [places, D]
     unsigned *next;  // the counter of tiles, and behind it whether a wait gave up
 };
-__host__ inline int64_t chain_floats(const Shape &p) { return slots(p) * p.D * 3; }
+// A chunk's place among them is start / kChunk + c in the forward and one less in the gradient.  A sequence of n chunks publishes
+// for n - 1 of them, the forward for all but its last and the gradient for all but its first, so no two share a place: the next
+// sequence starts at start / kChunk + n - 1 or behind.
+__host__ inline int64_t places(const Shape &p) { return total_rows(p) / kChunk + 1; }
+__host__ inline int64_t chain_floats(const Shape &p) { return places(p) * p.D * 3; }
 
 struct Tiles {
     Sequences q;
@@ -82,14 +86,13 @@ __device__ __forceinline__ void tile_at(const Tiles &t, unsigned k, unsigned n, 
         o.chunk = (int)(r / (unsigned)t.q.nseq);
         if (!kForth) o.chunk = t.per_seq - 1 - o.chunk;
         rows = rows_of(t.q, o.seq);
-        o.slot = rows.x / kChunk + o.seq + o.chunk;
     } else {
         const int2 task = __ldg(t.tasks + (kForth ? r : n / (unsigned)t.slabs - 1 - r));
         o.seq = task.x;
         o.chunk = task.y;
         rows = rows_of(t.q, o.seq);
-        o.slot = rows.x / kChunk + o.seq + o.chunk;
     }
+    o.slot = rows.x / kChunk + o.chunk - (kForth ? 0 : 1);
     o.row = rows.x + o.chunk * kChunk;
     o.len = min(kChunk, rows.y - o.chunk * kChunk);
     o.behind = (rows.y - 1) / kChunk - o.chunk;
