@@ -35,7 +35,7 @@ constexpr int kFwdThreads = 768;  // of an SM, at 85 registers each
 // Statistics are taken in two steps, a mean and then centred squares.
 template <typename T, typename TS, int kVec, bool kStage, int kMost>
 __global__ void __launch_bounds__(kMost, kMost <= 256 ? 3 : 1)
-fwd_kernel(const Inputs<3> in, Weights weights, int kind, int post, int act, float eps, TS *__restrict__ r, T *__restrict__ out,
+fwd_kernel(const Inputs<3> in, Weights weights, int kind, int post, int act, float eps, TS *r, T *__restrict__ out,
            int64_t rows, int D, int lanes) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ Bars bars;

@@ -449,7 +449,8 @@ GLA_API int gla_conv1d_silu_step(const void *x, const float *weight, const float
  *               sequence's are not written
  *   ws, ws_bytes  at least gla_conv1d_silu_bwd_workspace_bytes(...) bytes (device): the blocks' sums of dweight and dbias,
  *               which are added up in a fixed order
- *   D % 8 == 0; all rows together below 2^31 - 256; pointers 16-byte aligned.  Arithmetic is f32.  Returns a gla_status.
+ *   D % 8 == 0; all rows together below 2^31 - 256; pointers 16-byte aligned.  Arithmetic is f32.  No array may
+ *   alias another.  Returns a gla_status.
  */
 GLA_API long long gla_conv1d_silu_bwd_workspace_bytes(int B, int T, int D, int packed);
 GLA_API int gla_conv1d_silu_bwd(const void *dy, const void *x, const float *weight, const float *bias, const float *state_in,
@@ -607,7 +608,7 @@ GLA_API long long gla_scan_states_bytes(int B, int T, int D, int packed);
  *   cu_seqlens  NULL, or a DEVICE int32 [B+1] of offsets, as gla_delta_chunk_fwd: an empty sequence gets hT = h0; bad
  *               ones are taken as empty and GLA_ERR_DEVICE_ARG recorded, the others are what they are without them
  *   ws, ws_bytes  at least gla_scan_workspace_bytes(GLA_OP_FORWARD, ...) bytes (else GLA_ERR_ARG); NULL where that is 0
- * Rows of a packed batch that are no sequence's are not written.  Returns a gla_status.
+ * Rows of a packed batch that are no sequence's are not written.  No array may alias another.  Returns a gla_status.
  */
 GLA_API int gla_scan_fwd(const void *x, const void *g, const void *gate, const float *h0, void *out, float *hT,
                          float *states, int B, int T, int D, int form, int act, int dtype, int g_dtype,
@@ -634,7 +635,7 @@ GLA_API int gla_scan_bwd(const void *x, const void *g, const void *gate, const v
  *   state       [N, D] f32; with slots: a pool [nslots, D] of pages, as gla_delta_decode_step (a negative slot is a padding
  *               row: zero out, no page touched; >= nslots: the same, and GLA_ERR_DEVICE_ARG is recorded).  Two rows must
  *               not name the same page
- *   N = 0 does nothing
+ *   N = 0 does nothing.  No array may alias another
  * Makes no allocation or synchronisation: it can be captured in a CUDA graph.  Returns a gla_status.
  */
 GLA_API int gla_scan_step(const void *x, const void *g, const void *gate, float *state, const int32_t *slots, int nslots,
@@ -653,7 +654,8 @@ GLA_API int gla_scan_step(const void *x, const void *g, const void *gate, float 
  *   scale, weight, bias, post_weight, post_bias  [D] f32; NULL for ones / zeros
  *   dtype        GLA_BF16 or GLA_F32;  stream_dtype  dtype, or GLA_F32
  *   D            a multiple of 8, 8 <= D <= 16384;  0 <= rows < 2^31 - 256;  eps > 0
- * Statistics and arithmetic are f32, out is of the sum before it is rounded to r.  Returns a gla_status.
+ * Statistics and arithmetic are f32, out is of the sum before it is rounded to r.  r may be x; no other array may alias
+ * another.  Returns a gla_status.
  */
 typedef enum { GLA_NORM_LAYER = 0, GLA_NORM_RMS = 1 } gla_norm_kind;
 GLA_API int gla_residual_norm(const void *x, const void *y, const void *gate, const float *scale, const float *post_weight,
@@ -669,7 +671,9 @@ GLA_API int gla_residual_norm(const void *x, const void *y, const void *gate, co
  *   dscale, dpost_weight, dpost_bias, dweight, dbias  [D] f32, written; any may be NULL, and those of an absent part must be
  *   ws           device workspace of at least gla_residual_norm_workspace_bytes(rows, D) bytes for the blocks' sums of these
  *                five, which are added up in a fixed order
- * Returns a gla_status.
+ * A layer norm's variance is taken of values less the mean of the row's first channels (8 in bf16, 128 in f32): it is good to
+ * 2^-24 (1 + (distance of that mean from the row's)^2 / variance), 2^-13 in bf16 and 2^-17 in f32 at worst, of 16,384 channels.
+ * No array may alias another.  Returns a gla_status.
  */
 GLA_API long long gla_residual_norm_workspace_bytes(long long rows, int D);
 GLA_API int gla_residual_norm_bwd(const void *dr, const void *dout, const void *r, const void *y, const void *gate,

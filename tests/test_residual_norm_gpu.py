@@ -277,3 +277,13 @@ def test_results_are_the_same_every_time(D):
     base = run()
     for _ in range(5):
         assert all(torch.equal(a, b) for a, b in zip(base, run()))
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("D", [72, 520, 2560, 5120, 8192])
+def test_the_stream_in_place(types, D):
+    v, block = make((400, D), types)
+    r, out = gla.residual_norm(v["x"], v["y"], v["weight"], v["bias"], gla.NORM_LAYER, **block)
+    again = torch.empty_like(out)
+    gla.gla_residual_norm(v["x"], v["y"], v["weight"], v["bias"], v["x"], again, gla.NORM_LAYER, **block)
+    assert torch.equal(v["x"], r) and torch.equal(again, out)
