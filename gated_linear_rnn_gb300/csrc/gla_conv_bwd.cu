@@ -244,13 +244,11 @@ Cut cut(int B, int T, int D, bool packed, int per_sm) {
     Cut c{};
     c.blocks = (int)(need < most ? need : most);
     const int64_t warps = (int64_t)c.blocks * kWarps;
-    int64_t runs = warps;
+    // so many times all warps that a run has fewer than 256 rows; a packed batch's sequence has a slot more than its rows make
+    const int64_t least = rows / 256 + 1 + (packed ? B + 1 : 0), runs = (least + warps - 1) / warps * warps;
     if (packed) {
-        // a sequence has a slot more than its rows make
-        while (runs <= B + 1 || rows / (runs - B - 1) >= 256) runs += warps;
         c.run_rows = (int)((rows + runs - B - 2) / (runs - B - 1));
     } else {
-        while (rows / runs >= 256) runs += warps;
         const int64_t per = runs / B > 1 ? runs / B : 1;
         c.run_rows = (int)((T + per - 1) / per);
     }
