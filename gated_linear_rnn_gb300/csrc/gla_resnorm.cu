@@ -100,6 +100,99 @@ fwd_kernel(const Inputs<3> in, Weights weights, int kind, int post, int act, flo
     it.end();
 }
 
+// Two rows at a time, a block's threads on the same channels of both: parameters are read once for two rows, and the rows' sums
+// meet together.
+constexpr int kTwoVecs = 2, kTwoMost = 640;
+template <typename T, typename TS>
+__global__ void __launch_bounds__(kTwoMost, 1)
+fwd_two_kernel(const Inputs<3> in, Weights weights, int kind, int post, int act, float eps, TS *r, T *__restrict__ out,
+               int64_t rows, int D, int lanes) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ Bars bars;
+    __shared__ __align__(16) Meeting<false> meet;
+    const Cluster<false> cl;
+    const Place<kTwoVecs> pl(D, lanes);
+    const float inv = 1.f / (float)D;
+    const bool has_y = in.from[1] != nullptr, has_gate = in.from[2] != nullptr, meets = post || out != nullptr;
+    Rows<true, 3, false> it(in, cl, ring, bars, rows, lanes);
+    meet.clear();
+    const Weights w = weights.from(pl.channel);
+    __syncthreads();
+    int half = 0;
+    auto two = [&](auto all) {
+        using Vs = Vectors<kTwoVecs, all.value>;
+        const Vs of[2] = {{pl.count}, {it.row + 1 < rows ? pl.count : 0}};
+        const int64_t at = it.row * D + pl.channel;
+        typename Vs::V v[2];
+        auto times = [&](typename Vs::V (&x)[2], const float *p) {
+            of[0].with(p, [&](int j, const Pair (&a)[2]) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) x[k][j][0] = x[k][j][0] * a[0], x[k][j][1] = x[k][j][1] * a[1];
+            });
+        };
+        auto plus = [&](typename Vs::V (&x)[2], const float *p) {
+            of[0].with(p, [&](int j, const Pair (&a)[2]) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) x[k][j][0] = x[k][j][0] + a[0], x[k][j][1] = x[k][j][1] + a[1];
+            });
+        };
+        auto normalise = [&](typename Vs::V (&x)[2]) {
+            if (kind == GLA_NORM_LAYER) {
+                const float2 o = row_sum(Vs::sum(x[0]), Vs::sum(x[1]), lanes, cl, meet, half);
+                of[0].shift(x[0], -o.x * inv), of[1].shift(x[1], -o.y * inv);
+            }
+            const float2 o = row_sum(Vs::squares(x[0]), Vs::squares(x[1]), lanes, cl, meet, half);
+            if (meets) it.refill();
+            of[0].times(x[0], rsqrtf(fmaf(o.x, inv, eps))), of[1].times(x[1], rsqrtf(fmaf(o.y, inv, eps)));
+        };
+        auto fetch = [&](typename Vs::V (&x)[2], const auto *from) {
+            of[0].fetch(x[0], from), of[1].fetch(x[1], from + D);
+        };
+        if (has_y) {
+            typename Vs::V u[2];
+            fetch(u, it.template at<T>(1, D, pl.channel));
+            if (post) {
+                normalise(u);
+                times(u, w.post_weight);
+                plus(u, w.post_bias);
+            }
+            if (has_gate) {
+                typename Vs::V g[2];
+                fetch(g, it.template at<T>(2, D, pl.channel));
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (act == kSilu) Vs::template gate<kSilu>(g[k]);
+                    else if (act == kSigmoid) Vs::template gate<kSigmoid>(g[k]);
+#pragma unroll
+                    for (int j = 0; j < kTwoVecs; ++j) u[k][j][0] = u[k][j][0] * g[k][j][0], u[k][j][1] = u[k][j][1] * g[k][j][1];
+                }
+            }
+            times(u, w.scale);
+            fetch(v, it.template at<TS>(0, D, pl.channel));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int j = 0; j < kTwoVecs; ++j) v[k][j][0] = v[k][j][0] + u[k][j][0], v[k][j][1] = v[k][j][1] + u[k][j][1];
+                of[k].store(r + at + k * D, v[k]);
+                of[k].clear(v[k]);
+            }
+        } else {
+            fetch(v, it.template at<TS>(0, D, pl.channel));
+        }
+        if (out != nullptr) {
+            normalise(v);
+            times(v, w.weight);
+            plus(v, w.bias);
+            of[0].store(out + at, v[0]), of[1].store(out + at + D, v[1]);
+        }
+    };
+    for (; it.begin(meets); it.next(), it.next()) {
+        if (D % (kStride * kTwoVecs) == 0 && it.row + 1 < rows) two(std::true_type{});
+        else two(std::false_type{});
+    }
+    it.end();
+}
+
 struct Sums {
     float *dscale, *dpost_weight, *dpost_bias, *dweight, *dbias;
 };
@@ -143,9 +236,26 @@ int launch_fwd(const void *x, const void *y, const void *gate, const Weights &w,
     Inputs<3> in{{x, y, gate}, {D * es, D * e, D * e}};
     const int n = per_sm(pl, kFwdThreads), nu = units(pl, rows, n);
     int params_at, bytes = lay_out(in, pl, rows, n, nu, 0, params_at);
-    // Two blocks of a wide row each want the L1 for the parameters more than stages (8,192 x 5,120 bf16: 123 us, 149 with
-    // stages; one block, 4,096 x 8,192: 125 and 107).
+    // Two blocks of a wide row each want the L1 for the parameters more than stages (8,192 x 5,120 bf16, one row at a time:
+    // 123 us, 149 with stages; one block, 4,096 x 8,192: 125 and 107).
     if (n > 1 && pl.threads > 256) in.stages = bytes = 0;
+    // Two rows at a time where that has as many rows on an SM, however many a call has, so that a row's result does not depend on
+    // the others (all parts, bf16, two and one:
+    // 16,435 x 2,552 104 and 123 us, 69,905 x 600 135 and 176, 8,192 x 5,120 104 and 123, 16,384 x 2,560 97 and 99; with fewer
+    // rows on an SM, 10,240 x 4,096 118 and 92).  What stages leave of shared memory, 60 KB or more, caches the parameters.
+    const Plan p2 = make_plan(D, kTwoVecs, 16384);
+    const int n2 = per_sm(p2, kTwoMost), room = kMostShared / n2 - (n2 == 1 ? 0 : 3328);
+    Inputs<3> two{{x, y, gate}, {D * es, D * e, D * e}};
+    two.passes = 2;
+    for (int i = 0; i < 3; ++i) {
+        two.at[i] = two.stage_bytes;
+        if (two.from[i] != nullptr) two.stage_bytes += (2 * two.row_bytes[i] + 127) / 128 * 128;
+    }
+    two.stages = (room - 60 * 1024 / n2) / two.stage_bytes;
+    two.stages = two.stages < 2 ? 2 : two.stages > kMaxStages ? kMaxStages : two.stages;
+    if (p2.lanes > 32 && p2.threads <= kTwoMost && 2 * n2 >= n * pl.rows && 2 * two.stage_bytes <= room)
+        return launch<fwd_two_kernel<T, TS>>(units(p2, (rows + 1) / 2, n2), 1, p2.threads, two.stages * two.stage_bytes, st, two, w, kind,
+                                             post, act, eps, (TS *)r, (T *)out, rows, D, p2.lanes);
 #define GLA_RUN(V, S, N)                                                                                                   \
     return launch<fwd_kernel<T, TS, V, S, N>>(nu, 1, pl.threads, bytes, st, in, w, kind, post, act, eps, (TS *)r, (T *)out, rows, D, pl.lanes);
     if (pl.vecs < kFwdVecs && in.stages < 2) return 0;  // (so few channels always have room)

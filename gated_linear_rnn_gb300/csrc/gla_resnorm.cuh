@@ -6,8 +6,8 @@
 // shared memory by bulk copies, some rows ahead, and are read from there by each step: what is in flight costs no registers.
 // Rows of the forward that two stages have no room for are read from memory.
 //
-// Measured with all parts (layer norms before and behind, gate, scale; bf16): forward of 16,384 x 2,560 98 us (the bytes at the
-// rate of a copy: 62), of an RMS norm alone behind the sum 56 (50); gradient 177 and 95 (99 and 74).  8,192 x 5,120: 123 and 187;
+// Measured with all parts (layer norms before and behind, gate, scale; bf16): forward of 16,384 x 2,560 97 us (the bytes at the
+// rate of a copy: 62), of an RMS norm alone behind the sum 55 (50); gradient 177 and 95 (99 and 74).  8,192 x 5,120: 105 and 187;
 // f32 8,192 x 2,560: 79 and 166 (62 and 99).  What bounds the gradient is its instructions, about 90 a channel, and two meetings
 // of a row's warps; the forward waits for its four meetings and for the parameters, which are as many bytes as the row.
 //

@@ -287,3 +287,21 @@ def test_the_stream_in_place(types, D):
     again = torch.empty_like(out)
     gla.gla_residual_norm(v["x"], v["y"], v["weight"], v["bias"], v["x"], again, gla.NORM_LAYER, **block)
     assert torch.equal(v["x"], r) and torch.equal(again, out)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("rows,D", [(8501, 520), (5001, 1160), (1300, 2560), (1217, 2552), (701, 5120), (700, 4616)])
+@pytest.mark.parametrize("parts", [True, False])
+def test_many_rows(types, rows, D, parts):
+    """As many as are taken two at a time, an odd one among them, against a few of them alone, which are not."""
+    v, block = make((rows, D), types, gate=parts, scale=parts, post=parts)
+    r, out = gla.residual_norm(v["x"], v["y"], v["weight"], v["bias"], KINDS[rows % 2], **block)
+    some = torch.tensor([0, 1, 2, rows // 2, rows - 3, rows - 2, rows - 1], device="cuda")
+    few = {k: None if x is None or x.dim() < 2 else x[some].contiguous() for k, x in v.items()}
+    kw = dict(kind=KINDS[rows % 2], **{**block, "gate": few["gate"]})
+    r_ref, o_ref = K.residual_norm(few["x"], few["y"], v["weight"], v["bias"], **kw)
+    close(r[some], r_ref, F32, "r")
+    close(out[some], o_ref, F32, "out")
+    r1, out1 = gla.residual_norm(few["x"], few["y"], v["weight"], v["bias"], **kw)
+    assert bool(r.isfinite().all()) and bool(out.isfinite().all())
+    close(r1, r_ref, F32, "r"), close(out1, o_ref, F32, "out")
