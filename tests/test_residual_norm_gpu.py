@@ -305,3 +305,21 @@ def test_many_rows(types, rows, D, parts):
     r1, out1 = gla.residual_norm(few["x"], few["y"], v["weight"], v["bias"], **kw)
     assert bool(r.isfinite().all()) and bool(out.isfinite().all())
     close(r1, r_ref, F32, "r"), close(out1, o_ref, F32, "out")
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("rows,D", [(30001, 72), (8501, 520), (2500, 2552), (2501, 2560), (1301, 4096), (1301, 5120)])
+def test_many_rows_of_the_sum_alone_and_of_the_norm_alone(types, rows, D):
+    v, block = make((rows, D), types, post=False)
+    r, out = gla.residual_norm(v["x"], v["y"], **block, norm=False)
+    assert out is None
+    some = torch.tensor([0, 1, rows // 2, rows - 2, rows - 1], device="cuda")
+    few = {k: None if x is None or x.dim() < 2 else x[some].contiguous() for k, x in v.items()}
+    want, _ = K.residual_norm(few["x"], few["y"], None, None, gate=few["gate"], scale=v["scale"])
+    close(r[some], want, F32, "r")
+    r, out = gla.residual_norm(v["x"], None, v["weight"], v["bias"], gla.NORM_LAYER, dtype=types[0])
+    assert r is None
+    close(out[some], K.residual_norm(few["x"], None, v["weight"], v["bias"], gla.NORM_LAYER)[1], F32, "out")
+    got = gla.residual_norm_bwd(v["dr"], None, v["x"], v["y"], **block)
+    want = K.residual_norm_bwd(few["dr"], None, few["x"], few["y"], None, gate=few["gate"], scale=v["scale"])
+    close(got.dx[some], want["dx"], F32, "dx"), close(got.dy[some], want["dy"], F32, "dy")
