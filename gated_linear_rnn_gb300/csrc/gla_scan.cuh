@@ -47,9 +47,6 @@ template <> struct Two<float> {
     static __device__ __forceinline__ Pair open(Raw w) { return pair(w.x, w.y); }
     static __device__ __forceinline__ Raw close(Pair x) { return parts(x); }
 };
-template <typename T> __device__ __forceinline__ Pair load_two(const T *p) {
-    return Two<T>::open(__ldg(reinterpret_cast<const typename Two<T>::Raw *>(p)));
-}
 template <typename T> __device__ __forceinline__ void store_two(T *p, Pair x) {
     *reinterpret_cast<typename Two<T>::Raw *>(p) = Two<T>::close(x);
 }
