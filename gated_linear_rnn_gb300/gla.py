@@ -979,11 +979,12 @@ def conv1d_silu_bwd(dy, x, weight, bias=None, state_in=None, dstate_out=None, cu
     return dx, dweight, dbias, dstate
 
 
-def scan_states(x, cu_seqlens=None):
-    """Allocate the states that scan_fwd keeps for scan_bwd, for inputs like ``x``."""
+def scan_states(x, cu_seqlens=None, stream=None):
+    """Allocate the states that scan_fwd keeps for scan_bwd, for inputs like ``x``.  ``stream``: that of both calls."""
     nseq = x.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
     n = gla_scan_states_bytes(nseq, x.shape[1], x.shape[2], cu_seqlens is not None) // 4
-    return torch.empty(n, dtype=torch.float32, device=x.device)
+    with _allocating_on(stream, x.device):
+        return torch.empty(n, dtype=torch.float32, device=x.device)
 
 
 def scan_fwd(x, g, form: int, gate=None, act: int = ACT_SILU, h0=None, cu_seqlens=None, final_state: bool = True,

@@ -352,6 +352,28 @@ def test_another_stream_and_a_workspace_of_the_callers():
     assert all(torch.equal(x, y) for x, y in zip(got, grads))
 
 
+def test_kept_states_on_another_stream():
+    """They come from that stream's pool: dropped right after the calls, they are not handed out to the current stream,
+    which writes over whatever it gets, before the gradient has read them."""
+    form = gla.SCAN_SIGMOID
+    t = make((2, 3000, 520), TYPES[0], form)
+    kept = gla.scan_states(t["x"])
+    base = gla.scan_fwd(t["x"], t["g"], form, t["gate"], h0=t["h0"], states=kept)
+    grads = gla.scan_bwd(t["x"], t["g"], form, t["dout"], t["gate"], h0=t["h0"], dhT=t["dhT"], states=kept)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        kept = gla.scan_states(t["x"], stream=handle)
+        at, n = kept.data_ptr(), kept.numel()
+        out = gla.scan_fwd(t["x"], t["g"], form, t["gate"], h0=t["h0"], states=kept, stream=handle)
+        got = gla.scan_bwd(t["x"], t["g"], form, t["dout"], t["gate"], h0=t["h0"], dhT=t["dhT"], states=kept, stream=handle)
+        del kept
+        other = torch.full((n,), float("nan"), device="cuda")
+        assert other.data_ptr() != at
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(base + grads, out + got))
+
+
 def test_two_captured_graphs_share_a_workspace_and_replay():
     form = gla.SCAN_LOG
     t = make((1, 1000, 136), TYPES[1], form, nseq=3)
