@@ -294,6 +294,7 @@ int check_scan_kind(int form, int act, int dtype, int g_dtype) {
     return GLA_OK;
 }
 
+// What both calls over whole sequences check of theirs; the device they ask for last.
 int check_scan(const void *x, const void *g, const void *gate, const float *h0, const void *out, const float *hT,
                const float *states, int B, int T, int D, int form, int act, int dtype, int g_dtype, const int32_t *cu,
                const void *ws) {
@@ -304,7 +305,6 @@ int check_scan(const void *x, const void *g, const void *gate, const float *h0, 
     if (!aligned16(x) || !aligned16(g) || !aligned16(gate) || !aligned16(h0) || !aligned16(out) || !aligned16(hT) ||
         !aligned16(states) || !aligned16(cu) || !aligned16(ws))
         return GLA_ERR_ALIGN;
-    if (!device_info().ok) return GLA_ERR_UNSUPPORTED;
     return GLA_OK;
 }
 
@@ -684,6 +684,7 @@ int gla_scan_fwd(const void *x, const void *g, const void *gate, const float *h0
     const scan::Shape p{B, T, D, form, act, cu_seqlens};
     const int64_t need = scan::workspace(GLA_OP_FORWARD, p);
     if (need > 0 && (!ws || ws_bytes < need)) return GLA_ERR_ARG;
+    if (!device_info().ok) return GLA_ERR_UNSUPPORTED;
     return scan::fwd(p, x, g, gate, h0, out, hT, states, dtype, g_dtype, ws, (cudaStream_t)stream);
 }
 
@@ -697,6 +698,7 @@ int gla_scan_bwd(const void *x, const void *g, const void *gate, const void *dou
     const scan::Shape p{B, T, D, form, act, cu_seqlens};
     const int64_t need = scan::workspace(GLA_OP_BACKWARD, p);
     if (need > 0 && (!ws || ws_bytes < need)) return GLA_ERR_ARG;
+    if (!device_info().ok) return GLA_ERR_UNSUPPORTED;
     return scan::bwd(p, x, g, gate, dout, h0, dhT, states, dx, dg, dgate, dh0, dtype, g_dtype, ws, (cudaStream_t)stream);
 }
 

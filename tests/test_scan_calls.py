@@ -38,6 +38,29 @@ def test_backward_refuses(lib):
     assert {bwd(dx=None), bwd(dg=None), bwd(gate=FAKE), bwd(dgate=FAKE), bwd()} <= {-1, -2}
 
 
+def test_backward_refuses_each_bad_argument_of_an_else_good_call(lib):
+    """Each call has room for its workspace and lacks one thing, and is refused for that before the device is asked for: on a
+    machine without one nothing else is left to refuse the good call, and with one the good call is not made."""
+    import torch
+    n = gla.gla_scan_workspace_bytes(gla.OP_BACKWARD, 1, 8, 64, False)
+    assert n > 0
+
+    def bwd(x=FAKE, g=FAKE, gate=None, dout=FAKE, h0=None, dhT=None, states=None, dx=FAKE, dg=FAKE, dgate=None, dh0=None, B=1, T=8,
+            D=64, form=0, act=1, dtype=0, g_dtype=1, cu=None, ws=FAKE, n=n):
+        return lib.gla_scan_bwd(x, g, gate, dout, h0, dhT, states, dx, dg, dgate, dh0, B, T, D, form, act, dtype, g_dtype, cu, ws, n,
+                                None)
+    assert bwd(x=None) == bwd(g=None) == bwd(dout=None) == bwd(dx=None) == bwd(dg=None) == -1
+    assert bwd(gate=FAKE) == bwd(dgate=FAKE) == -1  # a gate without its gradient, and a gradient without its gate
+    assert bwd(ws=None) == bwd(n=n - 1) == -1
+    assert bwd(B=0) == bwd(T=-1) == bwd(D=0) == bwd(form=4) == bwd(act=3) == bwd(dtype=2) == bwd(dtype=1, g_dtype=0) == -1
+    assert bwd(D=60) == bwd(B=1 << 20, T=1 << 12) == -2
+    for name in ("x", "g", "dout", "h0", "dhT", "states", "dx", "dg", "dh0", "cu", "ws"):
+        assert bwd(**{name: ODD}) == -3, name
+    assert bwd(gate=ODD, dgate=FAKE) == bwd(gate=FAKE, dgate=ODD) == -3
+    if not torch.cuda.is_available():
+        assert bwd() == -2
+
+
 def test_step_refuses(lib):
     def step(x=FAKE, g=FAKE, gate=None, state=FAKE, slots=None, nslots=0, out=FAKE, N=1, D=64, form=0, act=1):
         return lib.gla_scan_step(x, g, gate, state, slots, nslots, out, N, D, form, act, 0, 1, None)
