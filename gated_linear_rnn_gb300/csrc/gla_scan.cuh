@@ -50,6 +50,9 @@ template <> struct Two<float> {
 template <typename T> __device__ __forceinline__ void store_two(T *p, Pair x) {
     *reinterpret_cast<typename Two<T>::Raw *>(p) = Two<T>::close(x);
 }
+template <typename T> __device__ __forceinline__ Pair load_two(const T *p) {
+    return Two<T>::open(__ldg(reinterpret_cast<const typename Two<T>::Raw *>(p)));
+}
 // four of them, as they lie in memory
 template <typename T> struct FourRaw;
 template <> struct FourRaw<__nv_bfloat16> {

@@ -33,6 +33,7 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
     __shared__ float4 both_effects[2][kWarps][32];  // of this tile and the one before
     __shared__ float2 enters[32];
     __shared__ Window win;
+    __shared__ Apart apart;
     __shared__ Tile tiles[kMaxStages];
     __shared__ __align__(8) uint64_t full[kMaxStages];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = t.D;
@@ -53,6 +54,7 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
     const bool orders = threadIdx.x == kTileThreads - 32;  // not of the warp that folds what is looked back over
     if (orders) {
         win.gave_up = 0;
+        if (is_log(kForm)) apart.any = 0;
         turns.start(t, chain);
         for (int st = 0; st < stages; ++st) mbar_init(bar + 8u * (uint32_t)st, 1);
         fence_mbar_init();
@@ -137,17 +139,18 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
             const float4 f = effects[kWho][lane];
             tC = fma(pair(f.x, f.y), bC, pair(f.z, f.w));
             tA = bA * pair(f.x, f.y);
-            if (on && o.behind > 0 && o.chunk > 0) publish_effect(chain, at, tA, tC);
+            if (on && o.behind > 0 && o.chunk > 0) publish_effect<is_log(kForm)>(chain, at, tA, tC);
             if (on && o.behind == 0 && dhT != nullptr) S = load_state(dhT + (int64_t)o.seq * D + d);
         }
         if (o.behind > 0) ok = look_back<1, kWho>(chain, win, o.slot, D, d, min(o.behind, t.window), S);
         if (warp == kWho) {
             const Pair end = fma(tA, S, tC);
             if (on) {
-                if (o.chunk > 0) publish_result(chain, at, end);
+                if (o.chunk > 0) publish_result<is_log(kForm)>(chain, at, end);
                 else if (dh0 != nullptr) store_state(dh0 + (int64_t)o.seq * D + d, end);
             }
             enters[lane] = parts(S);
+            if (is_log(kForm)) find_apart(apart, chain, at, o, on && o.chunk > 0, tA, tC, end);
         }
         __syncthreads();
         ok = ok && !win.gave_up;
@@ -155,6 +158,29 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
         const float2 e = enters[lane];
         Pair K = fma(bA, pair(e.x, e.y), bC);
         next = state_of(tiles[st + 1 == stages ? 0 : st + 1]);
+        if (is_log(kForm) && apart.any) {  // channels that are apart: what is behind a warp's rows from one warp after the other
+            const int bits = apart.of[lane];
+            __syncthreads();  // all warps have read what is behind the tile
+            for (int w = kWarps - 1; w >= 0; --w) {
+                if (w == warp) {
+                    const float2 f = enters[lane];
+                    Pair L = pair(f.x, f.y);
+                    K = choose(bits, L, K);
+#pragma unroll
+                    for (int i = kLane - 1; i >= 0; --i)
+                        if (i < n) L = decayed(a[i], up[i] + L);
+                    enters[lane] = parts(L);
+                }
+                __syncthreads();
+            }
+            if (warp == kWho && bits != 0) {
+                const float2 f = enters[lane], l = apart.folded[lane];
+                const Pair end = choose(bits, pair(f.x, f.y), pair(l.x, l.y));
+                if (o.chunk > 0) publish_result<false>(chain, at, end);
+                else if (dh0 != nullptr) store_state(dh0 + (int64_t)o.seq * D + d, end);
+            }
+            apart.any = 0;
+        }
         auto backwards = [&](auto whole_run) {
             T *to = dx + out_at + (int64_t)(kLane - 1) * D;
             TG *to_g = dg + out_at + (int64_t)(kLane - 1) * D;

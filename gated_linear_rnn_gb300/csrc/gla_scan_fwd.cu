@@ -16,11 +16,47 @@ template <typename T, typename TG, bool kGate> struct Ring {
     static constexpr int bytes = z + (kGate ? tile_bytes<T>() : 0);
 };
 
+// The rows of a tile's channels that are apart, one warp after the other from the state that enters the tile; by all threads, after
+// a barrier behind the writes of enters and apart.  x and g come from memory: their stage has been refilled.
+template <typename T, typename TG, int kForm, bool kGate>
+__device__ __forceinline__ void again(const T *x, const TG *g, const T *gate, T *out, float *hT, float *states, Chain chain, int D,
+                                      int act, const Apart &apart, float2 (&enters)[32]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bits = apart.of[lane];
+    const Tile o = apart.tile;
+    const int d = o.col + 2 * lane, n = min(kLane, o.len - warp * kLane);
+    __syncthreads();  // all warps have read what enters the tile
+    for (int w = 0; w < kWarps; ++w) {
+        if (w == warp && bits != 0 && n > 0) {
+            const float2 e = enters[lane];
+            Pair S = pair(e.x, e.y);
+            if (states != nullptr)
+                store_some(states + state_slot(o.start(), o.seq, o.chunk * kChunk + warp * kLane) * D + d, S, bits);
+            int64_t at = (int64_t)(o.row + warp * kLane) * D + d;
+#pragma unroll 1
+            for (int i = 0; i < n; ++i, at += D) {
+                const Decay a = decay<kForm>(load_two(g + at));
+                S = decayed(a, S, input<kForm>(a, load_two(x + at)));
+                if (out == nullptr) continue;
+                store_some(out + at, kGate ? S * activation(load_two(gate + at), act) : S, bits);
+            }
+            enters[lane] = parts(S);
+        }
+        __syncthreads();
+    }
+    if (warp == kWarps - 1 && bits != 0) {
+        const float2 e = enters[lane], f = apart.folded[lane];
+        const Pair end = choose(bits, pair(e.x, e.y), pair(f.x, f.y));
+        if (o.behind > 0) publish_result<false>(chain, (int64_t)o.slot * D + d, end);
+        else if (hT != nullptr) store_state(hT + (int64_t)o.seq * D + d, end);
+    }
+}
+
 template <typename T, typename TG, int kForm, bool kGate>
 __global__ void __launch_bounds__(kTileThreads, kPerSm)
 tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
-                 const __grid_constant__ CUtensorMap mz, const float *__restrict__ h0, T *__restrict__ out,
-                 float *__restrict__ hT, float *__restrict__ states, Tiles t, Chain chain, int act, int stages) {
+                 const __grid_constant__ CUtensorMap mz, const T *x, const TG *g, const T *gate,
+                 const float *__restrict__ h0, T *__restrict__ out, float *__restrict__ hT, float *__restrict__ states, Tiles t,
+                 Chain chain, int act, int stages) {
     using namespace ptx;
     using R = Ring<T, TG, kGate>;
     if (tiles_of(t) == 0 && t.walked) return;
@@ -28,6 +64,7 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
     __shared__ float4 both_effects[2][kWarps][32];  // of this tile and the one before
     __shared__ float2 enters[32];
     __shared__ Window win;
+    __shared__ Apart apart;
     __shared__ Tile tiles[kMaxStages];
     __shared__ __align__(8) uint64_t full[kMaxStages];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = t.D;
@@ -53,6 +90,7 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
     };
     if (threadIdx.x == 0) {
         win.gave_up = 0;
+        if (is_log(kForm)) apart.any = 0;
         turns.start(t, chain);
         for (int st = 0; st < stages; ++st) mbar_init(bar + 8u * (uint32_t)st, kGate ? 2 : 1);
         fence_mbar_init();
@@ -118,17 +156,18 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
         }
         const Pair tA = A * P[kLane - 1], tH = fma(P[kLane - 1], H, h[kLane - 1]);
         if (warp == kWho && d < D) {  // tA and tH are the tile's effect
-            if (o.chunk > 0 && o.behind > 0) publish_effect(chain, at, tA, tH);
+            if (o.chunk > 0 && o.behind > 0) publish_effect<is_log(kForm)>(chain, at, tA, tH);
             if (o.chunk == 0 && h0 != nullptr) S = load_state(h0 + (int64_t)o.seq * D + d);
         }
         if (o.chunk > 0) ok = look_back<-1, kWho>(chain, win, o.slot, D, d, min(o.chunk, t.window), S);
         if (warp == kWho) {
             const Pair end = fma(tA, S, tH);
             if (d < D) {
-                if (o.behind > 0) publish_result(chain, at, end);
+                if (o.behind > 0) publish_result<is_log(kForm)>(chain, at, end);
                 else if (hT != nullptr) store_state(hT + (int64_t)o.seq * D + d, end);
             }
             enters[lane] = parts(S);
+            if (is_log(kForm)) find_apart(apart, chain, at, o, d < D && o.behind > 0, tA, tH, end);
         }
         __syncthreads();
         ok = ok && !win.gave_up;
@@ -154,6 +193,10 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
             else if (!kGate || act == kSilu) emit(std::true_type{}, kSilu);
             else if (act == kSigmoid) emit(std::true_type{}, kSigmoid);
             else emit(std::true_type{}, kNone);
+        }
+        if (is_log(kForm) && apart.any) {
+            again<T, TG, kForm, kGate>(x, g, gate, out, hT, states, chain, D, act, apart, enters);
+            apart.any = 0;
         }
         if (++st == stages) {
             st = 0;
@@ -189,7 +232,7 @@ bool launch(const Shape &p, Tiles t, const Chain &chain, const T *x, const TG *g
     if (grid > (int64_t)t.total) grid = t.total;
     if (grid < 1) grid = 1;
     t.window = window_for(t, grid);
-    kKernel<<<(unsigned)grid, kTileThreads, bytes, st>>>(mx, mg, mz, h0, out, hT, states, t, chain, p.act, room.stages);
+    kKernel<<<(unsigned)grid, kTileThreads, bytes, st>>>(mx, mg, mz, x, g, gate, h0, out, hT, states, t, chain, p.act, room.stages);
     count_launches(1);
     return true;
 }

@@ -8,6 +8,12 @@
 //
 // What is published is its own flag: a word that holds kUnset has not been written yet.
 //
+// Log decays may be above 0.  A tile's product of decays, or its result from a zero state, can then leave f32 where the states do
+// not: zeros, small states, those behind a reset.  A channel whose effect did so is apart: its effect and result stay unset, so that
+// nobody folds them, and once the state that enters the tile is known its warps go through their rows one after the other from
+// there, and the last one publishes the result.  (Decays below 0 pay 0 to 2% of a forward and -2 to 3% of a gradient for it, where
+// the tests of the result move the compiler's use of registers.  A sigmoid is at most 1, and its kernels have none of it.)
+//
 // Tiles are handed out by a counter in an order in which a tile comes after all that it waits for, so that a waiting block
 // waits only for blocks that run.  Rows come in by TMA, some tiles ahead.
 //
@@ -36,6 +42,7 @@ constexpr int kSlab = 64;                    // channels of a tile
 constexpr uint32_t kUnset = 0xffffffffu;     // a NaN that no result is: one that would be is stored as another
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s a wait
 constexpr int kBack = 2 * kWarps;            // tiles that a look back reads at once, at most
+constexpr float kMostF32 = 3.40282347e38f;
 
 // The chunks' effects and results, for one direction.
 struct Chain {
@@ -132,17 +139,23 @@ template <typename T> constexpr int tile_bytes() { return kChunk * kSlab * (int)
 
 // ---- what is published -----------------------------------------------------------------------------------------------
 __device__ __forceinline__ float settled(float x) { return __float_as_uint(x) == kUnset ? __uint_as_float(0x7fffffffu) : x; }
+// What is stored of x; of kernels whose effects may leave f32, those that did stay unset.
+template <bool kFinite> __device__ __forceinline__ float told(float x) {
+    return kFinite ? (fabsf(x) <= kMostF32 ? x : __uint_as_float(kUnset)) : settled(x);
+}
 __device__ __forceinline__ bool is_set(float x) { return __float_as_uint(x) != kUnset; }
 
+template <bool kFinite>
 __device__ __forceinline__ void publish_effect(const Chain &c, int64_t at, Pair A, Pair H) {
     const float2 a = parts(A), h = parts(H);
-    asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(c.effect + at * 2), "f"(settled(a.x)),
-                 "f"(settled(h.x)), "f"(settled(a.y)), "f"(settled(h.y))
+    asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(c.effect + at * 2), "f"(told<kFinite>(a.x)),
+                 "f"(told<kFinite>(h.x)), "f"(told<kFinite>(a.y)), "f"(told<kFinite>(h.y))
                  : "memory");
 }
+template <bool kFinite>
 __device__ __forceinline__ void publish_result(const Chain &c, int64_t at, Pair S) {
     const float2 s = parts(S);
-    asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(c.result + at), "f"(settled(s.x)), "f"(settled(s.y))
+    asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(c.result + at), "f"(told<kFinite>(s.x)), "f"(told<kFinite>(s.y))
                  : "memory");
 }
 __device__ __forceinline__ float4 read_effect(const Chain &c, int64_t at) {
@@ -225,6 +238,39 @@ __device__ __forceinline__ bool look_back(const Chain &c, Window &win, int64_t s
         __syncthreads();
         if (win.gave_up) return false;
     }
+}
+
+// The channels of a tile that are apart: whether there are any, two bits a lane, what the fold gave as their and their neighbours'
+// result, and the tile.
+struct Apart {
+    int any;
+    int of[32];
+    float2 folded[32];
+    Tile tile;
+};
+// By the warp that tells a tile's result, which stayed unset where it is not finite: such a channel is apart if it is the tile's
+// effect that left f32; else an infinity or a NaN enters the tile, and its result is told here.
+__device__ __forceinline__ void find_apart(Apart &apart, const Chain &c, int64_t at, const Tile &o, bool tells, Pair A, Pair H, Pair end) {
+    const float2 e = parts(end);
+    const bool odd = !(fabsf(e.x) <= kMostF32 && fabsf(e.y) <= kMostF32);
+    if (!__any_sync(0xffffffffu, odd)) return;
+    const float2 f = parts(fma(H, both(0.f), A * both(0.f)));  // a NaN where either is none or infinite
+    const int lane = threadIdx.x & 31, bits = (f.x == 0.f ? 0 : 1) | (f.y == 0.f ? 0 : 2);
+    apart.of[lane] = bits;
+    apart.folded[lane] = e;
+    if (lane == 0) apart.tile = o;
+    if (odd && bits == 0 && tells) publish_result<false>(c, at, end);
+    if (bits != 0) apart.any = 1;
+}
+__device__ __forceinline__ Pair choose(int bits, Pair x, Pair rest) {
+    const float2 f = parts(x), g = parts(rest);
+    return pair(bits & 1 ? f.x : g.x, bits & 2 ? f.y : g.y);
+}
+template <typename T> __device__ __forceinline__ void store_some(T *p, Pair x, int bits) {
+    const typename Two<T>::Raw raw = Two<T>::close(x);
+    const T *const f = reinterpret_cast<const T *>(&raw);
+    if (bits & 1) p[0] = f[0];
+    if (bits & 2) p[1] = f[1];
 }
 
 // ---- launches --------------------------------------------------------------------------------------------------------
