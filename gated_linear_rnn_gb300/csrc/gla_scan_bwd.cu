@@ -85,9 +85,13 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
         const bool on = d < D;
         const int64_t at = (int64_t)o.slot * D + d, out_at = (int64_t)(o.row + warp * kLane) * D + d;
         Pair h = next;
-        if (!mbar_wait(bar + 8u * (uint32_t)st, phase, nullptr, kWaitNs)) win.gave_up = 1;
         const uint8_t *stage = ring + st * R::bytes + (warp * kLane * kSlab + 2 * lane) * (int)sizeof(T);
-        const uint8_t *stage_g = ring + st * R::bytes + R::g + (warp * kLane * kSlab + 2 * lane) * (int)sizeof(TG);
+        uint8_t *stage_g = ring + st * R::bytes + R::g + (warp * kLane * kSlab + 2 * lane) * (int)sizeof(TG);
+        if (!mbar_wait(bar + 8u * (uint32_t)st, phase, nullptr, kWaitNs)) {
+            win.gave_up = 1;
+            // the thread's first row has a decay of NaN then, and so has all that is told of the tile
+            store_two(reinterpret_cast<TG *>(stage_g), both(__uint_as_float(0x7fffffffu)));
+        }
         auto &effects = both_effects[half];
         // the warp's rows: their decays, dout times the gate's factor, dg without dh, and the rows' effect
         Decay a[kLane];
@@ -206,6 +210,7 @@ tiles_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
     // a block that gave up waits for what it has ordered
     if (!ok && threadIdx.x == 0) {
         record_status(GLA_ERR_TIMEOUT);
+        if (t.chained) atomicExch(chain.next + 1, 1u);  // who waits for its tiles need not wait longer
         for (int i = 0; i < stages; ++i) {
             if (++st == stages) {
                 st = 0;

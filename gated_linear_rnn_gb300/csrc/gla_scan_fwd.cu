@@ -113,9 +113,13 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
     for (bool first = true;; first = false, half ^= 1) {
         const Tile o = tiles[st];
         if (o.row < 0) break;
-        if (!mbar_wait(bar + 8u * (uint32_t)st, phase, nullptr, kWaitNs)) win.gave_up = 1;
         const uint8_t *stage = ring + st * R::bytes + (warp * kLane * kSlab + 2 * lane) * (int)sizeof(T);
-        const uint8_t *stage_g = ring + st * R::bytes + R::g + (warp * kLane * kSlab + 2 * lane) * (int)sizeof(TG);
+        uint8_t *stage_g = ring + st * R::bytes + R::g + (warp * kLane * kSlab + 2 * lane) * (int)sizeof(TG);
+        if (!mbar_wait(bar + 8u * (uint32_t)st, phase, nullptr, kWaitNs)) {
+            win.gave_up = 1;
+            // the thread's first row has a decay of NaN then, and so has all that is told of the tile
+            store_two(reinterpret_cast<TG *>(stage_g), both(__uint_as_float(0x7fffffffu)));
+        }
         const int d = o.col + 2 * lane, n = min(kLane, o.len - warp * kLane);  // the warp's rows, none or fewer where n < 8
         auto &effects = both_effects[half];
         // the warp's rows from a zero state: h, and the product of the decays up to each
@@ -206,6 +210,7 @@ tiles_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__
     // a block that gave up waits for what it has ordered
     if (!ok && threadIdx.x == 0) {
         record_status(GLA_ERR_TIMEOUT);
+        if (t.chained) atomicExch(chain.next + 1, 1u);  // who waits for its tiles need not wait longer
         order_gate(st);
         for (int i = 0; i < stages; ++i) {
             if (++st == stages) {

@@ -174,7 +174,8 @@ __device__ __forceinline__ float2 read_result(const Chain &c, int64_t at) {
 
 // The state that enters a tile from the `n` tiles that are looked back over, by the whole block; kStep is how far a
 // neighbour's slot lies off.  Each warp reads two of them at most, so that one trip to memory serves all.  Warp kWho has the
-// state; a channel past the last has nothing to wait for.  False, for all threads, when the wait gave up.
+// state; a channel past the last has nothing to wait for.  False, for all threads, when the wait gave up: the state is then a NaN, so
+// that what the tile tells others is none either.
 struct Window {
     float4 effect[kBack][32];
     float2 result[kBack][32];
@@ -236,7 +237,10 @@ __device__ __forceinline__ bool look_back(const Chain &c, Window &win, int64_t s
             }
         }
         __syncthreads();
-        if (win.gave_up) return false;
+        if (win.gave_up) {
+            S = both(__uint_as_float(0x7fffffffu));
+            return false;
+        }
     }
 }
 
