@@ -458,3 +458,42 @@ def test_refusals_on_the_device():
     assert gla.gla_kernel_launches() == before
     out = gla.scan_step(x[0, :0].contiguous(), g[0, :0].contiguous(), gla.SCAN_LOG, torch.zeros(0, 64, device="cuda"))
     assert out.shape == (0, 64) and gla.gla_kernel_launches() == before
+
+
+# ---- sequences that are walked token by token ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("lengths", [[1] * 200 + [9, 17, 63, 64, 65, 0, 300], [64, 8, 16] + [2] * 60 + [0, 24, 15, 1],
+                                     [1] * 300 + [9, 16, 31, 32, 33, 0, 40, 57, 64, 128, 129]])
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("states", [False, True])
+def test_long_sequences_among_walked_ones(lengths, types, states):
+    """Eight tokens on average and fewer, so all of up to 64 tokens are walked: several runs of eight rows, whole and not, and
+    the states before each of them; the longer ones go by tiles."""
+    assert sum(lengths) <= 8 * len(lengths)
+    cu = np.concatenate([[0], np.cumsum(lengths)]).tolist()
+    form = FORMS[len(lengths) % 4]
+    t = make((1, cu[-1], 72), types, form, gated=states, nseq=len(lengths), seed=len(lengths))
+    check(t, form, gla.ACT_SIGMOID, cu, states)
+
+
+@pytest.mark.parametrize("T", [9, 17, 31, 32, 33])
+@pytest.mark.parametrize("types", TYPES)
+def test_large_batches_of_short_sequences(T, types):
+    """2,440 tiles: sequences of up to 32 tokens are walked, of 33 go by tiles.  Some of the sequences and channels against the
+    reference, of which each is by itself."""
+    B, D, form = 610, 256, FORMS[T % 4]
+    t = make((B, T, D), types, form, seed=T)
+    kept = gla.scan_states(t["x"])
+    out, hT = gla.scan_fwd(t["x"], t["g"], form, t["gate"], h0=t["h0"], states=kept)
+    run = lambda k: gla.scan_bwd(t["x"], t["g"], form, t["dout"], t["gate"], h0=t["h0"], dhT=t["dhT"], states=k)  # noqa: E731
+    got = run(kept)
+    for x, y in zip(got, run(None)):
+        assert torch.equal(x, y)
+    seqs = torch.tensor([0, 1, 303, 304, 608, 609], device="cuda")
+    some = {k: v[seqs][..., ::17] for k, v in t.items()}
+    o_ref, h_ref = S.forward(some["x"], some["g"], form, some["gate"], gla.ACT_SILU, some["h0"])
+    close(out[seqs][..., ::17], o_ref, F32, "out"), close(hT[seqs][:, ::17], h_ref, F32, "hT")
+    want = S.backward(some["x"], some["g"], form, some["dout"], some["gate"], gla.ACT_SILU, some["h0"], some["dhT"])
+    for name, x, y in zip(("dx", "dg", "dgate", "dh0"), got, want):
+        close(x[seqs][..., ::17], y, 2 * F32, name)
+        assert bool(x.isfinite().all())
