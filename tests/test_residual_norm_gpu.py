@@ -323,3 +323,42 @@ def test_many_rows_of_the_sum_alone_and_of_the_norm_alone(types, rows, D):
     got = gla.residual_norm_bwd(v["dr"], None, v["x"], v["y"], **block)
     want = K.residual_norm_bwd(few["dr"], None, few["x"], few["y"], None, gate=few["gate"], scale=v["scale"])
     close(got.dx[some], want["dx"], F32, "dx"), close(got.dy[some], want["dy"], F32, "dy")
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("D", [5128, 8192, 10248, 16384])
+@pytest.mark.parametrize("parts", [True, False])
+def test_many_rows_of_several_blocks_each(types, D, parts):
+    """331 rows above 5,120 channels are at least four for each of the 76 or fewer clusters of blocks: their stages are refilled,
+    their meetings alternate and their sums over tokens run over several rows."""
+    v, block = make((331, D), types, seed=D, gate=parts, scale=parts, post=parts)
+    check(v, block, KINDS[D % 3 % 2] if parts else gla.NORM_RMS)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("rows,D", [(10007, 72), (13001, 328), (5001, 600)])
+@pytest.mark.parametrize("parts", [True, False])
+def test_gradients_of_many_short_rows(types, rows, D, parts):
+    """So many that a copy brings several rows of each thread, an odd number of them at the end.  The parameters' gradients are
+    sums over all rows: a thread's over some ten, and of up to 1,520 blocks 190 and then 8 one after the other; with roundings of
+    2^-24 of partial sums that are no larger than a few times the whole, at random, they are off by 2^-24 x 3 x sqrt(210) = 3e-6
+    of it, within the bar."""
+    v, block = make((rows, D), types, seed=rows, gate=parts, scale=parts, post=parts)
+    check(v, block, KINDS[rows % 3 % 2] if parts else gla.NORM_RMS)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("D", [72, 200, 328, 600, 1160, 2048, 2552, 2560, 4096, 4616, 5120, 8192, 16384])
+@pytest.mark.parametrize("parts", [True, False])
+def test_a_row_of_a_forward_does_not_depend_on_the_others(types, D, parts):
+    """Bit for bit: beside as many others as several rows of a thread or of a block at once take, and beside few, with another
+    row of its pair, alone at the end, and as the only one."""
+    rows = 10007 if D <= 200 else 5001 if D <= 1160 else 1301
+    v, block = make((rows, D), types, seed=D, gate=parts, scale=parts, post=parts)
+    run = lambda v: gla.residual_norm(v["x"], v["y"], v["weight"], v["bias"], gla.NORM_LAYER,  # noqa: E731
+                                      **{**block, "gate": v["gate"]})
+    r, out = run(v)
+    for some in ([1, 0, 8, rows // 2, rows - 1, 17, 2], [rows - 2], [rows - 1], list(range(3, 259))):
+        at = torch.tensor(some, device="cuda")
+        r1, out1 = run({k: None if x is None else x if x.dim() < 2 else x[at].contiguous() for k, x in v.items()})
+        assert torch.equal(r[at], r1) and torch.equal(out[at], out1)
