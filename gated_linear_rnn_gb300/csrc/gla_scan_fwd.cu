@@ -17,13 +17,23 @@ template <typename T, typename TG, bool kGate> struct Ring {
 };
 
 // The rows of a tile's channels that are apart, one warp after the other from the state that enters the tile; by all threads, after
-// a barrier behind the writes of enters and apart.  x and g come from memory: their stage has been refilled.
+// a barrier behind the writes of enters and apart.  x and g come from memory, since their stage has been refilled, for all warps at
+// once, and wait in local memory: the kernel's registers are taken.
 template <typename T, typename TG, int kForm, bool kGate>
 __device__ __forceinline__ void again(const T *x, const TG *g, const T *gate, T *out, float *hT, float *states, Chain chain, int D,
                                       int act, const Apart &apart, float2 (&enters)[32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bits = apart.of[lane];
     const Tile o = apart.tile;
     const int d = o.col + 2 * lane, n = min(kLane, o.len - warp * kLane);
+    const int64_t first = (int64_t)(o.row + warp * kLane) * D + d;
+    Decay a[kLane];
+    Pair v[kLane];
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        if (bits == 0) break;
+        a[i] = decay<kForm>(load_two(g + first + (int64_t)i * D));
+        v[i] = input<kForm>(a[i], load_two(x + first + (int64_t)i * D));
+    }
     __syncthreads();  // all warps have read what enters the tile
     for (int w = 0; w < kWarps; ++w) {
         if (w == warp && bits != 0 && n > 0) {
@@ -31,14 +41,8 @@ __device__ __forceinline__ void again(const T *x, const TG *g, const T *gate, T 
             Pair S = pair(e.x, e.y);
             if (states != nullptr)
                 store_some(states + state_slot(o.start(), o.seq, o.chunk * kChunk + warp * kLane) * D + d, S, bits);
-            int64_t at = (int64_t)(o.row + warp * kLane) * D + d;
 #pragma unroll 1
-            for (int i = 0; i < n; ++i, at += D) {
-                const Decay a = decay<kForm>(load_two(g + at));
-                S = decayed(a, S, input<kForm>(a, load_two(x + at)));
-                if (out == nullptr) continue;
-                store_some(out + at, kGate ? S * activation(load_two(gate + at), act) : S, bits);
-            }
+            for (int i = 0; i < n; ++i) v[i] = S = decayed(a[i], S, v[i]);
             enters[lane] = parts(S);
         }
         __syncthreads();
@@ -48,6 +52,12 @@ __device__ __forceinline__ void again(const T *x, const TG *g, const T *gate, T 
         const Pair end = choose(bits, pair(e.x, e.y), pair(f.x, f.y));
         if (o.behind > 0) publish_result<false>(chain, (int64_t)o.slot * D + d, end);
         else if (hT != nullptr) store_state(hT + (int64_t)o.seq * D + d, end);
+    }
+    if (out == nullptr || bits == 0) return;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        const int64_t at = first + (int64_t)i * D;
+        store_some(out + at, kGate ? v[i] * activation(load_two(gate + at), act) : v[i], bits);
     }
 }
 
