@@ -80,3 +80,11 @@ def test_sizes(lib):
     assert gla.gla_scan_workspace_bytes(gla.OP_BACKWARD, 3, 300, 64, False) >= gla.gla_scan_states_bytes(3, 300, 64, False)
     with pytest.raises(gla.GLAError):
         gla.gla_scan_states_bytes(1, 8, 60, False)
+
+
+def test_forward_refuses_a_small_workspace(lib):
+    """As the gradient, before the device is asked for."""
+    n = gla.gla_scan_workspace_bytes(gla.OP_FORWARD, 1, 300, 64, True)
+    assert n > 0
+    assert fwd(lib, T=300, cu=FAKE) == fwd(lib, T=300, cu=FAKE, ws=FAKE, n=n - 1) == -1
+    assert fwd(lib, T=300, cu=FAKE, ws=ODD, n=n) == -3
