@@ -8,13 +8,14 @@
 //
 // Bound by HBM: x and dy are read and dx is written once.  A warp takes 128 channels, four a lane, of a run of rows of one
 // sequence: the last three inputs and the last three dz stay in registers, and the three dz behind the run, which its last rows
-// need, are computed again by the next run.  Rows come four at a time, the next four while four are worked on.  A run is as long
-// as gives every warp the same number of runs (104 rows for 8 x 2,048 x 4,608).  The warps' sums over tokens stay in registers
-// until their last run; the blocks' are added up by a second kernel in a fixed order.
+// need, are computed again by the next run.  Rows come four at a time, the next four while four are worked on.  Runs are as long as
+// makes a few of them for each warp (128 rows for 8 x 2,048 x 4,608, two a warp), see cut().  The warps' sums over tokens stay in
+// registers until their last run; the blocks' are added up by a second kernel in a fixed order.
 //
 // Measured, bf16: 8 x 2,048 x 4,608 102 us (the bytes at the rate of a copy: 67), 1 x 32,768 x 2,048 85 (60); f32 4 x 2,048 x 4,608
-// 80 (67).  The f32 pipe is half busy (two exponentials and reciprocals beside 40 products and sums an element), and half of the
-// issue slots are used.  Six or eight rows at a time, and three blocks of an SM in bf16, are no faster.
+// 80 (67).  Nothing is saturated: in bf16 the f32 pipe is busy for 43% of the time, half of the issue slots are used, and HBM is at
+// 53%.  What bounds it is how few rows are on their way: they wait in registers, which leave 16 warps of an SM.  Six or eight rows
+// at a time, and three blocks of an SM in bf16, are no faster.
 #include <type_traits>
 
 #include "gla_act.cuh"
@@ -232,7 +233,9 @@ sum_kernel(const float *__restrict__ part, int nblocks, int D, float *__restrict
 }
 
 // How the work is cut: blocks to a slab of channels, as many as the device holds at once (or there are runs of sixteen rows),
-// and rows to a run, a multiple of four that gives every warp the same few runs of at most 256.
+// and rows to a run, a multiple of four.  A packed batch's runs are as many as a few for every warp.  A dense batch's sequences are
+// cut into so many alike, rounded down: with between half as many sequences as a slab's warps and as many, each is one run, however
+// long, and up to half of the warps have none (bf16 33 x 496 x 4,608 182 us, 32 x 512 103).
 struct Cut {
     int blocks, run_rows, per_seq;  // per_seq: runs of a sequence of a dense batch
     int64_t slots;                  // runs, or (packed) slots for them
@@ -244,7 +247,7 @@ Cut cut(int B, int T, int D, bool packed, int per_sm) {
     Cut c{};
     c.blocks = (int)(need < most ? need : most);
     const int64_t warps = (int64_t)c.blocks * kWarps;
-    // so many times all warps that a run has fewer than 256 rows; a packed batch's sequence has a slot more than its rows make
+    // so many times all warps that 256 rows or fewer come to a run; a packed batch's sequence has a slot more than its rows make
     const int64_t least = rows / 256 + 1 + (packed ? B + 1 : 0), runs = (least + warps - 1) / warps * warps;
     if (packed) {
         c.run_rows = (int)((rows + runs - B - 2) / (runs - B - 1));

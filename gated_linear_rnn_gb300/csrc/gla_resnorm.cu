@@ -242,7 +242,9 @@ int launch_fwd(const void *x, const void *y, const void *gate, const Weights &w,
     // Two rows at a time where that has as many rows on an SM, however many a call has, so that a row's result does not depend on
     // the others (all parts, bf16, two and one:
     // 16,435 x 2,552 104 and 123 us, 69,905 x 600 135 and 176, 8,192 x 5,120 104 and 123, 16,384 x 2,560 97 and 99; with fewer
-    // rows on an SM, 10,240 x 4,096 118 and 92).  What stages leave of shared memory, 60 KB or more, caches the parameters.
+    // rows on an SM, 10,240 x 4,096 118 and 92).  What stages leave of shared memory caches the parameters: 60 KB on an SM where
+    // there is a choice of stages, less where two take more (f32 of all parts at 4,616 channels 1 KB: 4,543 rows 85 us; at 4,864, one
+    // row at a time, 4,311 rows 91).
     const Plan p2 = make_plan(D, kTwoVecs, 16384);
     const int n2 = per_sm(p2, kTwoMost), room = kMostShared / n2 - (n2 == 1 ? 0 : 3328);
     Inputs<3> two{{x, y, gate}, {D * es, D * e, D * e}};

@@ -2,14 +2,16 @@
 //
 // Both are bound by HBM.  A row is one block's, a part of a warp's where it is short, a cluster's where it is wide; a thread takes
 // four neighbouring channels at a time and keeps the same ones for all of its rows, so the gradient's sums over tokens stay in
-// registers until its last row.  An SM has several blocks, so that one row's barriers wait beside another's work.  Rows come into
-// shared memory by bulk copies, some rows ahead, and are read from there by each step: what is in flight costs no registers.
+// registers until its last row.  An SM has several blocks where their threads allow, so that one row's barriers wait beside another's
+// work; the gradient has one above 2,560 channels, of 352 to 640 threads.  Rows come into shared memory by bulk copies, some rows ahead, and are read from there by each step: what is in flight costs no registers.
 // Rows of the forward that two stages have no room for are read from memory.
 //
 // Measured with all parts (layer norms before and behind, gate, scale; bf16): forward of 16,384 x 2,560 97 us (the bytes at the
 // rate of a copy: 62), of an RMS norm alone behind the sum 55 (50); gradient 177 and 95 (99 and 74).  8,192 x 5,120: 105 and 187;
-// f32 8,192 x 2,560: 79 and 166 (62 and 99).  What bounds the gradient is its instructions, about 90 a channel, and two meetings
-// of a row's warps; the forward waits for its four meetings and for the parameters, which are as many bytes as the row.
+// f32 8,192 x 2,560: 79 and 166 (62 and 99).  The gradient between two sizes that fill 640 threads, for the same bytes: 2,568 323 and
+// 152, 3,584 230 and 115, 4,096 200 and 104, 5,112 214 and 101.  What bounds the gradient is this code's instructions, about 90 a
+// channel, and two meetings of a row's warps; the forward waits for its four meetings (for two rows) and for the parameters, which
+// are as many bytes as the row.
 //
 // The file that includes this defines record_status before it.
 #pragma once

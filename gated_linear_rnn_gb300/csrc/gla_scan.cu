@@ -298,6 +298,7 @@ Chain chain_at(const Layout &l, const Shape &p, void *ws, int dir) {
 // of a packed batch those of up to a tile's rows, and the tiles then take the others, if there are any (a decode step with a
 // prompt in it).  Forward and gradient of 16,384 x 2,560 bf16 in us, walked and by tiles: sequences of 17 tokens 63, 134 and 152,
 // 260; of 32 61, 126 and 98, 164; of 64 63, 129 and 66, 110; 8 sequences of 32 8, 13 and 4, 5; f32 256 x 32 52, 162 and 92, 146.
+// (One rule for both: from 33 to 64 tokens the forward alone would still gain by walking, 5 to 20%, and the gradient lose as much.)
 bool walks(const Shape &p) {
     const int64_t rows = total_rows(p), tiles = (int64_t)p.nseq * ((p.D + kSlab - 1) / kSlab);
     return rows <= (int64_t)kWalked * p.nseq ||

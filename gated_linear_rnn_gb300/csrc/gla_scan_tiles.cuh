@@ -18,11 +18,12 @@
 // waits only for blocks that run.  Rows come in by TMA, some tiles ahead.
 //
 // Each input is read once and each output written once.  Measured (bf16, sigmoid with a leak, gate): 8 x 2,048 x 2,560 forward
-// 80 us, gradient 127 (the bytes at the rate of a copy: 50 and 87); 256 x 64, without chains, 68 and 112.  What bounds it there
-// is the instructions of the decays and gates beside the wait for a tile's meeting; in few long sequences the look back, 0.3 us
-// from a tile to the next: 1 x 32,768 x 2,048 f32 log decays 151 and 215 (79 and 139).  Tiles of 64 x 64 in three blocks (two,
-// gradient) of an SM were measured against 128 x 32 (long 143 and 218, short sequences twice the time), clusters that hand the
-// state on in shared memory (8 x 2,048: 137) and a warp that only follows the chain (gradient 116, of long sequences 236).
+// 79 us, gradient 127 (the bytes at the rate of a copy: 50 and 87); 256 x 64, without chains, 67 and 110.  What bounds it there
+// is the instructions of the decays and gates beside the wait for a tile's meeting.  Few long sequences (1 x 32,768 x 2,048 f32 log
+// decays 153 and 214, for 79 and 139) take 4.2 us a tile and block where a batch without chains takes 3: some 14 tiles of a chain
+// are in flight, and the look back is less than half of what they take beyond their bytes.  Tiles of 64 x 64 were measured
+// against 128 x 32 (long 143 and 218, short sequences twice the time), clusters that hand the state on in shared memory (8 x 2,048:
+// 137) and a warp that only follows the chain (gradient 116, of long sequences 236).
 #pragma once
 
 #include <cuda.h>
@@ -279,7 +280,9 @@ template <typename T> __device__ __forceinline__ void store_some(T *p, Pair x, i
 
 // ---- launches --------------------------------------------------------------------------------------------------------
 
-// Blocks of an SM and stages of a block: as many blocks as the threads' registers allow and two stages each leave room for.
+// Blocks of an SM and stages of a block: as many blocks as the threads' registers allow and two stages each leave room for.  That is
+// three in the forward, but two of bf16 with f32 decays and a gate and of f32 without a gate, and one of f32 with it; two in the
+// gradient, but one of f32.
 struct Room {
     int per_sm, stages;
 };
