@@ -578,9 +578,9 @@ GLA_API int gla_group_norm_bwd(const void *dout, const void *x, const float *wei
  *     GLA_SCAN_SIGMOID       a = sigmoid(g),  w = 1          GLA_SCAN_SIGMOID_LEAK  a = sigmoid(g),  w = 1 - a
  * A log decay is at most 0 where the recurrence is to be stable.  Above 0 it grows, and results are the recurrence's as long as
  * e^g, the states and the gradient's dh are numbers of f32, whatever the decays of some tokens multiply to; what has decayed by
- * 2^-126 or more within a chunk of 64 tokens may count as gone, even where it would grow again.  (GLA_SCAN_SIGMOID adds a chunk's
- * inputs up before the state that enters it: they have to be of sums in f32 by themselves.)  g = -inf is a full reset of a finite state; a sigmoid's
- * g = +inf keeps it (and a leaking one then takes nothing of x).
+ * 2^-126 or more within a chunk of 64 tokens may count as gone, even where it would grow again.  The sigmoid forms add up what comes
+ * in over a chunk (w x, and dout act(gate) in the gradient) before the state that enters it: those sums have to be numbers of f32 by
+ * themselves.  g = -inf is a full reset of a finite state; a sigmoid's g = +inf keeps it (and a leaking one then takes nothing of x).
  *
  * x, g, gate and out are [B, T, D], or packed [1, T, D] with cu_seqlens (then B is the number of sequences); states and
  * their gradients [B, D] f32.
